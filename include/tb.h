@@ -71,6 +71,9 @@ enum {
 #define TB_DEV_BAD_ID 2    /* tb_embed_lookup: an id outside [0, V) (its row is written as zeros) */
 #define TB_DEV_TIMEOUT 4   /* a bounded wait inside a kernel gave up; outputs are not valid */
 #define TB_DEV_BAD_PLAN 8  /* tb_chain_run: the plan does not match the launch (nothing computed) */
+#define TB_DEV_BAD_SLOT 16 /* a slot or page number outside the cache (its token is left out) */
+#define TB_DEV_NO_PAGE 32  /* tb_cache_plan: no page left on the free list, or a table row too short */
+#define TB_DEV_BAD_LEN 64  /* lengths or row starts that do not fit together or the arguments */
 
 /* algorithm choice for tb_packed_linear_algo */
 #define TB_ALGO_AUTO 0       /* the GEMV for M <= 2, the batched GEMV on mma.sync for 3..32
@@ -387,6 +390,123 @@ int tb_packed_linear_gemv_noalloc(const uint16_t* x, int64_t M, int64_t K, const
                                   int block, const uint32_t* w, const uint16_t* scales,
                                   const uint16_t* biases, int64_t N, uint16_t* y,
                                   int32_t* dev_status, void* stream);
+
+/*
+ * The mixers between the packed linears ([ARCH] "混合注意力": 64 layers, full attention every
+ * fourth with 24 query heads, 4 KV heads of 256; linear attention in the others with 16 key heads,
+ * 48 value heads of 128 and an fp32 state).  Tokens of several requests lie packed one after
+ * another: request b's rows are row_start[b] .. row_start[b+1] - 1 (int32 [B + 1]).  q, k and v may
+ * be slices of a wider matrix (a fused projection): ld* is the distance of two tokens in elements,
+ * a multiple of 8 and at least heads * D; within a token, heads are contiguous.  Query head h
+ * reads KV (or key) head h / (heads / KV heads).  Rows of no request are neither read nor written.
+ * Inference only: these calls have no gradient.  16-byte alignment is asked of the fp16 arrays, the
+ * states and the workspaces; arrays of indices, lengths, decays and steps need that of their type.
+ *
+ * The paged K/V cache: two fp16 arrays [pages, Hkv, page, D]; page is 16, 32, 64, 128 or 256 tokens.
+ * table int32 [B, max_pages]: the page that holds tokens p*page .. of request b.  A slot (int64)
+ * is page number * page + place in the page; -1 is a padded token.
+ */
+
+/*
+ * tb_cache_plan — the cache's bookkeeping for one step, from the requests' lengths.
+ *   cached, fresh  int32 [B]: tokens already in the cache, and tokens this step adds (>= 0);
+ *   free_pages     int32 [n_free]: pages to hand out, taken from its front in the order of the
+ *                  requests and, within one, of its pages (may be NULL when n_free is 0);
+ *   table          int32 [B, max_pages] (in/out): entries of the ceil(cached/page) pages held are
+ *                  read, those of new pages written (-1 where none is left), others left alone;
+ *   slots          int64 [T] (out): the new tokens' slots, packed by request; -1 past the last
+ *                  token and for a token without a page (T: room, e.g. a graph's fixed size);
+ *   row_start      int32 [B + 1] (out): running sums of fresh;  total int32 [B] (out): cached + fresh;
+ *   used           int32 [1] (out) or NULL: pages taken from free_pages.
+ * One launch; the result depends on the inputs alone (a second call with them gives it again).
+ * Outputs must not overlap inputs.  B in 1..16384 (else TB_ERR_TOO_LARGE).  dev_status optional:
+ * TB_DEV_NO_PAGE, TB_DEV_BAD_LEN (a negative length is taken as 0, a sum above T is cut),
+ * TB_DEV_BAD_SLOT (a held page's entry is negative).
+ */
+int tb_cache_plan(const int32_t* cached, const int32_t* fresh, int64_t B, int64_t page,
+                  const int32_t* free_pages, int64_t n_free, int32_t* table, int64_t max_pages,
+                  int64_t* slots, int64_t T, int32_t* row_start, int32_t* total, int32_t* used,
+                  int32_t* dev_status, void* stream);
+
+/*
+ * tb_cache_write — write the new tokens' K and V rows to their slots.
+ *   k, v     fp16 [T, Hkv, D], tokens ldk / ldv elements apart;  slots int64 [T], no slot twice;
+ *   k_cache, v_cache  fp16 [pages, Hkv, page, D] (out).
+ * A negative slot is skipped; one past the cache is skipped and sets TB_DEV_BAD_SLOT.  D a multiple
+ * of 8 up to 1024; T >= 0 (T = 0 is a no-op).
+ */
+int tb_cache_write(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                   const int64_t* slots, int64_t T, int64_t Hkv, int64_t D, uint16_t* k_cache,
+                   uint16_t* v_cache, int64_t pages, int64_t page, int32_t* dev_status, void* stream);
+
+/*
+ * tb_tree_attention — attention of each request's newest tokens over its cache: one token per
+ * request (ordinary decode), a run of them, or a tree of drafted tokens to verify.
+ *   q        fp16 [T, Hq, D], tokens ldq apart; request b's n_b rows (n_b <= max_q <= 64) are the
+ *            last n_b of its total[b] cached tokens (their K and V already written);
+ *   tree     uint64 [T] or NULL: a row sees every token before its request's n_b newest, and of
+ *            those the i-th (i < n_b) when bit i of its word is set; NULL: the first up to itself;
+ *   scale    positive and finite, e.g. 1/sqrt(D);  o fp16 [T, Hq, D] (out).
+ * o_i = sum_j w_ij v_j, w_i the softmax of scale q_i . k_j over what row i sees; a row that sees
+ * nothing (or only scores of -infinity) gives zeros.  What a row does not see does not reach it,
+ * not even as NaN or infinity.  D 64, 128 or 256 (else TB_ERR_UNSUPPORTED); max_q above 64:
+ * TB_ERR_TOO_LARGE.  workspace: at least tb_tree_attention_workspace_size(B, T, max_q, Hq, Hkv, D)
+ * bytes (the size may be 0), zero before its first use and left zero by every completed call; calls
+ * that share one are ordered on one stream.  dev_status optional: TB_DEV_BAD_LEN (n_b above max_q,
+ * total[b] below n_b or above max_pages * page: zeros), TB_DEV_BAD_SLOT (a page outside the cache:
+ * its tokens are left out).
+ */
+size_t tb_tree_attention_workspace_size(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv,
+                                        int64_t D);
+int tb_tree_attention(const uint16_t* q, int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                      const uint16_t* k_cache, const uint16_t* v_cache, int64_t pages, int64_t page,
+                      const int32_t* table, int64_t max_pages, const int32_t* total,
+                      const int32_t* row_start, int64_t B, int64_t max_q, const uint64_t* tree,
+                      float scale, uint16_t* o, void* workspace, size_t workspace_bytes,
+                      int32_t* dev_status, void* stream);
+
+/*
+ * tb_prompt_attention — causal attention over whole prompts, packed.
+ *   q fp16 [Tq, Hq, D], k and v fp16 [Tk, Hkv, D], tokens ldq / ldk / ldv apart; request b's queries
+ *   are rows q_start[b] .. of q and its keys rows k_start[b] .. of k and v (int32 [B + 1] each): lq
+ *   and lk of them, the queries being the last lq of the lk positions, so query i sees keys
+ *   j <= i + lk - lq (fewer keys than queries: the first rows see nothing and give zeros);
+ *   scale, o, D: as for tb_tree_attention, with the same rule about what a row does not see.
+ * dev_status optional: TB_DEV_BAD_LEN (row starts out of order or past Tq / Tk: zeros where the
+ * rows can be told, else not written).
+ */
+int tb_prompt_attention(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk,
+                        const uint16_t* v, int64_t ldv, int64_t Tq, int64_t Tk, int64_t Hq,
+                        int64_t Hkv, int64_t D, const int32_t* q_start, const int32_t* k_start,
+                        int64_t B, float scale, uint16_t* o, int32_t* dev_status, void* stream);
+
+/*
+ * tb_gated_delta — the gated delta rule, over prompts or single tokens.  Per value head, S its
+ * D x D state (rows: k, columns: v), token by token:
+ *   S <- exp(g_t) S;  u = beta_t (v_t - S^T k_t);  S <- S + k_t u^T;  o_t = scale S^T q_t
+ *   q, k     fp16 [T, Hk, D], v fp16 [T, Hv, D], tokens ldq / ldk / ldv apart; Hv a multiple of Hk;
+ *   g, beta  fp32 [T, Hv]: logarithm of the decay (at most 0), and the step;
+ *   normalise  nonzero: q and k are first divided by sqrt(sum of squares + 1e-6) (in fp32);
+ *   state_in   fp32 [n_in, Hv, D, D] or NULL (zeros); request b starts from row slot_in[b] (int32 [B];
+ *              NULL: row b); a negative slot: zeros;
+ *   state_out  fp32 [n_out, Hv, D, D] or NULL; the final state goes to row slot_out[b] (NULL: b);
+ *              negative: not kept.  state_out may be state_in; a row one request writes must not be
+ *              one another request of the call reads or writes;
+ *   max_len    the longest request's tokens: chooses the kernel (any value gives right results);
+ *   o        fp16 [T, Hv, D] (out).
+ * A request of no tokens copies its state.  States, sums and decays are fp32.  D must be 128
+ * (TB_ERR_UNSUPPORTED).  workspace: at least tb_gated_delta_workspace_size(T, B, max_len, Hk, Hv)
+ * bytes of scratch (may be 0); its contents do not matter; calls that share one are ordered on one
+ * stream.  dev_status optional: TB_DEV_BAD_ID (a slot past its pool: taken as negative),
+ * TB_DEV_BAD_LEN (row starts out of order or past T: that request is taken as empty).
+ */
+size_t tb_gated_delta_workspace_size(int64_t T, int64_t B, int64_t max_len, int64_t Hk, int64_t Hv);
+int tb_gated_delta(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v,
+                   int64_t ldv, const float* g, const float* beta, int64_t T, int64_t Hk, int64_t Hv,
+                   int64_t D, const int32_t* row_start, int64_t B, int64_t max_len, int normalise,
+                   float scale, const float* state_in, const int32_t* slot_in, int64_t n_in,
+                   float* state_out, const int32_t* slot_out, int64_t n_out, uint16_t* o,
+                   void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,211 @@
+// Attention of the hybrid model's full-attention layers: over whole prompts, and over the paged
+// cache for one token or a tree of drafted tokens per request.
+//   o_i = sum_j w_ij v_j,  w_ij = softmax over the visible j of scale q_i . k_j;  no visible j: 0.
+//
+// One warp per (row, query head): the lanes share the head's elements, one key at a time, with the
+// softmax's running maximum and sum, so every key and value is read once per row.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "tb_common.cuh"
+#include "tb_host.h"
+
+namespace tb {
+
+constexpr int kAttnWarps = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct AttnArgs {
+  const __half* q;
+  const __half* k;
+  const __half* v;
+  const int32_t* q_start;
+  const int32_t* k_start;  // prompt form
+  const int32_t* table;    // paged form
+  const int32_t* total;
+  const int64_t* tree;
+  __half* o;
+  int32_t* status;
+  int64_t ldq, ldk, ldv, T, Tk, pages, max_pages;
+  int B, Hq, Hkv, page_log2, max_q;
+  float scale_log2;
+};
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(kAttnWarps * 32) attn_row_kernel(const AttnArgs a) {
+  constexpr int E = D / 32;  // elements per lane
+  const int lane = threadIdx.x & 31;
+  const int64_t item = blockIdx.x * (int64_t)kAttnWarps + (threadIdx.x >> 5);
+  if (item >= a.T * a.Hq) return;
+  const int64_t t = item / a.Hq;
+  const int h = (int)(item - t * a.Hq), hk = h / (a.Hq / a.Hkv);
+  int lo = 0, hi = a.B - 1;  // the last request that begins at or before row t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(a.q_start + mid) <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  const int64_t r0 = __ldg(a.q_start + lo), r1 = __ldg(a.q_start + lo + 1);
+  if (r0 < 0 || t < r0 || r1 > a.T) {
+    if (lane == 0) set_status(a.status, TB_DEV_BAD_LEN);
+    return;
+  }
+  if (t >= r1) return;  // a row of no request
+  const int64_t n = r1 - r0, i = t - r0;
+  int64_t len, k0 = 0;
+  bool ok = true;
+  if (PAGED) {
+    len = __ldg(a.total + lo);
+    ok = n <= a.max_q && len >= n && len <= a.max_pages << a.page_log2;
+  } else {
+    k0 = __ldg(a.k_start + lo);
+    len = __ldg(a.k_start + lo + 1) - k0;
+    ok = k0 >= 0 && len >= 0 && k0 + len <= a.Tk;
+  }
+  if (!ok) {
+    if (lane == 0) set_status(a.status, TB_DEV_BAD_LEN);
+    len = 0;
+  }
+  const int64_t prefix = len - n;
+  const uint64_t word = PAGED && a.tree ? (uint64_t)__ldg(reinterpret_cast<const long long*>(a.tree) + t) : 0;
+  const int64_t end = PAGED && a.tree ? len : (prefix + i + 1 < len ? prefix + i + 1 : len);
+
+  float q[E], acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    q[e] = __half2float(a.q[t * a.ldq + h * D + e * 32 + lane]) * a.scale_log2;
+    acc[e] = 0.f;
+  }
+  float m = -INFINITY, l = 0.f;
+  for (int64_t j = 0; j < end; ++j) {
+    if (PAGED && a.tree && j >= prefix && !((word >> (j - prefix)) & 1)) continue;
+    int64_t at_k, at_v;
+    if (PAGED) {
+      const int64_t pg = __ldg(a.table + lo * a.max_pages + (j >> a.page_log2));
+      if (pg < 0 || pg >= a.pages) {
+        if (lane == 0) set_status(a.status, TB_DEV_BAD_SLOT);
+        continue;
+      }
+      at_k = at_v = (((pg * a.Hkv + hk) << a.page_log2) + (j & ((1ll << a.page_log2) - 1))) * D;
+    } else {
+      at_k = (k0 + j) * a.ldk + hk * D;
+      at_v = (k0 + j) * a.ldv + hk * D;
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = fmaf(q[e], __half2float(a.k[at_k + e * 32 + lane]), s);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    const float m2 = fmaxf(m, s);
+    if (m2 == -INFINITY && s == -INFINITY) continue;  // a weight of zero
+    const float c = exp2f(m - m2), w = exp2f(s - m2);
+    l = l * c + w;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, __half2float(a.v[at_v + e * 32 + lane]), acc[e] * c);
+    m = m2;
+  }
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) a.o[(t * a.Hq + h) * D + e * 32 + lane] = __float2half_rn(acc[e] * inv);
+}
+
+template <bool PAGED>
+static int launch_rows(const AttnArgs& a, int64_t D, cudaStream_t s) {
+  const int64_t blocks = (a.T * a.Hq + kAttnWarps - 1) / kAttnWarps;
+  if (blocks > INT32_MAX) return TB_ERR_TOO_LARGE;
+  if (D == 64) attn_row_kernel<64, PAGED><<<(int)blocks, kAttnWarps * 32, 0, s>>>(a);
+  else if (D == 128) attn_row_kernel<128, PAGED><<<(int)blocks, kAttnWarps * 32, 0, s>>>(a);
+  else attn_row_kernel<256, PAGED><<<(int)blocks, kAttnWarps * 32, 0, s>>>(a);
+  return check_launch();
+}
+
+}  // namespace tb
+
+extern "C" int tb_prompt_attention(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v,
+                                   int64_t ldv, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D,
+                                   const int32_t* q_start, const int32_t* k_start, int64_t B, float scale, uint16_t* o,
+                                   int32_t* dev_status, void* stream) {
+  using namespace tb;
+  if (Tq < 0 || Tq > INT32_MAX || Tk < 0 || Tk > INT32_MAX || B < 1 || B > INT32_MAX || Hkv < 1 || Hq < Hkv ||
+      Hq > 1024 || Hq % Hkv)
+    return TB_ERR_SHAPE;
+  if (!supported_head(D)) return TB_ERR_UNSUPPORTED;
+  if (ldq < Hq * D || ldk < Hkv * D || ldv < Hkv * D || ldq % 8 || ldk % 8 || ldv % 8) return TB_ERR_SHAPE;
+  if (!(scale > 0.f && scale < INFINITY)) return TB_ERR_VALUE;
+  if (Tq == 0) return TB_OK;
+  if (!q || !o || !q_start || !k_start || (Tk && (!k || !v))) return TB_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned_to(q_start, 4) || !aligned_to(k_start, 4))
+    return TB_ERR_ALIGN;
+  AttnArgs a = {};
+  a.q = reinterpret_cast<const __half*>(q);
+  a.k = reinterpret_cast<const __half*>(k);
+  a.v = reinterpret_cast<const __half*>(v);
+  a.q_start = q_start;
+  a.k_start = k_start;
+  a.o = reinterpret_cast<__half*>(o);
+  a.status = dev_status;
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.T = Tq;
+  a.Tk = Tk;
+  a.B = (int)B;
+  a.Hq = (int)Hq;
+  a.Hkv = (int)Hkv;
+  a.scale_log2 = scale * kLog2e;
+  return launch_rows<false>(a, D, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t tb_tree_attention_workspace_size(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv,
+                                                   int64_t D) {
+  (void)B;
+  (void)T;
+  (void)max_q;
+  (void)Hq;
+  (void)Hkv;
+  (void)D;
+  return 0;
+}
+
+extern "C" int tb_tree_attention(const uint16_t* q, int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                 const uint16_t* k_cache, const uint16_t* v_cache, int64_t pages, int64_t page,
+                                 const int32_t* table, int64_t max_pages, const int32_t* total,
+                                 const int32_t* row_start, int64_t B, int64_t max_q, const uint64_t* tree, float scale,
+                                 uint16_t* o, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                 void* stream) {
+  using namespace tb;
+  if (T < 0 || T > INT32_MAX || B < 1 || B > INT32_MAX || Hkv < 1 || Hq < Hkv || Hq > 1024 || Hq % Hkv || pages < 1 ||
+      pages > INT32_MAX || max_pages < 1 || max_pages > INT32_MAX || max_q < 1)
+    return TB_ERR_SHAPE;
+  if (!supported_head(D) || !supported_page(page)) return TB_ERR_UNSUPPORTED;
+  if (ldq < Hq * D || ldq % 8) return TB_ERR_SHAPE;
+  if (max_q > 64) return TB_ERR_TOO_LARGE;
+  if (!(scale > 0.f && scale < INFINITY)) return TB_ERR_VALUE;
+  if (T == 0) return TB_OK;
+  if (!q || !k_cache || !v_cache || !table || !total || !row_start || !o) return TB_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned_to(table, 4) || !aligned_to(total, 4) ||
+      !aligned_to(row_start, 4) || !aligned_to(tree, 8) || !aligned16(o) || !aligned16(workspace))
+    return TB_ERR_ALIGN;
+  if (workspace_bytes < tb_tree_attention_workspace_size(B, T, max_q, Hq, Hkv, D)) return TB_ERR_WORKSPACE;
+  AttnArgs a = {};
+  a.q = reinterpret_cast<const __half*>(q);
+  a.k = reinterpret_cast<const __half*>(k_cache);
+  a.v = reinterpret_cast<const __half*>(v_cache);
+  a.q_start = row_start;
+  a.table = table;
+  a.total = total;
+  a.tree = reinterpret_cast<const int64_t*>(tree);
+  a.o = reinterpret_cast<__half*>(o);
+  a.status = dev_status;
+  a.ldq = ldq;
+  a.T = T;
+  a.pages = pages;
+  a.max_pages = max_pages;
+  a.B = (int)B;
+  a.Hq = (int)Hq;
+  a.Hkv = (int)Hkv;
+  a.page_log2 = log2_of(page);
+  a.max_q = (int)max_q;
+  a.scale_log2 = scale * kLog2e;
+  return launch_rows<true>(a, D, static_cast<cudaStream_t>(stream));
+}

@@ -30,6 +30,21 @@ inline bool supported_block(int block) {
   return block == 512 || block == 1024 || block == 2048 || block == 4096;
 }
 
+inline bool aligned_to(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// tokens per page of the K/V cache: a power of two, 16 .. 256
+inline bool supported_page(int64_t page) {
+  return page == 16 || page == 32 || page == 64 || page == 128 || page == 256;
+}
+inline int log2_of(int64_t p) {
+  int n = 0;
+  while ((1ll << n) < p) ++n;
+  return n;
+}
+
+// head widths of the attention kernels
+inline bool supported_head(int64_t D) { return D == 64 || D == 128 || D == 256; }
+
 // y = fwht(x) over blocks of `block` (a supported size; K a multiple of it); y may equal x
 int launch_fwht(const __half* x, __half* y, const int8_t* signs, int64_t M, int64_t K, int block,
                 int inverse, cudaStream_t s);

@@ -1,0 +1,231 @@
+"""GPU parity of the gated delta rule against the float64 recurrence.
+
+Tolerances.  Outputs: half an fp16 ulp, and three operands that may be rounded to fp16 (the state,
+the decayed products q . k, the corrections u) on the sum of absolute terms: 2^-11 |o| + 3 2^-11 mag.
+States: operands of 22 bits or more in fp32 sums, in a recurrence that does not amplify (|k| <= 1,
+beta <= 1, decays <= 1): 2^-17 of the 2-norm of each head's state (32 times 2^-22).
+"""
+import numpy as np
+import pytest
+
+from oracle import mixers
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+D = 128
+
+
+def make(seed, lens, Hk, Hv, normalise, rate=(-6, 0.5), fused=True):
+    gen = torch.Generator().manual_seed(seed)
+    T = sum(lens)
+    wide = torch.randn(T, (2 * Hk + Hv) * D + 16, generator=gen).half()
+    if not normalise:
+        n = 2 * Hk * D
+        x = wide[:, 8: 8 + n].float().unflatten(1, (2 * Hk, D))
+        wide[:, 8: 8 + n] = (x / x.norm(dim=-1, keepdim=True) * 0.999).half().flatten(1)
+    wide = wide.cuda()
+    q = wide[:, 8: 8 + Hk * D].unflatten(1, (Hk, D))
+    k = wide[:, 8 + Hk * D: 8 + 2 * Hk * D].unflatten(1, (Hk, D))
+    v = wide[:, 8 + 2 * Hk * D: 8 + (2 * Hk + Hv) * D].unflatten(1, (Hv, D))
+    if not fused:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    g = -torch.exp(torch.linspace(*rate, Hv)) * torch.nn.functional.softplus(torch.randn(T, Hv, generator=gen))
+    beta = torch.sigmoid(torch.randn(T, Hv, generator=gen))
+    state = torch.randn(len(lens), Hv, D, D, generator=gen) * 0.3
+    return q, k, v, g.cuda(), beta.cuda(), state.cuda()
+
+
+def starts(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+def workspace(T, B, n, Hk, Hv):
+    import ternary_hadamard_rotated_gb300 as tb
+
+    return torch.full((tb.tb_gated_delta_workspace_size(T, B, n, Hk, Hv),), 0xA5, dtype=torch.uint8, device="cuda")
+
+
+def check(o, state, args, lens, init, normalise, scale=D ** -0.5):
+    q, k, v, g, beta = (x.cpu().numpy() for x in args)
+    want, fin, mag = mixers.gated_delta(q, k, v, g, beta, starts(lens).tolist(), init.cpu().numpy(), normalise, scale)
+    got = o.double().cpu().numpy()
+    tol = 2.0 ** -11 * np.abs(want) + 3 * 2.0 ** -11 * mag + 2.0 ** -25
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), got[bad][:4], want[bad][:4], tol[bad][:4])
+    if state is not None:
+        s = state.double().cpu().numpy()
+        err = np.linalg.norm((s - fin).reshape(*s.shape[:2], -1), axis=-1)
+        ref = np.linalg.norm(fin.reshape(*s.shape[:2], -1), axis=-1)
+        assert (err <= 2.0 ** -17 * ref + 1e-30).all(), float((err / np.maximum(ref, 1e-30)).max())
+
+
+def run(seed, lens, Hk, Hv, normalise=True, max_len=None, with_state=True, **kw):
+    import ternary_hadamard_rotated_gb300 as tb
+
+    q, k, v, g, beta, init = make(seed, lens, Hk, Hv, normalise, **kw)
+    T, B = sum(lens), len(lens)
+    n = max(lens) if max_len is None else max_len
+    full = torch.full((T + 1, Hv, D), 7.0, dtype=torch.float16, device="cuda")
+    out = torch.full((B + 1, Hv, D, D), 7.0, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    if not with_state:
+        init = torch.zeros_like(init)
+    tb.tb_gated_delta(q, k, v, g, beta, starts(lens), n, full[:T], workspace(T, B, n, Hk, Hv),
+                      state_in=init if with_state else None, state_out=out[:B], normalise=normalise, dev_status=st)
+    torch.cuda.synchronize()
+    assert (full[T:] == 7.0).all() and (out[B:] == 7.0).all() and int(st) == 0
+    check(full[:T], out[:B], (q, k, v, g, beta), lens, init, normalise)
+
+
+@pytest.mark.parametrize("Hk,Hv", [(1, 1), (2, 6), (4, 4)])
+@pytest.mark.parametrize("lens", [[1], [1] * 9, [2, 1, 3], [5, 0, 1, 4]])
+def test_few_tokens(Hk, Hv, lens):
+    run(1, lens, Hk, Hv)
+    run(2, lens, Hk, Hv, normalise=False)
+
+
+def test_step_of_a_full_batch():
+    run(3, [1] * 40, 16, 48)
+
+
+@pytest.mark.parametrize("lens", [[16], [63], [64], [65], [128], [129, 1, 0, 64], [200, 17, 31], [700]])
+@pytest.mark.parametrize("normalise", [True, False])
+def test_prompts(lens, normalise):
+    run(4, lens, 2, 6, normalise=normalise)
+
+
+def test_prompts_of_all_heads():
+    run(5, [130, 70], 16, 48)
+
+
+def test_without_a_first_state():
+    run(6, [100, 3], 2, 2, with_state=False)
+
+
+@pytest.mark.parametrize("n", [0, 1, 7, 64, 100000])
+def test_any_max_len_gives_the_same(n):
+    run(7, [90, 1, 33], 2, 4, max_len=n)
+
+
+def test_strong_and_vanishing_decays():
+    run(8, [150], 2, 4, rate=(2.0, 5.0))     # the state is forgotten within a token or two
+    run(9, [150], 2, 4, rate=(-20.0, -12.0))  # hardly ever
+
+
+def test_small_and_large_values():
+    """The state's relative precision does not hang on the values' size."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    for scale in (1e-3, 300.0):
+        lens = [190]
+        q, k, v, g, beta, init = make(10, lens, 1, 2, True)
+        v = (v.float() * scale).half()
+        init = init * scale
+        o = torch.empty(190, 2, D, dtype=torch.float16, device="cuda")
+        out = torch.empty_like(init)
+        tb.tb_gated_delta(q, k, v, g, beta, starts(lens), 190, o, workspace(190, 1, 190, 1, 2), state_in=init, state_out=out, normalise=True)
+        check(o, out, (q, k, v, g, beta), lens, init, True)
+
+
+def test_keys_that_repeat():
+    """The same key again and again, steps near 1: the triangular system at its hardest."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    lens = [200]
+    q, k, v, g, beta, init = make(11, lens, 1, 2, True)
+    k = k[:1].expand(200, 1, D) + 0.05 * k
+    k = k.half().contiguous()
+    beta = torch.full_like(beta, 0.97)
+    g = g * 0.01
+    o = torch.empty(200, 2, D, dtype=torch.float16, device="cuda")
+    out = torch.empty_like(init)
+    tb.tb_gated_delta(q, k, v, g, beta, starts(lens), 200, o, workspace(200, 1, 200, 1, 2), state_in=init, state_out=out, normalise=True)
+    check(o, out, (q, k, v, g, beta), lens, init, True)
+
+
+def test_a_decay_of_zero_forgets_everything():
+    import ternary_hadamard_rotated_gb300 as tb
+
+    lens = [70]
+    q, k, v, g, beta, init = make(12, lens, 1, 1, True)
+    g[30] = -float("inf")
+    g[31] = -1e30
+    o = torch.empty(70, 1, D, dtype=torch.float16, device="cuda")
+    out = torch.empty_like(init)
+    tb.tb_gated_delta(q, k, v, g, beta, starts(lens), 70, o, workspace(70, 1, 70, 1, 1), state_in=init, state_out=out, normalise=True)
+    check(o, out, (q, k, v, g, beta), lens, init, True)
+
+
+@pytest.mark.parametrize("lens", [[1, 1, 1, 1], [70, 1, 0, 90]])
+def test_pools_and_slots(lens):
+    """States in a pool, in place, with requests that start from nothing or keep nothing."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    Hk, Hv, T = 2, 4, sum(lens)
+    q, k, v, g, beta, _ = make(13, lens, Hk, Hv, True)
+    pool = torch.randn(9, Hv, D, D, device="cuda") * 0.3
+    before = pool.clone()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    sin, sout = [7, -1, 3, 0], [7, 2, 3, -1]
+    o = torch.empty(T, Hv, D, dtype=torch.float16, device="cuda")
+    st = torch.zeros(1, **i32)
+    tb.tb_gated_delta(q, k, v, g, beta, starts(lens), max(lens), o, workspace(T, 4, max(lens), Hk, Hv), state_in=pool, state_out=pool,
+                      slot_in=torch.tensor(sin, **i32), slot_out=torch.tensor(sout, **i32), normalise=True, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    init = torch.stack([before[s] if s >= 0 else torch.zeros_like(before[0]) for s in sin])
+    q_, want_state = None, pool.clone()
+    got = torch.stack([pool[s] if s >= 0 else init[b] for b, s in enumerate(sout)])
+    kept = [b for b, s in enumerate(sout) if s >= 0]
+    args = (q, k, v, g, beta)
+    check(o, None, args, lens, init, True)
+    fin = mixers.gated_delta(*(x.cpu().numpy() for x in args), starts(lens).tolist(), init.cpu().numpy(), True, D ** -0.5)[1]
+    for b in kept:
+        s = got[b].double().cpu().numpy()
+        assert np.linalg.norm(s - fin[b]) <= 2.0 ** -17 * np.linalg.norm(fin[b]) + 1e-30
+    for r in set(range(9)) - {s for s in sout if s >= 0}:
+        assert torch.equal(pool[r], before[r])
+    # a slot past the pool
+    tb.tb_gated_delta(q, k, v, g, beta, starts(lens), max(lens), o, workspace(T, 4, max(lens), Hk, Hv), state_in=pool, state_out=None,
+                      slot_in=torch.tensor([9, 0, 1, 2], **i32), normalise=True, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == tb.TB_DEV_BAD_ID
+
+
+def test_row_starts_that_do_not_fit():
+    import ternary_hadamard_rotated_gb300 as tb
+
+    q, k, v, g, beta, init = make(14, [20, 20], 1, 2, True)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for n in (1, 40):
+        o = torch.full((41, 2, D), 7.0, dtype=torch.float16, device="cuda")
+        out = torch.empty_like(init)
+        st = torch.zeros(1, **i32)
+        tb.tb_gated_delta(q, k, v, g, beta, torch.tensor([0, 20, 41], **i32), n, o[:40], workspace(40, 2, n, 1, 2), state_in=init, state_out=out,
+                          normalise=True, dev_status=st)
+        torch.cuda.synchronize()
+        assert int(st) == tb.TB_DEV_BAD_LEN
+        assert torch.equal(out[1], init[1]) and (o[20:] == 7.0).all()
+
+
+def test_a_step_goes_on_where_a_prompt_ended():
+    """A prompt and then single tokens, against the whole at once."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    lens = [133]
+    q, k, v, g, beta, init = make(15, lens, 2, 6, True)
+    state = init.clone()
+    o = torch.empty(133, 6, D, dtype=torch.float16, device="cuda")
+
+    def part(a, b):
+        n = b - a
+        tb.tb_gated_delta(q[a:b], k[a:b], v[a:b], g[a:b], beta[a:b], starts([n]), n, o[a:b], workspace(n, 1, n, 2, 6), state_in=state, state_out=state,
+                          normalise=True)
+
+    part(0, 130)
+    for t in range(130, 133):
+        part(t, t + 1)
+    torch.cuda.synchronize()
+    check(o, state, (q, k, v, g, beta), lens, init, True)
