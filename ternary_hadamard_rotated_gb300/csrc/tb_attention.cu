@@ -7,38 +7,22 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include "tb_attention.cuh"
 #include "tb_common.cuh"
 #include "tb_host.h"
 
 namespace tb {
 
 constexpr int kAttnWarps = 4;
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct AttnArgs {
-  const __half* q;
-  const __half* k;
-  const __half* v;
-  const int32_t* q_start;
-  const int32_t* k_start;  // prompt form
-  const int32_t* table;    // paged form
-  const int32_t* total;
-  const int64_t* tree;
-  __half* o;
-  int32_t* status;
-  int64_t ldq, ldk, ldv, T, Tk, pages, max_pages;
-  int B, Hq, Hkv, page_log2, max_q;
-  float scale_log2;
-};
+constexpr int64_t kMaxLd = 1ll << 31;  // a tensor map's strides are below 2^40 bytes
 
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(kAttnWarps * 32) attn_row_kernel(const AttnArgs a) {
-  constexpr int E = D / 32;  // elements per lane
   const int lane = threadIdx.x & 31;
   const int64_t item = blockIdx.x * (int64_t)kAttnWarps + (threadIdx.x >> 5);
   if (item >= a.T * a.Hq) return;
   const int64_t t = item / a.Hq;
-  const int h = (int)(item - t * a.Hq), hk = h / (a.Hq / a.Hkv);
+  const int h = (int)(item - t * a.Hq);
   int lo = 0, hi = a.B - 1;  // the last request that begins at or before row t
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -70,43 +54,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32) attn_row_kernel(const AttnArg
   const uint64_t word = PAGED && a.tree ? (uint64_t)__ldg(reinterpret_cast<const long long*>(a.tree) + t) : 0;
   const int64_t end = PAGED && a.tree ? len : (prefix + i + 1 < len ? prefix + i + 1 : len);
 
-  float q[E], acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __half2float(a.q[t * a.ldq + h * D + e * 32 + lane]) * a.scale_log2;
-    acc[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int64_t j = 0; j < end; ++j) {
-    if (PAGED && a.tree && j >= prefix && !((word >> (j - prefix)) & 1)) continue;
-    int64_t at_k, at_v;
-    if (PAGED) {
-      const int64_t pg = __ldg(a.table + lo * a.max_pages + (j >> a.page_log2));
-      if (pg < 0 || pg >= a.pages) {
-        if (lane == 0) set_status(a.status, TB_DEV_BAD_SLOT);
-        continue;
-      }
-      at_k = at_v = (((pg * a.Hkv + hk) << a.page_log2) + (j & ((1ll << a.page_log2) - 1))) * D;
-    } else {
-      at_k = (k0 + j) * a.ldk + hk * D;
-      at_v = (k0 + j) * a.ldv + hk * D;
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], __half2float(a.k[at_k + e * 32 + lane]), s);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const float m2 = fmaxf(m, s);
-    if (m2 == -INFINITY && s == -INFINITY) continue;  // a weight of zero
-    const float c = exp2f(m - m2), w = exp2f(s - m2);
-    l = l * c + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, __half2float(a.v[at_v + e * 32 + lane]), acc[e] * c);
-    m = m2;
-  }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) a.o[(t * a.Hq + h) * D + e * 32 + lane] = __float2half_rn(acc[e] * inv);
+  attend_row<D, PAGED>(a, t, h, lo, k0, end, prefix, word, lane);
 }
 
 template <bool PAGED>
@@ -130,7 +78,9 @@ extern "C" int tb_prompt_attention(const uint16_t* q, int64_t ldq, const uint16_
       Hq > 1024 || Hq % Hkv)
     return TB_ERR_SHAPE;
   if (!supported_head(D)) return TB_ERR_UNSUPPORTED;
-  if (ldq < Hq * D || ldk < Hkv * D || ldv < Hkv * D || ldq % 8 || ldk % 8 || ldv % 8) return TB_ERR_SHAPE;
+  if (ldq < Hq * D || ldk < Hkv * D || ldv < Hkv * D || ldq % 8 || ldk % 8 || ldv % 8 || ldq > kMaxLd || ldk > kMaxLd ||
+      ldv > kMaxLd)
+    return TB_ERR_SHAPE;
   if (!(scale > 0.f && scale < INFINITY)) return TB_ERR_VALUE;
   if (Tq == 0) return TB_OK;
   if (!q || !o || !q_start || !k_start || (Tk && (!k || !v))) return TB_ERR_NULL;
@@ -153,7 +103,7 @@ extern "C" int tb_prompt_attention(const uint16_t* q, int64_t ldq, const uint16_
   a.Hq = (int)Hq;
   a.Hkv = (int)Hkv;
   a.scale_log2 = scale * kLog2e;
-  return launch_rows<false>(a, D, static_cast<cudaStream_t>(stream));
+  return launch_prompt_tiles(a, D, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t tb_tree_attention_workspace_size(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv,

@@ -1,0 +1,498 @@
+// Causal attention over packed prompts on tcgen05 (csrc/tb_attention.cu has the entry point's checks
+// and the row-by-row form).
+//
+// A tile is up to 128 rows of one KV head, a row being one (token, query head) pair: the query heads
+// that share the KV head lie next to each other in q, so a tile of 128 / G tokens by G heads is one
+// box of a 3-D tensor map.  Short requests fill a tile with few tokens, and the causal edge wastes
+// G times less than tiles of 128 tokens would.
+//
+// Per tile of 128 keys:  S = Q K^T (tensor memory, 128 x 128 fp32, two buffers), softmax with the
+// running maximum and sum in registers (one thread per row), P in fp16 back into S's columns, and
+// O += P V (tensor memory, 128 x D fp32).  The MMA thread issues S of the next tile before it waits
+// for P of this one, so the tensor cores work through the softmax.
+//   D = 256: 16.8 MFLOP a tile are 2048 clocks at 8192 FLOP per clock; 16384 exponentials 512 to 1024.
+// CG = 2: a CTA pair (cta_group::2) runs 256 rows on the same keys; each CTA loads half of K (its 64
+// keys) and half of V (its half of the columns) and the tensor cores read both halves.  One CTA alone
+// reads Q, K and V at 128 bytes a clock, all that shared memory gives, and loads 64 bytes a clock
+// from L2; the pair halves the K and V part of both.
+//
+// Precision: S, maxima, sums and O in fp32; P is rounded to fp16, O once at the end.  O is rescaled
+// only when a row's maximum has grown by more than 2^8 since the last time (P stays below 2^8, far
+// inside fp16, and the sum carries the same factor).
+//
+// Keys a row does not see get P = 0, which keeps them out as long as V is finite; a row whose output
+// is not finite is computed again from the keys it sees alone (attend_row).
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "tb_attention.cuh"
+#include "tb_attn_tc.cuh"
+#include "tb_host.h"
+
+namespace tb {
+
+constexpr int kPaThreads = 192;  // warps 0-3: softmax, one per tensor-memory lane quarter; 4: loads; 5: MMAs
+constexpr int kPaKeys = 128;     // keys per tile
+constexpr int kPaSlot = 16384;   // bytes of a ring slot
+#ifndef PA_CG
+#define PA_CG 1
+#endif
+
+template <int D, int CG>
+struct PaCfg {
+  static constexpr int kChunks = D / 64;             // 128-byte wide pieces of a row
+  static constexpr int kQBytes = kChunks * 16384;    // 128 rows
+  // K: each CTA holds 128 / CG keys, all of D; a slot holds kKChunks pieces of them
+  static constexpr int kKRows = kPaKeys / CG;
+  static constexpr int kKChunks = kPaSlot / (kKRows * 128);
+  static constexpr int kKSlots = kChunks / kKChunks;
+  // V: each CTA holds D / CG columns (kVChunks pieces) of all keys; a slot holds kVKeys keys
+  static constexpr int kVChunks = kChunks / CG;
+  static constexpr int kVKeys = kPaSlot / (kVChunks * 128);
+  static constexpr int kVSlots = kPaKeys / kVKeys;
+  static_assert(kKSlots >= 1 && kVChunks >= 1 && kVKeys <= kPaKeys, "D = 64 has no pair form");
+  static constexpr int kSlots = (220 * 1024 - kQBytes) / kPaSlot > 12 ? 12 : (220 * 1024 - kQBytes) / kPaSlot;
+  static constexpr int kSmem = 1024 + kQBytes + kSlots * kPaSlot + 512;
+  static constexpr uint32_t kIdescQK = (1u << 4) | ((uint32_t)(kPaKeys >> 3) << 17) | ((uint32_t)(128 * CG >> 4) << 24);
+  static constexpr uint32_t kIdescPV =
+      (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(128 * CG >> 4) << 24);
+  static constexpr uint32_t kTmemO = 2 * kPaKeys;  // columns: S0 | S1 | O
+};
+
+struct PaArgs {
+  AttnArgs a;
+  int gp, tok;      // query heads per tile, tokens per CTA's tile
+  int head_parts;   // tiles side by side over the heads: Hkv * (G / gp)
+};
+
+template <int D, int CG>
+__global__ void __launch_bounds__(kPaThreads, 1)
+    prompt_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const PaArgs p) {
+  using C = PaCfg<D, CG>;
+  const AttnArgs& a = p.a;
+  extern __shared__ uint8_t pa_raw[];
+  const uint32_t raw = smem_u32(pa_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = pa_raw + (base - raw);
+  const uint32_t ring = base + C::kQBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kQBytes + C::kSlots * kPaSlot);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + C::kSlots;
+  uint64_t* q_full = bars + 2 * C::kSlots;
+  uint64_t* s_full = q_full + 1;   // [2]
+  uint64_t* p_full = q_full + 3;   // [2]
+  uint64_t* o_done = q_full + 5;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 6);
+  __shared__ volatile int aborted;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = CG > 1 ? cta_rank_in_cluster() : 0;
+  const int64_t item = blockIdx.x / CG;
+
+  if (tid == 0) {
+    aborted = 0;
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(s_full, 1);
+    mbar_init(s_full + 1, 1);
+    mbar_init(p_full, 4 * CG);  // lane 0 of each softmax warp
+    mbar_init(p_full + 1, 4 * CG);
+    mbar_init(o_done, 1);
+    fence_barrier_init();
+  }
+  if (warp == 5) tmem_alloc_cg<CG>(tmem_slot, 512);
+
+  // the request and tile of this item: tiles of all requests in order, a request's last (longest)
+  // tile first, the heads side by side
+  const int hp = (int)(item % p.head_parts);
+  const int64_t tile_all = item / p.head_parts;
+  const int span = p.tok * CG;
+  int b = -1, tile = 0;
+  {
+    auto tiles = [&](int r) -> int64_t {
+      const int64_t x = __ldg(a.q_start + r), y = __ldg(a.q_start + r + 1);
+      if (x < 0 || y < x || y > a.T) return 0;
+      return (y - x + span - 1) / span;
+    };
+    // every warp looks for itself: a lane adds up its share of the requests, then a scan
+    const int per = (a.B + 31) / 32;
+    int64_t own = 0;
+    for (int i = lane * per; i < (lane + 1) * per && i < a.B; ++i) own += tiles(i);
+    int64_t upto = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += x;
+    }
+    int64_t before = upto - own;
+    const bool here = tile_all >= before && tile_all < upto;
+    if (here) {
+      for (int i = lane * per; b < 0; ++i) {
+        const int64_t t = tiles(i);
+        if (tile_all < before + t) {
+          b = i;
+          tile = (int)(t - 1 - (tile_all - before));
+        }
+        before += t;
+      }
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, here);
+    if (who) {
+      b = __shfl_sync(0xffffffffu, b, __ffs(who) - 1);
+      tile = __shfl_sync(0xffffffffu, tile, __ffs(who) - 1);
+    }
+    if (item == 0 && a.status) {  // the first item looks at every request's row starts
+      for (int b = tid; b < a.B; b += kPaThreads) {
+        const int64_t x = __ldg(a.q_start + b), y = __ldg(a.q_start + b + 1);
+        const int64_t u = __ldg(a.k_start + b), w = __ldg(a.k_start + b + 1);
+        if (x < 0 || y < x || y > a.T || u < 0 || w < u || w > a.Tk) set_status(a.status, TB_DEV_BAD_LEN);
+      }
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if constexpr (CG > 1) cluster_barrier();  // the peer's barriers exist
+  tmem_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  int64_t q0 = 0, lq = 0, k0 = 0, lk = 0;
+  if (b >= 0) {
+    q0 = __ldg(a.q_start + b);
+    lq = __ldg(a.q_start + b + 1) - q0;
+    k0 = __ldg(a.k_start + b);
+    lk = __ldg(a.k_start + b + 1) - k0;
+    if (k0 < 0 || lk < 0 || k0 + lk > a.Tk) {
+      k0 = 0;
+      lk = 0;
+    }
+  }
+  const int G = a.Hq / a.Hkv, parts = G / p.gp;
+  const int hk = hp / parts, h0 = hk * G + (hp % parts) * p.gp;
+  const int64_t span0 = (int64_t)tile * span;            // the pair's first token in the request
+  const int64_t t0 = span0 + (int64_t)rank * p.tok;          // this CTA's first token
+  // keys that the pair's last token sees: the same count of tiles in both CTAs
+  int64_t last = span0 + span - 1;
+  if (last > lq - 1) last = lq - 1;
+  int64_t keys = b >= 0 ? last + lk - lq + 1 : 0;
+  if (keys < 0) keys = 0;
+  const int n = (int)((keys + kPaKeys - 1) / kPaKeys);
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity) || aborted) return;
+    if (!mbar_wait(bar, parity)) {
+      aborted = 1;
+      set_status(a.status, TB_DEV_TIMEOUT);
+    }
+  };
+  auto wait_cluster = [&](uint64_t* bar, uint32_t parity) {  // arrivals from both CTAs
+    if (CG == 1) {
+      wait(bar, parity);
+      return;
+    }
+    if (mbar_try_wait_cluster(bar, parity) || aborted) return;
+    const uint64_t t = globaltimer_ns();
+    while (!mbar_try_wait_cluster(bar, parity)) {
+      if (aborted || globaltimer_ns() - t > TB_WAIT_NS) {
+        aborted = 1;
+        set_status(a.status, TB_DEV_TIMEOUT);
+        return;
+      }
+    }
+  };
+
+  if (warp == 4) {
+    if (lane == 0 && n > 0) {
+      const uint32_t qbar = CG > 1 ? cluster_addr(q_full, 0) : smem_u32(q_full);
+      if (rank == 0) mbar_arrive_expect_tx(q_full, CG * C::kChunks * 128 * p.gp * p.tok);
+#pragma unroll
+      for (int c = 0; c < C::kChunks; ++c)
+        tma_load_3d<CG>(base + c * 16384, &tmQ, c * 64, h0, (int)(q0 + t0), qbar);
+      int it = 0;
+      auto slot = [&](auto&& issue) {  // the next free slot; `issue` loads kPaSlot bytes into it
+        const int s = it % C::kSlots, ph = it / C::kSlots;
+        if (ph > 0) wait(empty + s, (ph - 1) & 1);
+        if (rank == 0) mbar_arrive_expect_tx(full + s, CG * kPaSlot);
+        issue(ring + s * kPaSlot, CG > 1 ? cluster_addr(full + s, 0) : smem_u32(full + s));
+        ++it;
+      };
+      auto load_k = [&](int i) {
+        const int row = (int)(k0 + (int64_t)i * kPaKeys) + (int)rank * C::kKRows;
+        for (int s = 0; s < C::kKSlots; ++s)
+          slot([&](uint32_t dst, uint32_t bar) {
+#pragma unroll
+            for (int c = 0; c < C::kKChunks; ++c)
+              tma_load_3d<CG>(dst + c * (C::kKRows * 128), &tmK, (s * C::kKChunks + c) * 64, hk, row, bar);
+          });
+      };
+      auto load_v = [&](int i) {
+        for (int s = 0; s < C::kVSlots; ++s) {
+          const int row = (int)(k0 + (int64_t)i * kPaKeys) + s * C::kVKeys;
+          slot([&](uint32_t dst, uint32_t bar) {
+#pragma unroll
+            for (int c = 0; c < C::kVChunks; ++c)
+              tma_load_3d<CG>(dst + c * (C::kVKeys * 128), &tmV, ((int)rank * C::kVChunks + c) * 64, hk, row, bar);
+          });
+        }
+      };
+      load_k(0);
+      for (int i = 0; i < n; ++i) {
+        if (i + 1 < n) load_k(i + 1);
+        load_v(i);
+      }
+      if (aborted) {  // a wait gave up: leave the copies in flight time to land before the CTA ends
+        const uint64_t t = globaltimer_ns();
+        while (globaltimer_ns() - t < 1000000) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    if (lane == 0 && rank == 0 && n > 0) {
+      int it = 0;
+      wait(q_full, 0);
+      tmem_fence_after();
+      auto qk = [&](int i) {
+        const uint32_t d = tmem + (uint32_t)(i & 1) * kPaKeys;
+        for (int s = 0; s < C::kKSlots; ++s, ++it) {
+          const int r = it % C::kSlots;
+          wait(full + r, (it / C::kSlots) & 1);
+          tmem_fence_after();
+#pragma unroll
+          for (int c = 0; c < C::kKChunks; ++c)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ss<CG>(d, smem_desc_sw128(base + (s * C::kKChunks + c) * 16384 + kk * 32, 1024),
+                             smem_desc_sw128(ring + r * kPaSlot + c * (C::kKRows * 128) + kk * 32, 1024), C::kIdescQK,
+                             (s | c | kk) != 0);
+          mma_commit_cg<CG>(empty + r);
+        }
+        mma_commit_cg<CG>(s_full + (i & 1));
+      };
+      qk(0);
+      for (int i = 0; i < n; ++i) {
+        if (i + 1 < n) qk(i + 1);
+        wait_cluster(p_full + (i & 1), (i >> 1) & 1);
+        tmem_fence_after();
+        for (int s = 0; s < C::kVSlots; ++s, ++it) {
+          const int r = it % C::kSlots;
+          wait(full + r, (it / C::kSlots) & 1);
+          tmem_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < C::kVKeys / 16; ++kk)
+            mma_f16_ts<CG>(tmem + C::kTmemO, tmem + (uint32_t)(i & 1) * kPaKeys + (s * (C::kVKeys / 16) + kk) * 8,
+                           smem_desc_mn128(ring + r * kPaSlot + kk * 2048, C::kVKeys * 128, 1024), C::kIdescPV,
+                           (i | s | kk) != 0);
+          mma_commit_cg<CG>(empty + r);
+        }
+        mma_commit_cg<CG>(o_done);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax: thread = row
+    const int row = warp * 32 + lane;
+    const int tr = row / p.gp, head = h0 + row - tr * p.gp;
+    const int64_t tok = t0 + tr;
+    const bool live = b >= 0 && tr < p.tok && tok < lq;
+    int64_t lim64 = live ? tok + lk - lq + 1 : 0;  // keys [0, lim) are visible
+    if (lim64 < 0) lim64 = 0;
+    const uint32_t mine = tmem + ((uint32_t)warp << 21);  // lane quarter: 32 lanes, in bits 16..
+    const float sc = a.scale_log2;
+    float m = -INFINITY, l = 0.f;  // the maximum in use (log2 units after scaling), and the sum
+    const uint32_t pbar0 = CG > 1 ? cluster_addr(p_full, 0) : smem_u32(p_full);
+    for (int i = 0; i < n; ++i) {
+      const int buf = i & 1;
+      wait(s_full + buf, (i >> 1) & 1);
+      tmem_fence_after();
+      float s[kPaKeys];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(mine + buf * kPaKeys + c * 32, s + 32 * c);
+      tmem_wait_ld();
+      const int64_t left = lim64 - (int64_t)i * kPaKeys;
+      if (__any_sync(0xffffffffu, left < kPaKeys)) {
+        const int lim = left < 0 ? 0 : (left > kPaKeys ? kPaKeys : (int)left);
+#pragma unroll
+        for (int c = 0; c < kPaKeys; ++c) s[c] = c < lim ? s[c] : -INFINITY;
+      }
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mx[c] = fmaxf(s[c], s[c + 4]);
+#pragma unroll
+      for (int c = 8; c < kPaKeys; c += 4)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
+      const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      // a new reference only when the old one is 2^8 too small (or there is none yet)
+      const bool grow = tmax > m + 8.f || (m == -INFINITY && tmax > -INFINITY);
+      if (__any_sync(0xffffffffu, grow && i > 0)) {
+        const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - tmax)) : 1.f;
+        l *= f;
+        wait(o_done, (i - 1) & 1);
+        tmem_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(mine + C::kTmemO + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 r = mul_f32x2(make_float2(o[e], o[e + 1]), make_float2(f, f));
+            o[e] = r.x;
+            o[e + 1] = r.y;
+          }
+          tmem_st32(mine + C::kTmemO + c, reinterpret_cast<uint32_t(&)[32]>(o));
+        }
+        tmem_wait_st();
+      }
+      if (grow) m = tmax;
+      const float ms = m == -INFINITY ? 0.f : -m;
+      float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int c = half * 64 + e * 2;
+          float2 x = fma_f32x2(make_float2(s[c], s[c + 1]), make_float2(sc, sc), make_float2(ms, ms));
+          x.x = ex2(x.x);
+          x.y = ex2(x.y);
+          if (e & 1) acc1 = add_f32x2(acc1, x);
+          else acc0 = add_f32x2(acc0, x);
+          pk[e] = pack_half2(x.x, x.y);
+        }
+        tmem_st32(mine + buf * kPaKeys + half * 32, pk);
+      }
+      acc0 = add_f32x2(acc0, acc1);
+      l += acc0.x + acc0.y;
+      tmem_wait_st();
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG > 1) mbar_arrive_cluster(pbar0 + 8u * (uint32_t)buf);
+        else mbar_arrive(p_full + buf);
+      }
+    }
+    // ---- O / l -> fp16
+    // one phase per tile; all but the last two are known to be over (S of the last tile came after
+    // them), and a parity tells only neighbouring phases apart: wait for both
+    if (n > 1) wait(o_done, (n - 2) & 1);
+    if (n > 0) {
+      wait(o_done, (n - 1) & 1);
+      tmem_fence_after();
+    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    bool odd = false;
+    __half* dst = a.o + ((q0 + tok) * a.Hq + head) * D;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      float o[32];
+      if (n > 0) {
+        tmem_ld32(mine + C::kTmemO + c, o);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (n > 0 && lim64 > 0) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) odd |= !(fabsf(o[e + x]) < INFINITY);
+          w = make_uint4(pack_half2(o[e] * inv, o[e + 1] * inv), pack_half2(o[e + 2] * inv, o[e + 3] * inv),
+                         pack_half2(o[e + 4] * inv, o[e + 5] * inv), pack_half2(o[e + 6] * inv, o[e + 7] * inv));
+        }
+        if (live) *reinterpret_cast<uint4*>(dst + c + e) = w;
+      }
+    }
+    odd = live && lim64 > 0 && (odd || !(l < INFINITY));
+    unsigned again = __ballot_sync(0xffffffffu, odd);
+    while (again) {
+      const int r = __ffs(again) - 1;
+      again &= again - 1;
+      const int64_t rt = __shfl_sync(0xffffffffu, q0 + tok, r);
+      const int rh = __shfl_sync(0xffffffffu, head, r);
+      const int64_t rl = __shfl_sync(0xffffffffu, lim64, r);
+      attend_row<D, false>(a, rt, rh, b, k0, rl, rl, 0, lane);
+    }
+  }
+
+  tmem_fence_before();
+  __syncthreads();
+  if constexpr (CG > 1) cluster_barrier();  // no CTA leaves while its peer may still signal it or read it
+  if (warp == 5) tmem_dealloc_cg<CG>(tmem, 512);
+}
+
+// 3-D map [tokens, heads, D] with `ld` elements between tokens; box 64 x heads x tokens
+static int token_map(CUtensorMap* m, const __half* p, int64_t tokens, int64_t heads, int64_t D, int64_t ld, int box_heads,
+                     int box_tokens) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return TB_ERR_CUDA;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(p), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? TB_OK : TB_ERR_CUDA;
+}
+
+template <int D, int CG>
+static int launch_tiles(const PaArgs& p, int sms_device, cudaStream_t s) {
+  using C = PaCfg<D, CG>;
+  const AttnArgs& a = p.a;
+  CUtensorMap tq, tk, tv;
+  int rc = token_map(&tq, a.q, a.T, a.Hq, D, a.ldq, p.gp, p.tok);
+  // without any keys the maps of K and V are never used, but have to be maps
+  const int64_t Tk = a.Tk ? a.Tk : 1;
+  if (rc == TB_OK) rc = token_map(&tk, a.Tk ? a.k : a.q, Tk, a.Hkv, D, a.ldk, 1, C::kKRows);
+  if (rc == TB_OK) rc = token_map(&tv, a.Tk ? a.v : a.q, Tk, a.Hkv, D, a.ldv, 1, C::kVKeys);
+  if (rc != TB_OK) return rc;
+  auto* fn = prompt_attn_kernel<D, CG>;
+  rc = ensure_dynamic_smem(reinterpret_cast<const void*>(fn), sms_device, C::kSmem);
+  if (rc != TB_OK) return rc;
+  const int64_t span = (int64_t)p.tok * CG;
+  const int64_t blocks = (a.T / span + a.B) * p.head_parts * CG;  // at most: ceil(x) <= floor(x) + 1 per request
+  if (blocks > INT32_MAX) return TB_ERR_TOO_LARGE;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kPaThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, tq, tk, tv, p);
+  if (e != cudaSuccess) {
+    record_cuda_error(e);
+    return TB_ERR_CUDA;
+  }
+  return check_launch();
+}
+
+int launch_prompt_tiles(const AttnArgs& a, int64_t D, cudaStream_t s) {
+  DeviceFacts f;
+  const int rc = device_facts(&f);
+  if (rc != TB_OK) return rc;
+  PaArgs p;
+  p.a = a;
+  // query heads per tile: the largest divisor of the group that leaves at most 8 of 128 rows unused
+  // (a group of a prime above 128 falls back to one head per tile)
+  const int G = a.Hq / a.Hkv;
+  p.gp = 1;
+  for (int d = 1; d <= G && d <= 128; ++d)
+    if (G % d == 0 && 128 / d * d >= 120) p.gp = d;
+  p.tok = 128 / p.gp;
+  p.head_parts = a.Hkv * (G / p.gp);
+  if (D == 64) return launch_tiles<64, 1>(p, f.device, s);
+  if (D == 128) return launch_tiles<128, PA_CG>(p, f.device, s);
+  return launch_tiles<256, PA_CG>(p, f.device, s);
+}
+
+}  // namespace tb
