@@ -35,9 +35,6 @@ namespace tb {
 constexpr int kPaThreads = 192;  // warps 0-3: softmax, one per tensor-memory lane quarter; 4: loads; 5: MMAs
 constexpr int kPaKeys = 128;     // keys per tile
 constexpr int kPaSlot = 16384;   // bytes of a ring slot
-#ifndef PA_CG
-#define PA_CG 1
-#endif
 
 template <int D, int CG>
 struct PaCfg {
@@ -491,8 +488,8 @@ int launch_prompt_tiles(const AttnArgs& a, int64_t D, cudaStream_t s) {
   p.tok = 128 / p.gp;
   p.head_parts = a.Hkv * (G / p.gp);
   if (D == 64) return launch_tiles<64, 1>(p, f.device, s);
-  if (D == 128) return launch_tiles<128, PA_CG>(p, f.device, s);
-  return launch_tiles<256, PA_CG>(p, f.device, s);
+  if (D == 128) return launch_tiles<128, 2>(p, f.device, s);
+  return launch_tiles<256, 2>(p, f.device, s);
 }
 
 }  // namespace tb
