@@ -23,8 +23,11 @@ TB_DEVI uint32_t cluster_addr(const void* p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
+// Arrival on a barrier of either CTA of the pair that hands over tensor memory alone: the order comes
+// from the tcgen05 fences around it, so it releases nothing (a release at cluster scope waits for
+// all earlier memory operations of the thread, and cost 15 % of the prompt kernel).
 TB_DEVI void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 TB_DEVI bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
