@@ -1,9 +1,7 @@
 // Attention of the hybrid model's full-attention layers: over whole prompts, and over the paged
 // cache for one token or a tree of drafted tokens per request.
 //   o_i = sum_j w_ij v_j,  w_ij = softmax over the visible j of scale q_i . k_j;  no visible j: 0.
-//
-// One warp per (row, query head): the lanes share the head's elements, one key at a time, with the
-// softmax's running maximum and sum, so every key and value is read once per row.
+// The kernels are in tb_attn_prompt.cu and tb_attn_tree.cu; here are the entry points' checks.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -13,59 +11,7 @@
 
 namespace tb {
 
-constexpr int kAttnWarps = 4;
 constexpr int64_t kMaxLd = 1ll << 31;  // a tensor map's strides are below 2^40 bytes
-
-template <int D, bool PAGED>
-__global__ void __launch_bounds__(kAttnWarps * 32) attn_row_kernel(const AttnArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = blockIdx.x * (int64_t)kAttnWarps + (threadIdx.x >> 5);
-  if (item >= a.T * a.Hq) return;
-  const int64_t t = item / a.Hq;
-  const int h = (int)(item - t * a.Hq);
-  int lo = 0, hi = a.B - 1;  // the last request that begins at or before row t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(a.q_start + mid) <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  const int64_t r0 = __ldg(a.q_start + lo), r1 = __ldg(a.q_start + lo + 1);
-  if (r0 < 0 || t < r0 || r1 > a.T) {
-    if (lane == 0) set_status(a.status, TB_DEV_BAD_LEN);
-    return;
-  }
-  if (t >= r1) return;  // a row of no request
-  const int64_t n = r1 - r0, i = t - r0;
-  int64_t len, k0 = 0;
-  bool ok = true;
-  if (PAGED) {
-    len = __ldg(a.total + lo);
-    ok = n <= a.max_q && len >= n && len <= a.max_pages << a.page_log2;
-  } else {
-    k0 = __ldg(a.k_start + lo);
-    len = __ldg(a.k_start + lo + 1) - k0;
-    ok = k0 >= 0 && len >= 0 && k0 + len <= a.Tk;
-  }
-  if (!ok) {
-    if (lane == 0) set_status(a.status, TB_DEV_BAD_LEN);
-    len = 0;
-  }
-  const int64_t prefix = len - n;
-  const uint64_t word = PAGED && a.tree ? (uint64_t)__ldg(reinterpret_cast<const long long*>(a.tree) + t) : 0;
-  const int64_t end = PAGED && a.tree ? len : (prefix + i + 1 < len ? prefix + i + 1 : len);
-
-  attend_row<D, PAGED>(a, t, h, lo, k0, end, prefix, word, lane);
-}
-
-template <bool PAGED>
-static int launch_rows(const AttnArgs& a, int64_t D, cudaStream_t s) {
-  const int64_t blocks = (a.T * a.Hq + kAttnWarps - 1) / kAttnWarps;
-  if (blocks > INT32_MAX) return TB_ERR_TOO_LARGE;
-  if (D == 64) attn_row_kernel<64, PAGED><<<(int)blocks, kAttnWarps * 32, 0, s>>>(a);
-  else if (D == 128) attn_row_kernel<128, PAGED><<<(int)blocks, kAttnWarps * 32, 0, s>>>(a);
-  else attn_row_kernel<256, PAGED><<<(int)blocks, kAttnWarps * 32, 0, s>>>(a);
-  return check_launch();
-}
 
 }  // namespace tb
 
@@ -108,13 +54,10 @@ extern "C" int tb_prompt_attention(const uint16_t* q, int64_t ldq, const uint16_
 
 extern "C" size_t tb_tree_attention_workspace_size(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv,
                                                    int64_t D) {
-  (void)B;
+  using namespace tb;
   (void)T;
-  (void)max_q;
-  (void)Hq;
-  (void)Hkv;
-  (void)D;
-  return 0;
+  if (B < 1 || max_q < 1 || max_q > 64 || Hkv < 1 || Hq < Hkv || Hq % Hkv || !supported_head(D)) return 0;
+  return tree_workspace(B, max_q, Hq, Hkv, D);
 }
 
 extern "C" int tb_tree_attention(const uint16_t* q, int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
@@ -128,15 +71,15 @@ extern "C" int tb_tree_attention(const uint16_t* q, int64_t ldq, int64_t T, int6
       pages > INT32_MAX || max_pages < 1 || max_pages > INT32_MAX || max_q < 1)
     return TB_ERR_SHAPE;
   if (!supported_head(D) || !supported_page(page)) return TB_ERR_UNSUPPORTED;
-  if (ldq < Hq * D || ldq % 8) return TB_ERR_SHAPE;
-  if (max_q > 64) return TB_ERR_TOO_LARGE;
+  if (ldq < Hq * D || ldq % 8 || ldq > kMaxLd) return TB_ERR_SHAPE;
+  if (max_q > 64 || pages * Hkv > INT32_MAX || B * Hq * max_q > INT32_MAX) return TB_ERR_TOO_LARGE;
   if (!(scale > 0.f && scale < INFINITY)) return TB_ERR_VALUE;
   if (T == 0) return TB_OK;
   if (!q || !k_cache || !v_cache || !table || !total || !row_start || !o) return TB_ERR_NULL;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned_to(table, 4) || !aligned_to(total, 4) ||
       !aligned_to(row_start, 4) || !aligned_to(tree, 8) || !aligned16(o) || !aligned16(workspace))
     return TB_ERR_ALIGN;
-  if (workspace_bytes < tb_tree_attention_workspace_size(B, T, max_q, Hq, Hkv, D)) return TB_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < tb_tree_attention_workspace_size(B, T, max_q, Hq, Hkv, D)) return TB_ERR_WORKSPACE;
   AttnArgs a = {};
   a.q = reinterpret_cast<const __half*>(q);
   a.k = reinterpret_cast<const __half*>(k_cache);
@@ -157,5 +100,5 @@ extern "C" int tb_tree_attention(const uint16_t* q, int64_t ldq, int64_t T, int6
   a.page_log2 = log2_of(page);
   a.max_q = (int)max_q;
   a.scale_log2 = scale * kLog2e;
-  return launch_rows<true>(a, D, static_cast<cudaStream_t>(stream));
+  return launch_tree_tiles(a, D, workspace, static_cast<cudaStream_t>(stream));
 }

@@ -1,6 +1,7 @@
 // What the attention kernels share: the arguments, and one row by one warp.
 #pragma once
 
+#include <cuda.h>
 #include <math.h>
 
 #include "tb_common.cuh"
@@ -27,8 +28,8 @@ struct AttnArgs {
 
 // o of row t, query head h, from keys [0, end) of request b, by one warp: the lanes share the head's
 // elements, one key at a time, with the softmax's running maximum and sum, so every key and value is
-// read once.  k0: the request's first key row (packed form); past `prefix` only keys whose bit is set
-// in `word` count (paged form with a tree).  Only keys the row sees are read.
+// read once.  k0: the request's first key row (packed form); from `prefix` on only keys whose bit
+// is set in `word` count (paged form).  Only keys the row sees are read.
 template <int D, bool PAGED>
 TB_DEVI void attend_row(const AttnArgs& a, int64_t t, int h, int64_t b, int64_t k0, int64_t end, int64_t prefix,
                         uint64_t word, int lane) {
@@ -42,7 +43,7 @@ TB_DEVI void attend_row(const AttnArgs& a, int64_t t, int h, int64_t b, int64_t 
   }
   float m = -INFINITY, l = 0.f;
   for (int64_t j = 0; j < end; ++j) {
-    if (PAGED && a.tree && j >= prefix && !((word >> (j - prefix)) & 1)) continue;
+    if (PAGED && j >= prefix && !((word >> (j - prefix)) & 1)) continue;
     int64_t at_k, at_v;
     if (PAGED) {
       const int64_t pg = __ldg(a.table + b * a.max_pages + (j >> a.page_log2));
@@ -73,7 +74,24 @@ TB_DEVI void attend_row(const AttnArgs& a, int64_t t, int h, int64_t b, int64_t 
   for (int e = 0; e < E; ++e) a.o[(t * a.Hq + h) * D + e * 32 + lane] = __float2half_rn(acc[e] * inv);
 }
 
+// query heads of one KV head in a tile of 128 rows: the largest divisor of the group that leaves at
+// most 8 rows unused (a group that is a prime above 128 falls back to one head per tile)
+inline int heads_per_tile(int group) {
+  int best = 1;
+  for (int d = 1; d <= group && d <= 128; ++d)
+    if (group % d == 0 && 128 / d * d >= 120) best = d;
+  return best;
+}
+
+// tensor map of fp16 [tokens, heads, D] with `ld` elements between tokens; box 64 x heads x tokens
+int token_map(CUtensorMap* m, const __half* p, int64_t tokens, int64_t heads, int64_t D, int64_t ld, int box_heads,
+              int box_tokens);
+
 // prompt form on the tensor cores
 int launch_prompt_tiles(const AttnArgs& a, int64_t D, cudaStream_t s);
+
+// paged form on the tensor cores, and its workspace
+int launch_tree_tiles(const AttnArgs& a, int64_t D, void* workspace, cudaStream_t s);
+size_t tree_workspace(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D);
 
 }  // namespace tb

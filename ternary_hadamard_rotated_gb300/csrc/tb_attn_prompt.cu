@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 }
 
 // 3-D map [tokens, heads, D] with `ld` elements between tokens; box 64 x heads x tokens
-static int token_map(CUtensorMap* m, const __half* p, int64_t tokens, int64_t heads, int64_t D, int64_t ld, int box_heads,
+int token_map(CUtensorMap* m, const __half* p, int64_t tokens, int64_t heads, int64_t D, int64_t ld, int box_heads,
                      int box_tokens) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return TB_ERR_CUDA;
@@ -479,12 +479,8 @@ int launch_prompt_tiles(const AttnArgs& a, int64_t D, cudaStream_t s) {
   if (rc != TB_OK) return rc;
   PaArgs p;
   p.a = a;
-  // query heads per tile: the largest divisor of the group that leaves at most 8 of 128 rows unused
-  // (a group of a prime above 128 falls back to one head per tile)
   const int G = a.Hq / a.Hkv;
-  p.gp = 1;
-  for (int d = 1; d <= G && d <= 128; ++d)
-    if (G % d == 0 && 128 / d * d >= 120) p.gp = d;
+  p.gp = heads_per_tile(G);
   p.tok = 128 / p.gp;
   p.head_parts = a.Hkv * (G / p.gp);
   if (D == 64) return launch_tiles<64, 1>(p, f.device, s);

@@ -1,0 +1,640 @@
+// Attention of the newest tokens over the paged cache, on tcgen05: one token per request (decode), a
+// run, or a tree of drafted tokens (csrc/tb_attention.cu has the entry point's checks).
+//
+// A tile is up to 128 rows of one KV head (row = token of the request x query head of the group) by
+// 128 keys, as in the prompt kernel.  With the few rows of decode most of the MMA's 128 rows are
+// idle, and that costs nothing: a tile's K and V are 512 D bytes, which at 6.8 TB/s over 152 SMs
+// arrive in 5600 clocks for D = 256, its two MMA passes take 2048, its softmax about 1000.  So one
+// kernel serves one row to 384, bound by the cache's bytes until several row tiles share them.
+//
+// Work: units of (request, head part, row tile, key tile), key tiles fastest, are cut into one equal
+// contiguous range per SM, so the longest request is spread over as many SMs as its bytes call for.
+// A CTA walks its range as segments (runs of key tiles of one item).  An item inside one range is
+// written at once; one cut between CTAs leaves fp32 parts (O, maximum, sum) in the workspace, and the
+// last CTA to count in adds them in CTA order, so the result does not depend on who came last.
+//
+// Warps 0-3: softmax (thread = row) and epilogue; 4: TMA loads (pages by the block table); 5: MMAs.
+// V rows past the request's last token are zeroed in shared memory before the MMAs read them (what
+// lies there may be anything); a row whose output is not finite is computed again from the keys it
+// sees alone (attend_row).
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "tb_attention.cuh"
+#include "tb_attn_tc.cuh"
+#include "tb_host.h"
+
+namespace tb {
+
+constexpr int kTaThreads = 192;
+constexpr int kTaKeys = 128;
+constexpr int kTaSlot = 16384;
+constexpr int kTaMaxCtas = 160;  // CTAs the workspace has room for
+
+template <int D>
+struct TaCfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kQBytes = kChunks * 16384;
+  static constexpr int kKSlots = kChunks;                     // a slot: 64 elements of 128 keys
+  static constexpr int kVKeys = kTaSlot / (D * 2);            // a slot: all elements of 128 / kChunks keys
+  static constexpr int kVSlots = kTaKeys / kVKeys;
+  static constexpr int kSlots = (220 * 1024 - kQBytes) / kTaSlot > 12 ? 12 : (220 * 1024 - kQBytes) / kTaSlot;
+  static_assert(kSlots > kKSlots + kVSlots, "the loads of a tile never wait for its own MMAs of P V");
+  static constexpr int kSmem = 1024 + kQBytes + kSlots * kTaSlot + 512;
+  static constexpr uint32_t kIdescQK = (1u << 4) | ((uint32_t)(kTaKeys >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+  static constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+  static constexpr uint32_t kTmemO = 2 * kTaKeys;
+};
+
+struct TaArgs {
+  AttnArgs a;
+  int gp, tok, head_parts, row_tiles;  // query heads and tokens per tile; row tiles at max_q tokens
+  int rows;                            // rows of a part in the workspace: gp * tok
+  int kbox, vbox;                      // keys per box of the K and V maps
+  float* part_o;                       // [2 * grid][rows][D]
+  float* part_ml;                      // [2 * grid][rows][2]
+  int* count;                          // [B * head_parts * row_tiles], zero between calls
+};
+
+// a run of key tiles of one item
+struct TaSegment {
+  int b, hp, rt;
+  int tile0, tiles, item_tiles;  // tiles 0: an item whose rows get zeros
+  int64_t q0, n, len;            // the request's first row, rows, and cached tokens
+  int64_t item_unit;             // the item's first unit
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTaThreads, 1)
+    tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const TaArgs p) {
+  using C = TaCfg<D>;
+  const AttnArgs& a = p.a;
+  extern __shared__ uint8_t ta_raw[];
+  const uint32_t raw = smem_u32(ta_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = ta_raw + (base - raw);
+  const uint32_t ring = base + C::kQBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kQBytes + C::kSlots * kTaSlot);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + C::kSlots;
+  uint64_t* q_full = bars + 2 * C::kSlots;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_full + 2;  // [2]
+  uint64_t* p_full = q_full + 4;  // [2]
+  uint64_t* o_done = q_full + 6;
+  uint64_t* o_free = q_full + 7;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 8);
+  __shared__ volatile int aborted;
+  __shared__ int last_flag;
+  __shared__ uint32_t granules[16];  // per key tile: which runs of 16 keys lie in a page of the cache
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    aborted = 0;
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4);  // lane 0 of each softmax warp
+    }
+    mbar_init(o_done, 1);
+    mbar_init(o_free, 4);
+    fence_barrier_init();
+  }
+  if (warp == 5) tmem_alloc(tmem_slot, 512);
+
+  // ---- the schedule: every warp adds up the units of all requests itself
+  struct Req {
+    int64_t q0, n, len;
+    int items, tiles;  // items 0: nothing to write
+    int bad;
+  };
+  auto request = [&](int b) {
+    Req r;
+    r.q0 = __ldg(a.q_start + b);
+    r.n = __ldg(a.q_start + b + 1) - r.q0;
+    r.len = __ldg(a.total + b);
+    r.bad = 0;
+    if (r.q0 < 0 || r.n < 0 || r.q0 + r.n > a.T) {
+      r.bad = 1;
+      r.n = 0;
+    }
+    if (r.n > 0 && (r.n > a.max_q || r.len < r.n || r.len > a.max_pages << a.page_log2)) {
+      r.bad = 1;
+      r.len = 0;
+    }
+    r.items = (int)((r.n + p.tok - 1) / p.tok) * p.head_parts;
+    const int64_t t = (r.len + kTaKeys - 1) / kTaKeys;
+    r.tiles = t > 0 ? (int)t : 1;
+    return r;
+  };
+  const int per = (a.B + 31) / 32;
+  int64_t upto = 0, own = 0;
+  int any_bad = 0;
+  for (int i = lane * per; i < (lane + 1) * per && i < a.B; ++i) {
+    const Req r = request(i);
+    own += (int64_t)r.items * r.tiles;
+    any_bad |= r.bad;
+  }
+  upto = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += x;
+  }
+  const int64_t units = __shfl_sync(0xffffffffu, upto, 31);
+  if (blockIdx.x == 0 && warp == 0 && any_bad) set_status(a.status, TB_DEV_BAD_LEN);
+  const int64_t grid = units < gridDim.x ? units : gridDim.x;  // no CTA of an item is without a unit
+  auto lo_of = [&](int64_t c) { return units * c / grid; };
+  auto owner = [&](int64_t u) { return ((u + 1) * grid - 1) / units; };  // the c with lo_of(c) <= u < lo_of(c + 1)
+  const bool works = blockIdx.x < grid;
+  const int64_t lo = works ? lo_of(blockIdx.x) : 0, hi = works ? lo_of((int64_t)blockIdx.x + 1) : 0;
+  // the segment that starts at unit u (whole warps call this)
+  auto segment = [&](int64_t u) {
+    TaSegment s;
+    const unsigned who = __ballot_sync(0xffffffffu, u < upto);
+    const int src = __ffs(who) - 1;
+    int64_t before = upto - own;
+    int b = 0;
+    if (lane == src) {
+      for (b = lane * per;; ++b) {
+        const Req r = request(b);
+        if (u < before + (int64_t)r.items * r.tiles) break;
+        before += (int64_t)r.items * r.tiles;
+      }
+    }
+    b = __shfl_sync(0xffffffffu, b, src);
+    before = __shfl_sync(0xffffffffu, before, src);
+    const Req r = request(b);
+    const int item = (int)((u - before) / r.tiles);
+    s.b = b;
+    s.hp = item % p.head_parts;
+    s.rt = item / p.head_parts;
+    s.item_unit = before + (int64_t)item * r.tiles;
+    s.tile0 = (int)(u - s.item_unit);
+    s.item_tiles = r.tiles;
+    s.tiles = (int)(hi - u < r.tiles - s.tile0 ? hi - u : r.tiles - s.tile0);
+    s.q0 = r.q0;
+    s.n = r.n;
+    s.len = r.len;
+    return s;
+  };
+  const int G = a.Hq / a.Hkv, parts = G / p.gp;
+
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity) || aborted) return;
+    if (!mbar_wait(bar, parity)) {
+      aborted = 1;
+      set_status(a.status, TB_DEV_TIMEOUT);
+    }
+  };
+
+  if (warp == 4) {
+    int it = 0, seg = 0, gt = 0;
+    for (int64_t u = lo; u < hi;) {
+      const TaSegment s = segment(u);
+      u += s.tiles;
+      if (s.len == 0) continue;
+      const int hk = s.hp / parts, h0 = hk * G + (s.hp % parts) * p.gp;
+      // pages of one key tile: the lanes look them up, lane 0 issues the boxes
+      auto slot = [&]() {
+        const int r = it % C::kSlots, ph = it / C::kSlots;
+        if (lane == 0) {
+          if (ph > 0) wait(empty + r, (ph - 1) & 1);
+          mbar_arrive_expect_tx(full + r, kTaSlot);
+        }
+        ++it;
+        return r;
+      };
+      // z coordinate (page, head) of the 16-key run that this lane (0-7) looks up; out of the map for a
+      // page that is not one (its boxes are filled with zeros), or past the last token
+      auto zrow = [&](int tile) {
+        const int64_t j = (int64_t)tile * kTaKeys + (lane & 7) * 16;
+        int64_t pg = -1;
+        if (j < s.len) {
+          pg = __ldg(a.table + (int64_t)s.b * a.max_pages + (j >> a.page_log2));
+          if (pg < 0 || pg >= a.pages) {
+            pg = -1;
+            if (lane < 8) set_status(a.status, TB_DEV_BAD_SLOT);
+          }
+        }
+        return pg;
+      };
+      const int page = 1 << a.page_log2;
+      auto coord = [&](int64_t pg) { return pg < 0 ? (int)(a.pages * a.Hkv) : (int)(pg * a.Hkv + hk); };
+      auto load_k = [&](int i) {
+        const int tile = s.tile0 + i;
+        const int64_t pg = zrow(tile);
+        const unsigned ok = __ballot_sync(0xffffffffu, pg >= 0) & 0xffu;
+        if (lane == 0) granules[(gt + i) & 15] = ok;
+        for (int c = 0; c < C::kChunks; ++c) {
+          const int r = slot();
+          for (int k = 0; k < kTaKeys; k += p.kbox) {
+            const int64_t g = __shfl_sync(0xffffffffu, pg, k / 16);
+            if (lane == 0)
+              tma_load_3d<1>(ring + r * kTaSlot + k * 128, &tmK, c * 64, (tile * kTaKeys + k) & (page - 1), coord(g),
+                             smem_u32(full + r));
+          }
+        }
+      };
+      auto load_v = [&](int i) {
+        const int tile = s.tile0 + i;
+        const int64_t pg = zrow(tile);
+        for (int v = 0; v < C::kVSlots; ++v) {
+          const int r = slot();
+          for (int k = 0; k < C::kVKeys; k += p.vbox) {
+            const int key = v * C::kVKeys + k;
+            const int64_t g = __shfl_sync(0xffffffffu, pg, key / 16);
+            if (lane == 0)
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_load_3d<1>(ring + r * kTaSlot + c * (C::kVKeys * 128) + k * 128, &tmV, c * 64,
+                               (tile * kTaKeys + key) & (page - 1), coord(g), smem_u32(full + r));
+          }
+        }
+      };
+      load_k(0);
+      if (lane == 0) {
+        if (seg > 0) wait(q_empty, (seg - 1) & 1);
+        mbar_arrive_expect_tx(q_full, C::kChunks * 128 * p.gp * p.tok);
+        for (int c = 0; c < C::kChunks; ++c)
+          tma_load_3d<1>(base + c * 16384, &tmQ, c * 64, h0, (int)(s.q0 + (int64_t)s.rt * p.tok), smem_u32(q_full));
+      }
+      __syncwarp();
+      for (int i = 0; i < s.tiles; ++i) {
+        if (i + 1 < s.tiles) load_k(i + 1);
+        load_v(i);
+      }
+      gt += s.tiles;
+      ++seg;
+    }
+    if (aborted) {  // a wait gave up: leave the copies in flight time to land before the CTA ends
+      const uint64_t t = globaltimer_ns();
+      while (globaltimer_ns() - t < 1000000) {
+      }
+    }
+  } else if (warp == 5) {
+    int it = 0, seg = 0, gt = 0;
+    for (int64_t u = lo; u < hi;) {
+      const TaSegment s = segment(u);
+      u += s.tiles;
+      if (s.len == 0) continue;
+      if (lane == 0) {
+        wait(q_full, seg & 1);
+        tmem_fence_after();
+        auto qk = [&](int i) {
+          const uint32_t d = tmem + (uint32_t)((gt + i) & 1) * kTaKeys;
+          for (int c = 0; c < C::kChunks; ++c, ++it) {
+            const int r = it % C::kSlots;
+            wait(full + r, (it / C::kSlots) & 1);
+            tmem_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ss<1>(d, smem_desc_sw128(base + c * 16384 + kk * 32, 1024),
+                            smem_desc_sw128(ring + r * kTaSlot + kk * 32, 1024), C::kIdescQK, (c | kk) != 0);
+            mma_commit(empty + r);
+          }
+          mma_commit(s_full + ((gt + i) & 1));
+        };
+        qk(0);
+        for (int i = 0; i < s.tiles; ++i) {
+          if (i + 1 < s.tiles) qk(i + 1);
+          else mma_commit(q_empty);
+          if (i == 0 && seg > 0) wait(o_free, (seg - 1) & 1);  // the last segment's O has been read
+          wait(p_full + ((gt + i) & 1), ((gt + i) >> 1) & 1);
+          tmem_fence_after();
+          for (int v = 0; v < C::kVSlots; ++v, ++it) {
+            const int r = it % C::kSlots;
+            wait(full + r, (it / C::kSlots) & 1);
+            tmem_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < C::kVKeys / 16; ++kk)
+              mma_f16_ts<1>(tmem + C::kTmemO, tmem + (uint32_t)((gt + i) & 1) * kTaKeys + (v * (C::kVKeys / 16) + kk) * 8,
+                            smem_desc_mn128(ring + r * kTaSlot + kk * 2048, C::kVKeys * 128, 1024), C::kIdescPV,
+                            (i | v | kk) != 0);
+            mma_commit(empty + r);
+          }
+          mma_commit(o_done);
+        }
+      }
+      __syncwarp();
+      gt += s.tiles;
+      ++seg;
+    }
+  } else {
+    const int row = warp * 32 + lane;
+    const uint32_t mine = tmem + ((uint32_t)warp << 21);
+    const float sc = a.scale_log2;
+    const int tr = row / p.gp;
+    auto sync128 = []() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    int gt = 0, it = 0;
+    for (int64_t u = lo; u < hi;) {
+      const TaSegment s = segment(u);
+      u += s.tiles;
+      const int hk = s.hp / parts;
+      const int head = hk * G + (s.hp % parts) * p.gp + row - tr * p.gp;
+      const int64_t tq = (int64_t)s.rt * p.tok + tr;  // token of the request
+      const bool live = tr < p.tok && tq < s.n;
+      __half* dst = a.o + ((s.q0 + tq) * a.Hq + head) * D;
+      if (s.len == 0) {  // lengths that do not fit: zeros
+        if (live)
+          for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      const int64_t prefix = s.len - s.n;
+      uint64_t word = 0;
+      if (live) {
+        word = a.tree ? (uint64_t)__ldg(reinterpret_cast<const long long*>(a.tree) + s.q0 + tq)
+                      : ~0ull >> (63 - (int)tq);
+        if (s.n < 64) word &= (1ull << s.n) - 1;
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < s.tiles; ++i) {
+        const int g = gt + i, buf = g & 1;
+        const int64_t j0 = (int64_t)(s.tile0 + i) * kTaKeys;
+        wait(s_full + buf, (g >> 1) & 1);
+        tmem_fence_after();
+        float x[kTaKeys];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(mine + buf * kTaKeys + c * 32, x + 32 * c);
+        tmem_wait_ld();
+        const uint32_t pages_ok = *reinterpret_cast<volatile uint32_t*>(granules + (g & 15));
+        if (j0 + kTaKeys > prefix || pages_ok != 0xffu) {
+          // which of the tile's keys the row sees: the prefix, then the word's bits
+          const int64_t d = prefix - j0;
+          uint64_t low, high;
+          if (d >= 128) low = high = ~0ull;
+          else if (d >= 64) {
+            low = ~0ull;
+            high = d == 64 ? word : ((1ull << (d - 64)) - 1) | (word << (d - 64));
+          } else if (d > 0) {
+            low = ((1ull << d) - 1) | (word << d);
+            high = word >> (64 - d);
+          } else {
+            low = d > -64 ? word >> (-d) : 0;
+            high = 0;
+          }
+          uint32_t seen[4] = {(uint32_t)low, (uint32_t)(low >> 32), (uint32_t)high, (uint32_t)(high >> 32)};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            seen[w] &= ((pages_ok >> (2 * w)) & 1 ? 0xffffu : 0u) | ((pages_ok >> (2 * w + 1)) & 1 ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[w * 32 + c] = (seen[w] >> c) & 1 ? x[w * 32 + c] : -INFINITY;
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = fmaxf(x[c], x[c + 4]);
+#pragma unroll
+        for (int c = 8; c < kTaKeys; c += 4)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[c + e]);
+        const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        const bool grow = tmax > m + 8.f || (m == -INFINITY && tmax > -INFINITY);
+        if (__any_sync(0xffffffffu, grow && i > 0 && live)) {
+          const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - tmax)) : 1.f;
+          l *= f;
+          wait(o_done, (g - 1) & 1);
+          tmem_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(mine + C::kTmemO + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f;
+            tmem_st32(mine + C::kTmemO + c, reinterpret_cast<uint32_t(&)[32]>(o));
+          }
+          tmem_wait_st();
+        }
+        if (grow) m = tmax;
+        const float ms = m == -INFINITY ? 0.f : -m;
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int c = half * 64 + e * 2;
+            float2 y = fma_f32x2(make_float2(x[c], x[c + 1]), make_float2(sc, sc), make_float2(ms, ms));
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            if (e & 1) acc1 = add_f32x2(acc1, y);
+            else acc0 = add_f32x2(acc0, y);
+            pk[e] = pack_half2(y.x, y.y);
+          }
+          tmem_st32(mine + buf * kTaKeys + half * 32, pk);
+        }
+        acc0 = add_f32x2(acc0, acc1);
+        l += acc0.x + acc0.y;
+        tmem_wait_st();
+        tmem_fence_before();
+        const int64_t tail = s.len - j0;  // keys of this tile that exist
+        if (tail < kTaKeys) {
+          // V's rows past the last token: zeroed once the tile's V is here.  Its slots follow the
+          // segment's K tiles and earlier V tiles in the ring; every earlier use of them is over,
+          // since S of this tile came after it, so one phase's parity cannot be taken for another's.
+          const int first = it + s.tiles * C::kKSlots + i * C::kVSlots;
+          for (int v = (int)(tail / C::kVKeys); v < C::kVSlots; ++v) {
+            const int r = (first + v) % C::kSlots;
+            wait(full + r, ((first + v) / C::kSlots) & 1);
+            const int k0 = tail > v * C::kVKeys ? (int)tail - v * C::kVKeys : 0;
+            for (int e = row; e < (C::kVKeys - k0) * C::kChunks * 8; e += 128) {
+              const int c = e / ((C::kVKeys - k0) * 8), w = e - c * ((C::kVKeys - k0) * 8);
+              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(ring + r * kTaSlot + c * (C::kVKeys * 128) +
+                                                                         k0 * 128 + w * 16),
+                           "r"(0)
+                           : "memory");
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + buf);
+      }
+      gt += s.tiles;
+      it += s.tiles * (C::kKSlots + C::kVSlots);
+      // ---- the segment's O: the output, or a part
+      if (s.tiles > 1) wait(o_done, (gt - 2) & 1);  // a parity tells only neighbouring phases apart
+      wait(o_done, (gt - 1) & 1);
+      tmem_fence_after();
+      const bool whole = s.tiles == s.item_tiles;
+      const int64_t slot = (int64_t)blockIdx.x * 2 + (s.tile0 == 0);
+      float* part = p.part_o + (slot * p.rows + row) * D;
+      const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+      bool odd = !(l < INFINITY);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tmem_ld32(mine + C::kTmemO + c, o);
+        tmem_wait_ld();
+        if (!live) continue;
+        const bool none = l == 0.f;  // the row saw nothing here: what the MMAs left is 0 times V
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              if (none) o[e + y] = 0.f;
+              odd |= !(fabsf(o[e + y]) < INFINITY);
+            }
+            *reinterpret_cast<uint4*>(dst + c + e) =
+                make_uint4(pack_half2(o[e] * inv, o[e + 1] * inv), pack_half2(o[e + 2] * inv, o[e + 3] * inv),
+                           pack_half2(o[e + 4] * inv, o[e + 5] * inv), pack_half2(o[e + 6] * inv, o[e + 7] * inv));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part + c + e) =
+                none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+      auto redo = [&](bool mineodd, int64_t rq, int rh, uint64_t rw) {
+        unsigned again = __ballot_sync(0xffffffffu, mineodd);
+        while (again) {
+          const int r = __ffs(again) - 1;
+          again &= again - 1;
+          attend_row<D, true>(a, __shfl_sync(0xffffffffu, s.q0 + rq, r), __shfl_sync(0xffffffffu, rh, r), s.b, 0, s.len,
+                              prefix, __shfl_sync(0xffffffffu, rw, r), lane);
+        }
+      };
+      if (whole) {
+        redo(live && odd, tq, head, word);
+        continue;
+      }
+      if (live) *reinterpret_cast<float2*>(p.part_ml + (slot * p.rows + row) * 2) = make_float2(m, l);
+      __threadfence();
+      sync128();
+      const int64_t c0 = owner(s.item_unit), c1 = owner(s.item_unit + s.item_tiles - 1);
+      int* count = p.count + ((int64_t)s.b * p.head_parts + s.hp) * p.row_tiles + s.rt;
+      if (row == 0) {
+        const int before = atomicAdd(count, 1);
+        last_flag = before == (int)(c1 - c0);
+        if (last_flag) *count = 0;
+        __threadfence();
+      }
+      sync128();
+      const bool last = last_flag;
+      sync128();  // the flag is read before the next segment may write it
+      if (!last) continue;
+      __threadfence();
+      // the last CTA of the item: rows over the warps, columns over the lanes
+      const int64_t live_tok = s.n - (int64_t)s.rt * p.tok;
+      const int nrows = (int)(live_tok < p.tok ? live_tok : p.tok) * p.gp;
+      for (int r = warp; r < nrows; r += 4) {
+        float M = -INFINITY;
+        for (int64_t c = c0 + lane; c <= c1; c += 32)
+          M = fmaxf(M, __ldcg(p.part_ml + ((2 * c + (c == c0)) * p.rows + r) * 2));
+#pragma unroll
+        for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        constexpr int E = D / 32;  // columns per lane: lane * 2 + 64 i (+ 1)
+        float acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        float L = 0.f;
+#pragma unroll 4
+        for (int64_t c = c0; c <= c1; ++c) {
+          const int64_t at = (2 * c + (c == c0)) * p.rows + r;
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2));
+          const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+          L = fmaf(w, ml.y, L);
+          const float* src = p.part_o + at * D + lane * 2;
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(src + e * 32));
+            acc[e] = fmaf(w, y.x, acc[e]);
+            acc[e + 1] = fmaf(w, y.y, acc[e + 1]);
+          }
+        }
+        const float iv = L > 0.f || L != L ? 1.f / L : 0.f;
+        const int64_t rq = (int64_t)s.rt * p.tok + r / p.gp;
+        const int rh = hk * G + (s.hp % parts) * p.gp + r % p.gp;
+        __half* out = a.o + ((s.q0 + rq) * a.Hq + rh) * D + lane * 2;
+        bool bad = !(L < INFINITY);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          bad |= !(fabsf(acc[e]) < INFINITY) || !(fabsf(acc[e + 1]) < INFINITY);
+          *reinterpret_cast<__half2*>(out + e * 32) = __floats2half2_rn(acc[e] * iv, acc[e + 1] * iv);
+        }
+        if (__any_sync(0xffffffffu, bad)) {
+          uint64_t rw = a.tree ? (uint64_t)__ldg(reinterpret_cast<const long long*>(a.tree) + s.q0 + rq)
+                               : ~0ull >> (63 - (int)rq);
+          if (s.n < 64) rw &= (1ull << s.n) - 1;
+          attend_row<D, true>(a, s.q0 + rq, rh, s.b, 0, s.len, prefix, rw, lane);
+        }
+      }
+    }
+  }
+
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 5) tmem_dealloc(tmem, 512);
+}
+
+static void tile_shape(int64_t Hq, int64_t Hkv, int64_t max_q, int* gp, int* tok) {
+  *gp = heads_per_tile((int)(Hq / Hkv));
+  *tok = 128 / *gp;
+  if (*tok > max_q) *tok = (int)max_q;
+}
+
+size_t tree_workspace(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D) {
+  int gp, tok;
+  tile_shape(Hq, Hkv, max_q, &gp, &tok);
+  const int64_t items = B * Hkv * (Hq / Hkv / gp) * ((max_q + tok - 1) / tok);
+  const int64_t rows = 2 * kTaMaxCtas * (int64_t)gp * tok;
+  return (size_t)((items * 4 + 255) / 256 * 256 + rows * 2 * 4 + rows * D * 4);
+}
+
+template <int D>
+static int launch_tree(TaArgs& p, const DeviceFacts& f, cudaStream_t s) {
+  using C = TaCfg<D>;
+  const AttnArgs& a = p.a;
+  const int page = 1 << a.page_log2;
+  p.kbox = page < kTaKeys ? page : kTaKeys;
+  p.vbox = page < C::kVKeys ? page : C::kVKeys;
+  CUtensorMap tq, tk, tv;
+  int rc = token_map(&tq, a.q, a.T, a.Hq, D, a.ldq, p.gp, p.tok);
+  // the cache as [pages * Hkv, page, D]
+  if (rc == TB_OK) rc = token_map(&tk, a.k, a.pages * a.Hkv, page, D, (int64_t)page * D, p.kbox, 1);
+  if (rc == TB_OK) rc = token_map(&tv, a.v, a.pages * a.Hkv, page, D, (int64_t)page * D, p.vbox, 1);
+  if (rc != TB_OK) return rc;
+  rc = ensure_dynamic_smem(reinterpret_cast<const void*>(tree_attn_kernel<D>), f.device, C::kSmem);
+  if (rc != TB_OK) return rc;
+  const int grid = f.sms < kTaMaxCtas ? f.sms : kTaMaxCtas;
+  tree_attn_kernel<D><<<grid, kTaThreads, C::kSmem, s>>>(tq, tk, tv, p);
+  return check_launch();
+}
+
+int launch_tree_tiles(const AttnArgs& a, int64_t D, void* workspace, cudaStream_t s) {
+  DeviceFacts f;
+  const int rc = device_facts(&f);
+  if (rc != TB_OK) return rc;
+  TaArgs p;
+  p.a = a;
+  tile_shape(a.Hq, a.Hkv, a.max_q, &p.gp, &p.tok);
+  p.head_parts = a.Hkv * (a.Hq / a.Hkv / p.gp);
+  p.row_tiles = (a.max_q + p.tok - 1) / p.tok;
+  p.rows = p.gp * p.tok;
+  const int64_t items = (int64_t)a.B * p.head_parts * p.row_tiles;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  p.count = reinterpret_cast<int*>(w);
+  p.part_ml = reinterpret_cast<float*>(w + (items * 4 + 255) / 256 * 256);
+  p.part_o = p.part_ml + 2 * kTaMaxCtas * (int64_t)p.rows * 2;
+  if (D == 64) return launch_tree<64>(p, f, s);
+  if (D == 128) return launch_tree<128>(p, f, s);
+  return launch_tree<256>(p, f, s);
+}
+
+}  // namespace tb
