@@ -451,8 +451,7 @@ int tb_cache_write(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ld
  * nothing (or only scores of -infinity) gives zeros.  What a row does not see does not reach it,
  * not even as NaN or infinity.  D 64, 128 or 256 (else TB_ERR_UNSUPPORTED); max_q above 64:
  * TB_ERR_TOO_LARGE.  workspace: at least tb_tree_attention_workspace_size(B, T, max_q, Hq, Hkv, D)
- * bytes (the size may be 0), zero before its first use and left zero by every completed call; calls
- * that share one are ordered on one stream.  dev_status optional: TB_DEV_BAD_LEN (n_b above max_q,
+ * bytes of scratch; its contents do not matter; calls that share one are ordered on one stream.  dev_status optional: TB_DEV_BAD_LEN (n_b above max_q,
  * total[b] below n_b or above max_pages * page: zeros), TB_DEV_BAD_SLOT (a page outside the cache:
  * its tokens are left out).
  */

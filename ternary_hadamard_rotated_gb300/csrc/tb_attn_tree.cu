@@ -10,8 +10,9 @@
 // Work: units of (request, head part, row tile, key tile), key tiles fastest, are cut into one equal
 // contiguous range per SM, so the longest request is spread over as many SMs as its bytes call for.
 // A CTA walks its range as segments (runs of key tiles of one item).  An item inside one range is
-// written at once; one cut between CTAs leaves fp32 parts (O, maximum, sum) in the workspace, and the
-// last CTA to count in adds them in CTA order, so the result does not depend on who came last.
+// written at once; one cut between CTAs leaves fp32 parts (O, maximum, sum) in the workspace, which a
+// second kernel joins, all rows at once (the last CTA of an item joining them alone took 10 us for 33
+// parts of 6 rows, and 70 us for 26 parts of 96).
 //
 // Warps 0-3: softmax (thread = row) and epilogue; 4: TMA loads (pages by the block table); 5: MMAs.
 // V rows past the request's last token are zeroed in shared memory before the MMAs read them (what
@@ -30,18 +31,19 @@ namespace tb {
 constexpr int kTaThreads = 192;
 constexpr int kTaKeys = 128;
 constexpr int kTaSlot = 16384;
+constexpr int kTaRing = 224 * 1024;  // Q and the ring
 constexpr int kTaMaxCtas = 160;  // CTAs the workspace has room for
 
 template <int D>
 struct TaCfg {
   static constexpr int kChunks = D / 64;
-  static constexpr int kQBytes = kChunks * 16384;
   static constexpr int kKSlots = kChunks;                     // a slot: 64 elements of 128 keys
   static constexpr int kVKeys = kTaSlot / (D * 2);            // a slot: all elements of 128 / kChunks keys
   static constexpr int kVSlots = kTaKeys / kVKeys;
-  static constexpr int kSlots = (220 * 1024 - kQBytes) / kTaSlot > 12 ? 12 : (220 * 1024 - kQBytes) / kTaSlot;
-  static_assert(kSlots > kKSlots + kVSlots, "the loads of a tile never wait for its own MMAs of P V");
-  static constexpr int kSmem = 1024 + kQBytes + kSlots * kTaSlot + 512;
+  // Q, then the ring: each row of Q that the tile has is there once (in eights), and the MMA's idle
+  // rows read on into what follows, so that the ring gets what a full tile of Q would take
+  static constexpr int kSmem = 1024 + kTaRing + 1024;
+  static int slots(int rows) { return (kTaRing - kChunks * ((rows + 7) / 8 * 1024)) / kTaSlot; }
   static constexpr uint32_t kIdescQK = (1u << 4) | ((uint32_t)(kTaKeys >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
   static constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
   static constexpr uint32_t kTmemO = 2 * kTaKeys;
@@ -52,9 +54,10 @@ struct TaArgs {
   int gp, tok, head_parts, row_tiles;  // query heads and tokens per tile; row tiles at max_q tokens
   int rows;                            // rows of a part in the workspace: gp * tok
   int kbox, vbox;                      // keys per box of the K and V maps
+  int slots;                           // slots of the ring
   float* part_o;                       // [2 * grid][rows][D]
   float* part_ml;                      // [2 * grid][rows][2]
-  int* count;                          // [B * head_parts * row_tiles], zero between calls
+  int2* meta;                          // [B * head_parts * row_tiles]: an item's first CTA, and how many
 };
 
 // a run of key tiles of one item
@@ -75,11 +78,13 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   const uint32_t raw = smem_u32(ta_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = ta_raw + (base - raw);
-  const uint32_t ring = base + C::kQBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kQBytes + C::kSlots * kTaSlot);
+  const int S = p.slots;
+  const uint32_t qchunk = (uint32_t)(p.rows + 7) / 8 * 1024;  // bytes of 64 elements of Q's rows
+  const uint32_t ring = base + C::kChunks * qchunk;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kTaRing);
   uint64_t* full = bars;
-  uint64_t* empty = bars + C::kSlots;
-  uint64_t* q_full = bars + 2 * C::kSlots;
+  uint64_t* empty = bars + S;
+  uint64_t* q_full = bars + 2 * S;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_full + 2;  // [2]
   uint64_t* p_full = q_full + 4;  // [2]
@@ -87,13 +92,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   uint64_t* o_free = q_full + 7;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 8);
   __shared__ volatile int aborted;
-  __shared__ int last_flag;
   __shared__ uint32_t granules[16];  // per key tile: which runs of 16 keys lie in a page of the cache
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     aborted = 0;
-    for (int i = 0; i < C::kSlots; ++i) {
+    for (int i = 0; i < S; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
     }
@@ -107,6 +111,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     mbar_init(o_free, 4);
     fence_barrier_init();
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 5) tmem_alloc(tmem_slot, 512);
 
   // ---- the schedule: every warp adds up the units of all requests itself
@@ -199,80 +204,101 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
   };
 
+  // a place in the ring: slot, and the parity of the phase its next use completes
+  struct Ring {
+    int r = 0;
+    uint32_t ph = 0;
+  };
+  auto advance = [&](Ring& x, int n) {
+    x.r += n;
+    if (x.r >= S) {
+      x.r -= S;
+      x.ph ^= 1;
+    }
+  };
+
   if (warp == 4) {
-    int it = 0, seg = 0, gt = 0;
+    // Each lane owns one box of a K tile and one of a V tile (at most 32 of each), waits for its slot
+    // and issues it; the page numbers of a tile are fetched two tiles ahead of its use.
+    int seg = 0, gt = 0;
+    Ring at;
+    int used = 0;  // slots handed out so far, up to S: a slot's first use waits for nobody
+    const int page = 1 << a.page_log2;
+    const int kb = kTaKeys / p.kbox, vb = C::kVKeys / p.vbox;
+    // K: slot (chunk) lane / kb, box lane % kb of it
+    const bool k_on = lane < C::kKSlots * kb;
+    const int k_slot = lane / kb, k_key = (lane - k_slot * kb) * p.kbox;
+    // V: slot lane / (vb * chunks), keys and chunk within it
+    const bool v_on = lane < C::kVSlots * vb * C::kChunks;
+    const int v_slot = lane / (vb * C::kChunks), v_rest = lane - v_slot * (vb * C::kChunks);
+    const int v_in = v_rest / C::kChunks * p.vbox, v_c = v_rest % C::kChunks;
+    const int v_key = v_slot * C::kVKeys + v_in;
     for (int64_t u = lo; u < hi;) {
       const TaSegment s = segment(u);
       u += s.tiles;
       if (s.len == 0) continue;
       const int hk = s.hp / parts, h0 = hk * G + (s.hp % parts) * p.gp;
-      // pages of one key tile: the lanes look them up, lane 0 issues the boxes
-      auto slot = [&]() {
-        const int r = it % C::kSlots, ph = it / C::kSlots;
-        if (lane == 0) {
-          if (ph > 0) wait(empty + r, (ph - 1) & 1);
-          mbar_arrive_expect_tx(full + r, kTaSlot);
-        }
-        ++it;
-        return r;
+      const int32_t* row = a.table + (int64_t)s.b * a.max_pages;
+      // page of the 16-key run that this lane (0-7) looks up; -1 past the last token or the segment
+      auto look = [&](int i) -> int {
+        const int64_t j = (int64_t)(s.tile0 + i) * kTaKeys + (lane & 7) * 16;
+        return i < s.tiles && j < s.len ? __ldg(row + (j >> a.page_log2)) : -1;
       };
-      // z coordinate (page, head) of the 16-key run that this lane (0-7) looks up; out of the map for a
-      // page that is not one (its boxes are filled with zeros), or past the last token
-      auto zrow = [&](int tile) {
-        const int64_t j = (int64_t)tile * kTaKeys + (lane & 7) * 16;
-        int64_t pg = -1;
-        if (j < s.len) {
-          pg = __ldg(a.table + (int64_t)s.b * a.max_pages + (j >> a.page_log2));
-          if (pg < 0 || pg >= a.pages) {
-            pg = -1;
-            if (lane < 8) set_status(a.status, TB_DEV_BAD_SLOT);
-          }
-        }
-        return pg;
+      // its row of the cache's map; out of the map, where boxes are filled with zeros, for no page
+      auto coord = [&](int i, int pg) -> int {
+        const int64_t j = (int64_t)(s.tile0 + i) * kTaKeys + (lane & 7) * 16;
+        const bool ok = pg >= 0 && pg < a.pages;
+        if (!ok && i < s.tiles && j < s.len && lane < 8) set_status(a.status, TB_DEV_BAD_SLOT);
+        return ok ? (int)(pg * a.Hkv + hk) : -1;
       };
-      const int page = 1 << a.page_log2;
-      auto coord = [&](int64_t pg) { return pg < 0 ? (int)(a.pages * a.Hkv) : (int)(pg * a.Hkv + hk); };
-      auto load_k = [&](int i) {
-        const int tile = s.tile0 + i;
-        const int64_t pg = zrow(tile);
-        const unsigned ok = __ballot_sync(0xffffffffu, pg >= 0) & 0xffu;
-        if (lane == 0) granules[(gt + i) & 15] = ok;
-        for (int c = 0; c < C::kChunks; ++c) {
-          const int r = slot();
-          for (int k = 0; k < kTaKeys; k += p.kbox) {
-            const int64_t g = __shfl_sync(0xffffffffu, pg, k / 16);
-            if (lane == 0)
-              tma_load_3d<1>(ring + r * kTaSlot + k * 128, &tmK, c * 64, (tile * kTaKeys + k) & (page - 1), coord(g),
-                             smem_u32(full + r));
-          }
-        }
+      const int none = (int)(a.pages * a.Hkv);
+      auto acquire = [&](int slot, bool first) -> int {  // this lane's slot, its bytes announced by one lane
+        Ring x = at;
+        advance(x, slot);
+        if (used + slot >= S) wait(empty + x.r, x.ph ^ 1);
+        if (first) mbar_arrive_expect_tx(full + x.r, kTaSlot);
+        return x.r;
       };
-      auto load_v = [&](int i) {
-        const int tile = s.tile0 + i;
-        const int64_t pg = zrow(tile);
-        for (int v = 0; v < C::kVSlots; ++v) {
-          const int r = slot();
-          for (int k = 0; k < C::kVKeys; k += p.vbox) {
-            const int key = v * C::kVKeys + k;
-            const int64_t g = __shfl_sync(0xffffffffu, pg, key / 16);
-            if (lane == 0)
-              for (int c = 0; c < C::kChunks; ++c)
-                tma_load_3d<1>(ring + r * kTaSlot + c * (C::kVKeys * 128) + k * 128, &tmV, c * 64,
-                               (tile * kTaKeys + key) & (page - 1), coord(g), smem_u32(full + r));
-          }
+      auto load_k = [&](int i, int z) {
+        const unsigned ok = __ballot_sync(0xffffffffu, z >= 0) & 0xffu;
+        if (lane == 0) *reinterpret_cast<volatile uint32_t*>(granules + ((gt + i) & 15)) = ok;
+        __syncwarp();
+        const int zz = __shfl_sync(0xffffffffu, z, k_key / 16);
+        if (k_on) {
+          const int r = acquire(k_slot, k_key == 0);
+          tma_load_3d<1>(ring + r * kTaSlot + k_key * 128, &tmK, k_slot * 64,
+                         ((s.tile0 + i) * kTaKeys + k_key) & (page - 1), zz < 0 ? none : zz, smem_u32(full + r));
         }
+        __syncwarp();
+        advance(at, C::kKSlots);
+        used += C::kKSlots;
       };
-      load_k(0);
+      auto load_v = [&](int i, int z) {
+        const int zz = __shfl_sync(0xffffffffu, z, (v_key / 16) & 7);
+        if (v_on) {
+          const int r = acquire(v_slot, v_rest == 0);
+          tma_load_3d<1>(ring + r * kTaSlot + v_c * (C::kVKeys * 128) + v_in * 128, &tmV, v_c * 64,
+                         ((s.tile0 + i) * kTaKeys + v_key) & (page - 1), zz < 0 ? none : zz, smem_u32(full + r));
+        }
+        __syncwarp();
+        advance(at, C::kVSlots);
+        used += C::kVSlots;
+      };
+      int z0 = coord(0, look(0)), ahead = look(1);
+      load_k(0, z0);
       if (lane == 0) {
         if (seg > 0) wait(q_empty, (seg - 1) & 1);
         mbar_arrive_expect_tx(q_full, C::kChunks * 128 * p.gp * p.tok);
         for (int c = 0; c < C::kChunks; ++c)
-          tma_load_3d<1>(base + c * 16384, &tmQ, c * 64, h0, (int)(s.q0 + (int64_t)s.rt * p.tok), smem_u32(q_full));
+          tma_load_3d<1>(base + c * qchunk, &tmQ, c * 64, h0, (int)(s.q0 + (int64_t)s.rt * p.tok), smem_u32(q_full));
       }
       __syncwarp();
       for (int i = 0; i < s.tiles; ++i) {
-        if (i + 1 < s.tiles) load_k(i + 1);
-        load_v(i);
+        const int z1 = coord(i + 1, ahead);
+        ahead = look(i + 2);
+        if (i + 1 < s.tiles) load_k(i + 1, z1);
+        load_v(i, z0);
+        z0 = z1;
       }
       gt += s.tiles;
       ++seg;
@@ -283,25 +309,30 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       }
     }
   } else if (warp == 5) {
-    int it = 0, seg = 0, gt = 0;
+    int seg = 0, gt = 0;
+    Ring at;
     for (int64_t u = lo; u < hi;) {
       const TaSegment s = segment(u);
       u += s.tiles;
       if (s.len == 0) continue;
       if (lane == 0) {
+        // descriptors of place 0; the address field counts 16 bytes, and no sum carries out of it
+        const uint64_t qdesc = smem_desc_sw128(base, 1024), kdesc = smem_desc_sw128(ring, 1024);
+        const uint64_t vdesc = smem_desc_mn128(ring, C::kVKeys * 128, 1024);
         wait(q_full, seg & 1);
         tmem_fence_after();
         auto qk = [&](int i) {
           const uint32_t d = tmem + (uint32_t)((gt + i) & 1) * kTaKeys;
-          for (int c = 0; c < C::kChunks; ++c, ++it) {
-            const int r = it % C::kSlots;
-            wait(full + r, (it / C::kSlots) & 1);
-            tmem_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16_ss<1>(d, smem_desc_sw128(base + c * 16384 + kk * 32, 1024),
-                            smem_desc_sw128(ring + r * kTaSlot + kk * 32, 1024), C::kIdescQK, (c | kk) != 0);
+          for (int c = 0; c < C::kChunks; ++c) {
+            const int r = at.r;
+            wait(full + r, at.ph);
+            tmem_fence_after();
+            const uint64_t qd = qdesc + c * (qchunk >> 4), kd = kdesc + r * (kTaSlot >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma_f16_ss<1>(d, qd + kk * 2, kd + kk * 2, C::kIdescQK, (c | kk) != 0);
             mma_commit(empty + r);
+            advance(at, 1);
           }
           mma_commit(s_full + ((gt + i) & 1));
         };
@@ -312,16 +343,18 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           if (i == 0 && seg > 0) wait(o_free, (seg - 1) & 1);  // the last segment's O has been read
           wait(p_full + ((gt + i) & 1), ((gt + i) >> 1) & 1);
           tmem_fence_after();
-          for (int v = 0; v < C::kVSlots; ++v, ++it) {
-            const int r = it % C::kSlots;
-            wait(full + r, (it / C::kSlots) & 1);
+#pragma unroll
+          for (int v = 0; v < C::kVSlots; ++v) {
+            const int r = at.r;
+            wait(full + r, at.ph);
             tmem_fence_after();
+            const uint64_t vd = vdesc + r * (kTaSlot >> 4);
 #pragma unroll
             for (int kk = 0; kk < C::kVKeys / 16; ++kk)
               mma_f16_ts<1>(tmem + C::kTmemO, tmem + (uint32_t)((gt + i) & 1) * kTaKeys + (v * (C::kVKeys / 16) + kk) * 8,
-                            smem_desc_mn128(ring + r * kTaSlot + kk * 2048, C::kVKeys * 128, 1024), C::kIdescPV,
-                            (i | v | kk) != 0);
+                            vd + kk * (2048 >> 4), C::kIdescPV, (i | v | kk) != 0);
             mma_commit(empty + r);
+            advance(at, 1);
           }
           mma_commit(o_done);
         }
@@ -335,11 +368,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const uint32_t mine = tmem + ((uint32_t)warp << 21);
     const float sc = a.scale_log2;
     const int tr = row / p.gp;
-    auto sync128 = []() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-    int gt = 0, it = 0;
+    int gt = 0;
+    int64_t it = 0;  // slots used before this segment
     for (int64_t u = lo; u < hi;) {
       const TaSegment s = segment(u);
       u += s.tiles;
+      if (row == 0 && s.tile0 == 0)  // where the item's parts are, for the joining kernel
+        p.meta[((int64_t)s.b * p.head_parts + s.hp) * p.row_tiles + s.rt] =
+            make_int2((int)blockIdx.x, (int)(owner(s.item_unit + s.item_tiles - 1) - blockIdx.x) + 1);
       const int hk = s.hp / parts;
       const int head = hk * G + (s.hp % parts) * p.gp + row - tr * p.gp;
       const int64_t tq = (int64_t)s.rt * p.tok + tr;  // token of the request
@@ -443,10 +479,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           // V's rows past the last token: zeroed once the tile's V is here.  Its slots follow the
           // segment's K tiles and earlier V tiles in the ring; every earlier use of them is over,
           // since S of this tile came after it, so one phase's parity cannot be taken for another's.
-          const int first = it + s.tiles * C::kKSlots + i * C::kVSlots;
+          const int64_t first = it + (int64_t)s.tiles * C::kKSlots + (int64_t)i * C::kVSlots;
           for (int v = (int)(tail / C::kVKeys); v < C::kVSlots; ++v) {
-            const int r = (first + v) % C::kSlots;
-            wait(full + r, ((first + v) / C::kSlots) & 1);
+            const int r = (int)((first + v) % S);
+            wait(full + r, (uint32_t)((first + v) / S) & 1);
             const int k0 = tail > v * C::kVKeys ? (int)tail - v * C::kVKeys : 0;
             for (int e = row; e < (C::kVKeys - k0) * C::kChunks * 8; e += 128) {
               const int c = e / ((C::kVKeys - k0) * 8), w = e - c * ((C::kVKeys - k0) * 8);
@@ -462,7 +498,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (lane == 0) mbar_arrive(p_full + buf);
       }
       gt += s.tiles;
-      it += s.tiles * (C::kKSlots + C::kVSlots);
+      it += (int64_t)s.tiles * (C::kKSlots + C::kVSlots);
       // ---- the segment's O: the output, or a part
       if (s.tiles > 1) wait(o_done, (gt - 2) & 1);  // a parity tells only neighbouring phases apart
       wait(o_done, (gt - 1) & 1);
@@ -501,79 +537,16 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free);
-      auto redo = [&](bool mineodd, int64_t rq, int rh, uint64_t rw) {
-        unsigned again = __ballot_sync(0xffffffffu, mineodd);
-        while (again) {
-          const int r = __ffs(again) - 1;
-          again &= again - 1;
-          attend_row<D, true>(a, __shfl_sync(0xffffffffu, s.q0 + rq, r), __shfl_sync(0xffffffffu, rh, r), s.b, 0, s.len,
-                              prefix, __shfl_sync(0xffffffffu, rw, r), lane);
-        }
-      };
-      if (whole) {
-        redo(live && odd, tq, head, word);
+      if (!whole) {
+        if (live) *reinterpret_cast<float2*>(p.part_ml + (slot * p.rows + row) * 2) = make_float2(m, l);
         continue;
       }
-      if (live) *reinterpret_cast<float2*>(p.part_ml + (slot * p.rows + row) * 2) = make_float2(m, l);
-      __threadfence();
-      sync128();
-      const int64_t c0 = owner(s.item_unit), c1 = owner(s.item_unit + s.item_tiles - 1);
-      int* count = p.count + ((int64_t)s.b * p.head_parts + s.hp) * p.row_tiles + s.rt;
-      if (row == 0) {
-        const int before = atomicAdd(count, 1);
-        last_flag = before == (int)(c1 - c0);
-        if (last_flag) *count = 0;
-        __threadfence();
-      }
-      sync128();
-      const bool last = last_flag;
-      sync128();  // the flag is read before the next segment may write it
-      if (!last) continue;
-      __threadfence();
-      // the last CTA of the item: rows over the warps, columns over the lanes
-      const int64_t live_tok = s.n - (int64_t)s.rt * p.tok;
-      const int nrows = (int)(live_tok < p.tok ? live_tok : p.tok) * p.gp;
-      for (int r = warp; r < nrows; r += 4) {
-        float M = -INFINITY;
-        for (int64_t c = c0 + lane; c <= c1; c += 32)
-          M = fmaxf(M, __ldcg(p.part_ml + ((2 * c + (c == c0)) * p.rows + r) * 2));
-#pragma unroll
-        for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        constexpr int E = D / 32;  // columns per lane: lane * 2 + 64 i (+ 1)
-        float acc[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        float L = 0.f;
-#pragma unroll 4
-        for (int64_t c = c0; c <= c1; ++c) {
-          const int64_t at = (2 * c + (c == c0)) * p.rows + r;
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2));
-          const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-          L = fmaf(w, ml.y, L);
-          const float* src = p.part_o + at * D + lane * 2;
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(src + e * 32));
-            acc[e] = fmaf(w, y.x, acc[e]);
-            acc[e + 1] = fmaf(w, y.y, acc[e + 1]);
-          }
-        }
-        const float iv = L > 0.f || L != L ? 1.f / L : 0.f;
-        const int64_t rq = (int64_t)s.rt * p.tok + r / p.gp;
-        const int rh = hk * G + (s.hp % parts) * p.gp + r % p.gp;
-        __half* out = a.o + ((s.q0 + rq) * a.Hq + rh) * D + lane * 2;
-        bool bad = !(L < INFINITY);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          bad |= !(fabsf(acc[e]) < INFINITY) || !(fabsf(acc[e + 1]) < INFINITY);
-          *reinterpret_cast<__half2*>(out + e * 32) = __floats2half2_rn(acc[e] * iv, acc[e + 1] * iv);
-        }
-        if (__any_sync(0xffffffffu, bad)) {
-          uint64_t rw = a.tree ? (uint64_t)__ldg(reinterpret_cast<const long long*>(a.tree) + s.q0 + rq)
-                               : ~0ull >> (63 - (int)rq);
-          if (s.n < 64) rw &= (1ull << s.n) - 1;
-          attend_row<D, true>(a, s.q0 + rq, rh, s.b, 0, s.len, prefix, rw, lane);
-        }
+      unsigned again = __ballot_sync(0xffffffffu, live && odd);
+      while (again) {
+        const int r = __ffs(again) - 1;
+        again &= again - 1;
+        attend_row<D, true>(a, __shfl_sync(0xffffffffu, s.q0 + tq, r), __shfl_sync(0xffffffffu, head, r), s.b, 0, s.len,
+                            prefix, __shfl_sync(0xffffffffu, word, r), lane);
       }
     }
   }
@@ -581,6 +554,88 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   tmem_fence_before();
   __syncthreads();
   if (warp == 5) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- parts -> output
+// One CTA per (row, head): its warps share the parts of the row's item, the lanes the columns; rows of
+// items that one CTA finished are done already.  The order of the sums is fixed by the schedule.
+constexpr int kTjThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kTjThreads) tree_join_kernel(const TaArgs p) {
+  const AttnArgs& a = p.a;
+  constexpr int E = D / 32, W = kTjThreads / 32;  // columns of a lane: lane * 2 + 64 i (+ 1)
+  __shared__ float acc_s[W][D];
+  __shared__ float ml_s[W][2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x / a.Hq;
+  const int h = (int)(blockIdx.x - t * a.Hq);
+  int b = 0;
+  {
+    int hi = a.B - 1;  // the last request that begins at or before row t
+    while (b < hi) {
+      const int mid = (b + hi + 1) >> 1;
+      if (__ldg(a.q_start + mid) <= t) b = mid;
+      else hi = mid - 1;
+    }
+  }
+  const int64_t q0 = __ldg(a.q_start + b), n = __ldg(a.q_start + b + 1) - q0, len = __ldg(a.total + b);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+  if (q0 < 0 || t < q0 || t >= q0 + n || q0 + n > a.T) return;
+  const int G = a.Hq / a.Hkv, parts = G / p.gp, hk = h / G;
+  const int hp = hk * parts + (h - hk * G) / p.gp;
+  const int tq = (int)(t - q0), rt = tq / p.tok;
+  const int2 meta = p.meta[((int64_t)b * p.head_parts + hp) * p.row_tiles + rt];
+  if (meta.y < 2) return;
+  const int row = (tq - rt * p.tok) * p.gp + (h - hk * G) % p.gp;
+  // part i is CTA meta.x + i's: its first segment (0), or for the item's first CTA its last (1)
+  auto at = [&](int i) { return (int64_t)(2 * (meta.x + i) + (i == 0)) * p.rows + row; };
+  float M = -INFINITY;
+  for (int i = lane; i < meta.y; i += 32) M = fmaxf(M, __ldcg(p.part_ml + at(i) * 2));
+#pragma unroll
+  for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  float acc[E], L = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < meta.y; i += W) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at(i) * 2));
+    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+    L = fmaf(w, ml.y, L);
+    const float* src = p.part_o + at(i) * D + lane * 2;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 y = __ldcg(reinterpret_cast<const float2*>(src + e * 32));
+      acc[e] = fmaf(w, y.x, acc[e]);
+      acc[e + 1] = fmaf(w, y.y, acc[e + 1]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<float2*>(&acc_s[warp][e * 32 + lane * 2]) = make_float2(acc[e], acc[e + 1]);
+  if (lane == 0) ml_s[warp][0] = L;
+  __syncthreads();
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < W; ++w) L += ml_s[w][0];
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+  bool bad = !(L < INFINITY);
+  __half* out = a.o + (t * a.Hq + h) * D;
+  for (int c = threadIdx.x * 2; c < D; c += kTjThreads * 2) {
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      x += acc_s[w][c];
+      y += acc_s[w][c + 1];
+    }
+    bad |= !(fabsf(x) < INFINITY) || !(fabsf(y) < INFINITY);
+    *reinterpret_cast<__half2*>(out + c) = __floats2half2_rn(x * inv, y * inv);
+  }
+  if (__syncthreads_or(bad) && warp == 0) {
+    uint64_t word = a.tree ? (uint64_t)__ldg(reinterpret_cast<const long long*>(a.tree) + t) : ~0ull >> (63 - tq);
+    if (n < 64) word &= (1ull << n) - 1;
+    attend_row<D, true>(a, t, h, b, 0, len, len - n, word, lane);
+  }
 }
 
 static void tile_shape(int64_t Hq, int64_t Hkv, int64_t max_q, int* gp, int* tok) {
@@ -594,7 +649,7 @@ size_t tree_workspace(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t
   tile_shape(Hq, Hkv, max_q, &gp, &tok);
   const int64_t items = B * Hkv * (Hq / Hkv / gp) * ((max_q + tok - 1) / tok);
   const int64_t rows = 2 * kTaMaxCtas * (int64_t)gp * tok;
-  return (size_t)((items * 4 + 255) / 256 * 256 + rows * 2 * 4 + rows * D * 4);
+  return (size_t)((items * 8 + 255) / 256 * 256 + rows * 2 * 4 + rows * D * 4);
 }
 
 template <int D>
@@ -613,7 +668,25 @@ static int launch_tree(TaArgs& p, const DeviceFacts& f, cudaStream_t s) {
   rc = ensure_dynamic_smem(reinterpret_cast<const void*>(tree_attn_kernel<D>), f.device, C::kSmem);
   if (rc != TB_OK) return rc;
   const int grid = f.sms < kTaMaxCtas ? f.sms : kTaMaxCtas;
+  p.slots = C::slots(p.rows) < 16 ? C::slots(p.rows) : 16;
   tree_attn_kernel<D><<<grid, kTaThreads, C::kSmem, s>>>(tq, tk, tv, p);
+  rc = check_launch();
+  if (rc != TB_OK) return rc;
+  // the joining kernel starts while the last CTAs still run and waits for them on the device
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.T * a.Hq));
+  cfg.blockDim = dim3(kTjThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, p);
+  if (e != cudaSuccess) {
+    record_cuda_error(e);
+    return TB_ERR_CUDA;
+  }
   return check_launch();
 }
 
@@ -629,8 +702,8 @@ int launch_tree_tiles(const AttnArgs& a, int64_t D, void* workspace, cudaStream_
   p.rows = p.gp * p.tok;
   const int64_t items = (int64_t)a.B * p.head_parts * p.row_tiles;
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  p.count = reinterpret_cast<int*>(w);
-  p.part_ml = reinterpret_cast<float*>(w + (items * 4 + 255) / 256 * 256);
+  p.meta = reinterpret_cast<int2*>(w);
+  p.part_ml = reinterpret_cast<float*>(w + (items * 8 + 255) / 256 * 256);
   p.part_o = p.part_ml + 2 * kTaMaxCtas * (int64_t)p.rows * 2;
   if (D == 64) return launch_tree<64>(p, f, s);
   if (D == 128) return launch_tree<128>(p, f, s);
