@@ -130,10 +130,17 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current_stream = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle, without the Stream object around it: 0.3 us instead of 5 a call
+        global _current_stream
+        if _current_stream is None:
+            import torch._C as c
+            _current_stream = lambda: c._cuda_getCurrentRawStream(c._cuda_getDevice())  # noqa: E731
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -339,10 +346,21 @@ class Chain:
         tb_chain_run(self.plan, self.n, self.M, self.max_K, self.workspace, dev_status, stream)
 
 
-def _tokens(name, t, dtype="torch.float16"):
-    """Distance of two tokens of t [T, heads, D] in elements; its heads and elements must be contiguous."""
-    if t.dim() != 3 or str(t.dtype) != dtype:
-        raise ValueError(f"{name} must be {dtype} [tokens, heads, D], got {t.dtype} {list(t.shape)}")
+_dtypes = None
+
+
+def _types():
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = torch.float16, torch.float32, torch.int32, torch.int64
+    return _dtypes
+
+
+def _tokens(name, t, f16):
+    """Distance of two tokens of t fp16 [T, heads, D] in elements; its heads and elements must be contiguous."""
+    if t.dim() != 3 or t.dtype is not f16:
+        raise ValueError(f"{name} must be {f16} [tokens, heads, D], got {t.dtype} {list(t.shape)}")
     s0, s1, s2 = t.stride()
     T, H, D = t.shape
     if (D > 1 and s2 != 1) or (H > 1 and s1 != D):
@@ -350,11 +368,18 @@ def _tokens(name, t, dtype="torch.float16"):
     return s0 if T > 1 else max(s0, H * D)
 
 
-def _flat(name, t, dtype, shape):
-    """A contiguous tensor of this type and shape (None passes)."""
-    if t is not None and (t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous()):
+def _flat(name, t, dtype, *shape):
+    """Address of a contiguous tensor of this type and shape (None passes)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)} "
                          f"with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _scratch(workspace):
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def tb_cache_plan(cached, fresh, page, free_pages, table, slots, row_start, total, used=None, dev_status=None,
@@ -362,38 +387,29 @@ def tb_cache_plan(cached, fresh, page, free_pages, table, slots, row_start, tota
     """Block table entries, slots and row starts of a step's new tokens: cached, fresh int32 [B],
     free_pages int32 [n], table int32 [B, max_pages] (in/out) -> slots int64 [T], row_start int32
     [B + 1], total int32 [B], used int32 [1] (or None)."""
-    import torch
-
+    _, _, i32, i64 = _types()
     B, max_pages = table.shape
-    _flat("cached", cached, torch.int32, (B,))
-    _flat("fresh", fresh, torch.int32, (B,))
-    _flat("free_pages", free_pages, torch.int32, (free_pages.numel(),))
-    _flat("table", table, torch.int32, (B, max_pages))
-    _flat("slots", slots, torch.int64, (slots.numel(),))
-    _flat("row_start", row_start, torch.int32, (B + 1,))
-    _flat("total", total, torch.int32, (B,))
-    _flat("used", used, torch.int32, (1,))
-    _check("tb_cache_plan", load().tb_cache_plan(_ptr(cached), _ptr(fresh), B, page, _ptr(free_pages),
-                                                 free_pages.numel(), _ptr(table), max_pages, _ptr(slots),
-                                                 slots.numel(), _ptr(row_start), _ptr(total), _ptr(used),
-                                                 _ptr(dev_status), _stream(stream)))
+    n, T = free_pages.numel(), slots.numel()
+    _check("tb_cache_plan", load().tb_cache_plan(
+        _flat("cached", cached, i32, B), _flat("fresh", fresh, i32, B), B, page, _flat("free_pages", free_pages, i32, n),
+        n, _flat("table", table, i32, B, max_pages), max_pages, _flat("slots", slots, i64, T), T,
+        _flat("row_start", row_start, i32, B + 1), _flat("total", total, i32, B), _flat("used", used, i32, 1),
+        _ptr(dev_status), _stream(stream)))
 
 
 def tb_cache_write(k, v, slots, k_cache, v_cache, dev_status=None, stream=None):
     """k, v fp16 [T, Hkv, D] -> their slots (int64 [T], negative: skipped) of the caches fp16
     [pages, Hkv, page, D]."""
-    import torch
-
+    f16, _, _, i64 = _types()
+    ldk, ldv = _tokens("k", k, f16), _tokens("v", v, f16)
     T, H, D = k.shape
     pages, _, page, _ = k_cache.shape
-    ldk, ldv = _tokens("k", k), _tokens("v", v)
     if v.shape != k.shape:
         raise ValueError(f"k and v differ in shape: {list(k.shape)} and {list(v.shape)}")
-    _flat("slots", slots, torch.int64, (T,))
-    _flat("k_cache", k_cache, torch.float16, (pages, H, page, D))
-    _flat("v_cache", v_cache, torch.float16, (pages, H, page, D))
-    _check("tb_cache_write", load().tb_cache_write(_ptr(k), ldk, _ptr(v), ldv, _ptr(slots), T, H, D, _ptr(k_cache),
-                                                   _ptr(v_cache), pages, page, _ptr(dev_status), _stream(stream)))
+    _check("tb_cache_write", load().tb_cache_write(
+        k.data_ptr(), ldk, v.data_ptr(), ldv, _flat("slots", slots, i64, T), T, H, D,
+        _flat("k_cache", k_cache, f16, pages, H, page, D), _flat("v_cache", v_cache, f16, pages, H, page, D), pages, page,
+        _ptr(dev_status), _stream(stream)))
 
 
 def tb_tree_attention_workspace_size(B, T, max_q, Hq, Hkv, D):
@@ -404,45 +420,34 @@ def tb_tree_attention(q, k_cache, v_cache, table, total, row_start, max_q, o, wo
                       dev_status=None, stream=None):
     """Attention of the newest tokens (q fp16 [T, Hq, D]; at most max_q <= 64 a request) over the paged
     cache; tree: uint64 words as int64 [T], or None (causal); scale: 1/sqrt(D) unless given."""
-    import torch
-
+    f16, _, i32, i64 = _types()
+    ldq = _tokens("q", q, f16)
     T, Hq, D = q.shape
     pages, Hkv, page, _ = k_cache.shape
     B, max_pages = table.shape
-    ldq = _tokens("q", q)
-    _flat("k_cache", k_cache, torch.float16, (pages, Hkv, page, D))
-    _flat("v_cache", v_cache, torch.float16, (pages, Hkv, page, D))
-    _flat("table", table, torch.int32, (B, max_pages))
-    _flat("total", total, torch.int32, (B,))
-    _flat("row_start", row_start, torch.int32, (B + 1,))
-    _flat("tree", tree, torch.int64, (T,))
-    _flat("o", o, torch.float16, (T, Hq, D))
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check("tb_tree_attention",
-           load().tb_tree_attention(_ptr(q), ldq, T, Hq, Hkv, D, _ptr(k_cache), _ptr(v_cache), pages, page,
-                                    _ptr(table), max_pages, _ptr(total), _ptr(row_start), B, max_q, _ptr(tree),
-                                    D ** -0.5 if scale is None else scale, _ptr(o), _ptr(workspace), ws_bytes,
-                                    _ptr(dev_status), _stream(stream)))
+    ws, ws_bytes = _scratch(workspace)
+    _check("tb_tree_attention", load().tb_tree_attention(
+        q.data_ptr(), ldq, T, Hq, Hkv, D, _flat("k_cache", k_cache, f16, pages, Hkv, page, D),
+        _flat("v_cache", v_cache, f16, pages, Hkv, page, D), pages, page, _flat("table", table, i32, B, max_pages),
+        max_pages, _flat("total", total, i32, B), _flat("row_start", row_start, i32, B + 1), B, max_q,
+        _flat("tree", tree, i64, T), D ** -0.5 if scale is None else scale, _flat("o", o, f16, T, Hq, D), ws, ws_bytes,
+        _ptr(dev_status), _stream(stream)))
 
 
 def tb_prompt_attention(q, k, v, q_start, k_start, o, scale=None, dev_status=None, stream=None):
     """Causal attention over packed prompts: q fp16 [Tq, Hq, D], k, v fp16 [Tk, Hkv, D], q_start and
     k_start int32 [B + 1]; scale: 1/sqrt(D) unless given."""
-    import torch
-
+    f16, _, i32, _ = _types()
+    ldq, ldk, ldv = _tokens("q", q, f16), _tokens("k", k, f16), _tokens("v", v, f16)
     Tq, Hq, D = q.shape
     Tk, Hkv, _ = k.shape
     B = q_start.numel() - 1
-    ldq, ldk, ldv = _tokens("q", q), _tokens("k", k), _tokens("v", v)
     if v.shape != k.shape or k.shape[2] != D:
         raise ValueError(f"q, k and v do not match: {list(q.shape)}, {list(k.shape)}, {list(v.shape)}")
-    _flat("q_start", q_start, torch.int32, (B + 1,))
-    _flat("k_start", k_start, torch.int32, (B + 1,))
-    _flat("o", o, torch.float16, (Tq, Hq, D))
-    _check("tb_prompt_attention",
-           load().tb_prompt_attention(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, Tq, Tk, Hq, Hkv, D, _ptr(q_start),
-                                      _ptr(k_start), B, D ** -0.5 if scale is None else scale, _ptr(o),
-                                      _ptr(dev_status), _stream(stream)))
+    _check("tb_prompt_attention", load().tb_prompt_attention(
+        q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, Tq, Tk, Hq, Hkv, D,
+        _flat("q_start", q_start, i32, B + 1), _flat("k_start", k_start, i32, B + 1), B,
+        D ** -0.5 if scale is None else scale, _flat("o", o, f16, Tq, Hq, D), _ptr(dev_status), _stream(stream)))
 
 
 def tb_gated_delta_workspace_size(T, B, max_len, Hk, Hv):
@@ -453,28 +458,20 @@ def tb_gated_delta(q, k, v, g, beta, row_start, max_len, o, workspace=None, stat
                    slot_in=None, slot_out=None, normalise=False, scale=None, dev_status=None, stream=None):
     """The gated delta rule: q, k fp16 [T, Hk, D], v fp16 [T, Hv, D], g, beta fp32 [T, Hv], row_start
     int32 [B + 1], states fp32 [n, Hv, D, D] -> o fp16 [T, Hv, D]; scale: 1/sqrt(D) unless given."""
-    import torch
-
+    f16, f32, i32, _ = _types()
+    ldq, ldk, ldv = _tokens("q", q, f16), _tokens("k", k, f16), _tokens("v", v, f16)
     T, Hk, D = q.shape
     Hv = v.shape[1]
     B = row_start.numel() - 1
-    ldq, ldk, ldv = _tokens("q", q), _tokens("k", k), _tokens("v", v)
     if k.shape != q.shape or v.shape[0] != T or v.shape[2] != D:
         raise ValueError(f"q, k and v do not match: {list(q.shape)}, {list(k.shape)}, {list(v.shape)}")
-    _flat("g", g, torch.float32, (T, Hv))
-    _flat("beta", beta, torch.float32, (T, Hv))
-    _flat("row_start", row_start, torch.int32, (B + 1,))
-    _flat("o", o, torch.float16, (T, Hv, D))
     n_in = 0 if state_in is None else state_in.shape[0]
     n_out = 0 if state_out is None else state_out.shape[0]
-    _flat("state_in", state_in, torch.float32, (n_in, Hv, D, D))
-    _flat("state_out", state_out, torch.float32, (n_out, Hv, D, D))
-    _flat("slot_in", slot_in, torch.int32, (B,))
-    _flat("slot_out", slot_out, torch.int32, (B,))
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check("tb_gated_delta",
-           load().tb_gated_delta(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(g), _ptr(beta), T, Hk, Hv, D,
-                                 _ptr(row_start), B, max_len, int(bool(normalise)),
-                                 D ** -0.5 if scale is None else scale, _ptr(state_in), _ptr(slot_in), n_in,
-                                 _ptr(state_out), _ptr(slot_out), n_out, _ptr(o), _ptr(workspace), ws_bytes,
-                                 _ptr(dev_status), _stream(stream)))
+    ws, ws_bytes = _scratch(workspace)
+    _check("tb_gated_delta", load().tb_gated_delta(
+        q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, _flat("g", g, f32, T, Hv),
+        _flat("beta", beta, f32, T, Hv), T, Hk, Hv, D, _flat("row_start", row_start, i32, B + 1), B, max_len,
+        int(bool(normalise)), D ** -0.5 if scale is None else scale, _flat("state_in", state_in, f32, n_in, Hv, D, D),
+        _flat("slot_in", slot_in, i32, B), n_in, _flat("state_out", state_out, f32, n_out, Hv, D, D),
+        _flat("slot_out", slot_out, i32, B), n_out, _flat("o", o, f16, T, Hv, D), ws, ws_bytes, _ptr(dev_status),
+        _stream(stream)))
