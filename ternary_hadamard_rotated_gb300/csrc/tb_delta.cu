@@ -164,12 +164,9 @@ __global__ void __launch_bounds__(kDlThreads) delta_step_kernel(const DeltaArgs 
 }  // namespace tb
 
 extern "C" size_t tb_gated_delta_workspace_size(int64_t T, int64_t B, int64_t max_len, int64_t Hk, int64_t Hv) {
-  (void)T;
-  (void)B;
-  (void)max_len;
   (void)Hk;
-  (void)Hv;
-  return 0;
+  if (T < 1 || B < 1 || Hv < 1 || max_len <= tb::kDeltaStepTokens) return 0;
+  return tb::delta_chunk_workspace(T, B, Hv);
 }
 
 extern "C" int tb_gated_delta(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v,
@@ -182,7 +179,9 @@ extern "C" int tb_gated_delta(const uint16_t* q, int64_t ldq, const uint16_t* k,
   if (T < 0 || T > INT32_MAX || B < 1 || B > INT32_MAX || Hk < 1 || Hv < Hk || Hv > 1024 || Hv % Hk || max_len < 0)
     return TB_ERR_SHAPE;
   if (D != kDeltaD) return TB_ERR_UNSUPPORTED;
-  if (ldq < Hk * D || ldk < Hk * D || ldv < Hv * D || ldq % 8 || ldk % 8 || ldv % 8) return TB_ERR_SHAPE;
+  if (ldq < Hk * D || ldk < Hk * D || ldv < Hv * D || ldq % 8 || ldk % 8 || ldv % 8 || ldq > 1ll << 31 ||
+      ldk > 1ll << 31)
+    return TB_ERR_SHAPE;
   if ((state_in && (n_in < 1 || (!slot_in && n_in < B))) || (state_out && (n_out < 1 || (!slot_out && n_out < B))))
     return TB_ERR_SHAPE;
   if (!(scale > -INFINITY && scale < INFINITY)) return TB_ERR_VALUE;
@@ -191,6 +190,7 @@ extern "C" int tb_gated_delta(const uint16_t* q, int64_t ldq, const uint16_t* k,
       !aligned16(o) || !aligned_to(row_start, 4) || !aligned16(state_in) || !aligned16(state_out) ||
       !aligned_to(slot_in, 4) || !aligned_to(slot_out, 4) || !aligned16(workspace))
     return TB_ERR_ALIGN;
+  if (max_len > kDeltaStepTokens && T && !workspace) return TB_ERR_WORKSPACE;
   if (workspace_bytes < tb_gated_delta_workspace_size(T, B, max_len, Hk, Hv)) return TB_ERR_WORKSPACE;
   DeviceFacts f;
   int rc = device_facts(&f);
@@ -222,6 +222,7 @@ extern "C" int tb_gated_delta(const uint16_t* q, int64_t ldq, const uint16_t* k,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t heads = B * Hv;
   if (heads * 4 > INT32_MAX) return TB_ERR_TOO_LARGE;
+  if (max_len > kDeltaStepTokens && T) return launch_delta_chunks(a, workspace, s);
   // whole heads per CTA once they fill the SMs twice over; below that a quarter of a head each
   if (heads >= 2 * f.sms) delta_step_kernel<128><<<(int)heads, kDlThreads, 0, s>>>(a);
   else delta_step_kernel<32><<<(int)(heads * 4), kDlThreads, 0, s>>>(a);

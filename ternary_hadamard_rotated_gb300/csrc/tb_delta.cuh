@@ -44,6 +44,13 @@ TB_DEVI int64_t delta_slot(const int32_t* slots, int b, int64_t n, int32_t* stat
   return s;
 }
 
+// requests of up to so many tokens take the recurrent kernel
+constexpr int64_t kDeltaStepTokens = 8;
+
+// the chunked form, and its workspace
+int launch_delta_chunks(const DeltaArgs& a, void* workspace, cudaStream_t s);
+size_t delta_chunk_workspace(int64_t T, int64_t B, int64_t Hv);
+
 TB_DEVI float4 load_half4(const __half* p) {
   const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
   const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
