@@ -16,22 +16,16 @@
 // per column, the column in registers), P T by mma.sync.  It writes T (fp16, high and low part) and
 // P T (fp16) as the shared-memory image that kernel 2's MMAs read, and each token's factors.
 //
-// Kernel 2, a CTA per (request, value head, 32 columns of v), walks the chunks.  The state is fp32 in
-// registers (thread = row of S); every product is a tcgen05 MMA of 128 rows, its fp32 result in tensor
-// memory:
-//   [K; Q] S      rows: 64 tokens of K and of Q       -> S^T k, S^T q
-//   [T; P T] R    rows: 64 tokens twice               -> U, the chunk's part of o
-//   K^T (w U)     rows: the 128 rows of the state     -> the state's increment
-// An fp32 factor (S, R, w U) goes in as two fp16 terms, x 2^e = hi + lo 2^-11, side by side in the 64
-// columns of one operand, so that one MMA gives both partial sums: 22 bits of x, with a power of two
-// per chunk that keeps it inside fp16's range (operand_scale).  K and Q are fp16 already.  T also has
-// two terms.  What goes into o alone (P T) has one.
-// The products of a chunk depend on one another through S, so a CTA's chunk costs three round trips
-// between tensor memory and registers, about 1.3 us; two CTAs share an SM and fill each other's waits.
-//
-// [K; Q] has to be 128 consecutive rows, K is needed until the chunk's last product, and Q's room can
-// be used again after the first: K has two places, with Q between them, and every other chunk reads
-// [Q; K] and [P T; T] instead.
+// Kernel 2 walks the chunks, a warp per 16 columns of v, which no other warp's columns depend on: S^T
+// stays in the warp's registers as fp32 accumulators of mma.sync, and every product's left factor (S^T,
+// R^T, (w U)^T, 16 rows) comes out of the product before it in the layout that the next one wants, so
+// a chunk has no exchange between warps at all.  K, Q, V and kernel 1's results come by TMA, three
+// chunks deep.  An fp32 factor goes in as two fp16 terms, x 2^e = hi + lo with the warp's largest |x|
+// at 2^14: 22 bits, and K and Q are fp16 already.  T has two terms too; what goes into o alone has one.
+// About 400 MMAs a warp and chunk, at one per 7.8 clocks and SM sub-partition 1.6 us: what bounds it.
+// (The same walk on tcgen05, 32 columns a CTA, took 2.7 us a chunk alone on its SM and 3.4 with a
+// second CTA: 20 MMAs of 44 to 60 clocks, and three trips through registers, shared memory and a
+// barrier of 800 to 1000 each.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -45,9 +39,8 @@
 namespace tb {
 
 constexpr int kDcTok = 64;    // tokens per chunk
-constexpr int kDcCols = 32;   // columns of v per CTA of kernel 2
 constexpr int kDcBlock = kDcTok * 128;  // bytes of a 64 x 64 fp16 image
-// a (chunk, value head) in the workspace: [T; P T] (or [P T; T]), T's low part, factors
+// a (chunk, value head) in the workspace: T, P T, T's low part, factors
 constexpr int kDcItem = 3 * kDcBlock + 1024;
 constexpr int kDcFactors = 3 * kDcBlock;  // floats: c [64], w [64], q [64], exp(gamma_C)
 
@@ -298,11 +291,10 @@ __global__ void __launch_bounds__(kD1Threads, 2) delta_prep_kernel(const ChunkAr
       }
     }
     sync_pair();
-    const int t_at = (c & 1) ? kDcBlock : 0, pt_at = kDcBlock - t_at;  // odd chunks: [P T; T]
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int o = (e * 64 + l64) * 16;
-      *reinterpret_cast<uint4*>(item + t_at + o) = *reinterpret_cast<const uint4*>(img + o);
+      *reinterpret_cast<uint4*>(item + o) = *reinterpret_cast<const uint4*>(img + o);
       *reinterpret_cast<uint4*>(item + 2 * kDcBlock + o) = *reinterpret_cast<const uint4*>(img + kDcBlock + o);
     }
     // P T: 32 rows a warp, P made from Q K^T as the A fragments
@@ -347,7 +339,7 @@ __global__ void __launch_bounds__(kD1Threads, 2) delta_prep_kernel(const ChunkAr
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int i = i0 + e * 8;
-          *reinterpret_cast<uint32_t*>(item + pt_at + i * 128 + ((j ^ (i & 7)) << 4) + (lane & 3) * 4) =
+          *reinterpret_cast<uint32_t*>(item + kDcBlock + i * 128 + ((j ^ (i & 7)) << 4) + (lane & 3) * 4) =
               pack_half2(acc[j][2 * e], acc[j][2 * e + 1]);
         }
     }
@@ -356,132 +348,73 @@ __global__ void __launch_bounds__(kD1Threads, 2) delta_prep_kernel(const ChunkAr
 }
 
 // ---------------------------------------------------------------- kernel 2
-constexpr int kD2Threads = 192;  // warps 0-3: registers <-> tensor memory; 4: loads; 5: MMAs
-constexpr int kD2KQ = 24576;     // 64 elements of [K even | Q | K odd], 64 rows each
-constexpr int kD2X = 2 * kD2KQ;              // [T; P T]
-constexpr int kD2TLow = kD2X + 2 * kDcBlock; // T's low part (what lies behind it is read as idle rows)
-constexpr int kD2S = kD2TLow + kDcBlock;     // the state's operand: 128 rows of 128 bytes
-constexpr int kD2R = kD2S + 16384;           // R, then w U: 64 rows of 128 bytes
-constexpr int kD2Bars = kD2R + kDcBlock;
-constexpr int kD2Smem = kD2Bars + 256 + 1024;
-constexpr float kDcLow = 1.f / 2048.f;
+constexpr int kD2Stages = 3;
+constexpr int kD2Q = 2 * kDcBlock, kD2Item = 4 * kDcBlock, kD2V = kD2Item + 26624;  // places in a stage
 
-// 16 fp32 values (columns 16 half ..) of a row of the operand [hi (32 halves) | lo (32 halves)], in the
-// 128-byte swizzle; x = hi + lo / 2048
-TB_DEVI void store_split(uint32_t base, int row, int half, const float (&x)[16]) {
-  const uint32_t at = base + (uint32_t)row * 128u, sw = (uint32_t)row & 7u;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float u = x[c * 8 + e * 2], v = x[c * 8 + e * 2 + 1];
-      const __half2 h = __floats2half2_rn(u, v);
-      const float2 f = __half22float2(h);
-      hi[e] = *reinterpret_cast<const uint32_t*>(&h);
-      lo[e] = pack_half2((u - f.x) * 2048.f, (v - f.y) * 2048.f);
-    }
-    const uint32_t k = (uint32_t)(half * 2 + c);
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + 16u * (k ^ sw)), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]),
-                 "r"(hi[3])
-                 : "memory");
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + 16u * ((k + 4) ^ sw)), "r"(lo[0]), "r"(lo[1]),
-                 "r"(lo[2]), "r"(lo[3])
-                 : "memory");
-  }
-}
+template <int W>
+struct ScanCfg {
+  static constexpr int kThreads = (W + 1) * 32;
+  static constexpr int kStage = kD2V + W / 4 * kDcBlock;
+  static constexpr int kBytes = 4 * kDcBlock + kDcItem + W / 4 * kDcBlock;  // loaded per chunk
+  static constexpr int kSmem = 1024 + kD2Stages * kStage + 128;
+};
 
-// 16 columns of the high and of the low partial sums of the thread's lane; complete after tmem_wait_ld()
-TB_DEVI void tmem_ld16(uint32_t taddr, float (&d)[16]) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(d);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-
-// The operands' scale for magnitudes up to `bits` (an fp32's): a power of two that takes them to 2^7.
-// S, R and w U of the next chunk are at most some 2^8 times the largest of S now and of the next v
-// (a column of S grows by at most 64 steps of |v|, and 128 of its elements meet a k of norm 1), so
-// fp16's 2^15 holds them, and 22 bits remain down to 2^-26 of that.  Inputs for which this does not
-// hold (steps above 1 on long keys) overflow to infinity, as the recurrence itself then does.
+// a power of two that takes magnitudes up to `bits` (an fp32's) to 2^14, and its inverse
 TB_DEVI float operand_scale(uint32_t bits, float& inverse) {
-  int e = 261 - (int)(bits >> 23);
-  e = e < 127 - 60 ? 127 - 60 : (e > 127 + 60 ? 127 + 60 : e);
+  int e = 268 - (int)(bits >> 23);
+  e = e < 127 - 100 ? 127 - 100 : (e > 127 + 100 ? 127 + 100 : e);
   inverse = __int_as_float((254 - e) << 23);
   return __int_as_float(e << 23);
 }
+TB_DEVI uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }  // orders as the values do, NaN last
+// x, y -> fp16 pair and the fp16 pair of what it leaves
+TB_DEVI void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack_half2(x - f.x, y - f.y);
+}
+TB_DEVI uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
 
-__global__ void __launch_bounds__(kD2Threads, 2)
-    delta_scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ, const ChunkArgs p) {
+// W warps per CTA, 16 columns of v each; warp W loads.
+template <int W>
+__global__ void __launch_bounds__((W + 1) * 32, 1)
+    delta_scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmV, const ChunkArgs p) {
+  using C = ScanCfg<W>;
   const DeltaArgs& a = p.a;
   extern __shared__ uint8_t d2_raw[];
   const uint32_t raw = smem_u32(d2_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = d2_raw + (base - raw);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kD2Bars);
-  uint64_t *k_full = bars, *k_empty = bars + 2;  // [2] each
-  uint64_t *q_full = bars + 4, *q_empty = bars + 5, *x_full = bars + 6, *x_empty = bars + 7;
-  uint64_t *s_ready = bars + 8, *r_ready = bars + 9, *u_ready = bars + 10;
-  uint64_t *d1_full = bars + 11, *d2_full = bars + 12, *d3_full = bars + 13;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
-  volatile int* aborted = reinterpret_cast<volatile int*>(bars + 15);
-  // largest |S|, |v| that a chunk's operands come from, as fp32 bits: one word for this chunk, one that
-  // is being collected for the next, one to spare
-  uint32_t* largest = reinterpret_cast<uint32_t*>(bars + 16);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kD2Stages * C::kStage);
+  uint64_t* empty = full + kD2Stages;
+  volatile int* aborted = reinterpret_cast<volatile int*>(full + 2 * kD2Stages);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kSlices = kDeltaD / kDcCols;
+  constexpr int kSlices = 8 / W;
   const int slice = (int)(blockIdx.x % kSlices);
   const int64_t bh = blockIdx.x / kSlices;
   const int h = (int)(bh % a.Hv), b = (int)(bh / a.Hv), hk = h / (a.Hv / a.Hk);
-
   if (tid == 0) {
     *aborted = 0;
-    largest[0] = largest[1] = largest[2] = 0;
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + i, 1);
-      mbar_init(k_empty + i, 1);
+    for (int i = 0; i < kD2Stages; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, W);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    mbar_init(x_full, 1);
-    mbar_init(x_empty, 1);
-    mbar_init(s_ready, 4);
-    mbar_init(r_ready, 2);
-    mbar_init(u_ready, 4);
-    mbar_init(d1_full, 1);
-    mbar_init(d2_full, 1);
-    mbar_init(d3_full, 1);
     fence_barrier_init();
   }
-  if (warp == 5) tmem_alloc(tmem_slot, 256);
-
   int64_t t0, len;
   if (!delta_rows(a, b, t0, len)) {
     if (tid == 0 && h == 0 && slice == 0) set_status(a.status, TB_DEV_BAD_LEN);
     len = 0;
   }
   const int nc = (int)((len + kDcTok - 1) / kDcTok);
-  // the request's first chunk
-  int64_t first = 0;
-  {
-    const ChunkScan sc = chunk_scan(a, lane);
-    int64_t before = sc.upto - sc.own;
-    const int src = b / sc.per;
-    if (lane == src)
-      for (int i = lane * sc.per; i < b; ++i) before += chunks_of(a, i);
-    first = __shfl_sync(0xffffffffu, before, src);
-  }
-  auto item = [&](int c) { return p.ws + ((first + c) * a.Hv + h) * (int64_t)kDcItem; };
-
-  tmem_fence_before();
   __syncthreads();
-  tmem_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  // tensor memory: [K;Q] S | [T;PT] R | T low R | K^T wU, 64 columns each
-  constexpr uint32_t kT1 = 0, kT2 = 64, kT2b = 128, kT3 = 192;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity) || *aborted) return;
     if (!mbar_wait(bar, parity)) {
@@ -490,25 +423,29 @@ __global__ void __launch_bounds__(kD2Threads, 2)
     }
   };
 
-  if (warp == 4) {
+  if (warp == W) {
+    // the request's first chunk
+    const ChunkScan sc = chunk_scan(a, lane);
+    int64_t first = sc.upto - sc.own;
+    const int src = b / sc.per;
+    if (lane == src)
+      for (int i = lane * sc.per; i < b; ++i) first += chunks_of(a, i);
+    first = __shfl_sync(0xffffffffu, first, src);
     if (lane == 0) {
-      bool waited = false;
       for (int c = 0; c < nc; ++c) {
-        const int odd = c & 1, row = (int)(t0 + (int64_t)c * kDcTok);
-        if (c >= 2) wait(k_empty + odd, ((c >> 1) - 1) & 1);
-        mbar_arrive_expect_tx(k_full + odd, 2 * kDcBlock);
-        for (int d = 0; d < 2; ++d)
-          tma_load_3d<1>(base + d * kD2KQ + odd * 2 * kDcBlock, &tmK, d * 64, hk, row, smem_u32(k_full + odd));
-        if (c >= 1) wait(q_empty, (c - 1) & 1);
-        mbar_arrive_expect_tx(q_full, 2 * kDcBlock);
-        for (int d = 0; d < 2; ++d) tma_load_3d<1>(base + d * kD2KQ + kDcBlock, &tmQ, d * 64, hk, row, smem_u32(q_full));
-        if (c >= 1) wait(x_empty, (c - 1) & 1);
-        if (!waited) {  // kernel 1's results
-          asm volatile("griddepcontrol.wait;" ::: "memory");
-          waited = true;
+        const int s = c % kD2Stages, row = (int)(t0 + (int64_t)c * kDcTok);
+        uint8_t* st = smem + s * C::kStage;
+        const uint32_t sa = base + s * C::kStage, bar = smem_u32(full + s);
+        if (c >= kD2Stages) wait(empty + s, (c / kD2Stages - 1) & 1);
+        mbar_arrive_expect_tx(full + s, C::kBytes);
+        for (int d = 0; d < 2; ++d) {
+          tma_load_3d<1>(sa + d * kDcBlock, &tmK, d * 64, hk, row, bar);
+          tma_load_3d<1>(sa + kD2Q + d * kDcBlock, &tmQ, d * 64, hk, row, bar);
         }
-        mbar_arrive_expect_tx(x_full, 3 * kDcBlock);
-        bulk_g2s(smem + kD2X, item(c), 3 * kDcBlock, x_full);
+        for (int d = 0; d < W / 4; ++d)
+          tma_load_3d<1>(sa + kD2V + d * kDcBlock, &tmV, (slice * (W / 4) + d) * 64, h, row, bar);
+        if (c == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1's results
+        bulk_g2s(st + kD2Item, p.ws + ((first + c) * a.Hv + h) * (int64_t)kDcItem, kDcItem, full + s);
       }
       if (*aborted) {  // a wait gave up: leave the copies in flight time to land before the CTA ends
         const uint64_t t = globaltimer_ns();
@@ -516,268 +453,242 @@ __global__ void __launch_bounds__(kD2Threads, 2)
         }
       }
     }
-    __syncwarp();
-  } else if (warp == 5) {
-    if (lane == 0) {
-      constexpr uint32_t kN64 = (64u >> 3) << 17, kM128 = (128u >> 4) << 24, kF32 = 1u << 4, kTransA = 1u << 15,
-                         kTransB = 1u << 16;
-      constexpr uint32_t kId = kF32 | kTransB | kN64 | kM128, kIdT = kId | kTransA;
-      const uint64_t sdesc = smem_desc_mn128(base + kD2S, 0, 1024), rdesc = smem_desc_mn128(base + kD2R, 0, 1024);
-      for (int c = 0; c < nc; ++c) {
-        const int odd = c & 1;
-        wait(k_full + odd, (c >> 1) & 1);
-        wait(q_full, c & 1);
-        wait(s_ready, c & 1);
-        tmem_fence_after();
+    return;
+  }
+
+  const int g = lane >> 2, t2 = (lane & 3) * 2;
+  const int64_t si = delta_slot(a.slot_in, b, a.n_in, a.status), so = delta_slot(a.slot_out, b, a.n_out, a.status);
+  const int64_t head_size = (int64_t)a.Hv * kDeltaD * kDeltaD;
+  const int col = slice * W * 16 + warp * 16;  // the warp's first column of v
+  // S^T: rows g, g + 8 (columns of v), columns 8 j + t2, + 1 (of k)
+  float S[16][4];
+  {
+    const bool have = a.state_in && si >= 0;
+    const float* src = a.state_in + si * head_size + ((int64_t)h * kDeltaD + t2) * kDeltaD + col + g;
 #pragma unroll
-        for (int d = 0; d < 2; ++d)
+    for (int j = 0; j < 16; ++j)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ss<1>(tmem + kT1, smem_desc_sw128(base + d * kD2KQ + odd * kDcBlock + kk * 32, 1024),
-                          sdesc + (d * 4 + kk) * (2048 >> 4), kId, (d | kk) != 0);
-        mma_commit(d1_full);
-        mma_commit(q_empty);
-        wait(x_full, c & 1);
-        wait(r_ready, c & 1);
-        tmem_fence_after();
+      for (int e = 0; e < 4; ++e)
+        S[j][e] = have ? __ldg(src + (j * 8 + (e & 1)) * kDeltaD + (e >> 1) * 8) : 0.f;
+  }
+  // addresses of the ldmatrix lanes inside a 64 x 64 image: rows by the lane, a 16-byte piece per k
+  const uint32_t sw = (uint32_t)lane & 7u;
+  const uint32_t row_n = (((uint32_t)lane & 7u) + ((uint32_t)lane >> 4) * 8u) * 128u;  // rows are n
+  const uint32_t row_k = ((uint32_t)lane & 15u) * 128u;                                // rows are k
+  const uint32_t pc_n = ((uint32_t)lane >> 3) & 1u, pc_k = (uint32_t)lane >> 4;
+  const uint32_t v_row = ((((uint32_t)lane >> 4) & 1u) * 8u + sw) * 128u;
+  const uint32_t v_pc = (((uint32_t)(warp & 3) * 2u + pc_n) ^ sw) << 4;
+
+  for (int c = 0; c < nc; ++c) {
+    const int s = c % kD2Stages;
+    const uint32_t K = base + s * C::kStage, Q = K + kD2Q, X = K + kD2Item, V = K + kD2V + (warp >> 2) * kDcBlock;
+    const float* f = reinterpret_cast<const float*>(smem + s * C::kStage + kD2Item + kDcFactors);
+    const int n = (int)(len - (int64_t)c * kDcTok < kDcTok ? len - (int64_t)c * kDcTok : kDcTok);
+    uint32_t big = 0;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_f16_ss<1>(tmem + kT2, smem_desc_sw128(base + kD2X + kk * 32, 1024), rdesc + kk * (2048 >> 4), kId, kk != 0);
-        // T's low part in the rows that T has: the other 64 rows read whatever lies there, into lanes
-        // that nobody reads
+    for (int j = 0; j < 16; ++j)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_f16_ss<1>(tmem + kT2b, smem_desc_sw128(base + kD2TLow - odd * kDcBlock + kk * 32, 1024),
-                        rdesc + kk * (2048 >> 4), kId, kk != 0);
-        mma_commit(d2_full);
-        mma_commit(x_empty);
-        wait(u_ready, c & 1);
-        tmem_fence_after();
-        const uint64_t kt = smem_desc_mn128(base + odd * 2 * kDcBlock, kD2KQ, 1024);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_f16_ss<1>(tmem + kT3, kt + kk * (2048 >> 4), rdesc + kk * (2048 >> 4), kIdT, kk != 0);
-        mma_commit(d3_full);
-        mma_commit(k_empty + odd);
+      for (int e = 0; e < 4; ++e) big = max(big, magnitude(S[j][e]));
+    float down_s;
+    const float up_s = operand_scale(__reduce_max_sync(0xffffffffu, big), down_s);
+    wait(full + s, (c / kD2Stages) & 1);
+    if (n < kDcTok) {  // the last chunk: rows of K that are another request's, out of the sum over the tokens
+      for (int i = tid; i < (kDcTok - n) * 16; i += W * 32) {
+        const int r = n + (i >> 4), x = i & 15;
+        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(K + (x >> 3) * kDcBlock + r * 128 + (x & 7) * 16), "r"(0)
+                     : "memory");
       }
+      asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
+    }
+    // S^T k, S^T q
+    float R[8][4], O[8][4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) R[j][e] = O[j][e] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float* x = S[2 * ks + (q >> 1)] + (q & 1) * 2;
+        split2(x[0] * up_s, x[1] * up_s, hi[q], lo[q]);
+      }
+      const uint32_t at = (ks >> 2) * kDcBlock + row_n + (((uint32_t)(ks & 3) * 2u + pc_n) ^ sw) * 16u;
+      uint32_t bk[4][4], bq[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ldsm4(K + at + j * 2048, bk[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mma_16816(R[2 * j], hi, bk[j][0], bk[j][1]);
+        mma_16816(R[2 * j + 1], hi, bk[j][2], bk[j][3]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ldsm4(Q + at + j * 2048, bq[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mma_16816(R[2 * j], lo, bk[j][0], bk[j][1]);
+        mma_16816(R[2 * j + 1], lo, bk[j][2], bk[j][3]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mma_16816(O[2 * j], hi, bq[j][0], bq[j][1]);
+        mma_16816(O[2 * j + 1], hi, bq[j][2], bq[j][3]);
+      }
+    }
+    // R = v - exp(gamma) S^T k
+    big = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t vv[4];
+      ldsm4_trans(V + j * 2048 + v_row + v_pc, vv);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {  // token tile 2 j + q / 2, columns of v g + 8 (q % 2)
+        const int nt = 2 * j + (q >> 1), tok = nt * 8 + t2, e = (q & 1) * 2;
+        const float2 cc = *reinterpret_cast<const float2*>(f + tok);
+        const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&vv[q]));
+        R[nt][e] = tok < n ? fmaf(-cc.x * down_s, R[nt][e], w.x) : 0.f;
+        R[nt][e + 1] = tok + 1 < n ? fmaf(-cc.y * down_s, R[nt][e + 1], w.y) : 0.f;
+        big = max(big, max(magnitude(R[nt][e]), magnitude(R[nt][e + 1])));
+      }
+    }
+    float down_r;
+    const float up_r = operand_scale(__reduce_max_sync(0xffffffffu, big), down_r);
+    uint32_t rh[4][4], rl[4][4];
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float* x = R[2 * ks + (q >> 1)] + (q & 1) * 2;
+        split2(x[0] * up_r, x[1] * up_r, rh[ks][q], rl[ks][q]);
+      }
+    // U = T R (rows past a token do not reach it: their tiles are left out), o = q-part + P T R
+    float U[8][4];
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      const float2 qq = *reinterpret_cast<const float2*>(f + 128 + nt * 8 + t2);
+      const float qx = qq.x * down_s * up_r, qy = qq.y * down_s * up_r;
+      O[nt][0] *= qx;
+      O[nt][1] *= qy;
+      O[nt][2] *= qx;
+      O[nt][3] *= qy;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) U[nt][e] = 0.f;
+    }
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      const uint32_t at = X + row_n + (((uint32_t)ks * 2u + pc_n) ^ sw) * 16u;
+#pragma unroll
+      for (int j = ks; j < 4; ++j) {
+        uint32_t th[4], tl[4], pt[4];
+        ldsm4(at + j * 2048, th);
+        ldsm4(at + 2 * kDcBlock + j * 2048, tl);
+        ldsm4(at + kDcBlock + j * 2048, pt);
+        mma_16816(U[2 * j], rh[ks], th[0], th[1]);
+        mma_16816(U[2 * j + 1], rh[ks], th[2], th[3]);
+        mma_16816(O[2 * j], rh[ks], pt[0], pt[1]);
+        mma_16816(O[2 * j + 1], rh[ks], pt[2], pt[3]);
+        mma_16816(U[2 * j], rl[ks], th[0], th[1]);
+        mma_16816(U[2 * j + 1], rl[ks], th[2], th[3]);
+        mma_16816(U[2 * j], rh[ks], tl[0], tl[1]);
+        mma_16816(U[2 * j + 1], rh[ks], tl[2], tl[3]);
+      }
+    }
+    // w U
+    big = 0;
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      const float2 ww = *reinterpret_cast<const float2*>(f + 64 + nt * 8 + t2);
+      const float wx = ww.x * down_r, wy = ww.y * down_r;
+      U[nt][0] *= wx;
+      U[nt][1] *= wy;
+      U[nt][2] *= wx;
+      U[nt][3] *= wy;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) big = max(big, magnitude(U[nt][e]));
+    }
+    float down_u;
+    const float up_u = operand_scale(__reduce_max_sync(0xffffffffu, big), down_u);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float* x = U[2 * ks + (q >> 1)] + (q & 1) * 2;
+        split2(x[0] * up_u, x[1] * up_u, rh[ks][q], rl[ks][q]);
+      }
+    // S <- exp(gamma_C) S + K^T (w U); the increment is summed by itself, so that the state's own
+    // rounding is one fp32 fma a chunk
+    const float dec = f[192];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float dh[2][4], dl[2][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dh[0][e] = dh[1][e] = dl[0][e] = dl[1][e] = 0.f;
+      const uint32_t at = K + (j >> 2) * kDcBlock + row_k + (((uint32_t)(j & 3) * 2u + pc_k) ^ sw) * 16u;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        uint32_t bk[4];
+        ldsm4_trans(at + ks * 2048, bk);
+        mma_16816(dh[0], rh[ks], bk[0], bk[1]);
+        mma_16816(dh[1], rh[ks], bk[2], bk[3]);
+        mma_16816(dl[0], rl[ks], bk[0], bk[1]);
+        mma_16816(dl[1], rl[ks], bk[2], bk[3]);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[2 * j + x][e] = fmaf(dec, S[2 * j + x][e], (dh[x][e] + dl[x][e]) * down_u);
     }
     __syncwarp();
-  } else {
-    const int row = tid;  // of the state, and lane of tensor memory
-    const uint32_t mine = tmem + ((uint32_t)warp << 21);
-    const int64_t si = delta_slot(a.slot_in, b, a.n_in, a.status), so = delta_slot(a.slot_out, b, a.n_out, a.status);
-    const int64_t in_head = ((int64_t)h * kDeltaD + row) * kDeltaD + slice * kDcCols;
-    const int64_t head_size = (int64_t)a.Hv * kDeltaD * kDeltaD;
-    float S[32];
-    if (a.state_in && si >= 0) {
-      const float4* src = reinterpret_cast<const float4*>(a.state_in + si * head_size + in_head);
+    if (lane == 0) mbar_arrive(empty + s);
+    // o: back to rows of tokens
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 v = __ldg(src + i);
-        S[4 * i] = v.x;
-        S[4 * i + 1] = v.y;
-        S[4 * i + 2] = v.z;
-        S[4 * i + 3] = v.w;
+    for (int nt = 0; nt < 8; ++nt) {
+      const uint32_t x = transpose8x8(pack_half2(O[nt][0] * down_r, O[nt][1] * down_r));
+      const uint32_t y = transpose8x8(pack_half2(O[nt][2] * down_r, O[nt][3] * down_r));
+      const int tok = nt * 8 + g;
+      if (tok < n) {
+        __half* dst = a.o + ((t0 + (int64_t)c * kDcTok + tok) * a.Hv + h) * kDeltaD + col + t2;
+        *reinterpret_cast<uint32_t*>(dst) = x;
+        *reinterpret_cast<uint32_t*>(dst + 8) = y;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) S[i] = 0.f;
-    }
-    const int tok = row & 63;
-    // what a chunk needs besides the MMAs: the token's factors, and v where the thread has its K row
-    // (it has K rows in one chunk and Q rows in the next); fetched a chunk ahead
-    float f0 = 0.f, f1 = 0.f, decay = 0.f;
-    uint4 v[4];
-    auto fetch = [&](int c) {
-      const float* f = reinterpret_cast<const float*>(item(c) + kDcFactors);
-      const bool keys = (row >> 6) == (c & 1);
-      decay = __ldcg(f + 192);
-      f0 = __ldcg(f + (keys ? 0 : 128) + tok);
-      if (keys) {
-        f1 = __ldcg(f + 64 + tok);
-        const int64_t t = t0 + (int64_t)c * kDcTok + tok;
-        const uint4* vp = reinterpret_cast<const uint4*>(a.v + t * a.ldv + h * kDeltaD + slice * kDcCols);
-        const bool live = t < t0 + len;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = live ? __ldg(vp + i) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto collect = [&](uint32_t bits, int c) {  // into the word of chunk c
-      bits = __reduce_max_sync(0xffffffffu, bits);
-      if (lane == 0) atomicMax(largest + c % 3, bits);
-    };
-    auto largest_s = [&]() {
-      float m = 0.f;
-      bool nan = false;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        m = fmaxf(m, fabsf(S[i]));
-        nan |= S[i] != S[i];
-      }
-      return nan ? 0x7f800000u : __float_as_uint(m);
-    };
-    auto largest_v = [&]() {  // fp16 magnitudes order as integers
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-      }
-      return m >= 0x7c00u ? 0x7f800000u : __float_as_uint(half_bits_to_float((uint16_t)m));
-    };
-    float up = 1.f, down = 1.f;  // the chunk's scale and its inverse
-    auto store_state = [&]() {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float y[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = S[half * 16 + i] * up;
-        store_split(base + kD2S, row, half, y);
-      }
-      fence_proxy_async_smem();
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(s_ready);
-    };
-    if (nc > 0) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      fetch(0);
-      collect(largest_s(), 0);
-      if ((row >> 6) == 0) collect(largest_v(), 0);
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      up = operand_scale(*reinterpret_cast<volatile uint32_t*>(largest), down);
-      store_state();
-    }
-    for (int c = 0; c < nc; ++c) {
-      const int odd = c & 1;
-      const bool keys = (row >> 6) == odd;  // this thread's token: its K row (R, U), or its Q row (o)
-      const bool live = (int64_t)c * kDcTok + tok < len;
-      const float c0 = f0, c1 = f1, dec = decay;
-      uint4 cv[4];
-      if (keys) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) cv[i] = v[i];
-      }
-      if (c + 1 < nc) fetch(c + 1);
-      if (row == 0) largest[(c + 2) % 3] = 0;
-      collect(largest_s(), c + 1);
-      wait(d1_full, c & 1);
-      tmem_fence_after();
-      if (keys) {
-        // R = v - exp(gamma) S^T k, all times the scale
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x[16], y[16];
-          tmem_ld16(mine + kT1 + half * 16, x);
-          tmem_ld16(mine + kT1 + 32 + half * 16, y);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const __half2* hv = reinterpret_cast<const __half2*>(&cv[half * 2 + i]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int k = i * 8 + e * 2;
-              const float2 w = __half22float2(hv[e]);
-              x[k] = live ? fmaf(-c0, fmaf(y[k], kDcLow, x[k]), w.x * up) : 0.f;
-              x[k + 1] = live ? fmaf(-c0, fmaf(y[k + 1], kDcLow, x[k + 1]), w.y * up) : 0.f;
-            }
-          }
-          store_split(base + kD2R, tok, half, x);
-        }
-        fence_proxy_async_smem();
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(r_ready);
-        wait(d2_full, c & 1);
-        tmem_fence_after();
-        // w U
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x[16], y[16], z[16];
-          tmem_ld16(mine + kT2 + half * 16, x);
-          tmem_ld16(mine + kT2 + 32 + half * 16, y);
-          tmem_ld16(mine + kT2b + half * 16, z);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = live ? c1 * (fmaf(y[i], kDcLow, x[i]) + z[i]) : 0.f;
-          store_split(base + kD2R, tok, half, x);
-        }
-        if (!live) {  // rows of K that are another request's: out of the sum over the tokens
-#pragma unroll
-          for (int d = 0; d < 2; ++d)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(base + d * kD2KQ + odd * 2 * kDcBlock +
-                                                                         (uint32_t)tok * 128u + e * 16),
-                           "r"(0)
-                           : "memory");
-        }
-        fence_proxy_async_smem();
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(u_ready);
-      } else {
-        // o = exp(gamma) scale S^T q + the chunk's own part
-        float y[32];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x[16], z[16];
-          tmem_ld16(mine + kT1 + half * 16, x);
-          tmem_ld16(mine + kT1 + 32 + half * 16, z);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) y[half * 16 + i] = c0 * fmaf(z[i], kDcLow, x[i]);
-        }
-        if (c + 1 < nc) collect(largest_v(), c + 1);  // the next chunk's v, which this thread has
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(u_ready);  // the word for the next chunk's scale is complete
-        wait(d2_full, c & 1);
-        tmem_fence_after();
-        uint4* dst = reinterpret_cast<uint4*>(a.o + ((t0 + (int64_t)c * kDcTok + tok) * a.Hv + h) * kDeltaD + slice * kDcCols);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x[16], z[16];
-          tmem_ld16(mine + kT2 + half * 16, x);
-          tmem_ld16(mine + kT2 + 32 + half * 16, z);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = down * (y[half * 16 + i] + fmaf(z[i], kDcLow, x[i]));
-          if (live) {
-            dst[half * 2] = make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]),
-                                       pack_half2(x[6], x[7]));
-            dst[half * 2 + 1] = make_uint4(pack_half2(x[8], x[9]), pack_half2(x[10], x[11]), pack_half2(x[12], x[13]),
-                                           pack_half2(x[14], x[15]));
-          }
-        }
-      }
-      wait(d3_full, c & 1);
-      tmem_fence_after();
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float x[16], y[16];
-        tmem_ld16(mine + kT3 + half * 16, x);
-        tmem_ld16(mine + kT3 + 32 + half * 16, y);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          S[half * 16 + i] = fmaf(dec, S[half * 16 + i], fmaf(y[i], kDcLow, x[i]) * down);
-      }
-      if (c + 1 < nc) {
-        up = operand_scale(*reinterpret_cast<volatile uint32_t*>(largest + (c + 1) % 3), down);
-        store_state();
-      }
-    }
-    if (a.state_out && so >= 0) {
-      float4* dst = reinterpret_cast<float4*>(a.state_out + so * head_size + in_head);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) dst[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
     }
   }
-  tmem_fence_before();
-  __syncthreads();
-  if (warp == 5) tmem_dealloc(tmem, 256);
+  if (a.state_out && so >= 0) {
+    float* dst = a.state_out + so * head_size + ((int64_t)h * kDeltaD + t2) * kDeltaD + col + g;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dst[(j * 8 + (e & 1)) * kDeltaD + (e >> 1) * 8] = S[j][e];
+  }
+}
+
+template <int W>
+static int launch_scan(const ChunkArgs& p, const DeviceFacts& f, cudaStream_t s) {
+  using C = ScanCfg<W>;
+  const DeltaArgs& a = p.a;
+  CUtensorMap tk, tq, tv;
+  int rc = token_map(&tk, a.k, a.T, a.Hk, kDeltaD, a.ldk, 1, kDcTok);
+  if (rc == TB_OK) rc = token_map(&tq, a.q, a.T, a.Hk, kDeltaD, a.ldq, 1, kDcTok);
+  if (rc == TB_OK) rc = token_map(&tv, a.v, a.T, a.Hv, kDeltaD, a.ldv, 1, kDcTok);
+  if (rc == TB_OK) rc = ensure_dynamic_smem(reinterpret_cast<const void*>(delta_scan_kernel<W>), f.device, C::kSmem);
+  if (rc != TB_OK) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.B * a.Hv * (8 / W)));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, delta_scan_kernel<W>, tk, tq, tv, p);
+  if (e != cudaSuccess) {
+    record_cuda_error(e);
+    return TB_ERR_CUDA;
+  }
+  return check_launch();
 }
 
 size_t delta_chunk_workspace(int64_t T, int64_t B, int64_t Hv) {
@@ -791,33 +702,16 @@ int launch_delta_chunks(const DeltaArgs& a, void* workspace, cudaStream_t s) {
   ChunkArgs p;
   p.a = a;
   p.ws = static_cast<uint8_t*>(workspace);
-  CUtensorMap tk, tq;
-  rc = token_map(&tk, a.k, a.T, a.Hk, kDeltaD, a.ldk, 1, kDcTok);
-  if (rc == TB_OK) rc = token_map(&tq, a.q, a.T, a.Hk, kDeltaD, a.ldq, 1, kDcTok);
-  if (rc == TB_OK) rc = ensure_dynamic_smem(reinterpret_cast<const void*>(delta_prep_kernel), f.device, kD1Smem);
-  if (rc == TB_OK) rc = ensure_dynamic_smem(reinterpret_cast<const void*>(delta_scan_kernel), f.device, kD2Smem);
+  rc = ensure_dynamic_smem(reinterpret_cast<const void*>(delta_prep_kernel), f.device, kD1Smem);
   if (rc != TB_OK) return rc;
-  const int64_t prep = (a.T / kDcTok + a.B) * a.Hk, scan = (int64_t)a.B * a.Hv * (kDeltaD / kDcCols);
-  if (prep > INT32_MAX || scan > INT32_MAX) return TB_ERR_TOO_LARGE;
+  const int64_t prep = (a.T / kDcTok + a.B) * a.Hk, heads = (int64_t)a.B * a.Hv;
+  if (prep > INT32_MAX || heads > INT32_MAX / 2) return TB_ERR_TOO_LARGE;
   delta_prep_kernel<<<(unsigned)prep, kD1Threads, kD1Smem, s>>>(p);
   rc = check_launch();
   if (rc != TB_OK) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)scan);
-  cfg.blockDim = dim3(kD2Threads);
-  cfg.dynamicSmemBytes = kD2Smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, delta_scan_kernel, tk, tq, p);
-  if (e != cudaSuccess) {
-    record_cuda_error(e);
-    return TB_ERR_CUDA;
-  }
-  return check_launch();
+  // half heads per CTA while they do not fill the SMs: one warp per SM sub-partition each, where two
+  // would share its tensor core
+  return heads * 2 <= f.sms ? launch_scan<4>(p, f, s) : launch_scan<8>(p, f, s);
 }
 
 }  // namespace tb
