@@ -72,17 +72,16 @@ TB_DEVI ChunkScan chunk_scan(const DeltaArgs& a, int lane) {
   return s;
 }
 
+// (volatile keeps them in order with barriers and waits, which are volatile too and clobber memory)
 TB_DEVI void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 TB_DEVI void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 TB_DEVI void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -353,7 +352,10 @@ constexpr int kD2Q = 2 * kDcBlock, kD2Item = 4 * kDcBlock, kD2V = kD2Item + 2662
 
 template <int W>
 struct ScanCfg {
-  static constexpr int kThreads = (W + 1) * 32;
+  // a warp of its own for the loads, unless that makes a third warp in an SM sub-partition, whose
+  // registers two warps of 255 fill
+  static constexpr bool kLoader = W == 4;
+  static constexpr int kThreads = (W + kLoader) * 32;
   static constexpr int kStage = kD2V + W / 4 * kDcBlock;
   static constexpr int kBytes = 4 * kDcBlock + kDcItem + W / 4 * kDcBlock;  // loaded per chunk
   static constexpr int kSmem = 1024 + kD2Stages * kStage + 128;
@@ -380,9 +382,15 @@ TB_DEVI uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
-// W warps per CTA, 16 columns of v each; warp W loads.
+// Arrival that hands a place back after reads whose values have been used: nothing to release (a release
+// waits for the warp's global stores too, 400 clocks a chunk).
+TB_DEVI void mbar_arrive_reads(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// W warps per CTA, 16 columns of v each.
 template <int W>
-__global__ void __launch_bounds__((W + 1) * 32, 1)
+__global__ void __launch_bounds__(ScanCfg<W>::kThreads, 1)
     delta_scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmV, const ChunkArgs p) {
   using C = ScanCfg<W>;
@@ -423,36 +431,45 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
     }
   };
 
-  if (warp == W) {
-    // the request's first chunk
+  int64_t first = 0;  // the request's first chunk
+  constexpr int kLoads = C::kLoader ? W : 0;  // the warp that loads
+  if (warp == kLoads) {
     const ChunkScan sc = chunk_scan(a, lane);
-    int64_t first = sc.upto - sc.own;
+    first = sc.upto - sc.own;
     const int src = b / sc.per;
     if (lane == src)
       for (int i = lane * sc.per; i < b; ++i) first += chunks_of(a, i);
     first = __shfl_sync(0xffffffffu, first, src);
+  }
+  // a lane per copy
+  constexpr int kCopies = 5 + W / 4;
+  auto load = [&](int c) {
+    const int s = c % kD2Stages, row = (int)t0 + c * kDcTok;
+    const uint32_t sa = base + s * C::kStage, bar = smem_u32(full + s);
+    if (c >= kD2Stages) wait(empty + s, (c / kD2Stages - 1) & 1);
     if (lane == 0) {
-      for (int c = 0; c < nc; ++c) {
-        const int s = c % kD2Stages, row = (int)(t0 + (int64_t)c * kDcTok);
-        uint8_t* st = smem + s * C::kStage;
-        const uint32_t sa = base + s * C::kStage, bar = smem_u32(full + s);
-        if (c >= kD2Stages) wait(empty + s, (c / kD2Stages - 1) & 1);
-        mbar_arrive_expect_tx(full + s, C::kBytes);
-        for (int d = 0; d < 2; ++d) {
-          tma_load_3d<1>(sa + d * kDcBlock, &tmK, d * 64, hk, row, bar);
-          tma_load_3d<1>(sa + kD2Q + d * kDcBlock, &tmQ, d * 64, hk, row, bar);
-        }
-        for (int d = 0; d < W / 4; ++d)
-          tma_load_3d<1>(sa + kD2V + d * kDcBlock, &tmV, (slice * (W / 4) + d) * 64, h, row, bar);
-        if (c == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1's results
-        bulk_g2s(st + kD2Item, p.ws + ((first + c) * a.Hv + h) * (int64_t)kDcItem, kDcItem, full + s);
-      }
-      if (*aborted) {  // a wait gave up: leave the copies in flight time to land before the CTA ends
-        const uint64_t t = globaltimer_ns();
-        while (globaltimer_ns() - t < 1000000) {
-        }
-      }
+      mbar_arrive_expect_tx(full + s, C::kBytes);
+      if (c == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1's results
+      bulk_g2s(smem + s * C::kStage + kD2Item, p.ws + ((first + c) * a.Hv + h) * (int64_t)kDcItem, kDcItem, full + s);
+    } else if (lane < kCopies) {
+      const int d = (lane - 1) & 1;
+      const bool v = lane >= 5;
+      const CUtensorMap* tm = v ? &tmV : (lane >= 3 ? &tmQ : &tmK);
+      const uint32_t dst = sa + (v ? kD2V : (lane >= 3 ? kD2Q : 0)) + d * kDcBlock;
+      tma_load_3d<1>(dst, tm, v ? (slice * (W / 4) + d) * 64 : d * 64, v ? h : hk, row, bar);
     }
+    __syncwarp();
+  };
+  if (warp == kLoads)
+    for (int c = 0; c < (C::kLoader ? nc : kD2Stages - 1) && c < nc; ++c) load(c);
+
+  auto linger = [&]() {  // a wait gave up: leave the copies in flight time to land before the CTA ends
+    const uint64_t t = globaltimer_ns();
+    while (*aborted && globaltimer_ns() - t < 1000000) {
+    }
+  };
+  if (C::kLoader && warp == W) {
+    linger();
     return;
   }
 
@@ -471,6 +488,11 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
       for (int e = 0; e < 4; ++e)
         S[j][e] = have ? __ldg(src + (j * 8 + (e & 1)) * kDeltaD + (e >> 1) * 8) : 0.f;
   }
+  uint32_t sbig[4] = {0, 0, 0, 0};  // the largest |S|, four chains of it
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sbig[e] = max(sbig[e], magnitude(S[j][e]));
   // addresses of the ldmatrix lanes inside a 64 x 64 image: rows by the lane, a 16-byte piece per k
   const uint32_t sw = (uint32_t)lane & 7u;
   const uint32_t row_n = (((uint32_t)lane & 7u) + ((uint32_t)lane >> 4) * 8u) * 128u;  // rows are n
@@ -484,13 +506,8 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
     const uint32_t K = base + s * C::kStage, Q = K + kD2Q, X = K + kD2Item, V = K + kD2V + (warp >> 2) * kDcBlock;
     const float* f = reinterpret_cast<const float*>(smem + s * C::kStage + kD2Item + kDcFactors);
     const int n = (int)(len - (int64_t)c * kDcTok < kDcTok ? len - (int64_t)c * kDcTok : kDcTok);
-    uint32_t big = 0;
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) big = max(big, magnitude(S[j][e]));
     float down_s;
-    const float up_s = operand_scale(__reduce_max_sync(0xffffffffu, big), down_s);
+    const float up_s = operand_scale(__reduce_max_sync(0xffffffffu, max(max(sbig[0], sbig[1]), max(sbig[2], sbig[3]))), down_s);
     wait(full + s, (c / kD2Stages) & 1);
     if (n < kDcTok) {  // the last chunk: rows of K that are another request's, out of the sum over the tokens
       for (int i = tid; i < (kDcTok - n) * 16; i += W * 32) {
@@ -500,159 +517,206 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
       }
       asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
     }
-    // S^T k, S^T q
+    // A warp has its SM sub-partition to itself, so nothing but its own other work fills the latency of a
+    // load or the time of an MMA: loads run a step ahead, and what is not on the way from S to the next
+    // S (the products for o, its output) is spread over the steps that are.
     float R[8][4], O[8][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) R[j][e] = O[j][e] = 0.f;
+    auto at_n = [&](int ks) { return (ks >> 2) * kDcBlock + row_n + (((uint32_t)(ks & 3) * 2u + pc_n) ^ sw) * 16u; };
+    uint32_t bk[4][4], sh[8][4];
+    // S^T k
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ldsm4(K + at_n(0) + j * 2048, bk[j]);
+    uint32_t lo[2][4];
+    auto split_s = [&](int ks, int q) {
+      const float* x = S[2 * ks + (q >> 1)] + (q & 1) * 2;
+      split2(x[0] * up_s, x[1] * up_s, sh[ks][q], lo[ks & 1][q]);
+    };
+#pragma unroll
+    for (int q = 0; q < 4; ++q) split_s(0, q);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float* x = S[2 * ks + (q >> 1)] + (q & 1) * 2;
-        split2(x[0] * up_s, x[1] * up_s, hi[q], lo[q]);
-      }
-      const uint32_t at = (ks >> 2) * kDcBlock + row_n + (((uint32_t)(ks & 3) * 2u + pc_n) ^ sw) * 16u;
-      uint32_t bk[4][4], bq[4][4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) ldsm4(K + at + j * 2048, bk[j]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        mma_16816(R[2 * j], hi, bk[j][0], bk[j][1]);
-        mma_16816(R[2 * j + 1], hi, bk[j][2], bk[j][3]);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) ldsm4(Q + at + j * 2048, bq[j]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        mma_16816(R[2 * j], lo, bk[j][0], bk[j][1]);
-        mma_16816(R[2 * j + 1], lo, bk[j][2], bk[j][3]);
+        mma_16816(R[2 * j], sh[ks], bk[j][0], bk[j][1]);
+        if (ks < 7) split_s(ks + 1, j);
+        mma_16816(R[2 * j + 1], sh[ks], bk[j][2], bk[j][3]);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        mma_16816(O[2 * j], hi, bq[j][0], bq[j][1]);
-        mma_16816(O[2 * j + 1], hi, bq[j][2], bq[j][3]);
+        mma_16816(R[2 * j], lo[ks & 1], bk[j][0], bk[j][1]);
+        mma_16816(R[2 * j + 1], lo[ks & 1], bk[j][2], bk[j][3]);
+        ldsm4((ks < 7 ? K + at_n(ks + 1) : Q + at_n(0)) + j * 2048, bk[j]);
       }
     }
-    // R = v - exp(gamma) S^T k
-    big = 0;
+    if (!C::kLoader && warp == 0 && c + kD2Stages - 1 < nc) load(c + kD2Stages - 1);  // the other warps left that stage a chunk ago
+    // S^T q, and beside it R = v - exp(gamma) S^T k
+    uint32_t big[4] = {0, 0, 0, 0}, vv[4];
+    ldsm4_trans(V + v_row + v_pc, vv);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t vv[4];
-      ldsm4_trans(V + j * 2048 + v_row + v_pc, vv);
+    for (int ks = 0; ks < 8; ++ks) {
+      const int tok = ks * 8 + t2;
+      const float2 cc = *reinterpret_cast<const float2*>(f + tok);
+      auto residual = [&](int q) {  // columns of v g + 8 q
+        const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&vv[(ks & 1) * 2 + q]));
+        float &x = R[ks][q * 2], &y = R[ks][q * 2 + 1];
+        x = tok < n ? fmaf(-cc.x * down_s, x, w.x) : 0.f;
+        y = tok + 1 < n ? fmaf(-cc.y * down_s, y, w.y) : 0.f;
+        big[q * 2] = max(big[q * 2], magnitude(x));
+        big[q * 2 + 1] = max(big[q * 2 + 1], magnitude(y));
+      };
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {  // token tile 2 j + q / 2, columns of v g + 8 (q % 2)
-        const int nt = 2 * j + (q >> 1), tok = nt * 8 + t2, e = (q & 1) * 2;
-        const float2 cc = *reinterpret_cast<const float2*>(f + tok);
-        const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&vv[q]));
-        R[nt][e] = tok < n ? fmaf(-cc.x * down_s, R[nt][e], w.x) : 0.f;
-        R[nt][e + 1] = tok + 1 < n ? fmaf(-cc.y * down_s, R[nt][e + 1], w.y) : 0.f;
-        big = max(big, max(magnitude(R[nt][e]), magnitude(R[nt][e + 1])));
+      for (int j = 0; j < 4; ++j) {
+        mma_16816(O[2 * j], sh[ks], bk[j][0], bk[j][1]);
+        if (j == 1) residual(0);
+        if (j == 2) residual(1);
+        mma_16816(O[2 * j + 1], sh[ks], bk[j][2], bk[j][3]);
+        if (ks < 7) ldsm4(Q + at_n(ks + 1) + j * 2048, bk[j]);
       }
+      if ((ks & 1) && ks < 7) ldsm4_trans(V + (ks / 2 + 1) * 2048 + v_row + v_pc, vv);
     }
     float down_r;
-    const float up_r = operand_scale(__reduce_max_sync(0xffffffffu, big), down_r);
+    const float up_r = operand_scale(__reduce_max_sync(0xffffffffu, max(max(big[0], big[1]), max(big[2], big[3]))), down_r);
     uint32_t rh[4][4], rl[4][4];
+    auto split_r = [&](int ks, int q) {
+      const float* x = R[2 * ks + (q >> 1)] + (q & 1) * 2;
+      split2(x[0] * up_r, x[1] * up_r, rh[ks][q], rl[ks][q]);
+    };
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float* x = R[2 * ks + (q >> 1)] + (q & 1) * 2;
-        split2(x[0] * up_r, x[1] * up_r, rh[ks][q], rl[ks][q]);
-      }
-    // U = T R (rows past a token do not reach it: their tiles are left out), o = q-part + P T R
+    for (int q = 0; q < 4; ++q) split_r(0, q);
+    // U = T R (rows past a token do not reach it: their tiles are left out); o's first part to R's scale
     float U[8][4];
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      const float2 qq = *reinterpret_cast<const float2*>(f + 128 + nt * 8 + t2);
-      const float qx = qq.x * down_s * up_r, qy = qq.y * down_s * up_r;
-      O[nt][0] *= qx;
-      O[nt][1] *= qy;
-      O[nt][2] *= qx;
-      O[nt][3] *= qy;
+    for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) U[nt][e] = 0.f;
-    }
+    auto at_x = [&](int ks, int j) { return X + row_n + (((uint32_t)ks * 2u + pc_n) ^ sw) * 16u + j * 2048; };
+    constexpr int kAt[11][2] = {{0, 0}, {0, 1}, {0, 2}, {0, 3}, {1, 1}, {1, 2}, {1, 3}, {2, 2}, {2, 3}, {3, 3}, {3, 3}};
+    uint32_t th[2][4], tl[2][4];
+    ldsm4(at_x(0, 0), th[0]);
+    ldsm4(at_x(0, 0) + 2 * kDcBlock, tl[0]);
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      const uint32_t at = X + row_n + (((uint32_t)ks * 2u + pc_n) ^ sw) * 16u;
-#pragma unroll
-      for (int j = ks; j < 4; ++j) {
-        uint32_t th[4], tl[4], pt[4];
-        ldsm4(at + j * 2048, th);
-        ldsm4(at + 2 * kDcBlock + j * 2048, tl);
-        ldsm4(at + kDcBlock + j * 2048, pt);
-        mma_16816(U[2 * j], rh[ks], th[0], th[1]);
-        mma_16816(U[2 * j + 1], rh[ks], th[2], th[3]);
-        mma_16816(O[2 * j], rh[ks], pt[0], pt[1]);
-        mma_16816(O[2 * j + 1], rh[ks], pt[2], pt[3]);
-        mma_16816(U[2 * j], rl[ks], th[0], th[1]);
-        mma_16816(U[2 * j + 1], rl[ks], th[2], th[3]);
-        mma_16816(U[2 * j], rh[ks], tl[0], tl[1]);
-        mma_16816(U[2 * j + 1], rh[ks], tl[2], tl[3]);
+    for (int i = 0; i < 10; ++i) {
+      const int ks = kAt[i][0], j = kAt[i][1], x = i & 1;
+      const uint32_t at = at_x(kAt[i + 1][0], kAt[i + 1][1]);
+      if (i < 9) {
+        ldsm4(at, th[x ^ 1]);
+        ldsm4(at + 2 * kDcBlock, tl[x ^ 1]);
+      } else {
+        ldsm4(at_x(0, 0) + kDcBlock, th[x ^ 1]);  // P T's first
       }
+      mma_16816(U[2 * j], rh[ks], th[x][0], th[x][1]);
+      mma_16816(U[2 * j + 1], rh[ks], th[x][2], th[x][3]);
+      // R's later terms, a step or more ahead of their first use
+      if (i < 4) split_r(1, i);
+      if (i >= 4 && i < 6) {
+        split_r(2, (i - 4) * 2);
+        split_r(2, (i - 4) * 2 + 1);
+      }
+      if (i >= 6 && i < 8) {
+        split_r(3, (i - 6) * 2);
+        split_r(3, (i - 6) * 2 + 1);
+      }
+      if (i < 8) {
+        const float2 qq = *reinterpret_cast<const float2*>(f + 128 + i * 8 + t2);
+        const float qx = qq.x * down_s * up_r, qy = qq.y * down_s * up_r;
+        O[i][0] *= qx;
+        O[i][1] *= qy;
+        O[i][2] *= qx;
+        O[i][3] *= qy;
+      }
+      mma_16816(U[2 * j], rl[ks], th[x][0], th[x][1]);
+      mma_16816(U[2 * j + 1], rl[ks], th[x][2], th[x][3]);
+      mma_16816(U[2 * j], rh[ks], tl[x][0], tl[x][1]);
+      mma_16816(U[2 * j + 1], rh[ks], tl[x][2], tl[x][3]);
     }
-    // w U
-    big = 0;
+    // w U, and beside it o += P T R
+    big[0] = big[1] = big[2] = big[3] = 0;
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      const float2 ww = *reinterpret_cast<const float2*>(f + 64 + nt * 8 + t2);
-      const float wx = ww.x * down_r, wy = ww.y * down_r;
-      U[nt][0] *= wx;
-      U[nt][1] *= wy;
-      U[nt][2] *= wx;
-      U[nt][3] *= wy;
+    for (int i = 0; i < 10; ++i) {
+      const int ks = kAt[i][0], j = kAt[i][1], x = i & 1;
+      if (i < 9) ldsm4(at_x(kAt[i + 1][0], kAt[i + 1][1]) + kDcBlock, th[x ^ 1]);
+      mma_16816(O[2 * j], rh[ks], th[x][0], th[x][1]);
+      mma_16816(O[2 * j + 1], rh[ks], th[x][2], th[x][3]);
+      if (i < 8) {
+        const float2 ww = *reinterpret_cast<const float2*>(f + 64 + i * 8 + t2);
+        const float wx = ww.x * down_r, wy = ww.y * down_r;
+        U[i][0] *= wx;
+        U[i][1] *= wy;
+        U[i][2] *= wx;
+        U[i][3] *= wy;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) big = max(big, magnitude(U[nt][e]));
+        for (int e = 0; e < 4; ++e) big[e] = max(big[e], magnitude(U[i][e]));
+      }
     }
     float down_u;
-    const float up_u = operand_scale(__reduce_max_sync(0xffffffffu, big), down_u);
+    const float up_u = operand_scale(__reduce_max_sync(0xffffffffu, max(max(big[0], big[1]), max(big[2], big[3]))), down_u);
+    auto split_u = [&](int ks, int q) {
+      const float* x = U[2 * ks + (q >> 1)] + (q & 1) * 2;
+      split2(x[0] * up_u, x[1] * up_u, rh[ks][q], rl[ks][q]);
+    };
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float* x = U[2 * ks + (q >> 1)] + (q & 1) * 2;
-        split2(x[0] * up_u, x[1] * up_u, rh[ks][q], rl[ks][q]);
-      }
+    for (int q = 0; q < 4; ++q) split_u(0, q);
     // S <- exp(gamma_C) S + K^T (w U); the increment is summed by itself, so that the state's own
-    // rounding is one fp32 fma a chunk
+    // rounding is one fp32 fma a chunk.  Beside it o goes out, back in rows of tokens.
     const float dec = f[192];
+    sbig[0] = sbig[1] = sbig[2] = sbig[3] = 0;
+    auto at_k = [&](int i) {  // step i: 16 columns i / 4 of k, 16 tokens i % 4
+      const int j = i >> 2;
+      return K + (j >> 2) * kDcBlock + row_k + (((uint32_t)(j & 3) * 2u + pc_k) ^ sw) * 16u + (i & 3) * 2048;
+    };
+    __half* dst = a.o + ((t0 + (int64_t)c * kDcTok + g) * a.Hv + h) * kDeltaD + col + t2;
+    const int64_t step = (int64_t)8 * a.Hv * kDeltaD;
+    uint32_t kt[2][4];
+    ldsm4_trans(at_k(0), kt[0]);
+    float dh[2][2][4], dl[2][2][4];  // of two steps: one is summed up while the next one's MMAs run
+    auto add_up = [&](int j, int x) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        S[2 * j + x][e] = fmaf(dec, S[2 * j + x][e], (dh[j & 1][x][e] + dl[j & 1][x][e]) * down_u);
+        sbig[e] = max(sbig[e], magnitude(S[2 * j + x][e]));
+      }
+    };
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float dh[2][4], dl[2][4];
+      const int z = j & 1;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) dh[0][e] = dh[1][e] = dl[0][e] = dl[1][e] = 0.f;
-      const uint32_t at = K + (j >> 2) * kDcBlock + row_k + (((uint32_t)(j & 3) * 2u + pc_k) ^ sw) * 16u;
+      for (int e = 0; e < 4; ++e) dh[z][0][e] = dh[z][1][e] = dl[z][0][e] = dl[z][1][e] = 0.f;
+      uint32_t ox = 0, oy = 0;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        uint32_t bk[4];
-        ldsm4_trans(at + ks * 2048, bk);
-        mma_16816(dh[0], rh[ks], bk[0], bk[1]);
-        mma_16816(dh[1], rh[ks], bk[2], bk[3]);
-        mma_16816(dl[0], rl[ks], bk[0], bk[1]);
-        mma_16816(dl[1], rl[ks], bk[2], bk[3]);
+        const int i = j * 4 + ks, x = i & 1;
+        if (i < 31) ldsm4_trans(at_k(i + 1), kt[x ^ 1]);
+        mma_16816(dh[z][0], rh[ks], kt[x][0], kt[x][1]);
+        if (j == 0 && ks < 3) {
+          split_u(ks + 1, 0);
+          split_u(ks + 1, 1);
+        }
+        if (j > 0 && ks == 1) add_up(j - 1, 0);
+        mma_16816(dh[z][1], rh[ks], kt[x][2], kt[x][3]);
+        if (j == 0 && ks < 3) {
+          split_u(ks + 1, 2);
+          split_u(ks + 1, 3);
+        }
+        if (j > 0 && ks == 2) add_up(j - 1, 1);
+        mma_16816(dl[z][0], rl[ks], kt[x][0], kt[x][1]);
+        if (ks == 0) ox = transpose8x8(pack_half2(O[j][0] * down_r, O[j][1] * down_r));
+        if (ks == 1) oy = transpose8x8(pack_half2(O[j][2] * down_r, O[j][3] * down_r));
+        mma_16816(dl[z][1], rl[ks], kt[x][2], kt[x][3]);
       }
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[2 * j + x][e] = fmaf(dec, S[2 * j + x][e], (dh[x][e] + dl[x][e]) * down_u);
+      if (j * 8 + g < n) {
+        *reinterpret_cast<uint32_t*>(dst) = ox;
+        *reinterpret_cast<uint32_t*>(dst + 8) = oy;
+      }
+      dst += step;
     }
+    add_up(7, 0);
+    add_up(7, 1);
     __syncwarp();
-    if (lane == 0) mbar_arrive(empty + s);
-    // o: back to rows of tokens
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      const uint32_t x = transpose8x8(pack_half2(O[nt][0] * down_r, O[nt][1] * down_r));
-      const uint32_t y = transpose8x8(pack_half2(O[nt][2] * down_r, O[nt][3] * down_r));
-      const int tok = nt * 8 + g;
-      if (tok < n) {
-        __half* dst = a.o + ((t0 + (int64_t)c * kDcTok + tok) * a.Hv + h) * kDeltaD + col + t2;
-        *reinterpret_cast<uint32_t*>(dst) = x;
-        *reinterpret_cast<uint32_t*>(dst + 8) = y;
-      }
-    }
+    if (lane == 0) mbar_arrive_reads(empty + s);
   }
   if (a.state_out && so >= 0) {
     float* dst = a.state_out + so * head_size + ((int64_t)h * kDeltaD + t2) * kDeltaD + col + g;
@@ -661,6 +725,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) dst[(j * 8 + (e & 1)) * kDeltaD + (e >> 1) * 8] = S[j][e];
   }
+  if (!C::kLoader && warp == 0) linger();
 }
 
 template <int W>
