@@ -90,20 +90,37 @@ TB_DEVI void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// ---------------------------------------------------------------- kernel 1
-constexpr int kD1Threads = 256;
-constexpr int kD1Pitch = 136;   // halves per row of K and Q in shared memory
-constexpr int kD1Dots = 65;     // floats per row of K K^T and Q K^T
-constexpr int kD1At = 68;       // floats per row of A^T
-constexpr int kD1Region = 64 * kD1At * 4;  // 17408 bytes: K, or Q, or one head's A^T, or its T
-constexpr int kD1Smem = 4 * kD1Region + 2 * 64 * kD1Dots * 4;
+// x, y -> fp16 pair and the fp16 pair of what it leaves
+TB_DEVI void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack_half2(x - f.x, y - f.y);
+}
+TB_DEVI uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
 
-__global__ void __launch_bounds__(kD1Threads, 2) delta_prep_kernel(const ChunkArgs p) {
+// ---------------------------------------------------------------- kernel 1
+constexpr int kD1Threads = 128;
+constexpr int kD1Pitch = 136;               // halves per row of K and Q in shared memory
+constexpr int kD1KQ = 64 * kD1Pitch * 2;    // bytes of one of them
+static_assert(2 * kD1KQ >= 4 * kDcBlock, "two heads' images take the place of K and Q");
+
+// Warp w has rows 16 w .. of the chunk's matrices, as accumulator tiles of 8 columns.  (I + A)^-1 block by
+// block of 16: the diagonal blocks D_w by substitution (a lane per column), then with E = D A (left of
+// the diagonal) T_w = D_w diag(beta) - sum_{s < w} E_ws T_s, one block row a step, fp32 factors in two
+// fp16 terms (three products).  P T goes along, P from Q K^T's accumulators as they are.
+__global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkArgs p) {
   const DeltaArgs& a = p.a;
-  extern __shared__ __align__(16) uint8_t d1_smem[];
+  __shared__ __align__(1024) uint8_t kq[2 * kD1KQ];
   __shared__ float rk[64], rq[64];
-  __shared__ float2 gam[4][64];  // running sums of the decays, high and low part
+  __shared__ float2 gam[4][64];  // running sums of the decays in log2 units, high and low part
   __shared__ float bet[4][64];
+  __shared__ __align__(16) float diag_t[4][16][20];  // a warp's diagonal block of A, transposed
+  __shared__ float diag[4][16][17];                  // its inverse
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -130,219 +147,277 @@ __global__ void __launch_bounds__(kD1Threads, 2) delta_prep_kernel(const ChunkAr
   t0 += c * kDcTok;
   const int n = (int)(len - c * kDcTok < kDcTok ? len - c * kDcTok : kDcTok);
 
-  // K and Q: four threads a row, 32 elements each; rows past the request's end are zeros
-  __half* Ks = reinterpret_cast<__half*>(d1_smem);
-  __half* Qs = reinterpret_cast<__half*>(d1_smem + kD1Region);
+  // K and Q: a thread has half a row of each; rows past the request's end are zeros
+  __half* Ks = reinterpret_cast<__half*>(kq);
+  __half* Qs = reinterpret_cast<__half*>(kq + kD1KQ);
   {
-    const int row = tid >> 2, part = (tid & 3) * 32;
-    float sk = 0.f, sq = 0.f;
+    const int part = (tid & 15) * 8;
+    float sk[8], sq[8];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const __half* g = (m ? a.q + (t0 + row) * a.ldq : a.k + (t0 + row) * a.ldk) + hk * kDeltaD + part;
-      __half* d = (m ? Qs : Ks) + row * kD1Pitch + part;
-      float& s = m ? sq : sk;
+    for (int r = 0; r < 8; ++r) {  // eight rows at a time, sixteen threads a row
+      const int row = r * 8 + (tid >> 4);
+      uint4 wk = make_uint4(0, 0, 0, 0), wq = wk;
+      if (row < n) {
+        wk = __ldg(reinterpret_cast<const uint4*>(a.k + (t0 + row) * a.ldk + hk * kDeltaD + part));
+        wq = __ldg(reinterpret_cast<const uint4*>(a.q + (t0 + row) * a.ldq + hk * kDeltaD + part));
+      }
+      *reinterpret_cast<uint4*>(Ks + row * kD1Pitch + part) = wk;
+      *reinterpret_cast<uint4*>(Qs + row * kD1Pitch + part) = wq;
+      sk[r] = sq[r] = 0.f;
+      const __half2 *hk2 = reinterpret_cast<const __half2*>(&wk), *hq2 = reinterpret_cast<const __half2*>(&wq);
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (row < n) w = __ldg(reinterpret_cast<const uint4*>(g + e));
-        *reinterpret_cast<uint4*>(d + e) = w;
-        const __half2* h = reinterpret_cast<const __half2*>(&w);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float2 f = __half22float2(h[x]);
-          s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
-        }
+      for (int x = 0; x < 4; ++x) {
+        const float2 f = __half22float2(hk2[x]), g = __half22float2(hq2[x]);
+        sk[r] = fmaf(f.x, f.x, fmaf(f.y, f.y, sk[r]));
+        sq[r] = fmaf(g.x, g.x, fmaf(g.y, g.y, sq[r]));
       }
     }
 #pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      sk += __shfl_xor_sync(0xffffffffu, sk, d);
-      sq += __shfl_xor_sync(0xffffffffu, sq, d);
-    }
-    if ((tid & 3) == 0) {
-      rk[row] = a.normalise ? 1.f / sqrtf(sk + kDeltaEps) : 1.f;
-      rq[row] = (a.normalise ? 1.f / sqrtf(sq + kDeltaEps) : 1.f) * a.scale;
+    for (int r = 0; r < 8; ++r) {
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) {
+        sk[r] += __shfl_xor_sync(0xffffffffu, sk[r], d);
+        sq[r] += __shfl_xor_sync(0xffffffffu, sq[r], d);
+      }
+      if ((tid & 15) == 0) {
+        const int row = r * 8 + (tid >> 4);
+        rk[row] = a.normalise ? 1.f / sqrtf(sk[r] + kDeltaEps) : 1.f;
+        rq[row] = (a.normalise ? 1.f / sqrtf(sq[r] + kDeltaEps) : 1.f) * a.scale;
+      }
     }
   }
   __syncthreads();
 
-  // K K^T (warps 0-3) and Q K^T (4-7), 16 rows a warp, the lower triangle's tiles
-  float* dots = reinterpret_cast<float*>(d1_smem + 4 * kD1Region);
-  float* qdots = dots + 64 * kD1Dots;
+  // K K^T and Q K^T, tiles up to the diagonal
+  float G[8][4], QK[8][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) G[j][e] = QK[j][e] = 0.f;
+#pragma unroll 2
+  for (int k = 0; k < kDeltaD; k += 16) {
+    uint32_t ak[4], aq[4];
+    const int at = (warp * 16 + (lane & 15)) * kD1Pitch + k + (lane >> 4) * 8;
+    ldsm4(smem_u32(Ks + at), ak);
+    ldsm4(smem_u32(Qs + at), aq);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j > warp) break;
+      uint32_t bf[4];  // keys j*16 + 0..7 (k, k+8), then 8..15
+      ldsm4(smem_u32(Ks + (j * 16 + (lane & 7) + (lane >> 4) * 8) * kD1Pitch + k + ((lane >> 3) & 1) * 8), bf);
+      mma_16816(G[2 * j], ak, bf[0], bf[1]);
+      mma_16816(G[2 * j + 1], ak, bf[2], bf[3]);
+      mma_16816(QK[2 * j], aq, bf[0], bf[1]);
+      mma_16816(QK[2 * j + 1], aq, bf[2], bf[3]);
+    }
+  }
+  const int g = lane >> 2, t2 = (lane & 3) * 2, i0 = warp * 16 + g;
+  // every value head weighs them by the keys' and queries' norms
   {
-    const int r0 = (warp & 3) * 16;
-    const __half* A = warp < 4 ? Ks : Qs;
-    float acc[8][4];
+    const float k0 = rk[i0], k1 = rk[i0 + 8], f0 = rq[i0], f1 = rq[i0 + 8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = rk[j * 8 + t2], y = rk[j * 8 + t2 + 1];
+      G[j][0] *= k0 * x;
+      G[j][1] *= k0 * y;
+      G[j][2] *= k1 * x;
+      G[j][3] *= k1 * y;
+      QK[j][0] *= f0 * x;
+      QK[j][1] *= f0 * y;
+      QK[j][2] *= f1 * x;
+      QK[j][3] *= f1 * y;
+    }
+  }
+
+  const int group = a.Hv / a.Hk;
+  for (int h4 = 0; h4 < group; ++h4) {
+    const int slot = h4 & 3, h = hk * group + h4;
+    if (slot == 0) {
+      __syncthreads();  // K and Q, and the last four heads' sums, have been read
+      if (h4 + warp < group) {  // a warp per head: the decays' sums in double (differences of large sums)
+        double x[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = lane * 2 + e;
+          float gv = i < n ? __ldg(a.g + (t0 + i) * a.Hv + h + warp) : 0.f;
+          if (gv < -200.f) gv = -200.f;  // e^-200 is 0 in fp32 already
+          x[e] = (double)gv * 1.4426950408889634;
+          bet[warp][i] = i < n ? __ldg(a.beta + (t0 + i) * a.Hv + h + warp) : 0.f;
+        }
+        double s = x[0] + x[1];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const double y = __shfl_up_sync(0xffffffffu, s, d);
+          if (lane >= d) s += y;
+        }
+        const double s0 = s - x[1];
+        gam[warp][lane * 2] = make_float2((float)s0, (float)(s0 - (double)(float)s0));
+        gam[warp][lane * 2 + 1] = make_float2((float)s, (float)(s - (double)(float)s));
+      }
+      __syncthreads();
+    }
+    uint8_t* item = p.ws + (chunk * a.Hv + h) * (int64_t)kDcItem;
+    uint8_t* img = kq + (h4 & 1) * 2 * kDcBlock;  // T's high part, then its low part
+    const float2* gm = gam[slot];
+    const float* be = bet[slot];
+    if (tid < 64) {
+      float* f = reinterpret_cast<float*>(item + kDcFactors);
+      const float2 mine = gm[tid], last = gm[63];
+      const float eg = ex2(mine.x) * (1.f + 0.6931472f * mine.y);
+      f[tid] = eg * rk[tid];
+      f[64 + tid] = ex2((last.x - mine.x) + (last.y - mine.y)) * rk[tid];
+      f[128 + tid] = eg * rq[tid];
+      if (tid == 0) f[192] = ex2(last.x) * (1.f + 0.6931472f * last.y);
+    }
+    // A (fp32, as accumulator tiles), P (fp16, as the left factor's tiles)
+    float A[8][4];
+    uint32_t P[4][4];
+    {
+      const float2 g0 = gm[i0], g1 = gm[i0 + 8];
+      const float b0 = be[i0], b1 = be[i0 + 8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j > 2 * warp + 1) {
+          if ((j & 1) == 0) P[j >> 1][0] = P[j >> 1][1] = P[j >> 1][2] = P[j >> 1][3] = 0;
+          continue;
+        }
+        float pv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = j * 8 + t2 + (e & 1), i = i0 + (e >> 1) * 8;
+          const float2 gk = gm[k], gi = (e >> 1) ? g1 : g0;
+          const float d = k <= i ? ex2((gi.x - gk.x) + (gi.y - gk.y)) : 0.f;
+          A[j][e] = k < i ? ((e >> 1) ? b1 : b0) * G[j][e] * d : 0.f;
+          pv[e] = k <= i ? QK[j][e] * d : 0.f;
+        }
+        P[j >> 1][(j & 1) * 2] = pack_half2(pv[0], pv[1]);
+        P[j >> 1][(j & 1) * 2 + 1] = pack_half2(pv[2], pv[3]);
+      }
+    }
+    // the diagonal block's inverse
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {  // (the block's registers by a constant index)
+      if (w != warp) continue;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) diag_t[warp][x * 8 + t2 + (e & 1)][g + (e >> 1) * 8] = A[2 * w + x][e];
+    }
+    __syncwarp();
+    if (lane < 16) {
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = i == lane ? 1.f : 0.f;
+#pragma unroll
+      for (int k = 0; k < 15; ++k) {
+#pragma unroll
+        for (int q = (k + 1) / 4; q < 4; ++q) {
+          const float4 w = *reinterpret_cast<const float4*>(&diag_t[warp][k][q * 4]);
+          if (q * 4 > k) x[q * 4] = fmaf(-w.x, x[k], x[q * 4]);
+          if (q * 4 + 1 > k) x[q * 4 + 1] = fmaf(-w.y, x[k], x[q * 4 + 1]);
+          if (q * 4 + 2 > k) x[q * 4 + 2] = fmaf(-w.z, x[k], x[q * 4 + 2]);
+          x[q * 4 + 3] = fmaf(-w.w, x[k], x[q * 4 + 3]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) diag[warp][i][lane] = x[i];
+    }
+    __syncwarp();
+    // E = D A, negated, left of the diagonal block
+    uint32_t eh[3][4], el[3][4];
+    float T[8][4];
+    {
+      uint32_t dh[4], dl[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float* d = &diag[warp][g + (q & 1) * 8][t2 + (q >> 1) * 8];
+        split2(-d[0], -d[1], dh[q], dl[q]);
+      }
+#pragma unroll
+      for (int j = 0; j < 6; ++j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) T[j][e] = 0.f;
+        if (j >= 2 * warp) continue;
+        uint32_t h0, h1, l0, l1;
+        split2(A[j][0], A[j][1], h0, l0);
+        split2(A[j][2], A[j][3], h1, l1);
+        h0 = transpose8x8(h0);
+        h1 = transpose8x8(h1);
+        l0 = transpose8x8(l0);
+        l1 = transpose8x8(l1);
+        mma_16816(T[j], dh, h0, h1);
+        mma_16816(T[j], dh, l0, l1);
+        mma_16816(T[j], dl, h0, h1);
+      }
+#pragma unroll
+      for (int s = 0; s < 3; ++s)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float* x = T[2 * s + (q >> 1)] + (q & 1) * 2;
+          split2(x[0], x[1], eh[s][q], el[s][q]);
+        }
+    }
+    // T's rows start from D diag(beta)
+    float PT[8][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-    for (int k = 0; k < kDeltaD; k += 16) {
-      uint32_t af[4];
-      ldsm4(smem_u32(A + (r0 + (lane & 15)) * kD1Pitch + k + (lane >> 4) * 8), af);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j * 16 > r0) break;
-        uint32_t bf[4];  // keys j*16 + 0..7 (k, k+8), then 8..15
-        ldsm4(smem_u32(Ks + (j * 16 + (lane & 7) + (lane >> 4) * 8) * kD1Pitch + k + ((lane >> 3) & 1) * 8), bf);
-        mma_16816(acc[2 * j], af, bf[0], bf[1]);
-        mma_16816(acc[2 * j + 1], af, bf[2], bf[3]);
+      for (int e = 0; e < 4; ++e) {
+        T[j][e] = PT[j][e] = 0.f;
+        if (j >> 1 == warp) T[j][e] = diag[warp][g + (e >> 1) * 8][(j & 1) * 8 + t2 + (e & 1)] * be[j * 8 + t2 + (e & 1)];
       }
-    }
-    float* out = warp < 4 ? dots : qdots;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j * 8 > r0 + 15) break;
+    for (int s = 0; s < 4; ++s) {
+      if (warp == s) {  // this block row is complete
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        out[(r0 + (lane >> 2) + (e >> 1) * 8) * kD1Dots + j * 8 + (lane & 3) * 2 + (e & 1)] = acc[j][e];
-    }
-  }
-  __syncthreads();
-
-  // the value heads of this key head, four at a time, a pair of warps each
-  const int group = a.Hv / a.Hk, pair = warp >> 1, l64 = tid & 63;
-  float* At = reinterpret_cast<float*>(d1_smem + pair * kD1Region);
-  auto sync_pair = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory"); };
-  for (int h0 = 0; h0 < group; h0 += 4) {
-    if (h0 + pair >= group) continue;
-    const int h = hk * group + h0 + pair;
-    if ((warp & 1) == 0) {  // the decays' sums in double: differences of large sums stay exact enough
-      double x[2];
+        for (int j = 0; j < 2 * s + 2; ++j)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = lane * 2 + e;
-        float g = i < n ? __ldg(a.g + (t0 + i) * a.Hv + h) : 0.f;
-        if (g < -200.f) g = -200.f;  // e^-200 is 0 in fp32 already
-        x[e] = g;
-        bet[pair][i] = i < n ? __ldg(a.beta + (t0 + i) * a.Hv + h) : 0.f;
+          for (int e = 0; e < 2; ++e) {
+            uint32_t hi, lo;
+            split2(T[j][2 * e], T[j][2 * e + 1], hi, lo);
+            const int i = i0 + e * 8, at = i * 128 + ((j ^ (i & 7)) << 4) + t2 * 2;
+            *reinterpret_cast<uint32_t*>(img + at) = hi;
+            *reinterpret_cast<uint32_t*>(img + kDcBlock + at) = lo;
+          }
       }
-      double s = x[0] + x[1];
+      __syncthreads();
+      if (warp < s) continue;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, s, d);
-        if (lane >= d) s += y;
-      }
-      const double s0 = s - x[1];
-      gam[pair][lane * 2] = make_float2((float)s0, (float)(s0 - (double)(float)s0));
-      gam[pair][lane * 2 + 1] = make_float2((float)s, (float)(s - (double)(float)s));
-    }
-    sync_pair();
-    uint8_t* item = p.ws + (chunk * a.Hv + h) * (int64_t)kDcItem;
-    const float2 mine = gam[pair][l64], last = gam[pair][63];
-    {
-      float* f = reinterpret_cast<float*>(item + kDcFactors);
-      const float eg = expf(mine.x) * (1.f + mine.y);
-      f[l64] = eg * rk[l64];
-      f[64 + l64] = expf((last.x - mine.x) + (last.y - mine.y)) * rk[l64];
-      f[128 + l64] = eg * rq[l64];
-      if (l64 == 0) f[192] = expf(last.x) * (1.f + last.y);
-    }
-    // A^T: thread = row i of A
-    {
-      const float bi = bet[pair][l64] * rk[l64];
-      for (int k = 0; k < 63; ++k) {
-        const float2 gk = gam[pair][k];
-        const float d = expf((mine.x - gk.x) + (mine.y - gk.y));
-        At[k * kD1At + l64] = l64 > k ? bi * rk[k] * dots[l64 * kD1Dots + k] * d : 0.f;
-      }
-    }
-    sync_pair();
-    // column l64 of (I + A)^-1 by substitution; the upper half's warp starts at its first column
-    float x[64];
-#pragma unroll
-    for (int i = 0; i < 64; ++i) x[i] = i == l64 ? 1.f : 0.f;
-    if ((warp & 1) == 0) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-#pragma unroll
-        for (int i4 = (k + 1) / 4; i4 < 16; ++i4) {
-          const float4 w = *reinterpret_cast<const float4*>(At + k * kD1At + i4 * 4);
-          if (i4 * 4 > k) x[i4 * 4] = fmaf(-w.x, x[k], x[i4 * 4]);
-          if (i4 * 4 + 1 > k) x[i4 * 4 + 1] = fmaf(-w.y, x[k], x[i4 * 4 + 1]);
-          if (i4 * 4 + 2 > k) x[i4 * 4 + 2] = fmaf(-w.z, x[k], x[i4 * 4 + 2]);
-          x[i4 * 4 + 3] = fmaf(-w.w, x[k], x[i4 * 4 + 3]);
+      for (int j = 0; j <= s; ++j) {
+        uint32_t th[4], tl[4];
+        const uint32_t at = smem_u32(img) + (s * 16 + (lane & 15)) * 128 + (((j * 2 + (lane >> 4)) ^ (lane & 7)) << 4);
+        ldsm4_trans(at, th);
+        mma_16816(PT[2 * j], P[s], th[0], th[1]);
+        mma_16816(PT[2 * j + 1], P[s], th[2], th[3]);
+        if (s < 3 && warp > s) {
+          ldsm4_trans(at + kDcBlock, tl);
+          mma_16816(T[2 * j], eh[s < 3 ? s : 0], th[0], th[1]);
+          mma_16816(T[2 * j + 1], eh[s < 3 ? s : 0], th[2], th[3]);
+          mma_16816(T[2 * j], eh[s < 3 ? s : 0], tl[0], tl[1]);
+          mma_16816(T[2 * j + 1], eh[s < 3 ? s : 0], tl[2], tl[3]);
+          mma_16816(T[2 * j], el[s < 3 ? s : 0], th[0], th[1]);
+          mma_16816(T[2 * j + 1], el[s < 3 ? s : 0], th[2], th[3]);
         }
       }
     }
+    // out: T's image as it lies in shared memory, P T from the registers; the blocks above the diagonal
+    // are never read
 #pragma unroll
-    for (int k = 32; k < 63; ++k) {
-#pragma unroll
-      for (int i4 = (k + 1) / 4; i4 < 16; ++i4) {
-        const float4 w = *reinterpret_cast<const float4*>(At + k * kD1At + i4 * 4);
-        if (i4 * 4 > k) x[i4 * 4] = fmaf(-w.x, x[k], x[i4 * 4]);
-        if (i4 * 4 + 1 > k) x[i4 * 4 + 1] = fmaf(-w.y, x[k], x[i4 * 4 + 1]);
-        if (i4 * 4 + 2 > k) x[i4 * 4 + 2] = fmaf(-w.z, x[k], x[i4 * 4 + 2]);
-        x[i4 * 4 + 3] = fmaf(-w.w, x[k], x[i4 * 4 + 3]);
-      }
-    }
-    sync_pair();  // A^T has been read: its room takes T's image (high part, then low)
-    uint8_t* img = d1_smem + pair * kD1Region;
-    {
-      const float bj = bet[pair][l64];
-#pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        const float v = x[i] * bj;
-        const __half hi = __float2half_rn(v);
-        const int at = i * 128 + (((l64 >> 3) ^ (i & 7)) << 4) + (l64 & 7) * 2;
-        *reinterpret_cast<__half*>(img + at) = hi;
-        *reinterpret_cast<__half*>(img + kDcBlock + at) = __float2half_rn(v - __half2float(hi));
-      }
-    }
-    sync_pair();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int o = (e * 64 + l64) * 16;
+    for (int e = 0; e < 4; ++e) {
+      const int o = (e * kD1Threads + tid) * 16;
       *reinterpret_cast<uint4*>(item + o) = *reinterpret_cast<const uint4*>(img + o);
       *reinterpret_cast<uint4*>(item + 2 * kDcBlock + o) = *reinterpret_cast<const uint4*>(img + kDcBlock + o);
     }
-    // P T: 32 rows a warp, P made from Q K^T as the A fragments
-#pragma unroll 1
-    for (int m = 0; m < 2; ++m) {
-      const int r0 = (warp & 1) * 16 + m * 32;  // the pair's warps share the longer rows
-      float acc[8][4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 8; ++j) {
+      if (j > 2 * warp + 1) break;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-      const int i0 = r0 + (lane >> 2);
-      const float2 g0 = gam[pair][i0], g1 = gam[pair][i0 + 8];
-      const float f0 = rq[i0], f1 = rq[i0 + 8];
-      for (int k = 0; k <= r0; k += 16) {
-        uint32_t af[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {  // rows i0, i0 + 8; columns k + 2 (lane % 4) (+ 8)
-          const int i = i0 + (q & 1) * 8, j = k + (lane & 3) * 2 + (q >> 1) * 8;
-          const float2 gi = (q & 1) ? g1 : g0;
-          float v[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 gj = gam[pair][j + e];
-            v[e] = j + e <= i ? qdots[i * kD1Dots + j + e] * ((q & 1) ? f1 : f0) * rk[j + e] *
-                                    expf((gi.x - gj.x) + (gi.y - gj.y))
-                              : 0.f;
-          }
-          af[q] = pack_half2(v[0], v[1]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int kr = k + (lane & 15), ch = j * 2 + (lane >> 4);
-          uint32_t bf[4];  // columns j*16 + 0..7 (k, k+8), then 8..15
-          ldsm4_trans(smem_u32(img + kr * 128 + ((ch ^ (kr & 7)) << 4)), bf);
-          mma_16816(acc[2 * j], af, bf[0], bf[1]);
-          mma_16816(acc[2 * j + 1], af, bf[2], bf[3]);
-        }
+      for (int e = 0; e < 2; ++e) {
+        const int i = i0 + e * 8;
+        *reinterpret_cast<uint32_t*>(item + kDcBlock + i * 128 + ((j ^ (i & 7)) << 4) + t2 * 2) =
+            pack_half2(PT[j][2 * e], PT[j][2 * e + 1]);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int i = i0 + e * 8;
-          *reinterpret_cast<uint32_t*>(item + kDcBlock + i * 128 + ((j ^ (i & 7)) << 4) + (lane & 3) * 4) =
-              pack_half2(acc[j][2 * e], acc[j][2 * e + 1]);
-        }
     }
-    sync_pair();  // the image has been read before the next head's A^T takes its place
   }
 }
 
@@ -369,19 +444,6 @@ TB_DEVI float operand_scale(uint32_t bits, float& inverse) {
   return __int_as_float(e << 23);
 }
 TB_DEVI uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }  // orders as the values do, NaN last
-// x, y -> fp16 pair and the fp16 pair of what it leaves
-TB_DEVI void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x, y);
-  const float2 f = __half22float2(h);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = pack_half2(x - f.x, y - f.y);
-}
-TB_DEVI uint32_t transpose8x8(uint32_t a) {
-  uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-  return d;
-}
-
 // Arrival that hands a place back after reads whose values have been used: nothing to release (a release
 // waits for the warp's global stores too, 400 clocks a chunk).
 TB_DEVI void mbar_arrive_reads(uint64_t* bar) {
@@ -767,11 +829,9 @@ int launch_delta_chunks(const DeltaArgs& a, void* workspace, cudaStream_t s) {
   ChunkArgs p;
   p.a = a;
   p.ws = static_cast<uint8_t*>(workspace);
-  rc = ensure_dynamic_smem(reinterpret_cast<const void*>(delta_prep_kernel), f.device, kD1Smem);
-  if (rc != TB_OK) return rc;
   const int64_t prep = (a.T / kDcTok + a.B) * a.Hk, heads = (int64_t)a.B * a.Hv;
   if (prep > INT32_MAX || heads > INT32_MAX / 2) return TB_ERR_TOO_LARGE;
-  delta_prep_kernel<<<(unsigned)prep, kD1Threads, kD1Smem, s>>>(p);
+  delta_prep_kernel<<<(unsigned)prep, kD1Threads, 0, s>>>(p);
   rc = check_launch();
   if (rc != TB_OK) return rc;
   // half heads per CTA while they do not fill the SMs: one warp per SM sub-partition each, where two
