@@ -103,6 +103,15 @@ TB_DEVI uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
+// (hi, lo) += (x, y): a sum of fp32 pairs, hi the rounded sum and lo what it leaves (Knuth's two-sum)
+TB_DEVI void add_pair(float& hi, float& lo, float x, float y) {
+  const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
+  const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b));
+  const float t = __fadd_rn(__fadd_rn(lo, y), e);
+  hi = __fadd_rn(s, t);
+  lo = __fsub_rn(t, __fsub_rn(hi, s));
+}
+
 // ---------------------------------------------------------------- kernel 1
 constexpr int kD1Threads = 128;
 constexpr int kD1Pitch = 136;               // halves per row of K and Q in shared memory
@@ -147,44 +156,59 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
   t0 += c * kDcTok;
   const int n = (int)(len - c * kDcTok < kDcTok ? len - c * kDcTok : kDcTok);
 
-  // K and Q: a thread has half a row of each; rows past the request's end are zeros
+  // the decays and steps of the head that this warp sums up next, two tokens a lane
+  const int group = a.Hv / a.Hk;
+  float next_g[2] = {0.f, 0.f}, next_b[2] = {0.f, 0.f};
+  auto fetch_decays = [&](int h4) {
+    if (h4 + warp >= group) return;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t at = (t0 + lane * 2 + e) * a.Hv + hk * group + h4 + warp;
+      const bool in = lane * 2 + e < n;
+      next_g[e] = in ? __ldg(a.g + at) : 0.f;
+      next_b[e] = in ? __ldg(a.beta + at) : 0.f;
+    }
+  };
+  fetch_decays(0);
+
+  // K and Q; rows past the request's end are zeros
   __half* Ks = reinterpret_cast<__half*>(kq);
   __half* Qs = reinterpret_cast<__half*>(kq + kD1KQ);
   {
     const int part = (tid & 15) * 8;
-    float sk[8], sq[8];
+    uint4 w[16];  // eight rows of K, then of Q, sixteen threads a row
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {  // eight rows at a time, sixteen threads a row
-      const int row = r * 8 + (tid >> 4);
-      uint4 wk = make_uint4(0, 0, 0, 0), wq = wk;
-      if (row < n) {
-        wk = __ldg(reinterpret_cast<const uint4*>(a.k + (t0 + row) * a.ldk + hk * kDeltaD + part));
-        wq = __ldg(reinterpret_cast<const uint4*>(a.q + (t0 + row) * a.ldq + hk * kDeltaD + part));
-      }
-      *reinterpret_cast<uint4*>(Ks + row * kD1Pitch + part) = wk;
-      *reinterpret_cast<uint4*>(Qs + row * kD1Pitch + part) = wq;
-      sk[r] = sq[r] = 0.f;
-      const __half2 *hk2 = reinterpret_cast<const __half2*>(&wk), *hq2 = reinterpret_cast<const __half2*>(&wq);
+    for (int r = 0; r < 16; ++r) {
+      const int row = (r & 7) * 8 + (tid >> 4);
+      const __half* src = r < 8 ? a.k + (t0 + row) * a.ldk : a.q + (t0 + row) * a.ldq;
+      w[r] = row < n ? __ldg(reinterpret_cast<const uint4*>(src + hk * kDeltaD + part)) : make_uint4(0, 0, 0, 0);
+    }
+    float v[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      *reinterpret_cast<uint4*>((r < 8 ? Ks : Qs) + ((r & 7) * 8 + (tid >> 4)) * kD1Pitch + part) = w[r];
+      const __half2* h2 = reinterpret_cast<const __half2*>(&w[r]);
+      v[r] = 0.f;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const float2 f = __half22float2(hk2[x]), g = __half22float2(hq2[x]);
-        sk[r] = fmaf(f.x, f.x, fmaf(f.y, f.y, sk[r]));
-        sq[r] = fmaf(g.x, g.x, fmaf(g.y, g.y, sq[r]));
+        const float2 f = __half22float2(h2[x]);
+        v[r] = fmaf(f.x, f.x, fmaf(f.y, f.y, v[r]));
       }
     }
+    // the sixteen sums over sixteen lanes: each step halves the sums a lane carries; lane l ends with sum l
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
+    for (int d = 8; d; d >>= 1) {
+      const bool up = lane & d;
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) {
-        sk[r] += __shfl_xor_sync(0xffffffffu, sk[r], d);
-        sq[r] += __shfl_xor_sync(0xffffffffu, sq[r], d);
-      }
-      if ((tid & 15) == 0) {
-        const int row = r * 8 + (tid >> 4);
-        rk[row] = a.normalise ? 1.f / sqrtf(sk[r] + kDeltaEps) : 1.f;
-        rq[row] = (a.normalise ? 1.f / sqrtf(sq[r] + kDeltaEps) : 1.f) * a.scale;
+      for (int r = 0; r < d; ++r) {
+        const float keep = up ? v[r + d] : v[r], give = up ? v[r] : v[r + d];
+        v[r] = keep + __shfl_xor_sync(0xffffffffu, give, d);
       }
     }
+    const int r = lane & 15, row = (r & 7) * 8 + (tid >> 4);
+    const float inv = a.normalise ? 1.f / sqrtf(v[0] + kDeltaEps) : 1.f;
+    if (r < 8) rk[row] = inv;
+    else rq[row] = inv * a.scale;
   }
   __syncthreads();
 
@@ -229,31 +253,33 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
     }
   }
 
-  const int group = a.Hv / a.Hk;
   for (int h4 = 0; h4 < group; ++h4) {
     const int slot = h4 & 3, h = hk * group + h4;
     if (slot == 0) {
       __syncthreads();  // K and Q, and the last four heads' sums, have been read
-      if (h4 + warp < group) {  // a warp per head: the decays' sums in double (differences of large sums)
-        double x[2];
+      if (h4 + warp < group) {  // a warp per head: the decays' sums, of two tokens a lane, as two floats
+        float hi[2], lo[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int i = lane * 2 + e;
-          float gv = i < n ? __ldg(a.g + (t0 + i) * a.Hv + h + warp) : 0.f;
-          if (gv < -200.f) gv = -200.f;  // e^-200 is 0 in fp32 already
-          x[e] = (double)gv * 1.4426950408889634;
-          bet[warp][i] = i < n ? __ldg(a.beta + (t0 + i) * a.Hv + h + warp) : 0.f;
+          const float gv = next_g[e] < -200.f ? -200.f : next_g[e];  // e^-200 is 0 in fp32 already
+          hi[e] = gv * 1.44269502f;  // times log2 e, in two parts as well
+          lo[e] = fmaf(gv, 1.44269502f, -hi[e]) + gv * 1.92596303e-8f;
+          bet[warp][lane * 2 + e] = next_b[e];
         }
-        double s = x[0] + x[1];
+        add_pair(hi[1], lo[1], hi[0], lo[0]);
+        float sh = hi[1], sl = lo[1];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-          const double y = __shfl_up_sync(0xffffffffu, s, d);
-          if (lane >= d) s += y;
+          const float yh = __shfl_up_sync(0xffffffffu, sh, d), yl = __shfl_up_sync(0xffffffffu, sl, d);
+          if (lane >= d) add_pair(sh, sl, yh, yl);
         }
-        const double s0 = s - x[1];
-        gam[warp][lane * 2] = make_float2((float)s0, (float)(s0 - (double)(float)s0));
-        gam[warp][lane * 2 + 1] = make_float2((float)s, (float)(s - (double)(float)s));
+        float ph = __shfl_up_sync(0xffffffffu, sh, 1), pl = __shfl_up_sync(0xffffffffu, sl, 1);
+        if (lane == 0) ph = pl = 0.f;
+        add_pair(hi[0], lo[0], ph, pl);
+        gam[warp][lane * 2] = make_float2(hi[0], lo[0]);
+        gam[warp][lane * 2 + 1] = make_float2(sh, sl);
       }
+      fetch_decays(h4 + 4);
       __syncthreads();
     }
     uint8_t* item = p.ws + (chunk * a.Hv + h) * (int64_t)kDcItem;
@@ -358,12 +384,11 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
         }
     }
     // T's rows start from D diag(beta)
-    float PT[8][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        T[j][e] = PT[j][e] = 0.f;
+        T[j][e] = 0.f;
         if (j >> 1 == warp) T[j][e] = diag[warp][g + (e >> 1) * 8][(j & 1) * 8 + t2 + (e & 1)] * be[j * 8 + t2 + (e & 1)];
       }
 #pragma unroll
@@ -381,23 +406,20 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
           }
       }
       __syncthreads();
-      if (warp < s) continue;
+      if (warp <= s) continue;
 #pragma unroll
       for (int j = 0; j <= s; ++j) {
         uint32_t th[4], tl[4];
         const uint32_t at = smem_u32(img) + (s * 16 + (lane & 15)) * 128 + (((j * 2 + (lane >> 4)) ^ (lane & 7)) << 4);
         ldsm4_trans(at, th);
-        mma_16816(PT[2 * j], P[s], th[0], th[1]);
-        mma_16816(PT[2 * j + 1], P[s], th[2], th[3]);
-        if (s < 3 && warp > s) {
-          ldsm4_trans(at + kDcBlock, tl);
-          mma_16816(T[2 * j], eh[s < 3 ? s : 0], th[0], th[1]);
-          mma_16816(T[2 * j + 1], eh[s < 3 ? s : 0], th[2], th[3]);
-          mma_16816(T[2 * j], eh[s < 3 ? s : 0], tl[0], tl[1]);
-          mma_16816(T[2 * j + 1], eh[s < 3 ? s : 0], tl[2], tl[3]);
-          mma_16816(T[2 * j], el[s < 3 ? s : 0], th[0], th[1]);
-          mma_16816(T[2 * j + 1], el[s < 3 ? s : 0], th[2], th[3]);
-        }
+        ldsm4_trans(at + kDcBlock, tl);
+        const int x = s < 3 ? s : 0;  // (no warp is past the last step)
+        mma_16816(T[2 * j], eh[x], th[0], th[1]);
+        mma_16816(T[2 * j + 1], eh[x], th[2], th[3]);
+        mma_16816(T[2 * j], eh[x], tl[0], tl[1]);
+        mma_16816(T[2 * j + 1], eh[x], tl[2], tl[3]);
+        mma_16816(T[2 * j], el[x], th[0], th[1]);
+        mma_16816(T[2 * j + 1], el[x], th[2], th[3]);
       }
     }
     // out: T's image as it lies in shared memory, P T from the registers; the blocks above the diagonal
@@ -409,14 +431,27 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
       *reinterpret_cast<uint4*>(item + 2 * kDcBlock + o) = *reinterpret_cast<const uint4*>(img + kDcBlock + o);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j > 2 * warp + 1) break;
+    for (int j = 0; j < 4; ++j) {
+      if (j > warp) break;
+      float x[2][4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = i0 + e * 8;
-        *reinterpret_cast<uint32_t*>(item + kDcBlock + i * 128 + ((j ^ (i & 7)) << 4) + t2 * 2) =
-            pack_half2(PT[j][2 * e], PT[j][2 * e + 1]);
+      for (int e = 0; e < 4; ++e) x[0][e] = x[1][e] = 0.f;
+#pragma unroll
+      for (int s = j; s < 4; ++s) {
+        if (s > warp) break;
+        uint32_t th[4];
+        ldsm4_trans(smem_u32(img) + (s * 16 + (lane & 15)) * 128 + (((j * 2 + (lane >> 4)) ^ (lane & 7)) << 4), th);
+        mma_16816(x[0], P[s], th[0], th[1]);
+        mma_16816(x[1], P[s], th[2], th[3]);
       }
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = i0 + e * 8;
+          *reinterpret_cast<uint32_t*>(item + kDcBlock + i * 128 + (((2 * j + y) ^ (i & 7)) << 4) + t2 * 2) =
+              pack_half2(x[y][2 * e], x[y][2 * e + 1]);
+        }
     }
   }
 }
