@@ -460,16 +460,12 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
 constexpr int kD2Stages = 3;
 constexpr int kD2Q = 2 * kDcBlock, kD2Item = 4 * kDcBlock, kD2V = kD2Item + 26624;  // places in a stage
 
-template <int W>
-struct ScanCfg {
-  // a warp of its own for the loads, unless that makes a third warp in an SM sub-partition, whose
-  // registers two warps of 255 fill
-  static constexpr bool kLoader = W == 4;
-  static constexpr int kThreads = (W + kLoader) * 32;
-  static constexpr int kStage = kD2V + W / 4 * kDcBlock;
-  static constexpr int kBytes = 4 * kDcBlock + kDcItem + W / 4 * kDcBlock;  // loaded per chunk
-  static constexpr int kSmem = 1024 + kD2Stages * kStage + 128;
-};
+constexpr int kD2Warps = 4;                     // that walk, 16 columns of v each; one more loads
+constexpr int kD2Threads = (kD2Warps + 1) * 32;
+constexpr int kD2Slices = kDeltaD / (kD2Warps * 16);  // CTAs a head
+constexpr int kD2Stage = kD2V + kDcBlock;
+constexpr int kD2Bytes = 5 * kDcBlock + kDcItem;  // loaded per chunk
+constexpr int kD2Smem = 1024 + kD2Stages * kD2Stage + 128;
 
 // a power of two that takes magnitudes up to `bits` (an fp32's) to 2^14, and its inverse
 TB_DEVI float operand_scale(uint32_t bits, float& inverse) {
@@ -485,31 +481,42 @@ TB_DEVI void mbar_arrive_reads(uint64_t* bar) {
   asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// W warps per CTA, 16 columns of v each.
-template <int W>
-__global__ void __launch_bounds__(ScanCfg<W>::kThreads, 1)
+__global__ void __launch_bounds__(kD2Threads, 1)
     delta_scan_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmV, const ChunkArgs p) {
-  using C = ScanCfg<W>;
   const DeltaArgs& a = p.a;
   extern __shared__ uint8_t d2_raw[];
   const uint32_t raw = smem_u32(d2_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = d2_raw + (base - raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kD2Stages * C::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kD2Stages * kD2Stage);
   uint64_t* empty = full + kD2Stages;
   volatile int* aborted = reinterpret_cast<volatile int*>(full + 2 * kD2Stages);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kSlices = 8 / W;
-  const int slice = (int)(blockIdx.x % kSlices);
-  const int64_t bh = blockIdx.x / kSlices;
-  const int h = (int)(bh % a.Hv), b = (int)(bh / a.Hv), hk = h / (a.Hv / a.Hk);
+  const int slice = (int)(blockIdx.x % kD2Slices);
+  const int64_t bh = blockIdx.x / kD2Slices;
+  const int h = (int)(bh % a.Hv), hk = h / (a.Hv / a.Hk);
+  int b = (int)(bh / a.Hv);
+  if (a.B > 1 && a.B <= 64) {
+    // the requests with the most chunks first: what comes last then is short.  Each lane ranks two.
+    int mine[2], rank[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) mine[e] = lane + 32 * e < a.B ? (int)chunks_of(a, lane + 32 * e) : -1;
+    for (int i = 0; i < a.B; ++i) {
+      const int other = __shfl_sync(0xffffffffu, i < 32 ? mine[0] : mine[1], i & 31);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) rank[e] += other > mine[e] || (other == mine[e] && i < lane + 32 * e);
+    }
+    const unsigned w0 = __ballot_sync(0xffffffffu, lane < a.B && rank[0] == b);
+    const unsigned w1 = __ballot_sync(0xffffffffu, lane + 32 < a.B && rank[1] == b);
+    b = w0 ? __ffs(w0) - 1 : __ffs(w1) + 31;
+  }
   if (tid == 0) {
     *aborted = 0;
     for (int i = 0; i < kD2Stages; ++i) {
       mbar_init(full + i, 1);
-      mbar_init(empty + i, W);
+      mbar_init(empty + i, kD2Warps);
     }
     fence_barrier_init();
   }
@@ -529,8 +536,7 @@ __global__ void __launch_bounds__(ScanCfg<W>::kThreads, 1)
   };
 
   int64_t first = 0;  // the request's first chunk
-  constexpr int kLoads = C::kLoader ? W : 0;  // the warp that loads
-  if (warp == kLoads) {
+  if (warp == kD2Warps) {
     const ChunkScan sc = chunk_scan(a, lane);
     first = sc.upto - sc.own;
     const int src = b / sc.per;
@@ -538,42 +544,35 @@ __global__ void __launch_bounds__(ScanCfg<W>::kThreads, 1)
       for (int i = lane * sc.per; i < b; ++i) first += chunks_of(a, i);
     first = __shfl_sync(0xffffffffu, first, src);
   }
-  // a lane per copy
-  constexpr int kCopies = 5 + W / 4;
-  auto load = [&](int c) {
-    const int s = c % kD2Stages, row = (int)t0 + c * kDcTok;
-    const uint32_t sa = base + s * C::kStage, bar = smem_u32(full + s);
-    if (c >= kD2Stages) wait(empty + s, (c / kD2Stages - 1) & 1);
-    if (lane == 0) {
-      mbar_arrive_expect_tx(full + s, C::kBytes);
-      if (c == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1's results
-      bulk_g2s(smem + s * C::kStage + kD2Item, p.ws + ((first + c) * a.Hv + h) * (int64_t)kDcItem, kDcItem, full + s);
-    } else if (lane < kCopies) {
-      const int d = (lane - 1) & 1;
-      const bool v = lane >= 5;
-      const CUtensorMap* tm = v ? &tmV : (lane >= 3 ? &tmQ : &tmK);
-      const uint32_t dst = sa + (v ? kD2V : (lane >= 3 ? kD2Q : 0)) + d * kDcBlock;
-      tma_load_3d<1>(dst, tm, v ? (slice * (W / 4) + d) * 64 : d * 64, v ? h : hk, row, bar);
+  if (warp == kD2Warps) {  // loads, a lane per copy
+    for (int c = 0; c < nc; ++c) {
+      const int s = c % kD2Stages, row = (int)t0 + c * kDcTok;
+      const uint32_t sa = base + s * kD2Stage, bar = smem_u32(full + s);
+      if (c >= kD2Stages) wait(empty + s, (c / kD2Stages - 1) & 1);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(full + s, kD2Bytes);
+        if (c == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1's results
+        bulk_g2s(smem + s * kD2Stage + kD2Item, p.ws + ((first + c) * a.Hv + h) * (int64_t)kDcItem, kDcItem, full + s);
+      } else if (lane < 6) {
+        const int d = (lane - 1) & 1;
+        const CUtensorMap* tm = lane == 5 ? &tmV : (lane >= 3 ? &tmQ : &tmK);
+        const uint32_t dst = sa + (lane == 5 ? kD2V : (lane >= 3 ? kD2Q : 0) + d * kDcBlock);
+        tma_load_3d<1>(dst, tm, (lane == 5 ? slice : d) * 64, lane == 5 ? h : hk, row, bar);
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  };
-  if (warp == kLoads)
-    for (int c = 0; c < (C::kLoader ? nc : kD2Stages - 1) && c < nc; ++c) load(c);
-
-  auto linger = [&]() {  // a wait gave up: leave the copies in flight time to land before the CTA ends
-    const uint64_t t = globaltimer_ns();
-    while (*aborted && globaltimer_ns() - t < 1000000) {
+    if (*aborted) {  // a wait gave up: leave the copies in flight time to land before the CTA ends
+      const uint64_t t = globaltimer_ns();
+      while (globaltimer_ns() - t < 1000000) {
+      }
     }
-  };
-  if (C::kLoader && warp == W) {
-    linger();
     return;
   }
 
   const int g = lane >> 2, t2 = (lane & 3) * 2;
   const int64_t si = delta_slot(a.slot_in, b, a.n_in, a.status), so = delta_slot(a.slot_out, b, a.n_out, a.status);
   const int64_t head_size = (int64_t)a.Hv * kDeltaD * kDeltaD;
-  const int col = slice * W * 16 + warp * 16;  // the warp's first column of v
+  const int col = (slice * kD2Warps + warp) * 16;  // the warp's first column of v
   // S^T: rows g, g + 8 (columns of v), columns 8 j + t2, + 1 (of k)
   float S[16][4];
   {
@@ -596,23 +595,23 @@ __global__ void __launch_bounds__(ScanCfg<W>::kThreads, 1)
   const uint32_t row_k = ((uint32_t)lane & 15u) * 128u;                                // rows are k
   const uint32_t pc_n = ((uint32_t)lane >> 3) & 1u, pc_k = (uint32_t)lane >> 4;
   const uint32_t v_row = ((((uint32_t)lane >> 4) & 1u) * 8u + sw) * 128u;
-  const uint32_t v_pc = (((uint32_t)(warp & 3) * 2u + pc_n) ^ sw) << 4;
+  const uint32_t v_pc = (((uint32_t)warp * 2u + pc_n) ^ sw) << 4;
 
   for (int c = 0; c < nc; ++c) {
     const int s = c % kD2Stages;
-    const uint32_t K = base + s * C::kStage, Q = K + kD2Q, X = K + kD2Item, V = K + kD2V + (warp >> 2) * kDcBlock;
-    const float* f = reinterpret_cast<const float*>(smem + s * C::kStage + kD2Item + kDcFactors);
+    const uint32_t K = base + s * kD2Stage, Q = K + kD2Q, X = K + kD2Item, V = K + kD2V;
+    const float* f = reinterpret_cast<const float*>(smem + s * kD2Stage + kD2Item + kDcFactors);
     const int n = (int)(len - (int64_t)c * kDcTok < kDcTok ? len - (int64_t)c * kDcTok : kDcTok);
     float down_s;
     const float up_s = operand_scale(__reduce_max_sync(0xffffffffu, max(max(sbig[0], sbig[1]), max(sbig[2], sbig[3]))), down_s);
     wait(full + s, (c / kD2Stages) & 1);
     if (n < kDcTok) {  // the last chunk: rows of K that are another request's, out of the sum over the tokens
-      for (int i = tid; i < (kDcTok - n) * 16; i += W * 32) {
+      for (int i = tid; i < (kDcTok - n) * 16; i += kD2Warps * 32) {
         const int r = n + (i >> 4), x = i & 15;
         asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(K + (x >> 3) * kDcBlock + r * 128 + (x & 7) * 16), "r"(0)
                      : "memory");
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(kD2Warps * 32) : "memory");
     }
     // A warp has its SM sub-partition to itself, so nothing but its own other work fills the latency of a
     // load or the time of an MMA: loads run a step ahead, and what is not on the way from S to the next
@@ -649,7 +648,6 @@ __global__ void __launch_bounds__(ScanCfg<W>::kThreads, 1)
         ldsm4((ks < 7 ? K + at_n(ks + 1) : Q + at_n(0)) + j * 2048, bk[j]);
       }
     }
-    if (!C::kLoader && warp == 0 && c + kD2Stages - 1 < nc) load(c + kD2Stages - 1);  // the other warps left that stage a chunk ago
     // S^T q, and beside it R = v - exp(gamma) S^T k
     uint32_t big[4] = {0, 0, 0, 0}, vv[4];
     ldsm4_trans(V + v_row + v_pc, vv);
@@ -822,30 +820,27 @@ __global__ void __launch_bounds__(ScanCfg<W>::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) dst[(j * 8 + (e & 1)) * kDeltaD + (e >> 1) * 8] = S[j][e];
   }
-  if (!C::kLoader && warp == 0) linger();
 }
 
-template <int W>
 static int launch_scan(const ChunkArgs& p, const DeviceFacts& f, cudaStream_t s) {
-  using C = ScanCfg<W>;
   const DeltaArgs& a = p.a;
   CUtensorMap tk, tq, tv;
   int rc = token_map(&tk, a.k, a.T, a.Hk, kDeltaD, a.ldk, 1, kDcTok);
   if (rc == TB_OK) rc = token_map(&tq, a.q, a.T, a.Hk, kDeltaD, a.ldq, 1, kDcTok);
   if (rc == TB_OK) rc = token_map(&tv, a.v, a.T, a.Hv, kDeltaD, a.ldv, 1, kDcTok);
-  if (rc == TB_OK) rc = ensure_dynamic_smem(reinterpret_cast<const void*>(delta_scan_kernel<W>), f.device, C::kSmem);
+  if (rc == TB_OK) rc = ensure_dynamic_smem(reinterpret_cast<const void*>(delta_scan_kernel), f.device, kD2Smem);
   if (rc != TB_OK) return rc;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.B * a.Hv * (8 / W)));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.gridDim = dim3((unsigned)(a.B * a.Hv * kD2Slices));
+  cfg.blockDim = dim3(kD2Threads);
+  cfg.dynamicSmemBytes = kD2Smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, delta_scan_kernel<W>, tk, tq, tv, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, delta_scan_kernel, tk, tq, tv, p);
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return TB_ERR_CUDA;
@@ -865,13 +860,11 @@ int launch_delta_chunks(const DeltaArgs& a, void* workspace, cudaStream_t s) {
   p.a = a;
   p.ws = static_cast<uint8_t*>(workspace);
   const int64_t prep = (a.T / kDcTok + a.B) * a.Hk, heads = (int64_t)a.B * a.Hv;
-  if (prep > INT32_MAX || heads > INT32_MAX / 2) return TB_ERR_TOO_LARGE;
+  if (prep > INT32_MAX || heads > INT32_MAX / kD2Slices) return TB_ERR_TOO_LARGE;
   delta_prep_kernel<<<(unsigned)prep, kD1Threads, 0, s>>>(p);
   rc = check_launch();
   if (rc != TB_OK) return rc;
-  // half heads per CTA while they do not fill the SMs: one warp per SM sub-partition each, where two
-  // would share its tensor core
-  return heads * 2 <= f.sms ? launch_scan<4>(p, f, s) : launch_scan<8>(p, f, s);
+  return launch_scan(p, f, s);
 }
 
 }  // namespace tb
