@@ -8,9 +8,11 @@
 //
 // Per tile of 128 keys:  S = Q K^T (tensor memory, 128 x 128 fp32, two buffers), softmax with the
 // running maximum and sum in registers (one thread per row), P in fp16 back into S's columns, and
-// O += P V (tensor memory, 128 x D fp32).  The MMA thread issues S of the next tile before it waits
-// for P of this one, so the tensor cores work through the softmax.
-//   D = 256: 16.8 MFLOP a tile are 2048 clocks at 8192 FLOP per clock; 16384 exponentials 512 to 1024.
+// O += P V (tensor memory, 128 x D fp32).  A tile's softmax takes about 2100 clocks from S to P with one
+// warp per SM sub-partition, as long as its MMAs (D = 256: 16.8 MFLOP are 2048 clocks at 8192 a clock),
+// so two groups of four warps take turns at the tiles: while one is in the softmax of a tile, the
+// tensor cores run P V of the tile before and S of the next.  The groups pass the rows' maxima on in
+// tile order, as O has one scale.
 // CG = 2: a CTA pair (cta_group::2) runs 256 rows on the same keys; each CTA loads half of K (its 64
 // keys) and half of V (its half of the columns) and the tensor cores read both halves.  One CTA alone
 // reads Q, K and V at 128 bytes a clock, all that shared memory gives, and loads 64 bytes a clock
@@ -32,7 +34,7 @@
 
 namespace tb {
 
-constexpr int kPaThreads = 192;  // warps 0-3: softmax, one per tensor-memory lane quarter; 4: loads; 5: MMAs
+constexpr int kPaThreads = 320;  // warps 0-3 and 4-7: softmax of even and odd key tiles; 8: loads; 9: MMAs
 constexpr int kPaKeys = 128;     // keys per tile
 constexpr int kPaSlot = 16384;   // bytes of a ring slot
 
@@ -81,8 +83,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   uint64_t* s_full = q_full + 1;   // [2]
   uint64_t* p_full = q_full + 3;   // [2]
   uint64_t* o_done = q_full + 5;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 6);
+  uint64_t* m_full = q_full + 6;   // [2][4]: a warp's row maxima after its tile, for the other group's warp
+  uint64_t* o_last = q_full + 14;  // every tile's P V is done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 15);
   __shared__ volatile int aborted;
+  __shared__ float maxima[2][128];
+  __shared__ float2 sums[2][128];  // (sum, the maximum it refers to) of each group's rows
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CG > 1 ? cta_rank_in_cluster() : 0;
@@ -100,9 +106,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     mbar_init(p_full, 4 * CG);  // lane 0 of each softmax warp
     mbar_init(p_full + 1, 4 * CG);
     mbar_init(o_done, 1);
+    mbar_init(o_last, 1);
+    for (int i = 0; i < 8; ++i) mbar_init(m_full + i, 1);
     fence_barrier_init();
   }
-  if (warp == 5) tmem_alloc_cg<CG>(tmem_slot, 512);
+  if (warp == 9) tmem_alloc_cg<CG>(tmem_slot, 512);
 
   // the request and tile of this item: tiles of all requests in order, a request's last (longest)
   // tile first, the heads side by side
@@ -202,7 +210,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
   };
 
-  if (warp == 4) {
+  if (warp == 8) {
     if (lane == 0 && n > 0) {
       const uint32_t qbar = CG > 1 ? cluster_addr(q_full, 0) : smem_u32(q_full);
       if (rank == 0) mbar_arrive_expect_tx(q_full, CG * C::kChunks * 128 * p.gp * p.tok);
@@ -248,7 +256,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     if (lane == 0 && rank == 0 && n > 0) {
       int it = 0;
       wait(q_full, 0);
@@ -271,8 +279,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         mma_commit_cg<CG>(s_full + (i & 1));
       };
       qk(0);
+      if (n > 1) qk(1);
       for (int i = 0; i < n; ++i) {
-        if (i + 1 < n) qk(i + 1);
         wait_cluster(p_full + (i & 1), (i >> 1) & 1);
         tmem_fence_after();
         for (int s = 0; s < C::kVSlots; ++s, ++it) {
@@ -287,28 +295,29 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           mma_commit_cg<CG>(empty + r);
         }
         mma_commit_cg<CG>(o_done);
+        if (i + 2 < n) qk(i + 2);  // over P of this tile, which the MMAs before it have read
       }
+      mma_commit_cg<CG>(o_last);
     }
     __syncwarp();
   } else {
-    // ---- softmax: thread = row
-    const int row = warp * 32 + lane;
+    // ---- softmax: thread = row; two groups of four warps take turns at the key tiles
+    const int group = warp >> 2, row = tid & 127;
     const int tr = row / p.gp, head = h0 + row - tr * p.gp;
     const int64_t tok = t0 + tr;
     const bool live = b >= 0 && tr < p.tok && tok < lq;
     int64_t lim64 = live ? tok + lk - lq + 1 : 0;  // keys [0, lim) are visible
     if (lim64 < 0) lim64 = 0;
-    const uint32_t mine = tmem + ((uint32_t)warp << 21);  // lane quarter: 32 lanes, in bits 16..
+    const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);  // lane quarter: 32 lanes, in bits 16..
     const float sc = a.scale_log2;
-    float m = -INFINITY, l = 0.f;  // the maximum in use (log2 units after scaling), and the sum
+    float m = -INFINITY, l = 0.f;  // the group's reference (log2 units after scaling), and its sum
     const uint32_t pbar0 = CG > 1 ? cluster_addr(p_full, 0) : smem_u32(p_full);
-    for (int i = 0; i < n; ++i) {
-      const int buf = i & 1;
-      wait(s_full + buf, (i >> 1) & 1);
+    for (int i = group; i < n; i += 2) {
+      wait(s_full + group, (i >> 1) & 1);
       tmem_fence_after();
       float s[kPaKeys];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(mine + buf * kPaKeys + c * 32, s + 32 * c);
+      for (int c = 0; c < 4; ++c) tmem_ld32(mine + group * kPaKeys + c * 32, s + 32 * c);
       tmem_wait_ld();
       const int64_t left = lim64 - (int64_t)i * kPaKeys;
       if (__any_sync(0xffffffffu, left < kPaKeys)) {
@@ -324,11 +333,24 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
       const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      // the reference of the tile before, from the other group
+      float before = -INFINITY;
+      if (i > 0) {
+        wait(m_full + (group ^ 1) * 4 + (warp & 3), ((i - 1) >> 1) & 1);
+        before = *reinterpret_cast<volatile float*>(&maxima[group ^ 1][row]);
+      }
       // a new reference only when the old one is 2^8 too small (or there is none yet)
-      const bool grow = tmax > m + 8.f || (m == -INFINITY && tmax > -INFINITY);
+      const bool grow = tmax > before + 8.f || (before == -INFINITY && tmax > -INFINITY);
+      const float now = grow ? tmax : before;
+      if (i + 1 < n) {
+        maxima[group][row] = now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(m_full + group * 4 + (warp & 3));
+      }
       if (__any_sync(0xffffffffu, grow && i > 0)) {
-        const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - tmax)) : 1.f;
-        l *= f;
+        const float f = grow ? (before == -INFINITY ? 0.f : ex2(before - now)) : 1.f;
+        // a parity tells only neighbouring phases apart: tile i - 2's is over, as S of tile i came after
+        // it, and tile i's cannot be over before this warp's part of P is there
         wait(o_done, (i - 1) & 1);
         tmem_fence_after();
 #pragma unroll 1
@@ -346,7 +368,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         }
         tmem_wait_st();
       }
-      if (grow) m = tmax;
+      if (now != m) l *= m == -INFINITY ? 0.f : ex2(m - now);
+      m = now;
       const float ms = m == -INFINITY ? 0.f : -m;
       float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
 #pragma unroll
@@ -362,7 +385,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           else acc0 = add_f32x2(acc0, x);
           pk[e] = pack_half2(x.x, x.y);
         }
-        tmem_st32(mine + buf * kPaKeys + half * 32, pk);
+        tmem_st32(mine + group * kPaKeys + half * 32, pk);
       }
       acc0 = add_f32x2(acc0, acc1);
       l += acc0.x + acc0.y;
@@ -370,23 +393,28 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (CG > 1) mbar_arrive_cluster(pbar0 + 8u * (uint32_t)buf);
-        else mbar_arrive(p_full + buf);
+        if constexpr (CG > 1) mbar_arrive_cluster(pbar0 + 8u * (uint32_t)group);
+        else mbar_arrive(p_full + group);
       }
     }
-    // ---- O / l -> fp16
-    // one phase per tile; all but the last two are known to be over (S of the last tile came after
-    // them), and a parity tells only neighbouring phases apart: wait for both
-    if (n > 1) wait(o_done, (n - 2) & 1);
+    // ---- O / l -> fp16, half of the columns per group
+    sums[group][row] = make_float2(l, m);
+    auto sync256 = []() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    sync256();
+    {
+      const float2 other = sums[group ^ 1][row];
+      const float M = fmaxf(m, other.y);  // the last reference: references only grow
+      l = (m == -INFINITY ? l : l * ex2(m - M)) + (other.y == -INFINITY ? other.x : other.x * ex2(other.y - M));
+    }
     if (n > 0) {
-      wait(o_done, (n - 1) & 1);
+      wait(o_last, 0);
       tmem_fence_after();
     }
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
     bool odd = false;
     __half* dst = a.o + ((q0 + tok) * a.Hq + head) * D;
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
+    for (int c = group * (D / 2); c < (group + 1) * (D / 2); c += 32) {
       float o[32];
       if (n > 0) {
         tmem_ld32(mine + C::kTmemO + c, o);
@@ -405,6 +433,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
     }
     odd = live && lim64 > 0 && (odd || !(l < INFINITY));
+    sync256();  // both halves are written before a row is written again
     unsigned again = __ballot_sync(0xffffffffu, odd);
     while (again) {
       const int r = __ffs(again) - 1;
@@ -419,7 +448,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   tmem_fence_before();
   __syncthreads();
   if constexpr (CG > 1) cluster_barrier();  // no CTA leaves while its peer may still signal it or read it
-  if (warp == 5) tmem_dealloc_cg<CG>(tmem, 512);
+  if (warp == 9) tmem_dealloc_cg<CG>(tmem, 512);
 }
 
 // 3-D map [tokens, heads, D] with `ld` elements between tokens; box 64 x heads x tokens

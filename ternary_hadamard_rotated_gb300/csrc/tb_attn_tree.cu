@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   uint64_t* p_full = q_full + 4;  // [2]
   uint64_t* o_done = q_full + 6;
   uint64_t* o_free = q_full + 7;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 8);
+  uint64_t* o_last = q_full + 8;  // the segment's last P V is done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 9);
   __shared__ volatile int aborted;
   __shared__ uint32_t granules[16];  // per key tile: which runs of 16 keys lie in a page of the cache
 
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       mbar_init(p_full + i, 4);  // lane 0 of each softmax warp
     }
     mbar_init(o_done, 1);
+    mbar_init(o_last, 1);
     mbar_init(o_free, 4);
     fence_barrier_init();
   }
@@ -358,6 +360,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           }
           mma_commit(o_done);
         }
+        mma_commit(o_last);
       }
       __syncwarp();
       gt += s.tiles;
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const uint32_t mine = tmem + ((uint32_t)warp << 21);
     const float sc = a.scale_log2;
     const int tr = row / p.gp;
-    int gt = 0;
+    int gt = 0, seg = 0;
     int64_t it = 0;  // slots used before this segment
     for (int64_t u = lo; u < hi;) {
       const TaSegment s = segment(u);
@@ -439,6 +442,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (__any_sync(0xffffffffu, grow && i > 0 && live)) {
           const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - tmax)) : 1.f;
           l *= f;
+          // a parity tells only neighbouring phases apart: tile i - 2's is over, as S of tile i came after
+          // it, and tile i's cannot be over before this warp's part of P is there
           wait(o_done, (g - 1) & 1);
           tmem_fence_after();
 #pragma unroll 1
@@ -500,8 +505,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       gt += s.tiles;
       it += (int64_t)s.tiles * (C::kKSlots + C::kVSlots);
       // ---- the segment's O: the output, or a part
-      if (s.tiles > 1) wait(o_done, (gt - 2) & 1);  // a parity tells only neighbouring phases apart
-      wait(o_done, (gt - 1) & 1);
+      wait(o_last, seg & 1);
+      ++seg;
       tmem_fence_after();
       const bool whole = s.tiles == s.item_tiles;
       const int64_t slot = (int64_t)blockIdx.x * 2 + (s.tile0 == 0);
