@@ -36,23 +36,18 @@ namespace tb {
 
 constexpr int kPaThreads = 320;  // warps 0-3 and 4-7: softmax of even and odd key tiles; 8: loads; 9: MMAs
 constexpr int kPaKeys = 128;     // keys per tile
-constexpr int kPaSlot = 16384;   // bytes of a ring slot
 
 template <int D, int CG>
 struct PaCfg {
   static constexpr int kChunks = D / 64;             // 128-byte wide pieces of a row
   static constexpr int kQBytes = kChunks * 16384;    // 128 rows
-  // K: each CTA holds 128 / CG keys, all of D; a slot holds kKChunks pieces of them
+  // of a tile's keys a CTA loads 128 / CG rows of K, and D / CG columns of V
   static constexpr int kKRows = kPaKeys / CG;
-  static constexpr int kKChunks = kPaSlot / (kKRows * 128);
-  static constexpr int kKSlots = kChunks / kKChunks;
-  // V: each CTA holds D / CG columns (kVChunks pieces) of all keys; a slot holds kVKeys keys
   static constexpr int kVChunks = kChunks / CG;
-  static constexpr int kVKeys = kPaSlot / (kVChunks * 128);
-  static constexpr int kVSlots = kPaKeys / kVKeys;
-  static_assert(kKSlots >= 1 && kVChunks >= 1 && kVKeys <= kPaKeys, "D = 64 has no pair form");
-  static constexpr int kSlots = (220 * 1024 - kQBytes) / kPaSlot > 12 ? 12 : (220 * 1024 - kQBytes) / kPaSlot;
-  static constexpr int kSmem = 1024 + kQBytes + kSlots * kPaSlot + 512;
+  static_assert(kVChunks >= 1, "D = 64 has no pair form");
+  static constexpr int kTileBytes = kPaKeys * D * 2 / CG;  // of K, or of V
+  static constexpr int kK = kQBytes, kV = kK + 2 * kTileBytes, kBars = kV + 2 * kTileBytes;  // two of each
+  static constexpr int kSmem = 1024 + kBars + 256;
   static constexpr uint32_t kIdescQK = (1u << 4) | ((uint32_t)(kPaKeys >> 3) << 17) | ((uint32_t)(128 * CG >> 4) << 24);
   static constexpr uint32_t kIdescPV =
       (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(128 * CG >> 4) << 24);
@@ -75,17 +70,14 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   const uint32_t raw = smem_u32(pa_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = pa_raw + (base - raw);
-  const uint32_t ring = base + C::kQBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kQBytes + C::kSlots * kPaSlot);
-  uint64_t* full = bars;
-  uint64_t* empty = bars + C::kSlots;
-  uint64_t* q_full = bars + 2 * C::kSlots;
-  uint64_t* s_full = q_full + 1;   // [2]
-  uint64_t* p_full = q_full + 3;   // [2]
-  uint64_t* o_done = q_full + 5;
-  uint64_t* m_full = q_full + 6;   // [2][4]: a warp's row maxima after its tile, for the other group's warp
-  uint64_t* o_last = q_full + 14;  // every tile's P V is done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 15);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
+  // per key tile, two of each in turn: K and V have landed; S is computed (and K read); P is written;
+  // P V is added (and V read)
+  uint64_t *k_full = bars, *v_full = bars + 2, *s_full = bars + 4, *p_full = bars + 6, *o_done = bars + 8;
+  uint64_t* m_full = bars + 10;  // [2][4]: a warp's row maxima after its tile, for the other group's warp
+  uint64_t* q_full = bars + 18;
+  uint64_t* o_last = bars + 19;  // every tile's P V is done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
   __shared__ volatile int aborted;
   __shared__ float maxima[2][128];
   __shared__ float2 sums[2][128];  // (sum, the maximum it refers to) of each group's rows
@@ -96,18 +88,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 
   if (tid == 0) {
     aborted = 0;
-    for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + i, 1);
+      mbar_init(v_full + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4 * CG);  // lane 0 of each warp of the group, of both CTAs
+      mbar_init(o_done + i, 1);
     }
-    mbar_init(q_full, 1);
-    mbar_init(s_full, 1);
-    mbar_init(s_full + 1, 1);
-    mbar_init(p_full, 4 * CG);  // lane 0 of each softmax warp
-    mbar_init(p_full + 1, 4 * CG);
-    mbar_init(o_done, 1);
-    mbar_init(o_last, 1);
     for (int i = 0; i < 8; ++i) mbar_init(m_full + i, 1);
+    mbar_init(q_full, 1);
+    mbar_init(o_last, 1);
     fence_barrier_init();
   }
   if (warp == 9) tmem_alloc_cg<CG>(tmem_slot, 512);
@@ -213,41 +203,34 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   if (warp == 8) {
     if (lane == 0 && n > 0) {
       const uint32_t qbar = CG > 1 ? cluster_addr(q_full, 0) : smem_u32(q_full);
+      const uint32_t kbar = CG > 1 ? cluster_addr(k_full, 0) : smem_u32(k_full);
+      const uint32_t vbar = CG > 1 ? cluster_addr(v_full, 0) : smem_u32(v_full);
       if (rank == 0) mbar_arrive_expect_tx(q_full, CG * C::kChunks * 128 * p.gp * p.tok);
 #pragma unroll
       for (int c = 0; c < C::kChunks; ++c)
         tma_load_3d<CG>(base + c * 16384, &tmQ, c * 64, h0, (int)(q0 + t0), qbar);
-      int it = 0;
-      auto slot = [&](auto&& issue) {  // the next free slot; `issue` loads kPaSlot bytes into it
-        const int s = it % C::kSlots, ph = it / C::kSlots;
-        if (ph > 0) wait(empty + s, (ph - 1) & 1);
-        if (rank == 0) mbar_arrive_expect_tx(full + s, CG * kPaSlot);
-        issue(ring + s * kPaSlot, CG > 1 ? cluster_addr(full + s, 0) : smem_u32(full + s));
-        ++it;
-      };
       auto load_k = [&](int i) {
-        const int row = (int)(k0 + (int64_t)i * kPaKeys) + (int)rank * C::kKRows;
-        for (int s = 0; s < C::kKSlots; ++s)
-          slot([&](uint32_t dst, uint32_t bar) {
+        const int x = i & 1, row = (int)(k0 + (int64_t)i * kPaKeys) + (int)rank * C::kKRows;
+        if (i >= 2) wait(s_full + x, ((i >> 1) - 1) & 1);  // S of two tiles ago has read its K
+        if (rank == 0) mbar_arrive_expect_tx(k_full + x, CG * C::kTileBytes);
 #pragma unroll
-            for (int c = 0; c < C::kKChunks; ++c)
-              tma_load_3d<CG>(dst + c * (C::kKRows * 128), &tmK, (s * C::kKChunks + c) * 64, hk, row, bar);
-          });
+        for (int c = 0; c < C::kChunks; ++c)
+          tma_load_3d<CG>(base + C::kK + x * C::kTileBytes + c * (C::kKRows * 128), &tmK, c * 64, hk, row, kbar + 8u * x);
       };
       auto load_v = [&](int i) {
-        for (int s = 0; s < C::kVSlots; ++s) {
-          const int row = (int)(k0 + (int64_t)i * kPaKeys) + s * C::kVKeys;
-          slot([&](uint32_t dst, uint32_t bar) {
+        const int x = i & 1, row = (int)(k0 + (int64_t)i * kPaKeys);
+        if (i >= 2) wait(o_done + x, ((i >> 1) - 1) & 1);
+        if (rank == 0) mbar_arrive_expect_tx(v_full + x, CG * C::kTileBytes);
 #pragma unroll
-            for (int c = 0; c < C::kVChunks; ++c)
-              tma_load_3d<CG>(dst + c * (C::kVKeys * 128), &tmV, ((int)rank * C::kVChunks + c) * 64, hk, row, bar);
-          });
-        }
+        for (int c = 0; c < C::kVChunks; ++c)
+          tma_load_3d<CG>(base + C::kV + x * C::kTileBytes + c * (kPaKeys * 128), &tmV, ((int)rank * C::kVChunks + c) * 64, hk,
+                          row, vbar + 8u * x);
       };
       load_k(0);
+      if (n > 1) load_k(1);
       for (int i = 0; i < n; ++i) {
-        if (i + 1 < n) load_k(i + 1);
         load_v(i);
+        if (i + 2 < n) load_k(i + 2);
       }
       if (aborted) {  // a wait gave up: leave the copies in flight time to land before the CTA ends
         const uint64_t t = globaltimer_ns();
@@ -257,44 +240,40 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
+    // An MMA is issued about when its predecessor starts, so what this thread does between two of them
+    // is idle time of the tensor cores: a tile costs it three waits and two commits.
     if (lane == 0 && rank == 0 && n > 0) {
-      int it = 0;
+      // descriptors of place 0; the address field counts 16 bytes, and no sum carries out of it
+      const uint64_t qdesc = smem_desc_sw128(base, 1024), kdesc = smem_desc_sw128(base + C::kK, 1024);
+      const uint64_t vdesc = smem_desc_mn128(base + C::kV, kPaKeys * 128, 1024);
       wait(q_full, 0);
-      tmem_fence_after();
       auto qk = [&](int i) {
-        const uint32_t d = tmem + (uint32_t)(i & 1) * kPaKeys;
-        for (int s = 0; s < C::kKSlots; ++s, ++it) {
-          const int r = it % C::kSlots;
-          wait(full + r, (it / C::kSlots) & 1);
-          tmem_fence_after();
+        const int x = i & 1;
+        const uint32_t d = tmem + (uint32_t)x * kPaKeys;
+        const uint64_t kd = kdesc + x * (C::kTileBytes >> 4);
+        wait(k_full + x, (i >> 1) & 1);
+        tmem_fence_after();
 #pragma unroll
-          for (int c = 0; c < C::kKChunks; ++c)
+        for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16_ss<CG>(d, smem_desc_sw128(base + (s * C::kKChunks + c) * 16384 + kk * 32, 1024),
-                             smem_desc_sw128(ring + r * kPaSlot + c * (C::kKRows * 128) + kk * 32, 1024), C::kIdescQK,
-                             (s | c | kk) != 0);
-          mma_commit_cg<CG>(empty + r);
-        }
-        mma_commit_cg<CG>(s_full + (i & 1));
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ss<CG>(d, qdesc + c * (16384 >> 4) + kk * 2, kd + c * (C::kKRows * 128 >> 4) + kk * 2, C::kIdescQK,
+                           (c | kk) != 0);
+        mma_commit_cg<CG>(s_full + x);
       };
       qk(0);
       if (n > 1) qk(1);
       for (int i = 0; i < n; ++i) {
-        wait_cluster(p_full + (i & 1), (i >> 1) & 1);
+        const int x = i & 1;
+        const uint32_t pa = tmem + (uint32_t)x * kPaKeys;
+        const uint64_t vd = vdesc + x * (C::kTileBytes >> 4);
+        wait(v_full + x, (i >> 1) & 1);
+        wait_cluster(p_full + x, (i >> 1) & 1);
         tmem_fence_after();
-        for (int s = 0; s < C::kVSlots; ++s, ++it) {
-          const int r = it % C::kSlots;
-          wait(full + r, (it / C::kSlots) & 1);
-          tmem_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < C::kVKeys / 16; ++kk)
-            mma_f16_ts<CG>(tmem + C::kTmemO, tmem + (uint32_t)(i & 1) * kPaKeys + (s * (C::kVKeys / 16) + kk) * 8,
-                           smem_desc_mn128(ring + r * kPaSlot + kk * 2048, C::kVKeys * 128, 1024), C::kIdescPV,
-                           (i | s | kk) != 0);
-          mma_commit_cg<CG>(empty + r);
-        }
-        mma_commit_cg<CG>(o_done);
+        for (int kk = 0; kk < kPaKeys / 16; ++kk)
+          mma_f16_ts<CG>(tmem + C::kTmemO, pa + kk * 8, vd + kk * (2048 >> 4), C::kIdescPV, (i | kk) != 0);
+        mma_commit_cg<CG>(o_done + x);
         if (i + 2 < n) qk(i + 2);  // over P of this tile, which the MMAs before it have read
       }
       mma_commit_cg<CG>(o_last);
@@ -349,9 +328,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
       if (__any_sync(0xffffffffu, grow && i > 0)) {
         const float f = grow ? (before == -INFINITY ? 0.f : ex2(before - now)) : 1.f;
-        // a parity tells only neighbouring phases apart: tile i - 2's is over, as S of tile i came after
-        // it, and tile i's cannot be over before this warp's part of P is there
-        wait(o_done, (i - 1) & 1);
+        // a parity tells only neighbouring phases apart: tile i - 3's is over, as S of tile i came after
+        // it, and tile i + 1's cannot be over before this warp's part of P is there
+        wait(o_done + (group ^ 1), ((i - 1) >> 1) & 1);
         tmem_fence_after();
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -475,7 +454,7 @@ static int launch_tiles(const PaArgs& p, int sms_device, cudaStream_t s) {
   // without any keys the maps of K and V are never used, but have to be maps
   const int64_t Tk = a.Tk ? a.Tk : 1;
   if (rc == TB_OK) rc = token_map(&tk, a.Tk ? a.k : a.q, Tk, a.Hkv, D, a.ldk, 1, C::kKRows);
-  if (rc == TB_OK) rc = token_map(&tv, a.Tk ? a.v : a.q, Tk, a.Hkv, D, a.ldv, 1, C::kVKeys);
+  if (rc == TB_OK) rc = token_map(&tv, a.Tk ? a.v : a.q, Tk, a.Hkv, D, a.ldv, 1, kPaKeys);
   if (rc != TB_OK) return rc;
   auto* fn = prompt_attn_kernel<D, CG>;
   rc = ensure_dynamic_smem(reinterpret_cast<const void*>(fn), sms_device, C::kSmem);
