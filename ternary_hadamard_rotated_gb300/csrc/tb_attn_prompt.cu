@@ -60,6 +60,91 @@ struct PaArgs {
   int head_parts;   // tiles side by side over the heads: Hkv * (G / gp)
 };
 
+// a tile of 128 CG rows and what it needs; n < 0: no more of them
+struct PaItem {
+  int n, hp;            // key tiles; which heads
+  int q0, lq, k0, lk;   // the request's rows
+  int first;            // the tile's first token in the request
+  int pad;
+};
+
+// Item k of the schedule: all requests' tiles by falling number of key tiles, the heads side by side, so
+// that clusters which take turns at them, back and forth, end together.  Nothing is sorted: the number
+// of tiles with more than c key tiles is a sum over the requests, and a bisection over c finds item
+// k's; whole warps call this, each lane with its share of the requests.
+TB_DEVI bool pa_rows(const AttnArgs& a, int b, int& q0, int& lq, int& k0, int& lk) {
+  const int64_t x = __ldg(a.q_start + b), y = __ldg(a.q_start + b + 1);
+  const int64_t u = __ldg(a.k_start + b), w = __ldg(a.k_start + b + 1);
+  const bool q_ok = x >= 0 && y >= x && y <= a.T, k_ok = u >= 0 && w >= u && w <= a.Tk;
+  q0 = (int)x;
+  lq = q_ok ? (int)(y - x) : 0;
+  k0 = k_ok ? (int)u : 0;
+  lk = k_ok ? (int)(w - u) : 0;
+  return q_ok && k_ok;
+}
+// tiles of a request with more than c key tiles (c = -1: all)
+TB_DEVI int pa_longer(int lq, int lk, int span, int c) {
+  const int tiles = (lq + span - 1) / span;
+  const int64_t x = c < 0 ? -1 : (int64_t)c * kPaKeys - ((int64_t)lk - lq);  // tokens that see at most c tiles of keys
+  return x < 0 ? tiles : (x >= lq ? 0 : tiles - (int)(x / span));
+}
+TB_DEVI PaItem pa_item(const PaArgs& p, int span, int64_t k, int lane) {
+  const AttnArgs& a = p.a;
+  const int per = (a.B + 31) / 32;
+  PaItem it;
+  it.n = -1;
+  it.hp = (int)(k % p.head_parts);
+  const int64_t rank = k / p.head_parts;
+  int q0, lq, k0, lk;
+  auto own = [&](int c) {
+    int64_t n = 0;
+    for (int b = lane * per; b < (lane + 1) * per && b < a.B; ++b) {
+      pa_rows(a, b, q0, lq, k0, lk);
+      n += pa_longer(lq, lk, span, c);
+    }
+    return n;
+  };
+  auto total = [&](int64_t n) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+    return n;
+  };
+  if (rank >= total(own(-1))) return it;
+  int lo = 0, hi = (int)((a.Tk + kPaKeys - 1) / kPaKeys);  // the least c with at most `rank` longer tiles
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (total(own(mid)) <= rank) hi = mid;
+    else lo = mid + 1;
+  }
+  const int64_t longer = own(lo), as_long = own(lo - 1) - longer;
+  int64_t upto = as_long;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += x;
+  }
+  int64_t r = rank - total(longer);
+  const int src = __ffs(__ballot_sync(0xffffffffu, r < upto)) - 1;
+  r -= upto - as_long;  // among the lane's own
+  int b = lane * per, first = 0;
+  if (lane == src) {
+    for (;; ++b) {
+      pa_rows(a, b, q0, lq, k0, lk);
+      const int more = pa_longer(lq, lk, span, lo), same = pa_longer(lq, lk, span, lo - 1) - more;
+      if (r < same) {
+        first = ((lq + span - 1) / span - 1 - more - (int)r) * span;  // the longest such tile first
+        break;
+      }
+      r -= same;
+    }
+  }
+  b = __shfl_sync(0xffffffffu, b, src);
+  it.first = __shfl_sync(0xffffffffu, first, src);
+  pa_rows(a, b, it.q0, it.lq, it.k0, it.lk);
+  it.n = lo;
+  return it;
+}
+
 template <int D, int CG>
 __global__ void __launch_bounds__(kPaThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -75,16 +160,17 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   // P V is added (and V read)
   uint64_t *k_full = bars, *v_full = bars + 2, *s_full = bars + 4, *p_full = bars + 6, *o_done = bars + 8;
   uint64_t* m_full = bars + 10;  // [2][4]: a warp's row maxima after its tile, for the other group's warp
-  uint64_t* q_full = bars + 18;
-  uint64_t* o_last = bars + 19;  // every tile's P V is done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
+  // per item: Q has landed, has been read; O is complete, has been read; the item's words are there, read
+  uint64_t *q_full = bars + 18, *q_empty = bars + 19, *o_last = bars + 20, *o_free = bars + 21;
+  uint64_t *item_full = bars + 22, *item_empty = bars + 24;  // [2] each
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
   __shared__ volatile int aborted;
   __shared__ float maxima[2][128];
   __shared__ float2 sums[2][128];  // (sum, the maximum it refers to) of each group's rows
+  __shared__ PaItem items[2];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CG > 1 ? cta_rank_in_cluster() : 0;
-  const int64_t item = blockIdx.x / CG;
 
   if (tid == 0) {
     aborted = 0;
@@ -94,88 +180,28 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4 * CG);  // lane 0 of each warp of the group, of both CTAs
       mbar_init(o_done + i, 1);
+      mbar_init(item_full + i, 1);
+      mbar_init(item_empty + i, 9);  // the MMA warp and the softmax warps
     }
     for (int i = 0; i < 8; ++i) mbar_init(m_full + i, 1);
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     mbar_init(o_last, 1);
+    mbar_init(o_free, 8 * CG);
     fence_barrier_init();
   }
   if (warp == 9) tmem_alloc_cg<CG>(tmem_slot, 512);
-
-  // the request and tile of this item: tiles of all requests in order, a request's last (longest)
-  // tile first, the heads side by side
-  const int hp = (int)(item % p.head_parts);
-  const int64_t tile_all = item / p.head_parts;
-  const int span = p.tok * CG;
-  int b = -1, tile = 0;
-  {
-    auto tiles = [&](int r) -> int64_t {
-      const int64_t x = __ldg(a.q_start + r), y = __ldg(a.q_start + r + 1);
-      if (x < 0 || y < x || y > a.T) return 0;
-      return (y - x + span - 1) / span;
-    };
-    // every warp looks for itself: a lane adds up its share of the requests, then a scan
-    const int per = (a.B + 31) / 32;
-    int64_t own = 0;
-    for (int i = lane * per; i < (lane + 1) * per && i < a.B; ++i) own += tiles(i);
-    int64_t upto = own;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += x;
-    }
-    int64_t before = upto - own;
-    const bool here = tile_all >= before && tile_all < upto;
-    if (here) {
-      for (int i = lane * per; b < 0; ++i) {
-        const int64_t t = tiles(i);
-        if (tile_all < before + t) {
-          b = i;
-          tile = (int)(t - 1 - (tile_all - before));
-        }
-        before += t;
-      }
-    }
-    const unsigned who = __ballot_sync(0xffffffffu, here);
-    if (who) {
-      b = __shfl_sync(0xffffffffu, b, __ffs(who) - 1);
-      tile = __shfl_sync(0xffffffffu, tile, __ffs(who) - 1);
-    }
-    if (item == 0 && a.status) {  // the first item looks at every request's row starts
-      for (int b = tid; b < a.B; b += kPaThreads) {
-        const int64_t x = __ldg(a.q_start + b), y = __ldg(a.q_start + b + 1);
-        const int64_t u = __ldg(a.k_start + b), w = __ldg(a.k_start + b + 1);
-        if (x < 0 || y < x || y > a.T || u < 0 || w < u || w > a.Tk) set_status(a.status, TB_DEV_BAD_LEN);
-      }
-    }
+  if (blockIdx.x == 0 && a.status) {  // one CTA looks at every request's row starts
+    int x, y, z, w;
+    for (int b = tid; b < a.B; b += kPaThreads)
+      if (!pa_rows(a, b, x, y, z, w)) set_status(a.status, TB_DEV_BAD_LEN);
   }
   tmem_fence_before();
   __syncthreads();
   if constexpr (CG > 1) cluster_barrier();  // the peer's barriers exist
   tmem_fence_after();
   const uint32_t tmem = *tmem_slot;
-
-  int64_t q0 = 0, lq = 0, k0 = 0, lk = 0;
-  if (b >= 0) {
-    q0 = __ldg(a.q_start + b);
-    lq = __ldg(a.q_start + b + 1) - q0;
-    k0 = __ldg(a.k_start + b);
-    lk = __ldg(a.k_start + b + 1) - k0;
-    if (k0 < 0 || lk < 0 || k0 + lk > a.Tk) {
-      k0 = 0;
-      lk = 0;
-    }
-  }
   const int G = a.Hq / a.Hkv, parts = G / p.gp;
-  const int hk = hp / parts, h0 = hk * G + (hp % parts) * p.gp;
-  const int64_t span0 = (int64_t)tile * span;            // the pair's first token in the request
-  const int64_t t0 = span0 + (int64_t)rank * p.tok;          // this CTA's first token
-  // keys that the pair's last token sees: the same count of tiles in both CTAs
-  int64_t last = span0 + span - 1;
-  if (last > lq - 1) last = lq - 1;
-  int64_t keys = b >= 0 ? last + lk - lq + 1 : 0;
-  if (keys < 0) keys = 0;
-  const int n = (int)((keys + kPaKeys - 1) / kPaKeys);
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity) || aborted) return;
@@ -199,228 +225,293 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
     }
   };
+  const int64_t clusters = gridDim.x / CG, me = blockIdx.x / CG;
+  auto my_item = [&](int i) {  // back and forth over the clusters
+    return pa_item(p, p.tok * CG, i * clusters + ((i & 1) ? clusters - 1 - me : me), lane);
+  };
+  // the words of this CTA's item number i, handed back when the warp has them
+  auto next_item = [&](int i) {
+    PaItem it;
+    wait(item_full + (i & 1), (i >> 1) & 1);
+    // a wait somewhere gave up: the words may not be there, but every warp still takes the same items,
+    // so that none is left alone at a barrier
+    if (aborted) return my_item(i);
+    const volatile int* w = reinterpret_cast<const volatile int*>(&items[i & 1]);
+    it.n = w[0];
+    it.hp = w[1];
+    it.q0 = w[2];
+    it.lq = w[3];
+    it.k0 = w[4];
+    it.lk = w[5];
+    it.first = w[6];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_empty + (i & 1));
+    return it;
+  };
 
   if (warp == 8) {
-    if (lane == 0 && n > 0) {
-      const uint32_t qbar = CG > 1 ? cluster_addr(q_full, 0) : smem_u32(q_full);
-      const uint32_t kbar = CG > 1 ? cluster_addr(k_full, 0) : smem_u32(k_full);
-      const uint32_t vbar = CG > 1 ? cluster_addr(v_full, 0) : smem_u32(v_full);
-      if (rank == 0) mbar_arrive_expect_tx(q_full, CG * C::kChunks * 128 * p.gp * p.tok);
+    const uint32_t qbar = CG > 1 ? cluster_addr(q_full, 0) : smem_u32(q_full);
+    const uint32_t kbar = CG > 1 ? cluster_addr(k_full, 0) : smem_u32(k_full);
+    const uint32_t vbar = CG > 1 ? cluster_addr(v_full, 0) : smem_u32(v_full);
+    int gt = 0, seg = 0;  // key tiles and items with keys so far
+    for (int i = 0;; ++i) {
+      const PaItem it = my_item(i);
+      if (i >= 2) wait(item_empty + (i & 1), ((i >> 1) - 1) & 1);
+      if (lane == 0) {
+        items[i & 1] = it;
+        mbar_arrive(item_full + (i & 1));
+      }
+      __syncwarp();
+      if (it.n < 0 || aborted) break;
+      if (it.n == 0) continue;
+      if (lane == 0) {
+        const int hk = it.hp / parts, h0 = hk * G + (it.hp % parts) * p.gp;
+        auto load_k = [&](int j) {
+          const int g = gt + j, x = g & 1, row = it.k0 + j * kPaKeys + (int)rank * C::kKRows;
+          if (g >= 2) wait(s_full + x, ((g >> 1) - 1) & 1);  // S of two tiles ago has read its K
+          if (rank == 0) mbar_arrive_expect_tx(k_full + x, CG * C::kTileBytes);
 #pragma unroll
-      for (int c = 0; c < C::kChunks; ++c)
-        tma_load_3d<CG>(base + c * 16384, &tmQ, c * 64, h0, (int)(q0 + t0), qbar);
-      auto load_k = [&](int i) {
-        const int x = i & 1, row = (int)(k0 + (int64_t)i * kPaKeys) + (int)rank * C::kKRows;
-        if (i >= 2) wait(s_full + x, ((i >> 1) - 1) & 1);  // S of two tiles ago has read its K
-        if (rank == 0) mbar_arrive_expect_tx(k_full + x, CG * C::kTileBytes);
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_3d<CG>(base + C::kK + x * C::kTileBytes + c * (C::kKRows * 128), &tmK, c * 64, hk, row, kbar + 8u * x);
+        };
+        auto load_v = [&](int j) {
+          const int g = gt + j, x = g & 1, row = it.k0 + j * kPaKeys;
+          if (g >= 2) wait(o_done + x, ((g >> 1) - 1) & 1);
+          if (rank == 0) mbar_arrive_expect_tx(v_full + x, CG * C::kTileBytes);
+#pragma unroll
+          for (int c = 0; c < C::kVChunks; ++c)
+            tma_load_3d<CG>(base + C::kV + x * C::kTileBytes + c * (kPaKeys * 128), &tmV, ((int)rank * C::kVChunks + c) * 64,
+                            hk, row, vbar + 8u * x);
+        };
+        load_k(0);
+        if (seg > 0) wait(q_empty, (seg - 1) & 1);
+        if (rank == 0) mbar_arrive_expect_tx(q_full, CG * C::kChunks * 128 * p.gp * p.tok);
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c)
-          tma_load_3d<CG>(base + C::kK + x * C::kTileBytes + c * (C::kKRows * 128), &tmK, c * 64, hk, row, kbar + 8u * x);
-      };
-      auto load_v = [&](int i) {
-        const int x = i & 1, row = (int)(k0 + (int64_t)i * kPaKeys);
-        if (i >= 2) wait(o_done + x, ((i >> 1) - 1) & 1);
-        if (rank == 0) mbar_arrive_expect_tx(v_full + x, CG * C::kTileBytes);
-#pragma unroll
-        for (int c = 0; c < C::kVChunks; ++c)
-          tma_load_3d<CG>(base + C::kV + x * C::kTileBytes + c * (kPaKeys * 128), &tmV, ((int)rank * C::kVChunks + c) * 64, hk,
-                          row, vbar + 8u * x);
-      };
-      load_k(0);
-      if (n > 1) load_k(1);
-      for (int i = 0; i < n; ++i) {
-        load_v(i);
-        if (i + 2 < n) load_k(i + 2);
-      }
-      if (aborted) {  // a wait gave up: leave the copies in flight time to land before the CTA ends
-        const uint64_t t = globaltimer_ns();
-        while (globaltimer_ns() - t < 1000000) {
+          tma_load_3d<CG>(base + c * 16384, &tmQ, c * 64, h0, it.q0 + it.first + (int)rank * p.tok, qbar);
+        if (it.n > 1) load_k(1);
+        for (int j = 0; j < it.n; ++j) {
+          load_v(j);
+          if (j + 2 < it.n) load_k(j + 2);
         }
       }
+      __syncwarp();
+      gt += it.n;
+      ++seg;
     }
-    __syncwarp();
+    if (aborted) {  // a wait gave up: leave the copies in flight time to land before the CTA ends
+      const uint64_t t = globaltimer_ns();
+      while (globaltimer_ns() - t < 1000000) {
+      }
+    }
   } else if (warp == 9) {
     // An MMA is issued about when its predecessor starts, so what this thread does between two of them
     // is idle time of the tensor cores: a tile costs it three waits and two commits.
-    if (lane == 0 && rank == 0 && n > 0) {
-      // descriptors of place 0; the address field counts 16 bytes, and no sum carries out of it
-      const uint64_t qdesc = smem_desc_sw128(base, 1024), kdesc = smem_desc_sw128(base + C::kK, 1024);
-      const uint64_t vdesc = smem_desc_mn128(base + C::kV, kPaKeys * 128, 1024);
-      wait(q_full, 0);
-      auto qk = [&](int i) {
-        const int x = i & 1;
-        const uint32_t d = tmem + (uint32_t)x * kPaKeys;
-        const uint64_t kd = kdesc + x * (C::kTileBytes >> 4);
-        wait(k_full + x, (i >> 1) & 1);
-        tmem_fence_after();
+    // descriptors of place 0; the address field counts 16 bytes, and no sum carries out of it
+    const uint64_t qdesc = smem_desc_sw128(base, 1024), kdesc = smem_desc_sw128(base + C::kK, 1024);
+    const uint64_t vdesc = smem_desc_mn128(base + C::kV, kPaKeys * 128, 1024);
+    int gt = 0, seg = 0;
+    for (int i = 0;; ++i) {
+      const PaItem it = next_item(i);
+      if (it.n < 0) break;
+      if (it.n == 0) continue;
+      if (lane == 0 && rank == 0) {
+        wait(q_full, seg & 1);
+        auto qk = [&](int j) {
+          const int x = (gt + j) & 1;
+          const uint32_t d = tmem + (uint32_t)x * kPaKeys;
+          const uint64_t kd = kdesc + x * (C::kTileBytes >> 4);
+          wait(k_full + x, ((gt + j) >> 1) & 1);
+          tmem_fence_after();
 #pragma unroll
-        for (int c = 0; c < C::kChunks; ++c)
+          for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ss<CG>(d, qdesc + c * (16384 >> 4) + kk * 2, kd + c * (C::kKRows * 128 >> 4) + kk * 2, C::kIdescQK,
-                           (c | kk) != 0);
-        mma_commit_cg<CG>(s_full + x);
-      };
-      qk(0);
-      if (n > 1) qk(1);
-      for (int i = 0; i < n; ++i) {
-        const int x = i & 1;
-        const uint32_t pa = tmem + (uint32_t)x * kPaKeys;
-        const uint64_t vd = vdesc + x * (C::kTileBytes >> 4);
-        wait(v_full + x, (i >> 1) & 1);
-        wait_cluster(p_full + x, (i >> 1) & 1);
-        tmem_fence_after();
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ss<CG>(d, qdesc + c * (16384 >> 4) + kk * 2, kd + c * (C::kKRows * 128 >> 4) + kk * 2, C::kIdescQK,
+                             (c | kk) != 0);
+          mma_commit_cg<CG>(s_full + x);
+          if (j + 1 == it.n) mma_commit_cg<CG>(q_empty);
+        };
+        qk(0);
+        if (it.n > 1) qk(1);
+        if (seg > 0) wait_cluster(o_free, (seg - 1) & 1);  // the last item's O has been read
+        for (int j = 0; j < it.n; ++j) {
+          const int x = (gt + j) & 1;
+          const uint32_t pa = tmem + (uint32_t)x * kPaKeys;
+          const uint64_t vd = vdesc + x * (C::kTileBytes >> 4);
+          wait(v_full + x, ((gt + j) >> 1) & 1);
+          wait_cluster(p_full + x, ((gt + j) >> 1) & 1);
+          tmem_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kPaKeys / 16; ++kk)
-          mma_f16_ts<CG>(tmem + C::kTmemO, pa + kk * 8, vd + kk * (2048 >> 4), C::kIdescPV, (i | kk) != 0);
-        mma_commit_cg<CG>(o_done + x);
-        if (i + 2 < n) qk(i + 2);  // over P of this tile, which the MMAs before it have read
+          for (int kk = 0; kk < kPaKeys / 16; ++kk)
+            mma_f16_ts<CG>(tmem + C::kTmemO, pa + kk * 8, vd + kk * (2048 >> 4), C::kIdescPV, (j | kk) != 0);
+          mma_commit_cg<CG>(o_done + x);
+          if (j + 2 < it.n) qk(j + 2);  // over P of this tile, which the MMAs before it have read
+        }
+        mma_commit_cg<CG>(o_last);
       }
-      mma_commit_cg<CG>(o_last);
+      __syncwarp();
+      gt += it.n;
+      ++seg;
     }
-    __syncwarp();
   } else {
     // ---- softmax: thread = row; two groups of four warps take turns at the key tiles
     const int group = warp >> 2, row = tid & 127;
-    const int tr = row / p.gp, head = h0 + row - tr * p.gp;
-    const int64_t tok = t0 + tr;
-    const bool live = b >= 0 && tr < p.tok && tok < lq;
-    int64_t lim64 = live ? tok + lk - lq + 1 : 0;  // keys [0, lim) are visible
-    if (lim64 < 0) lim64 = 0;
+    const int tr = row / p.gp;
     const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);  // lane quarter: 32 lanes, in bits 16..
     const float sc = a.scale_log2;
-    float m = -INFINITY, l = 0.f;  // the group's reference (log2 units after scaling), and its sum
-    const uint32_t pbar0 = CG > 1 ? cluster_addr(p_full, 0) : smem_u32(p_full);
-    for (int i = group; i < n; i += 2) {
-      wait(s_full + group, (i >> 1) & 1);
-      tmem_fence_after();
-      float s[kPaKeys];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(mine + group * kPaKeys + c * 32, s + 32 * c);
-      tmem_wait_ld();
-      const int64_t left = lim64 - (int64_t)i * kPaKeys;
-      if (__any_sync(0xffffffffu, left < kPaKeys)) {
-        const int lim = left < 0 ? 0 : (left > kPaKeys ? kPaKeys : (int)left);
-#pragma unroll
-        for (int c = 0; c < kPaKeys; ++c) s[c] = c < lim ? s[c] : -INFINITY;
+    const uint32_t pbar = (CG > 1 ? cluster_addr(p_full, 0) : smem_u32(p_full)) + 8u * (uint32_t)group;
+    const uint32_t obar = CG > 1 ? cluster_addr(o_free, 0) : smem_u32(o_free);
+    auto sync256 = []() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    int gt = 0, seg = 0;
+    for (int i = 0;; ++i) {
+      const PaItem it = next_item(i);
+      if (it.n < 0) break;
+      const int hk = it.hp / parts, head = hk * G + (it.hp % parts) * p.gp + row - tr * p.gp;
+      const int tok = it.first + (int)rank * p.tok + tr;
+      const bool live = tr < p.tok && tok < it.lq;
+      const int lim = live && tok + it.lk - it.lq + 1 > 0 ? tok + it.lk - it.lq + 1 : 0;  // keys [0, lim) are visible
+      __half* dst = a.o + (((int64_t)it.q0 + tok) * a.Hq + head) * D;
+      if (it.n == 0) {  // no row of the tile sees a key
+        if (live)
+          for (int c = group * (D / 2); c < (group + 1) * (D / 2); c += 8)
+            *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
+        continue;
       }
-      float mx[4];
+      float m = -INFINITY, l = 0.f;  // the group's reference (log2 units after scaling), and its sum
+      for (int j = (gt ^ group) & 1; j < it.n; j += 2) {
+        const int g = gt + j;
+        wait(s_full + group, (g >> 1) & 1);
+        tmem_fence_after();
+        float s[kPaKeys];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) mx[c] = fmaxf(s[c], s[c + 4]);
+        for (int c = 0; c < 4; ++c) tmem_ld32(mine + group * kPaKeys + c * 32, s + 32 * c);
+        tmem_wait_ld();
+        const int left = lim - j * kPaKeys;
+        if (__any_sync(0xffffffffu, left < kPaKeys)) {
 #pragma unroll
-      for (int c = 8; c < kPaKeys; c += 4)
+          for (int c = 0; c < kPaKeys; ++c) s[c] = c < left ? s[c] : -INFINITY;
+        }
+        float mx[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
-      const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-      // the reference of the tile before, from the other group
-      float before = -INFINITY;
-      if (i > 0) {
-        wait(m_full + (group ^ 1) * 4 + (warp & 3), ((i - 1) >> 1) & 1);
-        before = *reinterpret_cast<volatile float*>(&maxima[group ^ 1][row]);
-      }
-      // a new reference only when the old one is 2^8 too small (or there is none yet)
-      const bool grow = tmax > before + 8.f || (before == -INFINITY && tmax > -INFINITY);
-      const float now = grow ? tmax : before;
-      if (i + 1 < n) {
+        for (int c = 0; c < 8; ++c) mx[c] = s[c];
+#pragma unroll
+        for (int c = 8; c < kPaKeys - 8; c += 16)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx[e] = max3(mx[e], s[c + e], s[c + 8 + e]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx[e] = fmaxf(mx[e], s[kPaKeys - 8 + e]);
+        const float tmax = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
+        // the reference of the tile before, from the other group
+        float before = -INFINITY;
+        if (j > 0) {
+          wait(m_full + (group ^ 1) * 4 + (warp & 3), ((g - 1) >> 1) & 1);
+          before = *reinterpret_cast<volatile float*>(&maxima[group ^ 1][row]);
+        }
+        // a new reference only when the old one is 2^8 too small (or there is none yet)
+        const bool grow = tmax > before + 8.f || (before == -INFINITY && tmax > -INFINITY);
+        const float now = grow ? tmax : before;
         maxima[group][row] = now;
         __syncwarp();
         if (lane == 0) mbar_arrive(m_full + group * 4 + (warp & 3));
-      }
-      if (__any_sync(0xffffffffu, grow && i > 0)) {
-        const float f = grow ? (before == -INFINITY ? 0.f : ex2(before - now)) : 1.f;
-        // a parity tells only neighbouring phases apart: tile i - 3's is over, as S of tile i came after
-        // it, and tile i + 1's cannot be over before this warp's part of P is there
-        wait(o_done + (group ^ 1), ((i - 1) >> 1) & 1);
-        tmem_fence_after();
+        if (__any_sync(0xffffffffu, grow && j > 0)) {
+          const float f = grow ? (before == -INFINITY ? 0.f : ex2(before - now)) : 1.f;
+          // a parity tells only neighbouring phases apart: tile g - 3's is over, as S of tile g came after
+          // it, and tile g + 1's cannot be over before this warp's part of P is there
+          wait(o_done + (group ^ 1), ((g - 1) >> 1) & 1);
+          tmem_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(mine + C::kTmemO + c, o);
-          tmem_wait_ld();
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(mine + C::kTmemO + c, o);
+            tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 r = mul_f32x2(make_float2(o[e], o[e + 1]), make_float2(f, f));
-            o[e] = r.x;
-            o[e + 1] = r.y;
+            for (int e = 0; e < 32; e += 2) {
+              const float2 r = mul_f32x2(make_float2(o[e], o[e + 1]), make_float2(f, f));
+              o[e] = r.x;
+              o[e + 1] = r.y;
+            }
+            tmem_st32(mine + C::kTmemO + c, reinterpret_cast<uint32_t(&)[32]>(o));
           }
-          tmem_st32(mine + C::kTmemO + c, reinterpret_cast<uint32_t(&)[32]>(o));
+          tmem_wait_st();
         }
+        if (now != m) l *= m == -INFINITY ? 0.f : ex2(m - now);
+        m = now;
+        const float ms = m == -INFINITY ? 0.f : -m;
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int c = half * 64 + e * 2;
+            float2 x = fma_f32x2(make_float2(s[c], s[c + 1]), make_float2(sc, sc), make_float2(ms, ms));
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            if (e & 1) acc1 = add_f32x2(acc1, x);
+            else acc0 = add_f32x2(acc0, x);
+            pk[e] = pack_half2(x.x, x.y);
+          }
+          tmem_st32(mine + group * kPaKeys + half * 32, pk);
+        }
+        acc0 = add_f32x2(acc0, acc1);
+        l += acc0.x + acc0.y;
         tmem_wait_st();
-      }
-      if (now != m) l *= m == -INFINITY ? 0.f : ex2(m - now);
-      m = now;
-      const float ms = m == -INFINITY ? 0.f : -m;
-      float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int c = half * 64 + e * 2;
-          float2 x = fma_f32x2(make_float2(s[c], s[c + 1]), make_float2(sc, sc), make_float2(ms, ms));
-          x.x = ex2(x.x);
-          x.y = ex2(x.y);
-          if (e & 1) acc1 = add_f32x2(acc1, x);
-          else acc0 = add_f32x2(acc0, x);
-          pk[e] = pack_half2(x.x, x.y);
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG > 1) mbar_arrive_cluster(pbar);
+          else mbar_arrive(p_full + group);
         }
-        tmem_st32(mine + group * kPaKeys + half * 32, pk);
       }
-      acc0 = add_f32x2(acc0, acc1);
-      l += acc0.x + acc0.y;
-      tmem_wait_st();
+      gt += it.n;
+      // ---- O / l -> fp16, half of the columns per group
+      sums[group][row] = make_float2(l, m);
+      sync256();
+      {
+        const float2 other = sums[group ^ 1][row];
+        const float M = fmaxf(m, other.y);  // the last reference: references only grow
+        l = (m == -INFINITY ? l : l * ex2(m - M)) + (other.y == -INFINITY ? other.x : other.x * ex2(other.y - M));
+      }
+      wait(o_last, seg & 1);
+      ++seg;
+      tmem_fence_after();
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      bool odd = false;
+#pragma unroll 1
+      for (int c = group * (D / 2); c < (group + 1) * (D / 2); c += 32) {
+        float o[32];
+        tmem_ld32(mine + C::kTmemO + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (lim > 0) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) odd |= !(fabsf(o[e + x]) < INFINITY);
+            w = make_uint4(pack_half2(o[e] * inv, o[e + 1] * inv), pack_half2(o[e + 2] * inv, o[e + 3] * inv),
+                           pack_half2(o[e + 4] * inv, o[e + 5] * inv), pack_half2(o[e + 6] * inv, o[e + 7] * inv));
+          }
+          if (live) *reinterpret_cast<uint4*>(dst + c + e) = w;
+        }
+      }
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (CG > 1) mbar_arrive_cluster(pbar0 + 8u * (uint32_t)group);
-        else mbar_arrive(p_full + group);
+        if constexpr (CG > 1) mbar_arrive_cluster(obar);
+        else mbar_arrive(o_free);
       }
-    }
-    // ---- O / l -> fp16, half of the columns per group
-    sums[group][row] = make_float2(l, m);
-    auto sync256 = []() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
-    sync256();
-    {
-      const float2 other = sums[group ^ 1][row];
-      const float M = fmaxf(m, other.y);  // the last reference: references only grow
-      l = (m == -INFINITY ? l : l * ex2(m - M)) + (other.y == -INFINITY ? other.x : other.x * ex2(other.y - M));
-    }
-    if (n > 0) {
-      wait(o_last, 0);
-      tmem_fence_after();
-    }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    bool odd = false;
-    __half* dst = a.o + ((q0 + tok) * a.Hq + head) * D;
-#pragma unroll 1
-    for (int c = group * (D / 2); c < (group + 1) * (D / 2); c += 32) {
-      float o[32];
-      if (n > 0) {
-        tmem_ld32(mine + C::kTmemO + c, o);
-        tmem_wait_ld();
+      odd = live && lim > 0 && (odd || !(l < INFINITY));
+      sync256();  // both halves are written before a row is written again; the sums have been read
+      unsigned again = __ballot_sync(0xffffffffu, odd);
+      while (again) {
+        const int r = __ffs(again) - 1;
+        again &= again - 1;
+        const int64_t rt = __shfl_sync(0xffffffffu, (int64_t)it.q0 + tok, r);
+        const int rh = __shfl_sync(0xffffffffu, head, r);
+        const int64_t rl = __shfl_sync(0xffffffffu, lim, r);
+        attend_row<D, false>(a, rt, rh, 0, it.k0, rl, rl, 0, lane);
       }
-#pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (n > 0 && lim64 > 0) {
-#pragma unroll
-          for (int x = 0; x < 8; ++x) odd |= !(fabsf(o[e + x]) < INFINITY);
-          w = make_uint4(pack_half2(o[e] * inv, o[e + 1] * inv), pack_half2(o[e + 2] * inv, o[e + 3] * inv),
-                         pack_half2(o[e + 4] * inv, o[e + 5] * inv), pack_half2(o[e + 6] * inv, o[e + 7] * inv));
-        }
-        if (live) *reinterpret_cast<uint4*>(dst + c + e) = w;
-      }
-    }
-    odd = live && lim64 > 0 && (odd || !(l < INFINITY));
-    sync256();  // both halves are written before a row is written again
-    unsigned again = __ballot_sync(0xffffffffu, odd);
-    while (again) {
-      const int r = __ffs(again) - 1;
-      again &= again - 1;
-      const int64_t rt = __shfl_sync(0xffffffffu, q0 + tok, r);
-      const int rh = __shfl_sync(0xffffffffu, head, r);
-      const int64_t rl = __shfl_sync(0xffffffffu, lim64, r);
-      attend_row<D, false>(a, rt, rh, b, k0, rl, rl, 0, lane);
     }
   }
 
@@ -446,7 +537,7 @@ int token_map(CUtensorMap* m, const __half* p, int64_t tokens, int64_t heads, in
 }
 
 template <int D, int CG>
-static int launch_tiles(const PaArgs& p, int sms_device, cudaStream_t s) {
+static int launch_tiles(const PaArgs& p, int device, int sms, cudaStream_t s) {
   using C = PaCfg<D, CG>;
   const AttnArgs& a = p.a;
   CUtensorMap tq, tk, tv;
@@ -457,13 +548,13 @@ static int launch_tiles(const PaArgs& p, int sms_device, cudaStream_t s) {
   if (rc == TB_OK) rc = token_map(&tv, a.Tk ? a.v : a.q, Tk, a.Hkv, D, a.ldv, 1, kPaKeys);
   if (rc != TB_OK) return rc;
   auto* fn = prompt_attn_kernel<D, CG>;
-  rc = ensure_dynamic_smem(reinterpret_cast<const void*>(fn), sms_device, C::kSmem);
+  rc = ensure_dynamic_smem(reinterpret_cast<const void*>(fn), device, C::kSmem);
   if (rc != TB_OK) return rc;
   const int64_t span = (int64_t)p.tok * CG;
-  const int64_t blocks = (a.T / span + a.B) * p.head_parts * CG;  // at most: ceil(x) <= floor(x) + 1 per request
-  if (blocks > INT32_MAX) return TB_ERR_TOO_LARGE;
+  // at most: ceil(x) <= floor(x) + 1 per request
+  const int64_t most = (a.T / span + a.B) * p.head_parts, clusters = sms / CG < most ? sms / CG : most;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = dim3((unsigned)(clusters * CG));
   cfg.blockDim = dim3(kPaThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
@@ -491,9 +582,9 @@ int launch_prompt_tiles(const AttnArgs& a, int64_t D, cudaStream_t s) {
   p.gp = heads_per_tile(G);
   p.tok = 128 / p.gp;
   p.head_parts = a.Hkv * (G / p.gp);
-  if (D == 64) return launch_tiles<64, 1>(p, f.device, s);
-  if (D == 128) return launch_tiles<128, 2>(p, f.device, s);
-  return launch_tiles<256, 2>(p, f.device, s);
+  if (D == 64) return launch_tiles<64, 1>(p, f.device, f.sms, s);
+  if (D == 128) return launch_tiles<128, 2>(p, f.device, f.sms, s);
+  return launch_tiles<256, 2>(p, f.device, f.sms, s);
 }
 
 }  // namespace tb

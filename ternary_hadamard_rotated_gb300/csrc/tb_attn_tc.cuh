@@ -152,6 +152,11 @@ TB_DEVI float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+TB_DEVI float max3(float x, float y, float z) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
+  return d;
+}
 // two fp32 operations in one instruction
 TB_DEVI float2 fma_f32x2(float2 a, float2 b, float2 c) {
   float2 d;
