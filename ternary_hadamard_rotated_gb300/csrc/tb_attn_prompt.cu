@@ -46,7 +46,8 @@ struct PaCfg {
   static constexpr int kVChunks = kChunks / CG;
   static_assert(kVChunks >= 1, "D = 64 has no pair form");
   static constexpr int kTileBytes = kPaKeys * D * 2 / CG;  // of K, or of V
-  static constexpr int kK = kQBytes, kV = kK + 2 * kTileBytes, kBars = kV + 2 * kTileBytes;  // two of each
+  static constexpr int kK = kQBytes, kV = kK + 2 * kTileBytes, kStage = kV + 2 * kTileBytes;  // two of each
+  static constexpr int kBars = kStage + 8 * 2048;  // a warp's 32 rows of output, 64 bytes of each at a time
   static constexpr int kSmem = 1024 + kBars + 256;
   static constexpr uint32_t kIdescQK = (1u << 4) | ((uint32_t)(kPaKeys >> 3) << 17) | ((uint32_t)(128 * CG >> 4) << 24);
   static constexpr uint32_t kIdescPV =
@@ -58,6 +59,7 @@ struct PaArgs {
   AttnArgs a;
   int gp, tok;      // query heads per tile, tokens per CTA's tile
   int head_parts;   // tiles side by side over the heads: Hkv * (G / gp)
+  unsigned magic;   // for divisions by the tokens of a tile
 };
 
 // a tile of 128 CG rows and what it needs; n < 0: no more of them
@@ -82,57 +84,73 @@ TB_DEVI bool pa_rows(const AttnArgs& a, int b, int& q0, int& lq, int& k0, int& l
   lk = k_ok ? (int)(w - u) : 0;
   return q_ok && k_ok;
 }
-// tiles of a request with more than c key tiles (c = -1: all)
-TB_DEVI int pa_longer(int lq, int lk, int span, int c) {
-  const int tiles = (lq + span - 1) / span;
-  const int64_t x = c < 0 ? -1 : (int64_t)c * kPaKeys - ((int64_t)lk - lq);  // tokens that see at most c tiles of keys
-  return x < 0 ? tiles : (x >= lq ? 0 : tiles - (int)(x / span));
+struct PaSpan {
+  unsigned tokens, magic;  // of a tile, and 2^32 / tokens rounded up (0 for one token)
+};
+TB_DEVI int pa_div(int x, const PaSpan& s) {  // x >= 0
+  if (s.tokens == 1) return x;
+  unsigned q = __umulhi((unsigned)x, s.magic);  // at most one too large
+  if (q * s.tokens > (unsigned)x) --q;
+  return (int)q;
 }
-TB_DEVI PaItem pa_item(const PaArgs& p, int span, int64_t k, int lane) {
+// tiles of a request with more than c key tiles (c = -1: all)
+TB_DEVI int pa_longer(int lq, int lk, const PaSpan& span, int c) {
+  const int tiles = pa_div(lq + (int)span.tokens - 1, span);
+  const int64_t x = c < 0 ? -1 : (int64_t)c * kPaKeys - ((int64_t)lk - lq);  // tokens that see at most c tiles of keys
+  return x < 0 ? tiles : (x >= lq ? 0 : tiles - pa_div((int)x, span));
+}
+// (counts of tiles fit 32 bits: there are no more than tokens and requests together)
+struct PaShare {
+  int per, lq, lk;  // a lane's requests, and the first one's lengths
+};
+TB_DEVI PaShare pa_share(const AttnArgs& a, int lane) {
+  PaShare s;
+  s.per = (a.B + 31) / 32;
+  s.lq = s.lk = 0;
+  int q0, k0;
+  if (lane * s.per < a.B) pa_rows(a, lane * s.per, q0, s.lq, k0, s.lk);
+  return s;
+}
+TB_DEVI PaItem pa_item(const PaArgs& p, const PaShare& sh, const PaSpan& span, unsigned k, int lane) {
   const AttnArgs& a = p.a;
-  const int per = (a.B + 31) / 32;
   PaItem it;
   it.n = -1;
-  it.hp = (int)(k % p.head_parts);
-  const int64_t rank = k / p.head_parts;
+  const int place = (int)(k / (unsigned)p.head_parts);
+  it.hp = (int)(k - (unsigned)place * (unsigned)p.head_parts);
   int q0, lq, k0, lk;
   auto own = [&](int c) {
-    int64_t n = 0;
-    for (int b = lane * per; b < (lane + 1) * per && b < a.B; ++b) {
+    int n = pa_longer(sh.lq, sh.lk, span, c);
+    for (int b = lane * sh.per + 1; b < (lane + 1) * sh.per && b < a.B; ++b) {
       pa_rows(a, b, q0, lq, k0, lk);
       n += pa_longer(lq, lk, span, c);
     }
     return n;
   };
-  auto total = [&](int64_t n) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-    return n;
-  };
-  if (rank >= total(own(-1))) return it;
-  int lo = 0, hi = (int)((a.Tk + kPaKeys - 1) / kPaKeys);  // the least c with at most `rank` longer tiles
+  auto total = [&](int n) { return (int)__reduce_add_sync(0xffffffffu, (unsigned)n); };
+  if (place >= total(own(-1))) return it;
+  int lo = 0, hi = (int)((a.Tk + kPaKeys - 1) / kPaKeys);  // the least c with at most `place` longer tiles
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (total(own(mid)) <= rank) hi = mid;
+    if (total(own(mid)) <= place) hi = mid;
     else lo = mid + 1;
   }
-  const int64_t longer = own(lo), as_long = own(lo - 1) - longer;
-  int64_t upto = as_long;
+  const int longer = own(lo), as_long = own(lo - 1) - longer;
+  int upto = as_long;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+    const int x = __shfl_up_sync(0xffffffffu, upto, d);
     if (lane >= d) upto += x;
   }
-  int64_t r = rank - total(longer);
+  int r = place - total(longer);
   const int src = __ffs(__ballot_sync(0xffffffffu, r < upto)) - 1;
   r -= upto - as_long;  // among the lane's own
-  int b = lane * per, first = 0;
+  int b = lane * sh.per, first = 0;
   if (lane == src) {
     for (;; ++b) {
       pa_rows(a, b, q0, lq, k0, lk);
       const int more = pa_longer(lq, lk, span, lo), same = pa_longer(lq, lk, span, lo - 1) - more;
       if (r < same) {
-        first = ((lq + span - 1) / span - 1 - more - (int)r) * span;  // the longest such tile first
+        first = (pa_div(lq + (int)span.tokens - 1, span) - 1 - more - r) * (int)span.tokens;  // the longest such tile first
         break;
       }
       r -= same;
@@ -225,9 +243,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
     }
   };
-  const int64_t clusters = gridDim.x / CG, me = blockIdx.x / CG;
-  auto my_item = [&](int i) {  // back and forth over the clusters
-    return pa_item(p, p.tok * CG, i * clusters + ((i & 1) ? clusters - 1 - me : me), lane);
+  const unsigned clusters = gridDim.x / CG, me = blockIdx.x / CG;
+  const PaShare share = pa_share(a, lane);
+  const PaSpan span = {(unsigned)(p.tok * CG), p.magic};
+  auto my_item = [&](unsigned i) {  // back and forth over the clusters
+    return pa_item(p, share, span, i * clusters + ((i & 1) ? clusters - 1 - me : me), lane);
   };
   // the words of this CTA's item number i, handed back when the warp has them
   auto next_item = [&](int i) {
@@ -254,8 +274,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const uint32_t kbar = CG > 1 ? cluster_addr(k_full, 0) : smem_u32(k_full);
     const uint32_t vbar = CG > 1 ? cluster_addr(v_full, 0) : smem_u32(v_full);
     int gt = 0, seg = 0;  // key tiles and items with keys so far
+    PaItem it = my_item(0);
     for (int i = 0;; ++i) {
-      const PaItem it = my_item(i);
       if (i >= 2) wait(item_empty + (i & 1), ((i >> 1) - 1) & 1);
       if (lane == 0) {
         items[i & 1] = it;
@@ -263,41 +283,53 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
       __syncwarp();
       if (it.n < 0 || aborted) break;
-      if (it.n == 0) continue;
+      PaItem next;
+      if (it.n == 0) {
+        it = my_item(i + 1);
+        continue;
+      }
+      const int hk = it.hp / parts, h0 = hk * G + (it.hp % parts) * p.gp;
       if (lane == 0) {
-        const int hk = it.hp / parts, h0 = hk * G + (it.hp % parts) * p.gp;
-        auto load_k = [&](int j) {
-          const int g = gt + j, x = g & 1, row = it.k0 + j * kPaKeys + (int)rank * C::kKRows;
-          if (g >= 2) wait(s_full + x, ((g >> 1) - 1) & 1);  // S of two tiles ago has read its K
-          if (rank == 0) mbar_arrive_expect_tx(k_full + x, CG * C::kTileBytes);
-#pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-            tma_load_3d<CG>(base + C::kK + x * C::kTileBytes + c * (C::kKRows * 128), &tmK, c * 64, hk, row, kbar + 8u * x);
-        };
-        auto load_v = [&](int j) {
-          const int g = gt + j, x = g & 1, row = it.k0 + j * kPaKeys;
-          if (g >= 2) wait(o_done + x, ((g >> 1) - 1) & 1);
-          if (rank == 0) mbar_arrive_expect_tx(v_full + x, CG * C::kTileBytes);
-#pragma unroll
-          for (int c = 0; c < C::kVChunks; ++c)
-            tma_load_3d<CG>(base + C::kV + x * C::kTileBytes + c * (kPaKeys * 128), &tmV, ((int)rank * C::kVChunks + c) * 64,
-                            hk, row, vbar + 8u * x);
-        };
-        load_k(0);
         if (seg > 0) wait(q_empty, (seg - 1) & 1);
         if (rank == 0) mbar_arrive_expect_tx(q_full, CG * C::kChunks * 128 * p.gp * p.tok);
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c)
           tma_load_3d<CG>(base + c * 16384, &tmQ, c * 64, h0, it.q0 + it.first + (int)rank * p.tok, qbar);
+      }
+      auto load_k = [&](int j) {
+        const int g = gt + j, x = g & 1, row = it.k0 + j * kPaKeys + (int)rank * C::kKRows;
+        if (g >= 2) wait(s_full + x, ((g >> 1) - 1) & 1);  // S of two tiles ago has read its K
+        if (rank == 0) mbar_arrive_expect_tx(k_full + x, CG * C::kTileBytes);
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+          tma_load_3d<CG>(base + C::kK + x * C::kTileBytes + c * (C::kKRows * 128), &tmK, c * 64, hk, row, kbar + 8u * x);
+      };
+      auto load_v = [&](int j) {
+        const int g = gt + j, x = g & 1, row = it.k0 + j * kPaKeys;
+        if (g >= 2) wait(o_done + x, ((g >> 1) - 1) & 1);
+        if (rank == 0) mbar_arrive_expect_tx(v_full + x, CG * C::kTileBytes);
+#pragma unroll
+        for (int c = 0; c < C::kVChunks; ++c)
+          tma_load_3d<CG>(base + C::kV + x * C::kTileBytes + c * (kPaKeys * 128), &tmV, ((int)rank * C::kVChunks + c) * 64, hk,
+                          row, vbar + 8u * x);
+      };
+      if (lane == 0) {
+        load_k(0);
         if (it.n > 1) load_k(1);
-        for (int j = 0; j < it.n; ++j) {
+        load_v(0);
+      }
+      __syncwarp();
+      next = my_item(i + 1);  // while the tensor cores have something to do
+      if (lane == 0) {
+        for (int j = 1; j < it.n; ++j) {
+          if (j + 1 < it.n) load_k(j + 1);
           load_v(j);
-          if (j + 2 < it.n) load_k(j + 2);
         }
       }
       __syncwarp();
       gt += it.n;
       ++seg;
+      it = next;
     }
     if (aborted) {  // a wait gave up: leave the copies in flight time to land before the CTA ends
       const uint64_t t = globaltimer_ns();
@@ -478,22 +510,44 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       tmem_fence_after();
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       bool odd = false;
+      // through shared memory, so that a store instruction covers eight rows (a thread's own row at a time it
+      // touches 32: 3 us an item)
+      int64_t out[4];  // where the rows that this lane stores begin
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int rr = (warp & 3) * 32 + x * 8 + (lane >> 2), rt = rr / p.gp, rtok = it.first + (int)rank * p.tok + rt;
+        out[x] = rt < p.tok && rtok < it.lq
+                     ? (((int64_t)it.q0 + rtok) * a.Hq + hk * G + (it.hp % parts) * p.gp + rr - rt * p.gp) * D
+                     : -1;
+      }
+      const uint32_t stage = base + C::kStage + (uint32_t)warp * 2048u;
 #pragma unroll 1
       for (int c = group * (D / 2); c < (group + 1) * (D / 2); c += 32) {
         float o[32];
         tmem_ld32(mine + C::kTmemO + c, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint4 w = make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < 4; ++e) {  // (the pieces of neighbouring rows in turn, so that banks differ)
+          uint32_t w[4] = {0, 0, 0, 0};
           if (lim > 0) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) odd |= !(fabsf(o[e + x]) < INFINITY);
-            w = make_uint4(pack_half2(o[e] * inv, o[e + 1] * inv), pack_half2(o[e + 2] * inv, o[e + 3] * inv),
-                           pack_half2(o[e + 4] * inv, o[e + 5] * inv), pack_half2(o[e + 6] * inv, o[e + 7] * inv));
+            for (int y = 0; y < 8; ++y) odd |= !(fabsf(o[e * 8 + y]) < INFINITY);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) w[y] = pack_half2(o[e * 8 + 2 * y] * inv, o[e * 8 + 2 * y + 1] * inv);
           }
-          if (live) *reinterpret_cast<uint4*>(dst + c + e) = w;
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(stage + (uint32_t)lane * 64u +
+                                                                     (((uint32_t)e ^ (((uint32_t)lane >> 1) & 3u)) << 4)),
+                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
         }
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = x * 8 + (lane >> 2), pc = lane & 3;
+          const uint4 w = ld_shared_v4(stage + (uint32_t)r * 64u + (((uint32_t)pc ^ (((uint32_t)r >> 1) & 3u)) << 4));
+          if (out[x] >= 0) *reinterpret_cast<uint4*>(a.o + out[x] + c + pc * 8) = w;
+        }
+        __syncwarp();
       }
       tmem_fence_before();
       __syncwarp();
@@ -537,7 +591,7 @@ int token_map(CUtensorMap* m, const __half* p, int64_t tokens, int64_t heads, in
 }
 
 template <int D, int CG>
-static int launch_tiles(const PaArgs& p, int device, int sms, cudaStream_t s) {
+static int launch_tiles(PaArgs& p, int device, int sms, cudaStream_t s) {
   using C = PaCfg<D, CG>;
   const AttnArgs& a = p.a;
   CUtensorMap tq, tk, tv;
@@ -551,6 +605,7 @@ static int launch_tiles(const PaArgs& p, int device, int sms, cudaStream_t s) {
   rc = ensure_dynamic_smem(reinterpret_cast<const void*>(fn), device, C::kSmem);
   if (rc != TB_OK) return rc;
   const int64_t span = (int64_t)p.tok * CG;
+  p.magic = (unsigned)(((1ull << 32) + span - 1) / span);  // (of one token: overflows, and is not used)
   // at most: ceil(x) <= floor(x) + 1 per request
   const int64_t most = (a.T / span + a.B) * p.head_parts, clusters = sms / CG < most ? sms / CG : most;
   cudaLaunchConfig_t cfg = {};
@@ -581,6 +636,7 @@ int launch_prompt_tiles(const AttnArgs& a, int64_t D, cudaStream_t s) {
   const int G = a.Hq / a.Hkv;
   p.gp = heads_per_tile(G);
   p.tok = 128 / p.gp;
+  p.magic = 0;  // set with the tile's tokens
   p.head_parts = a.Hkv * (G / p.gp);
   if (D == 64) return launch_tiles<64, 1>(p, f.device, f.sms, s);
   if (D == 128) return launch_tiles<128, 2>(p, f.device, f.sms, s);
