@@ -72,7 +72,10 @@ extern "C" int tb_tree_attention(const uint16_t* q, int64_t ldq, int64_t T, int6
     return TB_ERR_SHAPE;
   if (!supported_head(D) || !supported_page(page)) return TB_ERR_UNSUPPORTED;
   if (ldq < Hq * D || ldq % 8 || ldq > kMaxLd) return TB_ERR_SHAPE;
-  if (max_q > 64 || pages * Hkv > INT32_MAX || B * Hq * max_q > INT32_MAX || T * Hq > INT32_MAX) return TB_ERR_TOO_LARGE;
+  // the schedule counts tiles of work, of 128 keys of a request's longest context, in 32 bits
+  if (max_q > 64 || pages * Hkv > INT32_MAX || T * Hq > INT32_MAX ||
+      (double)tree_items(B, max_q, Hq, Hkv) * ((double)max_pages * (double)page / 128 + 1) > INT32_MAX)
+    return TB_ERR_TOO_LARGE;
   if (!(scale > 0.f && scale < INFINITY)) return TB_ERR_VALUE;
   if (T == 0) return TB_OK;
   if (!q || !k_cache || !v_cache || !table || !total || !row_start || !o) return TB_ERR_NULL;

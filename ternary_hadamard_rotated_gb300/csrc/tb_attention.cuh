@@ -90,8 +90,9 @@ int token_map(CUtensorMap* m, const __half* p, int64_t tokens, int64_t heads, in
 // prompt form on the tensor cores
 int launch_prompt_tiles(const AttnArgs& a, int64_t D, cudaStream_t s);
 
-// paged form on the tensor cores, and its workspace
+// paged form on the tensor cores; its items of work at most, and its workspace
 int launch_tree_tiles(const AttnArgs& a, int64_t D, void* workspace, cudaStream_t s);
+int64_t tree_items(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv);
 size_t tree_workspace(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D);
 
 }  // namespace tb

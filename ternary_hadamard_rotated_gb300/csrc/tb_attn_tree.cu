@@ -65,7 +65,7 @@ struct TaSegment {
   int b, hp, rt;
   int tile0, tiles, item_tiles;  // tiles 0: an item whose rows get zeros
   int64_t q0, n, len;            // the request's first row, rows, and cached tokens
-  int64_t item_unit;             // the item's first unit
+  unsigned item_unit;            // the item's first unit
 };
 
 template <int D>
@@ -114,6 +114,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     fence_barrier_init();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 4 && lane < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane == 0 ? &tmQ : (lane == 1 ? &tmK : &tmV)))
+                 : "memory");
   if (warp == 5) tmem_alloc(tmem_slot, 512);
 
   // ---- the schedule: every warp adds up the units of all requests itself
@@ -136,57 +139,62 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       r.bad = 1;
       r.len = 0;
     }
-    r.items = (int)((r.n + p.tok - 1) / p.tok) * p.head_parts;
+    r.items = ((int)r.n + p.tok - 1) / p.tok * p.head_parts;
     const int64_t t = (r.len + kTaKeys - 1) / kTaKeys;
     r.tiles = t > 0 ? (int)t : 1;
     return r;
   };
+  // (units fit 32 bits: the entry point checks that they do at max_q tokens and max_pages a request)
   const int per = (a.B + 31) / 32;
-  int64_t upto = 0, own = 0;
+  unsigned upto = 0, own = 0;
   int any_bad = 0;
   for (int i = lane * per; i < (lane + 1) * per && i < a.B; ++i) {
     const Req r = request(i);
-    own += (int64_t)r.items * r.tiles;
+    own += (unsigned)r.items * (unsigned)r.tiles;
     any_bad |= r.bad;
   }
   upto = own;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+    const unsigned x = __shfl_up_sync(0xffffffffu, upto, d);
     if (lane >= d) upto += x;
   }
-  const int64_t units = __shfl_sync(0xffffffffu, upto, 31);
+  const unsigned units = __shfl_sync(0xffffffffu, upto, 31);
   if (blockIdx.x == 0 && warp == 0 && any_bad) set_status(a.status, TB_DEV_BAD_LEN);
-  const int64_t grid = units < gridDim.x ? units : gridDim.x;  // no CTA of an item is without a unit
-  auto lo_of = [&](int64_t c) { return units * c / grid; };
-  auto owner = [&](int64_t u) { return ((u + 1) * grid - 1) / units; };  // the c with lo_of(c) <= u < lo_of(c + 1)
+  // equal ranges: the first `more` CTAs have one unit more than the others (and no CTA of an item is
+  // without a unit)
+  const unsigned grid = units < gridDim.x ? units : gridDim.x;
+  const unsigned share = grid ? units / grid : 0, more = units - share * grid, big = more * (share + 1);
+  auto lo_of = [&](unsigned c) { return c * share + (c < more ? c : more); };
+  auto owner = [&](unsigned u) { return u < big ? u / (share + 1) : more + (u - big) / share; };
   const bool works = blockIdx.x < grid;
-  const int64_t lo = works ? lo_of(blockIdx.x) : 0, hi = works ? lo_of((int64_t)blockIdx.x + 1) : 0;
+  const unsigned lo = works ? lo_of(blockIdx.x) : 0, hi = works ? lo_of(blockIdx.x + 1) : 0;
   // the segment that starts at unit u (whole warps call this)
-  auto segment = [&](int64_t u) {
+  auto segment = [&](unsigned u) {
     TaSegment s;
     const unsigned who = __ballot_sync(0xffffffffu, u < upto);
     const int src = __ffs(who) - 1;
-    int64_t before = upto - own;
+    unsigned before = upto - own;
     int b = 0;
     if (lane == src) {
       for (b = lane * per;; ++b) {
         const Req r = request(b);
-        if (u < before + (int64_t)r.items * r.tiles) break;
-        before += (int64_t)r.items * r.tiles;
+        const unsigned n = (unsigned)r.items * (unsigned)r.tiles;
+        if (u < before + n) break;
+        before += n;
       }
     }
     b = __shfl_sync(0xffffffffu, b, src);
     before = __shfl_sync(0xffffffffu, before, src);
     const Req r = request(b);
-    const int item = (int)((u - before) / r.tiles);
+    const unsigned item = (u - before) / (unsigned)r.tiles;
     s.b = b;
-    s.hp = item % p.head_parts;
-    s.rt = item / p.head_parts;
-    s.item_unit = before + (int64_t)item * r.tiles;
+    s.rt = (int)(item / (unsigned)p.head_parts);
+    s.hp = (int)item - s.rt * p.head_parts;
+    s.item_unit = before + item * (unsigned)r.tiles;
     s.tile0 = (int)(u - s.item_unit);
     s.item_tiles = r.tiles;
-    s.tiles = (int)(hi - u < r.tiles - s.tile0 ? hi - u : r.tiles - s.tile0);
+    s.tiles = hi - u < (unsigned)(r.tiles - s.tile0) ? (int)(hi - u) : r.tiles - s.tile0;
     s.q0 = r.q0;
     s.n = r.n;
     s.len = r.len;
@@ -235,7 +243,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const int v_slot = lane / (vb * C::kChunks), v_rest = lane - v_slot * (vb * C::kChunks);
     const int v_in = v_rest / C::kChunks * p.vbox, v_c = v_rest % C::kChunks;
     const int v_key = v_slot * C::kVKeys + v_in;
-    for (int64_t u = lo; u < hi;) {
+    for (unsigned u = lo; u < hi;) {
       const TaSegment s = segment(u);
       u += s.tiles;
       if (s.len == 0) continue;
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   } else if (warp == 5) {
     int seg = 0, gt = 0;
     Ring at;
-    for (int64_t u = lo; u < hi;) {
+    for (unsigned u = lo; u < hi;) {
       const TaSegment s = segment(u);
       u += s.tiles;
       if (s.len == 0) continue;
@@ -373,12 +381,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const int tr = row / p.gp;
     int gt = 0, seg = 0;
     int64_t it = 0;  // slots used before this segment
-    for (int64_t u = lo; u < hi;) {
+    for (unsigned u = lo; u < hi;) {
       const TaSegment s = segment(u);
       u += s.tiles;
       if (row == 0 && s.tile0 == 0)  // where the item's parts are, for the joining kernel
         p.meta[((int64_t)s.b * p.head_parts + s.hp) * p.row_tiles + s.rt] =
-            make_int2((int)blockIdx.x, (int)(owner(s.item_unit + s.item_tiles - 1) - blockIdx.x) + 1);
+            make_int2((int)blockIdx.x, (int)(owner(s.item_unit + (unsigned)s.item_tiles - 1) - blockIdx.x) + 1);
       const int hk = s.hp / parts;
       const int head = hk * G + (s.hp % parts) * p.gp + row - tr * p.gp;
       const int64_t tq = (int64_t)s.rt * p.tok + tr;  // token of the request
@@ -595,34 +603,46 @@ __global__ void __launch_bounds__(kTjThreads) tree_join_kernel(const TaArgs p) {
   const int row = (tq - rt * p.tok) * p.gp + (h - hk * G) % p.gp;
   // part i is CTA meta.x + i's: its first segment (0), or for the item's first CTA its last (1)
   auto at = [&](int i) { return (int64_t)(2 * (meta.x + i) + (i == 0)) * p.rows + row; };
-  float M = -INFINITY;
-  for (int i = lane; i < meta.y; i += 32) M = fmaxf(M, __ldcg(p.part_ml + at(i) * 2));
-#pragma unroll
-  for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  float acc[E], L = 0.f;
+  // each warp takes every W-th part with a running maximum; parts without a key have a sum of 0 and
+  // zeros, whatever their weight
+  float acc[E], M = -INFINITY, L = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
   for (int i = warp; i < meta.y; i += W) {
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at(i) * 2));
-    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-    L = fmaf(w, ml.y, L);
     const float* src = p.part_o + at(i) * D + lane * 2;
+    float2 y[E / 2];
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 y = __ldcg(reinterpret_cast<const float2*>(src + e * 32));
-      acc[e] = fmaf(w, y.x, acc[e]);
-      acc[e + 1] = fmaf(w, y.y, acc[e + 1]);
+    for (int e = 0; e < E / 2; ++e) y[e] = __ldcg(reinterpret_cast<const float2*>(src + e * 64));
+    const float m2 = fmaxf(M, ml.x);
+    const float c = M == m2 ? 1.f : ex2(M - m2), w = ml.x == m2 ? 1.f : ex2(ml.x - m2);
+    L = fmaf(w, ml.y, L * c);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      acc[2 * e] = fmaf(w, y[e].x, acc[2 * e] * c);
+      acc[2 * e + 1] = fmaf(w, y[e].y, acc[2 * e + 1] * c);
     }
+    M = m2;
   }
 #pragma unroll
   for (int e = 0; e < E; e += 2)
     *reinterpret_cast<float2*>(&acc_s[warp][e * 32 + lane * 2]) = make_float2(acc[e], acc[e + 1]);
-  if (lane == 0) ml_s[warp][0] = L;
+  if (lane == 0) {
+    ml_s[warp][0] = L;
+    ml_s[warp][1] = M;
+  }
   __syncthreads();
+  M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < W; ++w) M = fmaxf(M, ml_s[w][1]);
+  float f[W];
   L = 0.f;
 #pragma unroll
-  for (int w = 0; w < W; ++w) L += ml_s[w][0];
+  for (int w = 0; w < W; ++w) {
+    f[w] = ml_s[w][1] == M ? 1.f : ex2(ml_s[w][1] - M);
+    L = fmaf(f[w], ml_s[w][0], L);
+  }
   const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
   bool bad = !(L < INFINITY);
   __half* out = a.o + (t * a.Hq + h) * D;
@@ -630,8 +650,8 @@ __global__ void __launch_bounds__(kTjThreads) tree_join_kernel(const TaArgs p) {
     float x = 0.f, y = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      x += acc_s[w][c];
-      y += acc_s[w][c + 1];
+      x = fmaf(f[w], acc_s[w][c], x);
+      y = fmaf(f[w], acc_s[w][c + 1], y);
     }
     bad |= !(fabsf(x) < INFINITY) || !(fabsf(y) < INFINITY);
     *reinterpret_cast<__half2*>(out + c) = __floats2half2_rn(x * inv, y * inv);
@@ -649,10 +669,16 @@ static void tile_shape(int64_t Hq, int64_t Hkv, int64_t max_q, int* gp, int* tok
   if (*tok > max_q) *tok = (int)max_q;
 }
 
+int64_t tree_items(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv) {
+  int gp, tok;
+  tile_shape(Hq, Hkv, max_q, &gp, &tok);
+  return B * Hkv * (Hq / Hkv / gp) * ((max_q + tok - 1) / tok);
+}
+
 size_t tree_workspace(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D) {
   int gp, tok;
   tile_shape(Hq, Hkv, max_q, &gp, &tok);
-  const int64_t items = B * Hkv * (Hq / Hkv / gp) * ((max_q + tok - 1) / tok);
+  const int64_t items = tree_items(B, max_q, Hq, Hkv);
   const int64_t rows = 2 * kTaMaxCtas * (int64_t)gp * tok;
   return (size_t)((items * 8 + 255) / 256 * 256 + rows * 2 * 4 + rows * D * 4);
 }
@@ -705,7 +731,7 @@ int launch_tree_tiles(const AttnArgs& a, int64_t D, void* workspace, cudaStream_
   p.head_parts = a.Hkv * (a.Hq / a.Hkv / p.gp);
   p.row_tiles = (a.max_q + p.tok - 1) / p.tok;
   p.rows = p.gp * p.tok;
-  const int64_t items = (int64_t)a.B * p.head_parts * p.row_tiles;
+  const int64_t items = tree_items(a.B, a.max_q, a.Hq, a.Hkv);
   uint8_t* w = static_cast<uint8_t*>(workspace);
   p.meta = reinterpret_cast<int2*>(w);
   p.part_ml = reinterpret_cast<float*>(w + (items * 8 + 255) / 256 * 256);
