@@ -28,6 +28,7 @@
 // barrier of 800 to 1000 each.)
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math.h>
 
 #include "tb_attention.cuh"
@@ -42,7 +43,9 @@ constexpr int kDcTok = 64;    // tokens per chunk
 constexpr int kDcBlock = kDcTok * 128;  // bytes of a 64 x 64 fp16 image
 // a (chunk, value head) in the workspace: T, P T, T's low part, factors
 constexpr int kDcItem = 3 * kDcBlock + 1024;
-constexpr int kDcFactors = 3 * kDcBlock;  // floats: c [64], w [64], q [64], exp(gamma_C)
+// floats: c [64], w [64], q [64], exp(gamma_C), and the tokens before the first whose k, decay or step
+// is not finite
+constexpr int kDcFactors = 3 * kDcBlock;
 
 struct ChunkArgs {
   DeltaArgs a;
@@ -128,6 +131,7 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
   __shared__ float rk[64], rq[64];
   __shared__ float2 gam[4][64];  // running sums of the decays in log2 units, high and low part
   __shared__ float bet[4][64];
+  __shared__ int sound[4];       // tokens before the first whose k, decay or step is not finite
   __shared__ __align__(16) float diag_t[4][16][20];  // a warp's diagonal block of A, transposed
   __shared__ float diag[4][16][17];                  // its inverse
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -206,7 +210,8 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
       }
     }
     const int r = lane & 15, row = (r & 7) * 8 + (tid >> 4);
-    const float inv = a.normalise ? 1.f / sqrtf(v[0] + kDeltaEps) : 1.f;
+    float inv = a.normalise ? 1.f / sqrtf(v[0] + kDeltaEps) : 1.f;
+    if (!(v[0] < INFINITY)) inv = NAN;
     if (r < 8) rk[row] = inv;
     else rq[row] = inv * a.scale;
   }
@@ -259,12 +264,22 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
       __syncthreads();  // K and Q, and the last four heads' sums, have been read
       if (h4 + warp < group) {  // a warp per head: the decays' sums, of two tokens a lane, as two floats
         float hi[2], lo[2];
+        // From such a token on nothing is computed here (a zero times it would reach the tokens before it);
+        // kernel 2 makes o and the state NaN from there.  A decay of minus infinity forgets, and is sound.
+        unsigned bad[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          bad[e] = __ballot_sync(0xffffffffu, !(next_g[e] < INFINITY) || !(fabsf(next_b[e]) < INFINITY) ||
+                                                  !(rk[lane * 2 + e] < INFINITY));
+        const int f0 = bad[0] ? (__ffs(bad[0]) - 1) * 2 : 64, f1 = bad[1] ? (__ffs(bad[1]) - 1) * 2 + 1 : 64;
+        const int ok = f0 < f1 ? f0 : f1;
+        if (lane == 0) sound[warp] = ok;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float gv = next_g[e] < -200.f ? -200.f : next_g[e];  // e^-200 is 0 in fp32 already
           hi[e] = gv * 1.44269502f;  // times log2 e, in two parts as well
           lo[e] = fmaf(gv, 1.44269502f, -hi[e]) + gv * 1.92596303e-8f;
-          bet[warp][lane * 2 + e] = next_b[e];
+          bet[warp][lane * 2 + e] = lane * 2 + e < ok ? next_b[e] : 0.f;
         }
         add_pair(hi[1], lo[1], hi[0], lo[0]);
         float sh = hi[1], sl = lo[1];
@@ -290,10 +305,13 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
       float* f = reinterpret_cast<float*>(item + kDcFactors);
       const float2 mine = gm[tid], last = gm[63];
       const float eg = ex2(mine.x) * (1.f + 0.6931472f * mine.y);
-      f[tid] = eg * rk[tid];
+      f[tid] = tid < sound[slot] ? eg * rk[tid] : 0.f;  // (0 where kernel 2 has a row of zeros)
       f[64 + tid] = ex2((last.x - mine.x) + (last.y - mine.y)) * rk[tid];
       f[128 + tid] = eg * rq[tid];
-      if (tid == 0) f[192] = ex2(last.x) * (1.f + 0.6931472f * last.y);
+      if (tid == 0) {
+        f[192] = ex2(last.x) * (1.f + 0.6931472f * last.y);
+        f[193] = (float)sound[slot];
+      }
     }
     // A (fp32, as accumulator tiles), P (fp16, as the left factor's tiles)
     float A[8][4];
@@ -301,6 +319,7 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
     {
       const float2 g0 = gm[i0], g1 = gm[i0 + 8];
       const float b0 = be[i0], b1 = be[i0 + 8];
+      const int ok = sound[slot];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (j > 2 * warp + 1) {
@@ -312,9 +331,10 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
         for (int e = 0; e < 4; ++e) {
           const int k = j * 8 + t2 + (e & 1), i = i0 + (e >> 1) * 8;
           const float2 gk = gm[k], gi = (e >> 1) ? g1 : g0;
-          const float d = k <= i ? ex2((gi.x - gk.x) + (gi.y - gk.y)) : 0.f;
-          A[j][e] = k < i ? ((e >> 1) ? b1 : b0) * G[j][e] * d : 0.f;
-          pv[e] = k <= i ? QK[j][e] * d : 0.f;
+          const bool in = i < ok;
+          const float d = in && k <= i ? ex2((gi.x - gk.x) + (gi.y - gk.y)) : 0.f;
+          A[j][e] = in && k < i ? ((e >> 1) ? b1 : b0) * G[j][e] * d : 0.f;
+          pv[e] = in && k <= i ? QK[j][e] * d : 0.f;
         }
         P[j >> 1][(j & 1) * 2] = pack_half2(pv[0], pv[1]);
         P[j >> 1][(j & 1) * 2 + 1] = pack_half2(pv[2], pv[3]);
@@ -465,7 +485,7 @@ constexpr int kD2Threads = (kD2Warps + 1) * 32;
 constexpr int kD2Slices = kDeltaD / (kD2Warps * 16);  // CTAs a head
 constexpr int kD2Stage = kD2V + kDcBlock;
 constexpr int kD2Bytes = 5 * kDcBlock + kDcItem;  // loaded per chunk
-constexpr int kD2Smem = 1024 + kD2Stages * kD2Stage + 128;
+constexpr int kD2Smem = 1024 + kD2Stages * kD2Stage + 512;
 
 // a power of two that takes magnitudes up to `bits` (an fp32's) to 2^14, and its inverse
 TB_DEVI float operand_scale(uint32_t bits, float& inverse) {
@@ -475,6 +495,7 @@ TB_DEVI float operand_scale(uint32_t bits, float& inverse) {
   return __int_as_float(e << 23);
 }
 TB_DEVI uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }  // orders as the values do, NaN last
+constexpr uint32_t kInfBits = 0x7f800000u;
 // Arrival that hands a place back after reads whose values have been used: nothing to release (a release
 // waits for the warp's global stores too, 400 clocks a chunk).
 TB_DEVI void mbar_arrive_reads(uint64_t* bar) {
@@ -490,8 +511,11 @@ __global__ void __launch_bounds__(kD2Threads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = d2_raw + (base - raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kD2Stages * kD2Stage);
-  uint64_t* empty = full + kD2Stages;
-  volatile int* aborted = reinterpret_cast<volatile int*>(full + 2 * kD2Stages);
+  uint64_t* ready = full + kD2Stages;  // the loading warp has looked the stage over
+  uint64_t* empty = full + 2 * kD2Stages;
+  volatile int* aborted = reinterpret_cast<volatile int*>(full + 3 * kD2Stages);
+  // per column of v of this CTA: the request's first token from which o and the state are NaN
+  int* spoilt = reinterpret_cast<int*>(full + 3 * kD2Stages + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slice = (int)(blockIdx.x % kD2Slices);
@@ -512,10 +536,12 @@ __global__ void __launch_bounds__(kD2Threads, 1)
     const unsigned w1 = __ballot_sync(0xffffffffu, lane + 32 < a.B && rank[1] == b);
     b = w0 ? __ffs(w0) - 1 : __ffs(w1) + 31;
   }
+  if (tid < 64) spoilt[tid] = INT_MAX;
   if (tid == 0) {
     *aborted = 0;
     for (int i = 0; i < kD2Stages; ++i) {
       mbar_init(full + i, 1);
+      mbar_init(ready + i, 1);
       mbar_init(empty + i, kD2Warps);
     }
     fence_barrier_init();
@@ -544,8 +570,20 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       for (int i = lane * sc.per; i < b; ++i) first += chunks_of(a, i);
     first = __shfl_sync(0xffffffffu, first, src);
   }
-  if (warp == kD2Warps) {  // loads, a lane per copy
-    for (int c = 0; c < nc; ++c) {
+  const int64_t so = delta_slot(a.slot_out, b, a.n_out, a.status), head_size = (int64_t)a.Hv * kDeltaD * kDeltaD;
+  // at the end of all warps: what is NaN (rarely anything), over what the walk wrote there
+  auto finish = [&]() {
+    __syncthreads();
+    for (int i = warp; i < 64; i += kD2Warps + 1) {
+      const int from = spoilt[i], col = slice * 64 + i;
+      if (from == INT_MAX) continue;
+      for (int64_t t = from + lane; t < len; t += 32) a.o[((t0 + t) * a.Hv + h) * kDeltaD + col] = __float2half_rn(NAN);
+      if (a.state_out && so >= 0)
+        for (int k = lane; k < kDeltaD; k += 32) a.state_out[so * head_size + ((int64_t)h * kDeltaD + k) * kDeltaD + col] = NAN;
+    }
+  };
+  if (warp == kD2Warps) {
+    auto load = [&](int c) {  // a lane per copy
       const int s = c % kD2Stages, row = (int)t0 + c * kDcTok;
       const uint32_t sa = base + s * kD2Stage, bar = smem_u32(full + s);
       if (c >= kD2Stages) wait(empty + s, (c / kD2Stages - 1) & 1);
@@ -560,18 +598,66 @@ __global__ void __launch_bounds__(kD2Threads, 1)
         tma_load_3d<1>(dst, tm, (lane == 5 ? slice : d) * 64, lane == 5 ? h : hk, row, bar);
       }
       __syncwarp();
+    };
+    // What must not meet the zeros of T or of the sums over the tokens is taken out of the stage before the
+    // others see it, and noted: tokens of another request behind the last one, tokens from one on whose k,
+    // decay or step is not finite, and a v that is not.
+    auto look_over = [&](int c) {
+      const int s = c % kD2Stages;
+      const uint32_t st = base + s * kD2Stage;
+      wait(full + s, (c / kD2Stages) & 1);
+      const int left = (int)(len - (int64_t)c * kDcTok < kDcTok ? len - (int64_t)c * kDcTok : kDcTok);
+      const int sound = (int)reinterpret_cast<const float*>(smem + s * kD2Stage + kD2Item + kDcFactors)[193];
+      const int ok = min(left, sound);
+      if (ok < left)
+        for (int i = lane; i < 64; i += 32) atomicMin(spoilt + i, c * kDcTok + ok);
+      if (ok < kDcTok) {
+        for (int i = lane; i < (kDcTok - ok) * 24; i += 32) {  // 16-byte pieces: 16 of K, 8 of V a row
+          const int r = ok + i / 24, x = i % 24;
+          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(st + (x < 16 ? (x >> 3) * kDcBlock : kD2V) + r * 128 +
+                                                                     (x & 7) * 16),
+                       "r"(0)
+                       : "memory");
+        }
+        __syncwarp();
+      }
+      __half2 odd[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};  // 0 times what is not finite is NaN
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        uint4 w = ld_shared_v4(st + kD2V + (i * 32 + lane) * 16);
+        const __half2* hv = reinterpret_cast<const __half2*>(&w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) odd[e & 1] = __hfma2(hv[e], __half2half2(__ushort_as_half(0)), odd[e & 1]);
+      }
+      odd[0] = __hadd2(odd[0], odd[1]);
+      if (__any_sync(0xffffffffu, __hisnan(__low2half(odd[0])) || __hisnan(__high2half(odd[0])))) {
+        for (int i = lane; i < kDcTok * 64; i += 32) {
+          const int r = i >> 6, col = i & 63;
+          __half* v = reinterpret_cast<__half*>(smem + s * kD2Stage + kD2V + r * 128 + (((col >> 3) ^ (r & 7)) << 4)) + (col & 7);
+          if ((__half_as_ushort(*v) & 0x7c00u) == 0x7c00u) {
+            atomicMin(spoilt + col, c * kDcTok + r);
+            *v = __ushort_as_half(0);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ready + s);
+    };
+    for (int c = 0; c <= nc; ++c) {  // a chunk's copies go out before the last one's are looked over
+      if (c < nc) load(c);
+      if (c > 0) look_over(c - 1);
     }
     if (*aborted) {  // a wait gave up: leave the copies in flight time to land before the CTA ends
       const uint64_t t = globaltimer_ns();
       while (globaltimer_ns() - t < 1000000) {
       }
     }
+    finish();
     return;
   }
 
   const int g = lane >> 2, t2 = (lane & 3) * 2;
-  const int64_t si = delta_slot(a.slot_in, b, a.n_in, a.status), so = delta_slot(a.slot_out, b, a.n_out, a.status);
-  const int64_t head_size = (int64_t)a.Hv * kDeltaD * kDeltaD;
+  const int64_t si = delta_slot(a.slot_in, b, a.n_in, a.status);
   const int col = (slice * kD2Warps + warp) * 16;  // the warp's first column of v
   // S^T: rows g, g + 8 (columns of v), columns 8 j + t2, + 1 (of k)
   float S[16][4];
@@ -588,7 +674,13 @@ __global__ void __launch_bounds__(kD2Threads, 1)
 #pragma unroll
   for (int j = 0; j < 16; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sbig[e] = max(sbig[e], magnitude(S[j][e]));
+    for (int e = 0; e < 4; ++e) {
+      if (nc > 0 && magnitude(S[j][e]) >= kInfBits) {  // a column that is NaN from the start
+        atomicMin(&spoilt[warp * 16 + g + (e >> 1) * 8], 0);
+        S[j][e] = 0.f;
+      }
+      sbig[e] = max(sbig[e], magnitude(S[j][e]));
+    }
   // addresses of the ldmatrix lanes inside a 64 x 64 image: rows by the lane, a 16-byte piece per k
   const uint32_t sw = (uint32_t)lane & 7u;
   const uint32_t row_n = (((uint32_t)lane & 7u) + ((uint32_t)lane >> 4) * 8u) * 128u;  // rows are n
@@ -604,15 +696,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
     const int n = (int)(len - (int64_t)c * kDcTok < kDcTok ? len - (int64_t)c * kDcTok : kDcTok);
     float down_s;
     const float up_s = operand_scale(__reduce_max_sync(0xffffffffu, max(max(sbig[0], sbig[1]), max(sbig[2], sbig[3]))), down_s);
-    wait(full + s, (c / kD2Stages) & 1);
-    if (n < kDcTok) {  // the last chunk: rows of K that are another request's, out of the sum over the tokens
-      for (int i = tid; i < (kDcTok - n) * 16; i += kD2Warps * 32) {
-        const int r = n + (i >> 4), x = i & 15;
-        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(K + (x >> 3) * kDcBlock + r * 128 + (x & 7) * 16), "r"(0)
-                     : "memory");
-      }
-      asm volatile("bar.sync 1, %0;" ::"n"(kD2Warps * 32) : "memory");
-    }
+    wait(ready + s, (c / kD2Stages) & 1);
     // A warp has its SM sub-partition to itself, so nothing but its own other work fills the latency of a
     // load or the time of an MMA: loads run a step ahead, and what is not on the way from S to the next
     // S (the products for o, its output) is spread over the steps that are.
@@ -658,8 +742,8 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       auto residual = [&](int q) {  // columns of v g + 8 q
         const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&vv[(ks & 1) * 2 + q]));
         float &x = R[ks][q * 2], &y = R[ks][q * 2 + 1];
-        x = tok < n ? fmaf(-cc.x * down_s, x, w.x) : 0.f;
-        y = tok + 1 < n ? fmaf(-cc.y * down_s, y, w.y) : 0.f;
+        x = fmaf(-cc.x * down_s, x, w.x);
+        y = fmaf(-cc.y * down_s, y, w.y);
         big[q * 2] = max(big[q * 2], magnitude(x));
         big[q * 2 + 1] = max(big[q * 2 + 1], magnitude(y));
       };
@@ -810,6 +894,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
     }
     add_up(7, 0);
     add_up(7, 1);
+    fence_proxy_async_smem();  // this warp's reads before the copy that refills the stage
     __syncwarp();
     if (lane == 0) mbar_arrive_reads(empty + s);
   }
@@ -820,6 +905,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) dst[(j * 8 + (e & 1)) * kDeltaD + (e >> 1) * 8] = S[j][e];
   }
+  finish();
 }
 
 static int launch_scan(const ChunkArgs& p, const DeviceFacts& f, cudaStream_t s) {

@@ -229,3 +229,55 @@ def test_a_step_goes_on_where_a_prompt_ended():
         part(t, t + 1)
     torch.cuda.synchronize()
     check(o, state, (q, k, v, g, beta), lens, init, True)
+
+
+@pytest.mark.parametrize("what", ["v", "k", "g", "beta", "q", "state"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("at", [0, 40, 131])
+def test_what_is_not_finite_stays_behind_its_token(what, bad, at):
+    """The tokens before it, the other requests, the other heads and (for v and a state) the other
+    columns are as without it; from it on its own head (column) is not finite."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    lens, Hk, Hv, req, head, col = [70, 150, 65], 2, 4, 1, 3, 77
+    x = dict(zip(("q", "k", "v", "g", "beta", "state"), make(20, lens, Hk, Hv, True)))
+    row = lens[0] + at
+    T, B = sum(lens), len(lens)
+
+    def call(a):
+        o = torch.empty(T, Hv, D, dtype=torch.float16, device="cuda")
+        out = torch.empty_like(a["state"])
+        tb.tb_gated_delta(a["q"], a["k"], a["v"], a["g"], a["beta"], starts(lens), max(lens), o, workspace(T, B, max(lens), Hk, Hv), state_in=a["state"],
+                          state_out=out, normalise=True)
+        torch.cuda.synchronize()
+        return o, out
+
+    want_o, want_s = call(x)
+    y = {k: v.clone() for k, v in x.items()}
+    if what == "state":
+        y["state"][req, head, 5, col] = bad
+        row = lens[0]
+    elif what == "v":
+        y["v"][row, head, col] = bad
+    elif what in ("g", "beta"):
+        y[what][row, head] = bad
+    else:
+        y[what][row, head // (Hv // Hk), 9] = bad
+    o, s = call(y)
+    touched = torch.zeros(T, Hv, D, dtype=torch.bool, device="cuda")  # what may differ
+    state = torch.zeros(B, Hv, D, D, dtype=torch.bool, device="cuda")
+    end = lens[0] + lens[1]
+    heads = slice(2, 4) if what in ("k", "q") else slice(head, head + 1)
+    if what == "q":
+        touched[row, heads] = True
+    elif what in ("v", "state"):
+        touched[row:end, head, col] = True
+        state[req, head, :, col] = True
+    else:
+        touched[row:end, heads] = True
+        state[req, heads] = True
+    assert torch.equal(o[~touched], want_o[~touched])
+    assert torch.equal(s[~state], want_s[~state])
+    assert not torch.isfinite(o[touched]).any() if bad != bad else not torch.isfinite(o[touched]).all()
+    if what != "q" and bad != bad:
+        assert not torch.isfinite(s[state]).any()
