@@ -21,8 +21,9 @@
 // R^T, (w U)^T, 16 rows) comes out of the product before it in the layout that the next one wants, so
 // a chunk has no exchange between warps at all.  K, Q, V and kernel 1's results come by TMA, three
 // chunks deep.  An fp32 factor goes in as two fp16 terms, x 2^e = hi + lo with the warp's largest |x|
-// at 2^14: 22 bits, and K and Q are fp16 already.  T has two terms too; what goes into o alone has one.
-// About 400 MMAs a warp and chunk, at one per 7.8 clocks and SM sub-partition 1.6 us: what bounds it.
+// at 2^14: 22 bits, and K and Q are fp16 already.  T has two terms too.  What goes into o alone is rounded once:
+// P T, and the state in S^T q, to fp16.
+// About 420 MMAs a warp and chunk, at one per 7.8 clocks and SM sub-partition 1.6 us: what bounds it.
 // (The same walk on tcgen05, 32 columns a CTA, took 2.7 us a chunk alone on its SM and 3.4 with a
 // second CTA: 20 MMAs of 44 to 60 clocks, and three trips through registers, shared memory and a
 // barrier of 800 to 1000 each.)
@@ -313,9 +314,9 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
         f[193] = (float)sound[slot];
       }
     }
-    // A (fp32, as accumulator tiles), P (fp16, as the left factor's tiles)
+    // A (fp32, as accumulator tiles), P (two fp16 terms, as the left factor's tiles)
     float A[8][4];
-    uint32_t P[4][4];
+    uint32_t P[4][4], Pl[4][4];
     {
       const float2 g0 = gm[i0], g1 = gm[i0 + 8];
       const float b0 = be[i0], b1 = be[i0 + 8];
@@ -323,7 +324,6 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (j > 2 * warp + 1) {
-          if ((j & 1) == 0) P[j >> 1][0] = P[j >> 1][1] = P[j >> 1][2] = P[j >> 1][3] = 0;
           continue;
         }
         float pv[4];
@@ -336,8 +336,8 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
           A[j][e] = in && k < i ? ((e >> 1) ? b1 : b0) * G[j][e] * d : 0.f;
           pv[e] = in && k <= i ? QK[j][e] * d : 0.f;
         }
-        P[j >> 1][(j & 1) * 2] = pack_half2(pv[0], pv[1]);
-        P[j >> 1][(j & 1) * 2 + 1] = pack_half2(pv[2], pv[3]);
+        split2(pv[0], pv[1], P[j >> 1][(j & 1) * 2], Pl[j >> 1][(j & 1) * 2]);
+        split2(pv[2], pv[3], P[j >> 1][(j & 1) * 2 + 1], Pl[j >> 1][(j & 1) * 2 + 1]);
       }
     }
     // the diagonal block's inverse
@@ -459,10 +459,16 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
 #pragma unroll
       for (int s = j; s < 4; ++s) {
         if (s > warp) break;
-        uint32_t th[4];
-        ldsm4_trans(smem_u32(img) + (s * 16 + (lane & 15)) * 128 + (((j * 2 + (lane >> 4)) ^ (lane & 7)) << 4), th);
+        uint32_t th[4], tl[4];
+        const uint32_t at = smem_u32(img) + (s * 16 + (lane & 15)) * 128 + (((j * 2 + (lane >> 4)) ^ (lane & 7)) << 4);
+        ldsm4_trans(at, th);
+        ldsm4_trans(at + kDcBlock, tl);
         mma_16816(x[0], P[s], th[0], th[1]);
         mma_16816(x[1], P[s], th[2], th[3]);
+        mma_16816(x[0], P[s], tl[0], tl[1]);
+        mma_16816(x[1], P[s], tl[2], tl[3]);
+        mma_16816(x[0], Pl[s], th[0], th[1]);
+        mma_16816(x[1], Pl[s], th[2], th[3]);
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y)
@@ -820,6 +826,8 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       if (i < 9) ldsm4(at_x(kAt[i + 1][0], kAt[i + 1][1]) + kDcBlock, th[x ^ 1]);
       mma_16816(O[2 * j], rh[ks], th[x][0], th[x][1]);
       mma_16816(O[2 * j + 1], rh[ks], th[x][2], th[x][3]);
+      mma_16816(O[2 * j], rl[ks], th[x][0], th[x][1]);
+      mma_16816(O[2 * j + 1], rl[ks], th[x][2], th[x][3]);
       if (i < 8) {
         const float2 ww = *reinterpret_cast<const float2*>(f + 64 + i * 8 + t2);
         const float wx = ww.x * down_r, wy = ww.y * down_r;
