@@ -101,6 +101,20 @@ TB_DEVI void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = pack_half2(x - f.x, y - f.y);
 }
+// the same of x * scale, y * scale
+TB_DEVI void split2(const float* x, float scale, uint32_t& hi, uint32_t& lo) {
+  const float2 u = mul_f32x2(make_float2(x[0], x[1]), make_float2(scale, scale));
+  const __half2 h = __floats2half2_rn(u.x, u.y);
+  const float2 r = fma_f32x2(__half22float2(h), make_float2(-1.f, -1.f), u);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack_half2(r.x, r.y);
+}
+// two values of a tile's row by their own factors
+TB_DEVI void mul_pair(float* x, float2 f) {
+  const float2 y = mul_f32x2(make_float2(x[0], x[1]), f);
+  x[0] = y.x;
+  x[1] = y.y;
+}
 TB_DEVI uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -493,15 +507,15 @@ constexpr int kD2Stage = kD2V + kDcBlock;
 constexpr int kD2Bytes = 5 * kDcBlock + kDcItem;  // loaded per chunk
 constexpr int kD2Smem = 1024 + kD2Stages * kD2Stage + 512;
 
-// a power of two that takes magnitudes up to `bits` (an fp32's) to 2^14, and its inverse
-TB_DEVI float operand_scale(uint32_t bits, float& inverse) {
+// a power of two that takes the warp's largest magnitude to 2^14, and its inverse
+TB_DEVI float operand_scale(const float (&most)[4], float& inverse) {
+  const float m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+  const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));  // orders as the values do
   int e = 268 - (int)(bits >> 23);
   e = e < 127 - 100 ? 127 - 100 : (e > 127 + 100 ? 127 + 100 : e);
   inverse = __int_as_float((254 - e) << 23);
   return __int_as_float(e << 23);
 }
-TB_DEVI uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }  // orders as the values do, NaN last
-constexpr uint32_t kInfBits = 0x7f800000u;
 // Arrival that hands a place back after reads whose values have been used: nothing to release (a release
 // waits for the warp's global stores too, 400 clocks a chunk).
 TB_DEVI void mbar_arrive_reads(uint64_t* bar) {
@@ -676,16 +690,16 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       for (int e = 0; e < 4; ++e)
         S[j][e] = have ? __ldg(src + (j * 8 + (e & 1)) * kDeltaD + (e >> 1) * 8) : 0.f;
   }
-  uint32_t sbig[4] = {0, 0, 0, 0};  // the largest |S|, four chains of it
+  float sbig[4] = {0.f, 0.f, 0.f, 0.f};  // the largest |S|, four chains of it
 #pragma unroll
   for (int j = 0; j < 16; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if (nc > 0 && magnitude(S[j][e]) >= kInfBits) {  // a column that is NaN from the start
+      if (nc > 0 && !(fabsf(S[j][e]) < INFINITY)) {  // a column that is NaN from the start
         atomicMin(&spoilt[warp * 16 + g + (e >> 1) * 8], 0);
         S[j][e] = 0.f;
       }
-      sbig[e] = max(sbig[e], magnitude(S[j][e]));
+      sbig[e] = fmaxf(sbig[e], fabsf(S[j][e]));
     }
   // addresses of the ldmatrix lanes inside a 64 x 64 image: rows by the lane, a 16-byte piece per k
   const uint32_t sw = (uint32_t)lane & 7u;
@@ -701,7 +715,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
     const float* f = reinterpret_cast<const float*>(smem + s * kD2Stage + kD2Item + kDcFactors);
     const int n = (int)(len - (int64_t)c * kDcTok < kDcTok ? len - (int64_t)c * kDcTok : kDcTok);
     float down_s;
-    const float up_s = operand_scale(__reduce_max_sync(0xffffffffu, max(max(sbig[0], sbig[1]), max(sbig[2], sbig[3]))), down_s);
+    const float up_s = operand_scale(sbig, down_s);
     wait(ready + s, (c / kD2Stages) & 1);
     // A warp has its SM sub-partition to itself, so nothing but its own other work fills the latency of a
     // load or the time of an MMA: loads run a step ahead, and what is not on the way from S to the next
@@ -718,8 +732,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
     for (int j = 0; j < 4; ++j) ldsm4(K + at_n(0) + j * 2048, bk[j]);
     uint32_t lo[2][4];
     auto split_s = [&](int ks, int q) {
-      const float* x = S[2 * ks + (q >> 1)] + (q & 1) * 2;
-      split2(x[0] * up_s, x[1] * up_s, sh[ks][q], lo[ks & 1][q]);
+      split2(S[2 * ks + (q >> 1)] + (q & 1) * 2, up_s, sh[ks][q], lo[ks & 1][q]);
     };
 #pragma unroll
     for (int q = 0; q < 4; ++q) split_s(0, q);
@@ -739,19 +752,22 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       }
     }
     // S^T q, and beside it R = v - exp(gamma) S^T k
-    uint32_t big[4] = {0, 0, 0, 0}, vv[4];
+    float big[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t vv[4];
     ldsm4_trans(V + v_row + v_pc, vv);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
       const int tok = ks * 8 + t2;
       const float2 cc = *reinterpret_cast<const float2*>(f + tok);
+      const float2 cn = mul_f32x2(cc, make_float2(-down_s, -down_s));
       auto residual = [&](int q) {  // columns of v g + 8 q
         const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&vv[(ks & 1) * 2 + q]));
-        float &x = R[ks][q * 2], &y = R[ks][q * 2 + 1];
-        x = fmaf(-cc.x * down_s, x, w.x);
-        y = fmaf(-cc.y * down_s, y, w.y);
-        big[q * 2] = max(big[q * 2], magnitude(x));
-        big[q * 2 + 1] = max(big[q * 2 + 1], magnitude(y));
+        float* x = R[ks] + q * 2;
+        const float2 r = fma_f32x2(cn, make_float2(x[0], x[1]), w);
+        x[0] = r.x;
+        x[1] = r.y;
+        big[q * 2] = fmaxf(big[q * 2], fabsf(r.x));
+        big[q * 2 + 1] = fmaxf(big[q * 2 + 1], fabsf(r.y));
       };
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -764,11 +780,10 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       if ((ks & 1) && ks < 7) ldsm4_trans(V + (ks / 2 + 1) * 2048 + v_row + v_pc, vv);
     }
     float down_r;
-    const float up_r = operand_scale(__reduce_max_sync(0xffffffffu, max(max(big[0], big[1]), max(big[2], big[3]))), down_r);
+    const float up_r = operand_scale(big, down_r);
     uint32_t rh[4][4], rl[4][4];
     auto split_r = [&](int ks, int q) {
-      const float* x = R[2 * ks + (q >> 1)] + (q & 1) * 2;
-      split2(x[0] * up_r, x[1] * up_r, rh[ks][q], rl[ks][q]);
+      split2(R[2 * ks + (q >> 1)] + (q & 1) * 2, up_r, rh[ks][q], rl[ks][q]);
     };
 #pragma unroll
     for (int q = 0; q < 4; ++q) split_r(0, q);
@@ -807,11 +822,9 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       }
       if (i < 8) {
         const float2 qq = *reinterpret_cast<const float2*>(f + 128 + i * 8 + t2);
-        const float qx = qq.x * down_s * up_r, qy = qq.y * down_s * up_r;
-        O[i][0] *= qx;
-        O[i][1] *= qy;
-        O[i][2] *= qx;
-        O[i][3] *= qy;
+        const float2 qs = mul_f32x2(qq, make_float2(down_s * up_r, down_s * up_r));
+        mul_pair(O[i], qs);
+        mul_pair(O[i] + 2, qs);
       }
       mma_16816(U[2 * j], rl[ks], th[x][0], th[x][1]);
       mma_16816(U[2 * j + 1], rl[ks], th[x][2], th[x][3]);
@@ -819,7 +832,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       mma_16816(U[2 * j + 1], rh[ks], tl[x][2], tl[x][3]);
     }
     // w U, and beside it o += P T R
-    big[0] = big[1] = big[2] = big[3] = 0;
+    big[0] = big[1] = big[2] = big[3] = 0.f;
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
       const int ks = kAt[i][0], j = kAt[i][1], x = i & 1;
@@ -830,27 +843,24 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       mma_16816(O[2 * j + 1], rl[ks], th[x][2], th[x][3]);
       if (i < 8) {
         const float2 ww = *reinterpret_cast<const float2*>(f + 64 + i * 8 + t2);
-        const float wx = ww.x * down_r, wy = ww.y * down_r;
-        U[i][0] *= wx;
-        U[i][1] *= wy;
-        U[i][2] *= wx;
-        U[i][3] *= wy;
+        const float2 ws = mul_f32x2(ww, make_float2(down_r, down_r));
+        mul_pair(U[i], ws);
+        mul_pair(U[i] + 2, ws);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) big[e] = max(big[e], magnitude(U[i][e]));
+        for (int e = 0; e < 4; ++e) big[e] = fmaxf(big[e], fabsf(U[i][e]));
       }
     }
     float down_u;
-    const float up_u = operand_scale(__reduce_max_sync(0xffffffffu, max(max(big[0], big[1]), max(big[2], big[3]))), down_u);
+    const float up_u = operand_scale(big, down_u);
     auto split_u = [&](int ks, int q) {
-      const float* x = U[2 * ks + (q >> 1)] + (q & 1) * 2;
-      split2(x[0] * up_u, x[1] * up_u, rh[ks][q], rl[ks][q]);
+      split2(U[2 * ks + (q >> 1)] + (q & 1) * 2, up_u, rh[ks][q], rl[ks][q]);
     };
 #pragma unroll
     for (int q = 0; q < 4; ++q) split_u(0, q);
     // S <- exp(gamma_C) S + K^T (w U); the increment is summed by itself, so that the state's own
     // rounding is one fp32 fma a chunk.  Beside it o goes out, back in rows of tokens.
     const float dec = f[192];
-    sbig[0] = sbig[1] = sbig[2] = sbig[3] = 0;
+    sbig[0] = sbig[1] = sbig[2] = sbig[3] = 0.f;
     auto at_k = [&](int i) {  // step i: 16 columns i / 4 of k, 16 tokens i % 4
       const int j = i >> 2;
       return K + (j >> 2) * kDcBlock + row_k + (((uint32_t)(j & 3) * 2u + pc_k) ^ sw) * 16u + (i & 3) * 2048;
@@ -862,9 +872,15 @@ __global__ void __launch_bounds__(kD2Threads, 1)
     float dh[2][2][4], dl[2][2][4];  // of two steps: one is summed up while the next one's MMAs run
     auto add_up = [&](int j, int x) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        S[2 * j + x][e] = fmaf(dec, S[2 * j + x][e], (dh[j & 1][x][e] + dl[j & 1][x][e]) * down_u);
-        sbig[e] = max(sbig[e], magnitude(S[2 * j + x][e]));
+      for (int e = 0; e < 4; e += 2) {
+        float* y = S[2 * j + x] + e;
+        const float *h = dh[j & 1][x] + e, *l = dl[j & 1][x] + e;
+        const float2 d = add_f32x2(make_float2(h[0], h[1]), make_float2(l[0], l[1]));
+        const float2 r = fma_f32x2(make_float2(dec, dec), make_float2(y[0], y[1]), mul_f32x2(d, make_float2(down_u, down_u)));
+        y[0] = r.x;
+        y[1] = r.y;
+        sbig[e] = fmaxf(sbig[e], fabsf(r.x));
+        sbig[e + 1] = fmaxf(sbig[e + 1], fabsf(r.y));
       }
     };
 #pragma unroll
