@@ -132,62 +132,94 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanArgs
       a.table[(int64_t)b * a.max_pages + p] = f < a.n_free ? __ldg(a.free_pages + f) : -1;
     }
   }
-  // the slots: each thread takes every (grid)-th token; the request by bisection of the sums
-  const int64_t step = (int64_t)gridDim.x * kPlanThreads;
+  // the slots: a run of tokens per warp, so that a lane finds its first token's request by bisection of
+  // the sums and the next ones' by going on from there
   const int64_t have_tok = base_tok < a.T ? base_tok : a.T;
-  for (int64_t t = (int64_t)blockIdx.x * kPlanThreads + tid; t < a.T; t += step) {
+  const int64_t run = ((a.T + warps - 1) / warps + 31) & ~31ll;
+  const int64_t t0 = ((int64_t)blockIdx.x * (kPlanThreads / 32) + warp) * run;
+  const int64_t t1 = t0 + run < a.T ? t0 + run : a.T;
+  const int64_t pmask = (1ll << a.page_log2) - 1;
+  int b = -1;
+  int64_t b_end = 0;  // the request's tokens end here
+  PlanLen l = {0, 0, 0, 0, 0};
+  for (int64_t t = t0 + lane; t < t1; t += 32) {
     int64_t slot = -1;
     if (t < have_tok) {
-      int lo = 0, hi = a.B - 1;  // the last request whose first token is at or before t
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first_tok[mid] <= t) lo = mid;
-        else hi = mid - 1;
+      if (t >= b_end) {
+        int lo = b < 0 ? 0 : b, hi = a.B - 1;
+        if (b < 0) {
+          while (lo < hi) {  // the last request whose first token is at or before t
+            const int mid = (lo + hi + 1) >> 1;
+            if (first_tok[mid] <= t) lo = mid;
+            else hi = mid - 1;
+          }
+        } else {
+          while (lo < hi && first_tok[lo + 1] <= t) ++lo;
+        }
+        b = lo;
+        l = plan_len(a, b);
+        b_end = (int64_t)first_tok[b] + l.fresh;
       }
-      const PlanLen l = plan_len(a, lo);
-      const int64_t pos = (int64_t)l.cached + (t - first_tok[lo]);
+      const int64_t pos = (int64_t)l.cached + (t - first_tok[b]);
       const int64_t p = pos >> a.page_log2;
       int32_t pg = -1;
       if (p < l.have) {
-        pg = a.table[(int64_t)lo * a.max_pages + p];
+        pg = a.table[(int64_t)b * a.max_pages + p];
         if (pg < 0) set_status(a.status, TB_DEV_BAD_SLOT);
       } else if (p < l.need) {
-        const int64_t f = (int64_t)first_new[lo] + (p - l.have);
+        const int64_t f = (int64_t)first_new[b] + (p - l.have);
         if (f < a.n_free) pg = __ldg(a.free_pages + f);
       }
-      if (pg >= 0) slot = ((int64_t)pg << a.page_log2) + (pos & ((1ll << a.page_log2) - 1));
+      if (pg >= 0) slot = ((int64_t)pg << a.page_log2) + (pos & pmask);
     }
     a.slots[t] = slot;
   }
 }
 
 // ---------------------------------------------------------------- write
-// One thread per 16 bytes of a K or V row; rows are contiguous on both sides, so every warp reads
-// and writes whole 512-byte runs (D = 256) or two to four runs of one row each.
-constexpr int kWriteThreads = 256;
+// A warp per token: 16 bytes a lane, four pieces of K and of V in flight, so that a head's row is one
+// contiguous run on both sides.  Bound by the bytes: 40001 tokens of 4 heads of 256 (328 MB) in 51 us.
+constexpr int kWriteThreads = 256, kWriteUnroll = 4;
 
 __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(
     const __half* __restrict__ k, int64_t ldk, const __half* __restrict__ v, int64_t ldv,
     const int64_t* __restrict__ slots, int64_t T, int Hkv, int D, __half* __restrict__ kc,
     __half* __restrict__ vc, int64_t n_slots, int page_log2, int32_t* __restrict__ status) {
-  const int vec = D / 8, row = Hkv * vec;  // 16-byte pieces of a head's row and of a token
-  const int64_t items = T * (int64_t)row;
+  const int lane = threadIdx.x & 31;
+  const unsigned vec = (unsigned)D / 8, row = (unsigned)Hkv * vec;  // 16-byte pieces of a head's row and of a token
   const int64_t pmask = (1ll << page_log2) - 1;
-  for (int64_t i = blockIdx.x * (int64_t)kWriteThreads + threadIdx.x; i < items;
-       i += (int64_t)gridDim.x * kWriteThreads) {
-    const int64_t t = i / row;
-    const int c = (int)(i - t * row), h = c / vec, d = (c - h * vec) * 8;
+  const int64_t step = (int64_t)gridDim.x * (kWriteThreads / 32);
+  for (int64_t t = blockIdx.x * (int64_t)(kWriteThreads / 32) + (threadIdx.x >> 5); t < T; t += step) {
     const int64_t slot = __ldg(slots + t);
     if (slot < 0) continue;  // a padded token
     if (slot >= n_slots) {
-      if (c == 0) set_status(status, TB_DEV_BAD_SLOT);
+      if (lane == 0) set_status(status, TB_DEV_BAD_SLOT);
       continue;
     }
-    const int64_t dst = ((((slot >> page_log2) * Hkv + h) << page_log2) + (slot & pmask)) * D + d;
-    const uint4 kk = *reinterpret_cast<const uint4*>(k + t * ldk + h * D + d);
-    const uint4 vv = *reinterpret_cast<const uint4*>(v + t * ldv + h * D + d);
-    *reinterpret_cast<uint4*>(kc + dst) = kk;
-    *reinterpret_cast<uint4*>(vc + dst) = vv;
+    // head h of the token: page, h, place in the page
+    const int64_t base = ((((slot >> page_log2) * Hkv) << page_log2) + (slot & pmask)) * D;
+    const int64_t head = (int64_t)D << page_log2;
+    const uint4 *ks = reinterpret_cast<const uint4*>(k + t * ldk), *vs = reinterpret_cast<const uint4*>(v + t * ldv);
+    for (unsigned c0 = lane; c0 < row; c0 += 32 * kWriteUnroll) {
+      uint4 kk[kWriteUnroll], vv[kWriteUnroll];
+#pragma unroll
+      for (int u = 0; u < kWriteUnroll; ++u) {
+        const unsigned c = c0 + 32 * u;
+        if (c < row) {
+          kk[u] = __ldcs(ks + c);
+          vv[u] = __ldcs(vs + c);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kWriteUnroll; ++u) {
+        const unsigned c = c0 + 32 * u, h = c / vec;
+        if (c < row) {
+          const int64_t dst = base + h * head + (c - h * vec) * 8;
+          *reinterpret_cast<uint4*>(kc + dst) = kk[u];
+          *reinterpret_cast<uint4*>(vc + dst) = vv[u];
+        }
+      }
+    }
   }
 }
 
@@ -251,8 +283,7 @@ extern "C" int tb_cache_write(const uint16_t* k, int64_t ldk, const uint16_t* v,
   DeviceFacts f;
   int rc = device_facts(&f);
   if (rc != TB_OK) return rc;
-  const int64_t items = T * Hkv * (D / 8);
-  int64_t blocks = (items + kWriteThreads - 1) / kWriteThreads;
+  int64_t blocks = (T + kWriteThreads / 32 - 1) / (kWriteThreads / 32);
   const int64_t cap = (int64_t)f.sms * 8;
   if (blocks > cap) blocks = cap;
   cache_write_kernel<<<(int)blocks, kWriteThreads, 0, static_cast<cudaStream_t>(stream)>>>(
