@@ -140,7 +140,7 @@ static_assert(2 * kD1KQ >= 4 * kDcBlock, "two heads' images take the place of K 
 // block of 16: the diagonal blocks D_w by substitution (a lane per column), then with E = D A (left of
 // the diagonal) T_w = D_w diag(beta) - sum_{s < w} E_ws T_s, one block row a step, fp32 factors in two
 // fp16 terms (three products).  P T goes along, P from Q K^T's accumulators as they are.
-__global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkArgs p) {
+__global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkArgs p) {
   const DeltaArgs& a = p.a;
   __shared__ __align__(1024) uint8_t kq[2 * kD1KQ];
   __shared__ float rk[64], rq[64];
@@ -441,19 +441,30 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
       }
       __syncthreads();
       if (warp <= s) continue;
+      uint32_t th[3][4], tl[3][4];
+      const int x = s < 3 ? s : 0;  // (no warp is past the last step)
+      const uint32_t row = smem_u32(img) + (s * 16 + (lane & 15)) * 128;
 #pragma unroll
-      for (int j = 0; j <= s; ++j) {
-        uint32_t th[4], tl[4];
-        const uint32_t at = smem_u32(img) + (s * 16 + (lane & 15)) * 128 + (((j * 2 + (lane >> 4)) ^ (lane & 7)) << 4);
-        ldsm4_trans(at, th);
-        ldsm4_trans(at + kDcBlock, tl);
-        const int x = s < 3 ? s : 0;  // (no warp is past the last step)
-        mma_16816(T[2 * j], eh[x], th[0], th[1]);
-        mma_16816(T[2 * j + 1], eh[x], th[2], th[3]);
-        mma_16816(T[2 * j], eh[x], tl[0], tl[1]);
-        mma_16816(T[2 * j + 1], eh[x], tl[2], tl[3]);
-        mma_16816(T[2 * j], el[x], th[0], th[1]);
-        mma_16816(T[2 * j + 1], el[x], th[2], th[3]);
+      for (int j = 0; j <= x; ++j) {
+        const uint32_t at = row + (((j * 2 + (lane >> 4)) ^ (lane & 7)) << 4);
+        ldsm4_trans(at, th[j]);
+        ldsm4_trans(at + kDcBlock, tl[j]);
+      }
+      // (term by term over the tiles, so that no product waits for the one before it)
+#pragma unroll
+      for (int j = 0; j <= x; ++j) {
+        mma_16816(T[2 * j], eh[x], th[j][0], th[j][1]);
+        mma_16816(T[2 * j + 1], eh[x], th[j][2], th[j][3]);
+      }
+#pragma unroll
+      for (int j = 0; j <= x; ++j) {
+        mma_16816(T[2 * j], eh[x], tl[j][0], tl[j][1]);
+        mma_16816(T[2 * j + 1], eh[x], tl[j][2], tl[j][3]);
+      }
+#pragma unroll
+      for (int j = 0; j <= x; ++j) {
+        mma_16816(T[2 * j], el[x], th[j][0], th[j][1]);
+        mma_16816(T[2 * j + 1], el[x], th[j][2], th[j][3]);
       }
     }
     // out: T's image as it lies in shared memory, P T from the registers; the blocks above the diagonal
@@ -464,34 +475,37 @@ __global__ void __launch_bounds__(kD1Threads, 3) delta_prep_kernel(const ChunkAr
       *reinterpret_cast<uint4*>(item + o) = *reinterpret_cast<const uint4*>(img + o);
       *reinterpret_cast<uint4*>(item + 2 * kDcBlock + o) = *reinterpret_cast<const uint4*>(img + kDcBlock + o);
     }
+    // P T, in T's registers
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j > warp) break;
-      float x[2][4];
+    for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[0][e] = x[1][e] = 0.f;
+      for (int e = 0; e < 4; ++e) T[j][e] = 0.f;
 #pragma unroll
-      for (int s = j; s < 4; ++s) {
-        if (s > warp) break;
+    for (int s = 0; s < 4; ++s) {
+      if (s > warp) break;
+#pragma unroll
+      for (int j = 0; j <= s; ++j) {
         uint32_t th[4], tl[4];
         const uint32_t at = smem_u32(img) + (s * 16 + (lane & 15)) * 128 + (((j * 2 + (lane >> 4)) ^ (lane & 7)) << 4);
         ldsm4_trans(at, th);
         ldsm4_trans(at + kDcBlock, tl);
-        mma_16816(x[0], P[s], th[0], th[1]);
-        mma_16816(x[1], P[s], th[2], th[3]);
-        mma_16816(x[0], P[s], tl[0], tl[1]);
-        mma_16816(x[1], P[s], tl[2], tl[3]);
-        mma_16816(x[0], Pl[s], th[0], th[1]);
-        mma_16816(x[1], Pl[s], th[2], th[3]);
+        mma_16816(T[2 * j], P[s], th[0], th[1]);
+        mma_16816(T[2 * j + 1], P[s], th[2], th[3]);
+        mma_16816(T[2 * j], P[s], tl[0], tl[1]);
+        mma_16816(T[2 * j + 1], P[s], tl[2], tl[3]);
+        mma_16816(T[2 * j], Pl[s], th[0], th[1]);
+        mma_16816(T[2 * j + 1], Pl[s], th[2], th[3]);
       }
+    }
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+    for (int j = 0; j < 8; ++j) {
+      if (j > 2 * warp + 1) break;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int i = i0 + e * 8;
-          *reinterpret_cast<uint32_t*>(item + kDcBlock + i * 128 + (((2 * j + y) ^ (i & 7)) << 4) + t2 * 2) =
-              pack_half2(x[y][2 * e], x[y][2 * e + 1]);
-        }
+      for (int e = 0; e < 2; ++e) {
+        const int i = i0 + e * 8;
+        *reinterpret_cast<uint32_t*>(item + kDcBlock + i * 128 + ((j ^ (i & 7)) << 4) + t2 * 2) =
+            pack_half2(T[j][2 * e], T[j][2 * e + 1]);
+      }
     }
   }
 }
