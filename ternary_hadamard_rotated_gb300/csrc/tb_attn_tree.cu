@@ -31,7 +31,8 @@ namespace tb {
 constexpr int kTaThreads = 192;
 constexpr int kTaKeys = 128;
 constexpr int kTaSlot = 16384;
-constexpr int kTaRing = 224 * 1024;  // Q and the ring
+constexpr int kTaRing = 208 * 1024;  // Q and the ring
+constexpr int kTaStage = 4 * 4096;   // a warp's 32 rows of output, 32 columns at a time
 constexpr int kTaMaxCtas = 160;  // CTAs the workspace has room for
 
 template <int D>
@@ -42,7 +43,7 @@ struct TaCfg {
   static constexpr int kVSlots = kTaKeys / kVKeys;
   // Q, then the ring: each row of Q that the tile has is there once (in eights), and the MMA's idle
   // rows read on into what follows, so that the ring gets what a full tile of Q would take
-  static constexpr int kSmem = 1024 + kTaRing + 1024;
+  static constexpr int kSmem = 1024 + kTaRing + kTaStage + 1024;
   static int slots(int rows) { return (kTaRing - kChunks * ((rows + 7) / 8 * 1024)) / kTaSlot; }
   static constexpr uint32_t kIdescQK = (1u << 4) | ((uint32_t)(kTaKeys >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
   static constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   const int S = p.slots;
   const uint32_t qchunk = (uint32_t)(p.rows + 7) / 8 * 1024;  // bytes of 64 elements of Q's rows
   const uint32_t ring = base + C::kChunks * qchunk;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kTaRing);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kTaRing + kTaStage);
   uint64_t* full = bars;
   uint64_t* empty = bars + S;
   uint64_t* q_full = bars + 2 * S;
@@ -518,34 +519,57 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       tmem_fence_after();
       const bool whole = s.tiles == s.item_tiles;
       const int64_t slot = (int64_t)blockIdx.x * 2 + (s.tile0 == 0);
-      float* part = p.part_o + (slot * p.rows + row) * D;
       const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+      const bool none = l == 0.f;  // the row saw nothing here: what the MMAs left is 0 times V
       bool odd = !(l < INFINITY);
+      // through shared memory, so that a store instruction covers whole runs of a few rows (a thread's own
+      // row at a time it touches 32: 3 us for 96 rows)
+      const uint32_t stage = base + kTaRing + (uint32_t)warp * 4096u;
+      const unsigned rows = __ballot_sync(0xffffffffu, live);
+      const int64_t begin = dst - a.o;
+      float* part = p.part_o + (slot * p.rows + warp * 32) * D;
+      auto piece = [&](int r, int pc) { return stage + (uint32_t)r * 128u + (((uint32_t)pc ^ ((uint32_t)r & 7u)) << 4); };
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; rows && c < D; c += 32) {
         float o[32];
         tmem_ld32(mine + C::kTmemO + c, o);
         tmem_wait_ld();
-        if (!live) continue;
-        const bool none = l == 0.f;  // the row saw nothing here: what the MMAs left is 0 times V
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e];
         if (whole) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              if (none) o[e + y] = 0.f;
-              odd |= !(fabsf(o[e + y]) < INFINITY);
-            }
-            *reinterpret_cast<uint4*>(dst + c + e) =
-                make_uint4(pack_half2(o[e] * inv, o[e + 1] * inv), pack_half2(o[e + 2] * inv, o[e + 3] * inv),
-                           pack_half2(o[e + 4] * inv, o[e + 5] * inv), pack_half2(o[e + 6] * inv, o[e + 7] * inv));
+            for (int y = 0; y < 8; ++y) odd |= !(fabsf(o[e * 8 + y]) < INFINITY);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) w[y] = pack_half2(o[e * 8 + 2 * y] * inv, o[e * 8 + 2 * y + 1] * inv);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(piece(lane, e)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
+          }
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = x * 8 + (lane >> 2), pc = lane & 3;
+            const uint4 w = ld_shared_v4(piece(r, pc));
+            const int64_t to = __shfl_sync(0xffffffffu, begin, r);
+            if (rows >> r & 1) *reinterpret_cast<uint4*>(a.o + to + c + pc * 8) = w;
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(part + c + e) =
-                none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 8; ++e)
+            asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(piece(lane, e)), "f"(o[e * 4]), "f"(o[e * 4 + 1]),
+                         "f"(o[e * 4 + 2]), "f"(o[e * 4 + 3])
+                         : "memory");
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int r = x * 4 + (lane >> 3), pc = lane & 7;
+            const uint4 w = ld_shared_v4(piece(r, pc));
+            if (rows >> r & 1) *reinterpret_cast<uint4*>(part + r * D + c + pc * 4) = w;
+          }
         }
+        __syncwarp();
       }
       tmem_fence_before();
       __syncwarp();
