@@ -594,14 +594,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 }
 
 // ---------------------------------------------------------------- parts -> output
-// One CTA per (row, head): its warps share the parts of the row's item, the lanes the columns; rows of
-// items that one CTA finished are done already.  The order of the sums is fixed by the schedule.
-constexpr int kTjThreads = 128;
-
-template <int D>
-__global__ void __launch_bounds__(kTjThreads) tree_join_kernel(const TaArgs p) {
+// One CTA of W warps per (row, head): the warps share the parts of the row's item, the lanes the columns;
+// rows of items that one CTA finished are done already.  The order of the sums is fixed by the schedule.
+template <int D, int W>
+__global__ void __launch_bounds__(W * 32) tree_join_kernel(const TaArgs p) {
   const AttnArgs& a = p.a;
-  constexpr int E = D / 32, W = kTjThreads / 32;  // columns of a lane: lane * 2 + 64 i (+ 1)
+  constexpr int E = D / 32;  // columns of a lane: lane * 2 + 64 i (+ 1)
   __shared__ float acc_s[W][D];
   __shared__ float ml_s[W][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -670,7 +668,7 @@ __global__ void __launch_bounds__(kTjThreads) tree_join_kernel(const TaArgs p) {
   const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
   bool bad = !(L < INFINITY);
   __half* out = a.o + (t * a.Hq + h) * D;
-  for (int c = threadIdx.x * 2; c < D; c += kTjThreads * 2) {
+  for (int c = threadIdx.x * 2; c < D; c += W * 64) {
     float x = 0.f, y = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
@@ -727,17 +725,20 @@ static int launch_tree(TaArgs& p, const DeviceFacts& f, cudaStream_t s) {
   tree_attn_kernel<D><<<grid, kTaThreads, C::kSmem, s>>>(tq, tk, tv, p);
   rc = check_launch();
   if (rc != TB_OK) return rc;
-  // the joining kernel starts while the last CTAs still run and waits for them on the device
+  // the joining kernel starts while the last CTAs still run and waits for them on the device.  Sixteen warps
+  // a row while every row has an SM of its own (one context of 4097, 24 rows of 33 parts: 16.5 us with the
+  // parts' kernel, 19.4 with four warps), else four (2304 rows of up to 26 parts: 25.2 and 38.1 us).
+  const bool few = a.T * a.Hq <= f.sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.T * a.Hq));
-  cfg.blockDim = dim3(kTjThreads);
+  cfg.blockDim = dim3(few ? 512 : 128);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, p);
+  const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, tree_join_kernel<D, 16>, p) : cudaLaunchKernelEx(&cfg, tree_join_kernel<D, 4>, p);
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return TB_ERR_CUDA;
