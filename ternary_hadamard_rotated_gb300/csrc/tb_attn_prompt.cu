@@ -100,15 +100,30 @@ TB_DEVI int pa_longer(int lq, int lk, const PaSpan& span, int c) {
   return x < 0 ? tiles : (x >= lq ? 0 : tiles - pa_div((int)x, span));
 }
 // (counts of tiles fit 32 bits: there are no more than tokens and requests together)
+//
+// With more than kPaSorted requests a lane the bisection would cost more than a tile of them; they
+// then go in the order they come in, each one's longest tile first.
+constexpr int kPaSorted = 4;
 struct PaShare {
   int per, lq, lk;  // a lane's requests, and the first one's lengths
+  int own, upto;    // its tiles, and those up to it
 };
-TB_DEVI PaShare pa_share(const AttnArgs& a, int lane) {
+TB_DEVI PaShare pa_share(const AttnArgs& a, const PaSpan& span, int lane) {
   PaShare s;
   s.per = (a.B + 31) / 32;
-  s.lq = s.lk = 0;
-  int q0, k0;
+  s.lq = s.lk = s.own = 0;
+  int q0, k0, lq, lk;
   if (lane * s.per < a.B) pa_rows(a, lane * s.per, q0, s.lq, k0, s.lk);
+  for (int b = lane * s.per; b < (lane + 1) * s.per && b < a.B; ++b) {
+    pa_rows(a, b, q0, lq, k0, lk);
+    s.own += pa_longer(lq, lk, span, -1);
+  }
+  s.upto = s.own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, s.upto, d);
+    if (lane >= d) s.upto += x;
+  }
   return s;
 }
 TB_DEVI PaItem pa_item(const PaArgs& p, const PaShare& sh, const PaSpan& span, unsigned k, int lane) {
@@ -127,7 +142,28 @@ TB_DEVI PaItem pa_item(const PaArgs& p, const PaShare& sh, const PaSpan& span, u
     return n;
   };
   auto total = [&](int n) { return (int)__reduce_add_sync(0xffffffffu, (unsigned)n); };
-  if (place >= total(own(-1))) return it;
+  if (place >= __shfl_sync(0xffffffffu, sh.upto, 31)) return it;
+  if (sh.per > kPaSorted) {
+    const int src = __ffs(__ballot_sync(0xffffffffu, place < sh.upto)) - 1;
+    int b = lane * sh.per, r = place - (sh.upto - sh.own), tile = 0;
+    if (lane == src) {
+      for (;; ++b) {
+        pa_rows(a, b, q0, lq, k0, lk);
+        const int tiles = pa_longer(lq, lk, span, -1);
+        if (r < tiles) {
+          tile = tiles - 1 - r;
+          break;
+        }
+        r -= tiles;
+      }
+    }
+    b = __shfl_sync(0xffffffffu, b, src);
+    it.first = __shfl_sync(0xffffffffu, tile, src) * (int)span.tokens;
+    pa_rows(a, b, it.q0, it.lq, it.k0, it.lk);
+    const int64_t end = it.first + (int64_t)span.tokens, keys = (end < it.lq ? end : it.lq) + (int64_t)it.lk - it.lq;
+    it.n = keys > 0 ? (int)((keys + kPaKeys - 1) / kPaKeys) : 0;
+    return it;
+  }
   int lo = 0, hi = (int)((a.Tk + kPaKeys - 1) / kPaKeys);  // the least c with at most `place` longer tiles
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -244,8 +280,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
   };
   const unsigned clusters = gridDim.x / CG, me = blockIdx.x / CG;
-  const PaShare share = pa_share(a, lane);
   const PaSpan span = {(unsigned)(p.tok * CG), p.magic};
+  const PaShare share = pa_share(a, span, lane);
   auto my_item = [&](unsigned i) {  // back and forth over the clusters
     return pa_item(p, share, span, i * clusters + ((i & 1) ? clusters - 1 - me : me), lane);
   };

@@ -79,6 +79,14 @@ def test_prompt_with_earlier_keys_and_with_too_few(D, ql, kl):
         a += lq
 
 
+@pytest.mark.parametrize("B", [31, 100, 128, 129, 400])
+def test_prompt_many_requests(B):
+    rng = np.random.default_rng(B)
+    ql = rng.integers(0, 70, B).tolist()
+    kl = [q + int(rng.integers(-3, 60)) if q else int(rng.integers(0, 9)) for q in ql]
+    prompt_case(B, ql, [max(0, k) for k in kl], 3, 1, 64 if B == 100 else 128, fused=False)
+
+
 @pytest.mark.parametrize("D", [128, 256])
 def test_prompt_long(D):
     prompt_case(9, [1500, 700], [1500, 700], 3, 1, D, fused=True)
