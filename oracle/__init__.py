@@ -12,6 +12,8 @@ Parity status of each function (what pins it is in tests/test_oracle_pins.py):
   embed_lookup    pinned: forward transform recovers the dequantised row
   pq2_0_*, ptq1_0_*, transcode_to_w2
                   pinned: hand-computed blocks, round trips, invalid values refused
+  mixers          the mixers between the linears (oracle.mixers): pinned by hand-worked cases,
+                  closed forms and identities (tests/test_oracle_mixers.py)
 Parity with the trained model is unpinned (no weights exist here).
 """
 from .w2_hadamard import (GROUP, BITS, CODES_PER_WORD, fwht, pack_w2, unpack_w2,
