@@ -495,7 +495,7 @@ int tb_prompt_attention(const uint16_t* q, int64_t ldq, const uint16_t* k, int64
  *   o        fp16 [T, Hv, D] (out).
  * A request of no tokens copies its state.  States, sums and decays are fp32.  What is not finite in a
  * token's inputs reaches neither the tokens before it nor other requests, and by v no other column;
- * past 8 tokens a request, o and the state are NaN from that token on where it does reach.  D must be 128
+ * with max_len above 16, o and the state are NaN from that token on where it does reach.  D must be 128
  * (TB_ERR_UNSUPPORTED).  workspace: at least tb_gated_delta_workspace_size(T, B, max_len, Hk, Hv)
  * bytes of scratch (may be 0); its contents do not matter; calls that share one are ordered on one
  * stream.  dev_status optional: TB_DEV_BAD_ID (a slot past its pool: taken as negative),

@@ -12,21 +12,23 @@
 // one product [T; P T] R.
 //
 // Kernel 1, a CTA per (chunk, key head), which its value heads share: K K^T and Q K^T by mma.sync (fp16
-// inputs, exact products), per value head the triangular system by substitution in fp32 (a thread
-// per column, the column in registers), P T by mma.sync.  It writes T (fp16, high and low part) and
-// P T (fp16) as the shared-memory image that kernel 2's MMAs read, and each token's factors.
+// inputs, exact products), per value head the triangular system by blocks of 16 and P T.  It writes T
+// (fp16, high and low part) and P T (fp16) as the shared-memory images that kernel 2's MMAs read, and each
+// token's factors.  8192 tokens, 16/48 heads: 107 us, bound by the latency of each head's chain of steps.
 //
 // Kernel 2 walks the chunks, a warp per 16 columns of v, which no other warp's columns depend on: S^T
 // stays in the warp's registers as fp32 accumulators of mma.sync, and every product's left factor (S^T,
 // R^T, (w U)^T, 16 rows) comes out of the product before it in the layout that the next one wants, so
 // a chunk has no exchange between warps at all.  K, Q, V and kernel 1's results come by TMA, three
 // chunks deep.  An fp32 factor goes in as two fp16 terms, x 2^e = hi + lo with the warp's largest |x|
-// at 2^14: 22 bits, and K and Q are fp16 already.  T has two terms too.  What goes into o alone is rounded once:
-// P T, and the state in S^T q, to fp16.
-// About 420 MMAs a warp and chunk, at one per 7.8 clocks and SM sub-partition 1.6 us: what bounds it.
-// (The same walk on tcgen05, 32 columns a CTA, took 2.7 us a chunk alone on its SM and 3.4 with a
-// second CTA: 20 MMAs of 44 to 60 clocks, and three trips through registers, shared memory and a
-// barrier of 800 to 1000 each.)
+// at 2^14: 22 bits, and K and Q are fp16 already.  T has two terms too.  What goes into o alone is rounded
+// once: P T, and the state in S^T q, to fp16.
+// 8192 tokens: 350 us, 2.7 us a chunk.  Its 420 MMAs a warp, at one per 7.8 clocks and SM sub-partition,
+// are 1.7 of them; the rest is the latency of one warp's own chain.  (The same walk on tcgen05, 32
+// columns a CTA, took 2.7 us a chunk alone on its SM and 3.4 with a second CTA, with fewer terms: 20
+// MMAs of 44 to 60 clocks, and three trips through registers, shared memory and a barrier of 800 to
+// 1000 each.)  CTAs stay and take the (request, head, half) items with the most chunks first; the loading
+// warp goes on to the next item's chunks.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -519,7 +521,7 @@ constexpr int kD2Threads = (kD2Warps + 1) * 32;
 constexpr int kD2Slices = kDeltaD / (kD2Warps * 16);  // CTAs a head
 constexpr int kD2Stage = kD2V + kDcBlock;
 constexpr int kD2Bytes = 5 * kDcBlock + kDcItem;  // loaded per chunk
-constexpr int kD2Smem = 1024 + kD2Stages * kD2Stage + 512;
+constexpr int kD2Smem = 1024 + kD2Stages * kD2Stage + 128 + 1024;
 
 // a power of two that takes the warp's largest magnitude to 2^14, and its inverse
 TB_DEVI float operand_scale(const float (&most)[4], float& inverse) {
@@ -548,17 +550,15 @@ __global__ void __launch_bounds__(kD2Threads, 1)
   uint64_t* ready = full + kD2Stages;  // the loading warp has looked the stage over
   uint64_t* empty = full + 2 * kD2Stages;
   volatile int* aborted = reinterpret_cast<volatile int*>(full + 3 * kD2Stages);
-  // per column of v of this CTA: the request's first token from which o and the state are NaN
+  // per column of v of the item, for four items in turn: the request's first token from which o and the
+  // state are NaN (three chunks are under way at most, so four items with chunks)
   int* spoilt = reinterpret_cast<int*>(full + 3 * kD2Stages + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slice = (int)(blockIdx.x % kD2Slices);
-  const int64_t bh = blockIdx.x / kD2Slices;
-  const int h = (int)(bh % a.Hv), hk = h / (a.Hv / a.Hk);
-  int b = (int)(bh / a.Hv);
-  if (a.B > 1 && a.B <= 64) {
-    // the requests with the most chunks first: what comes last then is short.  Each lane ranks two.
-    int mine[2], rank[2] = {0, 0};
+  // the requests with the most chunks first, so that what comes last is short; each lane ranks two
+  int rank[2] = {0, 0};
+  if (a.B <= 64) {
+    int mine[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) mine[e] = lane + 32 * e < a.B ? (int)chunks_of(a, lane + 32 * e) : -1;
     for (int i = 0; i < a.B; ++i) {
@@ -566,11 +566,34 @@ __global__ void __launch_bounds__(kD2Threads, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) rank[e] += other > mine[e] || (other == mine[e] && i < lane + 32 * e);
     }
-    const unsigned w0 = __ballot_sync(0xffffffffu, lane < a.B && rank[0] == b);
-    const unsigned w1 = __ballot_sync(0xffffffffu, lane + 32 < a.B && rank[1] == b);
-    b = w0 ? __ffs(w0) - 1 : __ffs(w1) + 31;
   }
-  if (tid < 64) spoilt[tid] = INT_MAX;
+  // the i-th item of this CTA: a request, a value head and half of its columns; CTAs take turns back and
+  // forth.  False: no more.
+  struct Item {
+    int b, h, slice, nc;
+    int64_t t0, len;
+  };
+  auto item_at = [&](int i, Item& it) {
+    const int64_t k = (int64_t)i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    const int64_t r = k / (a.Hv * kD2Slices);
+    const int rest = (int)(k - r * (a.Hv * kD2Slices));
+    it.h = rest / kD2Slices;
+    it.slice = rest - it.h * kD2Slices;
+    it.b = (int)r;
+    if (r >= a.B) return false;
+    if (a.B <= 64) {
+      const unsigned w0 = __ballot_sync(0xffffffffu, lane < a.B && rank[0] == it.b);
+      const unsigned w1 = __ballot_sync(0xffffffffu, lane + 32 < a.B && rank[1] == it.b);
+      it.b = w0 ? __ffs(w0) - 1 : __ffs(w1) + 31;
+    }
+    if (!delta_rows(a, it.b, it.t0, it.len)) {
+      if (tid == 0 && rest == 0) set_status(a.status, TB_DEV_BAD_LEN);
+      it.len = 0;
+    }
+    it.nc = (int)((it.len + kDcTok - 1) / kDcTok);
+    return true;
+  };
+  for (int i = tid; i < 256; i += kD2Threads) spoilt[i] = INT_MAX;
   if (tid == 0) {
     *aborted = 0;
     for (int i = 0; i < kD2Stages; ++i) {
@@ -580,12 +603,6 @@ __global__ void __launch_bounds__(kD2Threads, 1)
     }
     fence_barrier_init();
   }
-  int64_t t0, len;
-  if (!delta_rows(a, b, t0, len)) {
-    if (tid == 0 && h == 0 && slice == 0) set_status(a.status, TB_DEV_BAD_LEN);
-    len = 0;
-  }
-  const int nc = (int)((len + kDcTok - 1) / kDcTok);
   __syncthreads();
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity) || *aborted) return;
@@ -595,35 +612,17 @@ __global__ void __launch_bounds__(kD2Threads, 1)
     }
   };
 
-  int64_t first = 0;  // the request's first chunk
   if (warp == kD2Warps) {
     const ChunkScan sc = chunk_scan(a, lane);
-    first = sc.upto - sc.own;
-    const int src = b / sc.per;
-    if (lane == src)
-      for (int i = lane * sc.per; i < b; ++i) first += chunks_of(a, i);
-    first = __shfl_sync(0xffffffffu, first, src);
-  }
-  const int64_t so = delta_slot(a.slot_out, b, a.n_out, a.status), head_size = (int64_t)a.Hv * kDeltaD * kDeltaD;
-  // at the end of all warps: what is NaN (rarely anything), over what the walk wrote there
-  auto finish = [&]() {
-    __syncthreads();
-    for (int i = warp; i < 64; i += kD2Warps + 1) {
-      const int from = spoilt[i], col = slice * 64 + i;
-      if (from == INT_MAX) continue;
-      for (int64_t t = from + lane; t < len; t += 32) a.o[((t0 + t) * a.Hv + h) * kDeltaD + col] = __float2half_rn(NAN);
-      if (a.state_out && so >= 0)
-        for (int k = lane; k < kDeltaD; k += 32) a.state_out[so * head_size + ((int64_t)h * kDeltaD + k) * kDeltaD + col] = NAN;
-    }
-  };
-  if (warp == kD2Warps) {
-    auto load = [&](int c) {  // a lane per copy
-      const int s = c % kD2Stages, row = (int)t0 + c * kDcTok;
+    int loaded = 0, looked = 0;  // chunks of all items
+    auto load = [&](const Item& it, int64_t first, int c) {  // a lane per copy
+      const int s = loaded % kD2Stages, row = (int)it.t0 + c * kDcTok;
+      const int h = it.h, hk = h / (a.Hv / a.Hk), slice = it.slice;
       const uint32_t sa = base + s * kD2Stage, bar = smem_u32(full + s);
-      if (c >= kD2Stages) wait(empty + s, (c / kD2Stages - 1) & 1);
+      if (loaded >= kD2Stages) wait(empty + s, (loaded / kD2Stages - 1) & 1);
       if (lane == 0) {
         mbar_arrive_expect_tx(full + s, kD2Bytes);
-        if (c == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1's results
+        if (loaded == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1's results
         bulk_g2s(smem + s * kD2Stage + kD2Item, p.ws + ((first + c) * a.Hv + h) * (int64_t)kDcItem, kDcItem, full + s);
       } else if (lane < 6) {
         const int d = (lane - 1) & 1;
@@ -632,14 +631,16 @@ __global__ void __launch_bounds__(kD2Threads, 1)
         tma_load_3d<1>(dst, tm, (lane == 5 ? slice : d) * 64, lane == 5 ? h : hk, row, bar);
       }
       __syncwarp();
+      ++loaded;
     };
     // What must not meet the zeros of T or of the sums over the tokens is taken out of the stage before the
     // others see it, and noted: tokens of another request behind the last one, tokens from one on whose k,
     // decay or step is not finite, and a v that is not.
-    auto look_over = [&](int c) {
-      const int s = c % kD2Stages;
+    auto look_over = [&](int64_t len, int* spoilt, int c) {
+      const int s = looked % kD2Stages;
       const uint32_t st = base + s * kD2Stage;
-      wait(full + s, (c / kD2Stages) & 1);
+      wait(full + s, (looked / kD2Stages) & 1);
+      ++looked;
       const int left = (int)(len - (int64_t)c * kDcTok < kDcTok ? len - (int64_t)c * kDcTok : kDcTok);
       const int sound = (int)reinterpret_cast<const float*>(smem + s * kD2Stage + kD2Item + kDcFactors)[193];
       const int ok = min(left, sound);
@@ -677,44 +678,37 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(ready + s);
     };
-    for (int c = 0; c <= nc; ++c) {  // a chunk's copies go out before the last one's are looked over
-      if (c < nc) load(c);
-      if (c > 0) look_over(c - 1);
+    // a chunk's copies go out before the last one's are looked over, also from one item to the next
+    Item it;
+    int64_t last_len = 0;
+    int last_c = -1, seg = 0;
+    int* last_spoilt = spoilt;
+    for (int i = 0; item_at(i, it); ++i) {
+      if (it.nc == 0) continue;
+      int64_t first = sc.upto - sc.own;  // the request's first chunk
+      const int src = it.b / sc.per;
+      if (lane == src)
+        for (int r = lane * sc.per; r < it.b; ++r) first += chunks_of(a, r);
+      first = __shfl_sync(0xffffffffu, first, src);
+      for (int c = 0; c < it.nc; ++c) {
+        load(it, first, c);
+        if (last_c >= 0) look_over(last_len, last_spoilt, last_c);
+        last_c = c;
+        last_len = it.len;
+        last_spoilt = spoilt + (seg & 3) * 64;
+      }
+      ++seg;
     }
+    if (last_c >= 0) look_over(last_len, last_spoilt, last_c);
     if (*aborted) {  // a wait gave up: leave the copies in flight time to land before the CTA ends
       const uint64_t t = globaltimer_ns();
       while (globaltimer_ns() - t < 1000000) {
       }
     }
-    finish();
     return;
   }
 
   const int g = lane >> 2, t2 = (lane & 3) * 2;
-  const int64_t si = delta_slot(a.slot_in, b, a.n_in, a.status);
-  const int col = (slice * kD2Warps + warp) * 16;  // the warp's first column of v
-  // S^T: rows g, g + 8 (columns of v), columns 8 j + t2, + 1 (of k)
-  float S[16][4];
-  {
-    const bool have = a.state_in && si >= 0;
-    const float* src = a.state_in + si * head_size + ((int64_t)h * kDeltaD + t2) * kDeltaD + col + g;
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        S[j][e] = have ? __ldg(src + (j * 8 + (e & 1)) * kDeltaD + (e >> 1) * 8) : 0.f;
-  }
-  float sbig[4] = {0.f, 0.f, 0.f, 0.f};  // the largest |S|, four chains of it
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (nc > 0 && !(fabsf(S[j][e]) < INFINITY)) {  // a column that is NaN from the start
-        atomicMin(&spoilt[warp * 16 + g + (e >> 1) * 8], 0);
-        S[j][e] = 0.f;
-      }
-      sbig[e] = fmaxf(sbig[e], fabsf(S[j][e]));
-    }
   // addresses of the ldmatrix lanes inside a 64 x 64 image: rows by the lane, a 16-byte piece per k
   const uint32_t sw = (uint32_t)lane & 7u;
   const uint32_t row_n = (((uint32_t)lane & 7u) + ((uint32_t)lane >> 4) * 8u) * 128u;  // rows are n
@@ -723,227 +717,272 @@ __global__ void __launch_bounds__(kD2Threads, 1)
   const uint32_t v_row = ((((uint32_t)lane >> 4) & 1u) * 8u + sw) * 128u;
   const uint32_t v_pc = (((uint32_t)warp * 2u + pc_n) ^ sw) << 4;
 
-  for (int c = 0; c < nc; ++c) {
-    const int s = c % kD2Stages;
-    const uint32_t K = base + s * kD2Stage, Q = K + kD2Q, X = K + kD2Item, V = K + kD2V;
-    const float* f = reinterpret_cast<const float*>(smem + s * kD2Stage + kD2Item + kDcFactors);
-    const int n = (int)(len - (int64_t)c * kDcTok < kDcTok ? len - (int64_t)c * kDcTok : kDcTok);
-    float down_s;
-    const float up_s = operand_scale(sbig, down_s);
-    wait(ready + s, (c / kD2Stages) & 1);
-    // A warp has its SM sub-partition to itself, so nothing but its own other work fills the latency of a
-    // load or the time of an MMA: loads run a step ahead, and what is not on the way from S to the next
-    // S (the products for o, its output) is spread over the steps that are.
-    float R[8][4], O[8][4];
+  int done = 0, seg = 0;  // chunks of all items, items with chunks
+  Item it;
+  for (int i = 0; item_at(i, it); ++i) {
+    const int h = it.h, nc = it.nc;
+    const int64_t t0 = it.t0, len = it.len, head_size = (int64_t)a.Hv * kDeltaD * kDeltaD;
+    const int col = (it.slice * kD2Warps + warp) * 16;  // the warp's first column of v
+    int* mine = spoilt + (seg & 3) * 64 + warp * 16;
+    // S^T: rows g, g + 8 (columns of v), columns 8 j + t2, + 1 (of k)
+    float S[16][4];
+    {
+      const int64_t si = delta_slot(a.slot_in, it.b, a.n_in, a.status);
+      const bool have = a.state_in && si >= 0;
+      const float* src = a.state_in + si * head_size + ((int64_t)h * kDeltaD + t2) * kDeltaD + col + g;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 16; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) R[j][e] = O[j][e] = 0.f;
-    auto at_n = [&](int ks) { return (ks >> 2) * kDcBlock + row_n + (((uint32_t)(ks & 3) * 2u + pc_n) ^ sw) * 16u; };
-    uint32_t bk[4][4], sh[8][4];
-    // S^T k
-#pragma unroll
-    for (int j = 0; j < 4; ++j) ldsm4(K + at_n(0) + j * 2048, bk[j]);
-    uint32_t lo[2][4];
-    auto split_s = [&](int ks, int q) {
-      split2(S[2 * ks + (q >> 1)] + (q & 1) * 2, up_s, sh[ks][q], lo[ks & 1][q]);
-    };
-#pragma unroll
-    for (int q = 0; q < 4; ++q) split_s(0, q);
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        mma_16816(R[2 * j], sh[ks], bk[j][0], bk[j][1]);
-        if (ks < 7) split_s(ks + 1, j);
-        mma_16816(R[2 * j + 1], sh[ks], bk[j][2], bk[j][3]);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        mma_16816(R[2 * j], lo[ks & 1], bk[j][0], bk[j][1]);
-        mma_16816(R[2 * j + 1], lo[ks & 1], bk[j][2], bk[j][3]);
-        ldsm4((ks < 7 ? K + at_n(ks + 1) : Q + at_n(0)) + j * 2048, bk[j]);
-      }
+        for (int e = 0; e < 4; ++e)
+          S[j][e] = have ? __ldg(src + (j * 8 + (e & 1)) * kDeltaD + (e >> 1) * 8) : 0.f;
     }
-    // S^T q, and beside it R = v - exp(gamma) S^T k
-    float big[4] = {0.f, 0.f, 0.f, 0.f};
-    uint32_t vv[4];
-    ldsm4_trans(V + v_row + v_pc, vv);
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      const int tok = ks * 8 + t2;
-      const float2 cc = *reinterpret_cast<const float2*>(f + tok);
-      const float2 cn = mul_f32x2(cc, make_float2(-down_s, -down_s));
-      auto residual = [&](int q) {  // columns of v g + 8 q
-        const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&vv[(ks & 1) * 2 + q]));
-        float* x = R[ks] + q * 2;
-        const float2 r = fma_f32x2(cn, make_float2(x[0], x[1]), w);
-        x[0] = r.x;
-        x[1] = r.y;
-        big[q * 2] = fmaxf(big[q * 2], fabsf(r.x));
-        big[q * 2 + 1] = fmaxf(big[q * 2 + 1], fabsf(r.y));
-      };
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        mma_16816(O[2 * j], sh[ks], bk[j][0], bk[j][1]);
-        if (j == 1) residual(0);
-        if (j == 2) residual(1);
-        mma_16816(O[2 * j + 1], sh[ks], bk[j][2], bk[j][3]);
-        if (ks < 7) ldsm4(Q + at_n(ks + 1) + j * 2048, bk[j]);
-      }
-      if ((ks & 1) && ks < 7) ldsm4_trans(V + (ks / 2 + 1) * 2048 + v_row + v_pc, vv);
-    }
-    float down_r;
-    const float up_r = operand_scale(big, down_r);
-    uint32_t rh[4][4], rl[4][4];
-    auto split_r = [&](int ks, int q) {
-      split2(R[2 * ks + (q >> 1)] + (q & 1) * 2, up_r, rh[ks][q], rl[ks][q]);
-    };
-#pragma unroll
-    for (int q = 0; q < 4; ++q) split_r(0, q);
-    // U = T R (rows past a token do not reach it: their tiles are left out); o's first part to R's scale
-    float U[8][4];
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) U[nt][e] = 0.f;
-    auto at_x = [&](int ks, int j) { return X + row_n + (((uint32_t)ks * 2u + pc_n) ^ sw) * 16u + j * 2048; };
-    constexpr int kAt[11][2] = {{0, 0}, {0, 1}, {0, 2}, {0, 3}, {1, 1}, {1, 2}, {1, 3}, {2, 2}, {2, 3}, {3, 3}, {3, 3}};
-    uint32_t th[2][4], tl[2][4];
-    ldsm4(at_x(0, 0), th[0]);
-    ldsm4(at_x(0, 0) + 2 * kDcBlock, tl[0]);
-#pragma unroll
-    for (int i = 0; i < 10; ++i) {
-      const int ks = kAt[i][0], j = kAt[i][1], x = i & 1;
-      const uint32_t at = at_x(kAt[i + 1][0], kAt[i + 1][1]);
-      if (i < 9) {
-        ldsm4(at, th[x ^ 1]);
-        ldsm4(at + 2 * kDcBlock, tl[x ^ 1]);
-      } else {
-        ldsm4(at_x(0, 0) + kDcBlock, th[x ^ 1]);  // P T's first
-      }
-      mma_16816(U[2 * j], rh[ks], th[x][0], th[x][1]);
-      mma_16816(U[2 * j + 1], rh[ks], th[x][2], th[x][3]);
-      // R's later terms, a step or more ahead of their first use
-      if (i < 4) split_r(1, i);
-      if (i >= 4 && i < 6) {
-        split_r(2, (i - 4) * 2);
-        split_r(2, (i - 4) * 2 + 1);
-      }
-      if (i >= 6 && i < 8) {
-        split_r(3, (i - 6) * 2);
-        split_r(3, (i - 6) * 2 + 1);
-      }
-      if (i < 8) {
-        const float2 qq = *reinterpret_cast<const float2*>(f + 128 + i * 8 + t2);
-        const float2 qs = mul_f32x2(qq, make_float2(down_s * up_r, down_s * up_r));
-        mul_pair(O[i], qs);
-        mul_pair(O[i] + 2, qs);
-      }
-      mma_16816(U[2 * j], rl[ks], th[x][0], th[x][1]);
-      mma_16816(U[2 * j + 1], rl[ks], th[x][2], th[x][3]);
-      mma_16816(U[2 * j], rh[ks], tl[x][0], tl[x][1]);
-      mma_16816(U[2 * j + 1], rh[ks], tl[x][2], tl[x][3]);
-    }
-    // w U, and beside it o += P T R
-    big[0] = big[1] = big[2] = big[3] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 10; ++i) {
-      const int ks = kAt[i][0], j = kAt[i][1], x = i & 1;
-      if (i < 9) ldsm4(at_x(kAt[i + 1][0], kAt[i + 1][1]) + kDcBlock, th[x ^ 1]);
-      mma_16816(O[2 * j], rh[ks], th[x][0], th[x][1]);
-      mma_16816(O[2 * j + 1], rh[ks], th[x][2], th[x][3]);
-      mma_16816(O[2 * j], rl[ks], th[x][0], th[x][1]);
-      mma_16816(O[2 * j + 1], rl[ks], th[x][2], th[x][3]);
-      if (i < 8) {
-        const float2 ww = *reinterpret_cast<const float2*>(f + 64 + i * 8 + t2);
-        const float2 ws = mul_f32x2(ww, make_float2(down_r, down_r));
-        mul_pair(U[i], ws);
-        mul_pair(U[i] + 2, ws);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) big[e] = fmaxf(big[e], fabsf(U[i][e]));
-      }
-    }
-    float down_u;
-    const float up_u = operand_scale(big, down_u);
-    auto split_u = [&](int ks, int q) {
-      split2(U[2 * ks + (q >> 1)] + (q & 1) * 2, up_u, rh[ks][q], rl[ks][q]);
-    };
-#pragma unroll
-    for (int q = 0; q < 4; ++q) split_u(0, q);
-    // S <- exp(gamma_C) S + K^T (w U); the increment is summed by itself, so that the state's own
-    // rounding is one fp32 fma a chunk.  Beside it o goes out, back in rows of tokens.
-    const float dec = f[192];
-    sbig[0] = sbig[1] = sbig[2] = sbig[3] = 0.f;
-    auto at_k = [&](int i) {  // step i: 16 columns i / 4 of k, 16 tokens i % 4
-      const int j = i >> 2;
-      return K + (j >> 2) * kDcBlock + row_k + (((uint32_t)(j & 3) * 2u + pc_k) ^ sw) * 16u + (i & 3) * 2048;
-    };
-    __half* dst = a.o + ((t0 + (int64_t)c * kDcTok + g) * a.Hv + h) * kDeltaD + col + t2;
-    const int64_t step = (int64_t)8 * a.Hv * kDeltaD;
-    uint32_t kt[2][4];
-    ldsm4_trans(at_k(0), kt[0]);
-    float dh[2][2][4], dl[2][2][4];  // of two steps: one is summed up while the next one's MMAs run
-    auto add_up = [&](int j, int x) {
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        float* y = S[2 * j + x] + e;
-        const float *h = dh[j & 1][x] + e, *l = dl[j & 1][x] + e;
-        const float2 d = add_f32x2(make_float2(h[0], h[1]), make_float2(l[0], l[1]));
-        const float2 r = fma_f32x2(make_float2(dec, dec), make_float2(y[0], y[1]), mul_f32x2(d, make_float2(down_u, down_u)));
-        y[0] = r.x;
-        y[1] = r.y;
-        sbig[e] = fmaxf(sbig[e], fabsf(r.x));
-        sbig[e + 1] = fmaxf(sbig[e + 1], fabsf(r.y));
-      }
-    };
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int z = j & 1;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) dh[z][0][e] = dh[z][1][e] = dl[z][0][e] = dl[z][1][e] = 0.f;
-      uint32_t ox = 0, oy = 0;
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const int i = j * 4 + ks, x = i & 1;
-        if (i < 31) ldsm4_trans(at_k(i + 1), kt[x ^ 1]);
-        mma_16816(dh[z][0], rh[ks], kt[x][0], kt[x][1]);
-        if (j == 0 && ks < 3) {
-          split_u(ks + 1, 0);
-          split_u(ks + 1, 1);
-        }
-        if (j > 0 && ks == 1) add_up(j - 1, 0);
-        mma_16816(dh[z][1], rh[ks], kt[x][2], kt[x][3]);
-        if (j == 0 && ks < 3) {
-          split_u(ks + 1, 2);
-          split_u(ks + 1, 3);
-        }
-        if (j > 0 && ks == 2) add_up(j - 1, 1);
-        mma_16816(dl[z][0], rl[ks], kt[x][0], kt[x][1]);
-        if (ks == 0) ox = transpose8x8(pack_half2(O[j][0] * down_r, O[j][1] * down_r));
-        if (ks == 1) oy = transpose8x8(pack_half2(O[j][2] * down_r, O[j][3] * down_r));
-        mma_16816(dl[z][1], rl[ks], kt[x][2], kt[x][3]);
-      }
-      if (j * 8 + g < n) {
-        *reinterpret_cast<uint32_t*>(dst) = ox;
-        *reinterpret_cast<uint32_t*>(dst + 8) = oy;
-      }
-      dst += step;
-    }
-    add_up(7, 0);
-    add_up(7, 1);
-    fence_proxy_async_smem();  // this warp's reads before the copy that refills the stage
-    __syncwarp();
-    if (lane == 0) mbar_arrive_reads(empty + s);
-  }
-  if (a.state_out && so >= 0) {
-    float* dst = a.state_out + so * head_size + ((int64_t)h * kDeltaD + t2) * kDeltaD + col + g;
+    float sbig[4] = {0.f, 0.f, 0.f, 0.f};  // the largest |S|, four chains of it
 #pragma unroll
     for (int j = 0; j < 16; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) dst[(j * 8 + (e & 1)) * kDeltaD + (e >> 1) * 8] = S[j][e];
+      for (int e = 0; e < 4; ++e) {
+        if (nc > 0 && !(fabsf(S[j][e]) < INFINITY)) {  // a column that is NaN from the start
+          atomicMin(&mine[g + (e >> 1) * 8], 0);
+          S[j][e] = 0.f;
+        }
+        sbig[e] = fmaxf(sbig[e], fabsf(S[j][e]));
+      }
+    for (int c = 0; c < nc; ++c) {
+      const int s = done % kD2Stages;
+      const uint32_t K = base + s * kD2Stage, Q = K + kD2Q, X = K + kD2Item, V = K + kD2V;
+      const float* f = reinterpret_cast<const float*>(smem + s * kD2Stage + kD2Item + kDcFactors);
+      const int n = (int)(len - (int64_t)c * kDcTok < kDcTok ? len - (int64_t)c * kDcTok : kDcTok);
+      float down_s;
+      const float up_s = operand_scale(sbig, down_s);
+      wait(ready + s, (done / kD2Stages) & 1);
+      ++done;
+      // A warp has its SM sub-partition to itself, so nothing but its own other work fills the latency of a
+      // load or the time of an MMA: loads run a step ahead, and what is not on the way from S to the next
+      // S (the products for o, its output) is spread over the steps that are.
+      float R[8][4], O[8][4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) R[j][e] = O[j][e] = 0.f;
+      auto at_n = [&](int ks) { return (ks >> 2) * kDcBlock + row_n + (((uint32_t)(ks & 3) * 2u + pc_n) ^ sw) * 16u; };
+      uint32_t bk[4][4], sh[8][4];
+      // S^T k
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ldsm4(K + at_n(0) + j * 2048, bk[j]);
+      uint32_t lo[2][4];
+      auto split_s = [&](int ks, int q) {
+        split2(S[2 * ks + (q >> 1)] + (q & 1) * 2, up_s, sh[ks][q], lo[ks & 1][q]);
+      };
+#pragma unroll
+      for (int q = 0; q < 4; ++q) split_s(0, q);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          mma_16816(R[2 * j], sh[ks], bk[j][0], bk[j][1]);
+          if (ks < 7) split_s(ks + 1, j);
+          mma_16816(R[2 * j + 1], sh[ks], bk[j][2], bk[j][3]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          mma_16816(R[2 * j], lo[ks & 1], bk[j][0], bk[j][1]);
+          mma_16816(R[2 * j + 1], lo[ks & 1], bk[j][2], bk[j][3]);
+          ldsm4((ks < 7 ? K + at_n(ks + 1) : Q + at_n(0)) + j * 2048, bk[j]);
+        }
+      }
+      // S^T q, and beside it R = v - exp(gamma) S^T k
+      float big[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t vv[4];
+      ldsm4_trans(V + v_row + v_pc, vv);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const int tok = ks * 8 + t2;
+        const float2 cc = *reinterpret_cast<const float2*>(f + tok);
+        const float2 cn = mul_f32x2(cc, make_float2(-down_s, -down_s));
+        auto residual = [&](int q) {  // columns of v g + 8 q
+          const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&vv[(ks & 1) * 2 + q]));
+          float* x = R[ks] + q * 2;
+          const float2 r = fma_f32x2(cn, make_float2(x[0], x[1]), w);
+          x[0] = r.x;
+          x[1] = r.y;
+          big[q * 2] = fmaxf(big[q * 2], fabsf(r.x));
+          big[q * 2 + 1] = fmaxf(big[q * 2 + 1], fabsf(r.y));
+        };
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          mma_16816(O[2 * j], sh[ks], bk[j][0], bk[j][1]);
+          if (j == 1) residual(0);
+          if (j == 2) residual(1);
+          mma_16816(O[2 * j + 1], sh[ks], bk[j][2], bk[j][3]);
+          if (ks < 7) ldsm4(Q + at_n(ks + 1) + j * 2048, bk[j]);
+        }
+        if ((ks & 1) && ks < 7) ldsm4_trans(V + (ks / 2 + 1) * 2048 + v_row + v_pc, vv);
+      }
+      float down_r;
+      const float up_r = operand_scale(big, down_r);
+      uint32_t rh[4][4], rl[4][4];
+      auto split_r = [&](int ks, int q) {
+        split2(R[2 * ks + (q >> 1)] + (q & 1) * 2, up_r, rh[ks][q], rl[ks][q]);
+      };
+#pragma unroll
+      for (int q = 0; q < 4; ++q) split_r(0, q);
+      // U = T R (rows past a token do not reach it: their tiles are left out); o's first part to R's scale
+      float U[8][4];
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) U[nt][e] = 0.f;
+      auto at_x = [&](int ks, int j) { return X + row_n + (((uint32_t)ks * 2u + pc_n) ^ sw) * 16u + j * 2048; };
+      constexpr int kAt[11][2] = {{0, 0}, {0, 1}, {0, 2}, {0, 3}, {1, 1}, {1, 2}, {1, 3}, {2, 2}, {2, 3}, {3, 3}, {3, 3}};
+      uint32_t th[2][4], tl[2][4];
+      ldsm4(at_x(0, 0), th[0]);
+      ldsm4(at_x(0, 0) + 2 * kDcBlock, tl[0]);
+#pragma unroll
+      for (int i = 0; i < 10; ++i) {
+        const int ks = kAt[i][0], j = kAt[i][1], x = i & 1;
+        const uint32_t at = at_x(kAt[i + 1][0], kAt[i + 1][1]);
+        if (i < 9) {
+          ldsm4(at, th[x ^ 1]);
+          ldsm4(at + 2 * kDcBlock, tl[x ^ 1]);
+        } else {
+          ldsm4(at_x(0, 0) + kDcBlock, th[x ^ 1]);  // P T's first
+        }
+        mma_16816(U[2 * j], rh[ks], th[x][0], th[x][1]);
+        mma_16816(U[2 * j + 1], rh[ks], th[x][2], th[x][3]);
+        // R's later terms, a step or more ahead of their first use
+        if (i < 4) split_r(1, i);
+        if (i >= 4 && i < 6) {
+          split_r(2, (i - 4) * 2);
+          split_r(2, (i - 4) * 2 + 1);
+        }
+        if (i >= 6 && i < 8) {
+          split_r(3, (i - 6) * 2);
+          split_r(3, (i - 6) * 2 + 1);
+        }
+        if (i < 8) {
+          const float2 qq = *reinterpret_cast<const float2*>(f + 128 + i * 8 + t2);
+          const float2 qs = mul_f32x2(qq, make_float2(down_s * up_r, down_s * up_r));
+          mul_pair(O[i], qs);
+          mul_pair(O[i] + 2, qs);
+        }
+        mma_16816(U[2 * j], rl[ks], th[x][0], th[x][1]);
+        mma_16816(U[2 * j + 1], rl[ks], th[x][2], th[x][3]);
+        mma_16816(U[2 * j], rh[ks], tl[x][0], tl[x][1]);
+        mma_16816(U[2 * j + 1], rh[ks], tl[x][2], tl[x][3]);
+      }
+      // w U, and beside it o += P T R
+      big[0] = big[1] = big[2] = big[3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 10; ++i) {
+        const int ks = kAt[i][0], j = kAt[i][1], x = i & 1;
+        if (i < 9) ldsm4(at_x(kAt[i + 1][0], kAt[i + 1][1]) + kDcBlock, th[x ^ 1]);
+        mma_16816(O[2 * j], rh[ks], th[x][0], th[x][1]);
+        mma_16816(O[2 * j + 1], rh[ks], th[x][2], th[x][3]);
+        mma_16816(O[2 * j], rl[ks], th[x][0], th[x][1]);
+        mma_16816(O[2 * j + 1], rl[ks], th[x][2], th[x][3]);
+        if (i < 8) {
+          const float2 ww = *reinterpret_cast<const float2*>(f + 64 + i * 8 + t2);
+          const float2 ws = mul_f32x2(ww, make_float2(down_r, down_r));
+          mul_pair(U[i], ws);
+          mul_pair(U[i] + 2, ws);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) big[e] = fmaxf(big[e], fabsf(U[i][e]));
+        }
+      }
+      float down_u;
+      const float up_u = operand_scale(big, down_u);
+      auto split_u = [&](int ks, int q) {
+        split2(U[2 * ks + (q >> 1)] + (q & 1) * 2, up_u, rh[ks][q], rl[ks][q]);
+      };
+#pragma unroll
+      for (int q = 0; q < 4; ++q) split_u(0, q);
+      // S <- exp(gamma_C) S + K^T (w U); the increment is summed by itself, so that the state's own
+      // rounding is one fp32 fma a chunk.  Beside it o goes out, back in rows of tokens.
+      const float dec = f[192];
+      sbig[0] = sbig[1] = sbig[2] = sbig[3] = 0.f;
+      auto at_k = [&](int i) {  // step i: 16 columns i / 4 of k, 16 tokens i % 4
+        const int j = i >> 2;
+        return K + (j >> 2) * kDcBlock + row_k + (((uint32_t)(j & 3) * 2u + pc_k) ^ sw) * 16u + (i & 3) * 2048;
+      };
+      __half* dst = a.o + ((t0 + (int64_t)c * kDcTok + g) * a.Hv + h) * kDeltaD + col + t2;
+      const int64_t step = (int64_t)8 * a.Hv * kDeltaD;
+      uint32_t kt[2][4];
+      ldsm4_trans(at_k(0), kt[0]);
+      float dh[2][2][4], dl[2][2][4];  // of two steps: one is summed up while the next one's MMAs run
+      auto add_up = [&](int j, int x) {
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          float* y = S[2 * j + x] + e;
+          const float *h = dh[j & 1][x] + e, *l = dl[j & 1][x] + e;
+          const float2 d = add_f32x2(make_float2(h[0], h[1]), make_float2(l[0], l[1]));
+          const float2 r = fma_f32x2(make_float2(dec, dec), make_float2(y[0], y[1]), mul_f32x2(d, make_float2(down_u, down_u)));
+          y[0] = r.x;
+          y[1] = r.y;
+          sbig[e] = fmaxf(sbig[e], fabsf(r.x));
+          sbig[e + 1] = fmaxf(sbig[e + 1], fabsf(r.y));
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int z = j & 1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dh[z][0][e] = dh[z][1][e] = dl[z][0][e] = dl[z][1][e] = 0.f;
+        uint32_t ox = 0, oy = 0;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          const int i = j * 4 + ks, x = i & 1;
+          if (i < 31) ldsm4_trans(at_k(i + 1), kt[x ^ 1]);
+          mma_16816(dh[z][0], rh[ks], kt[x][0], kt[x][1]);
+          if (j == 0 && ks < 3) {
+            split_u(ks + 1, 0);
+            split_u(ks + 1, 1);
+          }
+          if (j > 0 && ks == 1) add_up(j - 1, 0);
+          mma_16816(dh[z][1], rh[ks], kt[x][2], kt[x][3]);
+          if (j == 0 && ks < 3) {
+            split_u(ks + 1, 2);
+            split_u(ks + 1, 3);
+          }
+          if (j > 0 && ks == 2) add_up(j - 1, 1);
+          mma_16816(dl[z][0], rl[ks], kt[x][0], kt[x][1]);
+          if (ks == 0) ox = transpose8x8(pack_half2(O[j][0] * down_r, O[j][1] * down_r));
+          if (ks == 1) oy = transpose8x8(pack_half2(O[j][2] * down_r, O[j][3] * down_r));
+          mma_16816(dl[z][1], rl[ks], kt[x][2], kt[x][3]);
+        }
+        if (j * 8 + g < n) {
+          *reinterpret_cast<uint32_t*>(dst) = ox;
+          *reinterpret_cast<uint32_t*>(dst + 8) = oy;
+        }
+        dst += step;
+      }
+      add_up(7, 0);
+      add_up(7, 1);
+      fence_proxy_async_smem();  // this warp's reads before the copy that refills the stage
+      __syncwarp();
+      if (lane == 0) mbar_arrive_reads(empty + s);
+    }
+    const int64_t so = delta_slot(a.slot_out, it.b, a.n_out, a.status);
+    if (a.state_out && so >= 0) {
+      float* dst = a.state_out + so * head_size + ((int64_t)h * kDeltaD + t2) * kDeltaD + col + g;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[(j * 8 + (e & 1)) * kDeltaD + (e >> 1) * 8] = S[j][e];
+    }
+    if (nc == 0) continue;
+    ++seg;
+    // what is NaN (rarely anything), over what this warp wrote there
+    __syncwarp();
+    const int from = lane < 16 ? mine[lane] : INT_MAX;
+    for (unsigned who = __ballot_sync(0xffffffffu, from != INT_MAX); who; who &= who - 1) {
+      const int x = __ffs(who) - 1, at = __shfl_sync(0xffffffffu, from, x);
+      for (int64_t t = at + lane; t < len; t += 32) a.o[((t0 + t) * a.Hv + h) * kDeltaD + col + x] = __float2half_rn(NAN);
+      if (a.state_out && so >= 0)
+        for (int k = lane; k < kDeltaD; k += 32) a.state_out[so * head_size + ((int64_t)h * kDeltaD + k) * kDeltaD + col + x] = NAN;
+    }
+    if (from != INT_MAX) mine[lane] = INT_MAX;  // (for the item after the next three)
+    __syncwarp();
   }
-  finish();
 }
 
 static int launch_scan(const ChunkArgs& p, const DeviceFacts& f, cudaStream_t s) {
@@ -955,7 +994,8 @@ static int launch_scan(const ChunkArgs& p, const DeviceFacts& f, cudaStream_t s)
   if (rc == TB_OK) rc = ensure_dynamic_smem(reinterpret_cast<const void*>(delta_scan_kernel), f.device, kD2Smem);
   if (rc != TB_OK) return rc;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.B * a.Hv * kD2Slices));
+  const int64_t items = (int64_t)a.B * a.Hv * kD2Slices;
+  cfg.gridDim = dim3((unsigned)(items < f.sms ? items : f.sms));
   cfg.blockDim = dim3(kD2Threads);
   cfg.dynamicSmemBytes = kD2Smem;
   cfg.stream = s;
