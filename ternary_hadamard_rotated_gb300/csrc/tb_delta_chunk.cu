@@ -13,8 +13,8 @@
 //
 // Kernel 1, a CTA per (chunk, key head), which its value heads share: K K^T and Q K^T by mma.sync (fp16
 // inputs, exact products), per value head the triangular system by blocks of 16 and P T.  It writes T
-// (fp16, high and low part) and P T (fp16) as the shared-memory images that kernel 2's MMAs read, and each
-// token's factors.  8192 tokens, 16/48 heads: 107 us, bound by the latency of each head's chain of steps.
+// (fp16, high and low part) and P T (fp16) as the fragments that kernel 2's MMAs take, and each token's
+// factors.  8192 tokens, 16/48 heads: 103 us, bound by the latency of each head's chain of steps.
 //
 // Kernel 2 walks the chunks, a warp per 16 columns of v, which no other warp's columns depend on: S^T
 // stays in the warp's registers as fp32 accumulators of mma.sync, and every product's left factor (S^T,
@@ -23,7 +23,7 @@
 // chunks deep.  An fp32 factor goes in as two fp16 terms, x 2^e = hi + lo with the warp's largest |x|
 // at 2^14: 22 bits, and K and Q are fp16 already.  T has two terms too.  What goes into o alone is rounded
 // once: P T, and the state in S^T q, to fp16.
-// 8192 tokens: 350 us, 2.7 us a chunk.  Its 420 MMAs a warp, at one per 7.8 clocks and SM sub-partition,
+// 8192 tokens: 340 us, 2.65 us a chunk.  Its 420 MMAs a warp, at one per 7.8 clocks and SM sub-partition,
 // are 1.7 of them; the rest is the latency of one warp's own chain.  (The same walk on tcgen05, 32
 // columns a CTA, took 2.7 us a chunk alone on its SM and 3.4 with a second CTA, with fewer terms: 20
 // MMAs of 44 to 60 clocks, and three trips through registers, shared memory and a barrier of 800 to
@@ -42,13 +42,16 @@
 
 namespace tb {
 
-constexpr int kDcTok = 64;    // tokens per chunk
+constexpr int kDcTok = 64;              // tokens per chunk
 constexpr int kDcBlock = kDcTok * 128;  // bytes of a 64 x 64 fp16 image
-// a (chunk, value head) in the workspace: T, P T, T's low part, factors
-constexpr int kDcItem = 3 * kDcBlock + 1024;
+// A (chunk, value head) in the workspace: T, P T and T's low part, then the tokens' factors.  Of each matrix
+// the ten 16 x 16 blocks up to the diagonal, block (i, j) at i (i + 1) / 2 + j, as the right operand's
+// fragments of mma.sync: 16 bytes a lane.
+constexpr int kDcFrag = 512, kDcMatrix = 10 * kDcFrag;
+constexpr int kDcItem = 16384;
 // floats: c [64], w [64], q [64], exp(gamma_C), and the tokens before the first whose k, decay or step
 // is not finite
-constexpr int kDcFactors = 3 * kDcBlock;
+constexpr int kDcFactors = 3 * kDcMatrix;
 
 struct ChunkArgs {
   DeltaArgs a;
@@ -110,6 +113,9 @@ TB_DEVI void split2(const float* x, float scale, uint32_t& hi, uint32_t& lo) {
   const float2 r = fma_f32x2(__half22float2(h), make_float2(-1.f, -1.f), u);
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = pack_half2(r.x, r.y);
+}
+TB_DEVI void lds4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 // two values of a tile's row by their own factors
 TB_DEVI void mul_pair(float* x, float2 f) {
@@ -315,6 +321,7 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
       __syncthreads();
     }
     uint8_t* item = p.ws + (chunk * a.Hv + h) * (int64_t)kDcItem;
+    uint4* out = reinterpret_cast<uint4*>(item) + warp * (warp + 1) / 2 * 32 + lane;  // the warp's blocks
     uint8_t* img = kq + (h4 & 1) * 2 * kDcBlock;  // T's high part, then its low part
     const float2* gm = gam[slot];
     const float* be = bet[slot];
@@ -431,15 +438,19 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
     for (int s = 0; s < 4; ++s) {
       if (warp == s) {  // this block row is complete
 #pragma unroll
-        for (int j = 0; j < 2 * s + 2; ++j)
+        for (int b = 0; b <= s; ++b) {
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t hi, lo;
-            split2(T[j][2 * e], T[j][2 * e + 1], hi, lo);
+          for (int q = 0; q < 4; ++q) {
+            const int j = 2 * b + (q & 1), e = q >> 1;
+            split2(T[j][2 * e], T[j][2 * e + 1], hi[q], lo[q]);
             const int i = i0 + e * 8, at = i * 128 + ((j ^ (i & 7)) << 4) + t2 * 2;
-            *reinterpret_cast<uint32_t*>(img + at) = hi;
-            *reinterpret_cast<uint32_t*>(img + kDcBlock + at) = lo;
+            *reinterpret_cast<uint32_t*>(img + at) = hi[q];
+            *reinterpret_cast<uint32_t*>(img + kDcBlock + at) = lo[q];
           }
+          out[b * 32] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          out[kDcMatrix / 8 + b * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
       }
       __syncthreads();
       if (warp <= s) continue;
@@ -469,14 +480,6 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
         mma_16816(T[2 * j + 1], el[x], th[j][2], th[j][3]);
       }
     }
-    // out: T's image as it lies in shared memory, P T from the registers; the blocks above the diagonal
-    // are never read
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int o = (e * kD1Threads + tid) * 16;
-      *reinterpret_cast<uint4*>(item + o) = *reinterpret_cast<const uint4*>(img + o);
-      *reinterpret_cast<uint4*>(item + 2 * kDcBlock + o) = *reinterpret_cast<const uint4*>(img + kDcBlock + o);
-    }
     // P T, in T's registers
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -500,21 +503,17 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
       }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j > 2 * warp + 1) break;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = i0 + e * 8;
-        *reinterpret_cast<uint32_t*>(item + kDcBlock + i * 128 + ((j ^ (i & 7)) << 4) + t2 * 2) =
-            pack_half2(T[j][2 * e], T[j][2 * e + 1]);
-      }
+    for (int b = 0; b < 4; ++b) {
+      if (b > warp) break;
+      out[kDcMatrix / 16 + b * 32] = make_uint4(pack_half2(T[2 * b][0], T[2 * b][1]), pack_half2(T[2 * b + 1][0], T[2 * b + 1][1]),
+                                                pack_half2(T[2 * b][2], T[2 * b][3]), pack_half2(T[2 * b + 1][2], T[2 * b + 1][3]));
     }
   }
 }
 
 // ---------------------------------------------------------------- kernel 2
 constexpr int kD2Stages = 3;
-constexpr int kD2Q = 2 * kDcBlock, kD2Item = 4 * kDcBlock, kD2V = kD2Item + 26624;  // places in a stage
+constexpr int kD2Q = 2 * kDcBlock, kD2Item = 4 * kDcBlock, kD2V = kD2Item + kDcItem;  // places in a stage
 
 constexpr int kD2Warps = 4;                     // that walk, 16 columns of v each; one more loads
 constexpr int kD2Threads = (kD2Warps + 1) * 32;
@@ -826,26 +825,45 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       };
 #pragma unroll
       for (int q = 0; q < 4; ++q) split_r(0, q);
-      // U = T R (rows past a token do not reach it: their tiles are left out); o's first part to R's scale
+      // U = T R and o += P T R (rows past a token do not reach it: their blocks are left out), a block of
+      // T and one of P T at a time, so that no MMA waits for one of the last three; w U as its rows are done
       float U[8][4];
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) U[nt][e] = 0.f;
-      auto at_x = [&](int ks, int j) { return X + row_n + (((uint32_t)ks * 2u + pc_n) ^ sw) * 16u + j * 2048; };
-      constexpr int kAt[11][2] = {{0, 0}, {0, 1}, {0, 2}, {0, 3}, {1, 1}, {1, 2}, {1, 3}, {2, 2}, {2, 3}, {3, 3}, {3, 3}};
-      uint32_t th[2][4], tl[2][4];
-      ldsm4(at_x(0, 0), th[0]);
-      ldsm4(at_x(0, 0) + 2 * kDcBlock, tl[0]);
+      auto frag = [&](int matrix, int ks, int j, uint32_t (&r)[4]) {
+        lds4(X + matrix * kDcMatrix + (j * (j + 1) / 2 + ks) * kDcFrag + lane * 16, r);
+      };
+      auto scale_o = [&](int j) {  // o's first part to R's scale
+        const float2 qq = *reinterpret_cast<const float2*>(f + 128 + j * 8 + t2);
+        const float2 qs = mul_f32x2(qq, make_float2(down_s * up_r, down_s * up_r));
+        mul_pair(O[j], qs);
+        mul_pair(O[j] + 2, qs);
+      };
+      big[0] = big[1] = big[2] = big[3] = 0.f;
+      auto weigh = [&](int j) {
+        const float2 ww = *reinterpret_cast<const float2*>(f + 64 + j * 8 + t2);
+        const float2 ws = mul_f32x2(ww, make_float2(down_r, down_r));
+        mul_pair(U[j], ws);
+        mul_pair(U[j] + 2, ws);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) big[e] = fmaxf(big[e], fabsf(U[j][e]));
+      };
+      constexpr int kAt[10][2] = {{0, 0}, {0, 1}, {0, 2}, {0, 3}, {1, 1}, {1, 2}, {1, 3}, {2, 2}, {2, 3}, {3, 3}};
+      uint32_t th[2][4], tl[2][4], pt[2][4];
+      frag(0, 0, 0, th[0]);
+      frag(1, 0, 0, pt[0]);
+      frag(2, 0, 0, tl[0]);
+      scale_o(0);
+      scale_o(1);
 #pragma unroll
       for (int i = 0; i < 10; ++i) {
         const int ks = kAt[i][0], j = kAt[i][1], x = i & 1;
-        const uint32_t at = at_x(kAt[i + 1][0], kAt[i + 1][1]);
         if (i < 9) {
-          ldsm4(at, th[x ^ 1]);
-          ldsm4(at + 2 * kDcBlock, tl[x ^ 1]);
-        } else {
-          ldsm4(at_x(0, 0) + kDcBlock, th[x ^ 1]);  // P T's first
+          frag(0, kAt[i + 1][0], kAt[i + 1][1], th[x ^ 1]);
+          frag(1, kAt[i + 1][0], kAt[i + 1][1], pt[x ^ 1]);
+          frag(2, kAt[i + 1][0], kAt[i + 1][1], tl[x ^ 1]);
         }
         mma_16816(U[2 * j], rh[ks], th[x][0], th[x][1]);
         mma_16816(U[2 * j + 1], rh[ks], th[x][2], th[x][3]);
@@ -859,36 +877,21 @@ __global__ void __launch_bounds__(kD2Threads, 1)
           split_r(3, (i - 6) * 2);
           split_r(3, (i - 6) * 2 + 1);
         }
-        if (i < 8) {
-          const float2 qq = *reinterpret_cast<const float2*>(f + 128 + i * 8 + t2);
-          const float2 qs = mul_f32x2(qq, make_float2(down_s * up_r, down_s * up_r));
-          mul_pair(O[i], qs);
-          mul_pair(O[i] + 2, qs);
-        }
+        mma_16816(O[2 * j], rh[ks], pt[x][0], pt[x][1]);
+        mma_16816(O[2 * j + 1], rh[ks], pt[x][2], pt[x][3]);
+        if (i < 3) scale_o(2 * i + 2);
         mma_16816(U[2 * j], rl[ks], th[x][0], th[x][1]);
         mma_16816(U[2 * j + 1], rl[ks], th[x][2], th[x][3]);
+        if (i < 3) scale_o(2 * i + 3);
+        if (i == 1 || i == 5 || i == 8) weigh(i == 1 ? 0 : (i == 5 ? 2 : 4));
+        mma_16816(O[2 * j], rl[ks], pt[x][0], pt[x][1]);
+        mma_16816(O[2 * j + 1], rl[ks], pt[x][2], pt[x][3]);
+        if (i == 1 || i == 5 || i == 8) weigh(i == 1 ? 1 : (i == 5 ? 3 : 5));
         mma_16816(U[2 * j], rh[ks], tl[x][0], tl[x][1]);
         mma_16816(U[2 * j + 1], rh[ks], tl[x][2], tl[x][3]);
       }
-      // w U, and beside it o += P T R
-      big[0] = big[1] = big[2] = big[3] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 10; ++i) {
-        const int ks = kAt[i][0], j = kAt[i][1], x = i & 1;
-        if (i < 9) ldsm4(at_x(kAt[i + 1][0], kAt[i + 1][1]) + kDcBlock, th[x ^ 1]);
-        mma_16816(O[2 * j], rh[ks], th[x][0], th[x][1]);
-        mma_16816(O[2 * j + 1], rh[ks], th[x][2], th[x][3]);
-        mma_16816(O[2 * j], rl[ks], th[x][0], th[x][1]);
-        mma_16816(O[2 * j + 1], rl[ks], th[x][2], th[x][3]);
-        if (i < 8) {
-          const float2 ww = *reinterpret_cast<const float2*>(f + 64 + i * 8 + t2);
-          const float2 ws = mul_f32x2(ww, make_float2(down_r, down_r));
-          mul_pair(U[i], ws);
-          mul_pair(U[i] + 2, ws);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) big[e] = fmaxf(big[e], fabsf(U[i][e]));
-        }
-      }
+      weigh(6);
+      weigh(7);
       float down_u;
       const float up_u = operand_scale(big, down_u);
       auto split_u = [&](int ks, int q) {
