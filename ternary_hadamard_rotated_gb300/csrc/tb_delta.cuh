@@ -45,8 +45,8 @@ TB_DEVI int64_t delta_slot(const int32_t* slots, int b, int64_t n, int32_t* stat
 }
 
 // Requests of up to so many tokens take the recurrent kernel.  16/48 heads, recurrent and chunked:
-// 1 request of 8, 16, 24 tokens 13, 23, 33 and 25 us; 4 of them 28, 52, 75 and 40; 64 of them 184, 326,
-// 496 and 367.
+// 1 request of 8, 16, 24 tokens 13, 23, 33 and 25 us; 4 of them 28, 52, 75 and 38; 64 of them 184, 326,
+// 496 and 316.
 constexpr int64_t kDeltaStepTokens = 16;
 
 // the chunked form, and its workspace

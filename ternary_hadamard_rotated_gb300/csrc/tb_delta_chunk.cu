@@ -20,10 +20,11 @@
 // stays in the warp's registers as fp32 accumulators of mma.sync, and every product's left factor (S^T,
 // R^T, (w U)^T, 16 rows) comes out of the product before it in the layout that the next one wants, so
 // a chunk has no exchange between warps at all.  K, Q, V and kernel 1's results come by TMA, three
-// chunks deep.  An fp32 factor goes in as two fp16 terms, x 2^e = hi + lo with the warp's largest |x|
+// chunks deep, and the next item's state (read by the warps themselves, 64 requests of one chunk took 351
+// us instead of 308).  An fp32 factor goes in as two fp16 terms, x 2^e = hi + lo with the warp's largest |x|
 // at 2^14: 22 bits, and K and Q are fp16 already.  T has two terms too.  What goes into o alone is rounded
 // once: P T, and the state in S^T q, to fp16.
-// 8192 tokens: 340 us, 2.65 us a chunk.  Its 420 MMAs a warp, at one per 7.8 clocks and SM sub-partition,
+// 8192 tokens: 348 us, 2.7 us a chunk.  Its 420 MMAs a warp, at one per 7.8 clocks and SM sub-partition,
 // are 1.7 of them; the rest is the latency of one warp's own chain.  (The same walk on tcgen05, 32
 // columns a CTA, took 2.7 us a chunk alone on its SM and 3.4 with a second CTA, with fewer terms: 20
 // MMAs of 44 to 60 clocks, and three trips through registers, shared memory and a barrier of 800 to
@@ -114,8 +115,19 @@ TB_DEVI void split2(const float* x, float scale, uint32_t& hi, uint32_t& lo) {
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = pack_half2(r.x, r.y);
 }
+TB_DEVI float2 lds2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
 TB_DEVI void lds4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+// the largest magnitude
+TB_DEVI float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 // two values of a tile's row by their own factors
 TB_DEVI void mul_pair(float* x, float2 f) {
@@ -520,11 +532,13 @@ constexpr int kD2Threads = (kD2Warps + 1) * 32;
 constexpr int kD2Slices = kDeltaD / (kD2Warps * 16);  // CTAs a head
 constexpr int kD2Stage = kD2V + kDcBlock;
 constexpr int kD2Bytes = 5 * kDcBlock + kDcItem;  // loaded per chunk
-constexpr int kD2Smem = 1024 + kD2Stages * kD2Stage + 128 + 1024;
+// the next item's state: 128 rows of k, 64 columns of v, at a pitch that spreads the lanes' reads over the banks
+constexpr int kD2StatePitch = 64 * 4 + 16, kD2State = kDeltaD * kD2StatePitch;
+constexpr int kD2Smem = 1024 + kD2Stages * kD2Stage + kD2State + 128 + 1024;
 
 // a power of two that takes the warp's largest magnitude to 2^14, and its inverse
-TB_DEVI float operand_scale(const float (&most)[4], float& inverse) {
-  const float m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+TB_DEVI float operand_scale(const float (&most)[2], float& inverse) {
+  const float m = fmaxf(most[0], most[1]);
   const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));  // orders as the values do
   int e = 268 - (int)(bits >> 23);
   e = e < 127 - 100 ? 127 - 100 : (e > 127 + 100 ? 127 + 100 : e);
@@ -545,13 +559,15 @@ __global__ void __launch_bounds__(kD2Threads, 1)
   const uint32_t raw = smem_u32(d2_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = d2_raw + (base - raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kD2Stages * kD2Stage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kD2Stages * kD2Stage + kD2State);
   uint64_t* ready = full + kD2Stages;  // the loading warp has looked the stage over
   uint64_t* empty = full + 2 * kD2Stages;
-  volatile int* aborted = reinterpret_cast<volatile int*>(full + 3 * kD2Stages);
+  uint64_t* state_full = full + 3 * kD2Stages;
+  uint64_t* state_empty = state_full + 1;
+  volatile int* aborted = reinterpret_cast<volatile int*>(state_full + 2);
   // per column of v of the item, for four items in turn: the request's first token from which o and the
   // state are NaN (three chunks are under way at most, so four items with chunks)
-  int* spoilt = reinterpret_cast<int*>(full + 3 * kD2Stages + 1);
+  int* spoilt = reinterpret_cast<int*>(state_full + 3);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the requests with the most chunks first, so that what comes last is short; each lane ranks two
@@ -600,6 +616,8 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       mbar_init(ready + i, 1);
       mbar_init(empty + i, kD2Warps);
     }
+    mbar_init(state_full, 1);
+    mbar_init(state_empty, kD2Warps);
     fence_barrier_init();
   }
   __syncthreads();
@@ -613,7 +631,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
 
   if (warp == kD2Warps) {
     const ChunkScan sc = chunk_scan(a, lane);
-    int loaded = 0, looked = 0;  // chunks of all items
+    int loaded = 0, looked = 0, states = 0;  // chunks of all items; states
     auto load = [&](const Item& it, int64_t first, int c) {  // a lane per copy
       const int s = loaded % kD2Stages, row = (int)it.t0 + c * kDcTok;
       const int h = it.h, hk = h / (a.Hv / a.Hk), slice = it.slice;
@@ -631,6 +649,16 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       }
       __syncwarp();
       ++loaded;
+    };
+    auto load_state = [&](const Item& it, int64_t slot) {  // once the walking warps have taken up the last one
+      if (states > 0) wait(state_empty, (states - 1) & 1);
+      ++states;
+      if (lane == 0) mbar_arrive_expect_tx(state_full, kDeltaD * 256);
+      __syncwarp();
+      const float* src = a.state_in + (slot * a.Hv + it.h) * (int64_t)(kDeltaD * kDeltaD) + it.slice * 64;
+#pragma unroll
+      for (int r = lane; r < kDeltaD; r += 32)
+        bulk_g2s(smem + kD2Stages * kD2Stage + r * kD2StatePitch, src + r * kDeltaD, 256, state_full);
     };
     // What must not meet the zeros of T or of the sums over the tokens is taken out of the stage before the
     // others see it, and noted: tokens of another request behind the last one, tokens from one on whose k,
@@ -690,8 +718,12 @@ __global__ void __launch_bounds__(kD2Threads, 1)
         for (int r = lane * sc.per; r < it.b; ++r) first += chunks_of(a, r);
       first = __shfl_sync(0xffffffffu, first, src);
       for (int c = 0; c < it.nc; ++c) {
+        const int64_t si = c == 0 && a.state_in ? delta_slot(a.slot_in, it.b, a.n_in, a.status) : -1;
+        const bool first_state = si >= 0 && states == 0;
+        if (first_state) load_state(it, si);  // (does not wait for kernel 1)
         load(it, first, c);
         if (last_c >= 0) look_over(last_len, last_spoilt, last_c);
+        if (si >= 0 && !first_state) load_state(it, si);
         last_c = c;
         last_len = it.len;
         last_spoilt = spoilt + (seg & 3) * 64;
@@ -716,41 +748,59 @@ __global__ void __launch_bounds__(kD2Threads, 1)
   const uint32_t v_row = ((((uint32_t)lane >> 4) & 1u) * 8u + sw) * 128u;
   const uint32_t v_pc = (((uint32_t)warp * 2u + pc_n) ^ sw) << 4;
 
-  int done = 0, seg = 0;  // chunks of all items, items with chunks
+  int done = 0, seg = 0, states = 0;  // chunks of all items, items with chunks, states of those
   Item it;
   for (int i = 0; item_at(i, it); ++i) {
     const int h = it.h, nc = it.nc;
     const int64_t t0 = it.t0, len = it.len, head_size = (int64_t)a.Hv * kDeltaD * kDeltaD;
     const int col = (it.slice * kD2Warps + warp) * 16;  // the warp's first column of v
     int* mine = spoilt + (seg & 3) * 64 + warp * 16;
+    const int64_t si = delta_slot(a.slot_in, it.b, a.n_in, a.status);
+    const bool have = a.state_in && si >= 0;
+    if (nc == 0) {  // no tokens: the state goes through
+      const int64_t so = delta_slot(a.slot_out, it.b, a.n_out, a.status);
+      if (a.state_out && so >= 0) {
+        const int64_t at = (int64_t)h * kDeltaD * kDeltaD + col + (lane & 3) * 4;
+        for (int k = lane >> 2; k < kDeltaD; k += 8) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (have) x = *reinterpret_cast<const float4*>(a.state_in + si * head_size + at + k * kDeltaD);
+          *reinterpret_cast<float4*>(a.state_out + so * head_size + at + k * kDeltaD) = x;
+        }
+      }
+      continue;
+    }
     // S^T: rows g, g + 8 (columns of v), columns 8 j + t2, + 1 (of k)
     float S[16][4];
+    if (have) wait(state_full, states++ & 1);
     {
-      const int64_t si = delta_slot(a.slot_in, it.b, a.n_in, a.status);
-      const bool have = a.state_in && si >= 0;
-      const float* src = a.state_in + si * head_size + ((int64_t)h * kDeltaD + t2) * kDeltaD + col + g;
+      const uint8_t* src = smem + kD2Stages * kD2Stage + t2 * kD2StatePitch + (warp * 16 + g) * 4;
 #pragma unroll
       for (int j = 0; j < 16; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          S[j][e] = have ? __ldg(src + (j * 8 + (e & 1)) * kDeltaD + (e >> 1) * 8) : 0.f;
+          S[j][e] = have ? *reinterpret_cast<const float*>(src + (j * 8 + (e & 1)) * kD2StatePitch + (e >> 1) * 32) : 0.f;
     }
-    float sbig[4] = {0.f, 0.f, 0.f, 0.f};  // the largest |S|, four chains of it
+    float sbig[2] = {0.f, 0.f};  // the largest |S|, two chains of it
 #pragma unroll
     for (int j = 0; j < 16; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (nc > 0 && !(fabsf(S[j][e]) < INFINITY)) {  // a column that is NaN from the start
+        if (!(fabsf(S[j][e]) < INFINITY)) {  // a column that is NaN from the start
           atomicMin(&mine[g + (e >> 1) * 8], 0);
           S[j][e] = 0.f;
         }
-        sbig[e] = fmaxf(sbig[e], fabsf(S[j][e]));
+        sbig[e / 2] = fmaxf(sbig[e / 2], fabsf(S[j][e]));
       }
-    for (int c = 0; c < nc; ++c) {
+    if (have) {
+      fence_proxy_async_smem();  // the reads above before the next state's copy
+      __syncwarp();
+      if (lane == 0) mbar_arrive_reads(state_empty);
+    }
+    __half* dst = a.o + ((t0 + g) * a.Hv + h) * kDeltaD + col + t2;
+    for (int left = (int)len; left > 0; left -= kDcTok) {  // tokens
       const int s = done % kD2Stages;
       const uint32_t K = base + s * kD2Stage, Q = K + kD2Q, X = K + kD2Item, V = K + kD2V;
-      const float* f = reinterpret_cast<const float*>(smem + s * kD2Stage + kD2Item + kDcFactors);
-      const int n = (int)(len - (int64_t)c * kDcTok < kDcTok ? len - (int64_t)c * kDcTok : kDcTok);
+      auto factors = [&](int at) { return lds2(X + kDcFactors + (at + t2) * 4); };  // of two tokens
       float down_s;
       const float up_s = operand_scale(sbig, down_s);
       wait(ready + s, (done / kD2Stages) & 1);
@@ -790,13 +840,12 @@ __global__ void __launch_bounds__(kD2Threads, 1)
         }
       }
       // S^T q, and beside it R = v - exp(gamma) S^T k
-      float big[4] = {0.f, 0.f, 0.f, 0.f};
+      float big[2] = {0.f, 0.f};
       uint32_t vv[4];
       ldsm4_trans(V + v_row + v_pc, vv);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        const int tok = ks * 8 + t2;
-        const float2 cc = *reinterpret_cast<const float2*>(f + tok);
+        const float2 cc = factors(ks * 8);
         const float2 cn = mul_f32x2(cc, make_float2(-down_s, -down_s));
         auto residual = [&](int q) {  // columns of v g + 8 q
           const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&vv[(ks & 1) * 2 + q]));
@@ -804,8 +853,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
           const float2 r = fma_f32x2(cn, make_float2(x[0], x[1]), w);
           x[0] = r.x;
           x[1] = r.y;
-          big[q * 2] = fmaxf(big[q * 2], fabsf(r.x));
-          big[q * 2 + 1] = fmaxf(big[q * 2 + 1], fabsf(r.y));
+          big[q] = max3_abs(big[q], r.x, r.y);
         };
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -836,19 +884,19 @@ __global__ void __launch_bounds__(kD2Threads, 1)
         lds4(X + matrix * kDcMatrix + (j * (j + 1) / 2 + ks) * kDcFrag + lane * 16, r);
       };
       auto scale_o = [&](int j) {  // o's first part to R's scale
-        const float2 qq = *reinterpret_cast<const float2*>(f + 128 + j * 8 + t2);
+        const float2 qq = factors(128 + j * 8);
         const float2 qs = mul_f32x2(qq, make_float2(down_s * up_r, down_s * up_r));
         mul_pair(O[j], qs);
         mul_pair(O[j] + 2, qs);
       };
-      big[0] = big[1] = big[2] = big[3] = 0.f;
+      big[0] = big[1] = 0.f;
       auto weigh = [&](int j) {
-        const float2 ww = *reinterpret_cast<const float2*>(f + 64 + j * 8 + t2);
+        const float2 ww = factors(64 + j * 8);
         const float2 ws = mul_f32x2(ww, make_float2(down_r, down_r));
         mul_pair(U[j], ws);
         mul_pair(U[j] + 2, ws);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) big[e] = fmaxf(big[e], fabsf(U[j][e]));
+        big[0] = max3_abs(big[0], U[j][0], U[j][1]);
+        big[1] = max3_abs(big[1], U[j][2], U[j][3]);
       };
       constexpr int kAt[10][2] = {{0, 0}, {0, 1}, {0, 2}, {0, 3}, {1, 1}, {1, 2}, {1, 3}, {2, 2}, {2, 3}, {3, 3}};
       uint32_t th[2][4], tl[2][4], pt[2][4];
@@ -901,14 +949,12 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       for (int q = 0; q < 4; ++q) split_u(0, q);
       // S <- exp(gamma_C) S + K^T (w U); the increment is summed by itself, so that the state's own
       // rounding is one fp32 fma a chunk.  Beside it o goes out, back in rows of tokens.
-      const float dec = f[192];
-      sbig[0] = sbig[1] = sbig[2] = sbig[3] = 0.f;
+      const float dec = lds2(X + kDcFactors + 192 * 4).x;
+      sbig[0] = sbig[1] = 0.f;
       auto at_k = [&](int i) {  // step i: 16 columns i / 4 of k, 16 tokens i % 4
         const int j = i >> 2;
         return K + (j >> 2) * kDcBlock + row_k + (((uint32_t)(j & 3) * 2u + pc_k) ^ sw) * 16u + (i & 3) * 2048;
       };
-      __half* dst = a.o + ((t0 + (int64_t)c * kDcTok + g) * a.Hv + h) * kDeltaD + col + t2;
-      const int64_t step = (int64_t)8 * a.Hv * kDeltaD;
       uint32_t kt[2][4];
       ldsm4_trans(at_k(0), kt[0]);
       float dh[2][2][4], dl[2][2][4];  // of two steps: one is summed up while the next one's MMAs run
@@ -921,8 +967,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
           const float2 r = fma_f32x2(make_float2(dec, dec), make_float2(y[0], y[1]), mul_f32x2(d, make_float2(down_u, down_u)));
           y[0] = r.x;
           y[1] = r.y;
-          sbig[e] = fmaxf(sbig[e], fabsf(r.x));
-          sbig[e + 1] = fmaxf(sbig[e + 1], fabsf(r.y));
+          sbig[e / 2] = max3_abs(sbig[e / 2], r.x, r.y);
         }
       };
 #pragma unroll
@@ -948,15 +993,21 @@ __global__ void __launch_bounds__(kD2Threads, 1)
           }
           if (j > 0 && ks == 2) add_up(j - 1, 1);
           mma_16816(dl[z][0], rl[ks], kt[x][0], kt[x][1]);
-          if (ks == 0) ox = transpose8x8(pack_half2(O[j][0] * down_r, O[j][1] * down_r));
-          if (ks == 1) oy = transpose8x8(pack_half2(O[j][2] * down_r, O[j][3] * down_r));
+          if (ks == 0) {
+            mul_pair(O[j], make_float2(down_r, down_r));
+            ox = transpose8x8(pack_half2(O[j][0], O[j][1]));
+          }
+          if (ks == 1) {
+            mul_pair(O[j] + 2, make_float2(down_r, down_r));
+            oy = transpose8x8(pack_half2(O[j][2], O[j][3]));
+          }
           mma_16816(dl[z][1], rl[ks], kt[x][2], kt[x][3]);
         }
-        if (j * 8 + g < n) {
+        if (j * 8 + g < left) {
           *reinterpret_cast<uint32_t*>(dst) = ox;
           *reinterpret_cast<uint32_t*>(dst + 8) = oy;
         }
-        dst += step;
+        dst += (int64_t)8 * a.Hv * kDeltaD;
       }
       add_up(7, 0);
       add_up(7, 1);
@@ -972,7 +1023,6 @@ __global__ void __launch_bounds__(kD2Threads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) dst[(j * 8 + (e & 1)) * kDeltaD + (e >> 1) * 8] = S[j][e];
     }
-    if (nc == 0) continue;
     ++seg;
     // what is NaN (rarely anything), over what this warp wrote there
     __syncwarp();
