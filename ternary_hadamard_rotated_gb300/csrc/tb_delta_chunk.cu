@@ -25,7 +25,9 @@
 // at 2^14: 22 bits, and K and Q are fp16 already.  T has two terms too.  What goes into o alone is rounded
 // once: P T, and the state in S^T q, to fp16.
 // 8192 tokens: 348 us, 2.7 us a chunk.  Its 420 MMAs a warp, at one per 7.8 clocks and SM sub-partition,
-// are 1.7 of them; the rest is the latency of one warp's own chain.  (The same walk on tcgen05, 32
+// are 1.7 of them; the rest is the issue and the latencies of one warp's own chain.  (With a second warp on
+// the sub-partition that makes o from S and R, passed through shared memory, the call takes 476 us instead
+// of 445.  The same walk on tcgen05, 32
 // columns a CTA, took 2.7 us a chunk alone on its SM and 3.4 with a second CTA, with fewer terms: 20
 // MMAs of 44 to 60 clocks, and three trips through registers, shared memory and a barrier of 800 to
 // 1000 each.)  CTAs stay and take the (request, head, half) items with the most chunks first; the loading
