@@ -281,3 +281,33 @@ def test_what_is_not_finite_stays_behind_its_token(what, bad, at):
     assert not torch.isfinite(o[touched]).any() if bad != bad else not torch.isfinite(o[touched]).all()
     if what != "q" and bad != bad:
         assert not torch.isfinite(s[state]).any()
+
+
+@pytest.mark.parametrize("B", [25, 70])
+def test_many_requests_with_and_without_a_first_state(B):
+    """More (request, head) pairs than the GPU has room for at once, states in a pool and in place, some
+    requests from nothing, some without tokens."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    rng = np.random.default_rng(B)
+    lens = [int(n) for n in rng.choice([0, 1, 17, 63, 64, 65, 130], B)]
+    lens[0] = 130
+    Hk, Hv, T = 4, 12, sum(lens)
+    q, k, v, g, beta, _ = make(100 + B, lens, Hk, Hv, True)
+    gen = torch.Generator().manual_seed(B)
+    pool = (torch.randn(B + 3, Hv, D, D, generator=gen) * 0.3).cuda()
+    before = pool.clone()
+    slots = rng.permutation(B + 3)[:B]
+    fresh = rng.random(B) < 0.4
+    i32 = dict(dtype=torch.int32, device="cuda")
+    sin = [-1 if f else int(s) for s, f in zip(slots, fresh)]
+    o = torch.empty(T, Hv, D, dtype=torch.float16, device="cuda")
+    st = torch.zeros(1, **i32)
+    tb.tb_gated_delta(q, k, v, g, beta, starts(lens), max(lens), o, workspace(T, B, max(lens), Hk, Hv), state_in=pool, state_out=pool,
+                      slot_in=torch.tensor(sin, **i32), slot_out=torch.tensor(slots, **i32), normalise=True, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    init = torch.stack([before[s] if s >= 0 else torch.zeros_like(before[0]) for s in sin])
+    check(o, pool[torch.tensor(slots, device="cuda")], (q, k, v, g, beta), lens, init, True)
+    for r in set(range(B + 3)) - set(slots.tolist()):
+        assert torch.equal(pool[r], before[r])
