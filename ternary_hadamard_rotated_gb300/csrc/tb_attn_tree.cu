@@ -65,10 +65,16 @@ struct TaArgs {
   int2* meta;                          // [B * head_parts * row_tiles]: an item's first CTA, and how many
 };
 
+// Do a request's rows and length fit the arguments?  One that does not has no units and no entry in meta, which
+// has room for max_q rows a request; the joining kernel writes its zeros.
+TB_DEVI bool ta_fits(const AttnArgs& a, int64_t n, int64_t len) {
+  return n <= a.max_q && len >= n && len <= a.max_pages << a.page_log2;
+}
+
 // a run of key tiles of one item
 struct TaSegment {
   int b, hp, rt;
-  int tile0, tiles, item_tiles;  // tiles 0: an item whose rows get zeros
+  int tile0, tiles, item_tiles;
   int64_t q0, n, len;            // the request's first row, rows, and cached tokens
   unsigned item_unit;            // the item's first unit
 };
@@ -127,7 +133,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   // ---- the schedule: every warp adds up the units of all requests itself
   struct Req {
     int64_t q0, n, len;
-    int items, tiles;  // items 0: nothing to write
+    int items, tiles;  // items 0: no rows, or not to be computed
     int bad;
   };
   auto request = [&](int b) {
@@ -140,11 +146,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       r.bad = 1;
       r.n = 0;
     }
-    if (r.n > 0 && (r.n > a.max_q || r.len < r.n || r.len > a.max_pages << a.page_log2)) {
+    if (r.n > 0 && !ta_fits(a, r.n, r.len)) {
       r.bad = 1;
-      r.len = 0;
+      r.n = 0;
     }
-    r.items = ((int)r.n + p.tok - 1) / p.tok * p.head_parts;
+    r.items = ((int)r.n + p.tok - 1) / p.tok * p.head_parts;  // (at most row_tiles * head_parts)
     const int64_t t = (r.len + kTaKeys - 1) / kTaKeys;
     r.tiles = t > 0 ? (int)t : 1;
     return r;
@@ -251,7 +257,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     for (unsigned u = lo; u < hi;) {
       const TaSegment s = segment(u);
       u += s.tiles;
-      if (s.len == 0) continue;
       const int hk = s.hp / parts, h0 = hk * G + (s.hp % parts) * p.gp;
       const int32_t* row = a.table + (int64_t)s.b * a.max_pages;
       // page of the 16-key run that this lane (0-7) looks up; -1 past the last token or the segment
@@ -329,7 +334,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     for (unsigned u = lo; u < hi;) {
       const TaSegment s = segment(u);
       u += s.tiles;
-      if (s.len == 0) continue;
       if (lane == 0) {
         // descriptors of place 0; the address field counts 16 bytes, and no sum carries out of it
         const uint64_t qdesc = smem_desc_sw128(base, 1024), kdesc = smem_desc_sw128(ring, 1024);
@@ -397,11 +401,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       const int64_t tq = (int64_t)s.rt * p.tok + tr;  // token of the request
       const bool live = tr < p.tok && tq < s.n;
       __half* dst = a.o + ((s.q0 + tq) * a.Hq + head) * D;
-      if (s.len == 0) {  // lengths that do not fit: zeros
-        if (live)
-          for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
-        continue;
-      }
       const int64_t prefix = s.len - s.n;
       uint64_t word = 0;
       if (live) {
@@ -621,6 +620,10 @@ __global__ void __launch_bounds__(W * 32) tree_join_kernel(const TaArgs p) {
   const int64_t q0 = __ldg(a.q_start + b), n = __ldg(a.q_start + b + 1) - q0, len = __ldg(a.total + b);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
   if (q0 < 0 || t < q0 || t >= q0 + n || q0 + n > a.T) return;
+  if (!ta_fits(a, n, len)) {
+    for (int c = threadIdx.x * 2; c < D; c += W * 64) *reinterpret_cast<__half2*>(a.o + (t * a.Hq + h) * D + c) = __floats2half2_rn(0.f, 0.f);
+    return;
+  }
   const int G = a.Hq / a.Hkv, parts = G / p.gp, hk = h / G;
   const int hp = hk * parts + (h - hk * G) / p.gp;
   const int tq = (int)(t - q0), rt = tq / p.tok;

@@ -348,3 +348,39 @@ def test_other_stream():
     tb.tb_prompt_attention(q, k, k, starts([200]), starts([200]), b, stream=s)
     s.synchronize()
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,max_q,n", [(6, 2, 128, 1, 5), (6, 2, 64, 3, 130), (1, 1, 64, 1, 20000), (4, 2, 256, 64, 65)])
+@pytest.mark.parametrize("why", ["rows", "short", "long"])
+def test_tree_lengths_that_do_not_fit_among_others_that_do(Hq, Hkv, D, max_q, n, why):
+    """A request of more rows than max_q, or whose length does not fit, before requests whose keys are spread over
+    many CTAs and between them: zeros for it, the others as ever, and nothing written past the workspace."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    rng = np.random.default_rng(n)
+    page, width = 64, 100
+    bad = n if why == "rows" else max_q
+    fresh = [bad, max_q, bad, 1, bad]
+    wrong = {"rows": max(n, 70) if n < 6400 else 6400, "short": max_q - 1, "long": width * page + 1}[why]
+    total = [wrong, 6000, wrong, 3000, wrong]
+    table = np.full((5, width), -1, dtype=np.int32)
+    table[1], table[3] = rng.permutation(width), rng.permutation(width)
+    kc, vc = (rng.standard_normal((width, Hkv, page, D)).astype(np.float16) for _ in range(2))
+    T, i32 = sum(fresh), dict(dtype=torch.int32, device="cuda")
+    q = torch.randn(T, Hq, D, generator=torch.Generator().manual_seed(n)).half().cuda()
+    full, o = guarded(T, Hq, D)
+    size = tb.tb_tree_attention_workspace_size(5, T, max_q, Hq, Hkv, D)
+    ws = torch.full((size + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    st = torch.zeros(1, **i32)
+    tb.tb_tree_attention(q, torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(), torch.from_numpy(table).cuda(), torch.tensor(total, **i32),
+                         starts(fresh), max_q, o, ws[:size], dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == tb.TB_DEV_BAD_LEN
+    assert (ws[size:] == 0xA5).all() and (full[T:] == 7.0).all()
+    row = starts(fresh).tolist()
+    for b in (0, 2, 4):
+        assert (o[row[b]: row[b + 1]] == 0).all(), b
+    for b in (1, 3):
+        part = slice(row[b], row[b + 1])
+        want, tol = mixers.tree_attention(q[part].cpu().numpy(), kc, vc, table[b: b + 1], [total[b]], [0, fresh[b]], None, D ** -0.5)
+        close(o[part], want, tol, (b, why))
