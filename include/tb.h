@@ -499,7 +499,8 @@ int tb_prompt_attention(const uint16_t* q, int64_t ldq, const uint16_t* k, int64
  * (TB_ERR_UNSUPPORTED).  workspace: at least tb_gated_delta_workspace_size(T, B, max_len, Hk, Hv)
  * bytes of scratch (may be 0); its contents do not matter; calls that share one are ordered on one
  * stream.  dev_status optional: TB_DEV_BAD_ID (a slot past its pool: taken as negative),
- * TB_DEV_BAD_LEN (row starts out of order or past T: that request is taken as empty).
+ * TB_DEV_BAD_LEN (row starts out of order or past T: that request is taken as empty; so are the last
+ * requests where row starts that go back make them more together than T tokens and B requests can be).
  */
 size_t tb_gated_delta_workspace_size(int64_t T, int64_t B, int64_t max_len, int64_t Hk, int64_t Hv);
 int tb_gated_delta(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v,

@@ -84,6 +84,19 @@ TB_DEVI ChunkScan chunk_scan(const DeltaArgs& a, int lane) {
   return s;
 }
 
+// Chunks that the workspace has room for and kernel 1 makes.  Requests in order, one after another, have no more
+// (ceil(x) <= floor(x) + 1); where row starts go back, requests that lie in [0, T] one by one can have more
+// together, and those whose chunks come later than this are not computed.
+TB_DEVI int64_t chunk_room(const DeltaArgs& a) { return a.T / kDcTok + a.B; }
+// the request's first chunk among all requests' (whole warps call this)
+TB_DEVI int64_t first_chunk(const DeltaArgs& a, const ChunkScan& s, int b, int lane) {
+  int64_t first = s.upto - s.own;
+  const int src = b / s.per;
+  if (lane == src)
+    for (int r = lane * s.per; r < b; ++r) first += chunks_of(a, r);
+  return __shfl_sync(0xffffffffu, first, src);
+}
+
 // (volatile keeps them in order with barriers and waits, which are volatile too and clobber memory)
 TB_DEVI void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -584,6 +597,8 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       for (int e = 0; e < 2; ++e) rank[e] += other > mine[e] || (other == mine[e] && i < lane + 32 * e);
     }
   }
+  const ChunkScan sc = chunk_scan(a, lane);
+  const bool crowded = __shfl_sync(0xffffffffu, sc.upto, 31) > chunk_room(a);
   // the i-th item of this CTA: a request, a value head and half of its columns; CTAs take turns back and
   // forth.  False: no more.
   struct Item {
@@ -608,6 +623,10 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       it.len = 0;
     }
     it.nc = (int)((it.len + kDcTok - 1) / kDcTok);
+    if (crowded && first_chunk(a, sc, it.b, lane) + it.nc > chunk_room(a)) {
+      if (tid == 0 && rest == 0) set_status(a.status, TB_DEV_BAD_LEN);
+      it.len = it.nc = 0;
+    }
     return true;
   };
   for (int i = tid; i < 256; i += kD2Threads) spoilt[i] = INT_MAX;
@@ -632,7 +651,6 @@ __global__ void __launch_bounds__(kD2Threads, 1)
   };
 
   if (warp == kD2Warps) {
-    const ChunkScan sc = chunk_scan(a, lane);
     int loaded = 0, looked = 0, states = 0;  // chunks of all items; states
     auto load = [&](const Item& it, int64_t first, int c) {  // a lane per copy
       const int s = loaded % kD2Stages, row = (int)it.t0 + c * kDcTok;
@@ -714,11 +732,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
     int* last_spoilt = spoilt;
     for (int i = 0; item_at(i, it); ++i) {
       if (it.nc == 0) continue;
-      int64_t first = sc.upto - sc.own;  // the request's first chunk
-      const int src = it.b / sc.per;
-      if (lane == src)
-        for (int r = lane * sc.per; r < it.b; ++r) first += chunks_of(a, r);
-      first = __shfl_sync(0xffffffffu, first, src);
+      const int64_t first = first_chunk(a, sc, it.b, lane);
       for (int c = 0; c < it.nc; ++c) {
         const int64_t si = c == 0 && a.state_in ? delta_slot(a.slot_in, it.b, a.n_in, a.status) : -1;
         const bool first_state = si >= 0 && states == 0;
@@ -1068,7 +1082,7 @@ static int launch_scan(const ChunkArgs& p, const DeviceFacts& f, cudaStream_t s)
 }
 
 size_t delta_chunk_workspace(int64_t T, int64_t B, int64_t Hv) {
-  return (size_t)((T / kDcTok + B) * Hv) * kDcItem;  // at most: ceil(x) <= floor(x) + 1 per request
+  return (size_t)((T / kDcTok + B) * Hv) * kDcItem;  // chunk_room() of them
 }
 
 int launch_delta_chunks(const DeltaArgs& a, void* workspace, cudaStream_t s) {

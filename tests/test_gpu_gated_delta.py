@@ -311,3 +311,32 @@ def test_many_requests_with_and_without_a_first_state(B):
     check(o, pool[torch.tensor(slots, device="cuda")], (q, k, v, g, beta), lens, init, True)
     for r in set(range(B + 3)) - set(slots.tolist()):
         assert torch.equal(pool[r], before[r])
+
+
+@pytest.mark.parametrize("B", [3, 9, 81])
+@pytest.mark.parametrize("T", [640, 650])
+def test_row_starts_that_go_back(B, T):
+    """Requests 0, 2, 4, .. all have rows [0, T), those between them run backwards: together they have more chunks
+    than T tokens and B requests in order could.  What does not fit is taken as empty."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    Hk, Hv = 1, 2
+    q, k, v, g, beta, init = make(30, [T], Hk, Hv, True)
+    init = init.expand(B, -1, -1, -1).contiguous() * torch.arange(1, B + 1, device="cuda").view(-1, 1, 1, 1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    rows = torch.tensor([0, T] * ((B + 1) // 2), **i32)
+    assert rows.numel() == B + 1
+    o = torch.full((T + 1, Hv, D), 7.0, dtype=torch.float16, device="cuda")
+    out = torch.full_like(init, 5.0)
+    st = torch.zeros(1, **i32)
+    tb.tb_gated_delta(q, k, v, g, beta, rows, T, o[:T], workspace(T, B, T, Hk, Hv), state_in=init, state_out=out, normalise=True, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == tb.TB_DEV_BAD_LEN and (o[T:] == 7.0).all()
+    room, chunks, used = T // 64 + B, -(-T // 64), 0
+    for b in range(B):
+        if b % 2 or used + chunks > room:
+            assert torch.equal(out[b], init[b]), b
+        else:
+            fin = mixers.gated_delta(*(x.cpu().numpy() for x in (q, k, v, g, beta)), [0, T], init[b: b + 1].cpu().numpy(), True, D ** -0.5)[1][0]
+            assert np.linalg.norm(out[b].double().cpu().numpy() - fin) <= 2.0 ** -17 * np.linalg.norm(fin), b
+        used += 0 if b % 2 else chunks
