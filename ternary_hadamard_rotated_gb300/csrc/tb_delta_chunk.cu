@@ -3,13 +3,16 @@
 //
 // Inside a chunk, with gamma_i the decays' running sum, D_ij = exp(gamma_i - gamma_j) for j <= i, S the
 // state before the chunk, and q, k already divided by their norms:
-//   A_ij = beta_i (k_i . k_j) D_ij  (j < i),     T = (I + A)^-1 diag(beta)
-//   R_i  = v_i - exp(gamma_i) S^T k_i,           U = T R
+//   A_ij = (k_i . k_j) D_ij beta_j  (j < i),     T = (I + A)^-1
+//   R_i  = v_i - exp(gamma_i) S^T k_i,           U = diag(beta) T R
 //   o_i  = scale (exp(gamma_i) S^T q_i + sum_{j <= i} (q_i . k_j) D_ij u_j)
 //   S   <- exp(gamma_C) S + sum_j exp(gamma_C - gamma_j) k_j u_j^T
 // T does not depend on the state, so one kernel computes it for all chunks at once, and with it
-// P T, P_ij = scale (q_i . k_j) D_ij: the second kernel then gets U and the chunk's own part of o from
-// one product [T; P T] R.
+// P T, P_ij = scale (q_i . k_j) D_ij beta_j: the second kernel then gets U and the chunk's own part of o from
+// one product [T; P T] R.  The steps beta stand where no fp16 operand depends on their size: T has ones on its
+// diagonal and, as a step contracts (beta |k|^2 <= 2), nothing above beta_j |k_i| |k_j| beside it; P T, below
+// scale max|q| max(beta |k|), goes under a power of two a chunk and head; and U's rows take beta in fp32.  (With
+// diag(beta) inside T, steps below 2^-14 were left with the bits of fp16's subnormal numbers.)
 //
 // Kernel 1, a CTA per (chunk, key head), which its value heads share: K K^T and Q K^T by mma.sync (fp16
 // inputs, exact products), per value head the triangular system by blocks of 16 and P T.  It writes T
@@ -52,9 +55,13 @@ constexpr int kDcBlock = kDcTok * 128;  // bytes of a 64 x 64 fp16 image
 // fragments of mma.sync: 16 bytes a lane.
 constexpr int kDcFrag = 512, kDcMatrix = 10 * kDcFrag;
 constexpr int kDcItem = 16384;
-// floats: c [64], w [64], q [64], exp(gamma_C), and the tokens before the first whose k, decay or step
-// is not finite
+// floats: c [64], w [64], q [64], exp(gamma_C), the tokens before the first whose k, decay or step is not
+// finite, and what takes P T's power of two off again
 constexpr int kDcFactors = 3 * kDcMatrix;
+// The powers of two of P T, and of R against S, stay within 2^+-36, so that their product with a sum of 2^37
+// (S^T q) stays inside fp32.  P T below 2^-36 2^-25 adds nothing to an fp16 output, nor does R below 2^-36 of S
+// to a state in fp32.
+constexpr int kDcPScale = 36;
 
 struct ChunkArgs {
   DeltaArgs a;
@@ -173,12 +180,14 @@ static_assert(2 * kD1KQ >= 4 * kDcBlock, "two heads' images take the place of K 
 
 // Warp w has rows 16 w .. of the chunk's matrices, as accumulator tiles of 8 columns.  (I + A)^-1 block by
 // block of 16: the diagonal blocks D_w by substitution (a lane per column), then with E = D A (left of
-// the diagonal) T_w = D_w diag(beta) - sum_{s < w} E_ws T_s, one block row a step, fp32 factors in two
+// the diagonal) T_w = D_w - sum_{s < w} E_ws T_s, one block row a step, fp32 factors in two
 // fp16 terms (three products).  P T goes along, P from Q K^T's accumulators as they are.
 __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkArgs p) {
   const DeltaArgs& a = p.a;
   __shared__ __align__(1024) uint8_t kq[2 * kD1KQ];
   __shared__ float rk[64], rq[64];
+  __shared__ float nk[64], nq[64];  // the norms of k as it enters and of scale q
+  __shared__ float pscale[4];       // P's power of two
   __shared__ float2 gam[4][64];  // running sums of the decays in log2 units, high and low part
   __shared__ float bet[4][64];
   __shared__ int sound[4];       // tokens before the first whose k, decay or step is not finite
@@ -262,8 +271,14 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
     const int r = lane & 15, row = (r & 7) * 8 + (tid >> 4);
     float inv = a.normalise ? 1.f / sqrtf(v[0] + kDeltaEps) : 1.f;
     if (!(v[0] < INFINITY)) inv = NAN;
-    if (r < 8) rk[row] = inv;
-    else rq[row] = inv * a.scale;
+    const float norm = sqrtf(v[0]) * inv;
+    if (r < 8) {
+      rk[row] = inv;
+      nk[row] = norm;
+    } else {
+      rq[row] = inv * a.scale;
+      nq[row] = norm < INFINITY ? norm * fabsf(a.scale) : 0.f;
+    }
   }
   __syncthreads();
 
@@ -324,12 +339,22 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
         const int f0 = bad[0] ? (__ffs(bad[0]) - 1) * 2 : 64, f1 = bad[1] ? (__ffs(bad[1]) - 1) * 2 + 1 : 64;
         const int ok = f0 < f1 ? f0 : f1;
         if (lane == 0) sound[warp] = ok;
+        float most_b = 0.f;  // the largest beta |k|
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float gv = next_g[e] < -200.f ? -200.f : next_g[e];  // e^-200 is 0 in fp32 already
           hi[e] = gv * 1.44269502f;  // times log2 e, in two parts as well
           lo[e] = fmaf(gv, 1.44269502f, -hi[e]) + gv * 1.92596303e-8f;
-          bet[warp][lane * 2 + e] = lane * 2 + e < ok ? next_b[e] : 0.f;
+          const bool in = lane * 2 + e < ok;
+          bet[warp][lane * 2 + e] = in ? next_b[e] : 0.f;
+          if (in) most_b = fmaxf(most_b, fabsf(next_b[e]) * nk[lane * 2 + e]);
+        }
+        most_b = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most_b)));
+        const float most_q = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(nq[lane * 2], nq[lane * 2 + 1]))));
+        if (lane == 0) {  // takes the bound of P T to 2^12 .. 2^13, an eighth of what fp16 holds
+          int e = 266 - (int)(__float_as_uint(most_b * most_q) >> 23);
+          e = e < 127 - kDcPScale ? 127 - kDcPScale : (e > 127 + kDcPScale ? 127 + kDcPScale : e);
+          pscale[warp] = __int_as_float(e << 23);
         }
         add_pair(hi[1], lo[1], hi[0], lo[0]);
         float sh = hi[1], sl = lo[1];
@@ -357,11 +382,12 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
       const float2 mine = gm[tid], last = gm[63];
       const float eg = ex2(mine.x) * (1.f + 0.6931472f * mine.y);
       f[tid] = tid < sound[slot] ? eg * rk[tid] : 0.f;  // (0 where kernel 2 has a row of zeros)
-      f[64 + tid] = ex2((last.x - mine.x) + (last.y - mine.y)) * rk[tid];
-      f[128 + tid] = eg * rq[tid];
+      f[64 + tid] = tid < sound[slot] ? ex2((last.x - mine.x) + (last.y - mine.y)) * rk[tid] * be[tid] : 0.f;
+      f[128 + tid] = eg * rq[tid] * pscale[slot];
       if (tid == 0) {
         f[192] = ex2(last.x) * (1.f + 0.6931472f * last.y);
         f[193] = (float)sound[slot];
+        f[194] = 1.f / pscale[slot];
       }
     }
     // A (fp32, as accumulator tiles), P (two fp16 terms, as the left factor's tiles)
@@ -369,8 +395,8 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
     uint32_t P[4][4], Pl[4][4];
     {
       const float2 g0 = gm[i0], g1 = gm[i0 + 8];
-      const float b0 = be[i0], b1 = be[i0 + 8];
       const int ok = sound[slot];
+      const float ps = pscale[slot];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (j > 2 * warp + 1) {
@@ -383,8 +409,9 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
           const float2 gk = gm[k], gi = (e >> 1) ? g1 : g0;
           const bool in = i < ok;
           const float d = in && k <= i ? ex2((gi.x - gk.x) + (gi.y - gk.y)) : 0.f;
-          A[j][e] = in && k < i ? ((e >> 1) ? b1 : b0) * G[j][e] * d : 0.f;
-          pv[e] = in && k <= i ? QK[j][e] * d : 0.f;
+          const float db = d * be[k];
+          A[j][e] = in && k < i ? G[j][e] * db : 0.f;
+          pv[e] = in && k <= i ? QK[j][e] * db * ps : 0.f;
         }
         split2(pv[0], pv[1], P[j >> 1][(j & 1) * 2], Pl[j >> 1][(j & 1) * 2]);
         split2(pv[2], pv[3], P[j >> 1][(j & 1) * 2 + 1], Pl[j >> 1][(j & 1) * 2 + 1]);
@@ -453,13 +480,13 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
           split2(x[0], x[1], eh[s][q], el[s][q]);
         }
     }
-    // T's rows start from D diag(beta)
+    // T's rows start from D
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         T[j][e] = 0.f;
-        if (j >> 1 == warp) T[j][e] = diag[warp][g + (e >> 1) * 8][(j & 1) * 8 + t2 + (e & 1)] * be[j * 8 + t2 + (e & 1)];
+        if (j >> 1 == warp) T[j][e] = diag[warp][g + (e >> 1) * 8][(j & 1) * 8 + t2 + (e & 1)];
       }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -551,12 +578,12 @@ constexpr int kD2Bytes = 5 * kDcBlock + kDcItem;  // loaded per chunk
 constexpr int kD2StatePitch = 64 * 4 + 16, kD2State = kDeltaD * kD2StatePitch;
 constexpr int kD2Smem = 1024 + kD2Stages * kD2Stage + kD2State + 128 + 1024;
 
-// a power of two that takes the warp's largest magnitude to 2^14, and its inverse
-TB_DEVI float operand_scale(const float (&most)[2], float& inverse) {
+// a power of two that takes the warp's largest magnitude to 2^14, 2^(top - 127) at most, and its inverse
+TB_DEVI float operand_scale(const float (&most)[2], float& inverse, int top = 127 + 100) {
   const float m = fmaxf(most[0], most[1]);
   const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));  // orders as the values do
   int e = 268 - (int)(bits >> 23);
-  e = e < 127 - 100 ? 127 - 100 : (e > 127 + 100 ? 127 + 100 : e);
+  e = e < 127 - 100 ? 127 - 100 : (e > top ? top : e);
   inverse = __int_as_float((254 - e) << 23);
   return __int_as_float(e << 23);
 }
@@ -882,7 +909,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
         if ((ks & 1) && ks < 7) ldsm4_trans(V + (ks / 2 + 1) * 2048 + v_row + v_pc, vv);
       }
       float down_r;
-      const float up_r = operand_scale(big, down_r);
+      const float up_r = operand_scale(big, down_r, min((int)(__float_as_uint(up_s) >> 23) + kDcPScale, 127 + 100));
       uint32_t rh[4][4], rl[4][4];
       auto split_r = [&](int ks, int q) {
         split2(R[2 * ks + (q >> 1)] + (q & 1) * 2, up_r, rh[ks][q], rl[ks][q]);
@@ -965,7 +992,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       for (int q = 0; q < 4; ++q) split_u(0, q);
       // S <- exp(gamma_C) S + K^T (w U); the increment is summed by itself, so that the state's own
       // rounding is one fp32 fma a chunk.  Beside it o goes out, back in rows of tokens.
-      const float dec = lds2(X + kDcFactors + 192 * 4).x;
+      const float dec = lds2(X + kDcFactors + 192 * 4).x, down_o = lds2(X + kDcFactors + 194 * 4).x * down_r;
       sbig[0] = sbig[1] = 0.f;
       auto at_k = [&](int i) {  // step i: 16 columns i / 4 of k, 16 tokens i % 4
         const int j = i >> 2;
@@ -1010,11 +1037,11 @@ __global__ void __launch_bounds__(kD2Threads, 1)
           if (j > 0 && ks == 2) add_up(j - 1, 1);
           mma_16816(dl[z][0], rl[ks], kt[x][0], kt[x][1]);
           if (ks == 0) {
-            mul_pair(O[j], make_float2(down_r, down_r));
+            mul_pair(O[j], make_float2(down_o, down_o));
             ox = transpose8x8(pack_half2(O[j][0], O[j][1]));
           }
           if (ks == 1) {
-            mul_pair(O[j] + 2, make_float2(down_r, down_r));
+            mul_pair(O[j] + 2, make_float2(down_o, down_o));
             oy = transpose8x8(pack_half2(O[j][2], O[j][3]));
           }
           mma_16816(dl[z][1], rl[ks], kt[x][2], kt[x][3]);

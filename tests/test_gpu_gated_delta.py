@@ -340,3 +340,51 @@ def test_row_starts_that_go_back(B, T):
             fin = mixers.gated_delta(*(x.cpu().numpy() for x in (q, k, v, g, beta)), [0, T], init[b: b + 1].cpu().numpy(), True, D ** -0.5)[1][0]
             assert np.linalg.norm(out[b].double().cpu().numpy() - fin) <= 2.0 ** -17 * np.linalg.norm(fin), b
         used += 0 if b % 2 else chunks
+
+
+def small_steps_case(seed, n, step, rate=(-6, 0.5), v_scale=50.0, k_norm=None, scale=None, Hk=1, Hv=3):
+    """Zero first state, chunked; step: beta [T, Hv] of the (T, Hv) shape it is given."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    q, k, v, g, beta, init = make(seed, [n], Hk, Hv, k_norm is None, rate=rate)
+    v = (v.float() * v_scale).half()
+    if k_norm is not None:
+        k, q = (k.float() * k_norm).half(), (q.float() * k_norm).half()
+    beta = step(beta)
+    init = torch.zeros_like(init)
+    o = torch.empty(n, Hv, D, dtype=torch.float16, device="cuda")
+    out = torch.empty_like(init)
+    scale = D ** -0.5 if scale is None else scale
+    tb.tb_gated_delta(q, k, v, g, beta, starts([n]), n, o, workspace(n, 1, n, Hk, Hv), state_in=init, state_out=out, normalise=k_norm is None, scale=scale)
+    # (check's sum of absolute terms takes the scale's sign along)
+    check(o if scale > 0 else -o, out, (q, k, v, g, beta), [n], init, k_norm is None, abs(scale))
+
+
+@pytest.mark.parametrize("step", [1e-2, 1e-4, 1e-6, 1e-9])
+def test_chunks_of_small_steps(step):
+    """The state's and the outputs' precision does not hang on the steps' size."""
+    small_steps_case(21, 200, lambda beta: beta * step)
+
+
+def test_chunks_of_steps_of_every_size():
+    """Steps from 2^-30 to 1 in one chunk, the large ones forgotten behind decays of e^-8 and more."""
+    gen = torch.Generator().manual_seed(3)
+
+    def spread(beta):
+        return torch.exp2(-30 * torch.rand(beta.shape, generator=gen)).cuda()
+
+    small_steps_case(22, 200, spread)
+    small_steps_case(23, 150, spread, rate=(2.0, 5.0))
+
+
+@pytest.mark.parametrize("k_norm", [1e-2, 30.0, 200.0])
+def test_chunks_of_keys_that_are_not_normalised(k_norm):
+    """Keys and queries c times longer and steps c^2 times smaller: the recurrence of c = 1 with states c
+    times smaller, so that the same bounds hold."""
+    small_steps_case(24, 200, lambda beta: beta / k_norm ** 2, k_norm=k_norm)
+
+
+@pytest.mark.parametrize("scale,v_scale", [(1e-6, 1000.0), (-1e-4, 50.0), (20.0, 1.0)])
+def test_chunks_under_any_scale(scale, v_scale):
+    """check() asks for 2^-25 beside the relative bounds; outputs here are at least a hundred times that."""
+    small_steps_case(25, 130, lambda beta: beta, v_scale=v_scale, scale=scale)
