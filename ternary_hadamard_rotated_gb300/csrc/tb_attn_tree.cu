@@ -21,7 +21,8 @@
 // Warps 0-3: softmax (thread = row) and epilogue; 4: TMA loads (pages by the block table); 5: MMAs.
 // V rows past the request's last token are zeroed in shared memory before the MMAs read them (what
 // lies there may be anything); a row whose output is not finite is computed again from the keys it
-// sees alone (attend_row).
+// sees alone (attend_keys), by the joining kernel, where nothing waits under a limit: a CTA a row, the keys shared
+// out among its warps (one token over 131072 keys, one value of them NaN: 9.5 ms, without it 0.1).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -522,9 +523,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       tmem_fence_after();
       const bool whole = s.tiles == s.item_tiles;
       const int64_t slot = (int64_t)blockIdx.x * 2 + (s.tile0 == 0);
-      const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+      const float inv = whole ? inverse_sum(l) : 1.f;
       const bool none = l == 0.f;  // the row saw nothing here: what the MMAs left is 0 times V
-      bool odd = !(l < INFINITY);
       // through shared memory, so that a store instruction covers whole runs of a few rows (a thread's own
       // row at a time it touches 32: the drafts above took 28.0 us instead of 25.5)
       const uint32_t stage = base + kTaRing + (uint32_t)warp * 4096u;
@@ -543,8 +543,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t w[4];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) odd |= !(fabsf(o[e * 8 + y]) < INFINITY);
 #pragma unroll
             for (int y = 0; y < 4; ++y) w[y] = pack_half2(o[e * 8 + 2 * y] * inv, o[e * 8 + 2 * y + 1] * inv);
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(piece(lane, e)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
@@ -577,17 +575,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free);
-      if (!whole) {
-        if (live) *reinterpret_cast<float2*>(p.part_ml + (slot * p.rows + row) * 2) = make_float2(m, l);
-        continue;
-      }
-      unsigned again = __ballot_sync(0xffffffffu, live && odd);
-      while (again) {
-        const int r = __ffs(again) - 1;
-        again &= again - 1;
-        attend_row<D, true>(a, __shfl_sync(0xffffffffu, s.q0 + tq, r), __shfl_sync(0xffffffffu, head, r), s.b, 0, s.len,
-                            prefix, __shfl_sync(0xffffffffu, word, r), lane);
-      }
+      if (whole)
+        for (unsigned lost = __ballot_sync(0xffffffffu, live && !(l < INFINITY)); lost; lost &= lost - 1) {
+          const int64_t to = __shfl_sync(0xffffffffu, begin, __ffs(lost) - 1);
+          for (int c = lane; c < D; c += 32) a.o[to + c] = __ushort_as_half((unsigned short)kNanRow);
+        }
+      else if (live) *reinterpret_cast<float2*>(p.part_ml + (slot * p.rows + row) * 2) = make_float2(m, l);
     }
   }
 
@@ -598,9 +591,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 
 // ---------------------------------------------------------------- parts -> output
 // One CTA of W warps per (row, head): the warps share the parts of the row's item, the lanes the columns;
-// rows of items that one CTA finished are done already.  The order of the sums is fixed by the schedule.
+// rows of items that one CTA finished are done already.  The order of the sums is fixed by the schedule.  A row that
+// is not finite, of parts or done, is made again from its keys.
 template <int D, int W>
-__global__ void __launch_bounds__(W * 32) tree_join_kernel(const TaArgs p) {
+__global__ void __launch_bounds__(W * 32, 32 / W) tree_join_kernel(const TaArgs p) {
   const AttnArgs& a = p.a;
   constexpr int E = D / 32;  // columns of a lane: lane * 2 + 64 i (+ 1)
   __shared__ float acc_s[W][D];
@@ -628,67 +622,82 @@ __global__ void __launch_bounds__(W * 32) tree_join_kernel(const TaArgs p) {
   const int hp = hk * parts + (h - hk * G) / p.gp;
   const int tq = (int)(t - q0), rt = tq / p.tok;
   const int2 meta = p.meta[((int64_t)b * p.head_parts + hp) * p.row_tiles + rt];
-  if (meta.y < 2) return;
+  __half* out = a.o + (t * a.Hq + h) * D;
+  bool redo = false;
+  if (meta.y < 2) {
+    bool bad = false;
+    for (int c = threadIdx.x * 2; c < D; c += W * 64) {
+      const uint32_t x[1] = {__ldcg(reinterpret_cast<const unsigned*>(out + c))};
+      bad |= any_to_mend(x);
+    }
+    redo = __syncthreads_or(bad);
+    if (!redo) return;
+  }
   const int row = (tq - rt * p.tok) * p.gp + (h - hk * G) % p.gp;
   // part i is CTA meta.x + i's: its first segment (0), or for the item's first CTA its last (1)
   auto at = [&](int i) { return (int64_t)(2 * (meta.x + i) + (i == 0)) * p.rows + row; };
-  // each warp takes every W-th part with a running maximum; parts without a key have a sum of 0 and
-  // zeros, whatever their weight
-  float acc[E], M = -INFINITY, L = 0.f;
+  for (;; redo = true) {
+    // each warp takes every W-th part, or key, with a running maximum; parts without a key have a sum of 0 and
+    // zeros, whatever their weight
+    float acc[E], M = -INFINITY, L = 0.f;
+    if (!redo) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+      for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-  for (int i = warp; i < meta.y; i += W) {
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at(i) * 2));
-    const float* src = p.part_o + at(i) * D + lane * 2;
-    float2 y[E / 2];
+      for (int i = warp; i < meta.y; i += W) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at(i) * 2));
+        const float* src = p.part_o + at(i) * D + lane * 2;
+        float2 y[E / 2];
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) y[e] = __ldcg(reinterpret_cast<const float2*>(src + e * 64));
-    const float m2 = fmaxf(M, ml.x);
-    const float c = M == m2 ? 1.f : ex2(M - m2), w = ml.x == m2 ? 1.f : ex2(ml.x - m2);
-    L = fmaf(w, ml.y, L * c);
+        for (int e = 0; e < E / 2; ++e) y[e] = __ldcg(reinterpret_cast<const float2*>(src + e * 64));
+        const float m2 = fmaxf(M, ml.x);
+        const float c = M == m2 ? 1.f : ex2(M - m2), w = ml.x == m2 ? 1.f : ex2(ml.x - m2);
+        L = fmaf(w, ml.y, L * c);
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) {
-      acc[2 * e] = fmaf(w, y[e].x, acc[2 * e] * c);
-      acc[2 * e + 1] = fmaf(w, y[e].y, acc[2 * e + 1] * c);
+        for (int e = 0; e < E / 2; ++e) {
+          acc[2 * e] = fmaf(w, y[e].x, acc[2 * e] * c);
+          acc[2 * e + 1] = fmaf(w, y[e].y, acc[2 * e + 1] * c);
+        }
+        M = m2;
+      }
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<float2*>(&acc_s[warp][e * 32 + lane * 2]) = make_float2(acc[e], acc[e + 1]);
+    } else {
+      uint64_t word = a.tree ? (uint64_t)__ldg(reinterpret_cast<const long long*>(a.tree) + t) : ~0ull >> (63 - tq);
+      if (n < 64) word &= (1ull << n) - 1;
+      attend_keys<D, true>(a, t, h, b, 0, warp, W, len, len - n, word, lane, M, L, acc);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(&acc_s[warp][lane * E + e]) = make_float2(acc[e], acc[e + 1]);
     }
-    M = m2;
-  }
+    if (lane == 0) {
+      ml_s[warp][0] = L;
+      ml_s[warp][1] = M;
+    }
+    __syncthreads();
+    M = -INFINITY;
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<float2*>(&acc_s[warp][e * 32 + lane * 2]) = make_float2(acc[e], acc[e + 1]);
-  if (lane == 0) {
-    ml_s[warp][0] = L;
-    ml_s[warp][1] = M;
-  }
-  __syncthreads();
-  M = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < W; ++w) M = fmaxf(M, ml_s[w][1]);
-  float f[W];
-  L = 0.f;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    f[w] = ml_s[w][1] == M ? 1.f : ex2(ml_s[w][1] - M);
-    L = fmaf(f[w], ml_s[w][0], L);
-  }
-  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-  bool bad = !(L < INFINITY);
-  __half* out = a.o + (t * a.Hq + h) * D;
-  for (int c = threadIdx.x * 2; c < D; c += W * 64) {
-    float x = 0.f, y = 0.f;
+    for (int w = 0; w < W; ++w) M = fmaxf(M, ml_s[w][1]);
+    float f[W];
+    L = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      x = fmaf(f[w], acc_s[w][c], x);
-      y = fmaf(f[w], acc_s[w][c + 1], y);
+      f[w] = ml_s[w][1] == M ? 1.f : ex2(ml_s[w][1] - M);
+      L = fmaf(f[w], ml_s[w][0], L);
     }
-    bad |= !(fabsf(x) < INFINITY) || !(fabsf(y) < INFINITY);
-    *reinterpret_cast<__half2*>(out + c) = __floats2half2_rn(x * inv, y * inv);
-  }
-  if (__syncthreads_or(bad) && warp == 0) {
-    uint64_t word = a.tree ? (uint64_t)__ldg(reinterpret_cast<const long long*>(a.tree) + t) : ~0ull >> (63 - tq);
-    if (n < 64) word &= (1ull << n) - 1;
-    attend_row<D, true>(a, t, h, b, 0, len, len - n, word, lane);
+    const float inv = inverse_sum(L);
+    bool bad = false;  // (a sum that is not finite leaves NaN, and that is right)
+    for (int c = threadIdx.x * 2; c < D; c += W * 64) {
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        x = fmaf(f[w], acc_s[w][c], x);
+        y = fmaf(f[w], acc_s[w][c + 1], y);
+      }
+      bad |= L < INFINITY && (!(fabsf(x) < INFINITY) || !(fabsf(y) < INFINITY));
+      *reinterpret_cast<__half2*>(out + c) = L == 0.f ? __floats2half2_rn(0.f, 0.f) : __floats2half2_rn(x * inv, y * inv);
+    }
+    if (redo || !__syncthreads_or(bad)) break;
   }
 }
 

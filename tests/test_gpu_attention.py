@@ -384,3 +384,162 @@ def test_tree_lengths_that_do_not_fit_among_others_that_do(Hq, Hkv, D, max_q, n,
         part = slice(row[b], row[b + 1])
         want, tol = mixers.tree_attention(q[part].cpu().numpy(), kc, vc, table[b: b + 1], [total[b]], [0, fresh[b]], None, D ** -0.5)
         close(o[part], want, tol, (b, why))
+
+
+def attend_on_gpu(q, k, v, seen, scale):
+    """Rows q [n, D] of one head over k, v [L, D] in 64 bits, seen [n, L], and their tolerance."""
+    q, k, v = q.double(), k.double(), v.double()
+    s = (q @ k.T * scale).masked_fill(~seen, -float("inf"))
+    w = torch.exp(s - s.amax(1, keepdim=True))
+    l = w.sum(1, keepdim=True)
+    o, wv, tail = w @ v / l, w @ v.abs() / l, seen.double() @ v.abs() / l
+    sterm = (q.abs() @ k.abs().T * scale).amax(1, keepdim=True)
+    parts = [x.cpu().numpy() for x in (o, wv, tail, sterm)]
+    return parts[0], mixers.attention_tolerance(*parts, q.shape[1])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_prompt_one_bad_value_early_in_a_very_long_context(bad):
+    """Every row of the long request has to be made again from 160000 keys, which takes longer than any wait inside
+    the pipeline may last; the other columns of these rows and the other request stay right."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    D, H, ql, kl = 64, 6, [21, 60], [160000, 60]
+    gen = torch.Generator().manual_seed(5)
+    q = torch.randn(sum(ql), H, D, generator=gen).half().cuda()
+    k, v = (torch.randn(sum(kl), 1, D, generator=gen).half().cuda() for _ in range(2))
+    at, col = 5, 3
+    v[at, 0, col] = bad
+    o = torch.empty_like(q)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tb.tb_prompt_attention(q, k, v, starts(ql), starts(kl), o, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    clean = v.clone()
+    clean[at, 0, col] = 0
+    for a, b, x, y in ((0, 21, 0, 160000), (21, 81, 160000, 160060)):
+        n, L = b - a, y - x
+        seen = torch.arange(L, device="cuda")[None, :] <= torch.arange(n, device="cuda")[:, None] + L - n
+        for h in range(H):
+            want, tol = attend_on_gpu(q[a:b, h], k[x:y, 0], clean[x:y, 0], seen, D ** -0.5)
+            keep = [c for c in range(D) if a or c != col]
+            close(o[a:b, h][:, keep], want[:, keep], tol[:, keep], (a, h))
+    got = o[:21, :, col]
+    assert torch.isnan(got).all() if bad != bad else (got == bad).all()
+
+
+@pytest.mark.parametrize("n", [1, 16])
+@pytest.mark.parametrize("others", [0, 300])
+def test_tree_one_bad_value_early_in_a_very_long_context(n, others):
+    """The same over the paged cache, alone (rows joined from parts) and among requests enough that many rows are
+    finished by one CTA, every fifth of these with a bad value too."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    D, H, page = 128, 6, 64
+    fresh, total = [n] + [1] * others, [160000] + [257] * others
+    need = [-(-t // page) for t in total]
+    gen = torch.Generator().manual_seed(6)
+    kc, vc = (torch.randn(sum(need), 1, page, D, generator=gen).half().cuda() for _ in range(2))
+    table = torch.full((len(fresh), max(need)), -1, dtype=torch.int32)
+    first = np.concatenate([[0], np.cumsum(need)])
+    for b, c in enumerate(need):
+        table[b, :c] = torch.arange(first[b], first[b] + c)
+    q = torch.randn(sum(fresh), H, D, generator=gen).half().cuda()
+    clean = vc.clone()
+    hit = [b for b in range(len(fresh)) if b % 5 == 0]
+    for b in hit:
+        vc[first[b], 0, 7, 11] = float("nan")
+        clean[first[b], 0, 7, 11] = 0
+    o = torch.empty_like(q)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(tb.tb_tree_attention_workspace_size(len(fresh), sum(fresh), n, H, 1, D), dtype=torch.uint8, device="cuda")
+    tb.tb_tree_attention(q, kc, vc, table.cuda(), torch.tensor(total, dtype=torch.int32, device="cuda"), starts(fresh), n, o, ws, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    row = starts(fresh).tolist()
+    for b in range(len(fresh)):
+        k, v = (x[first[b]: first[b] + need[b], 0].reshape(-1, D)[: total[b]] for x in (kc, clean))
+        seen = torch.arange(total[b], device="cuda")[None, :] <= torch.arange(fresh[b], device="cuda")[:, None] + total[b] - fresh[b]
+        part = slice(row[b], row[b + 1])
+        keep = [c for c in range(D) if b not in hit or c != 11]
+        for h in range(H):
+            want, tol = attend_on_gpu(q[part, h], k, v, seen, D ** -0.5)
+            close(o[part, h][:, keep], want[:, keep], tol[:, keep], (b, h))
+        if b in hit:
+            assert torch.isnan(o[part, :, 11]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_score_of_minus_infinity_weighs_nothing(D):
+    """Keys of -infinity: rows of nothing else give zeros, whatever their values; beside other keys their weight
+    is 0, which leaves a finite value out."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    gen = torch.Generator().manual_seed(7)
+    L, page = 200, 16
+    q = torch.rand(L, 2, D, generator=gen).half().cuda() + 0.5
+    k, v = (torch.randn(L, 1, D, generator=gen).half().cuda() for _ in range(2))
+    k[:70] = -float("inf")
+    v[3, 0, 5] = float("inf")
+    o = torch.empty_like(q)
+    tb.tb_prompt_attention(q, k, v, starts([L]), starts([L]), o)
+    kc, vc = (torch.cat([x, x[:8]]).view(-1, page, 1, D).transpose(1, 2).contiguous() for x in (k, v))
+    table = torch.arange(kc.shape[0], dtype=torch.int32, device="cuda")[None]
+    n = 64
+    for total in (66, L):
+        p = torch.empty(n, 2, D, dtype=torch.float16, device="cuda")
+        ws = torch.zeros(tb.tb_tree_attention_workspace_size(1, n, n, 2, 1, D), dtype=torch.uint8, device="cuda")
+        tb.tb_tree_attention(q[total - n: total].contiguous(), kc, vc, table, torch.tensor([total], dtype=torch.int32, device="cuda"), starts([n]), n, p, ws)
+        for got, lo in ((o, 0), (p, total - n)):
+            for h in range(2):
+                rows = got[:, h]
+                pos = torch.arange(lo, lo + rows.shape[0])
+                assert (rows[pos < 70] == 0).all()
+                seen = (torch.arange(L)[None, :] <= pos[pos >= 70][:, None]) & (torch.arange(L)[None, :] >= 70)
+                if seen.shape[0]:
+                    at = pos[pos >= 70].cuda()
+                    # (a key of -infinity is as one that is not there)
+                    want, tol = attend_on_gpu(q[at, h], k[70:, 0], v[70:, 0], seen[:, 70:].cuda(), D ** -0.5)
+                    keep = [c for c in range(D) if c != 5]
+                    close(rows[pos >= 70][:, keep], want[:, keep], tol[:, keep], (lo, h))
+                    assert torch.isnan(rows[pos >= 70][:, 5]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rate", [0.002, 0.2])
+def test_values_that_are_not_finite_reach_the_columns_of_the_rows_that_see_them(D, rate):
+    """NaN and infinities strewn over V: each output is NaN, infinite or finite as its own sum is."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    rng = np.random.default_rng(int(1 / rate))
+    lens, H, page = [150, 1, 260], 3, 32
+    T = sum(lens)
+    q, k, v = (rng.standard_normal((T, h, D)).astype(np.float16) for h in (H, 1, 1))
+    kinds = np.array([np.nan, np.inf, -np.inf], dtype=np.float16)
+    hit = rng.random(v.shape) < rate
+    v[hit] = kinds[rng.integers(0, 3, int(hit.sum()))]
+    cuda = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+    o = torch.empty(T, H, D, dtype=torch.float16, device="cuda")
+    tb.tb_prompt_attention(cuda(q), cuda(k), cuda(v), starts(lens), starts(lens), o)
+    with np.errstate(invalid="ignore"):
+        want, tol = mixers.prompt_attention(q, k, v, starts(lens).tolist(), starts(lens).tolist(), D ** -0.5)
+
+    def same(got, want, tol):
+        got = got.double().cpu().numpy()
+        fin = np.isfinite(want)
+        assert not fin.all() and (fin.any() or rate > 0.1)  # (what the case is to hold)
+        assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+        assert (np.abs(got[fin] - want[fin]) <= tol[fin]).all()
+
+    same(o, want, tol)
+    # the last 40 tokens of the last request over the paged cache
+    n, L = 40, lens[2]
+    need = -(-L // page)
+    kc, vc = (np.zeros((need, 1, page, D), dtype=np.float16) for _ in range(2))
+    for j in range(L):
+        kc[j // page, 0, j % page], vc[j // page, 0, j % page] = k[151 + j, 0], v[151 + j, 0]
+    p = torch.empty(n, H, D, dtype=torch.float16, device="cuda")
+    ws = torch.zeros(tb.tb_tree_attention_workspace_size(1, n, n, H, 1, D), dtype=torch.uint8, device="cuda")
+    tb.tb_tree_attention(cuda(q[-n:]), cuda(kc), cuda(vc), torch.arange(need, dtype=torch.int32, device="cuda")[None],
+                         torch.tensor([L], dtype=torch.int32, device="cuda"), starts([n]), n, p, ws)
+    same(p, want[-n:], tol[-n:])
