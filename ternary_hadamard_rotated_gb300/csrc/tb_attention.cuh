@@ -9,6 +9,10 @@
 namespace tb {
 
 constexpr float kLog2e = 1.4426950408889634f;
+// A weight is 2^7 at the maximum that it refers to, and as that may be 2^8 too small, 2^15 at most: fp16's top.  So
+// weights of a 2^21st of the largest keep all of fp16's bits as the operand of P V, and what is rounded off those
+// below is under 2^-32 of it (with 1 at the maximum, weights below 2^-25 were in the sum but not in the output).
+constexpr float kPTop = 7.f;
 
 struct AttnArgs {
   const __half* q;

@@ -19,8 +19,8 @@
 // from L2; the pair halves the K and V part of both.
 //
 // Precision: S, maxima, sums and O in fp32; P is rounded to fp16, O once at the end.  O is rescaled
-// only when a row's maximum has grown by more than 2^8 since the last time (P stays below 2^8, far
-// inside fp16, and the sum carries the same factor).
+// only when a row's maximum has grown by more than 2^8 since the last time (P stays within 2^15,
+// kPTop, and the sum carries the same factor).
 //
 // One prompt of 12289 tokens, 24/4 heads of 256: 1.08 ms, 1712 TFLOP/s, 0.91 of measured (1.21 ms back to back
 // under the power cap); one of 4096: 0.15 ms; of 1024: 29 us.  Bound by the tensor cores from a few
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         }
         if (now != m) l *= m == -INFINITY ? 0.f : ex2(m - now);
         m = now;
-        const float ms = m == -INFINITY ? 0.f : -m;
+        const float ms = m == -INFINITY ? 0.f : kPTop - m;
         float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {

@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           tmem_wait_st();
         }
         if (grow) m = tmax;
-        const float ms = m == -INFINITY ? 0.f : -m;
+        const float ms = m == -INFINITY ? 0.f : kPTop - m;
         float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {

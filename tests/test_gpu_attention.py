@@ -543,3 +543,39 @@ def test_values_that_are_not_finite_reach_the_columns_of_the_rows_that_see_them(
     tb.tb_tree_attention(cuda(q[-n:]), cuda(kc), cuda(vc), torch.arange(need, dtype=torch.int32, device="cuda")[None],
                          torch.tensor([L], dtype=torch.int32, device="cuda"), starts([n]), n, p, ws)
     same(p, want[-n:], tol[-n:])
+
+
+def flat_tail(D, n, drop):
+    """A query, one key of the largest score and n whose weights are 2^-drop of it each: k [n + 1, 1, D], with
+    values of 0 and 1, so that the output is the tail's share."""
+    q = torch.zeros(1, 1, D)
+    q[..., 0] = D ** 0.5
+    k = torch.zeros(n + 1, 1, D)
+    k[n // 3, 0, 0] = drop * float(np.log(2.0))
+    v = torch.ones(n + 1, 1, D)
+    v[n // 3] = 0
+    return q.half().cuda(), k.half().cuda(), v.half().cuda()
+
+
+@pytest.mark.parametrize("drop", [16.0, 22.0, 24.6, 25.5, 27.0])
+@pytest.mark.parametrize("D", [64, 256])
+def test_many_small_weights_beside_a_large_one(D, drop):
+    """n weights far below the largest.  The weights are fp16 operands with the largest one at 2^7 or more, so
+    that a weight below 2^-14 of that is rounded by at most 2^-25 / 2^7 of the largest; scores and sums are exact
+    here up to fp32's 2^-20 (24 bits less those of a score of 19)."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    n = 2 ** 18 - 1
+    q, k, v = flat_tail(D, n, drop)
+    w = float(np.exp2(-(k[n // 3, 0, 0].double() * q[0, 0, 0].double()).item() * D ** -0.5 / np.log(2.0)))
+    want = n * w / (1 + n * w)
+    tol = 2.0 ** -11 * want + (2.0 ** -11 + 2.0 ** -20) * want + n * 2.0 ** -32 + 2.0 ** -25
+    o = torch.empty_like(q)
+    tb.tb_prompt_attention(q, k, v, starts([1]), starts([n + 1]), o)
+    assert (o.double() - want).abs().max().item() <= tol
+    page = 256
+    kc, vc = (x.view(-1, page, 1, D).transpose(1, 2).contiguous() for x in (k, v))
+    table = torch.arange(kc.shape[0], dtype=torch.int32, device="cuda")[None]
+    ws = torch.zeros(tb.tb_tree_attention_workspace_size(1, 1, 1, 1, 1, D), dtype=torch.uint8, device="cuda")
+    tb.tb_tree_attention(q, kc, vc, table, torch.tensor([n + 1], dtype=torch.int32, device="cuda"), starts([1]), 1, o, ws)
+    assert (o.double() - want).abs().max().item() <= tol
