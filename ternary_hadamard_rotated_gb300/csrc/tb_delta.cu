@@ -182,7 +182,7 @@ extern "C" int tb_gated_delta(const uint16_t* q, int64_t ldq, const uint16_t* k,
     return TB_ERR_SHAPE;
   if (D != kDeltaD) return TB_ERR_UNSUPPORTED;
   if (ldq < Hk * D || ldk < Hk * D || ldv < Hv * D || ldq % 8 || ldk % 8 || ldv % 8 || ldq > 1ll << 31 ||
-      ldk > 1ll << 31)
+      ldk > 1ll << 31 || ldv > 1ll << 31)
     return TB_ERR_SHAPE;
   if ((state_in && (n_in < 1 || (!slot_in && n_in < B))) || (state_out && (n_out < 1 || (!slot_out && n_out < B))))
     return TB_ERR_SHAPE;

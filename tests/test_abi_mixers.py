@@ -123,3 +123,16 @@ def test_binding_refuses_layouts_it_cannot_pass_on():
     g = torch.zeros(4, 2)
     with pytest.raises(ValueError):
         tb.tb_gated_delta(q, q, q, g.half(), g, i, 4, q)
+
+
+@pytest.mark.parametrize("ml", [1, 64])
+def test_gated_delta_refuses_tokens_too_far_apart(lib, ml):
+    """More than 2^31 elements between two tokens: refused for q, k and v alike, on both of its paths."""
+    call = caller(lib.tb_gated_delta, ["q", "ldq", "k", "ldk", "v", "ldv", "g", "beta", "T", "Hk", "Hv", "D", "row", "B", "ml", "norm", "scale", "si", "xi", "ni", "so",
+                                       "xo", "no", "o", "ws", "wsb", "st", "s"],
+                  q=P, ldq=2048, k=P, ldk=2048, v=P, ldv=6144, g=P, beta=P, T=70, Hk=16, Hv=48, D=128, row=P, B=2, ml=ml, norm=1, scale=0.1, si=P, xi=None, ni=2,
+                  so=P, xo=None, no=2, o=None, ws=P, wsb=1 << 40, st=None, s=None)
+    assert call() == -1  # everything is looked at but o
+    for name in ("ldq", "ldk", "ldv"):
+        assert call(**{name: 2 ** 31}) == -1
+        assert call(**{name: 2 ** 31 + 8}) == -2, name
