@@ -358,14 +358,15 @@ def _types():
 
 
 def _tokens(name, t, f16):
-    """Distance of two tokens of t fp16 [T, heads, D] in elements; its heads and elements must be contiguous."""
+    """Distance of two tokens of t fp16 [T, heads, D] in elements (of one token alone: its size, whatever the
+    tensor's stride says); its heads and elements must be contiguous."""
     if t.dim() != 3 or t.dtype is not f16:
         raise ValueError(f"{name} must be {f16} [tokens, heads, D], got {t.dtype} {list(t.shape)}")
     s0, s1, s2 = t.stride()
     T, H, D = t.shape
     if (D > 1 and s2 != 1) or (H > 1 and s1 != D):
         raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
-    return s0 if T > 1 else max(s0, H * D)
+    return s0 if T > 1 else H * D
 
 
 def _flat(name, t, dtype, *shape):

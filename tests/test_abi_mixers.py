@@ -136,3 +136,17 @@ def test_gated_delta_refuses_tokens_too_far_apart(lib, ml):
     for name in ("ldq", "ldk", "ldv"):
         assert call(**{name: 2 ** 31}) == -1
         assert call(**{name: 2 ** 31 + 8}) == -2, name
+
+
+def test_binding_takes_one_token_of_any_row_length():
+    """The distance of two tokens means nothing where there is one, as in a decode step's slice of a projection."""
+    import torch
+
+    import ternary_hadamard_rotated_gb300 as tb
+
+    f16 = torch.float16
+    wide = torch.zeros(3, 515, dtype=f16)
+    one = wide[1:2, :512].unflatten(1, (2, 256))
+    assert one.stride(0) == 515 and tb._tokens("q", one, f16) == 512
+    assert tb._tokens("q", wide[1:1, :512].unflatten(1, (2, 256)), f16) == 512
+    assert tb._tokens("q", wide[:, :512].unflatten(1, (2, 256)), f16) == 515  # (which the calls refuse)
