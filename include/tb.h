@@ -472,7 +472,8 @@ int tb_tree_attention(const uint16_t* q, int64_t ldq, int64_t T, int64_t Hq, int
  *   j <= i + lk - lq (fewer keys than queries: the first rows see nothing and give zeros);
  *   scale, o, D: as for tb_tree_attention, with the same rule about what a row does not see.
  * dev_status optional: TB_DEV_BAD_LEN (row starts out of order or past Tq / Tk: zeros where the
- * rows can be told, else not written).
+ * rows can be told, else not written; in calls so large that 32 bits might not hold the work of requests
+ * that overlap, nothing is written where they make more of it than Tq tokens and B requests in order can).
  */
 int tb_prompt_attention(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk,
                         const uint16_t* v, int64_t ldv, int64_t Tq, int64_t Tk, int64_t Hq,

@@ -68,6 +68,7 @@ struct PaArgs {
   AttnArgs a;
   int gp, tok;      // query heads per tile, tokens per CTA's tile
   int head_parts;   // tiles side by side over the heads: Hkv * (G / gp)
+  int64_t room;     // 0, or tiles of a head part that are to be counted and not to be exceeded
   unsigned magic;   // for divisions by the tokens of a tile
 };
 
@@ -108,7 +109,9 @@ TB_DEVI int pa_longer(int lq, int lk, const PaSpan& span, int c) {
   const int64_t x = c < 0 ? -1 : (int64_t)c * kPaKeys - ((int64_t)lk - lq);  // tokens that see at most c tiles of keys
   return x < 0 ? tiles : (x >= lq ? 0 : tiles - pa_div((int)x, span));
 }
-// (counts of tiles fit 32 bits: there are no more than tokens and requests together)
+// (Counts of tiles fit 32 bits: requests in order, one after another, have no more than T / span tokens + B together.
+// Where row starts go back they can have up to B times T / span; calls for which that is too much are counted in 64
+// bits first, pa_in_order.)
 //
 // With more than kPaSorted requests a lane the bisection would cost more than a tile of them; they
 // then go in the order they come in, each one's longest tile first.
@@ -134,6 +137,18 @@ TB_DEVI PaShare pa_share(const AttnArgs& a, const PaSpan& span, int lane) {
     if (lane >= d) s.upto += x;
   }
   return s;
+}
+// do the requests make no more tiles than `room`?
+TB_DEVI bool pa_in_order(const AttnArgs& a, const PaSpan& span, int64_t room, int lane) {
+  int64_t sum = 0;
+  int q0, k0, lq, lk;
+  for (int b = lane; b < a.B; b += 32) {
+    pa_rows(a, b, q0, lq, k0, lk);
+    sum += pa_longer(lq, lk, span, -1);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  return sum <= room;
 }
 TB_DEVI PaItem pa_item(const PaArgs& p, const PaShare& sh, const PaSpan& span, unsigned k, int lane) {
   const AttnArgs& a = p.a;
@@ -252,6 +267,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     mbar_init(o_last, 1);
     mbar_init(o_free, 8 * CG);
     fence_barrier_init();
+  }
+  if (p.room && !pa_in_order(a, PaSpan{(unsigned)(p.tok * CG), p.magic}, p.room, lane)) {
+    if (blockIdx.x == 0 && tid == 0) set_status(a.status, TB_DEV_BAD_LEN);
+    return;  // every thread of every CTA
   }
   if (warp == 9) tmem_alloc_cg<CG>(tmem_slot, 512);
   if (blockIdx.x == 0 && a.status) {  // one CTA looks at every request's row starts
@@ -738,7 +757,8 @@ static int launch_tiles(PaArgs& p, int device, int sms, cudaStream_t s) {
   const int64_t span = (int64_t)p.tok * CG;
   p.magic = (unsigned)(((1ull << 32) + span - 1) / span);  // (of one token: overflows, and is not used)
   // at most: ceil(x) <= floor(x) + 1 per request
-  const int64_t most = (a.T / span + a.B) * p.head_parts, clusters = sms / CG < most ? sms / CG : most;
+  const int64_t tiles = a.T / span + a.B, most = tiles * p.head_parts, clusters = sms / CG < most ? sms / CG : most;
+  p.room = (double)a.B * (double)(a.T / span + 1) * p.head_parts > INT_MAX ? tiles : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * CG));
   cfg.blockDim = dim3(kPaThreads);

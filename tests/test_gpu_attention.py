@@ -579,3 +579,34 @@ def test_many_small_weights_beside_a_large_one(D, drop):
     ws = torch.zeros(tb.tb_tree_attention_workspace_size(1, 1, 1, 1, 1, D), dtype=torch.uint8, device="cuda")
     tb.tb_tree_attention(q, kc, vc, table, torch.tensor([n + 1], dtype=torch.int32, device="cuda"), starts([1]), 1, o, ws)
     assert (o.double() - want).abs().max().item() <= tol
+
+
+def test_prompt_row_starts_that_go_back():
+    """Requests 0, 2, 4, .. all of the rows [0, T), more than 2^31 tiles together.  Nothing is computed."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    T, B = 1 << 20, 600001
+    q = torch.zeros(T, 1, 64, dtype=torch.float16, device="cuda")
+    k = torch.zeros(1, 1, 64, dtype=torch.float16, device="cuda")
+    rows = torch.tensor([0, T], dtype=torch.int32, device="cuda").repeat((B + 1) // 2)
+    assert rows.numel() == B + 1
+    o = torch.full_like(q, 7.0)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tb.tb_prompt_attention(q, k, k, rows, torch.zeros_like(rows), o, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == tb.TB_DEV_BAD_LEN and (o == 7.0).all()
+
+
+def test_prompt_of_very_many_requests():
+    """A call whose work is counted in 64 bits first; requests of one token: their own value."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    T, B = 1 << 19, 600001
+    rows = torch.arange(B + 1, device="cuda").clamp(max=T).int()
+    q = torch.zeros(T, 1, 64, dtype=torch.float16, device="cuda")
+    v = torch.randn(T, 1, 64, device="cuda").half()
+    o = torch.full_like(q, 7.0)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tb.tb_prompt_attention(q, v, v, rows, rows, o, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0 and torch.equal(o, v)
