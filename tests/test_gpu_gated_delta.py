@@ -388,3 +388,62 @@ def test_chunks_of_keys_that_are_not_normalised(k_norm):
 def test_chunks_under_any_scale(scale, v_scale):
     """check() asks for 2^-25 beside the relative bounds; outputs here are at least a hundred times that."""
     small_steps_case(25, 130, lambda beta: beta, v_scale=v_scale, scale=scale)
+
+
+@pytest.mark.parametrize("what", ["v", "k", "g", "beta", "q", "state"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("lens", [[3, 16, 5], [70, 150, 65]])
+def test_what_is_not_finite_on_both_paths(what, bad, lens):
+    """Up to 16 tokens a request and above: what a token's bad input does not reach is bit for bit as without it.
+    What it reaches is NaN on the chunked path (a decay of minus infinity only forgets), and not finite on the
+    other wherever an infinity is multiplied by nothing that is zero."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    Hk, Hv, req, head, col = 2, 4, 1, 3, 77
+    x = dict(zip(("q", "k", "v", "g", "beta", "state"), make(40, lens, Hk, Hv, True)))
+    row = lens[0] + lens[1] // 2
+    T, B, end = sum(lens), len(lens), lens[0] + lens[1]
+    chunked = max(lens) > 16
+
+    def call(a):
+        o = torch.empty(T, Hv, D, dtype=torch.float16, device="cuda")
+        out = torch.empty_like(a["state"])
+        tb.tb_gated_delta(a["q"], a["k"], a["v"], a["g"], a["beta"], starts(lens), max(lens), o, workspace(T, B, max(lens), Hk, Hv), state_in=a["state"],
+                          state_out=out, normalise=True)
+        torch.cuda.synchronize()
+        return o, out
+
+    want_o, want_s = call(x)
+    y = {k: v.clone() for k, v in x.items()}
+    if what == "state":
+        y["state"][req, head, 5, col] = bad
+        row = lens[0]
+    elif what == "v":
+        y["v"][row, head, col] = bad
+    elif what in ("g", "beta"):
+        y[what][row, head] = bad
+    else:
+        y[what][row, head // (Hv // Hk), 9] = bad
+    o, s = call(y)
+    touched = torch.zeros(T, Hv, D, dtype=torch.bool, device="cuda")
+    state = torch.zeros(B, Hv, D, D, dtype=torch.bool, device="cuda")
+    heads = slice(2, 4) if what in ("k", "q") else slice(head, head + 1)
+    if what == "q":
+        touched[row, heads] = True
+    elif what in ("v", "state"):
+        touched[row:end, head, col] = True
+        state[req, head, :, col] = True
+    else:
+        touched[row:end, heads] = True
+        state[req, heads] = True
+    assert torch.equal(o[~touched], want_o[~touched])
+    assert torch.equal(s[~state], want_s[~state])
+    if what == "g" and bad < 0:  # forgets, and goes on
+        assert torch.isfinite(o).all() and torch.isfinite(s).all()
+        y["g"][row, head] = -1e4
+        again_o, again_s = call(y)
+        assert torch.equal(o, again_o) and torch.equal(s, again_s)
+    elif chunked or bad != bad:
+        assert torch.isnan(o[touched]).all() and torch.isnan(s[state]).all()
+    else:
+        assert not torch.isfinite(o[touched][:1]).any() and (what == "q" or not torch.isfinite(s[state]).all())
