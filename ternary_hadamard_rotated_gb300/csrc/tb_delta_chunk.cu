@@ -187,9 +187,9 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
   __shared__ __align__(1024) uint8_t kq[2 * kD1KQ];
   __shared__ float rk[64], rq[64];
   __shared__ float nk[64], nq[64];  // the norms of k as it enters and of scale q
-  __shared__ float pscale[4];       // P's power of two
-  __shared__ float2 gam[4][64];  // running sums of the decays in log2 units, high and low part
-  __shared__ float bet[4][64];
+  __shared__ float2 pscale[4];      // P's power of two, and its inverse
+  __shared__ __align__(16) float2 gam[4][64];  // running sums of the decays in log2 units, high and low part
+  __shared__ __align__(8) float bet[4][64];
   __shared__ int sound[4];       // tokens before the first whose k, decay or step is not finite
   __shared__ __align__(16) float diag_t[4][16][20];  // a warp's diagonal block of A, transposed
   __shared__ float diag[4][16][17];                  // its inverse
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
     const int r = lane & 15, row = (r & 7) * 8 + (tid >> 4);
     float inv = a.normalise ? 1.f / sqrtf(v[0] + kDeltaEps) : 1.f;
     if (!(v[0] < INFINITY)) inv = NAN;
-    const float norm = sqrtf(v[0]) * inv;
+    const float norm = a.normalise ? 1.f : sqrtf(v[0]);  // (or a little less than 1)
     if (r < 8) {
       rk[row] = inv;
       nk[row] = norm;
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
         if (lane == 0) {  // takes the bound of P T to 2^12 .. 2^13, an eighth of what fp16 holds
           int e = 266 - (int)(__float_as_uint(most_b * most_q) >> 23);
           e = e < 127 - kDcPScale ? 127 - kDcPScale : (e > 127 + kDcPScale ? 127 + kDcPScale : e);
-          pscale[warp] = __int_as_float(e << 23);
+          pscale[warp] = make_float2(__int_as_float(e << 23), __int_as_float((254 - e) << 23));
         }
         add_pair(hi[1], lo[1], hi[0], lo[0]);
         float sh = hi[1], sl = lo[1];
@@ -383,11 +383,11 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
       const float eg = ex2(mine.x) * (1.f + 0.6931472f * mine.y);
       f[tid] = tid < sound[slot] ? eg * rk[tid] : 0.f;  // (0 where kernel 2 has a row of zeros)
       f[64 + tid] = tid < sound[slot] ? ex2((last.x - mine.x) + (last.y - mine.y)) * rk[tid] * be[tid] : 0.f;
-      f[128 + tid] = eg * rq[tid] * pscale[slot];
+      f[128 + tid] = eg * rq[tid] * pscale[slot].x;
       if (tid == 0) {
         f[192] = ex2(last.x) * (1.f + 0.6931472f * last.y);
         f[193] = (float)sound[slot];
-        f[194] = 1.f / pscale[slot];
+        f[194] = pscale[slot].y;
       }
     }
     // A (fp32, as accumulator tiles), P (two fp16 terms, as the left factor's tiles)
@@ -396,20 +396,22 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
     {
       const float2 g0 = gm[i0], g1 = gm[i0 + 8];
       const int ok = sound[slot];
-      const float ps = pscale[slot];
+      const float ps = pscale[slot].x;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (j > 2 * warp + 1) {
           continue;
         }
         float pv[4];
+        const float4 gk2 = *reinterpret_cast<const float4*>(&gm[j * 8 + t2]);  // of two tokens
+        const float2 be2 = *reinterpret_cast<const float2*>(&be[j * 8 + t2]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int k = j * 8 + t2 + (e & 1), i = i0 + (e >> 1) * 8;
-          const float2 gk = gm[k], gi = (e >> 1) ? g1 : g0;
+          const float2 gk = (e & 1) ? make_float2(gk2.z, gk2.w) : make_float2(gk2.x, gk2.y), gi = (e >> 1) ? g1 : g0;
           const bool in = i < ok;
           const float d = in && k <= i ? ex2((gi.x - gk.x) + (gi.y - gk.y)) : 0.f;
-          const float db = d * be[k];
+          const float db = d * ((e & 1) ? be2.y : be2.x);
           A[j][e] = in && k < i ? G[j][e] * db : 0.f;
           pv[e] = in && k <= i ? QK[j][e] * db * ps : 0.f;
         }
@@ -908,6 +910,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
         }
         if ((ks & 1) && ks < 7) ldsm4_trans(V + (ks / 2 + 1) * 2048 + v_row + v_pc, vv);
       }
+      const float up_p = lds2(X + kDcFactors + 194 * 4).x;
       float down_r;
       const float up_r = operand_scale(big, down_r, min((int)(__float_as_uint(up_s) >> 23) + kDcPScale, 127 + 100));
       uint32_t rh[4][4], rl[4][4];
@@ -983,6 +986,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       }
       weigh(6);
       weigh(7);
+      const float down_o = up_p * down_r;
       float down_u;
       const float up_u = operand_scale(big, down_u);
       auto split_u = [&](int ks, int q) {
@@ -992,7 +996,7 @@ __global__ void __launch_bounds__(kD2Threads, 1)
       for (int q = 0; q < 4; ++q) split_u(0, q);
       // S <- exp(gamma_C) S + K^T (w U); the increment is summed by itself, so that the state's own
       // rounding is one fp32 fma a chunk.  Beside it o goes out, back in rows of tokens.
-      const float dec = lds2(X + kDcFactors + 192 * 4).x, down_o = lds2(X + kDcFactors + 194 * 4).x * down_r;
+      const float dec = lds2(X + kDcFactors + 192 * 4).x;
       sbig[0] = sbig[1] = 0.f;
       auto at_k = [&](int i) {  // step i: 16 columns i / 4 of k, 16 tokens i % 4
         const int j = i >> 2;
