@@ -22,10 +22,11 @@
 // only when a row's maximum has grown by more than 2^8 since the last time (P stays within 2^15,
 // kPTop, and the sum carries the same factor).
 //
-// One prompt of 12289 tokens, 24/4 heads of 256: 1.08 ms, 1712 TFLOP/s, 0.91 of measured (1.21 ms back to back
-// under the power cap); one of 4096: 0.15 ms; of 1024: 29 us.  Bound by the tensor cores from a few
-// thousand tokens on, below by the first softmax and the output of each tile (about 2 us).  Heads of 128
-// and 64: 0.85 and 0.79 ms, bound by the exponentials (16384 a tile, 1024 clocks of their pipe).
+// One prompt of 12289 tokens, 24/4 heads of 256: 1.09 to 1.13 ms in a replayed graph (1640 to 1700 TFLOP/s, 0.87 to
+// 0.90 of measured), 1.20 to 1.23 ms a call in a row of calls (0.81; under the power cap); one of 4096: 0.15 ms; of
+// 1024: 24 us.  Bound by the tensor cores from a few thousand tokens on, below by what each tile has beside its MMAs
+// (first loads, first softmax, output).  Heads of 128 and 64: 0.82 and 0.76 ms, bound by the exponentials (16384 a
+// tile, 1024 clocks of their pipe).
 //
 // Keys a row does not see get P = 0, which keeps them out as long as V is finite.  Rows that are not finite are
 // looked at by all warps of their CTA once it has no item left, when nothing waits for anything under a limit: one

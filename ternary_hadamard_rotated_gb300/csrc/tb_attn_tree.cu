@@ -14,9 +14,9 @@
 // second kernel joins, all rows at once (with the last CTA of an item joining them alone, the calls
 // below took at that time 26.6 us instead of 23.6 for the one context, 92 instead of 38 for the drafts).
 //
-// 64 contexts of 2000 to 30000 tokens, one token each (2.65 GB): 391 us, 0.98 to 1.00 of measured HBM.  One
-// context of 4097: 17 us, a chain of latencies (schedule, a tile's data, its products and softmax, parts,
-// join).  9 requests of 5 to 16 drafts (53 MB): 26 us.
+// 64 contexts of 2000 to 30000 tokens, one token each (2.65 GB): 392 us, 0.99 of measured HBM.  One context of
+// 4097: 16.6 us in a replayed graph, 18.5 a call, a chain of latencies (schedule, a tile's data, its products and
+// softmax, parts, join).  9 requests of 5 to 16 drafts (53 MB): 26.0 and 30.9 us.
 //
 // Warps 0-3: softmax (thread = row) and epilogue; 4: TMA loads (pages by the block table); 5: MMAs.
 // V rows past the request's last token are zeroed in shared memory before the MMAs read them (what
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       const float inv = whole ? inverse_sum(l) : 1.f;
       const bool none = l == 0.f;  // the row saw nothing here: what the MMAs left is 0 times V
       // through shared memory, so that a store instruction covers whole runs of a few rows (a thread's own
-      // row at a time it touches 32: the drafts above took 28.0 us instead of 25.5)
+      // row at a time it touches 32: the drafts above took 28.0 us instead of 25.5 then)
       const uint32_t stage = base + kTaRing + (uint32_t)warp * 4096u;
       const unsigned rows = __ballot_sync(0xffffffffu, live);
       const int64_t begin = dst - a.o;
@@ -742,8 +742,9 @@ static int launch_tree(TaArgs& p, const DeviceFacts& f, cudaStream_t s) {
   rc = check_launch();
   if (rc != TB_OK) return rc;
   // the joining kernel starts while the last CTAs still run and waits for them on the device.  Sixteen warps
-  // a row while every row has an SM of its own (one context of 4097, 24 rows of 33 parts: 16.5 us with the
-  // parts' kernel, 19.4 with four warps), else four (2304 rows of up to 26 parts: 25.2 and 38.1 us).
+  // a row while every row has an SM of its own, else four.  Contexts of 4097, 24 rows each, both kernels, with
+  // sixteen and with four: 24 rows 16.8 and 18.1 us, 48 21.5 and 22.1, 144 28.4 and 28.4, 192 36.1 and 36.1, 384 56.7
+  // and 53.4, 768 98.7 and 92.2; contexts of 1000 the same way round.
   const bool few = a.T * a.Hq <= f.sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.T * a.Hq));

@@ -17,7 +17,8 @@ namespace tb {
 // 16384 requests: one pass over L2-resident words), so no CTA waits for another and one launch
 // does it all; the sums stay in shared memory, and each CTA then fills its share of the slots (by
 // tokens, so that one long prompt is spread over all CTAs) and of the table (by requests).
-// Bound by latency: 256 requests of one token 4.2 us, 500 of 1000 tokens each (4 MB of slots) 8.1 us.
+// Bound by latency: 256 requests of one token 3.8 us, 500 of 1000 tokens each (4 MB of slots) 8.1 us, in a
+// replayed graph (7.1 and 10.2 us a call).
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxB = 16384;
 
@@ -178,8 +179,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanArgs
 
 // ---------------------------------------------------------------- write
 // A warp per token: 16 bytes a lane, four pieces of K and of V in flight, so that a head's row is one
-// contiguous run on both sides.  Bound by the bytes: 40001 tokens of 4 heads of 256 (328 MB) in 52.6 us,
-// 0.92 of measured HBM.
+// contiguous run on both sides.  Bound by the bytes: 40001 tokens of 4 heads of 256 (328 MB) in 52.5 us,
+// 0.92 of measured HBM, in a replayed graph; 54.9 us a call, 0.88.
 constexpr int kWriteThreads = 256, kWriteUnroll = 4;
 
 __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(

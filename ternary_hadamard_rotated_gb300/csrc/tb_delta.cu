@@ -6,8 +6,8 @@
 // tokens of its request.  One pass over the slice per token gives both S^T k and S^T q, since
 //   o = scale (e^g S^T q + (k . q) u)       with S before the token,
 // so a token costs one reduction over the state's rows and one CTA barrier.
-// One token for each of 64 requests, 48 heads (405 MB, the states read and written once): 65 us, 6260 GB/s,
-// 0.92 of measured HBM.  One request: 4.1 us; each further token 1.2 us.
+// One token for each of 64 requests, 48 heads (405 MB, the states read and written once): 64.3 us, 6300 GB/s,
+// 0.93 of measured HBM, in a replayed graph, 66.9 us a call.  One request: 3.7 us; each further token 1.25 us.
 #include <cuda_runtime.h>
 #include <math.h>
 

@@ -44,9 +44,15 @@ TB_DEVI int64_t delta_slot(const int32_t* slots, int b, int64_t n, int32_t* stat
   return s;
 }
 
-// Requests of up to so many tokens take the recurrent kernel.  16/48 heads, recurrent and chunked:
-// 1 request of 8, 16, 24 tokens 13, 23, 33 and 25 us; 4 of them 28, 52, 75 and 38; 64 of them 184, 326,
-// 496 and 316.
+// Requests of up to so many tokens take the recurrent kernel: all in fp32 and without a workspace, for the runs of
+// drafted tokens that are verified at once.  Up to 8 tokens it is the faster one throughout; from 12 on it depends
+// on how many (request, head) pairs there are, which the rule does not look at.  Recurrent / chunked, us:
+//   16/48 heads, 4, 8, 12, 16, 24 tokens:   1 request     7 / 26   12 / 27   18 / 26   23 / 27   32 / 27
+//                                           4 requests   16 / 39   28 / 39   40 / 39   51 / 39   75 / 39
+//                                          16 requests   29 / 96   49 / 97   68 / 98   87 /101  125 / 98
+//                                          64 requests  112 /331  181 /330  254 /328  328 /328  488 /325
+//   16/16 heads:                           16 requests   22 / 43   39 / 43   57 / 43   75 / 43  109 / 43
+//                                          64 requests   37 /127   61 /126   85 /126  111 /126  164 /125
 constexpr int64_t kDeltaStepTokens = 16;
 
 // the chunked form, and its workspace

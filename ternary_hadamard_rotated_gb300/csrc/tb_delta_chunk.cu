@@ -17,20 +17,20 @@
 // Kernel 1, a CTA per (chunk, key head), which its value heads share: K K^T and Q K^T by mma.sync (fp16
 // inputs, exact products), per value head the triangular system by blocks of 16 and P T.  It writes T
 // (fp16, high and low part) and P T (fp16) as the fragments that kernel 2's MMAs take, and each token's
-// factors.  8192 tokens, 16/48 heads: 103 us, bound by the latency of each head's chain of steps.
+// factors.  8192 tokens, 16/48 heads: 105 us, bound by the latency of each head's chain of steps.
 //
 // Kernel 2 walks the chunks, a warp per 16 columns of v, which no other warp's columns depend on: S^T
 // stays in the warp's registers as fp32 accumulators of mma.sync, and every product's left factor (S^T,
 // R^T, (w U)^T, 16 rows) comes out of the product before it in the layout that the next one wants, so
 // a chunk has no exchange between warps at all.  K, Q, V and kernel 1's results come by TMA, three
 // chunks deep, and the next item's state (read by the warps themselves, 64 requests of one chunk took 351
-// us instead of 308).  An fp32 factor goes in as two fp16 terms, x 2^e = hi + lo with the warp's largest |x|
+// us instead of 308 at that time; 317 now).  An fp32 factor goes in as two fp16 terms, x 2^e = hi + lo with the warp's largest |x|
 // at 2^14: 22 bits, and K and Q are fp16 already.  T has two terms too.  What goes into o alone is rounded
 // once: P T, and the state in S^T q, to fp16.
-// 8192 tokens: 348 us, 2.7 us a chunk.  Its 420 MMAs a warp, at one per 7.8 clocks and SM sub-partition,
+// 8192 tokens: 349 us, 2.7 us a chunk.  Its 420 MMAs a warp, at one per 7.8 clocks and SM sub-partition,
 // are 1.7 of them; the rest is the issue and the latencies of one warp's own chain.  (With a second warp on
-// the sub-partition that makes o from S and R, passed through shared memory, the call takes 476 us instead
-// of 445.  The same walk on tcgen05, 32
+// the sub-partition that makes o from S and R, passed through shared memory, the call took 476 us instead
+// of 445; it is 450 now, with the power of two of P T.  The same walk on tcgen05, 32
 // columns a CTA, took 2.7 us a chunk alone on its SM and 3.4 with a second CTA, with fewer terms: 20
 // MMAs of 44 to 60 clocks, and three trips through registers, shared memory and a barrier of 800 to
 // 1000 each.)  CTAs stay and take the (request, head, half) items with the most chunks first; the loading
