@@ -492,7 +492,9 @@ int tb_prompt_attention(const uint16_t* q, int64_t ldq, const uint16_t* k, int64
  *   state_out  fp32 [n_out, Hv, D, D] or NULL; the final state goes to row slot_out[b] (NULL: b);
  *              negative: not kept.  state_out may be state_in; a row one request writes must not be
  *              one another request of the call reads or writes;
- *   max_len    the longest request's tokens: chooses the kernel (any value gives right results);
+ *   max_len    the longest request's tokens: chooses the kernel.  Any value gives right results, but for
+ *              steps that grow (beta |k|^2 above 2, k as normalised): above 16, where they grow by more than
+ *              about 2^16 within 64 tokens, o and the state are NaN from there on;
  *   o        fp16 [T, Hv, D] (out).
  * A request of no tokens copies its state.  States, sums and decays are fp32.  What is not finite in a
  * token's inputs reaches neither the tokens before it nor other requests, and by v no other column;

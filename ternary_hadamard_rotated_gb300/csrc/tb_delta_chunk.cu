@@ -10,9 +10,10 @@
 // T does not depend on the state, so one kernel computes it for all chunks at once, and with it
 // P T, P_ij = scale (q_i . k_j) D_ij beta_j: the second kernel then gets U and the chunk's own part of o from
 // one product [T; P T] R.  The steps beta stand where no fp16 operand depends on their size: T has ones on its
-// diagonal and, as a step contracts (beta |k|^2 <= 2), nothing above beta_j |k_i| |k_j| beside it; P T, below
-// scale max|q| max(beta |k|), goes under a power of two a chunk and head; and U's rows take beta in fp32.  (With
-// diag(beta) inside T, steps below 2^-14 were left with the bits of fp16's subnormal numbers.)
+// diagonal and, where a step contracts (beta |k|^2 <= 2), nothing above beta_j |k_i| |k_j| beside it; P T goes under
+// a power of two a chunk and head, from its largest value; and U's rows take beta in fp32.  (With diag(beta) inside
+// T, steps below 2^-14 were left with the bits of fp16's subnormal numbers.)  Steps that do not contract make T grow:
+// up to 65504 times within a chunk it is held.
 //
 // Kernel 1, a CTA per (chunk, key head), which its value heads share: K K^T and Q K^T by mma.sync (fp16
 // inputs, exact products), per value head the triangular system by blocks of 16 and P T.  It writes T
@@ -58,9 +59,9 @@ constexpr int kDcItem = 16384;
 // floats: c [64], w [64], q [64], exp(gamma_C), the tokens before the first whose k, decay or step is not
 // finite, and what takes P T's power of two off again
 constexpr int kDcFactors = 3 * kDcMatrix;
-// The powers of two of P T, and of R against S, stay within 2^+-36, so that their product with a sum of 2^37
-// (S^T q) stays inside fp32.  P T below 2^-36 2^-25 adds nothing to an fp16 output, nor does R below 2^-36 of S
-// to a state in fp32.
+// The powers of two of P T, and of R against S, stay below 2^36, so that their product with a sum of 2^37 (S^T q)
+// stays inside fp32.  P T below 2^-36 2^-25 adds nothing to an fp16 output, nor does R below 2^-36 of S to a state
+// in fp32.
 constexpr int kDcPScale = 36;
 
 struct ChunkArgs {
@@ -187,7 +188,8 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
   __shared__ __align__(1024) uint8_t kq[2 * kD1KQ];
   __shared__ float rk[64], rq[64];
   __shared__ float nk[64], nq[64];  // the norms of k as it enters and of scale q
-  __shared__ float2 pscale[4];      // P's power of two, and its inverse
+  __shared__ int pscale[4];         // the exponent of P's power of two
+  __shared__ float most_pt[2][4];   // the largest of P T, by warps, of two heads in turn
   __shared__ __align__(16) float2 gam[4][64];  // running sums of the decays in log2 units, high and low part
   __shared__ __align__(8) float bet[4][64];
   __shared__ int sound[4];       // tokens before the first whose k, decay or step is not finite
@@ -351,10 +353,9 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
         }
         most_b = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most_b)));
         const float most_q = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(nq[lane * 2], nq[lane * 2 + 1]))));
-        if (lane == 0) {  // takes the bound of P T to 2^12 .. 2^13, an eighth of what fp16 holds
-          int e = 266 - (int)(__float_as_uint(most_b * most_q) >> 23);
-          e = e < 127 - kDcPScale ? 127 - kDcPScale : (e > 127 + kDcPScale ? 127 + kDcPScale : e);
-          pscale[warp] = make_float2(__int_as_float(e << 23), __int_as_float((254 - e) << 23));
+        if (lane == 0) {  // takes P's bound, scale max|q| max(beta |k|), to 2^12 .. 2^13
+          const int e = 266 - (int)(__float_as_uint(most_b * most_q) >> 23);
+          pscale[warp] = e < 127 - 60 ? 127 - 60 : (e > 127 + 60 ? 127 + 60 : e);
         }
         add_pair(hi[1], lo[1], hi[0], lo[0]);
         float sh = hi[1], sl = lo[1];
@@ -383,11 +384,9 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
       const float eg = ex2(mine.x) * (1.f + 0.6931472f * mine.y);
       f[tid] = tid < sound[slot] ? eg * rk[tid] : 0.f;  // (0 where kernel 2 has a row of zeros)
       f[64 + tid] = tid < sound[slot] ? ex2((last.x - mine.x) + (last.y - mine.y)) * rk[tid] * be[tid] : 0.f;
-      f[128 + tid] = eg * rq[tid] * pscale[slot].x;
       if (tid == 0) {
         f[192] = ex2(last.x) * (1.f + 0.6931472f * last.y);
         f[193] = (float)sound[slot];
-        f[194] = pscale[slot].y;
       }
     }
     // A (fp32, as accumulator tiles), P (two fp16 terms, as the left factor's tiles)
@@ -396,7 +395,7 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
     {
       const float2 g0 = gm[i0], g1 = gm[i0 + 8];
       const int ok = sound[slot];
-      const float ps = pscale[slot].x;
+      const float ps = __int_as_float(pscale[slot] << 23);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (j > 2 * warp + 1) {
@@ -558,11 +557,34 @@ __global__ void __launch_bounds__(kD1Threads, 4) delta_prep_kernel(const ChunkAr
         mma_16816(T[2 * j + 1], Pl[s], th[2], th[3]);
       }
     }
+    // its largest value to 2^14 .. 2^15
+    float most = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) most = max3_abs(max3_abs(most, T[j][0], T[j][1]), T[j][2], T[j][3]);
+    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+    if (lane == 0) most_pt[h4 & 1][warp] = most;
+    __syncthreads();
+    const float* mp = most_pt[h4 & 1];
+    most = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
+    // both exponents together, biased, within kDcPScale above; what is left for here
+    int e = pscale[slot] + 14 + 127 - (int)(__float_as_uint(most) >> 23);
+    e = e < 127 - 100 ? 127 - 100 : (e > 127 + kDcPScale ? 127 + kDcPScale : e);
+    const float rest = __int_as_float((e - pscale[slot] + 127) << 23);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       if (b > warp) break;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) T[2 * b + x][q] *= rest;
       out[kDcMatrix / 16 + b * 32] = make_uint4(pack_half2(T[2 * b][0], T[2 * b][1]), pack_half2(T[2 * b + 1][0], T[2 * b + 1][1]),
                                                 pack_half2(T[2 * b][2], T[2 * b][3]), pack_half2(T[2 * b + 1][2], T[2 * b + 1][3]));
+    }
+    if (tid < 64) {
+      float* f = reinterpret_cast<float*>(item + kDcFactors);
+      const float2 mine = gm[tid];
+      f[128 + tid] = ex2(mine.x) * (1.f + 0.6931472f * mine.y) * rq[tid] * __int_as_float(e << 23);
+      if (tid == 0) f[194] = __int_as_float((254 - e) << 23);
     }
   }
 }

@@ -447,3 +447,30 @@ def test_what_is_not_finite_on_both_paths(what, bad, lens):
         assert torch.isnan(o[touched]).all() and torch.isnan(s[state]).all()
     else:
         assert not torch.isfinite(o[touched][:1]).any() and (what == "q" or not torch.isfinite(s[state]).all())
+
+
+@pytest.mark.parametrize("grow", [3.0, 5.0, 7.0, 8.0])
+@pytest.mark.parametrize("k_norm", [1.0, 50.0])
+@pytest.mark.parametrize("n", [64, 128])
+def test_chunks_of_steps_that_grow(grow, k_norm, n):
+    """Steps with beta |k|^2 above 2, under which a state grows (over 64 tokens of random keys up to 10^4 times):
+    the chunked path stays with the recurrent one as far as fp16 holds the outputs.  Both carry their rounding along
+    with the growth, so that the bounds are those of check() times the largest growth of a step, grow - 1, and of
+    the outputs as a whole."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    q, k, v, g, beta, _ = make(50, [n], 1, 2, False)
+    k, q = (k.float() * k_norm).half(), (q.float() * k_norm).half()
+    g = torch.full_like(g, -0.01)
+    beta = torch.full_like(beta, grow / k_norm ** 2)
+    want, fin, mag = mixers.gated_delta(*(x.cpu().numpy() for x in (q, k, v, g, beta)), [0, n], np.zeros((1, 2, D, D)), False, D ** -0.5)
+    if np.abs(want).max() > 30000:
+        pytest.skip("outputs past fp16")
+    o = torch.empty(n, 2, D, dtype=torch.float16, device="cuda")
+    out = torch.empty(1, 2, D, D, device="cuda")
+    tb.tb_gated_delta(q, k, v, g, beta, starts([n]), n, o, workspace(n, 1, n, 1, 2), state_out=out, normalise=False)
+    assert torch.isfinite(o).all() and torch.isfinite(out).all()
+    err = np.abs(o.double().cpu().numpy() - want)
+    tol = 2.0 ** -11 * np.abs(want) + (grow - 1) * 3 * 2.0 ** -11 * mag + 2.0 ** -25
+    assert (err <= tol).all(), float((err / tol).max())
+    assert np.linalg.norm(out.double().cpu().numpy() - fin) <= (grow - 1) * 2.0 ** -17 * np.linalg.norm(fin)
