@@ -18,7 +18,7 @@
 // Kernel 1, a CTA per (chunk, key head), which its value heads share: K K^T and Q K^T by mma.sync (fp16
 // inputs, exact products), per value head the triangular system by blocks of 16 and P T.  It writes T
 // (fp16, high and low part) and P T (fp16) as the fragments that kernel 2's MMAs take, and each token's
-// factors.  8192 tokens, 16/48 heads: 105 us, bound by the latency of each head's chain of steps.
+// factors.  8192 tokens, 16/48 heads: 109 us, bound by the latency of each head's chain of steps.
 //
 // Kernel 2 walks the chunks, a warp per 16 columns of v, which no other warp's columns depend on: S^T
 // stays in the warp's registers as fp32 accumulators of mma.sync, and every product's left factor (S^T,
@@ -28,10 +28,10 @@
 // us instead of 308 at that time; 317 now).  An fp32 factor goes in as two fp16 terms, x 2^e = hi + lo with the warp's largest |x|
 // at 2^14: 22 bits, and K and Q are fp16 already.  T has two terms too.  What goes into o alone is rounded
 // once: P T, and the state in S^T q, to fp16.
-// 8192 tokens: 349 us, 2.7 us a chunk.  Its 420 MMAs a warp, at one per 7.8 clocks and SM sub-partition,
+// 8192 tokens: 348 us, 2.7 us a chunk.  Its 420 MMAs a warp, at one per 7.8 clocks and SM sub-partition,
 // are 1.7 of them; the rest is the issue and the latencies of one warp's own chain.  (With a second warp on
 // the sub-partition that makes o from S and R, passed through shared memory, the call took 476 us instead
-// of 445; it is 450 now, with the power of two of P T.  The same walk on tcgen05, 32
+// of 445; it is 454 now, with the power of two of P T.  The same walk on tcgen05, 32
 // columns a CTA, took 2.7 us a chunk alone on its SM and 3.4 with a second CTA, with fewer terms: 20
 // MMAs of 44 to 60 clocks, and three trips through registers, shared memory and a barrier of 800 to
 // 1000 each.)  CTAs stay and take the (request, head, half) items with the most chunks first; the loading
