@@ -68,9 +68,11 @@ enum {
 /* bits OR-ed into *dev_status by kernels */
 #define TB_DEV_BAD_CODE 1  /* tb_pack_w2: a code outside {-1,0,1}; tb_transcode_gguf: a block
                               slot or digit that is not a trit */
-#define TB_DEV_BAD_ID 2    /* tb_embed_lookup: an id outside [0, V) (its row is written as zeros) */
+#define TB_DEV_BAD_ID 2    /* tb_embed_lookup: an id outside [0, V) (its row is written as zeros); a slot, an
+                              adapter, a token or a mask's row past its table (taken as none) */
 #define TB_DEV_TIMEOUT 4   /* a bounded wait inside a kernel gave up; outputs are not valid */
-#define TB_DEV_BAD_PLAN 8  /* tb_chain_run: the plan does not match the launch (nothing computed) */
+#define TB_DEV_BAD_PLAN 8  /* tb_chain_run, tb_rotary*, tb_adapter_linear: the plan does not match the launch
+                              (nothing computed); tb_rotary_plan: a frequency that is not finite (taken as 0) */
 #define TB_DEV_BAD_SLOT 16 /* a slot or page number outside the cache (its token is left out) */
 #define TB_DEV_NO_PAGE 32  /* tb_cache_plan: no page left on the free list, or a table row too short */
 #define TB_DEV_BAD_LEN 64  /* lengths or row starts that do not fit together or the arguments */
@@ -512,6 +514,139 @@ int tb_gated_delta(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ld
                    float scale, const float* state_in, const int32_t* slot_in, int64_t n_in,
                    float* state_out, const int32_t* slot_out, int64_t n_out, uint16_t* o,
                    void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * What a serving step does around the packed linears: rotary positions between the projection of q, k and v and
+ * the cache, the requests' low-rank adapters beside a linear, and changes to the lm_head's logits before a token
+ * is chosen.  Packing, row starts, token distances and alignment are those of the mixers above.
+ */
+
+/* pairs of a head that turn together: (x_i, x_{i+R/2}), or (x_2i, x_{2i+1}) */
+#define TB_ROTARY_HALF 0
+#define TB_ROTARY_PAIRS 1
+/* frequencies scaled for contexts longer than the model's own, by `factor` */
+#define TB_ROTARY_NONE 0    /* f_i = base^(-2i/R) */
+#define TB_ROTARY_LINEAR 1  /* f_i / factor */
+#define TB_ROTARY_BASE 2    /* base is first multiplied by factor^(R/(R-2)) (R above 2) */
+#define TB_ROTARY_PARTS 3   /* pairs that turn more than beta_fast times over `original` tokens as they are, those
+                               that turn less than beta_slow times divided by factor, a ramp over i between them */
+
+/*
+ * tb_rotary_plan — the table that tb_rotary reads: each pair's turns a token, and the rotation's amplitude.
+ *   plan       at least tb_rotary_plan_size(R) bytes of device memory (0: R is not an even number in 2..1024);
+ *   base       above 1;  factor positive;  original, beta_fast > beta_slow positive (TB_ROTARY_PARTS only);
+ *   amplitude  what cosines and sines are multiplied by; 0 chooses it: 0.1 ln(factor) + 1 for TB_ROTARY_PARTS
+ *              with a factor above 1, else 1;
+ *   freqs      float64 [R/2] on the device, radians a token of each pair, in place of base and scaling (which must
+ *              then be TB_ROTARY_NONE), or NULL.
+ * One small launch on `stream`; made once for a model.  dev_status optional: TB_DEV_BAD_PLAN.
+ */
+size_t tb_rotary_plan_size(int64_t R);
+int tb_rotary_plan(void* plan, size_t plan_bytes, int64_t R, double base, int scaling, double factor,
+                   double original, double beta_fast, double beta_slow, double amplitude,
+                   const double* freqs, int32_t* dev_status, void* stream);
+
+/*
+ * tb_rotary — q and k turned by their positions: a pair (a, b) of token t becomes
+ *   amplitude * (a cos - b sin, a sin + b cos) of the angle pos[t] f_i; elements from R on are copied.
+ *   q, k     fp16 [T, Hq, D] and [T, Hk, D], tokens ldq / ldk apart; Hk may be 0 (k and k_out then unused);
+ *   pos      int32 [T], any value (a negative one turns back; angles are exact to 2^-24 of a turn for all);
+ *   plan, R  from tb_rotary_plan with the same R <= D;  layout TB_ROTARY_HALF or TB_ROTARY_PAIRS;
+ *   inverse  nonzero: by the opposite angle (the transpose, amplitude included: the rotation's gradient);
+ *   q_out, k_out  fp16 (out), tokens ldqo / ldko apart; may be q and k (with their distances), and must not
+ *                 overlap them otherwise.
+ * D a multiple of 8 up to 1024; T = 0 is a no-op.  dev_status optional: TB_DEV_BAD_PLAN.
+ */
+int tb_rotary(const uint16_t* q, int64_t ldq, int64_t Hq, const uint16_t* k, int64_t ldk, int64_t Hk,
+              int64_t T, int64_t D, const int32_t* pos, const void* plan, int64_t R, int layout,
+              int inverse, uint16_t* q_out, int64_t ldqo, uint16_t* k_out, int64_t ldko,
+              int32_t* dev_status, void* stream);
+
+/*
+ * tb_rotary_cache_write — tb_rotary, with k (turned) and v written to their slots as tb_cache_write does.
+ *   k_out    NULL: the turned k is kept in the cache only.  Other arguments as in the two calls.
+ */
+int tb_rotary_cache_write(const uint16_t* q, int64_t ldq, int64_t Hq, const uint16_t* k, int64_t ldk,
+                          const uint16_t* v, int64_t ldv, int64_t Hkv, int64_t T, int64_t D,
+                          const int32_t* pos, const int64_t* slots, const void* plan, int64_t R,
+                          int layout, int inverse, uint16_t* q_out, int64_t ldqo, uint16_t* k_out,
+                          int64_t ldko, uint16_t* k_cache, uint16_t* v_cache, int64_t pages, int64_t page,
+                          int32_t* dev_status, void* stream);
+
+/*
+ * tb_adapter_plan — a step's tokens grouped by adapter, once for all linears of the step.
+ *   row_start  int32 [B + 1];  adapter int32 [B]: each request's adapter, negative: none;  n: adapters there are;
+ *   T          rows of the step's matrices (row_start[B] <= T; rows of no request are left alone);
+ *   plan       at least tb_adapter_plan_size(T, n) bytes of device memory; holds nothing but the grouping.
+ * One launch; the result depends on the inputs alone.  B and n up to 16384 (else TB_ERR_TOO_LARGE).  dev_status
+ * optional: TB_DEV_BAD_ID (an adapter past n: taken as none), TB_DEV_BAD_LEN (row starts out of order or past
+ * T: that request, and those after a row start that is too high, are taken as empty).
+ */
+size_t tb_adapter_plan_size(int64_t T, int64_t n);
+int tb_adapter_plan(const int32_t* row_start, const int32_t* adapter, int64_t B, int64_t T, int64_t n,
+                    void* plan, size_t plan_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * tb_adapter_linear — the requests' adapters beside a linear that they share:
+ *   out[t] = y[t] + scale[g] B[g] (A[g] x[t])   g the adapter of token t's request; out[t] = y[t] without one.
+ *   x        fp16 [T, K], rows ldx apart: the linear's input (as given to tb_packed_linear, not rotated);
+ *   a, b     fp16 [n, R, K] and [n, N, R];  scale fp32 [n];
+ *   rank     int32 [n] or NULL (all R): adapter g uses the first rank[g] rows of A[g] and columns of B[g];
+ *            what lies behind them does not matter;
+ *   plan     of tb_adapter_plan with the same T and n;
+ *   y, out   fp16 [T, N], rows ldy / ldo apart: the linear's output, and the result; out may be y (with its
+ *            distance; rows without an adapter are then not touched) and must not overlap it or x otherwise.
+ * A x and the sum are fp32 (A x enters the second product as two terms of 11 bits); one rounding at the end.  A token's row depends on no
+ * other token's.  K, N and R multiples of 8, R up to 256 (TB_ERR_UNSUPPORTED above).  workspace: at least
+ * tb_adapter_linear_workspace_size(T, n, K, N, R) bytes of scratch; its contents do not matter; calls that share
+ * one are ordered on one stream.  dev_status optional: TB_DEV_BAD_PLAN.
+ */
+size_t tb_adapter_linear_workspace_size(int64_t T, int64_t n, int64_t K, int64_t N, int64_t R);
+int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int64_t K, const uint16_t* a,
+                      const uint16_t* b, int64_t n, int64_t R, int64_t N, const int32_t* rank,
+                      const float* scale, const void* plan, const uint16_t* y, int64_t ldy,
+                      uint16_t* out, int64_t ldo, void* workspace, size_t workspace_bytes,
+                      int32_t* dev_status, void* stream);
+
+/* element type of an output */
+#define TB_OUT_F16 0
+#define TB_OUT_F32 1
+
+/*
+ * tb_logits_adjust — penalties, biases and grammar masks on logits.  Row t belongs to the request b with
+ * row_start[b] <= t < row_start[b+1] (row_start NULL: to request t, and B = T).  For each token v, in this order:
+ *   known (in the history's first hist_len[b] tokens, or on the row's path):  l <- l > 0 ? l / repetition[b]
+ *                                                                                       : l * repetition[b]
+ *   generated c times (behind the first prompt_len[b] of them, or on the path):  l <- l - frequency[b] c - presence[b]
+ *   biased:                                                                       l <- l + its bias
+ *   its bit of the row's mask is 0:                                               l <- -infinity
+ *   logits     fp16 [T, V], rows ld >= V apart (any distance; multiples of 8 are faster);
+ *   history    int32 [n_hist, ldh]: request b's tokens are row slot[b] (int32 [B]; NULL: row b; negative: none);
+ *   hist_len   int32 [B];  prompt_len int32 [B] or NULL (zeros);
+ *   fresh      int32 [T] or NULL: the tokens that the rows were computed from, where the history does not hold
+ *              them yet: up to 64 a request, in the order of its rows.  A row's path is itself and its request's
+ *              rows before it, or with tree (uint64 [T], as in tb_tree_attention) those whose bit its word has;
+ *   repetition, presence, frequency  fp32 [B], each may be NULL (1, 0, 0);
+ *   bias_start, bias_ids, bias_values  int32 [B + 1], int32 [n_bias], fp32 [n_bias]: request b's biased tokens
+ *              (n_bias 0: none; unused pointers may then be NULL); of a token listed twice the last one counts;
+ *   mask       uint32 [mask_rows, ceil(V/32)] or NULL, token v at bit v % 32 of word v / 32; row t reads row
+ *              mask_row[t] (int32 [T]; NULL: row t; negative: no mask);
+ *   out        [T, V] of out_type, rows ldo apart (out); may be logits where that is fp16 (with its distance), and
+ *              must not overlap it otherwise.
+ * Every step in fp32, rounded as written; one rounding to fp16.  A masked token gives -infinity whatever its logit
+ * is.  Negative tokens are padding; rows of no request are neither read nor written.  T and B up to 65535
+ * (TB_ERR_TOO_LARGE), V up to 2^24.  dev_status optional: TB_DEV_BAD_ID (a token, a history's or a mask's row past
+ * its table: left out), TB_DEV_BAD_LEN (a length, a list or row starts that do not fit: cut, taken as empty, or
+ * the row left out; more than 64 fresh tokens: the first 64).
+ */
+int tb_logits_adjust(const uint16_t* logits, int64_t ld, int64_t T, int64_t V, const int32_t* row_start,
+                     int64_t B, const int32_t* history, int64_t n_hist, int64_t ldh, const int32_t* slot,
+                     const int32_t* hist_len, const int32_t* prompt_len, const int32_t* fresh,
+                     const uint64_t* tree, const float* repetition, const float* presence,
+                     const float* frequency, const int32_t* bias_start, const int32_t* bias_ids,
+                     const float* bias_values, int64_t n_bias, const uint32_t* mask, int64_t mask_rows,
+                     const int32_t* mask_row, void* out, int64_t ldo, int out_type,
+                     int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -14,6 +14,8 @@ Parity status of each function (what pins it is in tests/test_oracle_pins.py):
                   pinned: hand-computed blocks, round trips, invalid values refused
   mixers          the mixers between the linears (oracle.mixers): pinned by hand-worked cases,
                   closed forms and identities (tests/test_oracle_mixers.py)
+  serving         rotary positions, adapters, logits (oracle.serving): pinned by hand-worked cases
+                  and identities (tests/test_oracle_serving.py)
 Parity with the trained model is unpinned (no weights exist here).
 """
 from .w2_hadamard import (GROUP, BITS, CODES_PER_WORD, fwht, pack_w2, unpack_w2,

@@ -10,7 +10,9 @@ Names follow the C ABI: ``tb_pack_w2``, ``tb_unpack_w2``, ``tb_fwht``,
 ``tb_packed_linear``, ``tb_packed_linear_multi``, ``tb_embed_lookup``, the chained decode
 ``tb_chain_plan`` / ``tb_chain_run`` (``ChainLink`` mirrors ``tb_chain_link``), and the mixers
 between the linears: ``tb_cache_plan`` / ``tb_cache_write`` (the paged K/V cache),
-``tb_tree_attention``, ``tb_prompt_attention`` and ``tb_gated_delta``.
+``tb_tree_attention``, ``tb_prompt_attention`` and ``tb_gated_delta``.  Around the linears:
+``tb_rotary_plan`` / ``tb_rotary`` / ``tb_rotary_cache_write`` (positions), ``tb_adapter_plan`` /
+``tb_adapter_linear`` (low-rank adapters) and ``tb_logits_adjust``.
 """
 from __future__ import annotations
 
@@ -49,6 +51,16 @@ TB_ALGO_GEMV_BATCH = 6
 TB_FMT_PQ2_0 = 1
 TB_FMT_PTQ1_0 = 2
 
+TB_ROTARY_HALF = 0
+TB_ROTARY_PAIRS = 1
+TB_ROTARY_NONE = 0
+TB_ROTARY_LINEAR = 1
+TB_ROTARY_BASE = 2
+TB_ROTARY_PARTS = 3
+
+TB_OUT_F16 = 0
+TB_OUT_F32 = 1
+
 _lib = None
 
 _P = ctypes.c_void_p
@@ -56,6 +68,7 @@ _I64 = ctypes.c_int64
 _INT = ctypes.c_int
 _SZ = ctypes.c_size_t
 _F32 = ctypes.c_float
+_F64 = ctypes.c_double
 
 _SIGNATURES = {
     "tb_status_string": (ctypes.c_char_p, [_INT]),
@@ -92,6 +105,19 @@ _SIGNATURES = {
     "tb_gated_delta_workspace_size": (_SZ, [_I64] * 5),
     "tb_gated_delta": (_INT, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P, _I64, _I64,
                               _INT, _F32, _P, _P, _I64, _P, _P, _I64, _P, _P, _SZ, _P, _P]),
+    "tb_rotary_plan_size": (_SZ, [_I64]),
+    "tb_rotary_plan": (_INT, [_P, _SZ, _I64, _F64, _INT, _F64, _F64, _F64, _F64, _F64, _P, _P, _P]),
+    "tb_rotary": (_INT, [_P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _I64, _INT, _INT, _P, _I64, _P, _I64,
+                         _P, _P]),
+    "tb_rotary_cache_write": (_INT, [_P, _I64, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _INT,
+                                     _INT, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _P, _P]),
+    "tb_adapter_plan_size": (_SZ, [_I64, _I64]),
+    "tb_adapter_plan": (_INT, [_P, _P, _I64, _I64, _I64, _P, _SZ, _P, _P]),
+    "tb_adapter_linear_workspace_size": (_SZ, [_I64] * 5),
+    "tb_adapter_linear": (_INT, [_P, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P,
+                                 _SZ, _P, _P]),
+    "tb_logits_adjust": (_INT, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                _P, _P, _I64, _P, _I64, _P, _P, _I64, _INT, _P, _P]),
 }
 
 EXPORTED = tuple(_SIGNATURES)
@@ -476,3 +502,150 @@ def tb_gated_delta(q, k, v, g, beta, row_start, max_len, o, workspace=None, stat
         _flat("slot_in", slot_in, i32, B), n_in, _flat("state_out", state_out, f32, n_out, Hv, D, D),
         _flat("slot_out", slot_out, i32, B), n_out, _flat("o", o, f16, T, Hv, D), ws, ws_bytes, _ptr(dev_status),
         _stream(stream)))
+
+
+def _here(name, t, stream):
+    """The launch goes to the current device: the tensor has to lie there (a given stream is the caller's word)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    if stream is None:
+        import torch._C as c
+        if t.get_device() != c._cuda_getDevice():
+            raise ValueError(f"{name} lies on {t.device}, which is not the current device")
+
+
+def _matrix(name, t, dtypes, shape=None):
+    """Distance of two rows of t [rows, columns] in elements (of one row alone: its columns); a row's elements
+    must be contiguous."""
+    if t.dim() != 2 or t.dtype not in dtypes or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))} {'[rows, columns]' if shape is None else list(shape)}, "
+                         f"got {t.dtype} {list(t.shape)}")
+    s0, s1 = t.stride()
+    if t.shape[1] > 1 and s1 != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous, got strides {t.stride()}")
+    return s0 if t.shape[0] > 1 else t.shape[1]
+
+
+def tb_rotary_plan_size(R):
+    return load().tb_rotary_plan_size(R)
+
+
+def tb_rotary_plan(plan, R, base=10000.0, scaling=TB_ROTARY_NONE, factor=1.0, original=0.0, beta_fast=32.0,
+                   beta_slow=1.0, amplitude=0.0, freqs=None, dev_status=None, stream=None):
+    """The table of R / 2 pairs that tb_rotary reads, into ``plan`` (tb_rotary_plan_size(R) bytes); freqs:
+    float64 [R / 2] on the device in place of base and scaling; amplitude 0: chosen by the scaling."""
+    import torch
+    buf, nbytes = _scratch(plan)
+    _here("plan", plan, stream)
+    _check("tb_rotary_plan", load().tb_rotary_plan(
+        buf, nbytes, R, base, scaling, factor, original, beta_fast, beta_slow, amplitude,
+        _flat("freqs", freqs, torch.float64, R // 2), _ptr(dev_status), _stream(stream)))
+
+
+def tb_rotary(q, k, pos, plan, R, layout, q_out, k_out, inverse=False, dev_status=None, stream=None):
+    """q fp16 [T, Hq, D] and k fp16 [T, Hk, D] (or None) turned by the positions pos int32 [T] into q_out and
+    k_out (which may be q and k)."""
+    f16, _, i32, _ = _types()
+    ldq, ldqo = _tokens("q", q, f16), _tokens("q_out", q_out, f16)
+    T, Hq, D = q.shape
+    if q_out.shape != q.shape:
+        raise ValueError(f"q and q_out differ in shape: {list(q.shape)} and {list(q_out.shape)}")
+    kp, ldk, Hk, kop, ldko = None, 0, 0, None, 0
+    if k is not None:
+        ldk, ldko, Hk = _tokens("k", k, f16), _tokens("k_out", k_out, f16), k.shape[1]
+        if k.shape != (T, Hk, D) or k_out.shape != k.shape:
+            raise ValueError(f"q, k and k_out do not match: {list(q.shape)}, {list(k.shape)}, {list(k_out.shape)}")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    _here("q", q, stream)
+    _check("tb_rotary", load().tb_rotary(
+        q.data_ptr(), ldq, Hq, kp, ldk, Hk, T, D, _flat("pos", pos, i32, T), plan.data_ptr(), R, layout,
+        int(bool(inverse)), q_out.data_ptr(), ldqo, kop, ldko, _ptr(dev_status), _stream(stream)))
+
+
+def tb_rotary_cache_write(q, k, v, pos, slots, plan, R, layout, q_out, k_cache, v_cache, k_out=None, inverse=False,
+                          dev_status=None, stream=None):
+    """tb_rotary, with the turned k and v fp16 [T, Hkv, D] written to their slots (int64 [T], negative: skipped) of
+    the caches fp16 [pages, Hkv, page, D]; k_out: the turned k beside the cache, or None."""
+    f16, _, i32, i64 = _types()
+    ldq, ldk, ldv, ldqo = _tokens("q", q, f16), _tokens("k", k, f16), _tokens("v", v, f16), _tokens("q_out", q_out, f16)
+    T, Hq, D = q.shape
+    H = k.shape[1]
+    if k.shape != (T, H, D) or v.shape != k.shape or q_out.shape != q.shape:
+        raise ValueError(f"q, k, v and q_out do not match: {list(q.shape)}, {list(k.shape)}, {list(v.shape)}, "
+                         f"{list(q_out.shape)}")
+    kop, ldko = None, 0
+    if k_out is not None:
+        ldko = _tokens("k_out", k_out, f16)
+        if k_out.shape != k.shape:
+            raise ValueError(f"k and k_out differ in shape: {list(k.shape)} and {list(k_out.shape)}")
+        kop = k_out.data_ptr()
+    pages, _, page, _ = k_cache.shape
+    _here("q", q, stream)
+    _check("tb_rotary_cache_write", load().tb_rotary_cache_write(
+        q.data_ptr(), ldq, Hq, k.data_ptr(), ldk, v.data_ptr(), ldv, H, T, D, _flat("pos", pos, i32, T),
+        _flat("slots", slots, i64, T), plan.data_ptr(), R, layout, int(bool(inverse)), q_out.data_ptr(), ldqo, kop, ldko,
+        _flat("k_cache", k_cache, f16, pages, H, page, D), _flat("v_cache", v_cache, f16, pages, H, page, D), pages, page,
+        _ptr(dev_status), _stream(stream)))
+
+
+def tb_adapter_plan_size(T, n):
+    return load().tb_adapter_plan_size(T, n)
+
+
+def tb_adapter_plan(row_start, adapter, T, n, plan, dev_status=None, stream=None):
+    """The T rows of a step grouped by adapter: row_start int32 [B + 1], adapter int32 [B] (negative: none), n
+    adapters -> plan (tb_adapter_plan_size(T, n) bytes)."""
+    _, _, i32, _ = _types()
+    B = adapter.numel()
+    buf, nbytes = _scratch(plan)
+    _here("plan", plan, stream)
+    _check("tb_adapter_plan", load().tb_adapter_plan(
+        _flat("row_start", row_start, i32, B + 1), _flat("adapter", adapter, i32, B), B, T, n, buf, nbytes, _ptr(dev_status),
+        _stream(stream)))
+
+
+def tb_adapter_linear_workspace_size(T, n, K, N, R):
+    return load().tb_adapter_linear_workspace_size(T, n, K, N, R)
+
+
+def tb_adapter_linear(x, a, b, scale, plan, y, workspace=None, out=None, rank=None, dev_status=None, stream=None):
+    """out[t] = y[t] + scale[g] b[g] (a[g] x[t]): x fp16 [T, K], a fp16 [n, R, K], b fp16 [n, N, R], scale fp32
+    [n], y fp16 [T, N], plan from tb_adapter_plan; rank: int32 [n] or None (all R); out: y unless given."""
+    f16, f32, i32, _ = _types()
+    T, K = x.shape
+    n, R, _ = a.shape
+    N = y.shape[1]
+    ldx, ldy = _matrix("x", x, (f16,)), _matrix("y", y, (f16,), (T, N))
+    ldo, op = (ldy, y.data_ptr()) if out is None else (_matrix("out", out, (f16,), (T, N)), out.data_ptr())
+    ws, ws_bytes = _scratch(workspace)
+    _here("x", x, stream)
+    _check("tb_adapter_linear", load().tb_adapter_linear(
+        x.data_ptr(), ldx, T, K, _flat("a", a, f16, n, R, K), _flat("b", b, f16, n, N, R), n, R, N, _flat("rank", rank, i32, n),
+        _flat("scale", scale, f32, n), plan.data_ptr(), y.data_ptr(), ldy, op, ldo, ws, ws_bytes, _ptr(dev_status),
+        _stream(stream)))
+
+
+def tb_logits_adjust(logits, out, history, hist_len, prompt_len=None, row_start=None, slot=None, fresh=None, tree=None,
+                     repetition=None, presence=None, frequency=None, bias_start=None, bias_ids=None, bias_values=None,
+                     mask=None, mask_row=None, dev_status=None, stream=None):
+    """Penalties, biases and masks on logits fp16 [T, V] -> out fp16 or fp32 [T, V] (may be logits): history int32
+    [n_hist, L] with hist_len and prompt_len int32 [B], rows by row_start int32 [B + 1] (None: a row a request),
+    history rows by slot int32 [B]; fresh int32 [T] and tree (uint64 words as int64 [T]): drafted tokens;
+    repetition, presence, frequency fp32 [B]; bias_start int32 [B + 1], bias_ids int32 and bias_values fp32 [n];
+    mask int32 (bits) [rows, ceil(V / 32)], mask_row int32 [T]."""
+    f16, f32, i32, i64 = _types()
+    T, V = logits.shape
+    ld, ldo = _matrix("logits", logits, (f16,)), _matrix("out", out, (f16, f32), (T, V))
+    B, (n_hist, L) = hist_len.numel(), history.shape
+    n_bias = 0 if bias_ids is None else bias_ids.numel()
+    mask_rows = 0 if mask is None else mask.shape[0]
+    _here("logits", logits, stream)
+    _check("tb_logits_adjust", load().tb_logits_adjust(
+        logits.data_ptr(), ld, T, V, _flat("row_start", row_start, i32, B + 1), B, _flat("history", history, i32, n_hist, L),
+        n_hist, L, _flat("slot", slot, i32, B), _flat("hist_len", hist_len, i32, B), _flat("prompt_len", prompt_len, i32, B),
+        _flat("fresh", fresh, i32, T), _flat("tree", tree, i64, T), _flat("repetition", repetition, f32, B),
+        _flat("presence", presence, f32, B), _flat("frequency", frequency, f32, B),
+        _flat("bias_start", bias_start, i32, B + 1), _flat("bias_ids", bias_ids, i32, n_bias),
+        _flat("bias_values", bias_values, f32, n_bias), n_bias, _flat("mask", mask, i32, mask_rows, (V + 31) // 32), mask_rows,
+        _flat("mask_row", mask_row, i32, T), out.data_ptr(), ldo, TB_OUT_F16 if out.dtype is f16 else TB_OUT_F32,
+        _ptr(dev_status), _stream(stream)))
