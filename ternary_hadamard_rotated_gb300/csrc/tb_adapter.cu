@@ -1,5 +1,11 @@
 // Low-rank adapters of many requests beside a shared linear: out[t] = y[t] + scale[g] B[g] (A[g] x[t]), g the
 // adapter of token t's request.
+//
+// Two launches, the second (programmatic) loading what the first does not write before it waits for it:
+//   down  h = scale A x, fp32 [T, R] in the order of the plan; mma.sync on tiles of 16 or 32 tokens of one adapter
+//   up    out = y + B h; few tokens: fp32 on the CUDA cores, every weight read once per 16 tokens;
+//         many: mma.sync on tiles of 128 tokens, h as two fp16 terms under a power of two of the token's own.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <limits.h>
 
@@ -9,6 +15,8 @@
 
 namespace tb {
 
+namespace cg = cooperative_groups;
+
 struct AdapterArgs {
   const __half *x, *a, *b, *y;
   __half* out;
@@ -16,17 +24,19 @@ struct AdapterArgs {
   const float* scale;
   const AdapterPlan* plan;
   const int32_t* order;
-  const AdapterTile* tiles;
+  const AdapterTile* down_tiles;
+  const AdapterTile* up_tiles;
   float* h;
   int32_t* status;
   int64_t ldx, ldy, ldo;
   int T, n, K, N, R;
+  int cluster, down_kind, up_kind;
+  int groups;  // of column tiles: CTAs a row tile has
 };
 
 TB_DEVI bool plan_fits(const AdapterArgs& a) {
-  const bool ok = a.plan->magic == kAdapterMagic && a.plan->T == a.T && a.plan->n == a.n;
-  if (!ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, TB_DEV_BAD_PLAN);
-  return ok;
+  const AdapterPlan& p = *a.plan;
+  return p.magic == kAdapterMagic && p.T == a.T && p.n == a.n;
 }
 
 TB_DEVI int live_rank(const AdapterArgs& a, int g) {
@@ -35,48 +45,396 @@ TB_DEVI int live_rank(const AdapterArgs& a, int g) {
   return r < 0 ? 0 : min(r, a.R);
 }
 
-// h = scale A x: a warp per (token, row of A)
-__global__ void __launch_bounds__(256) adapter_down_kernel(const AdapterArgs a) {
-  if (!plan_fits(a)) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = blockIdx.x; i < a.plan->tiles[0]; i += gridDim.x) {
-    const AdapterTile t = a.tiles[i];
-    const int live = live_rank(a, t.adapter);
-    for (int j = warp; j < t.count * live; j += 8) {
-      const int p = j / live, r = j - p * live;
-      const __half* x = a.x + a.order[t.first + p] * a.ldx;
-      const __half* w = a.a + ((int64_t)t.adapter * a.R + r) * a.K;
-      float s = 0.f;
-      for (int k = lane; k < a.K; k += 32) s = fmaf(__half2float(x[k]), __half2float(w[k]), s);
+TB_DEVI void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// ---------------------------------------------------------------- down
+// A CTA takes MT x 16 tokens by NT x 8 rows of A; its warps and those of its cluster share out K in steps of 32.
+// A step's operands go from global memory straight to the mma's registers: thread (g, c) of a warp holds 8
+// neighbouring elements of rows g (and g + 8), which serve as the k's 2c, 2c + 1, 2c + 8 and 2c + 9 of two MMAs: a
+// product over k does not mind their order, if both operands have the same.
+constexpr int kDownThreads = 256, kDownWarps = kDownThreads / 32;
+
+template <int MT, int NT>
+__global__ void __launch_bounds__(kDownThreads) adapter_down_kernel(const AdapterArgs a) {
+  constexpr int M = MT * 16, N = NT * 8;
+  constexpr int kUnroll = MT * 2 + NT <= 6 ? 4 : 2;
+  extern __shared__ __align__(16) float part_smem[];
+  float (*part)[M][N] = reinterpret_cast<float (*)[M][N]>(part_smem);  // of each warp
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!plan_fits(a)) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(a.status, TB_DEV_BAD_PLAN);
+    return;
+  }
+  const int tile = blockIdx.x / a.cluster, share = blockIdx.x - tile * a.cluster;
+  if (tile >= a.plan->tiles[a.down_kind]) return;  // (all CTAs of the cluster)
+  const AdapterTile t = a.down_tiles[tile];
+  if (t.adapter >= a.n) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int r0 = blockIdx.y * N, live = live_rank(a, t.adapter);
+  const int nt_live = min(NT, max(0, (live - r0 + 7) >> 3));
+
+  const __half* xr[MT * 2];
 #pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      if (lane == 0) a.h[(int64_t)(t.first + p) * a.R + r] = s * a.scale[t.adapter];
+  for (int i = 0; i < MT * 2; ++i) {
+    const int row = i * 8 + g;
+    xr[i] = row < t.count ? a.x + a.order[t.first + row] * a.ldx + c * 8 : nullptr;
+  }
+  const __half* ar = a.a + ((int64_t)t.adapter * a.R + r0 + g) * a.K + c * 8;
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+  const int steps = (a.K + 31) >> 5, stride = a.cluster * kDownWarps;
+  if (nt_live > 0) {
+    for (int s = share * kDownWarps + warp; s < steps; s += stride * kUnroll) {
+      uint4 xv[kUnroll][MT * 2], av[kUnroll][NT];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int k = (s + u * stride) * 32;
+        const bool in = k + c * 8 < a.K;
+#pragma unroll
+        for (int i = 0; i < MT * 2; ++i)
+          xv[u][i] = in && xr[i] ? __ldg(reinterpret_cast<const uint4*>(xr[i] + k)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          av[u][n] = in && n < nt_live && r0 + n * 8 + g < a.R ? __ldg(reinterpret_cast<const uint4*>(ar + (int64_t)n * 8 * a.K + k)) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint4 p = xv[u][2 * m], q = xv[u][2 * m + 1];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_16816(acc[m][n], p.x, q.x, p.y, q.y, av[u][n].x, av[u][n].y);
+            mma_16816(acc[m][n], p.z, q.z, p.w, q.w, av[u][n].z, av[u][n].w);
+          }
+        }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      *reinterpret_cast<float2*>(&part[warp][m * 16 + g][n * 8 + 2 * c]) = make_float2(acc[m][n][0], acc[m][n][1]);
+      *reinterpret_cast<float2*>(&part[warp][m * 16 + g + 8][n * 8 + 2 * c]) = make_float2(acc[m][n][2], acc[m][n][3]);
+    }
+  __syncthreads();
+  for (int e = tid; e < M * N; e += kDownThreads) {  // the warps' parts, in their order
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDownWarps; ++w) s += (&part[w][0][0])[e];
+    (&part[0][0][0])[e] = s;
+  }
+  const float scale = __ldg(a.scale + t.adapter);
+  auto store = [&](int e, float s) {
+    const int row = e / N, r = r0 + e % N;
+    if (row < t.count && r < a.R) a.h[(int64_t)(t.first + row) * a.R + r] = r < live ? s * scale : 0.f;
+  };
+  if (a.cluster == 1) {
+    for (int e = tid; e < M * N; e += kDownThreads) store(e, (&part[0][0][0])[e]);
+    return;
+  }
+  cg::cluster_group cl = cg::this_cluster();
+  cl.sync();
+  for (int e = share * kDownThreads + tid; e < M * N; e += a.cluster * kDownThreads) {  // the CTAs' parts, in theirs
+    float s = 0.f;
+    for (int r = 0; r < a.cluster; ++r) s += *cl.map_shared_rank(&part[0][0][0] + e, r);
+    store(e, s);
+  }
+  cl.sync();  // the parts stay until they have been read
+}
+
+// ---------------------------------------------------------------- up, few tokens
+// A warp takes 32 columns of out (rows of B) and a tile of at most 16 tokens.  L lanes share a row of B, 8
+// elements each (64 a pass where R is above); lane s of a group of L ends with the sum of the group's row s, by
+// exchanging halves of what is left, so that lane i stores column i.
+constexpr int kUpFewThreads = 256;
+
+template <int L>
+__global__ void __launch_bounds__(kUpFewThreads) adapter_up_few_kernel(const AdapterArgs a) {
+  constexpr int G = 4;  // tokens at a time
+  const int lane = threadIdx.x & 31, sub = lane % L;
+  const int n0 = (blockIdx.y * (kUpFewThreads / 32) + (threadIdx.x >> 5)) * 32;
+  if (!plan_fits(a)) return;
+  if ((int)blockIdx.x >= a.plan->tiles[a.up_kind] || n0 >= a.N) return;
+  const AdapterTile t = a.up_tiles[blockIdx.x];
+  const int live = live_rank(a, t.adapter);
+  if (live == 0 && a.out == a.y) return;
+  const int col = n0 + lane, row = n0 + lane - sub;  // the group's first row of B
+  const bool in = col < a.N;
+  const __half* b = a.b + ((int64_t)min(t.adapter, a.n - 1) * a.N + row) * a.R + sub * 8;
+  uint4 w[L];
+  auto load = [&](int r) {  // elements r + sub * 8 .. of the group's rows; zeros behind the rank
+    const int left = live - r - sub * 8;
+#pragma unroll
+    for (int u = 0; u < L; ++u) {
+      w[u] = left > 0 && row + u < a.N ? __ldg(reinterpret_cast<const uint4*>(b + (int64_t)u * a.R + r)) : make_uint4(0, 0, 0, 0);
+      if (left < 8) {
+        uint32_t* p = reinterpret_cast<uint32_t*>(&w[u]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (left <= 2 * j) p[j] = 0;
+          else if (left == 2 * j + 1) p[j] &= 0xffffu;
+        }
+      }
+    }
+  };
+  load(0);
+  bool waited = false;
+  for (int p0 = 0; p0 < t.count; p0 += G) {
+    int tok[G];
+    __half y[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      tok[i] = a.order[t.first + min(p0 + i, t.count - 1)];
+      y[i] = in ? a.y[tok[i] * a.ldy + col] : __half();
+    }
+    float acc[G][L];
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+#pragma unroll
+      for (int u = 0; u < L; ++u) acc[i][u] = 0.f;
+    if (!waited) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // h is written
+      waited = true;
+    }
+    for (int r = 0; r < live; r += L * 8) {
+      if (r > 0 || (p0 > 0 && a.R > L * 8)) load(r);
+      float h[G][8];
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const float* hp = a.h + (int64_t)(t.first + min(p0 + i, t.count - 1)) * a.R + r + sub * 8;
+        const bool have = r + sub * 8 < a.R;
+        const float4 lo = have ? *reinterpret_cast<const float4*>(hp) : make_float4(0, 0, 0, 0);
+        const float4 hi = have ? *reinterpret_cast<const float4*>(hp + 4) : make_float4(0, 0, 0, 0);
+        h[i][0] = lo.x, h[i][1] = lo.y, h[i][2] = lo.z, h[i][3] = lo.w;
+        h[i][4] = hi.x, h[i][5] = hi.y, h[i][6] = hi.z, h[i][7] = hi.w;
+      }
+#pragma unroll
+      for (int u = 0; u < L; ++u) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(&w[u]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[j]));
+#pragma unroll
+          for (int i = 0; i < G; ++i) acc[i][u] = fmaf(h[i][2 * j + 1], f.y, fmaf(h[i][2 * j], f.x, acc[i][u]));
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+#pragma unroll
+      for (int d = L / 2; d; d >>= 1)
+#pragma unroll
+        for (int u = 0; u < d; ++u) {
+          const bool up = (sub & d) != 0;
+          const float other = __shfl_xor_sync(0xffffffffu, up ? acc[i][u] : acc[i][u + d], d);
+          acc[i][u] = (up ? acc[i][u + d] : acc[i][u]) + other;
+        }
+      if (in && p0 + i < t.count) a.out[tok[i] * a.ldo + col] = live ? __float2half_rn(__half2float(y[i]) + acc[i][0]) : y[i];
     }
   }
 }
 
-// out = y + B h: a thread per (token, column)
-__global__ void __launch_bounds__(256) adapter_up_kernel(const AdapterArgs a) {
+// ---------------------------------------------------------------- up, many tokens
+// A CTA takes a tile of at most 128 tokens and a run of column tiles of 64.  h of the tile is split once into two
+// fp16 terms, h 2^e = hi + lo with 2^e of the token's own (its largest h 2^e in [2^14, 2^15)): 22 bits, of h down to
+// 2^-39 of the token's largest.  A column tile's rows of B and elements of y come by cp.async one tile ahead; the
+// result goes back to y's place in shared memory and from there to out in whole rows.
+constexpr int kUpThreads = 256, kUpRows = 128, kUpCols = 64;
+constexpr int kUpYPitch = kUpCols * 2 + 16;  // bytes
+
+TB_DEVI void cp_async16(uint32_t dst, const void* src, int bytes) {  // the rest of the 16 bytes is zeroed
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+TB_DEVI void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+
+TB_DEVI int up_pitch(int R) { return (R + 15) / 16 * 32 + 16; }  // bytes of a row of hi, lo or B: an odd number of 16
+
+__global__ void __launch_bounds__(kUpThreads) adapter_up_kernel(const AdapterArgs a) {
+  extern __shared__ __align__(16) unsigned char up_smem[];
+  __shared__ int tok[kUpRows];
+  __shared__ float back[kUpRows];  // 2^-e
   if (!plan_fits(a)) return;
-  for (int i = blockIdx.x; i < a.plan->tiles[0]; i += gridDim.x) {
-    const AdapterTile t = a.tiles[i];
-    const int live = live_rank(a, t.adapter);
-    if (!live && a.out == a.y) continue;
-    for (int p = 0; p < t.count; ++p) {
-      const int tok = a.order[t.first + p];
-      for (int c = blockIdx.y * 256 + threadIdx.x; c < a.N; c += gridDim.y * 256) {
-        const __half y = a.y[tok * a.ldy + c];
-        if (!live) {
-          a.out[tok * a.ldo + c] = y;
-          continue;
-        }
-        float s = 0.f;
-        for (int r = 0; r < live; ++r) s = fmaf(a.h[(int64_t)(t.first + p) * a.R + r], __half2float(a.b[((int64_t)t.adapter * a.N + c) * a.R + r]), s);
-        a.out[tok * a.ldo + c] = __float2half_rn(__half2float(y) + s);
+  const int tile = blockIdx.x / a.groups, group = blockIdx.x - tile * a.groups;
+  if (tile >= a.plan->tiles[a.up_kind]) return;
+  const AdapterTile t = a.up_tiles[tile];
+  const int live = live_rank(a, t.adapter);
+  if (live == 0 && a.out == a.y) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pitch = up_pitch(a.R), ks = (live + 15) >> 4;
+  const uint32_t hi_at = smem_u32(up_smem), lo_at = hi_at + kUpRows * pitch, stage_at = lo_at + kUpRows * pitch;
+  const uint32_t stage_bytes = kUpCols * pitch + kUpRows * kUpYPitch;
+  for (int i = tid; i < kUpRows; i += kUpThreads) tok[i] = i < t.count ? a.order[t.first + i] : -1;
+  __syncthreads();
+  const int tiles = (a.N + kUpCols - 1) / kUpCols;
+  const int n_begin = (int)((int64_t)tiles * group / a.groups), n_end = (int)((int64_t)tiles * (group + 1) / a.groups);
+
+  auto fetch = [&](int nt) {
+    const uint32_t bs = stage_at + (nt - n_begin & 1) * stage_bytes, ys = bs + kUpCols * pitch;
+    const int n0 = nt * kUpCols;
+    const int pieces = ks * 2;  // 16-byte pieces of a row of B
+    for (int i = tid; i < kUpCols * pieces; i += kUpThreads) {
+      const int row = i / pieces, p = i - row * pieces;
+      const int left = n0 + row < a.N ? min(16, max(0, (live - p * 8) * 2)) : 0;
+      cp_async16(bs + row * pitch + p * 16, left ? a.b + ((int64_t)t.adapter * a.N + n0 + row) * a.R + p * 8 : a.b, left);
+    }
+#pragma unroll
+    for (int i = tid; i < kUpRows * (kUpCols / 8); i += kUpThreads) {
+      const int row = i / (kUpCols / 8), p = i % (kUpCols / 8);
+      if (tok[row] >= 0 && n0 + p * 8 < a.N) cp_async16(ys + row * kUpYPitch + p * 16, a.y + tok[row] * a.ldy + n0 + p * 8, 16);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (n_begin < n_end) fetch(n_begin);
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // h is written
+  {  // two threads a token: its largest h, then its terms
+    const int row = tid >> 1, half = tid & 1;
+    const float* h = a.h + (int64_t)(t.first + min(row, t.count - 1)) * a.R;
+    float top = 0.f;
+    for (int r = half * 4; r < live; r += 8) {
+      const float4 v = *reinterpret_cast<const float4*>(h + r);
+      top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    // 2^(14 - exponent of top); 0 and what is not finite stay as they are
+    int e = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
+    if (!(top > 0.f) || !(top < INFINITY)) e = 0;
+    e = max(-126, min(126, e));
+    const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+    if (half == 0) back[row] = __uint_as_float((uint32_t)(127 - e) << 23);
+    for (int r = half * 4; r < ks * 16; r += 8) {
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (row < t.count && r < a.R) {
+        const float4 f = *reinterpret_cast<const float4*>(h + r);
+        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
       }
+      __half hi[4], lo[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float s = v[j] * up;
+        hi[j] = __float2half_rn(s);
+        const float f = __half2float(hi[j]);
+        lo[j] = fabsf(f) < INFINITY ? __float2half_rn(s - f) : __half();
+      }
+      unsigned char* p = up_smem + row * pitch + r * 2;
+      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(hi);
+      *reinterpret_cast<uint2*>(p + kUpRows * pitch) = *reinterpret_cast<const uint2*>(lo);
     }
   }
+  // warps: four by rows of 32, two by columns of 32
+  const int wr = (warp >> 1) * 32, wc = (warp & 1) * 32, g = lane >> 2, c = lane & 3;
+  const int m_live = min(2, max(0, (t.count - wr + 15) >> 4));
+  const uint32_t a_lane = hi_at + (wr + (lane & 15)) * pitch + (lane >> 4) * 16;
+  const uint32_t b_lane = (wc + (lane & 7) + (lane >> 4) * 8) * pitch + (lane >> 3 & 1) * 16;
+  for (int nt = n_begin; nt < n_end; ++nt) {
+    const uint32_t bs = stage_at + (nt - n_begin & 1) * stage_bytes;
+    unsigned char* ys = up_smem + (bs - hi_at) + kUpCols * pitch;
+    if (nt + 1 < n_end) {
+      fetch(nt + 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    __syncthreads();
+    float acc[2][4][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+    if (m_live > 0)
+      for (int k = 0; k < ks; ++k) {
+        uint32_t b[2][4];
+        ldmatrix4(b[0], bs + b_lane + k * 32);
+        ldmatrix4(b[1], bs + b_lane + 16 * pitch + k * 32);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          if (m >= m_live) break;
+          uint32_t hi[4], lo[4];
+          ldmatrix4(hi, a_lane + m * 16 * pitch + k * 32);
+          ldmatrix4(lo, a_lane + (kUpRows + m * 16) * pitch + k * 32);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            mma_16816(acc[m][n], lo[0], lo[1], lo[2], lo[3], b[n >> 1][(n & 1) * 2], b[n >> 1][(n & 1) * 2 + 1]);
+            mma_16816(acc[m][n], hi[0], hi[1], hi[2], hi[3], b[n >> 1][(n & 1) * 2], b[n >> 1][(n & 1) * 2 + 1]);
+          }
+        }
+      }
+    if (live) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = wr + m * 16 + i * 8 + g;
+          if (row >= t.count) continue;
+          const float f = back[row];
+          unsigned char* yr = ys + row * kUpYPitch + (wc + 2 * c) * 2;
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            __half2* p = reinterpret_cast<__half2*>(yr + n * 16);
+            const float2 y = __half22float2(*p);
+            *p = __floats2half2_rn(fmaf(acc[m][n][2 * i], f, y.x), fmaf(acc[m][n][2 * i + 1], f, y.y));
+          }
+        }
+    }
+    __syncwarp();
+    const int n0 = nt * kUpCols + wc;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // the warp's 32 x 32: a row of 64 bytes by four lanes
+      const int row = wr + i * 8 + (lane >> 2), col = n0 + (lane & 3) * 8;
+      if (row < t.count && col < a.N)
+        *reinterpret_cast<uint4*>(a.out + tok[row] * a.ldo + col) = *reinterpret_cast<const uint4*>(ys + row * kUpYPitch + (wc + (lane & 3) * 8) * 2);
+    }
+    __syncthreads();  // the stage may be filled again
+  }
 }
+
+static size_t up_smem_bytes(int R) {
+  const size_t pitch = (size_t)(R + 15) / 16 * 32 + 16;
+  return 2 * kUpRows * pitch + 2 * (kUpCols * pitch + (size_t)kUpRows * kUpYPitch);
+}
+
+template <typename... Args>
+static cudaError_t launch(void (*fn)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster, bool dependent, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = (unsigned)cluster;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (dependent) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = (unsigned)n;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+// Up to this many tokens of a step the product with B runs on the CUDA cores in fp32.
+constexpr int kFewTokens = 256;
 
 }  // namespace tb
 
@@ -104,7 +462,7 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   const size_t need = tb_adapter_linear_workspace_size(T, n, K, N, R);
   if (need && (!workspace || workspace_bytes < need)) return TB_ERR_WORKSPACE;
   DeviceFacts f;
-  const int rc = device_facts(&f);
+  int rc = device_facts(&f);
   if (rc != TB_OK) return rc;
   AdapterArgs g;
   g.x = reinterpret_cast<const __half*>(x);
@@ -114,10 +472,14 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   g.out = reinterpret_cast<__half*>(out);
   g.rank = rank;
   g.scale = scale;
+  const bool few = T <= kFewTokens;
+  g.down_kind = few ? 0 : 1;
+  g.up_kind = few ? 0 : 2;
   const char* base = static_cast<const char*>(plan);
   g.plan = static_cast<const AdapterPlan*>(plan);
   g.order = reinterpret_cast<const int32_t*>(base + adapter_order_at());
-  g.tiles = reinterpret_cast<const AdapterTile*>(base + adapter_tiles_at(T, n, 0));
+  g.down_tiles = reinterpret_cast<const AdapterTile*>(base + adapter_tiles_at(T, n, g.down_kind));
+  g.up_tiles = reinterpret_cast<const AdapterTile*>(base + adapter_tiles_at(T, n, g.up_kind));
   g.h = static_cast<float*>(workspace);
   g.status = dev_status;
   g.ldx = ldx;
@@ -129,9 +491,42 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   g.N = (int)N;
   g.R = (int)R;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int64_t tiles = adapter_max_tiles(T, n, 0);
-  if (tiles > 4096) tiles = 4096;
-  adapter_down_kernel<<<(int)tiles, 256, 0, s>>>(g);
-  adapter_up_kernel<<<dim3((unsigned)tiles, (unsigned)((N + 1023) / 1024)), 256, 0, s>>>(g);
+  const int64_t down = adapter_max_tiles(T, n, g.down_kind), up = adapter_max_tiles(T, n, g.up_kind);
+  // down: K is split over a cluster until there are four CTAs an SM, of at least four steps a warp
+  g.cluster = 1;
+  while (g.cluster < 8 && down * g.cluster * 2 <= 4 * f.sms && K / 32 >= g.cluster * 2 * kDownWarps) g.cluster *= 2;
+  const int nt = R <= 16 ? 2 : R <= 32 ? 4 : 8;
+  const dim3 grid((unsigned)(down * g.cluster), (unsigned)((R + nt * 8 - 1) / (nt * 8)));
+  cudaError_t e;
+  const int parts = kDownWarps * (few ? 16 : 32) * nt * 8 * 4;  // bytes
+  if (!few && nt == 8 && (rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_down_kernel<2, 8>), f.device, parts)) != TB_OK) return rc;
+#define TB_DOWN(MT, NT) launch(adapter_down_kernel<MT, NT>, grid, kDownThreads, (size_t)parts, s, g.cluster, false, g)
+  if (few)
+    e = nt == 2 ? TB_DOWN(1, 2) : nt == 4 ? TB_DOWN(1, 4) : TB_DOWN(1, 8);
+  else
+    e = nt == 2 ? TB_DOWN(2, 2) : nt == 4 ? TB_DOWN(2, 4) : TB_DOWN(2, 8);
+#undef TB_DOWN
+  if (e == cudaSuccess) {
+    if (few) {
+      const dim3 cols((unsigned)up, (unsigned)((N + kUpFewThreads - 1) / kUpFewThreads));
+      e = R <= 8    ? launch(adapter_up_few_kernel<1>, cols, kUpFewThreads, 0, s, 1, true, g)
+          : R <= 16 ? launch(adapter_up_few_kernel<2>, cols, kUpFewThreads, 0, s, 1, true, g)
+          : R <= 32 ? launch(adapter_up_few_kernel<4>, cols, kUpFewThreads, 0, s, 1, true, g)
+                    : launch(adapter_up_few_kernel<8>, cols, kUpFewThreads, 0, s, 1, true, g);
+    } else {
+      const size_t smem = up_smem_bytes((int)R);
+      rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_up_kernel), f.device, (int)smem);
+      if (rc != TB_OK) return rc;
+      // several CTAs a row tile, so that each SM has a few; each takes a run of column tiles
+      const int64_t col_tiles = (N + kUpCols - 1) / kUpCols;
+      int64_t groups = (6ll * f.sms + up - 1) / up;
+      g.groups = (int)(groups < 1 ? 1 : groups > col_tiles ? col_tiles : groups);
+      e = launch(adapter_up_kernel, dim3((unsigned)(up * g.groups)), kUpThreads, smem, s, 1, true, g);
+    }
+  }
+  if (e != cudaSuccess) {
+    record_cuda_error(e);
+    return TB_ERR_CUDA;
+  }
   return check_launch();
 }
