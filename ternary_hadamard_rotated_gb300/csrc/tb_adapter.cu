@@ -3,8 +3,8 @@
 //
 // Two launches, the second (programmatic) loading what the first does not write before it waits for it:
 //   down  h = scale A x, fp32 [T, R] in the order of the plan; mma.sync on tiles of 16 or 32 tokens of one adapter
-//   up    out = y + B h; few tokens: fp32 on the CUDA cores, every weight read once per 16 tokens;
-//         many: mma.sync on tiles of 128 tokens, h as two fp16 terms under a power of two of the token's own.
+//   up    out = y + B h, mma.sync with h as two fp16 terms; few tokens: tiles of 16, bound by the weights, which go
+//         from global memory straight to the registers; many: tiles of 128, bound by y and out
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -60,9 +60,9 @@ TB_DEVI void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uin
 constexpr int kDownThreads = 256, kDownWarps = kDownThreads / 32;
 
 template <int MT, int NT>
-__global__ void __launch_bounds__(kDownThreads) adapter_down_kernel(const AdapterArgs a) {
+__global__ void __launch_bounds__(kDownThreads, MT * NT > 8 ? 1 : 2) adapter_down_kernel(const AdapterArgs a) {
   constexpr int M = MT * 16, N = NT * 8;
-  constexpr int kUnroll = MT * 2 + NT <= 6 ? 4 : 2;
+  constexpr int kUnroll = MT * 2 + NT <= 4 ? 4 : 2;
   extern __shared__ __align__(16) float part_smem[];
   float (*part)[M][N] = reinterpret_cast<float (*)[M][N]>(part_smem);  // of each warp
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -153,102 +153,190 @@ __global__ void __launch_bounds__(kDownThreads) adapter_down_kernel(const Adapte
   cl.sync();  // the parts stay until they have been read
 }
 
-// ---------------------------------------------------------------- up, few tokens
-// A warp takes 32 columns of out (rows of B) and a tile of at most 16 tokens.  L lanes share a row of B, 8
-// elements each (64 a pass where R is above); lane s of a group of L ends with the sum of the group's row s, by
-// exchanging halves of what is left, so that lane i stores column i.
-constexpr int kUpFewThreads = 256;
+// ---------------------------------------------------------------- h as fp16
+// h 2^e = hi + lo with 2^e of the token's own (its largest h 2^e in [2^14, 2^15)): 22 bits, of h down to 2^-39 of the
+// token's largest; fp32 sums of hi B and lo B, then 2^-e.
 
-template <int L>
-__global__ void __launch_bounds__(kUpFewThreads) adapter_up_few_kernel(const AdapterArgs a) {
-  constexpr int G = 4;  // tokens at a time
-  const int lane = threadIdx.x & 31, sub = lane % L;
-  const int n0 = (blockIdx.y * (kUpFewThreads / 32) + (threadIdx.x >> 5)) * 32;
+// 2^e and 2^-e for a token whose largest |h| is top; 0 and what is not finite stay as they are
+TB_DEVI float up_scale(float top, float& back) {
+  int e = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
+  if (!(top > 0.f) || !(top < INFINITY)) e = 0;
+  e = max(-126, min(126, e));
+  back = __uint_as_float((uint32_t)(127 - e) << 23);
+  return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
+TB_DEVI void two_terms(float4 v, float up, uint2& hi, uint2& lo) {
+  const float f[4] = {v.x * up, v.y * up, v.z * up, v.w * up};
+  __half h[4], l[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    h[j] = __float2half_rn(f[j]);
+    const float b = __half2float(h[j]);
+    l[j] = fabsf(b) < INFINITY ? __float2half_rn(f[j] - b) : __half();
+  }
+  hi = *reinterpret_cast<const uint2*>(h);
+  lo = *reinterpret_cast<const uint2*>(l);
+}
+
+// ---------------------------------------------------------------- up, few tokens
+// The columns of out (rows of B) are the mma's 16 rows and the tokens its 8 columns, so that a weight is read once
+// for a tile of 16 tokens and an idle token costs nothing but its place.  A warp takes 32 columns at a time, and
+// every CTA an equal run of all tiles' columns.  Thread (g, c) holds columns n0 + 4 g .. + 3: 8 bytes of y and out a
+// token, and 8 neighbouring elements of each of their rows of B, as in `down`.  The next columns' rows of B are
+// loaded before the present ones are used.
+constexpr int kUpFewThreads = 256, kUpFewWarps = kUpFewThreads / 32;
+
+// W: elements of a row of B a thread loads at a time, by 4 threads: 16, 32 or 64 ranks a pass
+template <int W>
+__global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const AdapterArgs a) {
+  constexpr int kPass = W * 4, kMma = W / 4;  // ranks of a pass, its MMAs of 16
+  extern __shared__ __align__(16) unsigned char up_few_smem[];  // hi, lo of [16][pitch] ranks
+  __shared__ int tok[16];
+  __shared__ float back[16];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   if (!plan_fits(a)) return;
-  if ((int)blockIdx.x >= a.plan->tiles[a.up_kind] || n0 >= a.N) return;
-  const AdapterTile t = a.up_tiles[blockIdx.x];
-  const int live = live_rank(a, t.adapter);
-  if (live == 0 && a.out == a.y) return;
-  const int col = n0 + lane, row = n0 + lane - sub;  // the group's first row of B
-  const bool in = col < a.N;
-  const __half* b = a.b + ((int64_t)min(t.adapter, a.n - 1) * a.N + row) * a.R + sub * 8;
-  uint4 w[L];
-  auto load = [&](int r) {  // elements r + sub * 8 .. of the group's rows; zeros behind the rank
-    const int left = live - r - sub * 8;
-#pragma unroll
-    for (int u = 0; u < L; ++u) {
-      w[u] = left > 0 && row + u < a.N ? __ldg(reinterpret_cast<const uint4*>(b + (int64_t)u * a.R + r)) : make_uint4(0, 0, 0, 0);
-      if (left < 8) {
-        uint32_t* p = reinterpret_cast<uint32_t*>(&w[u]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (left <= 2 * j) p[j] = 0;
-          else if (left == 2 * j + 1) p[j] &= 0xffffu;
-        }
-      }
-    }
-  };
-  load(0);
+  const int tiles = a.plan->tiles[a.up_kind], units = (a.N + 31) / 32, passes = (a.R + kPass - 1) / kPass;
+  const int pitch = passes * kPass * 2 + 16;  // bytes of a token's hi or lo
+  const int64_t all = (int64_t)tiles * units;
+  int64_t at = all * blockIdx.x / gridDim.x;
+  const int64_t stop = all * (blockIdx.x + 1) / gridDim.x;
   bool waited = false;
-  for (int p0 = 0; p0 < t.count; p0 += G) {
-    int tok[G];
-    __half y[G];
+  while (at < stop) {
+    const int tile = (int)(at / units), begin = (int)(at - (int64_t)tile * units);
+    const int end = (int)(stop - at < units - begin ? begin + (stop - at) : units);
+    at += end - begin;
+    const AdapterTile t = a.up_tiles[tile];
+    const int live = live_rank(a, t.adapter);
+    if (live == 0 && a.out == a.y) continue;
+    const __half* b = a.b + (int64_t)min(t.adapter, a.n - 1) * a.N * a.R + c * W;
+    uint32_t w[4][W / 2], next[4][W / 2];
+    auto load = [&](uint32_t (&v)[4][W / 2], int u, int pass) {  // rows 4 g .. + 3 of unit u
+      const int r = pass * kPass;
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      tok[i] = a.order[t.first + min(p0 + i, t.count - 1)];
-      y[i] = in ? a.y[tok[i] * a.ldy + col] : __half();
-    }
-    float acc[G][L];
+      for (int j = 0; j < 4; ++j) {
+        const int row = u * 32 + 4 * g + j;
 #pragma unroll
-    for (int i = 0; i < G; ++i)
+        for (int i = 0; i < W; i += 8) {
+          const int left = row < a.N ? live - r - c * W - i : 0;
+          const __half* p = b + (int64_t)row * a.R + r + i;
+          if constexpr (W == 4) {
+            const uint2 q = left > 0 ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+            v[j][0] = q.x, v[j][1] = q.y;
+          } else {
+            const uint4 q = left > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+            v[j][i / 2] = q.x, v[j][i / 2 + 1] = q.y, v[j][i / 2 + 2] = q.z, v[j][i / 2 + 3] = q.w;
+          }
+        }
+      }
+    };
+    auto cut = [&](uint32_t (&v)[4][W / 2], int pass) {  // what the rank ends inside a thread's elements
+      const int left = live - pass * kPass - c * W;
 #pragma unroll
-      for (int u = 0; u < L; ++u) acc[i][u] = 0.f;
-    if (!waited) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");  // h is written
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) v[j][i] = left <= 2 * i ? 0u : left == 2 * i + 1 ? v[j][i] & 0xffffu : v[j][i];
+    };
+    int u = begin + warp;
+    if (live && u < end) load(w, u, 0);
+    __syncthreads();  // the tile before is done
+    if (tid < 16) tok[tid] = tid < t.count ? a.order[t.first + tid] : -1;
+    if (live) {
+      if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // h is written
       waited = true;
-    }
-    for (int r = 0; r < live; r += L * 8) {
-      if (r > 0 || (p0 > 0 && a.R > L * 8)) load(r);
-      float h[G][8];
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        const float* hp = a.h + (int64_t)(t.first + min(p0 + i, t.count - 1)) * a.R + r + sub * 8;
-        const bool have = r + sub * 8 < a.R;
-        const float4 lo = have ? *reinterpret_cast<const float4*>(hp) : make_float4(0, 0, 0, 0);
-        const float4 hi = have ? *reinterpret_cast<const float4*>(hp + 4) : make_float4(0, 0, 0, 0);
-        h[i][0] = lo.x, h[i][1] = lo.y, h[i][2] = lo.z, h[i][3] = lo.w;
-        h[i][4] = hi.x, h[i][5] = hi.y, h[i][6] = hi.z, h[i][7] = hi.w;
+      const int p = tid >> 4, q = tid & 15;  // 16 threads a token
+      const float* h = a.h + (int64_t)(t.first + min(p, t.count - 1)) * a.R;
+      float top = 0.f;
+      for (int r = q * 4; r < live; r += 64) {
+        const float4 v = *reinterpret_cast<const float4*>(h + r);
+        top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
       }
 #pragma unroll
-      for (int u = 0; u < L; ++u) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(&w[u]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[j]));
-#pragma unroll
-          for (int i = 0; i < G; ++i) acc[i][u] = fmaf(h[i][2 * j + 1], f.y, fmaf(h[i][2 * j], f.x, acc[i][u]));
-        }
+      for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      float bk;
+      const float up = up_scale(top, bk);
+      if (q == 0) back[p] = bk;
+      for (int r = q * 4; r < passes * kPass; r += 64) {
+        const float4 v = p < t.count && r < a.R ? *reinterpret_cast<const float4*>(h + r) : make_float4(0, 0, 0, 0);
+        uint2 hi, lo;
+        two_terms(v, up, hi, lo);
+        *reinterpret_cast<uint2*>(up_few_smem + p * pitch + r * 2) = hi;
+        *reinterpret_cast<uint2*>(up_few_smem + (16 + p) * pitch + r * 2) = lo;
       }
     }
+    __syncthreads();
+    const int nt = t.count > 8 ? 2 : 1;
+    int my_tok[4];
+    float my_back[4];
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
+    for (int i = 0; i < 4; ++i) {  // tokens 2 c, 2 c + 1 of each eight
+      const int p = (i >> 1) * 8 + 2 * c + (i & 1);
+      my_tok[i] = tok[p];
+      my_back[i] = live ? back[p] : 0.f;
+    }
+    const uint32_t terms = smem_u32(up_few_smem) + g * pitch + c * W * 2;
+    for (; u < end; u += kUpFewWarps) {
+      const int col = u * 32 + 4 * g;
+      uint2 y[4];
 #pragma unroll
-      for (int d = L / 2; d; d >>= 1)
+      for (int i = 0; i < 4; ++i)
+        if (my_tok[i] >= 0 && col < a.N) y[i] = *reinterpret_cast<const uint2*>(a.y + my_tok[i] * a.ldy + col);
+      float acc[2][2][4];  // [rows 4 g, 4 g + 1 or 4 g + 2, 4 g + 3][eight tokens]
 #pragma unroll
-        for (int u = 0; u < d; ++u) {
-          const bool up = (sub & d) != 0;
-          const float other = __shfl_xor_sync(0xffffffffu, up ? acc[i][u] : acc[i][u + d], d);
-          acc[i][u] = (up ? acc[i][u + d] : acc[i][u]) + other;
+      for (int i = 0; i < 16; ++i) (&acc[0][0][0])[i] = 0.f;
+      for (int pass = 0; pass * kPass < live; ++pass) {
+        if ((pass + 1) * kPass < live) load(next, u, pass + 1);
+        else if (u + kUpFewWarps < end) load(next, u + kUpFewWarps, 0);
+        if (live & 7) cut(w, pass);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          if (n >= nt) break;
+#pragma unroll
+          for (int term = 1; term >= 0; --term) {
+            uint32_t h[W / 2];
+            const uint32_t p = terms + (n * 8 + term * 16) * pitch + pass * kPass * 2;
+            if constexpr (W == 4) {
+              const uint2 v = ld_shared_v2(p);
+              h[0] = v.x, h[1] = v.y;
+            } else {
+#pragma unroll
+              for (int i = 0; i < W / 8; ++i) {
+                const uint4 v = ld_shared_v4(p + i * 16);
+                h[4 * i] = v.x, h[4 * i + 1] = v.y, h[4 * i + 2] = v.z, h[4 * i + 3] = v.w;
+              }
+            }
+#pragma unroll
+            for (int m = 0; m < kMma; ++m)
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+                mma_16816(acc[q][n], w[2 * q][2 * m], w[2 * q + 1][2 * m], w[2 * q][2 * m + 1], w[2 * q + 1][2 * m + 1], h[2 * m], h[2 * m + 1]);
+          }
         }
-      if (in && p0 + i < t.count) a.out[tok[i] * a.ldo + col] = live ? __float2half_rn(__half2float(y[i]) + acc[i][0]) : y[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < W / 2; ++i) w[j][i] = next[j][i];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (my_tok[i] < 0 || col >= a.N) continue;
+        uint2 o = y[i];
+        if (live) {
+          const int n = i >> 1, k = i & 1;
+          const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&y[i].x)), hi = __half22float2(*reinterpret_cast<const __half2*>(&y[i].y));
+          const float f = my_back[i];
+          o.x = pack_half2(fmaf(acc[0][n][k], f, lo.x), fmaf(acc[0][n][2 + k], f, lo.y));
+          o.y = pack_half2(fmaf(acc[1][n][k], f, hi.x), fmaf(acc[1][n][2 + k], f, hi.y));
+        }
+        *reinterpret_cast<uint2*>(a.out + my_tok[i] * a.ldo + col) = o;
+      }
     }
   }
 }
 
 // ---------------------------------------------------------------- up, many tokens
-// A CTA takes a tile of at most 128 tokens and a run of column tiles of 64.  h of the tile is split once into two
-// fp16 terms, h 2^e = hi + lo with 2^e of the token's own (its largest h 2^e in [2^14, 2^15)): 22 bits, of h down to
-// 2^-39 of the token's largest.  A column tile's rows of B and elements of y come by cp.async one tile ahead; the
+// A CTA takes a tile of at most 128 tokens and a run of column tiles of 64.  h of the tile is split once into its
+// terms.  A column tile's rows of B and elements of y come by cp.async one tile ahead; the
 // result goes back to y's place in shared memory and from there to out in whole rows.
 constexpr int kUpThreads = 256, kUpRows = 128, kUpCols = 64;
 constexpr int kUpYPitch = kUpCols * 2 + 16;  // bytes
@@ -309,29 +397,16 @@ __global__ void __launch_bounds__(kUpThreads) adapter_up_kernel(const AdapterArg
       top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
     }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    // 2^(14 - exponent of top); 0 and what is not finite stay as they are
-    int e = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
-    if (!(top > 0.f) || !(top < INFINITY)) e = 0;
-    e = max(-126, min(126, e));
-    const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-    if (half == 0) back[row] = __uint_as_float((uint32_t)(127 - e) << 23);
+    float bk;
+    const float up = up_scale(top, bk);
+    if (half == 0) back[row] = bk;
     for (int r = half * 4; r < ks * 16; r += 8) {
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (row < t.count && r < a.R) {
-        const float4 f = *reinterpret_cast<const float4*>(h + r);
-        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-      }
-      __half hi[4], lo[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float s = v[j] * up;
-        hi[j] = __float2half_rn(s);
-        const float f = __half2float(hi[j]);
-        lo[j] = fabsf(f) < INFINITY ? __float2half_rn(s - f) : __half();
-      }
+      const float4 v = row < t.count && r < a.R ? *reinterpret_cast<const float4*>(h + r) : make_float4(0, 0, 0, 0);
+      uint2 hi, lo;
+      two_terms(v, up, hi, lo);
       unsigned char* p = up_smem + row * pitch + r * 2;
-      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(hi);
-      *reinterpret_cast<uint2*>(p + kUpRows * pitch) = *reinterpret_cast<const uint2*>(lo);
+      *reinterpret_cast<uint2*>(p) = hi;
+      *reinterpret_cast<uint2*>(p + kUpRows * pitch) = lo;
     }
   }
   // warps: four by rows of 32, two by columns of 32
@@ -433,7 +508,7 @@ static cudaError_t launch(void (*fn)(Args...), dim3 grid, int threads, size_t sm
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-// Up to this many tokens of a step the product with B runs on the CUDA cores in fp32.
+// Up to this many tokens of a step the tiles are of 16.
 constexpr int kFewTokens = 256;
 
 }  // namespace tb
@@ -508,11 +583,15 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
 #undef TB_DOWN
   if (e == cudaSuccess) {
     if (few) {
-      const dim3 cols((unsigned)up, (unsigned)((N + kUpFewThreads - 1) / kUpFewThreads));
-      e = R <= 8    ? launch(adapter_up_few_kernel<1>, cols, kUpFewThreads, 0, s, 1, true, g)
-          : R <= 16 ? launch(adapter_up_few_kernel<2>, cols, kUpFewThreads, 0, s, 1, true, g)
-          : R <= 32 ? launch(adapter_up_few_kernel<4>, cols, kUpFewThreads, 0, s, 1, true, g)
-                    : launch(adapter_up_few_kernel<8>, cols, kUpFewThreads, 0, s, 1, true, g);
+      // two CTAs an SM share all tiles' columns; at least 128 columns each
+      const int W = R <= 16 ? 4 : R <= 32 ? 8 : 16;
+      const size_t smem = (size_t)32 * ((R + W * 4 - 1) / (W * 4) * W * 8 + 16);
+      int64_t ctas = up * ((N + 127) / 128);
+      if (ctas > 2 * f.sms) ctas = 2 * f.sms;
+      const dim3 some((unsigned)ctas);
+      e = W == 4   ? launch(adapter_up_few_kernel<4>, some, kUpFewThreads, smem, s, 1, true, g)
+          : W == 8 ? launch(adapter_up_few_kernel<8>, some, kUpFewThreads, smem, s, 1, true, g)
+                   : launch(adapter_up_few_kernel<16>, some, kUpFewThreads, smem, s, 1, true, g);
     } else {
       const size_t smem = up_smem_bytes((int)R);
       rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_up_kernel), f.device, (int)smem);
