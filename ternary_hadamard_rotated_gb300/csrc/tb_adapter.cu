@@ -52,19 +52,53 @@ TB_DEVI void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+TB_DEVI void cp_async16(uint32_t dst, const void* src, int bytes) {  // the rest of the 16 bytes is zeroed
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+TB_DEVI void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+
 // ---------------------------------------------------------------- down
-// A CTA takes MT x 16 tokens by NT x 8 rows of A; its warps and those of its cluster share out K in steps of 32.
-// A step's operands go from global memory straight to the mma's registers: thread (g, c) of a warp holds 8
+// Parts of a tile's h, [PARTS][M][N] in shared memory, summed in their order, then over the cluster's CTAs in theirs.
+template <int PARTS, int M, int N, int THREADS>
+TB_DEVI void join_down(const AdapterArgs& a, const AdapterTile& t, float* part, int share, int r0, int live) {
+  const int tid = threadIdx.x;
+  const float scale = __ldg(a.scale + t.adapter);
+  auto store = [&](int e, float s) {
+    const int row = e / N, r = r0 + e % N;
+    if (row < t.count && r < a.R) a.h[(int64_t)(t.first + row) * a.R + r] = r < live ? s * scale : 0.f;
+  };
+  __syncthreads();
+  for (int e = tid; e < M * N; e += THREADS) {
+    float s = part[e];
+#pragma unroll
+    for (int w = 1; w < PARTS; ++w) s += part[w * M * N + e];
+    if (a.cluster == 1) store(e, s);
+    else part[e] = s;
+  }
+  if (a.cluster == 1) return;
+  cg::cluster_group cl = cg::this_cluster();
+  cl.sync();
+  for (int e = share * THREADS + tid; e < M * N; e += a.cluster * THREADS) {
+    float s = 0.f;
+    for (int r = 0; r < a.cluster; ++r) s += *cl.map_shared_rank(part + e, r);
+    store(e, s);
+  }
+  cl.sync();  // the parts stay until they have been read
+}
+
+// Few tokens: a CTA takes 16 tokens by NT x 8 rows of A; its warps and those of its cluster share out K in steps of
+// 32.  A step's operands go from global memory straight to the mma's registers: thread (g, c) of a warp holds 8
 // neighbouring elements of rows g (and g + 8), which serve as the k's 2c, 2c + 1, 2c + 8 and 2c + 9 of two MMAs: a
 // product over k does not mind their order, if both operands have the same.
 constexpr int kDownThreads = 256, kDownWarps = kDownThreads / 32;
 
-template <int MT, int NT>
-__global__ void __launch_bounds__(kDownThreads, MT * NT > 8 ? 1 : 2) adapter_down_kernel(const AdapterArgs a) {
-  constexpr int M = MT * 16, N = NT * 8;
-  constexpr int kUnroll = MT * 2 + NT <= 4 ? 4 : 2;
-  extern __shared__ __align__(16) float part_smem[];
-  float (*part)[M][N] = reinterpret_cast<float (*)[M][N]>(part_smem);  // of each warp
+template <int NT>
+__global__ void __launch_bounds__(kDownThreads, 2) adapter_down_few_kernel(const AdapterArgs a) {
+  constexpr int N = NT * 8;
+  constexpr int kUnroll = NT <= 2 ? 4 : 2;
+  extern __shared__ __align__(128) unsigned char down_smem[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!plan_fits(a)) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(a.status, TB_DEV_BAD_PLAN);
@@ -78,79 +112,138 @@ __global__ void __launch_bounds__(kDownThreads, MT * NT > 8 ? 1 : 2) adapter_dow
   const int r0 = blockIdx.y * N, live = live_rank(a, t.adapter);
   const int nt_live = min(NT, max(0, (live - r0 + 7) >> 3));
 
-  const __half* xr[MT * 2];
+  const __half* xr[2];
 #pragma unroll
-  for (int i = 0; i < MT * 2; ++i) {
-    const int row = i * 8 + g;
-    xr[i] = row < t.count ? a.x + a.order[t.first + row] * a.ldx + c * 8 : nullptr;
-  }
+  for (int i = 0; i < 2; ++i) xr[i] = i * 8 + g < t.count ? a.x + a.order[t.first + i * 8 + g] * a.ldx + c * 8 : nullptr;
   const __half* ar = a.a + ((int64_t)t.adapter * a.R + r0 + g) * a.K + c * 8;
-  float acc[MT][NT][4];
+  float acc[NT][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
   const int steps = (a.K + 31) >> 5, stride = a.cluster * kDownWarps;
   if (nt_live > 0) {
     for (int s = share * kDownWarps + warp; s < steps; s += stride * kUnroll) {
-      uint4 xv[kUnroll][MT * 2], av[kUnroll][NT];
+      uint4 xv[kUnroll][2], av[kUnroll][NT];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int k = (s + u * stride) * 32;
         const bool in = k + c * 8 < a.K;
 #pragma unroll
-        for (int i = 0; i < MT * 2; ++i)
+        for (int i = 0; i < 2; ++i)
           xv[u][i] = in && xr[i] ? __ldg(reinterpret_cast<const uint4*>(xr[i] + k)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           av[u][n] = in && n < nt_live && r0 + n * 8 + g < a.R ? __ldg(reinterpret_cast<const uint4*>(ar + (int64_t)n * 8 * a.K + k)) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
+      for (int u = 0; u < kUnroll; ++u) {
+        const uint4 p = xv[u][0], q = xv[u][1];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint4 p = xv[u][2 * m], q = xv[u][2 * m + 1];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_16816(acc[m][n], p.x, q.x, p.y, q.y, av[u][n].x, av[u][n].y);
-            mma_16816(acc[m][n], p.z, q.z, p.w, q.w, av[u][n].z, av[u][n].w);
-          }
+        for (int n = 0; n < NT; ++n) {
+          mma_16816(acc[n], p.x, q.x, p.y, q.y, av[u][n].x, av[u][n].y);
+          mma_16816(acc[n], p.z, q.z, p.w, q.w, av[u][n].z, av[u][n].w);
         }
+      }
     }
   }
+  float* part = reinterpret_cast<float*>(down_smem) + warp * 16 * N;
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      *reinterpret_cast<float2*>(&part[warp][m * 16 + g][n * 8 + 2 * c]) = make_float2(acc[m][n][0], acc[m][n][1]);
-      *reinterpret_cast<float2*>(&part[warp][m * 16 + g + 8][n * 8 + 2 * c]) = make_float2(acc[m][n][2], acc[m][n][3]);
-    }
-  __syncthreads();
-  for (int e = tid; e < M * N; e += kDownThreads) {  // the warps' parts, in their order
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < kDownWarps; ++w) s += (&part[w][0][0])[e];
-    (&part[0][0][0])[e] = s;
+  for (int n = 0; n < NT; ++n) {
+    *reinterpret_cast<float2*>(part + g * N + n * 8 + 2 * c) = make_float2(acc[n][0], acc[n][1]);
+    *reinterpret_cast<float2*>(part + (g + 8) * N + n * 8 + 2 * c) = make_float2(acc[n][2], acc[n][3]);
   }
-  const float scale = __ldg(a.scale + t.adapter);
-  auto store = [&](int e, float s) {
-    const int row = e / N, r = r0 + e % N;
-    if (row < t.count && r < a.R) a.h[(int64_t)(t.first + row) * a.R + r] = r < live ? s * scale : 0.f;
-  };
-  if (a.cluster == 1) {
-    for (int e = tid; e < M * N; e += kDownThreads) store(e, (&part[0][0][0])[e]);
+  join_down<kDownWarps, 16, N, kDownThreads>(a, t, reinterpret_cast<float*>(down_smem), share, r0, live);
+}
+
+// Many tokens: a CTA takes 32 tokens by NT x 8 rows of A, both through shared memory by cp.async, 64 of K a stage and
+// kStages - 1 stages ahead; rows of 128 bytes, their 16-byte pieces exchanged by row (piece ^ row mod 8), so that
+// ldmatrix finds eight rows in eight different banks.  Warps: two by rows, four by the stage's k's.
+constexpr int kManyRows = 32, kStages = 8;
+
+template <int NT>
+constexpr int down_many_smem() {
+  const int stages = kStages * (kManyRows + NT * 8) * 128, parts = 4 * kManyRows * NT * 8 * 4;
+  return stages > parts ? stages : parts;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kDownThreads, 2) adapter_down_many_kernel(const AdapterArgs a) {
+  constexpr int N = NT * 8, kStageBytes = (kManyRows + N) * 128;
+  extern __shared__ __align__(128) unsigned char down_smem[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!plan_fits(a)) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(a.status, TB_DEV_BAD_PLAN);
     return;
   }
-  cg::cluster_group cl = cg::this_cluster();
-  cl.sync();
-  for (int e = share * kDownThreads + tid; e < M * N; e += a.cluster * kDownThreads) {  // the CTAs' parts, in theirs
-    float s = 0.f;
-    for (int r = 0; r < a.cluster; ++r) s += *cl.map_shared_rank(&part[0][0][0] + e, r);
-    store(e, s);
+  const int tile = blockIdx.x / a.cluster, share = blockIdx.x - tile * a.cluster;
+  if (tile >= a.plan->tiles[a.down_kind]) return;  // (all CTAs of the cluster)
+  const AdapterTile t = a.down_tiles[tile];
+  if (t.adapter >= a.n) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int r0 = blockIdx.y * N, live = live_rank(a, t.adapter);
+  const uint32_t base = smem_u32(down_smem);
+  const int steps = (a.K + 63) >> 6, mine = (steps - share + a.cluster - 1) / a.cluster;
+
+  // a thread's pieces of a stage: one of x, NT / 4 of A
+  const int row = tid >> 3, piece = tid & 7;
+  const uint32_t at = row * 128 + ((piece ^ (row & 7)) << 4);
+  const bool has_x = row < t.count;
+  const __half* xp = a.x + (has_x ? a.order[t.first + row] * a.ldx : 0) + piece * 8;
+  const __half* ap = a.a + ((int64_t)t.adapter * a.R + r0 + row) * a.K + piece * 8;
+  auto fetch = [&](int i) {
+    const int k = (share + i * a.cluster) * 64;
+    const uint32_t dst = base + (i % kStages) * kStageBytes + at;
+    const bool in = k + piece * 8 < a.K;
+    cp_async16(dst, has_x && in ? xp + k : a.x, has_x && in ? 16 : 0);
+#pragma unroll
+    for (int j = 0; j < (NT + 3) / 4; ++j)
+      if (NT >= 4 || row < N) {
+        const bool have = in && r0 + row + j * 32 < live;
+        cp_async16(dst + (kManyRows + j * 32) * 128, have ? ap + (int64_t)j * 32 * a.K + k : a.a, have ? 16 : 0);
+      }
+  };
+  float acc[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+  if (r0 < live) {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (i < mine) fetch(i);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    const int wm = warp & 1, wk = (warp >> 1) * 2;  // rows of 16, pieces of the stage
+    // ldmatrix: lanes 0-15 rows, lanes 16-31 the same rows' next piece; for A rows 0-7, their next piece, rows 8-15
+    const int xr = wm * 16 + (lane & 15), br = (lane & 7) + (lane >> 4) * 8;
+    const uint32_t x_at = xr * 128 + (((wk + (lane >> 4)) ^ (xr & 7)) << 4);
+    const uint32_t b_at = (kManyRows + br) * 128 + (((wk + (lane >> 3 & 1)) ^ (br & 7)) << 4);
+    for (int i = 0; i < mine; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncthreads();  // stage i is there, and stage i - 1 has been used
+      if (i + kStages - 1 < mine) fetch(i + kStages - 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      const uint32_t st = base + (i % kStages) * kStageBytes;
+      uint32_t x[4], b[4];
+      ldmatrix4(x, st + x_at);
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        ldmatrix4(b, st + b_at + n * 8 * 128);
+        mma_16816(acc[n], x[0], x[1], x[2], x[3], b[0], b[1]);
+        mma_16816(acc[n + 1], x[0], x[1], x[2], x[3], b[2], b[3]);
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the stages' place is the parts' now
   }
-  cl.sync();  // the parts stay until they have been read
+  float* part = reinterpret_cast<float*>(down_smem) + (warp >> 1) * kManyRows * N + (warp & 1) * 16 * N;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    *reinterpret_cast<float2*>(part + g * N + n * 8 + 2 * c) = make_float2(acc[n][0], acc[n][1]);
+    *reinterpret_cast<float2*>(part + (g + 8) * N + n * 8 + 2 * c) = make_float2(acc[n][2], acc[n][3]);
+  }
+  join_down<4, kManyRows, N, kDownThreads>(a, t, reinterpret_cast<float*>(down_smem), share, r0, live);
 }
 
 // ---------------------------------------------------------------- h as fp16
@@ -335,152 +428,176 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
 }
 
 // ---------------------------------------------------------------- up, many tokens
-// A CTA takes a tile of at most 128 tokens and a run of column tiles of 64.  h of the tile is split once into its
-// terms.  A column tile's rows of B and elements of y come by cp.async one tile ahead; the
-// result goes back to y's place in shared memory and from there to out in whole rows.
-constexpr int kUpThreads = 256, kUpRows = 128, kUpCols = 64;
-constexpr int kUpYPitch = kUpCols * 2 + 16;  // bytes
+// A CTA takes a tile of at most 128 tokens and a run of column tiles of 64, a warp 16 of the tokens.  A thread keeps its
+// tokens' terms as the mma's left operand (up to 64 ranks; above, they are read from shared memory), and B's rows
+// come by cp.async two column tiles ahead.  Which column of out is which of the MMAs' columns is free: thread (g, c)
+// has 16 neighbouring ones of tokens g and g + 8, so that y and out go between global memory and registers in whole
+// sectors, y one column tile ahead.
+constexpr int kUpThreads = 256, kUpCols = 64, kUpStages = 3;
 
-TB_DEVI void cp_async16(uint32_t dst, const void* src, int bytes) {  // the rest of the 16 bytes is zeroed
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-TB_DEVI void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
-}
+// bytes of a row of B in shared memory: an odd number of 32, so that four rows' 32 bytes lie in different banks
+__host__ __device__ __forceinline__ int up_pitch(int R) { return ((R + 15) / 16 | 1) * 32; }
 
-TB_DEVI int up_pitch(int R) { return (R + 15) / 16 * 32 + 16; }  // bytes of a row of hi, lo or B: an odd number of 16
-
-__global__ void __launch_bounds__(kUpThreads) adapter_up_kernel(const AdapterArgs a) {
-  extern __shared__ __align__(16) unsigned char up_smem[];
-  __shared__ int tok[kUpRows];
-  __shared__ float back[kUpRows];  // 2^-e
+// KS: steps of 16 ranks; kept in registers up to 4
+template <int KS>
+__global__ void __launch_bounds__(kUpThreads, KS <= 8 ? 2 : 1) adapter_up_many_kernel(const AdapterArgs a) {
+  constexpr bool kKeep = KS <= 4;
+  extern __shared__ __align__(128) unsigned char up_smem[];
   if (!plan_fits(a)) return;
-  const int tile = blockIdx.x / a.groups, group = blockIdx.x - tile * a.groups;
+  const int tile = blockIdx.x, group = blockIdx.y;  // tiles first: those of one adapter read the same rows of B
   if (tile >= a.plan->tiles[a.up_kind]) return;
   const AdapterTile t = a.up_tiles[tile];
   const int live = live_rank(a, t.adapter);
   if (live == 0 && a.out == a.y) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int pitch = up_pitch(a.R), ks = (live + 15) >> 4;
-  const uint32_t hi_at = smem_u32(up_smem), lo_at = hi_at + kUpRows * pitch, stage_at = lo_at + kUpRows * pitch;
-  const uint32_t stage_bytes = kUpCols * pitch + kUpRows * kUpYPitch;
-  for (int i = tid; i < kUpRows; i += kUpThreads) tok[i] = i < t.count ? a.order[t.first + i] : -1;
-  __syncthreads();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int pitch = up_pitch(a.R), ks = (live + 15) >> 4, pieces = a.R >> 3;
+  const uint32_t base = smem_u32(up_smem), stage_bytes = kUpCols * pitch, terms_at = base + kUpStages * stage_bytes;
   const int tiles = (a.N + kUpCols - 1) / kUpCols;
-  const int n_begin = (int)((int64_t)tiles * group / a.groups), n_end = (int)((int64_t)tiles * (group + 1) / a.groups);
+  const int begin = (int)((int64_t)tiles * group / a.groups), end = (int)((int64_t)tiles * (group + 1) / a.groups);
 
+  // column 16 c + 2 j + i of a tile is column 2 c + i of MMA j: its row of B lies at 8 j + 2 c + i
+  const __half* bg = a.b + (int64_t)min(t.adapter, a.n - 1) * a.N * a.R;
   auto fetch = [&](int nt) {
-    const uint32_t bs = stage_at + (nt - n_begin & 1) * stage_bytes, ys = bs + kUpCols * pitch;
-    const int n0 = nt * kUpCols;
-    const int pieces = ks * 2;  // 16-byte pieces of a row of B
-    for (int i = tid; i < kUpCols * pieces; i += kUpThreads) {
-      const int row = i / pieces, p = i - row * pieces;
-      const int left = n0 + row < a.N ? min(16, max(0, (live - p * 8) * 2)) : 0;
-      cp_async16(bs + row * pitch + p * 16, left ? a.b + ((int64_t)t.adapter * a.N + n0 + row) * a.R + p * 8 : a.b, left);
+    const uint32_t st = base + (nt - begin) % kUpStages * stage_bytes;
+    const int rows = min(kUpCols, a.N - nt * kUpCols);
+    const __half* src = bg + (int64_t)nt * kUpCols * a.R;
+    for (int i = tid; i < rows * pieces; i += kUpThreads) {  // (a tile's rows of B are one run of memory)
+      const int col = i / pieces, p = i - col * pieces;
+      const int at = (col >> 1 & 7) * 8 + (col >> 4) * 2 + (col & 1);
+      if (p * 8 < live) cp_async16(st + at * pitch + p * 16, src + i * 8, 16);
     }
-#pragma unroll
-    for (int i = tid; i < kUpRows * (kUpCols / 8); i += kUpThreads) {
-      const int row = i / (kUpCols / 8), p = i % (kUpCols / 8);
-      if (tok[row] >= 0 && n0 + p * 8 < a.N) cp_async16(ys + row * kUpYPitch + p * 16, a.y + tok[row] * a.ldy + n0 + p * 8, 16);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (n_begin < n_end) fetch(n_begin);
-
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // h is written
-  {  // two threads a token: its largest h, then its terms
-    const int row = tid >> 1, half = tid & 1;
-    const float* h = a.h + (int64_t)(t.first + min(row, t.count - 1)) * a.R;
-    float top = 0.f;
-    for (int r = half * 4; r < live; r += 8) {
-      const float4 v = *reinterpret_cast<const float4*>(h + r);
-      top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
-    }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    float bk;
-    const float up = up_scale(top, bk);
-    if (half == 0) back[row] = bk;
-    for (int r = half * 4; r < ks * 16; r += 8) {
-      const float4 v = row < t.count && r < a.R ? *reinterpret_cast<const float4*>(h + r) : make_float4(0, 0, 0, 0);
-      uint2 hi, lo;
-      two_terms(v, up, hi, lo);
-      unsigned char* p = up_smem + row * pitch + r * 2;
-      *reinterpret_cast<uint2*>(p) = hi;
-      *reinterpret_cast<uint2*>(p + kUpRows * pitch) = lo;
+  const int p0 = warp * 16 + g;  // the thread's tokens: p0 and p0 + 8 of the tile
+  int tok[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) tok[i] = p0 + 8 * i < t.count ? a.order[t.first + p0 + 8 * i] : -1;
+  uint4 y[2][2];
+  auto load_y = [&](uint4 (&v)[2][2], int nt) {
+    const int col = nt * kUpCols + 16 * c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (tok[i] >= 0 && col + 8 * q < a.N) v[i][q] = __ldcs(reinterpret_cast<const uint4*>(a.y + tok[i] * a.ldy + col) + q);
+  };
+  if (live) {
+#pragma unroll
+    for (int i = 0; i < kUpStages - 1; ++i) {
+      if (begin + i < end) fetch(begin + i);
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
   }
-  // warps: four by rows of 32, two by columns of 32
-  const int wr = (warp >> 1) * 32, wc = (warp & 1) * 32, g = lane >> 2, c = lane & 3;
-  const int m_live = min(2, max(0, (t.count - wr + 15) >> 4));
-  const uint32_t a_lane = hi_at + (wr + (lane & 15)) * pitch + (lane >> 4) * 16;
-  const uint32_t b_lane = (wc + (lane & 7) + (lane >> 4) * 8) * pitch + (lane >> 3 & 1) * 16;
-  for (int nt = n_begin; nt < n_end; ++nt) {
-    const uint32_t bs = stage_at + (nt - n_begin & 1) * stage_bytes;
-    unsigned char* ys = up_smem + (bs - hi_at) + kUpCols * pitch;
-    if (nt + 1 < n_end) {
-      fetch(nt + 1);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
+  load_y(y, begin);
+  uint32_t hi[kKeep ? KS : 1][4], lo[kKeep ? KS : 1][4];
+  float back[2];
+  if (live) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // h is written
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float* h = a.h + (int64_t)(t.first + min(p0 + 8 * i, t.count - 1)) * a.R;
+      float top = 0.f;
+      for (int r = 4 * c; r < live; r += 16) {
+        const float4 v = *reinterpret_cast<const float4*>(h + r);
+        top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float up = up_scale(top, back[i]);
+      // ranks 16 k + 4 c .. + 3 serve as the k's 2 c, 2 c + 1, 2 c + 8, 2 c + 9; B's are permuted below alike
+      auto at_step = [&](int k, uint2& h2, uint2& l2) {
+        const int r = 16 * k + 4 * c;
+        two_terms(r < a.R ? *reinterpret_cast<const float4*>(h + r) : make_float4(0, 0, 0, 0), up, h2, l2);
+      };
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          uint2 h2, l2;
+          at_step(k, h2, l2);
+          hi[k][i] = h2.x, hi[k][i + 2] = h2.y;
+          lo[k][i] = l2.x, lo[k][i + 2] = l2.y;
+        }
+      } else {
+        for (int k = 0; k < ks; ++k) {  // a lane's own 16 bytes of each term a step
+          uint2 h2, l2;
+          at_step(k, h2, l2);
+          uint32_t* p = reinterpret_cast<uint32_t*>(up_smem + kUpStages * stage_bytes + (((warp * KS + k) * 2) * 32 + lane) * 16);
+          p[i] = h2.x, p[i + 2] = h2.y;
+          p[i + 128] = l2.x, p[i + 130] = l2.y;
+        }
+      }
     }
-    __syncthreads();
-    float acc[2][4][4];
+  }
+  // the rank's end inside a step: what B holds behind it
+  const int left = live - (ks - 1) * 16 - 4 * c;
+  const uint32_t m0 = left <= 0 ? 0u : left == 1 ? 0xffffu : ~0u, m1 = left <= 2 ? 0u : left == 3 ? 0xffffu : ~0u;
+  for (int nt = begin; nt < end; ++nt) {
+    uint4 next[2][2];
+    float acc[8][4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int n = 0; n < 8; ++n)
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    if (nt + 1 < end) load_y(next, nt + 1);
+    if (live) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kUpStages - 2) : "memory");
+      __syncthreads();  // tile nt is there, and tile nt - 1 has been used
+      if (nt + kUpStages - 1 < end) fetch(nt + kUpStages - 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      const uint32_t st = base + (nt - begin) % kUpStages * stage_bytes + g * pitch + c * 8;
+      auto step = [&](int k, const uint32_t (&h)[4], const uint32_t (&l)[4], bool last) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-    if (m_live > 0)
-      for (int k = 0; k < ks; ++k) {
-        uint32_t b[2][4];
-        ldmatrix4(b[0], bs + b_lane + k * 32);
-        ldmatrix4(b[1], bs + b_lane + 16 * pitch + k * 32);
+        for (int n = 0; n < 8; ++n) {
+          uint2 b = ld_shared_v2(st + n * 8 * pitch + k * 32);
+          if (last) b.x &= m0, b.y &= m1;
+          mma_16816(acc[n], l[0], l[1], l[2], l[3], b.x, b.y);
+          mma_16816(acc[n], h[0], h[1], h[2], h[3], b.x, b.y);
+        }
+      };
+      if (warp * 16 < t.count) {
+        if constexpr (kKeep) {
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          if (m >= m_live) break;
-          uint32_t hi[4], lo[4];
-          ldmatrix4(hi, a_lane + m * 16 * pitch + k * 32);
-          ldmatrix4(lo, a_lane + (kUpRows + m * 16) * pitch + k * 32);
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            mma_16816(acc[m][n], lo[0], lo[1], lo[2], lo[3], b[n >> 1][(n & 1) * 2], b[n >> 1][(n & 1) * 2 + 1]);
-            mma_16816(acc[m][n], hi[0], hi[1], hi[2], hi[3], b[n >> 1][(n & 1) * 2], b[n >> 1][(n & 1) * 2 + 1]);
+          for (int k = 0; k < KS; ++k)
+            if (k < ks) step(k, hi[k], lo[k], k == ks - 1);
+        } else {
+          for (int k = 0; k < ks; ++k) {
+            uint32_t h[4], l[4];
+            const uint32_t p = terms_at + (((warp * KS + k) * 2) * 32 + lane) * 16;
+            const uint4 u = ld_shared_v4(p), v = ld_shared_v4(p + 512);
+            h[0] = u.x, h[1] = u.y, h[2] = u.z, h[3] = u.w;
+            l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
+            step(k, h, l, k == ks - 1);
           }
         }
       }
-    if (live) {
+    }
+    const int col = nt * kUpCols + 16 * c;
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = wr + m * 16 + i * 8 + g;
-          if (row >= t.count) continue;
-          const float f = back[row];
-          unsigned char* yr = ys + row * kUpYPitch + (wc + 2 * c) * 2;
+      for (int q = 0; q < 2; ++q) {
+        if (tok[i] < 0 || col + 8 * q >= a.N) continue;
+        uint4 o = y[i][q];
+        if (live) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(&o);
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            __half2* p = reinterpret_cast<__half2*>(yr + n * 16);
-            const float2 y = __half22float2(*p);
-            *p = __floats2half2_rn(fmaf(acc[m][n][2 * i], f, y.x), fmaf(acc[m][n][2 * i + 1], f, y.y));
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+            w[j] = pack_half2(fmaf(acc[4 * q + j][2 * i], back[i], f.x), fmaf(acc[4 * q + j][2 * i + 1], back[i], f.y));
           }
         }
-    }
-    __syncwarp();
-    const int n0 = nt * kUpCols + wc;
+        __stcs(reinterpret_cast<uint4*>(a.out + tok[i] * a.ldo + col) + q, o);
+      }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // the warp's 32 x 32: a row of 64 bytes by four lanes
-      const int row = wr + i * 8 + (lane >> 2), col = n0 + (lane & 3) * 8;
-      if (row < t.count && col < a.N)
-        *reinterpret_cast<uint4*>(a.out + tok[row] * a.ldo + col) = *reinterpret_cast<const uint4*>(ys + row * kUpYPitch + (wc + (lane & 3) * 8) * 2);
-    }
-    __syncthreads();  // the stage may be filled again
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) y[i][q] = next[i][q];
   }
 }
 
-static size_t up_smem_bytes(int R) {
-  const size_t pitch = (size_t)(R + 15) / 16 * 32 + 16;
-  return 2 * kUpRows * pitch + 2 * (kUpCols * pitch + (size_t)kUpRows * kUpYPitch);
+static size_t up_many_smem(int R) {
+  const size_t pitch = up_pitch(R);
+  const int steps = R <= 64 ? 0 : R <= 128 ? 8 : 16;
+  return kUpStages * kUpCols * pitch + (size_t)steps * 8 * 2 * 512;
 }
 
 template <typename... Args>
@@ -567,20 +684,28 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   g.R = (int)R;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t down = adapter_max_tiles(T, n, g.down_kind), up = adapter_max_tiles(T, n, g.up_kind);
-  // down: K is split over a cluster until there are four CTAs an SM, of at least four steps a warp
+  // few tokens: K is split over a cluster until there are two CTAs an SM, of at least four steps a warp; many: until
+  // every SM has one
   g.cluster = 1;
-  while (g.cluster < 8 && down * g.cluster * 2 <= 4 * f.sms && K / 32 >= g.cluster * 2 * kDownWarps) g.cluster *= 2;
+  if (few)
+    while (g.cluster < 8 && down * g.cluster < 2 * f.sms && K / 32 >= g.cluster * 2 * kDownWarps) g.cluster *= 2;
+  else
+    while (g.cluster < 8 && down * g.cluster * 2 <= 2 * f.sms && K / 64 >= g.cluster * 2 * kStages) g.cluster *= 2;
   const int nt = R <= 16 ? 2 : R <= 32 ? 4 : 8;
   const dim3 grid((unsigned)(down * g.cluster), (unsigned)((R + nt * 8 - 1) / (nt * 8)));
   cudaError_t e;
-  const int parts = kDownWarps * (few ? 16 : 32) * nt * 8 * 4;  // bytes
-  if (!few && nt == 8 && (rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_down_kernel<2, 8>), f.device, parts)) != TB_OK) return rc;
-#define TB_DOWN(MT, NT) launch(adapter_down_kernel<MT, NT>, grid, kDownThreads, (size_t)parts, s, g.cluster, false, g)
+#define TB_DOWN_FEW(NT) launch(adapter_down_few_kernel<NT>, grid, kDownThreads, (size_t)kDownWarps * 16 * NT * 8 * 4, s, g.cluster, false, g)
+#define TB_DOWN_MANY(NT)                                                                                                        \
+  ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_down_many_kernel<NT>), f.device, down_many_smem<NT>())) != TB_OK \
+       ? cudaErrorUnknown                                                                                                       \
+       : launch(adapter_down_many_kernel<NT>, grid, kDownThreads, (size_t)down_many_smem<NT>(), s, g.cluster, false, g))
   if (few)
-    e = nt == 2 ? TB_DOWN(1, 2) : nt == 4 ? TB_DOWN(1, 4) : TB_DOWN(1, 8);
+    e = nt == 2 ? TB_DOWN_FEW(2) : nt == 4 ? TB_DOWN_FEW(4) : TB_DOWN_FEW(8);
   else
-    e = nt == 2 ? TB_DOWN(2, 2) : nt == 4 ? TB_DOWN(2, 4) : TB_DOWN(2, 8);
-#undef TB_DOWN
+    e = nt == 2 ? TB_DOWN_MANY(2) : nt == 4 ? TB_DOWN_MANY(4) : TB_DOWN_MANY(8);
+#undef TB_DOWN_FEW
+#undef TB_DOWN_MANY
+  if (rc != TB_OK) return rc;
   if (e == cudaSuccess) {
     if (few) {
       // two CTAs an SM share all tiles' columns; at least 128 columns each
@@ -593,14 +718,19 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
           : W == 8 ? launch(adapter_up_few_kernel<8>, some, kUpFewThreads, smem, s, 1, true, g)
                    : launch(adapter_up_few_kernel<16>, some, kUpFewThreads, smem, s, 1, true, g);
     } else {
-      const size_t smem = up_smem_bytes((int)R);
-      rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_up_kernel), f.device, (int)smem);
-      if (rc != TB_OK) return rc;
-      // several CTAs a row tile, so that each SM has a few; each takes a run of column tiles
+      const size_t smem = up_many_smem((int)R);
+      // several CTAs a row tile, each with a run of column tiles
       const int64_t col_tiles = (N + kUpCols - 1) / kUpCols;
       int64_t groups = (6ll * f.sms + up - 1) / up;
       g.groups = (int)(groups < 1 ? 1 : groups > col_tiles ? col_tiles : groups);
-      e = launch(adapter_up_kernel, dim3((unsigned)(up * g.groups)), kUpThreads, smem, s, 1, true, g);
+      const dim3 some((unsigned)up, (unsigned)g.groups);
+#define TB_UP(KS)                                                                                                           \
+  ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_up_many_kernel<KS>), f.device, (int)smem)) != TB_OK \
+       ? cudaErrorUnknown                                                                                                   \
+       : launch(adapter_up_many_kernel<KS>, some, kUpThreads, smem, s, 1, true, g))
+      e = R <= 16 ? TB_UP(1) : R <= 32 ? TB_UP(2) : R <= 64 ? TB_UP(4) : R <= 128 ? TB_UP(8) : TB_UP(16);
+#undef TB_UP
+      if (rc != TB_OK) return rc;
     }
   }
   if (e != cudaSuccess) {
