@@ -2,9 +2,13 @@
 // adapter of token t's request.
 //
 // Two launches, the second (programmatic) loading what the first does not write before it waits for it:
-//   down  h = scale A x, fp32 [T, R] in the order of the plan; mma.sync on tiles of 16 or 32 tokens of one adapter
-//   up    out = y + B h, mma.sync with h as two fp16 terms; few tokens: tiles of 16, bound by the weights, which go
-//         from global memory straight to the registers; many: tiles of 128, bound by y and out
+//   down  h = scale A x, mma.sync on tiles of 16 or 32 tokens of one adapter, to the workspace in the plan's order
+//   up    out = y + B h, mma.sync; few tokens: tiles of 16, bound by the weights, which go from global memory straight
+//         to the registers; many: tiles of 128, bound by y and out
+//
+// h goes from one to the other as fp16 in two terms, h 2^e = hi + lo, with 2^e of the token's own for up to 64 ranks
+// (their largest |h| 2^e in [2^14, 2^15)): 22 bits, of h down to 2^-39 of that largest.  Products and sums are fp32, and
+// 2^-e is applied to each sum.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -26,12 +30,13 @@ struct AdapterArgs {
   const int32_t* order;
   const AdapterTile* down_tiles;
   const AdapterTile* up_tiles;
-  float* h;
+  __half* terms;  // [T][blocks][hi, lo][block]
+  float* back;    // [T][blocks], 2^-e
   int32_t* status;
   int64_t ldx, ldy, ldo;
   int T, n, K, N, R;
+  int block, blocks;  // ranks of a block (16, 32 or 64), blocks of R
   int cluster, down_kind, up_kind;
-  int groups;  // of column tiles: CTAs a row tile has
 };
 
 TB_DEVI bool plan_fits(const AdapterArgs& a) {
@@ -40,7 +45,6 @@ TB_DEVI bool plan_fits(const AdapterArgs& a) {
 }
 
 TB_DEVI int live_rank(const AdapterArgs& a, int g) {
-  if (g >= a.n) return 0;
   const int r = a.rank ? __ldg(a.rank + g) : a.R;
   return r < 0 ? 0 : min(r, a.R);
 }
@@ -59,58 +63,97 @@ TB_DEVI void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
 
+// ---------------------------------------------------------------- h as fp16
+// 2^e and 2^-e for numbers of which the largest |h| is top; 0 and what is not finite stay as they are
+TB_DEVI float up_scale(float top, float& back) {
+  int e = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
+  if (!(top > 0.f) || !(top < INFINITY)) e = 0;
+  e = max(-126, min(126, e));
+  back = __uint_as_float((uint32_t)(127 - e) << 23);
+  return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
 // ---------------------------------------------------------------- down
-// Parts of a tile's h, [PARTS][M][N] in shared memory, summed in their order, then over the cluster's CTAs in theirs.
+// Parts of a tile's h, [PARTS][M][N] in shared memory, summed in their order, then over the cluster's CTAs in theirs;
+// each CTA has some of the rows, a warp one at a time.
 template <int PARTS, int M, int N, int THREADS>
 TB_DEVI void join_down(const AdapterArgs& a, const AdapterTile& t, float* part, int share, int r0, int live) {
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   const float scale = __ldg(a.scale + t.adapter);
-  auto store = [&](int e, float s) {
-    const int row = e / N, r = r0 + e % N;
-    if (row < t.count && r < a.R) a.h[(int64_t)(t.first + row) * a.R + r] = r < live ? s * scale : 0.f;
-  };
   __syncthreads();
   for (int e = tid; e < M * N; e += THREADS) {
     float s = part[e];
 #pragma unroll
     for (int w = 1; w < PARTS; ++w) s += part[w * M * N + e];
-    if (a.cluster == 1) store(e, s);
-    else part[e] = s;
+    part[e] = s;
   }
-  if (a.cluster == 1) return;
   cg::cluster_group cl = cg::this_cluster();
-  cl.sync();
-  for (int e = share * THREADS + tid; e < M * N; e += a.cluster * THREADS) {
-    float s = 0.f;
-    for (int r = 0; r < a.cluster; ++r) s += *cl.map_shared_rank(part + e, r);
-    store(e, s);
+  if (a.cluster > 1) cl.sync();
+  else __syncthreads();
+  const int rows = M / a.cluster;
+  for (int i = tid >> 5; i < rows; i += THREADS / 32) {
+    const int row = share * rows + i;
+    if (row >= t.count) break;
+    constexpr int kCols = (N + 31) / 32;
+    float v[kCols], top = 0.f;
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      const int col = lane + 32 * j;
+      v[j] = 0.f;
+      if (col < N && r0 + col < live) {
+        float s = 0.f;
+        for (int r = 0; r < a.cluster; ++r) s += a.cluster > 1 ? *cl.map_shared_rank(part + row * N + col, r) : part[row * N + col];
+        v[j] = s * scale;
+      }
+      top = fmaxf(top, fabsf(v[j]));
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float back;
+    const float up = up_scale(top, back);
+    const int64_t at = (int64_t)(t.first + row) * a.blocks + blockIdx.y;
+    if (lane == 0) a.back[at] = back;
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      const int col = lane + 32 * j;
+      const __half hi = __float2half_rn(v[j] * up);
+      const float f = __half2float(hi);
+      if (col < N) {
+        a.terms[at * 2 * N + col] = hi;
+        a.terms[at * 2 * N + N + col] = fabsf(f) < INFINITY ? __float2half_rn(v[j] * up - f) : __half();
+      }
+    }
   }
-  cl.sync();  // the parts stay until they have been read
+  if (a.cluster > 1) cl.sync();  // the parts stay until they have been read
 }
 
 // Few tokens: a CTA takes 16 tokens by NT x 8 rows of A; its warps and those of its cluster share out K in steps of
-// 32.  A step's operands go from global memory straight to the mma's registers: thread (g, c) of a warp holds 8
-// neighbouring elements of rows g (and g + 8), which serve as the k's 2c, 2c + 1, 2c + 8 and 2c + 9 of two MMAs: a
-// product over k does not mind their order, if both operands have the same.
+// 32.  Thread (g, c) of a warp takes 8 neighbouring elements of rows g (and g + 8), which serve as the k's 2c, 2c + 1,
+// 2c + 8 and 2c + 9 of two MMAs: a product over k does not mind their order, if both operands have the same.  They
+// come by cp.async into a ring of the thread's own, so that several steps are in flight without registers, and no thread
+// waits for another.
 constexpr int kDownThreads = 256, kDownWarps = kDownThreads / 32;
+constexpr int few_stages(int NT) { return NT == 2 ? 5 : NT == 4 ? 4 : 2; }
+template <int NT>
+constexpr int down_few_smem() {
+  const int ring = few_stages(NT) * (2 + NT) * kDownThreads * 16, parts = kDownWarps * 16 * NT * 8 * 4;
+  return ring > parts ? ring : parts;
+}
 
 template <int NT>
 __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_few_kernel(const AdapterArgs a) {
-  constexpr int N = NT * 8;
-  constexpr int kUnroll = NT <= 2 ? 4 : 2;
+  constexpr int N = NT * 8, S = few_stages(NT);
   extern __shared__ __align__(128) unsigned char down_smem[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tile = blockIdx.x / a.cluster, share = blockIdx.x - tile * a.cluster;
+  const AdapterTile t = a.down_tiles[tile];  // (inside the plan, of a tile or not)
   if (!plan_fits(a)) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(a.status, TB_DEV_BAD_PLAN);
     return;
   }
-  const int tile = blockIdx.x / a.cluster, share = blockIdx.x - tile * a.cluster;
   if (tile >= a.plan->tiles[a.down_kind]) return;  // (all CTAs of the cluster)
-  const AdapterTile t = a.down_tiles[tile];
-  if (t.adapter >= a.n) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int r0 = blockIdx.y * N, live = live_rank(a, t.adapter);
-  const int nt_live = min(NT, max(0, (live - r0 + 7) >> 3));
 
   const __half* xr[2];
 #pragma unroll
@@ -121,31 +164,47 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_few_kernel(const
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-  const int steps = (a.K + 31) >> 5, stride = a.cluster * kDownWarps;
-  if (nt_live > 0) {
-    for (int s = share * kDownWarps + warp; s < steps; s += stride * kUnroll) {
-      uint4 xv[kUnroll][2], av[kUnroll][NT];
+  const int steps = (a.K + 31) >> 5, stride = a.cluster * kDownWarps, s0 = share * kDownWarps + warp;
+  const uint32_t ring = smem_u32(down_smem) + tid * 16;
+  auto piece = [&](int stage, int i) { return ring + (stage * (2 + NT) + i) * kDownThreads * 16; };
+  if (r0 < live) {
+    auto fetch = [&](int s, int stage) {
+      const int k = s * 32;
+      const bool in = k + c * 8 < a.K;
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int k = (s + u * stride) * 32;
-        const bool in = k + c * 8 < a.K;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          xv[u][i] = in && xr[i] ? __ldg(reinterpret_cast<const uint4*>(xr[i] + k)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          av[u][n] = in && n < nt_live && r0 + n * 8 + g < a.R ? __ldg(reinterpret_cast<const uint4*>(ar + (int64_t)n * 8 * a.K + k)) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const uint4 p = xv[u][0], q = xv[u][1];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma_16816(acc[n], p.x, q.x, p.y, q.y, av[u][n].x, av[u][n].y);
-          mma_16816(acc[n], p.z, q.z, p.w, q.w, av[u][n].z, av[u][n].w);
+      for (int i = 0; i < 2; ++i)
+        if (i == 0 || t.count > 8) {
+          const bool have = in && xr[i];
+          cp_async16(piece(stage, i), have ? xr[i] + k : a.x, have ? 16 : 0);
         }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const bool have = in && r0 + n * 8 + g < live;
+        cp_async16(piece(stage, 2 + n), have ? ar + (int64_t)n * 8 * a.K + k : a.a, have ? 16 : 0);
       }
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+      if (s0 + i * stride < steps) fetch(s0 + i * stride, i);
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    int stage = 0;
+    for (int s = s0; s < steps; s += stride) {
+      const int ahead = s + (S - 1) * stride;
+      if (ahead < steps) fetch(ahead, stage == 0 ? S - 1 : stage - 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+      const uint4 p = ld_shared_v4(piece(stage, 0)), q = t.count > 8 ? ld_shared_v4(piece(stage, 1)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 w = ld_shared_v4(piece(stage, 2 + n));
+        mma_16816(acc[n], p.x, q.x, p.y, q.y, w.x, w.y);
+        mma_16816(acc[n], p.z, q.z, p.w, q.w, w.z, w.w);
+      }
+      stage = stage == S - 1 ? 0 : stage + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the ring's place is the parts' now
   }
   float* part = reinterpret_cast<float*>(down_smem) + warp * 16 * N;
 #pragma unroll
@@ -159,17 +218,18 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_few_kernel(const
 // Many tokens: a CTA takes 32 tokens by NT x 8 rows of A, both through shared memory by cp.async, 64 of K a stage and
 // kStages - 1 stages ahead; rows of 128 bytes, their 16-byte pieces exchanged by row (piece ^ row mod 8), so that
 // ldmatrix finds eight rows in eight different banks.  Warps: two by rows, four by the stage's k's.
-constexpr int kManyRows = 32, kStages = 8;
+constexpr int kManyRows = 32;
+constexpr int many_stages(int NT) { return NT == 8 ? 5 : 8; }
 
 template <int NT>
 constexpr int down_many_smem() {
-  const int stages = kStages * (kManyRows + NT * 8) * 128, parts = 4 * kManyRows * NT * 8 * 4;
+  const int stages = many_stages(NT) * (kManyRows + NT * 8) * 128, parts = 4 * kManyRows * NT * 8 * 4;
   return stages > parts ? stages : parts;
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kDownThreads, 2) adapter_down_many_kernel(const AdapterArgs a) {
-  constexpr int N = NT * 8, kStageBytes = (kManyRows + N) * 128;
+__global__ void __launch_bounds__(kDownThreads, 3) adapter_down_many_kernel(const AdapterArgs a) {
+  constexpr int N = NT * 8, kStages = many_stages(NT), kStageBytes = (kManyRows + N) * 128;
   extern __shared__ __align__(128) unsigned char down_smem[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!plan_fits(a)) {
@@ -179,7 +239,6 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_many_kernel(cons
   const int tile = blockIdx.x / a.cluster, share = blockIdx.x - tile * a.cluster;
   if (tile >= a.plan->tiles[a.down_kind]) return;  // (all CTAs of the cluster)
   const AdapterTile t = a.down_tiles[tile];
-  if (t.adapter >= a.n) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int r0 = blockIdx.y * N, live = live_rank(a, t.adapter);
   const uint32_t base = smem_u32(down_smem);
@@ -246,54 +305,70 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_many_kernel(cons
   join_down<4, kManyRows, N, kDownThreads>(a, t, reinterpret_cast<float*>(down_smem), share, r0, live);
 }
 
-// ---------------------------------------------------------------- h as fp16
-// h 2^e = hi + lo with 2^e of the token's own (its largest h 2^e in [2^14, 2^15)): 22 bits, of h down to 2^-39 of the
-// token's largest; fp32 sums of hi B and lo B, then 2^-e.
+// ---------------------------------------------------------------- tokens without an adapter
+// out = y for them, where out is not y: all threads of a launch, kCopy pieces of 16 bytes each in flight (one after
+// another they would take a memory's latency each).
+constexpr int kCopy = 4;
 
-// 2^e and 2^-e for a token whose largest |h| is top; 0 and what is not finite stay as they are
-TB_DEVI float up_scale(float top, float& back) {
-  int e = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
-  if (!(top > 0.f) || !(top < INFINITY)) e = 0;
-  e = max(-126, min(126, e));
-  back = __uint_as_float((uint32_t)(127 - e) << 23);
-  return __uint_as_float((uint32_t)(127 + e) << 23);
-}
-
-TB_DEVI void two_terms(float4 v, float up, uint2& hi, uint2& lo) {
-  const float f[4] = {v.x * up, v.y * up, v.z * up, v.w * up};
-  __half h[4], l[4];
+TB_DEVI void copy_bare(const AdapterArgs& a) {
+  if (a.out == a.y) return;
+  const int width = a.N / 8, bare = a.plan->bare;
+  const int64_t pieces = (int64_t)(a.plan->rows - bare) * width, threads = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t e0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e0 < pieces; e0 += threads * kCopy) {
+    uint4 v[kCopy];
+    uint4* to[kCopy];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    h[j] = __float2half_rn(f[j]);
-    const float b = __half2float(h[j]);
-    l[j] = fabsf(b) < INFINITY ? __float2half_rn(f[j] - b) : __half();
+    for (int i = 0; i < kCopy; ++i) {
+      const int64_t e = e0 + i * threads, p = e / width;
+      if (e < pieces) {
+        const int64_t tok = a.order[bare + p];
+        v[i] = __ldcs(reinterpret_cast<const uint4*>(a.y + tok * a.ldy) + (e - p * width));
+        to[i] = reinterpret_cast<uint4*>(a.out + tok * a.ldo) + (e - p * width);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kCopy; ++i)
+      if (e0 + i * threads < pieces) __stcs(to[i], v[i]);
   }
-  hi = *reinterpret_cast<const uint2*>(h);
-  lo = *reinterpret_cast<const uint2*>(l);
 }
 
 // ---------------------------------------------------------------- up, few tokens
 // The columns of out (rows of B) are the mma's 16 rows and the tokens its 8 columns, so that a weight is read once
 // for a tile of 16 tokens and an idle token costs nothing but its place.  A warp takes 32 columns at a time, and
-// every CTA an equal run of all tiles' columns.  Thread (g, c) holds columns n0 + 4 g .. + 3: 8 bytes of y and out a
-// token, and 8 neighbouring elements of each of their rows of B, as in `down`.  The next columns' rows of B are
-// loaded before the present ones are used.
+// every warp an equal run of all tiles' columns.  Thread (g, c) holds columns n0 + 4 g .. + 3: 8 bytes of y and out a
+// token, and 8 neighbouring elements of each of their rows of B, as in `down`.  The next columns' rows of B and
+// elements of y are on their way while the present ones are used.
 constexpr int kUpFewThreads = 256, kUpFewWarps = kUpFewThreads / 32;
 
-// W: elements of a row of B a thread loads at a time, by 4 threads: 16, 32 or 64 ranks a pass
+// They come by cp.async into a ring of the thread's own.
+constexpr int up_few_stages(int W) { return W == 4 ? 6 : W == 8 ? 4 : 2; }
 template <int W>
+constexpr int up_few_smem() {
+  return up_few_stages(W) * kUpFewThreads * (4 * W * 2 + 4 * 8);
+}
+TB_DEVI void cp_async8(uint32_t dst, const void* src, int bytes) {  // the rest of the 8 bytes is zeroed
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// W: elements of a row of B a thread loads at a time, by 4 threads, of blocks of 16, 32 or 64 ranks; MULTI: several
+// blocks.  An item of the ring is a block of a unit, with the unit's y at its first block.
+template <int W, bool MULTI>
 __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const AdapterArgs a) {
-  constexpr int kPass = W * 4, kMma = W / 4;  // ranks of a pass, its MMAs of 16
-  extern __shared__ __align__(16) unsigned char up_few_smem[];  // hi, lo of [16][pitch] ranks
-  __shared__ int tok[16];
-  __shared__ float back[16];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  constexpr int kBlock = W * 4, kMma = W / 4, S = up_few_stages(W);  // ranks of a block, its MMAs of 16
+  constexpr int kPieces = W == 16 ? 2 : 1, kBytes = W * 2 / kPieces;  // of a thread's elements of a row
+  constexpr int kItem = kUpFewThreads * (4 * W * 2 + 4 * 8);
+  extern __shared__ __align__(16) unsigned char up_few_smem_[];
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   if (!plan_fits(a)) return;
-  const int tiles = a.plan->tiles[a.up_kind], units = (a.N + 31) / 32, passes = (a.R + kPass - 1) / kPass;
-  const int pitch = passes * kPass * 2 + 16;  // bytes of a token's hi or lo
-  const int64_t all = (int64_t)tiles * units;
-  int64_t at = all * blockIdx.x / gridDim.x;
-  const int64_t stop = all * (blockIdx.x + 1) / gridDim.x;
+  copy_bare(a);
+  const int units = (a.N + 31) / 32;
+  const int64_t all = (int64_t)a.plan->tiles[a.up_kind] * units;
+  const int64_t warps = (int64_t)gridDim.x * kUpFewWarps, warp = (int64_t)blockIdx.x * kUpFewWarps + (threadIdx.x >> 5);
+  int64_t at = all * warp / warps;
+  const int64_t stop = all * (warp + 1) / warps;
+  const uint32_t ring = smem_u32(up_few_smem_);
+  auto row_at = [&](int stage, int j, int i) { return ring + stage * kItem + (j * kPieces + i) * kUpFewThreads * kBytes + threadIdx.x * kBytes; };
+  auto y_at = [&](int stage, int i) { return ring + stage * kItem + 4 * W * 2 * kUpFewThreads + (i * kUpFewThreads + threadIdx.x) * 8; };
   bool waited = false;
   while (at < stop) {
     const int tile = (int)(at / units), begin = (int)(at - (int64_t)tile * units);
@@ -301,303 +376,297 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
     at += end - begin;
     const AdapterTile t = a.up_tiles[tile];
     const int live = live_rank(a, t.adapter);
-    if (live == 0 && a.out == a.y) continue;
-    const __half* b = a.b + (int64_t)min(t.adapter, a.n - 1) * a.N * a.R + c * W;
-    uint32_t w[4][W / 2], next[4][W / 2];
-    auto load = [&](uint32_t (&v)[4][W / 2], int u, int pass) {  // rows 4 g .. + 3 of unit u
-      const int r = pass * kPass;
+    const int half = t.count > 8 ? 4 : 2;  // tokens a thread has: 2 c, 2 c + 1 of each eight
+    int64_t yo[4], oo[4];  // where they begin in y and out, -1: no token
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = u * 32 + 4 * g + j;
+    for (int i = 0; i < 4; ++i) {
+      const int p = (i >> 1) * 8 + 2 * c + (i & 1);
+      yo[i] = oo[i] = -1;
+      if (p < t.count) {
+        const int64_t k = a.order[t.first + p];
+        yo[i] = k * a.ldy + 4 * g, oo[i] = k * a.ldo + 4 * g;
+      }
+    }
+    const __half* b = a.b + (int64_t)t.adapter * a.N * a.R + (int64_t)(4 * g) * a.R + c * W;
+    const int blocks = MULTI ? max(1, (live + kBlock - 1) / kBlock) : 1;
+    auto fetch = [&](int u, int blk, int stage) {  // rows 4 g .. + 3 of unit u; zeros behind the rank and the last row
+      const bool in = u * 32 + 4 * g < a.N;  // (N is a multiple of 8)
+      const int left = (live - blk * kBlock - c * W) * 2;
+      const __half* p = b + (int64_t)u * 32 * a.R + blk * kBlock;
 #pragma unroll
-        for (int i = 0; i < W; i += 8) {
-          const int left = row < a.N ? live - r - c * W - i : 0;
-          const __half* p = b + (int64_t)row * a.R + r + i;
-          if constexpr (W == 4) {
-            const uint2 q = left > 0 ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
-            v[j][0] = q.x, v[j][1] = q.y;
-          } else {
-            const uint4 q = left > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-            v[j][i / 2] = q.x, v[j][i / 2 + 1] = q.y, v[j][i / 2 + 2] = q.z, v[j][i / 2 + 3] = q.w;
-          }
+      for (int j = 0; j < 4; ++j, p += a.R)
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int bytes = in ? min(kBytes, max(0, left - i * kBytes)) : 0;
+          if constexpr (W == 4) cp_async8(row_at(stage, j, i), bytes ? p : a.b, bytes);
+          else cp_async16(row_at(stage, j, i), bytes ? p + i * 8 : a.b, bytes);
+        }
+      if (!MULTI || blk == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < half && yo[i] >= 0 && in) cp_async8(y_at(stage, i), a.y + yo[i] + u * 32, 8);
+      }
+    };
+    int fu = begin, fb = 0;  // the next item to fetch
+    auto next = [&](int stage) {
+      if (fu < end) {
+        fetch(fu, fb, stage);
+        if (!MULTI || ++fb == blocks) fb = 0, ++fu;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) next(i);
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // h is written
+    waited = true;
+    // the terms of token g of each eight, as the mma's right operand
+    auto term = [&](uint32_t (&h)[W / 2], int n, int lo, int blk) {
+      const int p = n * 8 + g;
+      const __half* q = a.terms + (((int64_t)(t.first + p) * a.blocks + blk) * 2 + lo) * kBlock + c * W;
+      if constexpr (W == 4) {
+        const uint2 v = p < t.count ? *reinterpret_cast<const uint2*>(q) : make_uint2(0, 0);
+        h[0] = v.x, h[1] = v.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < W / 2; i += 4) {
+          const uint4 v = p < t.count ? *reinterpret_cast<const uint4*>(q + i * 2) : make_uint4(0, 0, 0, 0);
+          h[i] = v.x, h[i + 1] = v.y, h[i + 2] = v.z, h[i + 3] = v.w;
         }
       }
     };
-    auto cut = [&](uint32_t (&v)[4][W / 2], int pass) {  // what the rank ends inside a thread's elements
-      const int left = live - pass * kPass - c * W;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) v[j][i] = left <= 2 * i ? 0u : left == 2 * i + 1 ? v[j][i] & 0xffffu : v[j][i];
-    };
-    int u = begin + warp;
-    if (live && u < end) load(w, u, 0);
-    __syncthreads();  // the tile before is done
-    if (tid < 16) tok[tid] = tid < t.count ? a.order[t.first + tid] : -1;
-    if (live) {
-      if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // h is written
-      waited = true;
-      const int p = tid >> 4, q = tid & 15;  // 16 threads a token
-      const float* h = a.h + (int64_t)(t.first + min(p, t.count - 1)) * a.R;
-      float top = 0.f;
-      for (int r = q * 4; r < live; r += 64) {
-        const float4 v = *reinterpret_cast<const float4*>(h + r);
-        top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
-      }
-#pragma unroll
-      for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      float bk;
-      const float up = up_scale(top, bk);
-      if (q == 0) back[p] = bk;
-      for (int r = q * 4; r < passes * kPass; r += 64) {
-        const float4 v = p < t.count && r < a.R ? *reinterpret_cast<const float4*>(h + r) : make_float4(0, 0, 0, 0);
-        uint2 hi, lo;
-        two_terms(v, up, hi, lo);
-        *reinterpret_cast<uint2*>(up_few_smem + p * pitch + r * 2) = hi;
-        *reinterpret_cast<uint2*>(up_few_smem + (16 + p) * pitch + r * 2) = lo;
-      }
-    }
-    __syncthreads();
-    const int nt = t.count > 8 ? 2 : 1;
-    int my_tok[4];
-    float my_back[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // tokens 2 c, 2 c + 1 of each eight
+    auto back = [&](int i, int blk) {
       const int p = (i >> 1) * 8 + 2 * c + (i & 1);
-      my_tok[i] = tok[p];
-      my_back[i] = live ? back[p] : 0.f;
-    }
-    const uint32_t terms = smem_u32(up_few_smem) + g * pitch + c * W * 2;
-    for (; u < end; u += kUpFewWarps) {
-      const int col = u * 32 + 4 * g;
+      return p < t.count ? a.back[(int64_t)(t.first + p) * a.blocks + blk] : 0.f;
+    };
+    uint32_t hi[2][W / 2], lo[2][W / 2];
+    float bk[4];
+    auto terms = [&](int blk) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+        if (2 * n < half) {
+          term(hi[n], n, 0, blk);
+          term(lo[n], n, 1, blk);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bk[i] = back(i, blk);
+    };
+    if (!MULTI) terms(0);
+    int stage = 0;
+    for (int u = begin; u < end; ++u) {
+      float sum[4][4];  // [token][column]
       uint2 y[4];
+      for (int blk = 0; blk < blocks; ++blk) {
+        next(stage == 0 ? S - 1 : stage - 1);
+        if (MULTI) terms(blk);
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        uint32_t w[4][W / 2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (my_tok[i] >= 0 && col < a.N) y[i] = *reinterpret_cast<const uint2*>(a.y + my_tok[i] * a.ldy + col);
-      float acc[2][2][4];  // [rows 4 g, 4 g + 1 or 4 g + 2, 4 g + 3][eight tokens]
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (W == 4) {
+            const uint2 v = ld_shared_v2(row_at(stage, j, 0));
+            w[j][0] = v.x, w[j][1] = v.y;
+          } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) (&acc[0][0][0])[i] = 0.f;
-      for (int pass = 0; pass * kPass < live; ++pass) {
-        if ((pass + 1) * kPass < live) load(next, u, pass + 1);
-        else if (u + kUpFewWarps < end) load(next, u + kUpFewWarps, 0);
-        if (live & 7) cut(w, pass);
+            for (int i = 0; i < kPieces; ++i) {
+              const uint4 v = ld_shared_v4(row_at(stage, j, i));
+              w[j][4 * i] = v.x, w[j][4 * i + 1] = v.y, w[j][4 * i + 2] = v.z, w[j][4 * i + 3] = v.w;
+            }
+          }
+        }
+        if (!MULTI || blk == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < half) y[i] = ld_shared_v2(y_at(stage, i));
+        }
+        stage = stage == S - 1 ? 0 : stage + 1;
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          if (n >= nt) break;
+          if (2 * n >= half) break;
+          float acc[2][4];  // [rows 4 g, 4 g + 1 or 4 g + 2, 4 g + 3]
 #pragma unroll
-          for (int term = 1; term >= 0; --term) {
-            uint32_t h[W / 2];
-            const uint32_t p = terms + (n * 8 + term * 16) * pitch + pass * kPass * 2;
-            if constexpr (W == 4) {
-              const uint2 v = ld_shared_v2(p);
-              h[0] = v.x, h[1] = v.y;
-            } else {
+          for (int i = 0; i < 8; ++i) (&acc[0][0])[i] = 0.f;
 #pragma unroll
-              for (int i = 0; i < W / 8; ++i) {
-                const uint4 v = ld_shared_v4(p + i * 16);
-                h[4 * i] = v.x, h[4 * i + 1] = v.y, h[4 * i + 2] = v.z, h[4 * i + 3] = v.w;
-              }
+          for (int m = 0; m < kMma; ++m)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              mma_16816(acc[q], w[2 * q][2 * m], w[2 * q + 1][2 * m], w[2 * q][2 * m + 1], w[2 * q + 1][2 * m + 1], lo[n][2 * m], lo[n][2 * m + 1]);
+              mma_16816(acc[q], w[2 * q][2 * m], w[2 * q + 1][2 * m], w[2 * q][2 * m + 1], w[2 * q + 1][2 * m + 1], hi[n][2 * m], hi[n][2 * m + 1]);
             }
 #pragma unroll
-            for (int m = 0; m < kMma; ++m)
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int q = 0; q < 2; ++q)
-                mma_16816(acc[q][n], w[2 * q][2 * m], w[2 * q + 1][2 * m], w[2 * q][2 * m + 1], w[2 * q + 1][2 * m + 1], h[2 * m], h[2 * m + 1]);
-          }
+            for (int e = 0; e < 4; ++e) {
+              const float v = acc[e >> 1][(e & 1) * 2 + k], f = bk[2 * n + k];
+              float& s = sum[2 * n + k][e];
+              s = MULTI && blk ? fmaf(v, f, s) : v * f;
+            }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < W / 2; ++i) w[j][i] = next[j][i];
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (my_tok[i] < 0 || col >= a.N) continue;
-        uint2 o = y[i];
-        if (live) {
-          const int n = i >> 1, k = i & 1;
-          const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&y[i].x)), hi = __half22float2(*reinterpret_cast<const __half2*>(&y[i].y));
-          const float f = my_back[i];
-          o.x = pack_half2(fmaf(acc[0][n][k], f, lo.x), fmaf(acc[0][n][2 + k], f, lo.y));
-          o.y = pack_half2(fmaf(acc[1][n][k], f, hi.x), fmaf(acc[1][n][2 + k], f, hi.y));
+      for (int i = 0; i < 4; ++i)
+        if (i < half && yo[i] >= 0 && u * 32 + 4 * g < a.N) {
+          const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&y[i].x)), q = __half22float2(*reinterpret_cast<const __half2*>(&y[i].y));
+          *reinterpret_cast<uint2*>(a.out + oo[i] + u * 32) = make_uint2(pack_half2(p.x + sum[i][0], p.y + sum[i][1]), pack_half2(q.x + sum[i][2], q.y + sum[i][3]));
         }
-        *reinterpret_cast<uint2*>(a.out + my_tok[i] * a.ldo + col) = o;
-      }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 }
 
 // ---------------------------------------------------------------- up, many tokens
-// A CTA takes a tile of at most 128 tokens and a run of column tiles of 64, a warp 16 of the tokens.  A thread keeps its
-// tokens' terms as the mma's left operand (up to 64 ranks; above, they are read from shared memory), and B's rows
-// come by cp.async two column tiles ahead.  Which column of out is which of the MMAs' columns is free: thread (g, c)
-// has 16 neighbouring ones of tokens g and g + 8, so that y and out go between global memory and registers in whole
-// sectors, y one column tile ahead.
+// Every CTA takes an equal run of all row tiles' (at most 128 tokens) column tiles of 64, a warp 16 of the tokens.  A
+// thread keeps its tokens' terms as the mma's left operand (of up to 64 ranks; above, they are read again), and B's
+// rows come by cp.async two column tiles ahead.  Which column of out is which of the MMAs' columns is free: thread
+// (g, c) has 16 neighbouring ones of tokens g and g + 8, so that y and out go between global memory and registers in
+// whole sectors, y one column tile ahead.
 constexpr int kUpThreads = 256, kUpCols = 64, kUpStages = 3;
 
 // bytes of a row of B in shared memory: an odd number of 32, so that four rows' 32 bytes lie in different banks
 __host__ __device__ __forceinline__ int up_pitch(int R) { return ((R + 15) / 16 | 1) * 32; }
 
-// KS: steps of 16 ranks; kept in registers up to 4
-template <int KS>
-__global__ void __launch_bounds__(kUpThreads, KS <= 8 ? 2 : 1) adapter_up_many_kernel(const AdapterArgs a) {
-  constexpr bool kKeep = KS <= 4;
+// KS: steps of 16 ranks of a block; MULTI: several blocks
+template <int KS, bool MULTI>
+__global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const AdapterArgs a) {
   extern __shared__ __align__(128) unsigned char up_smem[];
   if (!plan_fits(a)) return;
-  const int tile = blockIdx.x, group = blockIdx.y;  // tiles first: those of one adapter read the same rows of B
-  if (tile >= a.plan->tiles[a.up_kind]) return;
-  const AdapterTile t = a.up_tiles[tile];
-  const int live = live_rank(a, t.adapter);
-  if (live == 0 && a.out == a.y) return;
+  copy_bare(a);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  const int pitch = up_pitch(a.R), ks = (live + 15) >> 4, pieces = a.R >> 3;
-  const uint32_t base = smem_u32(up_smem), stage_bytes = kUpCols * pitch, terms_at = base + kUpStages * stage_bytes;
-  const int tiles = (a.N + kUpCols - 1) / kUpCols;
-  const int begin = (int)((int64_t)tiles * group / a.groups), end = (int)((int64_t)tiles * (group + 1) / a.groups);
-
-  // column 16 c + 2 j + i of a tile is column 2 c + i of MMA j: its row of B lies at 8 j + 2 c + i
-  const __half* bg = a.b + (int64_t)min(t.adapter, a.n - 1) * a.N * a.R;
-  auto fetch = [&](int nt) {
-    const uint32_t st = base + (nt - begin) % kUpStages * stage_bytes;
-    const int rows = min(kUpCols, a.N - nt * kUpCols);
-    const __half* src = bg + (int64_t)nt * kUpCols * a.R;
-    for (int i = tid; i < rows * pieces; i += kUpThreads) {  // (a tile's rows of B are one run of memory)
-      const int col = i / pieces, p = i - col * pieces;
-      const int at = (col >> 1 & 7) * 8 + (col >> 4) * 2 + (col & 1);
-      if (p * 8 < live) cp_async16(st + at * pitch + p * 16, src + i * 8, 16);
-    }
-  };
-  const int p0 = warp * 16 + g;  // the thread's tokens: p0 and p0 + 8 of the tile
-  int tok[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) tok[i] = p0 + 8 * i < t.count ? a.order[t.first + p0 + 8 * i] : -1;
-  uint4 y[2][2];
-  auto load_y = [&](uint4 (&v)[2][2], int nt) {
-    const int col = nt * kUpCols + 16 * c;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        if (tok[i] >= 0 && col + 8 * q < a.N) v[i][q] = __ldcs(reinterpret_cast<const uint4*>(a.y + tok[i] * a.ldy + col) + q);
-  };
-  if (live) {
+  const int pitch = up_pitch(a.R);
+  const uint32_t base = smem_u32(up_smem), stage_bytes = kUpCols * pitch;
+  const int cols = (a.N + kUpCols - 1) / kUpCols;
+  const int64_t all = (int64_t)a.plan->tiles[a.up_kind] * cols;
+  int64_t at = all * blockIdx.x / gridDim.x;
+  const int64_t stop = all * (blockIdx.x + 1) / gridDim.x;
+  bool waited = false;
+  while (at < stop) {
+    const int tile = (int)(at / cols), begin = (int)(at - (int64_t)tile * cols);
+    const int end = (int)(stop - at < cols - begin ? begin + (stop - at) : cols);
+    at += end - begin;
+    const AdapterTile t = a.up_tiles[tile];
+    const int live = live_rank(a, t.adapter), steps = max(1, (live + 15) >> 4);
+    // column 16 c + 2 j + i of a tile is column 2 c + i of MMA j: its row of B lies at 8 j + 2 c + i.  Zeros behind the
+    // rank up to whole steps
+    const __half* bg = a.b + (int64_t)t.adapter * a.N * a.R;
+    const int pieces = 2 * steps, more = kUpThreads / pieces, rest = kUpThreads - more * pieces;
+    const int col0 = tid / pieces, piece0 = tid - col0 * pieces;
+    auto fetch = [&](int nt) {
+      const uint32_t st = base + (nt - begin) % kUpStages * stage_bytes;
+      const __half* src = bg + (int64_t)nt * kUpCols * a.R;
+      const int have = min(kUpCols, a.N - nt * kUpCols);
+      for (int col = col0, p = piece0; col < kUpCols;) {
+        const int bytes = col < have ? min(16, max(0, (live - p * 8) * 2)) : 0;
+        cp_async16(st + ((col >> 1 & 7) * 8 + (col >> 4) * 2 + (col & 1)) * pitch + p * 16, bytes ? src + col * a.R + p * 8 : a.b, bytes);
+        col += more, p += rest;
+        if (p >= pieces) p -= pieces, ++col;
+      }
+    };
+    __syncthreads();  // the stages of the run before have been used
 #pragma unroll
     for (int i = 0; i < kUpStages - 1; ++i) {
       if (begin + i < end) fetch(begin + i);
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
-  }
-  load_y(y, begin);
-  uint32_t hi[kKeep ? KS : 1][4], lo[kKeep ? KS : 1][4];
-  float back[2];
-  if (live) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // h is written
+    const int p0 = warp * 16 + g;  // the thread's tokens: p0 and p0 + 8 of the tile
+    const __half* yp[2];
+    __half* op[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float* h = a.h + (int64_t)(t.first + min(p0 + 8 * i, t.count - 1)) * a.R;
-      float top = 0.f;
-      for (int r = 4 * c; r < live; r += 16) {
-        const float4 v = *reinterpret_cast<const float4*>(h + r);
-        top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
-      }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float up = up_scale(top, back[i]);
-      // ranks 16 k + 4 c .. + 3 serve as the k's 2 c, 2 c + 1, 2 c + 8, 2 c + 9; B's are permuted below alike
-      auto at_step = [&](int k, uint2& h2, uint2& l2) {
-        const int r = 16 * k + 4 * c;
-        two_terms(r < a.R ? *reinterpret_cast<const float4*>(h + r) : make_float4(0, 0, 0, 0), up, h2, l2);
-      };
-      if constexpr (kKeep) {
+      const int k = p0 + 8 * i < t.count ? a.order[t.first + p0 + 8 * i] : -1;
+      yp[i] = k >= 0 ? a.y + k * a.ldy + 16 * c : nullptr;
+      op[i] = a.out + (k >= 0 ? k : 0) * a.ldo + 16 * c;
+    }
+    struct Y {
+      uint4 v[2][2];
+    };
+    auto load_y = [&](Y& y, int nt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (yp[i] && nt * kUpCols + 16 * c + 8 * q < a.N) y.v[i][q] = __ldcs(reinterpret_cast<const uint4*>(yp[i] + nt * kUpCols) + q);
+    };
+    Y ya, yb;
+    load_y(ya, begin);
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // h is written
+    waited = true;
+    // ranks 16 k + 4 c .. + 3 of a block serve as the k's 2 c, 2 c + 1, 2 c + 8, 2 c + 9; B's are read below alike
+    uint32_t hi[KS][4], lo[KS][4];
+    float back[2];
+    auto terms = [&](int blk) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int p = p0 + 8 * i;
+        const int64_t q = ((int64_t)(t.first + p) * a.blocks + blk);
+        back[i] = p < t.count ? a.back[q] : 0.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          uint2 h2, l2;
-          at_step(k, h2, l2);
+          const __half* h = a.terms + q * 2 * (KS * 16) + 16 * k + 4 * c;
+          const uint2 h2 = p < t.count ? *reinterpret_cast<const uint2*>(h) : make_uint2(0, 0);
+          const uint2 l2 = p < t.count ? *reinterpret_cast<const uint2*>(h + KS * 16) : make_uint2(0, 0);
           hi[k][i] = h2.x, hi[k][i + 2] = h2.y;
           lo[k][i] = l2.x, lo[k][i + 2] = l2.y;
         }
-      } else {
-        for (int k = 0; k < ks; ++k) {  // a lane's own 16 bytes of each term a step
-          uint2 h2, l2;
-          at_step(k, h2, l2);
-          uint32_t* p = reinterpret_cast<uint32_t*>(up_smem + kUpStages * stage_bytes + (((warp * KS + k) * 2) * 32 + lane) * 16);
-          p[i] = h2.x, p[i + 2] = h2.y;
-          p[i + 128] = l2.x, p[i + 130] = l2.y;
-        }
       }
-    }
-  }
-  // the rank's end inside a step: what B holds behind it
-  const int left = live - (ks - 1) * 16 - 4 * c;
-  const uint32_t m0 = left <= 0 ? 0u : left == 1 ? 0xffffu : ~0u, m1 = left <= 2 ? 0u : left == 3 ? 0xffffu : ~0u;
-  for (int nt = begin; nt < end; ++nt) {
-    uint4 next[2][2];
-    float acc[8][4];
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    if (nt + 1 < end) load_y(next, nt + 1);
-    if (live) {
+    };
+    if (!MULTI) terms(0);
+    int nt = begin;
+    auto one = [&](Y& y, Y& next) {
+      if (nt + 1 < end) load_y(next, nt + 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kUpStages - 2) : "memory");
       __syncthreads();  // tile nt is there, and tile nt - 1 has been used
       if (nt + kUpStages - 1 < end) fetch(nt + kUpStages - 1);
       asm volatile("cp.async.commit_group;" ::: "memory");
       const uint32_t st = base + (nt - begin) % kUpStages * stage_bytes + g * pitch + c * 8;
-      auto step = [&](int k, const uint32_t (&h)[4], const uint32_t (&l)[4], bool last) {
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          uint2 b = ld_shared_v2(st + n * 8 * pitch + k * 32);
-          if (last) b.x &= m0, b.y &= m1;
-          mma_16816(acc[n], l[0], l[1], l[2], l[3], b.x, b.y);
-          mma_16816(acc[n], h[0], h[1], h[2], h[3], b.x, b.y);
-        }
-      };
       if (warp * 16 < t.count) {
-        if constexpr (kKeep) {
 #pragma unroll
-          for (int k = 0; k < KS; ++k)
-            if (k < ks) step(k, hi[k], lo[k], k == ks - 1);
-        } else {
-          for (int k = 0; k < ks; ++k) {
-            uint32_t h[4], l[4];
-            const uint32_t p = terms_at + (((warp * KS + k) * 2) * 32 + lane) * 16;
-            const uint4 u = ld_shared_v4(p), v = ld_shared_v4(p + 512);
-            h[0] = u.x, h[1] = u.y, h[2] = u.z, h[3] = u.w;
-            l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
-            step(k, h, l, k == ks - 1);
+        for (int q = 0; q < 2; ++q) {  // MMAs 4 q .. + 3: columns 16 c + 8 q .. + 7
+          float sum[4][4];
+          for (int blk = 0; blk < (MULTI ? (steps + KS - 1) / KS : 1); ++blk) {
+            if (MULTI) terms(blk);
+            float acc[4][4];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) (&acc[0][0])[j] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              if (blk * KS + k >= steps) break;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint2 b = ld_shared_v2(st + (4 * q + j) * 8 * pitch + (blk * KS + k) * 32);
+                mma_16816(acc[j], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b.x, b.y);
+                mma_16816(acc[j], hi[k][0], hi[k][1], hi[k][2], hi[k][3], b.x, b.y);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float f = back[j >> 1 & 1];
+              if (!MULTI || blk == 0) (&sum[0][0])[j] = (&acc[0][0])[j] * f;
+              else (&sum[0][0])[j] = fmaf((&acc[0][0])[j], f, (&sum[0][0])[j]);
+            }
+          }
+          if (nt * kUpCols + 16 * c + 8 * q < a.N) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!yp[i]) continue;
+              uint4 o = y.v[i][q];
+              uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+                w[j] = pack_half2(f.x + sum[j][2 * i], f.y + sum[j][2 * i + 1]);
+              }
+              __stcs(reinterpret_cast<uint4*>(op[i] + nt * kUpCols) + q, o);
+            }
           }
         }
       }
+      ++nt;
+    };
+    while (nt < end) {
+      one(ya, yb);
+      if (nt >= end) break;
+      one(yb, ya);
     }
-    const int col = nt * kUpCols + 16 * c;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (tok[i] < 0 || col + 8 * q >= a.N) continue;
-        uint4 o = y[i][q];
-        if (live) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(&o);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-            w[j] = pack_half2(fmaf(acc[4 * q + j][2 * i], back[i], f.x), fmaf(acc[4 * q + j][2 * i + 1], back[i], f.y));
-          }
-        }
-        __stcs(reinterpret_cast<uint4*>(a.out + tok[i] * a.ldo + col) + q, o);
-      }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) y[i][q] = next[i][q];
   }
-}
-
-static size_t up_many_smem(int R) {
-  const size_t pitch = up_pitch(R);
-  const int steps = R <= 64 ? 0 : R <= 128 ? 8 : 16;
-  return kUpStages * kUpCols * pitch + (size_t)steps * 8 * 2 * 512;
 }
 
 template <typename... Args>
@@ -625,6 +694,9 @@ static cudaError_t launch(void (*fn)(Args...), dim3 grid, int threads, size_t sm
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
+// ranks that share a power of two, and a launch of `down`'s part of A
+static int rank_block(int64_t R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
+
 // Up to this many tokens of a step the tiles are of 16.
 constexpr int kFewTokens = 256;
 
@@ -633,7 +705,8 @@ constexpr int kFewTokens = 256;
 extern "C" size_t tb_adapter_linear_workspace_size(int64_t T, int64_t n, int64_t K, int64_t N, int64_t R) {
   using namespace tb;
   if (T < 0 || T > INT_MAX / 2 || n < 1 || K < 8 || N < 8 || R < 8 || R > kAdapterMaxR) return 0;
-  return (size_t)T * R * 4;
+  const int64_t block = rank_block(R), blocks = (R + block - 1) / block;
+  return (size_t)T * blocks * (block * 4 + 4);
 }
 
 extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int64_t K, const uint16_t* a, const uint16_t* b, int64_t n,
@@ -672,7 +745,10 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   g.order = reinterpret_cast<const int32_t*>(base + adapter_order_at());
   g.down_tiles = reinterpret_cast<const AdapterTile*>(base + adapter_tiles_at(T, n, g.down_kind));
   g.up_tiles = reinterpret_cast<const AdapterTile*>(base + adapter_tiles_at(T, n, g.up_kind));
-  g.h = static_cast<float*>(workspace);
+  g.block = rank_block(R);
+  g.blocks = (int)((R + g.block - 1) / g.block);
+  g.terms = static_cast<__half*>(workspace);
+  g.back = reinterpret_cast<float*>(g.terms + (size_t)T * g.blocks * g.block * 2);
   g.status = dev_status;
   g.ldx = ldx;
   g.ldy = ldy;
@@ -684,17 +760,19 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   g.R = (int)R;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t down = adapter_max_tiles(T, n, g.down_kind), up = adapter_max_tiles(T, n, g.up_kind);
-  // few tokens: K is split over a cluster until there are two CTAs an SM, of at least four steps a warp; many: until
-  // every SM has one
+  // K is split over a cluster until there are two CTAs an SM, of at least four steps a warp (few) or 16 stages (many)
   g.cluster = 1;
   if (few)
     while (g.cluster < 8 && down * g.cluster < 2 * f.sms && K / 32 >= g.cluster * 2 * kDownWarps) g.cluster *= 2;
   else
-    while (g.cluster < 8 && down * g.cluster * 2 <= 2 * f.sms && K / 64 >= g.cluster * 2 * kStages) g.cluster *= 2;
-  const int nt = R <= 16 ? 2 : R <= 32 ? 4 : 8;
-  const dim3 grid((unsigned)(down * g.cluster), (unsigned)((R + nt * 8 - 1) / (nt * 8)));
+    while (g.cluster < 8 && down * g.cluster < 2 * f.sms && K / 64 >= g.cluster * 32) g.cluster *= 2;
+  const int nt = g.block / 8;
+  const dim3 grid((unsigned)(down * g.cluster), (unsigned)g.blocks);
   cudaError_t e;
-#define TB_DOWN_FEW(NT) launch(adapter_down_few_kernel<NT>, grid, kDownThreads, (size_t)kDownWarps * 16 * NT * 8 * 4, s, g.cluster, false, g)
+#define TB_DOWN_FEW(NT)                                                                                                         \
+  ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_down_few_kernel<NT>), f.device, down_few_smem<NT>())) != TB_OK \
+       ? cudaErrorUnknown                                                                                                       \
+       : launch(adapter_down_few_kernel<NT>, grid, kDownThreads, (size_t)down_few_smem<NT>(), s, g.cluster, false, g))
 #define TB_DOWN_MANY(NT)                                                                                                        \
   ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_down_many_kernel<NT>), f.device, down_many_smem<NT>())) != TB_OK \
        ? cudaErrorUnknown                                                                                                       \
@@ -708,27 +786,25 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   if (rc != TB_OK) return rc;
   if (e == cudaSuccess) {
     if (few) {
-      // two CTAs an SM share all tiles' columns; at least 128 columns each
-      const int W = R <= 16 ? 4 : R <= 32 ? 8 : 16;
-      const size_t smem = (size_t)32 * ((R + W * 4 - 1) / (W * 4) * W * 8 + 16);
-      int64_t ctas = up * ((N + 127) / 128);
-      if (ctas > 2 * f.sms) ctas = 2 * f.sms;
-      const dim3 some((unsigned)ctas);
-      e = W == 4   ? launch(adapter_up_few_kernel<4>, some, kUpFewThreads, smem, s, 1, true, g)
-          : W == 8 ? launch(adapter_up_few_kernel<8>, some, kUpFewThreads, smem, s, 1, true, g)
-                   : launch(adapter_up_few_kernel<16>, some, kUpFewThreads, smem, s, 1, true, g);
+      // two CTAs an SM share all tiles' columns; at least 32 columns a warp
+      int64_t ctas = (up * ((N + 31) / 32) + kUpFewWarps - 1) / kUpFewWarps;
+      const dim3 some((unsigned)(ctas < 2 * f.sms ? ctas : 2 * f.sms));
+#define TB_UP(W, MULTI)                                                                                                            \
+  ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_up_few_kernel<W, MULTI>), f.device, up_few_smem<W>())) != TB_OK \
+       ? cudaErrorUnknown                                                                                                          \
+       : launch(adapter_up_few_kernel<W, MULTI>, some, kUpFewThreads, (size_t)up_few_smem<W>(), s, 1, true, g))
+      e = R <= 16 ? TB_UP(4, false) : R <= 32 ? TB_UP(8, false) : R <= 64 ? TB_UP(16, false) : TB_UP(16, true);
+#undef TB_UP
+      if (rc != TB_OK) return rc;
     } else {
-      const size_t smem = up_many_smem((int)R);
-      // several CTAs a row tile, each with a run of column tiles
-      const int64_t col_tiles = (N + kUpCols - 1) / kUpCols;
-      int64_t groups = (6ll * f.sms + up - 1) / up;
-      g.groups = (int)(groups < 1 ? 1 : groups > col_tiles ? col_tiles : groups);
-      const dim3 some((unsigned)up, (unsigned)g.groups);
-#define TB_UP(KS)                                                                                                           \
-  ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_up_many_kernel<KS>), f.device, (int)smem)) != TB_OK \
-       ? cudaErrorUnknown                                                                                                   \
-       : launch(adapter_up_many_kernel<KS>, some, kUpThreads, smem, s, 1, true, g))
-      e = R <= 16 ? TB_UP(1) : R <= 32 ? TB_UP(2) : R <= 64 ? TB_UP(4) : R <= 128 ? TB_UP(8) : TB_UP(16);
+      const size_t smem = (size_t)kUpStages * kUpCols * up_pitch((int)R);
+      const int64_t ctas = up * ((N + kUpCols - 1) / kUpCols);
+      const dim3 some((unsigned)(ctas < 2 * f.sms ? ctas : 2 * f.sms));
+#define TB_UP(KS, MULTI)                                                                                                           \
+  ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_up_many_kernel<KS, MULTI>), f.device, (int)smem)) != TB_OK \
+       ? cudaErrorUnknown                                                                                                          \
+       : launch(adapter_up_many_kernel<KS, MULTI>, some, kUpThreads, smem, s, 1, true, g))
+      e = R <= 16 ? TB_UP(1, false) : R <= 32 ? TB_UP(2, false) : R <= 64 ? TB_UP(4, false) : TB_UP(4, true);
 #undef TB_UP
       if (rc != TB_OK) return rc;
     }

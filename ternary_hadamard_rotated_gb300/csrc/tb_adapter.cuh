@@ -11,26 +11,25 @@ constexpr int kAdapterMaxB = 16384, kAdapterMaxN = 16384;
 constexpr int kAdapterMaxR = 256;
 
 // Tokens are grouped by adapter (within one in the order they come in; behind the last adapter those without
-// one), and every group is cut into tiles of at most tile_rows(kind) tokens.
+// one), and every adapter's group is cut into tiles of at most tile_rows(kind) tokens.
 constexpr int kTileKinds = 3;
 constexpr int tile_rows(int kind) { return kind == 0 ? 16 : kind == 1 ? 32 : 128; }
 
 struct AdapterPlan {  // head of the plan; behind it order int32 [T], then the tiles of each kind
   int32_t magic, T, n;
-  int32_t tiles[kTileKinds];  // of the adapters' groups and of the bare tokens'
-  int32_t bare;               // where the tokens without an adapter begin
-  int32_t rows;               // tokens of all requests
+  int32_t tiles[kTileKinds];
+  int32_t bare;  // where the tokens without an adapter begin
+  int32_t rows;  // tokens of all requests
 };
 
 struct AdapterTile {
-  int32_t adapter;  // n: none
+  int32_t adapter;
   int32_t first, count;  // in `order`
   int32_t pad;
 };
 
 inline int64_t adapter_max_tiles(int64_t T, int64_t n, int kind) {
-  const int64_t whole = T / tile_rows(kind), groups = n + 1;  // a group's last tile may be a part of one
-  const int64_t m = whole + groups;
+  const int64_t m = T / tile_rows(kind) + n;  // a group's last tile may be a part of one
   return m < T ? m : T;
 }
 inline size_t adapter_order_at() { return sizeof(AdapterPlan); }

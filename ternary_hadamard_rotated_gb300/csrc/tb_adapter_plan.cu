@@ -73,7 +73,7 @@ TB_DEVI int block_max(int v, int* warps) {  // inclusive maximum, the same way
 __global__ void __launch_bounds__(kGroupThreads) adapter_plan_kernel(const GroupArgs a) {
   extern __shared__ int32_t group_smem[];
   int32_t* start = group_smem;              // [n + 2] tokens, then where a group begins in `order`
-  int32_t* tiles = group_smem + a.n + 2;    // [n + 2] where a group's tiles begin
+  int32_t* tiles = group_smem + a.n + 2;    // [n] where a group's tiles begin
   int32_t* at = group_smem + 2 * (a.n + 2); // [B] where a request's tokens begin in `order`, -1: none
   __shared__ int warps[32];
   __shared__ int highest;
@@ -119,15 +119,15 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_plan_kernel(const Group
   for (int kind = 0; kind < kTileKinds; ++kind) {
     const int rows = tile_rows(kind);
     int sums = 0;
-    for (int g0 = 0; g0 < groups; g0 += kGroupThreads) {
-      const int g = g0 + tid, c = g < groups ? (start[g + 1] - start[g] + rows - 1) / rows : 0;
+    for (int g0 = 0; g0 < a.n; g0 += kGroupThreads) {
+      const int g = g0 + tid, c = g < a.n ? (start[g + 1] - start[g] + rows - 1) / rows : 0;
       const int sum = block_sum(c, warps);
-      if (g < groups) tiles[g] = sums + sum - c;
+      if (g < a.n) tiles[g] = sums + sum - c;
       sums += warps[31];
       __syncthreads();
     }
     for (int i = blockIdx.x * kGroupThreads + tid; i < sums; i += gridDim.x * kGroupThreads) {
-      int lo = 0, hi = groups - 1;
+      int lo = 0, hi = a.n - 1;
       while (lo < hi) {  // the last group whose tiles begin at or before i
         const int mid = (lo + hi + 1) >> 1;
         if (tiles[mid] <= i) lo = mid;
