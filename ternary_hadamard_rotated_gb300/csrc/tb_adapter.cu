@@ -2,7 +2,7 @@
 // adapter of token t's request.
 //
 // Two launches, the second (programmatic) loading what the first does not write before it waits for it:
-//   down  h = scale A x, mma.sync on tiles of 16 or 32 tokens of one adapter, to the workspace in the plan's order
+//   down  h = scale A x, mma.sync on tiles of 16 or 64 tokens of one adapter, to the workspace in the plan's order
 //   up    out = y + B h, mma.sync; few tokens: tiles of 16, bound by the weights, which go from global memory straight
 //         to the registers; many: tiles of 128, bound by y and out
 //
@@ -54,6 +54,13 @@ TB_DEVI void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uin
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same with no sum before it
+TB_DEVI void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 TB_DEVI void cp_async16(uint32_t dst, const void* src, int bytes) {  // the rest of the 16 bytes is zeroed
@@ -215,11 +222,11 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_few_kernel(const
   join_down<kDownWarps, 16, N, kDownThreads>(a, t, reinterpret_cast<float*>(down_smem), share, r0, live);
 }
 
-// Many tokens: a CTA takes 32 tokens by NT x 8 rows of A, both through shared memory by cp.async, 64 of K a stage and
-// kStages - 1 stages ahead; rows of 128 bytes, their 16-byte pieces exchanged by row (piece ^ row mod 8), so that
-// ldmatrix finds eight rows in eight different banks.  Warps: two by rows, four by the stage's k's.
-constexpr int kManyRows = 32;
-constexpr int many_stages(int NT) { return NT == 8 ? 5 : 8; }
+// Many tokens: a CTA takes 64 tokens by NT x 8 rows of A, both through shared memory by cp.async, 64 of K a stage and
+// all stages but one ahead; rows of 128 bytes, their 16-byte pieces exchanged by row (piece ^ row mod 8), so that
+// ldmatrix finds eight rows in eight different banks.  Warps: two by 32 rows, four by the stage's k's.
+constexpr int kManyRows = 64;
+constexpr int many_stages(int NT) { return NT == 8 ? 5 : NT == 4 ? 6 : 7; }
 
 template <int NT>
 constexpr int down_many_smem() {
@@ -228,33 +235,35 @@ constexpr int down_many_smem() {
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kDownThreads, 3) adapter_down_many_kernel(const AdapterArgs a) {
-  constexpr int N = NT * 8, kStages = many_stages(NT), kStageBytes = (kManyRows + N) * 128;
+__global__ void __launch_bounds__(kDownThreads, NT == 8 ? 2 : 3) adapter_down_many_kernel(const AdapterArgs a) {
+  constexpr int N = NT * 8, S = many_stages(NT), kStageBytes = (kManyRows + N) * 128;
   extern __shared__ __align__(128) unsigned char down_smem[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tile = blockIdx.x / a.cluster, share = blockIdx.x - tile * a.cluster;
+  const AdapterTile t = a.down_tiles[tile];  // (inside the plan, of a tile or not)
   if (!plan_fits(a)) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(a.status, TB_DEV_BAD_PLAN);
     return;
   }
-  const int tile = blockIdx.x / a.cluster, share = blockIdx.x - tile * a.cluster;
   if (tile >= a.plan->tiles[a.down_kind]) return;  // (all CTAs of the cluster)
-  const AdapterTile t = a.down_tiles[tile];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int r0 = blockIdx.y * N, live = live_rank(a, t.adapter);
   const uint32_t base = smem_u32(down_smem);
   const int steps = (a.K + 63) >> 6, mine = (steps - share + a.cluster - 1) / a.cluster;
 
-  // a thread's pieces of a stage: one of x, NT / 4 of A
+  // a thread's pieces of a stage: two of x, NT / 4 of A
   const int row = tid >> 3, piece = tid & 7;
   const uint32_t at = row * 128 + ((piece ^ (row & 7)) << 4);
-  const bool has_x = row < t.count;
-  const __half* xp = a.x + (has_x ? a.order[t.first + row] * a.ldx : 0) + piece * 8;
+  const __half* xp[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) xp[i] = row + 32 * i < t.count ? a.x + a.order[t.first + row + 32 * i] * a.ldx + piece * 8 : nullptr;
   const __half* ap = a.a + ((int64_t)t.adapter * a.R + r0 + row) * a.K + piece * 8;
-  auto fetch = [&](int i) {
+  auto fetch = [&](int i, int stage) {
     const int k = (share + i * a.cluster) * 64;
-    const uint32_t dst = base + (i % kStages) * kStageBytes + at;
+    const uint32_t dst = base + stage * kStageBytes + at;
     const bool in = k + piece * 8 < a.K;
-    cp_async16(dst, has_x && in ? xp + k : a.x, has_x && in ? 16 : 0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) cp_async16(dst + j * 32 * 128, xp[j] && in ? xp[j] + k : a.x, xp[j] && in ? 16 : 0);
 #pragma unroll
     for (int j = 0; j < (NT + 3) / 4; ++j)
       if (NT >= 4 || row < N) {
@@ -262,46 +271,52 @@ __global__ void __launch_bounds__(kDownThreads, 3) adapter_down_many_kernel(cons
         cp_async16(dst + (kManyRows + j * 32) * 128, have ? ap + (int64_t)j * 32 * a.K + k : a.a, have ? 16 : 0);
       }
   };
-  float acc[NT][4];
+  float acc[2][NT][4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+  for (int i = 0; i < 2 * NT * 4; ++i) (&acc[0][0][0])[i] = 0.f;
   if (r0 < live) {
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (i < mine) fetch(i);
+    for (int i = 0; i < S - 1; ++i) {
+      if (i < mine) fetch(i, i);
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    const int wm = warp & 1, wk = (warp >> 1) * 2;  // rows of 16, pieces of the stage
+    const int wk = (warp >> 1) * 2;  // the warp's pieces of the stage
     // ldmatrix: lanes 0-15 rows, lanes 16-31 the same rows' next piece; for A rows 0-7, their next piece, rows 8-15
-    const int xr = wm * 16 + (lane & 15), br = (lane & 7) + (lane >> 4) * 8;
+    const int xr = (warp & 1) * 32 + (lane & 15), br = (lane & 7) + (lane >> 4) * 8;
     const uint32_t x_at = xr * 128 + (((wk + (lane >> 4)) ^ (xr & 7)) << 4);
     const uint32_t b_at = (kManyRows + br) * 128 + (((wk + (lane >> 3 & 1)) ^ (br & 7)) << 4);
+    int stage = 0;
     for (int i = 0; i < mine; ++i) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
       __syncthreads();  // stage i is there, and stage i - 1 has been used
-      if (i + kStages - 1 < mine) fetch(i + kStages - 1);
+      if (i + S - 1 < mine) fetch(i + S - 1, stage == 0 ? S - 1 : stage - 1);
       asm volatile("cp.async.commit_group;" ::: "memory");
-      const uint32_t st = base + (i % kStages) * kStageBytes;
-      uint32_t x[4], b[4];
-      ldmatrix4(x, st + x_at);
+      const uint32_t st = base + stage * kStageBytes;
+      uint32_t x[2][4], b[4];
+      ldmatrix4(x[0], st + x_at);
+      ldmatrix4(x[1], st + x_at + 16 * 128);
 #pragma unroll
       for (int n = 0; n < NT; n += 2) {
         ldmatrix4(b, st + b_at + n * 8 * 128);
-        mma_16816(acc[n], x[0], x[1], x[2], x[3], b[0], b[1]);
-        mma_16816(acc[n + 1], x[0], x[1], x[2], x[3], b[2], b[3]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          mma_16816(acc[m][n], x[m][0], x[m][1], x[m][2], x[m][3], b[0], b[1]);
+          mma_16816(acc[m][n + 1], x[m][0], x[m][1], x[m][2], x[m][3], b[2], b[3]);
+        }
       }
+      stage = stage == S - 1 ? 0 : stage + 1;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();  // the stages' place is the parts' now
   }
-  float* part = reinterpret_cast<float*>(down_smem) + (warp >> 1) * kManyRows * N + (warp & 1) * 16 * N;
+  float* part = reinterpret_cast<float*>(down_smem) + (warp >> 1) * kManyRows * N + (warp & 1) * 32 * N;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    *reinterpret_cast<float2*>(part + g * N + n * 8 + 2 * c) = make_float2(acc[n][0], acc[n][1]);
-    *reinterpret_cast<float2*>(part + (g + 8) * N + n * 8 + 2 * c) = make_float2(acc[n][2], acc[n][3]);
-  }
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      *reinterpret_cast<float2*>(part + (m * 16 + g) * N + n * 8 + 2 * c) = make_float2(acc[m][n][0], acc[m][n][1]);
+      *reinterpret_cast<float2*>(part + (m * 16 + g + 8) * N + n * 8 + 2 * c) = make_float2(acc[m][n][2], acc[m][n][3]);
+    }
   join_down<4, kManyRows, N, kDownThreads>(a, t, reinterpret_cast<float*>(down_smem), share, r0, live);
 }
 
@@ -350,8 +365,8 @@ TB_DEVI void cp_async8(uint32_t dst, const void* src, int bytes) {  // the rest 
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// W: elements of a row of B a thread loads at a time, by 4 threads, of blocks of 16, 32 or 64 ranks; MULTI: several
-// blocks.  An item of the ring is a block of a unit, with the unit's y at its first block.
+// W: elements of a row of B a thread loads at a time (16 as twice 8, so that four threads' are 64 bytes in a row), of
+// blocks of 16, 32 or 64 ranks; MULTI: several blocks.  An item of the ring is a block of a unit, with the unit's y at its first block.
 template <int W, bool MULTI>
 __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const AdapterArgs a) {
   constexpr int kBlock = W * 4, kMma = W / 4, S = up_few_stages(W);  // ranks of a block, its MMAs of 16
@@ -387,19 +402,19 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
         yo[i] = k * a.ldy + 4 * g, oo[i] = k * a.ldo + 4 * g;
       }
     }
-    const __half* b = a.b + (int64_t)t.adapter * a.N * a.R + (int64_t)(4 * g) * a.R + c * W;
+    const __half* b = a.b + (int64_t)t.adapter * a.N * a.R + (int64_t)(4 * g) * a.R + c * (W / kPieces);
     const int blocks = MULTI ? max(1, (live + kBlock - 1) / kBlock) : 1;
     auto fetch = [&](int u, int blk, int stage) {  // rows 4 g .. + 3 of unit u; zeros behind the rank and the last row
       const bool in = u * 32 + 4 * g < a.N;  // (N is a multiple of 8)
-      const int left = (live - blk * kBlock - c * W) * 2;
+      const int left = (live - blk * kBlock - c * (W / kPieces)) * 2;
       const __half* p = b + (int64_t)u * 32 * a.R + blk * kBlock;
 #pragma unroll
       for (int j = 0; j < 4; ++j, p += a.R)
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          const int bytes = in ? min(kBytes, max(0, left - i * kBytes)) : 0;
+          const int bytes = in ? min(kBytes, max(0, left - i * 64)) : 0;
           if constexpr (W == 4) cp_async8(row_at(stage, j, i), bytes ? p : a.b, bytes);
-          else cp_async16(row_at(stage, j, i), bytes ? p + i * 8 : a.b, bytes);
+          else cp_async16(row_at(stage, j, i), bytes ? p + i * 32 : a.b, bytes);
         }
       if (!MULTI || blk == 0) {
 #pragma unroll
@@ -422,14 +437,14 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
     // the terms of token g of each eight, as the mma's right operand
     auto term = [&](uint32_t (&h)[W / 2], int n, int lo, int blk) {
       const int p = n * 8 + g;
-      const __half* q = a.terms + (((int64_t)(t.first + p) * a.blocks + blk) * 2 + lo) * kBlock + c * W;
+      const __half* q = a.terms + (((int64_t)(t.first + p) * a.blocks + blk) * 2 + lo) * kBlock + c * (W / kPieces);
       if constexpr (W == 4) {
         const uint2 v = p < t.count ? *reinterpret_cast<const uint2*>(q) : make_uint2(0, 0);
         h[0] = v.x, h[1] = v.y;
       } else {
 #pragma unroll
         for (int i = 0; i < W / 2; i += 4) {
-          const uint4 v = p < t.count ? *reinterpret_cast<const uint4*>(q + i * 2) : make_uint4(0, 0, 0, 0);
+          const uint4 v = p < t.count ? *reinterpret_cast<const uint4*>(q + i * 8) : make_uint4(0, 0, 0, 0);
           h[i] = v.x, h[i + 1] = v.y, h[i + 2] = v.z, h[i + 3] = v.w;
         }
       }
@@ -515,24 +530,26 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
 
 // ---------------------------------------------------------------- up, many tokens
 // Every CTA takes an equal run of all row tiles' (at most 128 tokens) column tiles of 64, a warp 16 of the tokens.  A
-// thread keeps its tokens' terms as the mma's left operand (of up to 64 ranks; above, they are read again), and B's
-// rows come by cp.async two column tiles ahead.  Which column of out is which of the MMAs' columns is free: thread
-// (g, c) has 16 neighbouring ones of tokens g and g + 8, so that y and out go between global memory and registers in
-// whole sectors, y one column tile ahead.
-constexpr int kUpThreads = 256, kUpCols = 64, kUpStages = 3;
+// thread keeps its tokens' terms as the mma's left operand (of up to 64 ranks; above, they are read again); B's rows come
+// by cp.async three column tiles ahead, and y into a ring of the thread's own with them.  Which column of out is which of the MMAs' columns is free: thread
+// (g, c) has twice 8 neighbouring ones of tokens g and g + 8, so that four threads' y and out are 64 bytes in a row.
+constexpr int kUpThreads = 256, kUpCols = 64;
+constexpr int up_stages(bool multi) { return multi ? 3 : 4; }
 
 // bytes of a row of B in shared memory: an odd number of 32, so that four rows' 32 bytes lie in different banks
-__host__ __device__ __forceinline__ int up_pitch(int R) { return ((R + 15) / 16 | 1) * 32; }
+__host__ __device__ constexpr int up_pitch(int R) { return ((R + 15) / 16 | 1) * 32; }
+constexpr int kUpY = kUpThreads * 4 * 16;  // bytes of a stage's y
 
 // KS: steps of 16 ranks of a block; MULTI: several blocks
 template <int KS, bool MULTI>
 __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const AdapterArgs a) {
+  constexpr int S = up_stages(MULTI);
   extern __shared__ __align__(128) unsigned char up_smem[];
   if (!plan_fits(a)) return;
   copy_bare(a);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  const int pitch = up_pitch(a.R);
-  const uint32_t base = smem_u32(up_smem), stage_bytes = kUpCols * pitch;
+  const int pitch = MULTI ? up_pitch(a.R) : up_pitch(KS * 16);
+  const uint32_t base = smem_u32(up_smem), y_ring = base + tid * 16, b_ring = base + S * kUpY, stage_bytes = kUpCols * pitch;
   const int cols = (a.N + kUpCols - 1) / kUpCols;
   const int64_t all = (int64_t)a.plan->tiles[a.up_kind] * cols;
   int64_t at = all * blockIdx.x / gridDim.x;
@@ -544,49 +561,52 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const Ad
     at += end - begin;
     const AdapterTile t = a.up_tiles[tile];
     const int live = live_rank(a, t.adapter), steps = max(1, (live + 15) >> 4);
-    // column 16 c + 2 j + i of a tile is column 2 c + i of MMA j: its row of B lies at 8 j + 2 c + i.  Zeros behind the
-    // rank up to whole steps
-    const __half* bg = a.b + (int64_t)t.adapter * a.N * a.R;
-    const int pieces = 2 * steps, more = kUpThreads / pieces, rest = kUpThreads - more * pieces;
-    const int col0 = tid / pieces, piece0 = tid - col0 * pieces;
-    auto fetch = [&](int nt) {
-      const uint32_t st = base + (nt - begin) % kUpStages * stage_bytes;
-      const __half* src = bg + (int64_t)nt * kUpCols * a.R;
-      const int have = min(kUpCols, a.N - nt * kUpCols);
-      for (int col = col0, p = piece0; col < kUpCols;) {
-        const int bytes = col < have ? min(16, max(0, (live - p * 8) * 2)) : 0;
-        cp_async16(st + ((col >> 1 & 7) * 8 + (col >> 4) * 2 + (col & 1)) * pitch + p * 16, bytes ? src + col * a.R + p * 8 : a.b, bytes);
-        col += more, p += rest;
-        if (p >= pieces) p -= pieces, ++col;
-      }
-    };
-    __syncthreads();  // the stages of the run before have been used
-#pragma unroll
-    for (int i = 0; i < kUpStages - 1; ++i) {
-      if (begin + i < end) fetch(begin + i);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
     const int p0 = warp * 16 + g;  // the thread's tokens: p0 and p0 + 8 of the tile
     const __half* yp[2];
     __half* op[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int k = p0 + 8 * i < t.count ? a.order[t.first + p0 + 8 * i] : -1;
-      yp[i] = k >= 0 ? a.y + k * a.ldy + 16 * c : nullptr;
-      op[i] = a.out + (k >= 0 ? k : 0) * a.ldo + 16 * c;
+      yp[i] = k >= 0 ? a.y + k * a.ldy + 8 * c : nullptr;
+      op[i] = a.out + (k >= 0 ? k : 0) * a.ldo + begin * kUpCols + 8 * c;
     }
-    struct Y {
-      uint4 v[2][2];
-    };
-    auto load_y = [&](Y& y, int nt) {
+    // Column 32 q + 8 c + 2 j + i of a tile is column 2 c + i of MMA 4 q + j: its row of B lies at 8 (4 q + j) + 2 c + i.
+    // Zeros behind the rank up to whole steps
+    const __half* bg = a.b + (int64_t)t.adapter * a.N * a.R;
+    const int pieces = MULTI ? 2 * steps : 2 * KS, more = kUpThreads / pieces, rest = kUpThreads - more * pieces;
+    const int col0 = tid / pieces, piece0 = tid - col0 * pieces;
+    auto fetch = [&](int nt, int stage) {
+      const int n0 = nt * kUpCols, have = min(kUpCols, a.N - n0);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-          if (yp[i] && nt * kUpCols + 16 * c + 8 * q < a.N) y.v[i][q] = __ldcs(reinterpret_cast<const uint4*>(yp[i] + nt * kUpCols) + q);
+          if (yp[i] && 8 * c + 32 * q < have) cp_async16(y_ring + stage * kUpY + (2 * i + q) * kUpThreads * 16, yp[i] + n0 + 32 * q, 16);
+      const uint32_t st = b_ring + stage * stage_bytes;
+      const __half* src = bg + (int64_t)n0 * a.R;
+      auto one = [&](int col, int p) {
+        const int bytes = col < have ? min(16, max(0, (live - p * 8) * 2)) : 0;
+        cp_async16(st + ((col & 32) + (col >> 1 & 3) * 8 + (col >> 3 & 3) * 2 + (col & 1)) * pitch + p * 16, bytes ? src + col * a.R + p * 8 : a.b, bytes);
+      };
+      if constexpr (MULTI) {
+        for (int col = col0, p = piece0; col < kUpCols;) {
+          one(col, p);
+          col += more, p += rest;
+          if (p >= pieces) p -= pieces, ++col;
+        }
+      } else if constexpr (KS >= 2) {
+#pragma unroll
+        for (int i = 0; i < kUpCols * 2 * KS / kUpThreads; ++i) one(col0 + i * (kUpThreads / (2 * KS)), piece0);
+      } else {
+        if (col0 < kUpCols) one(col0, piece0);
+      }
     };
-    Y ya, yb;
-    load_y(ya, begin);
+    __syncthreads();  // the stages of the run before have been used
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+      if (begin + i < end) fetch(begin + i, i);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // h is written
     waited = true;
     // ranks 16 k + 4 c .. + 3 of a block serve as the k's 2 c, 2 c + 1, 2 c + 8, 2 c + 9; B's are read below alike
@@ -609,63 +629,61 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const Ad
       }
     };
     if (!MULTI) terms(0);
-    int nt = begin;
-    auto one = [&](Y& y, Y& next) {
-      if (nt + 1 < end) load_y(next, nt + 1);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kUpStages - 2) : "memory");
+    int stage = 0;
+    for (int nt = begin; nt < end; ++nt) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
       __syncthreads();  // tile nt is there, and tile nt - 1 has been used
-      if (nt + kUpStages - 1 < end) fetch(nt + kUpStages - 1);
+      if (nt + S - 1 < end) fetch(nt + S - 1, stage == 0 ? S - 1 : stage - 1);
       asm volatile("cp.async.commit_group;" ::: "memory");
-      const uint32_t st = base + (nt - begin) % kUpStages * stage_bytes + g * pitch + c * 8;
+      const uint32_t st = b_ring + stage * stage_bytes + g * pitch + c * 8;
+      const int left = a.N - nt * kUpCols - 8 * c;
       if (warp * 16 < t.count) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {  // MMAs 4 q .. + 3: columns 16 c + 8 q .. + 7
+        for (int q = 0; q < 2; ++q) {  // MMAs 4 q .. + 3: columns 32 q + 8 c .. + 7
           float sum[4][4];
           for (int blk = 0; blk < (MULTI ? (steps + KS - 1) / KS : 1); ++blk) {
             if (MULTI) terms(blk);
             float acc[4][4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) (&acc[0][0])[j] = 0.f;
-#pragma unroll
             for (int k = 0; k < KS; ++k) {
-              if (blk * KS + k >= steps) break;
+              if (k && blk * KS + k >= steps) break;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const uint2 b = ld_shared_v2(st + (4 * q + j) * 8 * pitch + (blk * KS + k) * 32);
-                mma_16816(acc[j], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b.x, b.y);
+                if (k == 0) mma_16816_first(acc[j], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b.x, b.y);
+                else mma_16816(acc[j], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b.x, b.y);
                 mma_16816(acc[j], hi[k][0], hi[k][1], hi[k][2], hi[k][3], b.x, b.y);
               }
             }
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const float f = back[j >> 1 & 1];
-              if (!MULTI || blk == 0) (&sum[0][0])[j] = (&acc[0][0])[j] * f;
-              else (&sum[0][0])[j] = fmaf((&acc[0][0])[j], f, (&sum[0][0])[j]);
+              float& s = (&sum[0][0])[j];
+              const float v = (&acc[0][0])[j];
+              s = !MULTI ? v : blk == 0 ? v * back[j >> 1 & 1] : fmaf(v, back[j >> 1 & 1], s);
             }
           }
-          if (nt * kUpCols + 16 * c + 8 * q < a.N) {
+          if (32 * q < left) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               if (!yp[i]) continue;
-              uint4 o = y.v[i][q];
+              uint4 o = ld_shared_v4(y_ring + stage * kUpY + (2 * i + q) * kUpThreads * 16);
               uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+              const float f = MULTI ? 1.f : back[i];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-                w[j] = pack_half2(f.x + sum[j][2 * i], f.y + sum[j][2 * i + 1]);
+                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+                w[j] = pack_half2(fmaf(sum[j][2 * i], f, v.x), fmaf(sum[j][2 * i + 1], f, v.y));
               }
-              __stcs(reinterpret_cast<uint4*>(op[i] + nt * kUpCols) + q, o);
+              __stcs(reinterpret_cast<uint4*>(op[i]) + 4 * q, o);
             }
           }
         }
       }
-      ++nt;
-    };
-    while (nt < end) {
-      one(ya, yb);
-      if (nt >= end) break;
-      one(yb, ya);
+      op[0] += kUpCols;
+      op[1] += kUpCols;
+      stage = stage == S - 1 ? 0 : stage + 1;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 }
 
@@ -760,12 +778,13 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   g.R = (int)R;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t down = adapter_max_tiles(T, n, g.down_kind), up = adapter_max_tiles(T, n, g.up_kind);
-  // K is split over a cluster until there are two CTAs an SM, of at least four steps a warp (few) or 16 stages (many)
+  // K is split over a cluster: few tokens, until there are two CTAs an SM, of at least four steps a warp; many, as long as
+  // all CTAs are there at once, of at least 16 stages
   g.cluster = 1;
   if (few)
     while (g.cluster < 8 && down * g.cluster < 2 * f.sms && K / 32 >= g.cluster * 2 * kDownWarps) g.cluster *= 2;
   else
-    while (g.cluster < 8 && down * g.cluster < 2 * f.sms && K / 64 >= g.cluster * 32) g.cluster *= 2;
+    while (g.cluster < 8 && down * g.cluster * 2 <= (R <= 32 ? 3 : 2) * f.sms && K / 64 >= g.cluster * 32) g.cluster *= 2;
   const int nt = g.block / 8;
   const dim3 grid((unsigned)(down * g.cluster), (unsigned)g.blocks);
   cudaError_t e;
@@ -797,7 +816,7 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
 #undef TB_UP
       if (rc != TB_OK) return rc;
     } else {
-      const size_t smem = (size_t)kUpStages * kUpCols * up_pitch((int)R);
+      const size_t smem = (size_t)up_stages(R > 64) * (kUpY + kUpCols * up_pitch(R <= 64 ? rank_block(R) : (int)R));
       const int64_t ctas = up * ((N + kUpCols - 1) / kUpCols);
       const dim3 some((unsigned)(ctas < 2 * f.sms ? ctas : 2 * f.sms));
 #define TB_UP(KS, MULTI)                                                                                                           \
