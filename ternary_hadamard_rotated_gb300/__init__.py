@@ -504,13 +504,20 @@ def tb_gated_delta(q, k, v, g, beta, row_start, max_len, o, workspace=None, stat
         _stream(stream)))
 
 
+_current_device = None
+
+
 def _here(name, t, stream):
     """The launch goes to the current device: the tensor has to lie there (a given stream is the caller's word)."""
-    if not t.is_cuda:
+    at = t.get_device()
+    if at < 0:
         raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
     if stream is None:
-        import torch._C as c
-        if t.get_device() != c._cuda_getDevice():
+        global _current_device
+        if _current_device is None:
+            import torch._C as c
+            _current_device = c._cuda_getDevice
+        if at != _current_device():
             raise ValueError(f"{name} lies on {t.device}, which is not the current device")
 
 

@@ -83,7 +83,8 @@ def same(got, want):
     ([1], 248320, 900, 700, {}), ([1], 1, 3, 3, dict(biases=1, grammar=1.0)), ([1, 1, 1], 31, 40, 40, dict(biases=9, grammar=0.7)),
     ([1] * 9, 50257, 3000, 3000, dict(biases=300, grammar=0.5, pad=7)), ([1] * 3, 8192, 0, 0, dict(biases=5)), ([1] * 2, 131072, 40000, 40000, dict(pad=64)),
     ([4, 0, 1, 9], 32000, 500, 500, dict(tree=True, grammar=0.3)), ([64, 3], 1000, 100, 100, dict(tree=True, biases=4)), ([5, 2], 300007, 60, 60, dict(fresh=True, biases=1000)),
-    ([1] * 200, 129, 20, 20, dict(grammar=0.5)), ([1] * 6, 8200, 64, 64, dict(fresh=True, biases=20, pad=8))])
+    ([1] * 200, 129, 20, 20, dict(grammar=0.5)), ([1] * 6, 8200, 64, 64, dict(fresh=True, biases=20, pad=8)),
+    ([1] * 64, 50000, 300, 300, dict(grammar=0.6)), ([7, 50, 30], 50003, 5000, 5000, dict(grammar=0.6, tree=True, biases=2000, pad=5))])
 @pytest.mark.parametrize("kind", ["half", "float", "in place"])
 def test_logits_match(lens, V, L, hist_hi, kw, kind):
     rng = np.random.default_rng(V + L)
