@@ -75,7 +75,7 @@ __global__ void rotary_plan_kernel(const RotaryPlanArgs a, RotaryPlan* __restric
   reinterpret_cast<unsigned long long*>(plan + 1)[i] = turns;
 }
 
-// ---------------------------------------------------------------- rotation
+// ---------------------------------------------------------------- rotation, any head
 struct RotaryArgs {
   const __half *q, *k, *v;
   __half *q_out, *k_out, *k_cache, *v_cache;
@@ -226,6 +226,132 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
   }
 }
 
+// ---------------------------------------------------------------- heads of 64, 128 and 256
+// L lanes hold a head's row, 16 bytes each, so that every access is a whole row; the row's other half of a pair comes
+// from the lane that holds it (neighbours in pairs are in one lane anyway).  A warp takes a token, or a part of its rows
+// where tokens are few: kAhead rows of loads on their way before the angles are made, by all lanes together, a pair at a
+// time, and kept in registers for all of the token's heads.  Bound by the bytes: 12289 tokens of 24/4 heads of 256, 64 of
+// them turned, with the cache's write, 428 MB in 72.6 us, 0.87 of measured HBM; 40001 tokens of 32/8 heads of 128, 819 MB
+// in 126 us, 0.96 (the form for any head: 137 and 147).  Four CTAs an SM: with five the registers spill (88, 137).
+constexpr int kRowsThreads = 256, kRowsWarps = kRowsThreads / 32;
+
+template <int L, bool PAIRS>
+__global__ void __launch_bounds__(kRowsThreads, 4) rotary_rows_kernel(const RotaryArgs a) {
+  constexpr int D = L * 8, kRows = 32 / L, kAhead = 4;
+  extern __shared__ __align__(16) float row_angles[];  // of each warp: cosines [R/2], sines [R/2]
+  if (a.plan->magic != kRotaryMagic || a.plan->R != a.R) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, TB_DEV_BAD_PLAN);
+    return;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % L, half = a.R / 2;
+  const float amp = a.plan->amplitude;
+  const unsigned long long* turns = reinterpret_cast<const unsigned long long*>(a.plan + 1);
+  float *cosines = row_angles + warp * a.R, *sines = cosines + half;
+  // the lane's elements: turned or not, and as the first or second of their pairs
+  const bool turned = c * 8 < a.R;
+  const int hop = half / 8;  // lanes from the first half of the pairs to the second
+  const bool second = !PAIRS && turned && c >= hop;
+  const int pair = PAIRS ? c * 4 : (second ? c - hop : c) * 8;
+  const int other = PAIRS || !turned ? lane : second ? lane - hop : lane + hop;
+  const int rows = a.Hq + a.Hk + (a.v_cache ? a.Hk : 0);
+  const int64_t head = (int64_t)D << a.page_log2;  // of the cache: elements from one head to the next
+  const int64_t units = a.T * a.split;
+  for (int64_t u = (int64_t)blockIdx.x * kRowsWarps + warp; u < units; u += (int64_t)gridDim.x * kRowsWarps) {
+    const int64_t t = u / a.split;
+    const int part = (int)(u - t * a.split);
+    const int begin = rows * part / a.split, end = rows * (part + 1) / a.split;
+    const __half *q = a.q + t * a.ldq + c * 8, *k = a.k + t * a.ldk + c * 8, *v = a.v + t * a.ldv + c * 8;
+    auto load = [&](int row) {
+      const __half* p = row < a.Hq ? q + row * D : row < a.Hq + a.Hk ? k + (row - a.Hq) * D : v + (row - a.Hq - a.Hk) * D;
+      return row < end ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+    };
+    uint4 x[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) x[i] = load(begin + i * kRows + lane / L);
+    int64_t slot = -1;
+    if (a.slots) {
+      slot = __ldg(a.slots + t);
+      if (slot >= a.n_slots) {
+        if (lane == 0) set_status(a.status, TB_DEV_BAD_SLOT);
+        slot = -1;
+      }
+    }
+    const int64_t place = slot < 0 ? 0 : (((slot >> a.page_log2) * a.Hk << a.page_log2) + (slot & ((1ll << a.page_log2) - 1))) * D + c * 8;
+    const unsigned long long pos = (unsigned long long)(long long)__ldg(a.pos + t);
+    __syncwarp();
+    for (int i = lane; i < half; i += 32) {
+      float sn, cs;
+      sincospif(__ll2float_rn((long long)(pos * turns[i])) * 0x1p-63f, &sn, &cs);
+      cosines[i] = amp * cs;
+      sines[i] = a.inverse ? -amp * sn : amp * sn;
+    }
+    __syncwarp();
+    float cs[PAIRS ? 4 : 8], sn[PAIRS ? 4 : 8];
+    if (turned) {
+#pragma unroll
+      for (int i = 0; i < (PAIRS ? 4 : 8); i += 4) {
+        const float4 p = *reinterpret_cast<const float4*>(cosines + pair + i), r = *reinterpret_cast<const float4*>(sines + pair + i);
+        cs[i] = p.x, cs[i + 1] = p.y, cs[i + 2] = p.z, cs[i + 3] = p.w;
+        sn[i] = r.x, sn[i + 1] = r.y, sn[i + 2] = r.z, sn[i + 3] = r.w;
+      }
+      if (second) {  // b cos + a sin, as a cos - b sin with the sine turned round
+#pragma unroll
+        for (int i = 0; i < (PAIRS ? 4 : 8); ++i) sn[i] = -sn[i];
+      }
+    }
+    for (int row0 = begin; row0 < end; row0 += kAhead * kRows) {
+      if (row0 > begin) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) x[i] = load(row0 + i * kRows + lane / L);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int row = row0 + i * kRows + lane / L;
+        uint4 y = x[i];
+        if (row0 + i * kRows < a.Hq + a.Hk) {  // (all lanes: some of its rows may be v's)
+          if constexpr (PAIRS) {
+            if (turned) {
+              const Eight e = unpack8(x[i]);
+              Eight o;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                o.v[2 * j] = e.v[2 * j] * cs[j] - e.v[2 * j + 1] * sn[j];
+                o.v[2 * j + 1] = e.v[2 * j] * sn[j] + e.v[2 * j + 1] * cs[j];
+              }
+              y = pack8(o);
+            }
+          } else {
+            uint4 z;
+            z.x = __shfl_sync(0xffffffffu, x[i].x, other);
+            z.y = __shfl_sync(0xffffffffu, x[i].y, other);
+            z.z = __shfl_sync(0xffffffffu, x[i].z, other);
+            z.w = __shfl_sync(0xffffffffu, x[i].w, other);
+            if (turned) {
+              const Eight e = unpack8(x[i]), f = unpack8(z);
+              Eight o;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o.v[j] = e.v[j] * cs[j] - f.v[j] * sn[j];
+              y = pack8(o);
+            }
+          }
+        }
+        if (row < end) {
+          if (row < a.Hq) {
+            __half* o = a.q_out + t * a.ldqo + row * D + c * 8;
+            if (turned || a.q_copy) *reinterpret_cast<uint4*>(o) = y;
+          } else if (row < a.Hq + a.Hk) {
+            const int h = row - a.Hq;
+            if (a.k_out && (turned || a.k_out != a.k)) *reinterpret_cast<uint4*>(a.k_out + t * a.ldko + h * D + c * 8) = y;
+            if (slot >= 0) *reinterpret_cast<uint4*>(a.k_cache + place + h * head) = y;
+          } else if (slot >= 0) {
+            *reinterpret_cast<uint4*>(a.v_cache + place + (row - a.Hq - a.Hk) * head) = x[i];
+          }
+        }
+      }
+    }
+  }
+}
+
 static int launch_rotary(RotaryArgs a, cudaStream_t stream) {
   DeviceFacts f;
   const int rc = device_facts(&f);
@@ -236,6 +362,21 @@ static int launch_rotary(RotaryArgs a, cudaStream_t stream) {
   a.q_copy = a.q_out != a.q ? copy : 0;
   a.k_copy = a.k_cache || (a.k_out && a.k_out != a.k) ? copy : 0;
   a.per_token = a.Hq * (a.rot + a.q_copy) + a.Hk * (a.rot + a.k_copy) + (a.v_cache ? a.Hk * (a.D / 8) : 0);
+  if (wide && (a.D == 64 || a.D == 128 || a.D == 256)) {
+    const int per = a.D / 8, step = 32 / per, rows = a.Hq + a.Hk + (a.v_cache ? a.Hk : 0), steps = (rows + step - 1) / step;
+    // a token's rows are shared out while tokens are few, down to four rows a lane
+    const int64_t enough = (int64_t)f.sms * 32;
+    int64_t split = (enough + a.T - 1) / a.T;
+    if (split > (steps + 3) / 4) split = (steps + 3) / 4;
+    a.split = (int)split;
+    int64_t ctas = (a.T * split + kRowsWarps - 1) / kRowsWarps;
+    if (ctas > (int64_t)f.sms * 16) ctas = (int64_t)f.sms * 16;
+    const int smem = kRowsWarps * a.R * 4;
+    void (*fn)(const RotaryArgs) = a.pairs ? (per == 8 ? rotary_rows_kernel<8, true> : per == 16 ? rotary_rows_kernel<16, true> : rotary_rows_kernel<32, true>)
+                                           : (per == 8 ? rotary_rows_kernel<8, false> : per == 16 ? rotary_rows_kernel<16, false> : rotary_rows_kernel<32, false>);
+    fn<<<(unsigned)ctas, kRowsThreads, smem, stream>>>(a);
+    return check_launch();
+  }
   a.tile = kRotaryAngles / (a.R / 2);
   if (a.tile > 8) a.tile = 8;
   const int64_t ctas = (int64_t)f.sms * 8;
