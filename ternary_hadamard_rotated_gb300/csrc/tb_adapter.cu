@@ -2,7 +2,8 @@
 // adapter of token t's request.
 //
 // Two launches, the second (programmatic) loading what the first does not write before it waits for it:
-//   down  h = scale A x, mma.sync on tiles of 16 or 64 tokens of one adapter, to the workspace in the plan's order
+//   down  h = scale A x, to the workspace in the plan's order; few tokens: mma.sync on tiles of 16 tokens of one adapter;
+//         many: tcgen05 on tiles of 128
 //   up    out = y + B h, mma.sync; few tokens: tiles of 16, bound by the weights, which go from global memory straight
 //         to the registers; many: tiles of 128, bound by y and out
 //
@@ -14,6 +15,7 @@
 #include <limits.h>
 
 #include "tb_adapter.cuh"
+#include "tb_attn_tc.cuh"
 #include "tb_common.cuh"
 #include "tb_host.h"
 
@@ -81,18 +83,20 @@ TB_DEVI float up_scale(float top, float& back) {
 }
 
 // ---------------------------------------------------------------- down
-// Parts of a tile's h, [PARTS][M][N] in shared memory, summed in their order, then over the cluster's CTAs in theirs;
+// Parts of a tile's h, [PARTS][M][PITCH] in shared memory, summed in their order, then over the cluster's CTAs in theirs;
 // each CTA has some of the rows, a warp one at a time.
-template <int PARTS, int M, int N, int THREADS>
+template <int PARTS, int M, int N, int PITCH, int THREADS>
 TB_DEVI void join_down(const AdapterArgs& a, const AdapterTile& t, float* part, int share, int r0, int live) {
   const int tid = threadIdx.x, lane = tid & 31;
   const float scale = __ldg(a.scale + t.adapter);
-  __syncthreads();
-  for (int e = tid; e < M * N; e += THREADS) {
-    float s = part[e];
+  if constexpr (PARTS > 1) {
+    __syncthreads();
+    for (int e = tid; e < M * PITCH; e += THREADS) {
+      float s = part[e];
 #pragma unroll
-    for (int w = 1; w < PARTS; ++w) s += part[w * M * N + e];
-    part[e] = s;
+      for (int w = 1; w < PARTS; ++w) s += part[w * M * PITCH + e];
+      part[e] = s;
+    }
   }
   cg::cluster_group cl = cg::this_cluster();
   if (a.cluster > 1) cl.sync();
@@ -109,7 +113,7 @@ TB_DEVI void join_down(const AdapterArgs& a, const AdapterTile& t, float* part, 
       v[j] = 0.f;
       if (col < N && r0 + col < live) {
         float s = 0.f;
-        for (int r = 0; r < a.cluster; ++r) s += a.cluster > 1 ? *cl.map_shared_rank(part + row * N + col, r) : part[row * N + col];
+        for (int r = 0; r < a.cluster; ++r) s += a.cluster > 1 ? *cl.map_shared_rank(part + row * PITCH + col, r) : part[row * PITCH + col];
         v[j] = s * scale;
       }
       top = fmaxf(top, fabsf(v[j]));
@@ -219,25 +223,31 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_few_kernel(const
     *reinterpret_cast<float2*>(part + g * N + n * 8 + 2 * c) = make_float2(acc[n][0], acc[n][1]);
     *reinterpret_cast<float2*>(part + (g + 8) * N + n * 8 + 2 * c) = make_float2(acc[n][2], acc[n][3]);
   }
-  join_down<kDownWarps, 16, N, kDownThreads>(a, t, reinterpret_cast<float*>(down_smem), share, r0, live);
+  join_down<kDownWarps, 16, N, N, kDownThreads>(a, t, reinterpret_cast<float*>(down_smem), share, r0, live);
 }
 
-// Many tokens: a CTA takes 64 tokens by NT x 8 rows of A, both through shared memory by cp.async, 64 of K a stage and
-// all stages but one ahead; rows of 128 bytes, their 16-byte pieces exchanged by row (piece ^ row mod 8), so that
-// ldmatrix finds eight rows in eight different banks.  Warps: two by 32 rows, four by the stage's k's.
-constexpr int kManyRows = 64;
-constexpr int many_stages(int NT) { return NT == 8 ? 5 : NT == 4 ? 6 : 7; }
-
-template <int NT>
+// Many tokens: a CTA takes 128 tokens by N rows of A, on tcgen05 with the sums in tensor memory.  Eight warps bring both
+// operands to shared memory by cp.async (the tokens lie anywhere, and what is not there is zeroed), 64 of K a stage, in the
+// 128-byte swizzle that the MMA's descriptors name (16-byte piece ^ row mod 8); when a thread's part of a stage has come it
+// counts itself on the stage's barrier, two stages later than it asked for it.  The ninth warp's first lane issues the MMAs.
+// With mma.sync instead (64 tokens a CTA), every warp took 100 instructions a stage at 11 clocks each: 28 us for 5935
+// tokens of K 5120 and 64 ranks, 52 for 8192 of K 17408 and 16.
+constexpr int kManyThreads = kDownThreads + 32, kManyRows = 128, kManyLag = 2;
+constexpr int many_stages(int N) { return N == 64 ? 4 : 5; }
+template <int N>
 constexpr int down_many_smem() {
-  const int stages = many_stages(NT) * (kManyRows + NT * 8) * 128, parts = 4 * kManyRows * NT * 8 * 4;
-  return stages > parts ? stages : parts;
+  return 1024 + many_stages(N) * (kManyRows + N) * 128;
 }
 
-template <int NT>
-__global__ void __launch_bounds__(kDownThreads, NT == 8 ? 2 : 3) adapter_down_many_kernel(const AdapterArgs a) {
-  constexpr int N = NT * 8, S = many_stages(NT), kStageBytes = (kManyRows + N) * 128;
-  extern __shared__ __align__(128) unsigned char down_smem[];
+template <int N>
+__global__ void __launch_bounds__(kManyThreads, 2) adapter_down_many_kernel(const AdapterArgs a) {
+  constexpr int S = many_stages(N), kStageBytes = (kManyRows + N) * 128, kCols = N < 32 ? 32 : N, kPitch = N + 4;
+  constexpr uint32_t kInstr = 1u << 4 | (uint32_t)(N / 8) << 17 | (uint32_t)(kManyRows / 16) << 24;  // fp16 operands, fp32 sums
+  static_assert(kManyRows * kPitch * 4 <= S * kStageBytes, "the sums take the stages' place");
+  extern __shared__ __align__(1024) unsigned char down_smem[];
+  __shared__ uint64_t full[S], empty[S], done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int aborted;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tile = blockIdx.x / a.cluster, share = blockIdx.x - tile * a.cluster;
   const AdapterTile t = a.down_tiles[tile];  // (inside the plan, of a tile or not)
@@ -246,78 +256,104 @@ __global__ void __launch_bounds__(kDownThreads, NT == 8 ? 2 : 3) adapter_down_ma
     return;
   }
   if (tile >= a.plan->tiles[a.down_kind]) return;  // (all CTAs of the cluster)
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = blockIdx.y * N, live = live_rank(a, t.adapter);
-  const uint32_t base = smem_u32(down_smem);
-  const int steps = (a.K + 63) >> 6, mine = (steps - share + a.cluster - 1) / a.cluster;
-
-  // a thread's pieces of a stage: two of x, NT / 4 of A
-  const int row = tid >> 3, piece = tid & 7;
-  const uint32_t at = row * 128 + ((piece ^ (row & 7)) << 4);
-  const __half* xp[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) xp[i] = row + 32 * i < t.count ? a.x + a.order[t.first + row + 32 * i] * a.ldx + piece * 8 : nullptr;
-  const __half* ap = a.a + ((int64_t)t.adapter * a.R + r0 + row) * a.K + piece * 8;
-  auto fetch = [&](int i, int stage) {
-    const int k = (share + i * a.cluster) * 64;
-    const uint32_t dst = base + stage * kStageBytes + at;
-    const bool in = k + piece * 8 < a.K;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) cp_async16(dst + j * 32 * 128, xp[j] && in ? xp[j] + k : a.x, xp[j] && in ? 16 : 0);
-#pragma unroll
-    for (int j = 0; j < (NT + 3) / 4; ++j)
-      if (NT >= 4 || row < N) {
-        const bool have = in && r0 + row + j * 32 < live;
-        cp_async16(dst + (kManyRows + j * 32) * 128, have ? ap + (int64_t)j * 32 * a.K + k : a.a, have ? 16 : 0);
-      }
-  };
-  float acc[2][NT][4];
-#pragma unroll
-  for (int i = 0; i < 2 * NT * 4; ++i) (&acc[0][0][0])[i] = 0.f;
-  if (r0 < live) {
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
-      if (i < mine) fetch(i, i);
-      asm volatile("cp.async.commit_group;" ::: "memory");
+  unsigned char* const stages = down_smem + ((1024 - (smem_u32(down_smem) & 1023)) & 1023);
+  const uint32_t base = smem_u32(stages);
+  const int steps = (a.K + 63) >> 6, mine = r0 < live ? (steps - share + a.cluster - 1) / a.cluster : 0;
+  if (tid == 0) {
+    aborted = 0;
+    for (int i = 0; i < S; ++i) {
+      mbar_init(full + i, kDownThreads);
+      mbar_init(empty + i, 1);
     }
-    const int wk = (warp >> 1) * 2;  // the warp's pieces of the stage
-    // ldmatrix: lanes 0-15 rows, lanes 16-31 the same rows' next piece; for A rows 0-7, their next piece, rows 8-15
-    const int xr = (warp & 1) * 32 + (lane & 15), br = (lane & 7) + (lane >> 4) * 8;
-    const uint32_t x_at = xr * 128 + (((wk + (lane >> 4)) ^ (xr & 7)) << 4);
-    const uint32_t b_at = (kManyRows + br) * 128 + (((wk + (lane >> 3 & 1)) ^ (br & 7)) << 4);
-    int stage = 0;
-    for (int i = 0; i < mine; ++i) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-      __syncthreads();  // stage i is there, and stage i - 1 has been used
-      if (i + S - 1 < mine) fetch(i + S - 1, stage == 0 ? S - 1 : stage - 1);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      const uint32_t st = base + stage * kStageBytes;
-      uint32_t x[2][4], b[4];
-      ldmatrix4(x[0], st + x_at);
-      ldmatrix4(x[1], st + x_at + 16 * 128);
-#pragma unroll
-      for (int n = 0; n < NT; n += 2) {
-        ldmatrix4(b, st + b_at + n * 8 * 128);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          mma_16816(acc[m][n], x[m][0], x[m][1], x[m][2], x[m][3], b[0], b[1]);
-          mma_16816(acc[m][n + 1], x[m][0], x[m][1], x[m][2], x[m][3], b[2], b[3]);
-        }
-      }
-      stage = stage == S - 1 ? 0 : stage + 1;
-    }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();  // the stages' place is the parts' now
+    mbar_init(&done, 1);
+    fence_barrier_init();
   }
-  float* part = reinterpret_cast<float*>(down_smem) + (warp >> 1) * kManyRows * N + (warp & 1) * 32 * N;
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      *reinterpret_cast<float2*>(part + (m * 16 + g) * N + n * 8 + 2 * c) = make_float2(acc[m][n][0], acc[m][n][1]);
-      *reinterpret_cast<float2*>(part + (m * 16 + g + 8) * N + n * 8 + 2 * c) = make_float2(acc[m][n][2], acc[m][n][3]);
+  if (warp == kDownWarps) tmem_alloc(&tmem_slot, kCols);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t sums = tmem_slot;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity) || aborted) return;
+    if (!mbar_wait(bar, parity)) {
+      aborted = 1;
+      set_status(a.status, TB_DEV_TIMEOUT);
     }
-  join_down<4, kManyRows, N, kDownThreads>(a, t, reinterpret_cast<float*>(down_smem), share, r0, live);
+  };
+  if (warp < kDownWarps) {
+    // a thread's pieces of a stage: four of x, N / 32 of A
+    const int row = tid >> 3, piece = tid & 7;
+    const uint32_t at = row * 128 + ((piece ^ (row & 7)) << 4);
+    const __half* xp[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) xp[i] = row + 32 * i < t.count ? a.x + a.order[t.first + row + 32 * i] * a.ldx + piece * 8 : nullptr;
+    const __half* ap = a.a + ((int64_t)t.adapter * a.R + r0 + row) * a.K + piece * 8;
+    int stage = 0, uses = 0, ready = 0;  // the stage asked for next, its uses before, the stage that has come next
+    for (int i = 0; i < mine + kManyLag; ++i) {
+      if (i < mine) {
+        if (uses > 0) wait(empty + stage, (uses - 1) & 1);
+        const int k = (share + i * a.cluster) * 64;
+        const uint32_t dst = base + stage * kStageBytes + at;
+        const bool in = k + piece * 8 < a.K;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cp_async16(dst + j * 32 * 128, xp[j] && in ? xp[j] + k : a.x, xp[j] && in ? 16 : 0);
+#pragma unroll
+        for (int j = 0; j < (N + 31) / 32; ++j)
+          if (N >= 32 || row < N) {
+            const bool have = in && r0 + row + j * 32 < live;
+            cp_async16(dst + (kManyRows + j * 32) * 128, have ? ap + (int64_t)j * 32 * a.K + k : a.a, have ? 16 : 0);
+          }
+        if (++stage == S) stage = 0, ++uses;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (i >= kManyLag) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kManyLag) : "memory");
+        fence_proxy_async_smem();
+        mbar_arrive(full + ready);
+        ready = ready == S - 1 ? 0 : ready + 1;
+      }
+    }
+  } else if (lane == 0) {
+    for (int i = 0; i < mine; ++i) {
+      const int stage = i % S;
+      wait(full + stage, i / S & 1);
+      tmem_fence_after();
+      const uint64_t x = smem_desc_sw128(base + stage * kStageBytes, 1024), w = smem_desc_sw128(base + stage * kStageBytes + kManyRows * 128, 1024);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mma_f16_ss<1>(sums, x + 2 * k, w + 2 * k, kInstr, i > 0 || k > 0);
+      mma_commit(empty + stage);
+    }
+    if (mine) mma_commit(&done);
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
+  if (mine) wait(&done, 0);
+  tmem_fence_after();
+  __syncthreads();  // the stages' place is the sums' now
+  // warp w: tokens 32 w .. of the tile, a lane each
+  float* const part = reinterpret_cast<float*>(stages);
+  if (warp < 4) {
+    float v[N];
+    if (mine) {
+      if constexpr (N == 16) {
+        tmem_ld8(sums + ((uint32_t)(warp * 32) << 16), *reinterpret_cast<float (*)[8]>(v));
+        tmem_ld8(sums + ((uint32_t)(warp * 32) << 16) + 8, *reinterpret_cast<float (*)[8]>(v + 8));
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 32) tmem_ld32(sums + ((uint32_t)(warp * 32) << 16) + i, v + i);
+      }
+      tmem_wait_ld();
+    }
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<float4*>(part + tid * kPitch + i) = mine ? make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]) : make_float4(0, 0, 0, 0);
+  }
+  tmem_fence_before();
+  join_down<1, kManyRows, N, kPitch, kManyThreads>(a, t, part, share, r0, live);
+  __syncthreads();
+  if (warp == kDownWarps) tmem_dealloc(sums, kCols);
 }
 
 // ---------------------------------------------------------------- tokens without an adapter
@@ -756,8 +792,7 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   g.rank = rank;
   g.scale = scale;
   const bool few = T <= kFewTokens;
-  g.down_kind = few ? 0 : 1;
-  g.up_kind = few ? 0 : 2;
+  g.down_kind = g.up_kind = few ? 0 : 1;
   const char* base = static_cast<const char*>(plan);
   g.plan = static_cast<const AdapterPlan*>(plan);
   g.order = reinterpret_cast<const int32_t*>(base + adapter_order_at());
@@ -784,7 +819,7 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   if (few)
     while (g.cluster < 8 && down * g.cluster < 2 * f.sms && K / 32 >= g.cluster * 2 * kDownWarps) g.cluster *= 2;
   else
-    while (g.cluster < 8 && down * g.cluster * 2 <= (R <= 32 ? 3 : 2) * f.sms && K / 64 >= g.cluster * 32) g.cluster *= 2;
+    while (g.cluster < 8 && down * g.cluster * 2 <= 2 * f.sms && K / 64 >= g.cluster * 16) g.cluster *= 2;
   const int nt = g.block / 8;
   const dim3 grid((unsigned)(down * g.cluster), (unsigned)g.blocks);
   cudaError_t e;
@@ -792,14 +827,14 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_down_few_kernel<NT>), f.device, down_few_smem<NT>())) != TB_OK \
        ? cudaErrorUnknown                                                                                                       \
        : launch(adapter_down_few_kernel<NT>, grid, kDownThreads, (size_t)down_few_smem<NT>(), s, g.cluster, false, g))
-#define TB_DOWN_MANY(NT)                                                                                                        \
-  ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_down_many_kernel<NT>), f.device, down_many_smem<NT>())) != TB_OK \
-       ? cudaErrorUnknown                                                                                                       \
-       : launch(adapter_down_many_kernel<NT>, grid, kDownThreads, (size_t)down_many_smem<NT>(), s, g.cluster, false, g))
+#define TB_DOWN_MANY(N)                                                                                                        \
+  ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_down_many_kernel<N>), f.device, down_many_smem<N>())) != TB_OK \
+       ? cudaErrorUnknown                                                                                                      \
+       : launch(adapter_down_many_kernel<N>, grid, kManyThreads, (size_t)down_many_smem<N>(), s, g.cluster, false, g))
   if (few)
     e = nt == 2 ? TB_DOWN_FEW(2) : nt == 4 ? TB_DOWN_FEW(4) : TB_DOWN_FEW(8);
   else
-    e = nt == 2 ? TB_DOWN_MANY(2) : nt == 4 ? TB_DOWN_MANY(4) : TB_DOWN_MANY(8);
+    e = nt == 2 ? TB_DOWN_MANY(16) : nt == 4 ? TB_DOWN_MANY(32) : TB_DOWN_MANY(64);
 #undef TB_DOWN_FEW
 #undef TB_DOWN_MANY
   if (rc != TB_OK) return rc;

@@ -12,14 +12,15 @@ constexpr int kAdapterMaxR = 256;
 
 // Tokens are grouped by adapter (within one in the order they come in; behind the last adapter those without
 // one), and every adapter's group is cut into tiles of at most tile_rows(kind) tokens.
-constexpr int kTileKinds = 3;
-constexpr int tile_rows(int kind) { return kind == 0 ? 16 : kind == 1 ? 64 : 128; }
+constexpr int kTileKinds = 2;
+constexpr int tile_rows(int kind) { return kind == 0 ? 16 : 128; }
 
 struct AdapterPlan {  // head of the plan; behind it order int32 [T], then the tiles of each kind
   int32_t magic, T, n;
   int32_t tiles[kTileKinds];
   int32_t bare;  // where the tokens without an adapter begin
   int32_t rows;  // tokens of all requests
+  int32_t pad;
 };
 
 struct AdapterTile {

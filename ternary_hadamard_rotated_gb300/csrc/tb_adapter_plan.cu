@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_plan_kernel(const Group
       a.plan->n = a.n;
       a.plan->bare = start[a.n];
       a.plan->rows = total;
+      a.plan->pad = 0;
     }
     if (bad) set_status(a.status, bad);
   }
