@@ -813,11 +813,11 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   g.R = (int)R;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t down = adapter_max_tiles(T, n, g.down_kind), up = adapter_max_tiles(T, n, g.up_kind);
-  // K is split over a cluster: few tokens, until there are two CTAs an SM, of at least four steps a warp; many, as long as
-  // all CTAs are there at once, of at least 16 stages
+  // K is split over a cluster, as long as two CTAs an SM are enough for all (64 tiles by eight, as more than fit at once:
+  // 22 us for 64 tokens; by four: 19): few tokens, of at least four steps a warp; many, of at least 16 stages
   g.cluster = 1;
   if (few)
-    while (g.cluster < 8 && down * g.cluster < 2 * f.sms && K / 32 >= g.cluster * 2 * kDownWarps) g.cluster *= 2;
+    while (g.cluster < 8 && down * g.cluster * 2 <= 2 * f.sms && K / 32 >= g.cluster * 2 * kDownWarps) g.cluster *= 2;
   else
     while (g.cluster < 8 && down * g.cluster * 2 <= 2 * f.sms && K / 64 >= g.cluster * 16) g.cluster *= 2;
   const int nt = g.block / 8;

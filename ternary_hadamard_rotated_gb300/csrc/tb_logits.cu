@@ -361,8 +361,14 @@ __global__ void __launch_bounds__(kFixThreads, 3) logits_fix_kernel(const Logits
         // first the logits alone, several on their way at once
         float* const result = s.result + i;
         const __half* in = a.in + t * a.ld + v;
-#pragma unroll 4
-        for (int r = 0; r < rows; ++r) result[r * listed] = __half2float(__ushort_as_half(*reinterpret_cast<const volatile unsigned short*>(in + r * a.ld)));
+        for (int r0 = 0; r0 < rows; r0 += 8) {
+          unsigned short x[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = r0 + j < rows ? __ldcg(reinterpret_cast<const unsigned short*>(in + (r0 + j) * a.ld)) : 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (r0 + j < rows) result[(r0 + j) * listed] = half_bits_to_float(x[j]);
+        }
 #pragma unroll 1
         for (int r = 0; r < rows; ++r) {
           const int m = s.mask_row[r];
