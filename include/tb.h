@@ -550,7 +550,8 @@ int tb_rotary_plan(void* plan, size_t plan_bytes, int64_t R, double base, int sc
  * tb_rotary — q and k turned by their positions: a pair (a, b) of token t becomes
  *   amplitude * (a cos - b sin, a sin + b cos) of the angle pos[t] f_i; elements from R on are copied.
  *   q, k     fp16 [T, Hq, D] and [T, Hk, D], tokens ldq / ldk apart; Hk may be 0 (k and k_out then unused);
- *   pos      int32 [T], any value (a negative one turns back; angles are exact to 2^-24 of a turn for all);
+ *   pos      int32 [T], any value (a negative one turns back); whole turns are taken off exactly: angles are right to
+ *            2^-22 of a turn for all positions and frequencies up to 1;
  *   plan, R  from tb_rotary_plan with the same R <= D;  layout TB_ROTARY_HALF or TB_ROTARY_PAIRS;
  *   inverse  nonzero: by the opposite angle (the transpose, amplitude included: the rotation's gradient);
  *   q_out, k_out  fp16 (out), tokens ldqo / ldko apart; may be q and k (with their distances), and must not
@@ -621,7 +622,7 @@ int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int64_t K, cons
  *   biased:                                                                       l <- l + its bias
  *   its bit of the row's mask is 0:                                               l <- -infinity
  *   logits     fp16 [T, V], rows ld >= V apart (any distance; multiples of 8 are faster);
- *   history    int32 [n_hist, ldh]: request b's tokens are row slot[b] (int32 [B]; NULL: row b; negative: none);
+ *   history    int32 [n_hist, ldh] (ldh up to 2^28): request b's tokens are row slot[b] (int32 [B]; NULL: row b; negative: none);
  *   hist_len   int32 [B];  prompt_len int32 [B] or NULL (zeros);
  *   fresh      int32 [T] or NULL: the tokens that the rows were computed from, where the history does not hold
  *              them yet: up to 64 a request, in the order of its rows.  A row's path is itself and its request's

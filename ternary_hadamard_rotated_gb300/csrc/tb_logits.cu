@@ -414,7 +414,7 @@ extern "C" int tb_logits_adjust(const uint16_t* logits, int64_t ld, int64_t T, i
                                 const float* bias_values, int64_t n_bias, const uint32_t* mask, int64_t mask_rows,
                                 const int32_t* mask_row, void* out, int64_t ldo, int out_type, int32_t* dev_status, void* stream) {
   using namespace tb;
-  if (T < 0 || T > INT_MAX || V < 1 || V > (1 << 24) || ld < V || ldo < V || B < 1 || n_hist < 1 || ldh < 0 || n_bias < 0 ||
+  if (T < 0 || T > INT_MAX || V < 1 || V > (1 << 24) || ld < V || ldo < V || B < 1 || n_hist < 1 || ldh < 0 || ldh > (1 << 28) || n_bias < 0 ||
       n_bias >= INT_MAX || mask_rows < 0)
     return TB_ERR_SHAPE;
   if (!row_start && B != T) return TB_ERR_SHAPE;  // row t is request t's

@@ -115,7 +115,7 @@ def test_logits_adjust_refuses(lib):
     for name in ("x", "row", "hist", "slot", "hl", "pl", "fresh", "rep", "pres", "freq", "bs", "bi", "bv", "mask", "mrow", "out"):
         assert call(**{name: P + 2}) == -6, name
     assert call(x=P + 8) == call(out=Q + 8) == call(tree=P + 4) == -6
-    for bad in (dict(V=0), dict(V=(1 << 24) + 1, ld=1 << 25, ldo=1 << 25), dict(ld=999), dict(ldo=999), dict(T=-1), dict(B=0), dict(nh=0), dict(ldh=-1), dict(nb=-1), dict(mr=-1),
+    for bad in (dict(V=0), dict(V=(1 << 24) + 1, ld=1 << 25, ldo=1 << 25), dict(ld=999), dict(ldo=999), dict(T=-1), dict(B=0), dict(nh=0), dict(ldh=-1), dict(ldh=(1 << 28) + 1), dict(nb=-1), dict(mr=-1),
                 dict(row=None), dict(slot=None, nh=3), dict(mrow=None)):
         assert call(**bad) == -2, bad
     assert call(out=P, kind=1) == call(out=P, ldo=1008) == -2  # in place at another type or distance

@@ -69,7 +69,9 @@ def check(got, x, a, b, scale, rank, rows, adapter, y):
     ([1], [0], 1, 16, 5120, 17408, False), ([1], [-1], 1, 8, 64, 64, False), ([1] * 5, [2, 2, 0, -1, 2], 3, 8, 8, 8, True), ([1] * 64, None, 40, 32, 2048, 1032, True),
     ([3, 0, 17, 1, 8], [1, 0, 1, 0, -1], 2, 24, 1000, 520, False), ([16, 16, 1], [0, 0, 0], 1, 64, 328, 4096, False), ([129, 5, 260], [1, 3, 1], 4, 64, 520, 264, True),
     ([700], [0], 2, 16, 5120, 1288, False), ([40, 300, 90, 1], [2, 0, -1, 2], 3, 128, 264, 776, True), ([33], [0], 1, 256, 5000, 72, False), ([500], [1], 2, 40, 40, 136, True),
-    ([1000, 7], [0, 1], 2, 200, 128, 1000, True), ([2], [0], 1, 8, 17408, 5120, False)])
+    ([1000, 7], [0, 1], 2, 200, 128, 1000, True), ([2], [0], 1, 8, 17408, 5120, False),
+    ([250, 6], [1, 0], 2, 24, 72, 2000, True), ([250, 7], [1, 0], 2, 24, 72, 2000, True), ([128, 128, 1, 0, 129], [0, 1, 0, 1, -1], 2, 56, 5120, 64, True),
+    ([400, 3], [0, 1], 2, 256, 2048, 72, False)])
 @pytest.mark.parametrize("place", ["out", "in"])
 def test_adapters_match(lens, adapter, n, R, K, N, ranks, place):
     rng = np.random.default_rng(len(lens) * 1000 + K + N)

@@ -153,6 +153,22 @@ def test_counts_above_sixteen_bits():
     assert st == 0 and got[0, 7] == 1 - 0.125 * (n // 2 - 1) and got[0, 8] == 1 - 0.125 * (n // 2 - 2) and got[0, 9] == 1
 
 
+@pytest.mark.parametrize("V,biased", [(300007, 0), (40000, 40000), (248320, 5000)])
+def test_every_token_in_the_history(V, biased):
+    """More different tokens than the tables of a request's CTAs take at once."""
+    rng = np.random.default_rng(V)
+    c = case(rng, [2, 1], V, 2 * V, 1, fresh=True)
+    for r in range(c["history"].shape[0]):
+        c["history"][r] = rng.permutation(np.concatenate([np.arange(V), rng.integers(0, V, V)]))
+    c["hist_len"][:] = [2 * V, V + V // 2]
+    c["prompt_len"][:] = [V // 3, V]
+    if biased:
+        c["biases"] = [[(int(v), float(i % 7) - 3) for i, v in enumerate(rng.permutation(V)[:biased])], []]
+    got, st = run(c, V, torch.float32)
+    assert st == 0
+    same(got, expect(c, V, np.float32))
+
+
 def test_what_does_not_fit_is_left_out_and_flagged():
     import ternary_hadamard_rotated_gb300 as tb
 
