@@ -52,14 +52,14 @@ TB_DEVI int live_rank(const AdapterArgs& a, int g) {
 }
 
 TB_DEVI void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // the same with no sum before it
 TB_DEVI void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) adapter_down_many_kernel(cons
   constexpr int S = many_stages(N), kStageBytes = (kManyRows + N) * 128, kCols = N < 32 ? 32 : N, kPitch = N + 4;
   constexpr uint32_t kInstr = 1u << 4 | (uint32_t)(N / 8) << 17 | (uint32_t)(kManyRows / 16) << 24;  // fp16 operands, fp32 sums
   static_assert(kManyRows * kPitch * 4 <= S * kStageBytes, "the sums take the stages' place");
-  extern __shared__ __align__(1024) unsigned char down_smem[];
+  extern __shared__ __align__(1024) unsigned char tile_smem[];
   __shared__ uint64_t full[S], empty[S], done;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int aborted;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) adapter_down_many_kernel(cons
   if (tile >= a.plan->tiles[a.down_kind]) return;  // (all CTAs of the cluster)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = blockIdx.y * N, live = live_rank(a, t.adapter);
-  unsigned char* const stages = down_smem + ((1024 - (smem_u32(down_smem) & 1023)) & 1023);
+  unsigned char* const stages = tile_smem + ((1024 - (smem_u32(tile_smem) & 1023)) & 1023);
   const uint32_t base = smem_u32(stages);
   const int steps = (a.K + 63) >> 6, mine = r0 < live ? (steps - share + a.cluster - 1) / a.cluster : 0;
   if (tid == 0) {
@@ -541,8 +541,12 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               mma_16816(acc[q], w[2 * q][2 * m], w[2 * q + 1][2 * m], w[2 * q][2 * m + 1], w[2 * q + 1][2 * m + 1], lo[n][2 * m], lo[n][2 * m + 1]);
-              mma_16816(acc[q], w[2 * q][2 * m], w[2 * q + 1][2 * m], w[2 * q][2 * m + 1], w[2 * q + 1][2 * m + 1], hi[n][2 * m], hi[n][2 * m + 1]);
             }
+#pragma unroll
+          for (int m = 0; m < kMma; ++m)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              mma_16816(acc[q], w[2 * q][2 * m], w[2 * q + 1][2 * m], w[2 * q][2 * m + 1], w[2 * q + 1][2 * m + 1], hi[n][2 * m], hi[n][2 * m + 1]);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -565,15 +569,17 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
 }
 
 // ---------------------------------------------------------------- up, many tokens
-// Every CTA takes an equal run of all row tiles' (at most 128 tokens) column tiles of 64, a warp 16 of the tokens.  A
+// Every CTA takes equal runs of all row tiles' (at most 128 tokens) column tiles of 64, back and forth over them, as tiles
+// of few tokens take less time (packed prompts 115 us; 120 with one run a CTA and with four); a warp takes 16 of the tokens.  A
 // thread keeps its tokens' terms as the mma's left operand (of up to 64 ranks; above, they are read again); B's rows come
 // by cp.async three column tiles ahead, and y into a ring of the thread's own with them.  Which column of out is which of the MMAs' columns is free: thread
 // (g, c) has twice 8 neighbouring ones of tokens g and g + 8, so that four threads' y and out are 64 bytes in a row.
-constexpr int kUpThreads = 256, kUpCols = 64;
+constexpr int kUpThreads = 256, kUpCols = 64, kUpRuns = 2;
 constexpr int up_stages(bool multi) { return multi ? 3 : 4; }
 
-// bytes of a row of B in shared memory: an odd number of 32, so that four rows' 32 bytes lie in different banks
-__host__ __device__ constexpr int up_pitch(int R) { return ((R + 15) / 16 | 1) * 32; }
+// bytes of a row of B in shared memory: whole blocks of 16, 32 or 64 ranks, without gaps.  In rows of 128 bytes and more
+// the 16-byte pieces of odd rows are exchanged in fours, so that two rows' 64 bytes lie in different banks
+__host__ __device__ constexpr int up_pitch(int block, int blocks) { return block * blocks * 2; }
 constexpr int kUpY = kUpThreads * 4 * 16;  // bytes of a stage's y
 
 // KS: steps of 16 ranks of a block; MULTI: several blocks
@@ -584,19 +590,26 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const Ad
   if (!plan_fits(a)) return;
   copy_bare(a);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  const int pitch = MULTI ? up_pitch(a.R) : up_pitch(KS * 16);
+  const int pitch = up_pitch(KS * 16, MULTI ? a.blocks : 1);
   const uint32_t base = smem_u32(up_smem), y_ring = base + tid * 16, b_ring = base + S * kUpY, stage_bytes = kUpCols * pitch;
   const int cols = (a.N + kUpCols - 1) / kUpCols;
   const int64_t all = (int64_t)a.plan->tiles[a.up_kind] * cols;
-  int64_t at = all * blockIdx.x / gridDim.x;
-  const int64_t stop = all * (blockIdx.x + 1) / gridDim.x;
   bool waited = false;
-  while (at < stop) {
+  int64_t at = 0, stop = 0;
+  for (int side = 0;;) {
+    if (at >= stop) {
+      if (side == kUpRuns) break;
+      const int64_t run = (int64_t)side * gridDim.x + (side & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), runs = (int64_t)kUpRuns * gridDim.x;
+      at = all * run / runs;
+      stop = all * (run + 1) / runs;
+      ++side;
+      continue;
+    }
     const int tile = (int)(at / cols), begin = (int)(at - (int64_t)tile * cols);
     const int end = (int)(stop - at < cols - begin ? begin + (stop - at) : cols);
     at += end - begin;
     const AdapterTile t = a.up_tiles[tile];
-    const int live = live_rank(a, t.adapter), steps = max(1, (live + 15) >> 4);
+    const int live = live_rank(a, t.adapter), blocks = MULTI ? max(1, (live + KS * 16 - 1) / (KS * 16)) : 1;
     const int p0 = warp * 16 + g;  // the thread's tokens: p0 and p0 + 8 of the tile
     const __half* yp[2];
     __half* op[2];
@@ -607,9 +620,9 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const Ad
       op[i] = a.out + (k >= 0 ? k : 0) * a.ldo + begin * kUpCols + 8 * c;
     }
     // Column 32 q + 8 c + 2 j + i of a tile is column 2 c + i of MMA 4 q + j: its row of B lies at 8 (4 q + j) + 2 c + i.
-    // Zeros behind the rank up to whole steps
+    // Zeros behind the rank up to whole blocks
     const __half* bg = a.b + (int64_t)t.adapter * a.N * a.R;
-    const int pieces = MULTI ? 2 * steps : 2 * KS, more = kUpThreads / pieces, rest = kUpThreads - more * pieces;
+    const int pieces = 2 * KS * blocks, more = kUpThreads / pieces, rest = kUpThreads - more * pieces;
     const int col0 = tid / pieces, piece0 = tid - col0 * pieces;
     auto fetch = [&](int nt, int stage) {
       const int n0 = nt * kUpCols, have = min(kUpCols, a.N - n0);
@@ -622,7 +635,8 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const Ad
       const __half* src = bg + (int64_t)n0 * a.R;
       auto one = [&](int col, int p) {
         const int bytes = col < have ? min(16, max(0, (live - p * 8) * 2)) : 0;
-        cp_async16(st + ((col & 32) + (col >> 1 & 3) * 8 + (col >> 3 & 3) * 2 + (col & 1)) * pitch + p * 16, bytes ? src + col * a.R + p * 8 : a.b, bytes);
+        const int at = (col & 32) + (col >> 1 & 3) * 8 + (col >> 3 & 3) * 2 + (col & 1);
+        cp_async16(st + at * pitch + (KS == 4 ? p ^ (at & 1) << 2 : p) * 16, bytes ? src + col * a.R + p * 8 : a.b, bytes);
       };
       if constexpr (MULTI) {
         for (int col = col0, p = piece0; col < kUpCols;) {
@@ -645,7 +659,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const Ad
     }
     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // h is written
     waited = true;
-    // ranks 16 k + 4 c .. + 3 of a block serve as the k's 2 c, 2 c + 1, 2 c + 8, 2 c + 9; B's are read below alike
+    // 8 neighbouring ranks of 32 (of 16: 4) are a thread's k's of two MMAs (of one), as in `down`; B's are read below alike
     uint32_t hi[KS][4], lo[KS][4];
     float back[2];
     auto terms = [&](int blk) {
@@ -654,14 +668,21 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const Ad
         const int p = p0 + 8 * i;
         const int64_t q = ((int64_t)(t.first + p) * a.blocks + blk);
         back[i] = p < t.count ? a.back[q] : 0.f;
+        auto load = [&](uint32_t (&w)[KS][4], const __half* h) {
+          if constexpr (KS == 1) {
+            const uint2 v = p < t.count ? *reinterpret_cast<const uint2*>(h + 4 * c) : make_uint2(0, 0);
+            w[0][i] = v.x, w[0][i + 2] = v.y;
+          } else {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const __half* h = a.terms + q * 2 * (KS * 16) + 16 * k + 4 * c;
-          const uint2 h2 = p < t.count ? *reinterpret_cast<const uint2*>(h) : make_uint2(0, 0);
-          const uint2 l2 = p < t.count ? *reinterpret_cast<const uint2*>(h + KS * 16) : make_uint2(0, 0);
-          hi[k][i] = h2.x, hi[k][i + 2] = h2.y;
-          lo[k][i] = l2.x, lo[k][i + 2] = l2.y;
-        }
+            for (int k = 0; k < KS; k += 2) {
+              const uint4 v = p < t.count ? *reinterpret_cast<const uint4*>(h + 16 * k + 8 * c) : make_uint4(0, 0, 0, 0);
+              w[k][i] = v.x, w[k][i + 2] = v.y;
+              w[k + 1][i] = v.z, w[k + 1][i + 2] = v.w;
+            }
+          }
+        };
+        load(hi, a.terms + q * 2 * (KS * 16));
+        load(lo, a.terms + q * 2 * (KS * 16) + KS * 16);
       }
     };
     if (!MULTI) terms(0);
@@ -671,24 +692,42 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const Ad
       __syncthreads();  // tile nt is there, and tile nt - 1 has been used
       if (nt + S - 1 < end) fetch(nt + S - 1, stage == 0 ? S - 1 : stage - 1);
       asm volatile("cp.async.commit_group;" ::: "memory");
-      const uint32_t st = b_ring + stage * stage_bytes + g * pitch + c * 8;
+      const uint32_t st = b_ring + stage * stage_bytes + g * pitch, swap = KS == 4 ? (g & 1) << 6 : 0;
       const int left = a.N - nt * kUpCols - 8 * c;
       if (warp * 16 < t.count) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {  // MMAs 4 q .. + 3: columns 32 q + 8 c .. + 7
           float sum[4][4];
-          for (int blk = 0; blk < (MULTI ? (steps + KS - 1) / KS : 1); ++blk) {
+          for (int blk = 0; blk < blocks; ++blk) {
             if (MULTI) terms(blk);
             float acc[4][4];
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              if (k && blk * KS + k >= steps) break;
+            auto step = [&](int k, const uint2 (&b)[4]) {
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const uint2 b = ld_shared_v2(st + (4 * q + j) * 8 * pitch + (blk * KS + k) * 32);
-                if (k == 0) mma_16816_first(acc[j], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b.x, b.y);
-                else mma_16816(acc[j], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b.x, b.y);
-                mma_16816(acc[j], hi[k][0], hi[k][1], hi[k][2], hi[k][3], b.x, b.y);
+                if (k == 0) mma_16816_first(acc[j], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b[j].x, b[j].y);
+                else mma_16816(acc[j], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b[j].x, b[j].y);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma_16816(acc[j], hi[k][0], hi[k][1], hi[k][2], hi[k][3], b[j].x, b[j].y);
+            };
+            const uint32_t row = st + 4 * q * 8 * pitch + blk * KS * 32;
+            if constexpr (KS == 1) {
+              uint2 b[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) b[j] = ld_shared_v2(row + j * 8 * pitch + c * 8);
+              step(0, b);
+            } else {
+#pragma unroll
+              for (int k = 0; k < KS; k += 2) {
+                if (k && (blk * KS + k) * 16 >= live) break;
+                uint2 b[2][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const uint4 v = ld_shared_v4(row + j * 8 * pitch + ((k * 32 + c * 16) ^ swap));
+                  b[0][j] = make_uint2(v.x, v.y), b[1][j] = make_uint2(v.z, v.w);
+                }
+                step(k, b[0]);
+                step(k + 1, b[1]);
               }
             }
 #pragma unroll
@@ -851,7 +890,7 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
 #undef TB_UP
       if (rc != TB_OK) return rc;
     } else {
-      const size_t smem = (size_t)up_stages(R > 64) * (kUpY + kUpCols * up_pitch(R <= 64 ? rank_block(R) : (int)R));
+      const size_t smem = (size_t)up_stages(R > 64) * (kUpY + kUpCols * up_pitch(g.block, g.blocks));
       const int64_t ctas = up * ((N + kUpCols - 1) / kUpCols);
       const dim3 some((unsigned)(ctas < 2 * f.sms ? ctas : 2 * f.sms));
 #define TB_UP(KS, MULTI)                                                                                                           \
