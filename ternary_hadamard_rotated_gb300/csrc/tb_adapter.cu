@@ -410,7 +410,10 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
   constexpr int kItem = kUpFewThreads * (4 * W * 2 + 4 * 8);
   extern __shared__ __align__(16) unsigned char up_few_smem_[];
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  if (!plan_fits(a)) return;
+  if (!plan_fits(a)) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   copy_bare(a);
   const int units = (a.N + 31) / 32;
   const int64_t all = (int64_t)a.plan->tiles[a.up_kind] * units;
@@ -566,6 +569,7 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // no launch is over before the one it began beside
 }
 
 // ---------------------------------------------------------------- up, many tokens
@@ -587,7 +591,10 @@ template <int KS, bool MULTI>
 __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const AdapterArgs a) {
   constexpr int S = up_stages(MULTI);
   extern __shared__ __align__(128) unsigned char up_smem[];
-  if (!plan_fits(a)) return;
+  if (!plan_fits(a)) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   copy_bare(a);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int pitch = up_pitch(KS * 16, MULTI ? a.blocks : 1);
@@ -760,6 +767,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const Ad
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // no launch is over before the one it began beside
 }
 
 template <typename... Args>

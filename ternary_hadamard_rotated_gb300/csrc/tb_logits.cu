@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) logits_move_kernel(const Logi
 // ---------------------------------------------------------------- counted and biased tokens
 // A CTA takes a request's tokens whose mixed numbers end in its part's; a part has about `part_tokens` of the history, so
 // that its table is nearly never too full.  Where it is, its tokens are done in two halves by the next bit, and so on.
-constexpr int kFixThreads = 512, kTable = 4096, kMostTokens = 3072;
+constexpr int kFixThreads = 512, kTable = 4096, kMostTokens = kTable / 4 * 3;
 constexpr int kRows = 64;    // of a request at a time
 constexpr int kResults = 4096;
 constexpr uint32_t kNoResult = 0xffffdeadu;  // (a NaN that no operation gives)
@@ -263,10 +263,13 @@ __global__ void __launch_bounds__(kFixThreads, 3) logits_fix_kernel(const Logits
     for (int i = tid; i < b; i += kFixThreads) wrong |= __ldg(a.row_start + i) > first;
     if (__syncthreads_or(wrong)) {
       if (tid == 0) set_status(a.status, TB_DEV_BAD_LEN);
-      return;
+      end = first;
     }
   }
-  if (first >= end) return;
+  if (first >= end) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // this launch is not over before the first
+    return;
+  }
   const int drafts = a.fresh ? min(end - first, kDrafts) : 0;
   if (a.fresh && end - first > kDrafts) bad |= TB_DEV_BAD_LEN;
   if (tid < drafts) s.draft[tid] = __ldg(a.fresh + first + tid);
