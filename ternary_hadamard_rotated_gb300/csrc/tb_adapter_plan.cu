@@ -70,6 +70,8 @@ TB_DEVI int block_max(int v, int* warps) {  // inclusive maximum, the same way
 // Every CTA groups all requests itself (they are few, and no CTA then waits for another); what is written is
 // shared out.  A request counts where no row start before it is above its own and it ends at or before T: such
 // requests never overlap, so their tokens are T at most, whatever the row starts hold.
+// Bound by latency (count, sums over adapters, order): 64 requests of one token 6.3 us, 13 prompts of 5935 7.7, 1000 of
+// 100000 15.2.
 __global__ void __launch_bounds__(kGroupThreads) adapter_plan_kernel(const GroupArgs a) {
   extern __shared__ int32_t group_smem[];
   int32_t* start = group_smem;              // [n + 2] tokens, then where a group begins in `order`
