@@ -234,3 +234,40 @@ def test_weights_past_two_to_the_31_elements():
     got = yd.cpu().numpy()
     check(got[:2], x[:2], small, b, scale, None, [0, 2], [0], y[:2])
     assert np.array_equal(got[2], y[2])
+
+
+@pytest.mark.parametrize("lens", [[4, 4, 4], [700, 1, 30]])
+def test_a_plan_of_another_step_in_its_own_buffer(lens):
+    import ternary_hadamard_rotated_gb300 as tb
+
+    rng = np.random.default_rng(10)
+    ad, bd, xd, yd, sd = dev(*make(rng, 2, 8, 64, 40, sum(lens)))
+    for small in (Step([1, 1], [0, 1], 2), Step(lens, [0, 1, 1], 3)):  # of fewer tokens, in fewer bytes; of more adapters
+        step = Step(lens, [0, 1, 0], 2)
+        step.plan = small.plan
+        out = torch.full_like(yd, 3.0)
+        step(xd, ad, bd, sd, yd, out=out)
+        assert int(step.status) == tb.TB_DEV_BAD_PLAN and (out == 3).all()
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_steps_one_after_another_in_the_same_plan(T):
+    """Steps with and without adapters in turn, each with its plan written over the one before it."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    rng = np.random.default_rng(11)
+    n, R, K, N, count = 5, 16, 512, 264, 24
+    a, b, x, y, scale = make(rng, n, R, K, N, T)
+    ad, bd, xd, yd, sd = dev(a, b, x, y, scale)
+    lens = [T - 12, 3, 9]
+    rows = dev(starts(lens))[0]
+    adapters = [[-1, -1, -1] if i % 2 else [int(v) for v in rng.integers(-1, n, 3)] for i in range(count)]
+    ids = [dev(np.array(g, dtype=np.int32))[0] for g in adapters]
+    plan = torch.empty(tb.tb_adapter_plan_size(T, n), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(tb.tb_adapter_linear_workspace_size(T, n, K, N, R), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(yd) for _ in range(count)]
+    for g, out in zip(ids, outs):
+        tb.tb_adapter_plan(rows, g, T, n, plan)
+        tb.tb_adapter_linear(xd, ad, bd, sd, plan, yd, ws, out=out)
+    for g, out in zip(adapters, outs):
+        check(out.cpu().numpy(), x, a, b, scale, None, starts(lens), g, y)

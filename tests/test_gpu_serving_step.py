@@ -183,3 +183,37 @@ def test_example_logits():
             one = layers.next_logits(x, [history[b] + path], [[2, 1][b]], lens=[5], **{k: v[b: b + 1] for k, v in pen.items()})
             assert torch.equal(one[row], got[row])
             row += 1
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Each operator on two streams at a time, with outputs and workspaces of their own and the same plans."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    randn = lambda *s: torch.randn(*s, generator=gen, device="cuda").half()  # noqa: E731
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    T, K, N, R, V = 900, 640, 512, 64, 50000
+    turns = torch.empty(tb.tb_rotary_plan_size(64), dtype=torch.uint8, device="cuda")
+    tb.tb_rotary_plan(turns, 64)
+    grouped = torch.empty(tb.tb_adapter_plan_size(T, 3), dtype=torch.uint8, device="cuda")
+    tb.tb_adapter_plan(ints(0, 300, 700, 900), ints(2, 0, 1), T, 3, grouped)
+    q, k, pos = randn(T, 8, 128), randn(T, 2, 128), torch.arange(T, dtype=torch.int32, device="cuda")
+    x, y, a, b, scale = randn(T, K), randn(T, N), randn(3, R, K) * 0.05, randn(3, N, R), torch.ones(3, device="cuda")
+    logits, history = randn(20, V), torch.randint(0, V, (20, 9000), generator=gen, dtype=torch.int32, device="cuda")
+    lengths, rate = torch.full((20,), 9000, dtype=torch.int32, device="cuda"), torch.rand(20, generator=gen, device="cuda")
+    outs = []
+    for _ in range(3):
+        ws = torch.empty(tb.tb_adapter_linear_workspace_size(T, 3, K, N, R), dtype=torch.uint8, device="cuda")
+        outs.append((torch.empty_like(q), torch.empty_like(k), torch.empty_like(y), torch.empty(20, V, device="cuda"), ws))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(), None]
+    torch.cuda.synchronize()
+    for s, o in zip(streams, outs):
+        if s is None:
+            torch.cuda.synchronize()  # the last by itself
+        tb.tb_adapter_linear(x, a, b, scale, grouped, y, o[4], out=o[2], stream=s)
+        tb.tb_logits_adjust(logits, o[3], history, lengths, frequency=rate, stream=s)
+        tb.tb_rotary(q, k, pos, turns, 64, tb.TB_ROTARY_HALF, o[0], o[1], stream=s)
+    torch.cuda.synchronize()
+    for o in outs[:2]:
+        for mine, alone in zip(o[:4], outs[2]):
+            assert torch.equal(mine, alone)
