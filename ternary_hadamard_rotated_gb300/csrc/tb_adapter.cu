@@ -47,7 +47,7 @@ TB_DEVI bool plan_fits(const AdapterArgs& a) {
 }
 
 TB_DEVI int live_rank(const AdapterArgs& a, int g) {
-  const int r = a.rank ? __ldg(a.rank + g) : a.R;
+  const int r = a.rank ? a.rank[g] : a.R;
   return r < 0 ? 0 : min(r, a.R);
 }
 
@@ -88,7 +88,7 @@ TB_DEVI float up_scale(float top, float& back) {
 template <int PARTS, int M, int N, int PITCH, int THREADS>
 TB_DEVI void join_down(const AdapterArgs& a, const AdapterTile& t, float* part, int share, int r0, int live) {
   const int tid = threadIdx.x, lane = tid & 31;
-  const float scale = __ldg(a.scale + t.adapter);
+  const float scale = a.scale[t.adapter];
   if constexpr (PARTS > 1) {
     __syncthreads();
     for (int e = tid; e < M * PITCH; e += THREADS) {
@@ -156,6 +156,7 @@ template <int NT>
 __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_few_kernel(const AdapterArgs a) {
   constexpr int N = NT * 8, S = few_stages(NT);
   extern __shared__ __align__(128) unsigned char down_smem[];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before is over (see launch_early), for the second launch too
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tile = blockIdx.x / a.cluster, share = blockIdx.x - tile * a.cluster;
   if (!plan_fits(a)) {
@@ -250,6 +251,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) adapter_down_many_kernel(cons
   __shared__ uint64_t full[S], empty[S], done;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int aborted;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before is over (see launch_early), for the second launch too
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tile = blockIdx.x / a.cluster, share = blockIdx.x - tile * a.cluster;
   if (!plan_fits(a)) {
@@ -774,7 +776,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const Ad
 }
 
 template <typename... Args>
-static cudaError_t launch(void (*fn)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster, bool dependent, Args... args) {
+static cudaError_t launch(void (*fn)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
@@ -788,11 +790,9 @@ static cudaError_t launch(void (*fn)(Args...), dim3 grid, int threads, size_t sm
     at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
     ++n;
   }
-  if (dependent) {
-    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
+  at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[n].val.programmaticStreamSerializationAllowed = 1;
+  ++n;
   cfg.attrs = at;
   cfg.numAttrs = (unsigned)n;
   return cudaLaunchKernelEx(&cfg, fn, args...);
@@ -876,11 +876,11 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
 #define TB_DOWN_FEW(NT)                                                                                                         \
   ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_down_few_kernel<NT>), f.device, down_few_smem<NT>())) != TB_OK \
        ? cudaErrorUnknown                                                                                                       \
-       : launch(adapter_down_few_kernel<NT>, grid, kDownThreads, (size_t)down_few_smem<NT>(), s, g.cluster, false, g))
+       : launch(adapter_down_few_kernel<NT>, grid, kDownThreads, (size_t)down_few_smem<NT>(), s, g.cluster, g))
 #define TB_DOWN_MANY(N)                                                                                                        \
   ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_down_many_kernel<N>), f.device, down_many_smem<N>())) != TB_OK \
        ? cudaErrorUnknown                                                                                                      \
-       : launch(adapter_down_many_kernel<N>, grid, kManyThreads, (size_t)down_many_smem<N>(), s, g.cluster, false, g))
+       : launch(adapter_down_many_kernel<N>, grid, kManyThreads, (size_t)down_many_smem<N>(), s, g.cluster, g))
   if (few)
     e = nt == 2 ? TB_DOWN_FEW(2) : nt == 4 ? TB_DOWN_FEW(4) : TB_DOWN_FEW(8);
   else
@@ -896,7 +896,7 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
 #define TB_UP(W, MULTI)                                                                                                            \
   ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_up_few_kernel<W, MULTI>), f.device, up_few_smem<W>())) != TB_OK \
        ? cudaErrorUnknown                                                                                                          \
-       : launch(adapter_up_few_kernel<W, MULTI>, some, kUpFewThreads, (size_t)up_few_smem<W>(), s, 1, true, g))
+       : launch(adapter_up_few_kernel<W, MULTI>, some, kUpFewThreads, (size_t)up_few_smem<W>(), s, 1, g))
       e = R <= 16 ? TB_UP(4, false) : R <= 32 ? TB_UP(8, false) : R <= 64 ? TB_UP(16, false) : TB_UP(16, true);
 #undef TB_UP
       if (rc != TB_OK) return rc;
@@ -907,7 +907,7 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
 #define TB_UP(KS, MULTI)                                                                                                           \
   ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_up_many_kernel<KS, MULTI>), f.device, (int)smem)) != TB_OK \
        ? cudaErrorUnknown                                                                                                          \
-       : launch(adapter_up_many_kernel<KS, MULTI>, some, kUpThreads, smem, s, 1, true, g))
+       : launch(adapter_up_many_kernel<KS, MULTI>, some, kUpThreads, smem, s, 1, g))
       e = R <= 16 ? TB_UP(1, false) : R <= 32 ? TB_UP(2, false) : R <= 64 ? TB_UP(4, false) : TB_UP(4, true);
 #undef TB_UP
       if (rc != TB_OK) return rc;

@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_plan_kernel(const Group
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = a.n + 1;
   int bad = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before is over (see launch_early)
   for (int i = tid; i < a.n + 2; i += kGroupThreads) start[i] = 0;
   if (tid == 0) highest = 0;
   __syncthreads();
@@ -90,9 +91,9 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_plan_kernel(const Group
     const int b = b0 + tid;
     int s = INT_MIN, e = INT_MIN, g = 0;
     if (b < a.B) {
-      s = __ldg(a.row_start + b);
-      e = __ldg(a.row_start + b + 1);
-      g = __ldg(a.adapter + b);
+      s = a.row_start[b];
+      e = a.row_start[b + 1];
+      g = a.adapter[b];
     }
     const int top = max(block_max(s, warps), highest);
     if (b < a.B) {
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_plan_kernel(const Group
   // between warps in turn (start[g] moves on as the group's requests are placed)
   for (int b0 = 0; b0 < a.B; b0 += kGroupThreads) {
     const int b = b0 + tid, g = b < a.B ? at[b] : -1;
-    const int len = g >= 0 ? __ldg(a.row_start + b + 1) - __ldg(a.row_start + b) : 0;
+    const int len = g >= 0 ? a.row_start[b + 1] - a.row_start[b] : 0;
     int before = 0, all = 0;
 #pragma unroll
     for (int l = 0; l < 32; ++l) {
@@ -183,16 +184,16 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_plan_kernel(const Group
   for (int b = warp_all; b < a.B; b += n_warps) {
     const int p = at[b];
     if (p < 0) continue;
-    const int s = __ldg(a.row_start + b), len = __ldg(a.row_start + b + 1) - s;
+    const int s = a.row_start[b], len = a.row_start[b + 1] - s;
     if (len <= kLongRequest)
       for (int i = lane; i < len; i += 32) a.order[p + i] = s + i;
   }
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
-    const bool is_long = b < a.B && at[b] >= 0 && __ldg(a.row_start + b + 1) - __ldg(a.row_start + b) > kLongRequest;
+    const bool is_long = b < a.B && at[b] >= 0 && a.row_start[b + 1] - a.row_start[b] > kLongRequest;
     for (unsigned m = __ballot_sync(0xffffffffu, is_long); m; m &= m - 1) {
       const int c = b0 + __ffs(m) - 1;
-      const int s = __ldg(a.row_start + c), len = __ldg(a.row_start + c + 1) - s;
+      const int s = a.row_start[c], len = a.row_start[c + 1] - s;
       for (int i = blockIdx.x * kGroupThreads + tid; i < len; i += gridDim.x * kGroupThreads) a.order[at[c] + i] = s + i;
     }
   }
@@ -233,6 +234,5 @@ extern "C" int tb_adapter_plan(const int32_t* row_start, const int32_t* adapter,
   a.n = (int)n;
   int64_t blocks = (T > B * 32 ? T : B * 32) / kGroupThreads + 1;
   if (blocks > f.sms) blocks = f.sms;
-  adapter_plan_kernel<<<(int)blocks, kGroupThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
-  return check_launch();
+  return launch_early(adapter_plan_kernel, dim3((unsigned)blocks), kGroupThreads, (size_t)smem, static_cast<cudaStream_t>(stream), a);
 }

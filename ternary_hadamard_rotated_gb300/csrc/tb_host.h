@@ -65,4 +65,27 @@ int device_facts(DeviceFacts* f);
 // costs host time that a stream of small launches does not hide)
 int ensure_dynamic_smem(const void* func, int device, int bytes);
 
+// A launch whose CTAs may be set up while the kernel before it ends (2.5 us of a row of calls): the kernel has to wait
+// (griddepcontrol.wait) before it reads or writes any memory of the caller's, and reads none of it by __ldg, which may
+// assume that it does not change while the kernel is there.
+template <typename... P, typename... A>
+inline int launch_early(void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, P(args)...);
+  if (e != cudaSuccess) {
+    record_cuda_error(e);
+    return TB_ERR_CUDA;
+  }
+  return check_launch();
+}
+
 }  // namespace tb

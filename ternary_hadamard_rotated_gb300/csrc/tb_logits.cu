@@ -81,13 +81,13 @@ TB_DEVI bool row_counts(const LogitsArgs& a, int t, int* found) {
   if (threadIdx.x == 0) *found = a.B;
   __syncthreads();
   for (int b = threadIdx.x; b < a.B; b += blockDim.x)
-    if (__ldg(a.row_start + b) <= t && t < __ldg(a.row_start + b + 1)) atomicMin(found, b);
+    if (a.row_start[b] <= t && t < a.row_start[b + 1]) atomicMin(found, b);
   __syncthreads();
   const int b = *found;
   if (b == a.B) return false;
-  const int first = __ldg(a.row_start + b);
-  bool wrong = first < 0 || __ldg(a.row_start + b + 1) > a.T;
-  for (int i = threadIdx.x; i < b; i += blockDim.x) wrong |= __ldg(a.row_start + i) > first;
+  const int first = a.row_start[b];
+  bool wrong = first < 0 || a.row_start[b + 1] > a.T;
+  for (int i = threadIdx.x; i < b; i += blockDim.x) wrong |= a.row_start[i] > first;
   return !__syncthreads_or(wrong);
 }
 
@@ -117,6 +117,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) logits_move_kernel(const Logi
   static_assert(kStage == K * (kPiece + kMoveThreads * 4), "pieces, then words");
   extern __shared__ __align__(16) unsigned char logits_smem[];
   __shared__ int found;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before is over (see launch_early), for the second launch too
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
   const uint32_t ring = smem_u32(logits_smem);
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) logits_move_kernel(const Logi
     int t, chunk;
   };
   auto mask_of = [&](int t) -> const uint32_t* {
-    const int64_t m = !a.mask ? -1 : a.mask_row ? __ldg(a.mask_row + t) : t;
+    const int64_t m = !a.mask ? -1 : a.mask_row ? a.mask_row[t] : t;
     return m >= 0 && m < a.mask_rows ? a.mask + m * mask_words : nullptr;
   };
   Cursor f;  // what is fetched next, and what is stored next
@@ -486,7 +487,8 @@ extern "C" int tb_logits_adjust(const uint16_t* logits, int64_t ld, int64_t T, i
     const int ring = kMoveStages * (half ? move_stage<__half>() : move_stage<float>());
     rc = ensure_dynamic_smem(reinterpret_cast<const void*>(move), f.device, ring);
     if (rc != TB_OK) return rc;
-    move<<<(unsigned)(units < most ? units : most), kMoveThreads, ring, s>>>(a);
+    rc = launch_early(move, dim3((unsigned)(units < most ? units : most)), kMoveThreads, (size_t)ring, s, a);
+    if (rc != TB_OK) return rc;
   }
   void (*fix)(const LogitsArgs) = half ? logits_fix_kernel<__half> : logits_fix_kernel<float>;
   const int smem = n_bias ? (int)sizeof(FixShared) : (int)offsetof(FixShared, bias);

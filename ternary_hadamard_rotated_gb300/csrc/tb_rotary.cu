@@ -117,6 +117,7 @@ constexpr int kRotaryAngles = 2048;  // (token, pair) angles a CTA holds: 16 KB
 template <bool WIDE>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs a) {
   __shared__ __align__(16) float cosines[kRotaryAngles], sines[kRotaryAngles];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before is over (see launch_early)
   if (a.plan->magic != kRotaryMagic || a.plan->R != a.R) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(a.status, TB_DEV_BAD_PLAN);
     return;
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
     __syncthreads();  // the tile before has been read
     for (int i = threadIdx.x; i < n * half; i += kRotaryThreads) {
       const int t = i / half;
-      const unsigned long long at = (unsigned long long)(long long)__ldg(a.pos + t0 + t) * turns[i - t * half];
+      const unsigned long long at = (unsigned long long)(long long)a.pos[t0 + t] * turns[i - t * half];
       float s, c;
       sincospif(__ll2float_rn((long long)at) * 0x1p-63f, &s, &c);
       cosines[i] = amp * c;
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
       const int64_t tok = t0 + t;
       int64_t slot = -1;
       if (a.slots && r >= row_q) {
-        slot = __ldg(a.slots + tok);
+        slot = a.slots[tok];
         if (slot >= a.n_slots) {
           set_status(a.status, TB_DEV_BAD_SLOT);
           slot = -1;
@@ -239,6 +240,7 @@ template <int L, bool PAIRS>
 __global__ void __launch_bounds__(kRowsThreads, 4) rotary_rows_kernel(const RotaryArgs a) {
   constexpr int D = L * 8, kRows = 32 / L, kAhead = 4;
   extern __shared__ __align__(16) float row_angles[];  // of each warp: cosines [R/2], sines [R/2]
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before is over (see launch_early)
   if (a.plan->magic != kRotaryMagic || a.plan->R != a.R) {
     if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, TB_DEV_BAD_PLAN);
     return;
@@ -270,14 +272,14 @@ __global__ void __launch_bounds__(kRowsThreads, 4) rotary_rows_kernel(const Rota
     for (int i = 0; i < kAhead; ++i) x[i] = load(begin + i * kRows + lane / L);
     int64_t slot = -1;
     if (a.slots) {
-      slot = __ldg(a.slots + t);
+      slot = a.slots[t];
       if (slot >= a.n_slots) {
         if (lane == 0) set_status(a.status, TB_DEV_BAD_SLOT);
         slot = -1;
       }
     }
     const int64_t place = slot < 0 ? 0 : (((slot >> a.page_log2) * a.Hk << a.page_log2) + (slot & ((1ll << a.page_log2) - 1))) * D + c * 8;
-    const unsigned long long pos = (unsigned long long)(long long)__ldg(a.pos + t);
+    const unsigned long long pos = (unsigned long long)(long long)a.pos[t];
     __syncwarp();
     for (int i = lane; i < half; i += 32) {
       float sn, cs;
@@ -374,8 +376,7 @@ static int launch_rotary(RotaryArgs a, cudaStream_t stream) {
     const int smem = kRowsWarps * a.R * 4;
     void (*fn)(const RotaryArgs) = a.pairs ? (per == 8 ? rotary_rows_kernel<8, true> : per == 16 ? rotary_rows_kernel<16, true> : rotary_rows_kernel<32, true>)
                                            : (per == 8 ? rotary_rows_kernel<8, false> : per == 16 ? rotary_rows_kernel<16, false> : rotary_rows_kernel<32, false>);
-    fn<<<(unsigned)ctas, kRowsThreads, smem, stream>>>(a);
-    return check_launch();
+    return launch_early(fn, dim3((unsigned)ctas), kRowsThreads, smem, stream, a);
   }
   a.tile = kRotaryAngles / (a.R / 2);
   if (a.tile > 8) a.tile = 8;
@@ -388,11 +389,7 @@ static int launch_rotary(RotaryArgs a, cudaStream_t stream) {
   if (a.split > most) a.split = most;
   if (tiles > ctas) tiles = ctas;
   const dim3 grid((unsigned)tiles, (unsigned)a.split);
-  if (wide)
-    rotary_kernel<true><<<grid, kRotaryThreads, 0, stream>>>(a);
-  else
-    rotary_kernel<false><<<grid, kRotaryThreads, 0, stream>>>(a);
-  return check_launch();
+  return launch_early(wide ? rotary_kernel<true> : rotary_kernel<false>, grid, kRotaryThreads, 0, stream, a);
 }
 
 // q, k and the plan, as both entry points take them

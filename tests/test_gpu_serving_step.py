@@ -217,3 +217,63 @@ def test_two_calls_at_once_on_two_streams():
     for o in outs[:2]:
         for mine, alone in zip(o[:4], outs[2]):
             assert torch.equal(mine, alone)
+
+
+def test_calls_behind_copies_kernels_and_other_streams():
+    """Each first launch may be set up before what is in front of it is over: its inputs are written by a copy, by a kernel, by
+    a kernel of another stream that is waited for, and by the operators themselves, one after another and in a graph."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    randn = lambda *s: torch.randn(*s, generator=gen, device="cuda").half()  # noqa: E731
+    T, K, N, R, V = 300, 512, 4096, 16, 4096
+    turns = torch.empty(tb.tb_rotary_plan_size(64), dtype=torch.uint8, device="cuda")
+    tb.tb_rotary_plan(turns, 64)
+    a, b, scale = randn(3, R, K) * 0.05, randn(3, N, R), torch.ones(3, device="cuda")
+    rows = torch.tensor([0, 100, 200, 300], dtype=torch.int32, device="cuda")
+    history, lengths = torch.randint(0, V, (T, 50), generator=gen, dtype=torch.int32, device="cuda"), torch.full((T,), 50, dtype=torch.int32, device="cuda")
+    rate = torch.rand(T, generator=gen, device="cuda")
+    sources = [(randn(T, K), randn(T, N), torch.tensor(ids, dtype=torch.int32, device="cuda"), torch.randint(0, 9999, (T,), generator=gen, dtype=torch.int32, device="cuda"))
+               for ids in ([0, 1, 2], [2, -1, 0], [1, 1, -1], [0, 2, 0])]
+    x, y, ids, pos = (torch.zeros_like(m) for m in sources[0])
+    plan = torch.empty(tb.tb_adapter_plan_size(T, 3), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(tb.tb_adapter_linear_workspace_size(T, 3, K, N, R), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step(source, out, settle):
+        now = torch.cuda.current_stream()
+        x.copy_(source[0])
+        torch.add(source[1], 0, out=y)
+        side.wait_stream(now)
+        with torch.cuda.stream(side):
+            pos.copy_(source[3])
+            torch.add(source[2], 0, out=ids)
+        now.wait_stream(side)
+        settle()
+        tb.tb_adapter_plan(rows, ids, T, 3, plan)
+        settle()
+        tb.tb_adapter_linear(x, a, b, scale, plan, y, ws)
+        settle()
+        q = y.view(T, N // 128, 128)
+        tb.tb_rotary(q, None, pos, turns, 64, tb.TB_ROTARY_HALF, q, None)
+        settle()
+        tb.tb_logits_adjust(y[:, :V], out, history, lengths, frequency=rate)
+
+    alone = [torch.empty(T, V, device="cuda") for _ in sources]
+    for s, o in zip(sources, alone):
+        step(s, o, torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    row = [torch.empty(T, V, device="cuda") for _ in sources * 5]
+    for i, o in enumerate(row):
+        step(sources[i % 4], o, lambda: None)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, alone[i % 4]) for i, o in enumerate(row))
+    captured = [torch.empty(T, V, device="cuda") for _ in sources]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for s, o in zip(sources, captured):
+            step(s, o, lambda: None)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(captured, alone))
