@@ -1,7 +1,7 @@
 // Low-rank adapters of many requests beside a shared linear: out[t] = y[t] + scale[g] B[g] (A[g] x[t]), g the
 // adapter of token t's request.
 //
-// Two launches, the second (programmatic) loading what the first does not write before it waits for it:
+// Two launches, the second (programmatic) beside the first, loading what that does not write before it waits for it:
 //   down  h = scale A x, to the workspace in the plan's order; few tokens: mma.sync on tiles of 16 tokens of one adapter;
 //         many: tcgen05 on tiles of 128
 //   up    out = y + B h, mma.sync; few tokens: tiles of 16, bound by the weights, which go from global memory straight
@@ -143,7 +143,7 @@ TB_DEVI void join_down(const AdapterArgs& a, const AdapterTile& t, float* part, 
 // 2c + 8 and 2c + 9 of two MMAs: a product over k does not mind their order, if both operands have the same.  They
 // come by cp.async into a ring of the thread's own, so that several steps are in flight without registers, and no thread
 // waits for another.  Bound by latency (first loads, join over the cluster): 64 tokens of K 5120, ranks up to 32 of 48
-// adapters, 10 MB in 9.7 us; both launches, 47 MB, 19.3 us in a graph, 2.5 TB/s.
+// adapters, 10 MB in 9.7 us; both launches, 47 MB, 19.2 us in a graph, 2.5 TB/s.
 constexpr int kDownThreads = 256, kDownWarps = kDownThreads / 32;
 constexpr int few_stages(int NT) { return NT == 2 ? 5 : NT == 4 ? 4 : 2; }
 template <int NT>
@@ -393,7 +393,7 @@ TB_DEVI void copy_bare(const AdapterArgs& a) {
 // every warp an equal run of all tiles' columns.  Thread (g, c) holds columns n0 + 4 g .. + 3: 8 bytes of y and out a
 // token, and 8 neighbouring elements of each of their rows of B, as in `down`.  The next columns' rows of B and
 // elements of y are on their way while the present ones are used.  64 tokens, N 17408, ranks up to 32 of 48 adapters:
-// 56 MB in 15.2 us by itself, 3.7 TB/s (three CTAs an SM: 24.8 for both launches against 19.3).
+// 56 MB in 15.2 us by itself, 3.7 TB/s (three CTAs an SM: 24.8 for both launches against 19.2).
 constexpr int kUpFewThreads = 256, kUpFewWarps = kUpFewThreads / 32;
 
 // They come by cp.async into a ring of the thread's own.

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) logits_move_kernel(const Logi
 // that its table is nearly never too full.  Where it is, its tokens are done in two halves by the next bit, and so on.
 // Bound by latency: every part reads the whole history (from L2) for its own tokens, counts them, and then a thread's tokens
 // have a chain of a scattered load and a scattered store a row.  64 requests with histories up to 8000, by itself 19.6 us,
-// both launches 25.8 in a graph; nine trees of 5 to 16 drafts behind 2000 to 30000, 31.4 and 42.5: about 13 to count, 10
+// both launches 25.4 in a graph; nine trees of 5 to 16 drafts behind 2000 to 30000, 31.4 and 42.2: about 13 to count, 10
 // to gather the rows' logits, 6 to store them, 3 for the masks.  (With counts of the whole vocabulary in one launch
 // that moves the rows too: 31 to 46, and 46 to 89.)
 constexpr int kFixThreads = 512, kTable = 4096, kMostTokens = kTable / 4 * 3;

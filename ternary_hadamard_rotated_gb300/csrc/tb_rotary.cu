@@ -232,8 +232,8 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
 // from the lane that holds it (neighbours in pairs are in one lane anyway).  A warp takes a token, or a part of its rows
 // where tokens are few: kAhead rows of loads on their way before the angles are made, by all lanes together, a pair at a
 // time, and kept in registers for all of the token's heads.  Bound by the bytes: 12289 tokens of 24/4 heads of 256, 64 of
-// them turned, with the cache's write, 428 MB in 72.6 us, 0.87 of measured HBM; 40001 tokens of 32/8 heads of 128, 819 MB
-// in 126 us, 0.96 (the form for any head: 137 and 147).  Four CTAs an SM: with five the registers spill (88, 137).
+// them turned, with the cache's write, 428 MB in 71.8 us, 0.88 of measured HBM; 40001 tokens of 32/8 heads of 128, 819 MB
+// in 125 us, 0.97 (the form for any head: 137 and 147).  Four CTAs an SM: with five the registers spill (88, 137).
 constexpr int kRowsThreads = 256, kRowsWarps = kRowsThreads / 32;
 
 template <int L, bool PAIRS>
