@@ -559,6 +559,8 @@ def tb_rotary(q, k, pos, plan, R, layout, q_out, k_out, inverse=False, dev_statu
         raise ValueError(f"q and q_out differ in shape: {list(q.shape)} and {list(q_out.shape)}")
     kp, ldk, Hk, kop, ldko = None, 0, 0, None, 0
     if k is not None:
+        if k_out is None:
+            raise ValueError("k is given without k_out")
         ldk, ldko, Hk = _tokens("k", k, f16), _tokens("k_out", k_out, f16), k.shape[1]
         if k.shape != (T, Hk, D) or k_out.shape != k.shape:
             raise ValueError(f"q, k and k_out do not match: {list(q.shape)}, {list(k.shape)}, {list(k_out.shape)}")

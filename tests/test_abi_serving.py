@@ -153,3 +153,13 @@ def test_binding_refuses_what_it_cannot_pass_on():
         with pytest.raises(ValueError):
             call()
             print(i)
+
+
+def test_rotary_of_k_needs_a_place_for_it():
+    import ternary_hadamard_rotated_gb300 as tb
+
+    torch = pytest.importorskip("torch")
+    q = torch.zeros(2, 4, 64, dtype=torch.float16)
+    pos, plan = torch.zeros(2, dtype=torch.int32), torch.zeros(512, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="k_out"):
+        tb.tb_rotary(q, q, pos, plan, 64, tb.TB_ROTARY_HALF, q, None)
