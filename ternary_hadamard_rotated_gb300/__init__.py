@@ -524,13 +524,15 @@ def _here(name, t, stream):
 def _matrix(name, t, dtypes, shape=None):
     """Distance of two rows of t [rows, columns] in elements (of one row alone: its columns); a row's elements
     must be contiguous."""
-    if t.dim() != 2 or t.dtype not in dtypes or (shape is not None and t.shape != shape):
+    got = t.shape
+    if len(got) != 2 or t.dtype not in dtypes or (shape is not None and got != shape):
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))} {'[rows, columns]' if shape is None else list(shape)}, "
-                         f"got {t.dtype} {list(t.shape)}")
+                         f"got {t.dtype} {list(got)}")
     s0, s1 = t.stride()
-    if t.shape[1] > 1 and s1 != 1:
+    rows, columns = got
+    if s1 != 1 and columns > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous, got strides {t.stride()}")
-    return s0 if t.shape[0] > 1 else t.shape[1]
+    return s0 if rows > 1 else columns
 
 
 def tb_rotary_plan_size(R):
