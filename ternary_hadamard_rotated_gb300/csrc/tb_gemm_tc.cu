@@ -54,25 +54,10 @@ TB_DEVI void tma_load_2d(void* dst, const CUtensorMap* tm, int x, int y, uint64_
       : "memory");
 }
 
-// the same box into the shared memory of every CTA of the cluster in `mask` (same offset), each
-// CTA's barrier at `bar`'s offset receiving the complete_tx of its copy
-TB_DEVI void tma_load_2d_mc(void* dst, const CUtensorMap* tm, int x, int y, uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
-      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"(mask)
-      : "memory");
-}
-
 TB_DEVI uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
-}
-
-// every thread of every CTA of the cluster (release / acquire)
-TB_DEVI void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 TB_DEVI void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -90,16 +75,6 @@ TB_DEVI void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_u32(bar))
                : "memory");
-}
-
-// one arrival on the barrier at `bar`'s offset in every CTA of `mask` once this thread's earlier
-// tcgen05 operations are complete
-TB_DEVI void tc_commit_mc(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(mask)
-      : "memory");
 }
 
 TB_DEVI void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -182,14 +157,16 @@ TB_DEVI int sk_owner(int u, int units, int grid) { return (int)(((int64_t)(u + 1
 TB_DEVI int sk_lo(int c, int units, int grid) { return (int)((int64_t)units * c / grid); }
 
 // CS = 1: one CTA per schedule slot.  CS = 2 (two 128-token subtiles): a cluster of two CTAs
-// takes one token tile and k-range on two neighbouring row tiles; each CTA loads one subtile of
-// every activation stage and multicasts it to both, so each SM reads half the activation bytes,
-// and a stage is refilled only when the MMAs of both CTAs have read it.
+// takes one token tile and k-range on two neighbouring row tiles, so that the second read of an
+// activation stage finds it in L2.  Each loads both subtiles itself, by plain copies: nothing
+// passes between the two (loads of one subtile each, multicast to both, took as long: 5120 ->
+// 17408 and 17408 -> 5120 at 4096 tokens 466 and 518 us against 467 and 520; single CTAs 464 and
+// 594).
 template <int NSUB, int BN, int CS>
 __global__ void __launch_bounds__(kTcThreads, 1)
     w2_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                       const TcSkArgs a) {
-  static_assert(CS == 1 || (CS == 2 && NSUB == 2), "a cluster pair shares two token subtiles");
+  static_assert(CS == 1 || (CS == 2 && NSUB == 2), "a cluster pair takes the same two token subtiles");
   using Cfg = TcCfg<NSUB, BN>;
   constexpr int S = Cfg::kStages;
   constexpr int kPartFloats = NSUB * kTcBM * BN;
@@ -234,7 +211,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     aborted = 0;
     for (int s = 0; s < S; ++s) {
       mbar_init(full + s, 1 + 8);
-      mbar_init(empty + s, CS);  // the MMAs of every CTA that reads the stage
+      mbar_init(empty + s, 1);
     }
     mbar_init(accum, 1);
     mbar_init(tfree, 8);  // lane 0 of each of the 8 drain warps
@@ -257,7 +234,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CS > 1) cluster_sync();  // the peer's barriers exist before anything lands in them
   tc_fence_after();
   const uint32_t tmem_d = *tmem_slot;
 
@@ -301,15 +277,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int s = it % S, ph = it / S;
           if (ph > 0) wait(empty + s, (ph - 1) & 1);
           mbar_arrive_expect_tx(full + s, NSUB * kTcABytes);
-          if constexpr (CS == 1) {
 #pragma unroll
-            for (int sub = 0; sub < NSUB; ++sub)
-              tma_load_2d(smem + s * Cfg::kStageBytes + sub * kTcABytes, &tmA, kb * kTcBK,
-                          m0 + sub * kTcBM, full + s);
-          } else {
-            tma_load_2d_mc(smem + s * Cfg::kStageBytes + crank * kTcABytes, &tmA, kb * kTcBK,
-                           m0 + crank * kTcBM, full + s, (uint16_t)((1u << CS) - 1u));
-          }
+          for (int sub = 0; sub < NSUB; ++sub)
+            tma_load_2d(smem + s * Cfg::kStageBytes + sub * kTcABytes, &tmA, kb * kTcBK,
+                        m0 + sub * kTcBM, full + s);
           const int jw = it + kWS;  // the words four k-blocks ahead, once their slot is read
           if (jw < nblk) {
             wait(wempty + jw % kWS, (jw / kWS - 1) & 1);
@@ -317,13 +288,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         u += k1 - k0;
-      }
-      if constexpr (CS > 1) {
-        // the peer's last commits into this CTA's barriers have landed before the cluster exits
-        for (int s = 0; s < S && s < it; ++s) {
-          const int last = it - 1 - ((it - 1 - s) % S);  // the last k-block that used stage s
-          wait(empty + s, (last / S) & 1);
-        }
       }
     }
     __syncwarp();
@@ -347,8 +311,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int sub = 0; sub < NSUB; ++sub)
               tc_mma(tmem_d + sub * BN, umma_desc_sw128(sa + sub * kTcABytes) + 2 * k, bd + 2 * k,
                      Cfg::kIdesc, (kb != k0) || (k != 0));
-          if constexpr (CS > 1) tc_commit_mc(empty + s, (uint16_t)((1u << CS) - 1u));
-          else tc_commit(empty + s);
+          tc_commit(empty + s);
         }
         tc_commit(accum);
         u += k1 - k0;
@@ -669,7 +632,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (CS > 1) cluster_sync();  // nothing of the peer's still lands in this CTA
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_d),
@@ -787,8 +749,8 @@ int launch_gemm_tc_rotated(const __half* xp, int64_t M, int64_t K, const uint32_
   // Tile shape and schedule.  Above 128 tokens: 256 x 256 tiles (two 128-token subtiles share
   // each decoded weight tile, which halves the decode work and the activation reads per flop
   // of smaller tiles; the per-k-block decode then hides behind the k-block's mma), taken by
-  // clusters of two CTAs on neighbouring row tiles that share each activation stage (one
-  // multicast load per CTA) when pairs can be resident; as stream-K over the resident slots
+  // clusters of two CTAs on neighbouring row tiles that read the same activation stages when
+  // pairs can be resident; as stream-K over the resident slots
   // (CTAs or pairs) when every slot gets a tile, one slot per tile when the tiles fill most of
   // the slots, else every tile split into q <= 4 k-ranges.  Up to 128 tokens: 128 x 256 tiles the
   // same way, or 128 x 128 tiles when those keep more SMs busy (the cost of a k-block grows with
