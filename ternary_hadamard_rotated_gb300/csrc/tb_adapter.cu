@@ -7,9 +7,12 @@
 //   up    out = y + B h, mma.sync; few tokens: tiles of 16, bound by the weights, which go from global memory straight
 //         to the registers; many: tiles of 128, bound by y and out
 //
-// h goes from one to the other as fp16 in two terms, h 2^e = hi + lo, with 2^e of the token's own for up to 64 ranks
-// (their largest |h| 2^e in [2^14, 2^15)): 22 bits, of h down to 2^-39 of that largest.  Products and sums are fp32, and
-// 2^-e is applied to each sum.
+// h goes from one to the other as fp16 in two terms, h 2^e = hi + lo 2^-12, with 2^e of the token's own for up to 64 ranks
+// (their largest |h| 2^e in [2^14, 2^15)).  What hi leaves is at most 2^3 there, and less in proportion below, so that lo
+// holds 11 bits more of it wherever hi is a normal number: h is off by at most 2^-22 of itself or 2^-51 of that largest, the
+// greater of the two (hi + lo at one scale is off by 2^-40 of the largest: half a thousandth of an h that is 2^-29 of it,
+// all that a column has whose B is 0 for the largest).  Products and sums are fp32; the
+// sum with lo takes 2^-12 before that with hi is added to it, and 2^-e is applied to each sum.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -73,6 +76,7 @@ TB_DEVI void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
 }
 
 // ---------------------------------------------------------------- h as fp16
+constexpr float kLowScale = 0x1p12f;  // of the low terms
 // 2^e and 2^-e for numbers of which the largest |h| is top; 0 and what is not finite stay as they are
 TB_DEVI float up_scale(float top, float& back) {
   int e = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
@@ -131,7 +135,7 @@ TB_DEVI void join_down(const AdapterArgs& a, const AdapterTile& t, float* part, 
       const float f = __half2float(hi);
       if (col < N) {
         a.terms[at * 2 * N + col] = hi;
-        a.terms[at * 2 * N + N + col] = fabsf(f) < INFINITY ? __float2half_rn(v[j] * up - f) : __half();
+        a.terms[at * 2 * N + N + col] = fabsf(f) < INFINITY ? __float2half_rn((v[j] * up - f) * kLowScale) : __half();
       }
     }
   }
@@ -551,6 +555,8 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
               mma_16816(acc[q], w[2 * q][2 * m], w[2 * q + 1][2 * m], w[2 * q][2 * m + 1], w[2 * q + 1][2 * m + 1], lo[n][2 * m], lo[n][2 * m + 1]);
             }
 #pragma unroll
+          for (int i = 0; i < 8; ++i) (&acc[0][0])[i] *= 1 / kLowScale;
+#pragma unroll
           for (int m = 0; m < kMma; ++m)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
@@ -579,7 +585,8 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
 
 // ---------------------------------------------------------------- up, many tokens
 // Every CTA takes equal runs of all row tiles' (at most 128 tokens) column tiles of 64, back and forth over them, as tiles
-// of few tokens take less time (packed prompts 115 us; 120 with one run a CTA and with four); a warp takes 16 of the tokens.  A
+// of few tokens take less time (packed prompts 115 us then, 122 now that the two terms of h have sums of their own; 120 with one run
+// a CTA and with four); a warp takes 16 of the tokens.  A
 // thread keeps its tokens' terms as the mma's left operand (of up to 64 ranks; above, they are read again); B's rows come
 // by cp.async three column tiles ahead, and y into a ring of the thread's own with them.  Which column of out is which of the MMAs' columns is free: thread
 // (g, c) has twice 8 neighbouring ones of tokens g and g + 8, so that four threads' y and out are 64 bytes in a row.
@@ -713,35 +720,48 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const Ad
           for (int blk = 0; blk < blocks; ++blk) {
             if (MULTI) terms(blk);
             float acc[4][4];
-            auto step = [&](int k, const uint2 (&b)[4]) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (k == 0) mma_16816_first(acc[j], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b[j].x, b[j].y);
-                else mma_16816(acc[j], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b[j].x, b[j].y);
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mma_16816(acc[j], hi[k][0], hi[k][1], hi[k][2], hi[k][3], b[j].x, b[j].y);
-            };
             const uint32_t row = st + 4 * q * 8 * pitch + blk * KS * 32;
-            if constexpr (KS == 1) {
-              uint2 b[4];
+            const bool more = KS == 4 && (blk * KS + 2) * 16 < live;
+            // sums with lo and with hi apart, by the B of two steps and two MMAs' columns at a time
+            float low[4][4];
+            constexpr int kAtOnce = KS == 1 ? 1 : 2, kSteps = 2 * (KS == 4 ? 2 : 1);
+            uint2 b[2][kAtOnce][2];
+            auto load = [&](int i) {
+              const int k0 = (i >> 1) * 2, j0 = (i & 1) * 2;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) b[j] = ld_shared_v2(row + j * 8 * pitch + c * 8);
-              step(0, b);
-            } else {
-#pragma unroll
-              for (int k = 0; k < KS; k += 2) {
-                if (k && (blk * KS + k) * 16 >= live) break;
-                uint2 b[2][4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const uint4 v = ld_shared_v4(row + j * 8 * pitch + ((k * 32 + c * 16) ^ swap));
-                  b[0][j] = make_uint2(v.x, v.y), b[1][j] = make_uint2(v.z, v.w);
+              for (int j = 0; j < 2; ++j) {
+                if constexpr (KS == 1) {
+                  b[i & 1][0][j] = ld_shared_v2(row + (j0 + j) * 8 * pitch + c * 8);
+                } else {
+                  const uint4 v = ld_shared_v4(row + (j0 + j) * 8 * pitch + ((k0 * 32 + c * 16) ^ swap));
+                  b[i & 1][0][j] = make_uint2(v.x, v.y), b[i & 1][kAtOnce - 1][j] = make_uint2(v.z, v.w);
                 }
-                step(k, b[0]);
-                step(k + 1, b[1]);
               }
+            };
+            // (the next B ahead: of ranks 65 to 128 388 us against 405, of up to 64 123.4 against 122.4)
+            if (MULTI) load(0);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+              if (i == 2 && !more) break;
+              if (!MULTI) load(i);
+              else if (i + 1 < kSteps) load(i + 1);
+#pragma unroll
+              for (int h = 0; h < kAtOnce; ++h)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const int k = (i >> 1) * 2 + h, jj = (i & 1) * 2 + j;
+                  const uint2 w = b[i & 1][h][j];
+                  if (k == 0) {
+                    mma_16816_first(low[jj], lo[k][0], lo[k][1], lo[k][2], lo[k][3], w.x, w.y);
+                    mma_16816_first(acc[jj], hi[k][0], hi[k][1], hi[k][2], hi[k][3], w.x, w.y);
+                  } else {
+                    mma_16816(low[jj], lo[k][0], lo[k][1], lo[k][2], lo[k][3], w.x, w.y);
+                    mma_16816(acc[jj], hi[k][0], hi[k][1], hi[k][2], hi[k][3], w.x, w.y);
+                  }
+                }
             }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) (&acc[0][0])[j] = fmaf((&low[0][0])[j], 1 / kLowScale, (&acc[0][0])[j]);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               float& s = (&sum[0][0])[j];
