@@ -77,10 +77,10 @@ TB_DEVI void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
 
 // ---------------------------------------------------------------- h as fp16
 constexpr float kLowScale = 0x1p12f;  // of the low terms
-// 2^e and 2^-e for numbers of which the largest |h| is top; 0 and what is not finite stay as they are
+// 2^e and 2^-e for numbers of which the largest finite |h| is top
 TB_DEVI float up_scale(float top, float& back) {
   int e = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
-  if (!(top > 0.f) || !(top < INFINITY)) e = 0;
+  if (!(top > 0.f)) e = 0;
   e = max(-126, min(126, e));
   back = __uint_as_float((uint32_t)(127 - e) << 23);
   return __uint_as_float((uint32_t)(127 + e) << 23);
@@ -120,7 +120,7 @@ TB_DEVI void join_down(const AdapterArgs& a, const AdapterTile& t, float* part, 
         for (int r = 0; r < a.cluster; ++r) s += a.cluster > 1 ? *cl.map_shared_rank(part + row * PITCH + col, r) : part[row * PITCH + col];
         v[j] = s * scale;
       }
-      top = fmaxf(top, fabsf(v[j]));
+      top = fmaxf(top, fabsf(v[j]) < INFINITY ? fabsf(v[j]) : 0.f);  // (what is not finite stays so at any scale)
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));

@@ -55,3 +55,34 @@ def test_small_ranks_beside_large_ones(T, R, below):
     tol = (K / 8 + R / 8 + 80) * 2.0 ** -23 * S + 2.0 ** -21 * H + floor + (R / 8 + 40) * 2.0 ** -23 * H1 + 2.0 ** -11 * np.abs(want) + 2.0 ** -25
     err = np.abs(got - want)
     assert (err <= tol).all(), np.max(err / tol)
+
+
+@pytest.mark.parametrize("T,R", [(1, 16), (40, 16), (300, 16), (40, 64), (300, 64), (40, 200), (300, 200)])
+def test_an_infinite_rank_beside_large_ones(T, R):
+    """One rank's A x is infinite, another's far above fp16's range: their sum is that infinity, where B reaches it."""
+    import ternary_hadamard_rotated_gb300 as tb
+
+    rng = np.random.default_rng(T + R)
+    K, N, n = 64, 72, 2
+    a = rng.standard_normal((n, R, K)).astype(np.float16)
+    b = rng.standard_normal((n, N, R)).astype(np.float16)
+    a[0, 7], b[0, :, 7] = 6e4, rng.choice([-9.0, 9.0], N)
+    a[0, 2, 5], b[0, :, 2] = np.inf, rng.choice([-1.0, 0.0, 1.0], N)
+    x = (rng.random((T, K)) + 0.5).astype(np.float16)
+    x[:, 5] = rng.choice([-2.0, 0.5], T)
+    y = rng.standard_normal((T, N)).astype(np.float16)
+    scale = np.array([0.5, 2.0], dtype=np.float32)
+    rows, adapter = [0, (T + 1) // 2, T], [0, 1]
+    dev = lambda m: torch.from_numpy(m).cuda()  # noqa: E731
+    plan = torch.empty(tb.tb_adapter_plan_size(T, n), dtype=torch.uint8, device="cuda")
+    tb.tb_adapter_plan(dev(np.array(rows, dtype=np.int32)), dev(np.array(adapter, dtype=np.int32)), T, n, plan)
+    ws = torch.empty(tb.tb_adapter_linear_workspace_size(T, n, K, N, R), dtype=torch.uint8, device="cuda")
+    out = dev(y)
+    tb.tb_adapter_linear(dev(x), dev(a), dev(b), dev(scale), plan, out, ws)
+    got = out.cpu().numpy().astype(np.float64)
+    with np.errstate(invalid="ignore"):
+        want, _, _ = serving.adapter_linear(x, a, b, scale, None, rows, adapter, y)
+    first = slice(0, rows[1])
+    assert np.isinf(want[first]).any() and not np.isfinite(want[first]).any()
+    assert np.array_equal(got[first], want[first], equal_nan=True)
+    assert np.isfinite(got[rows[1]:]).all()
