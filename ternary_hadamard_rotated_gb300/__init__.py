@@ -504,26 +504,37 @@ def tb_gated_delta(q, k, v, g, beta, row_start, max_len, o, workspace=None, stat
         _stream(stream)))
 
 
-_current_device = None
+def _elsewhere(name, t, at):
+    where = "cpu" if at < 0 else f"cuda:{at}"
+    raise ValueError(f"{name} lies on {t.device}, the call's first tensor on {where}")
 
 
-def _here(name, t, stream):
-    """The launch goes to the current device: the tensor has to lie there (a given stream is the caller's word)."""
-    at = t.get_device()
-    if at < 0:
-        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
-    if stream is None:
-        global _current_device
-        if _current_device is None:
-            import torch._C as c
-            _current_device = c._cuda_getDevice
-        if at != _current_device():
-            raise ValueError(f"{name} lies on {t.device}, which is not the current device")
+# The checks of the operators around the linears: as above, and that a tensor lies on device `at`, with the call's first one.
+
+def _flat_at(at, name, t, dtype, *shape):
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == at and t.is_contiguous():
+        return t.data_ptr()
+    _flat(name, t, dtype, *shape)
+    _elsewhere(name, t, at)
 
 
-def _matrix(name, t, dtypes, shape=None):
-    """Distance of two rows of t [rows, columns] in elements (of one row alone: its columns); a row's elements
-    must be contiguous."""
+def _tokens_at(at, name, t, f16, like=None):
+    """The distance of two tokens, and the shape (that of the argument named first in like, a pair of a name and a shape)."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or t.dtype is not f16 or strides[2] != 1 or strides[1] != shape[2]:
+        _tokens(name, t, f16)  # (of one element or head alone its stride does not count)
+    if like is not None and shape != like[1]:
+        raise ValueError(f"{name} and {like[0]} do not match: {list(shape)} and {list(like[1])}")
+    if t.get_device() != at:
+        _elsewhere(name, t, at)
+    return strides[0] if shape[0] > 1 else shape[1] * shape[2], shape
+
+
+def _matrix_at(at, name, t, dtypes, shape=None):
+    """Distance of two rows of t [rows, columns] in elements (of one row alone: its columns), and the shape; a row's
+    elements must be contiguous."""
     got = t.shape
     if len(got) != 2 or t.dtype not in dtypes or (shape is not None and got != shape):
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))} {'[rows, columns]' if shape is None else list(shape)}, "
@@ -532,7 +543,54 @@ def _matrix(name, t, dtypes, shape=None):
     rows, columns = got
     if s1 != 1 and columns > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous, got strides {t.stride()}")
-    return s0 if rows > 1 else columns
+    if t.get_device() != at:
+        _elsewhere(name, t, at)
+    return s0 if rows > 1 else columns, got
+
+
+def _bytes(at, name, t, least=0):
+    """Address and size of a contiguous buffer of at least so many bytes (None: no buffer)."""
+    if t is None:
+        return None, 0
+    n = t.nbytes
+    if t.get_device() == at and n >= least and t.is_contiguous():
+        return t.data_ptr(), n
+    if t.get_device() != at:
+        _elsewhere(name, t, at)
+    if n < least:
+        raise ValueError(f"{name} must hold at least {least} bytes, got {n}")
+    raise ValueError(f"{name} must be contiguous, got strides {t.stride()}")
+
+
+def _status(t, at):
+    if t is None or isinstance(t, int):
+        return t
+    if t.get_device() != at:
+        _elsewhere("dev_status", t, at)
+    return t.data_ptr()
+
+
+_current = None
+
+
+def _launch(name, at, stream):
+    """The stream's handle, for a call whose first tensor, `name`, lies on device at: the launch goes to the current
+    device, which that has to be (and the stream's)."""
+    global _current
+    if at < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if _current is None:
+        import torch._C as c
+        _current = c._cuda_getDevice, c._cuda_getCurrentRawStream
+    if at != _current[0]():
+        raise ValueError(f"{name} lies on cuda:{at}, which is not the current device")
+    if stream is None:
+        return _current[1](at)
+    if isinstance(stream, int):
+        return stream
+    if stream.device_index != at:
+        raise ValueError(f"{name} lies on cuda:{at}, the stream belongs to cuda:{stream.device_index}")
+    return stream.cuda_stream
 
 
 def tb_rotary_plan_size(R):
@@ -544,33 +602,34 @@ def tb_rotary_plan(plan, R, base=10000.0, scaling=TB_ROTARY_NONE, factor=1.0, or
     """The table of R / 2 pairs that tb_rotary reads, into ``plan`` (tb_rotary_plan_size(R) bytes); freqs:
     float64 [R / 2] on the device in place of base and scaling; amplitude 0: chosen by the scaling."""
     import torch
-    buf, nbytes = _scratch(plan)
-    _here("plan", plan, stream)
+    at = plan.get_device()
+    buf, nbytes = _bytes(at, "plan", plan)
     _check("tb_rotary_plan", load().tb_rotary_plan(
         buf, nbytes, R, base, scaling, factor, original, beta_fast, beta_slow, amplitude,
-        _flat("freqs", freqs, torch.float64, R // 2), _ptr(dev_status), _stream(stream)))
+        _flat_at(at, "freqs", freqs, torch.float64, R // 2), _status(dev_status, at), _launch("plan", at, stream)))
 
 
 def tb_rotary(q, k, pos, plan, R, layout, q_out, k_out, inverse=False, dev_status=None, stream=None):
     """q fp16 [T, Hq, D] and k fp16 [T, Hk, D] (or None) turned by the positions pos int32 [T] into q_out and
     k_out (which may be q and k)."""
     f16, _, i32, _ = _types()
-    ldq, ldqo = _tokens("q", q, f16), _tokens("q_out", q_out, f16)
-    T, Hq, D = q.shape
-    if q_out.shape != q.shape:
-        raise ValueError(f"q and q_out differ in shape: {list(q.shape)} and {list(q_out.shape)}")
+    at = q.get_device()
+    ldq, shape = _tokens_at(at, "q", q, f16)
+    T, Hq, D = shape
+    ldqo, _ = _tokens_at(at, "q_out", q_out, f16, ("q", shape))
     kp, ldk, Hk, kop, ldko = None, 0, 0, None, 0
     if k is not None:
         if k_out is None:
             raise ValueError("k is given without k_out")
-        ldk, ldko, Hk = _tokens("k", k, f16), _tokens("k_out", k_out, f16), k.shape[1]
-        if k.shape != (T, Hk, D) or k_out.shape != k.shape:
-            raise ValueError(f"q, k and k_out do not match: {list(q.shape)}, {list(k.shape)}, {list(k_out.shape)}")
+        ldk, of_k = _tokens_at(at, "k", k, f16)
+        Hk = of_k[1]
+        if of_k != (T, Hk, D):
+            raise ValueError(f"k and q do not match: {list(of_k)} and {list(shape)}")
+        ldko, _ = _tokens_at(at, "k_out", k_out, f16, ("k", of_k))
         kp, kop = k.data_ptr(), k_out.data_ptr()
-    _here("q", q, stream)
     _check("tb_rotary", load().tb_rotary(
-        q.data_ptr(), ldq, Hq, kp, ldk, Hk, T, D, _flat("pos", pos, i32, T), plan.data_ptr(), R, layout,
-        int(bool(inverse)), q_out.data_ptr(), ldqo, kop, ldko, _ptr(dev_status), _stream(stream)))
+        q.data_ptr(), ldq, Hq, kp, ldk, Hk, T, D, _flat_at(at, "pos", pos, i32, T), _bytes(at, "plan", plan, 16 + 4 * R)[0], R,
+        layout, 1 if inverse else 0, q_out.data_ptr(), ldqo, kop, ldko, _status(dev_status, at), _launch("q", at, stream)))
 
 
 def tb_rotary_cache_write(q, k, v, pos, slots, plan, R, layout, q_out, k_cache, v_cache, k_out=None, inverse=False,
@@ -578,25 +637,25 @@ def tb_rotary_cache_write(q, k, v, pos, slots, plan, R, layout, q_out, k_cache, 
     """tb_rotary, with the turned k and v fp16 [T, Hkv, D] written to their slots (int64 [T], negative: skipped) of
     the caches fp16 [pages, Hkv, page, D]; k_out: the turned k beside the cache, or None."""
     f16, _, i32, i64 = _types()
-    ldq, ldk, ldv, ldqo = _tokens("q", q, f16), _tokens("k", k, f16), _tokens("v", v, f16), _tokens("q_out", q_out, f16)
-    T, Hq, D = q.shape
-    H = k.shape[1]
-    if k.shape != (T, H, D) or v.shape != k.shape or q_out.shape != q.shape:
-        raise ValueError(f"q, k, v and q_out do not match: {list(q.shape)}, {list(k.shape)}, {list(v.shape)}, "
-                         f"{list(q_out.shape)}")
+    at = q.get_device()
+    ldq, shape = _tokens_at(at, "q", q, f16)
+    T, Hq, D = shape
+    ldk, of_k = _tokens_at(at, "k", k, f16)
+    H = of_k[1]
+    if of_k != (T, H, D):
+        raise ValueError(f"k and q do not match: {list(of_k)} and {list(shape)}")
+    ldv, _ = _tokens_at(at, "v", v, f16, ("k", of_k))
+    ldqo, _ = _tokens_at(at, "q_out", q_out, f16, ("q", shape))
     kop, ldko = None, 0
     if k_out is not None:
-        ldko = _tokens("k_out", k_out, f16)
-        if k_out.shape != k.shape:
-            raise ValueError(f"k and k_out differ in shape: {list(k.shape)} and {list(k_out.shape)}")
+        ldko, _ = _tokens_at(at, "k_out", k_out, f16, ("k", of_k))
         kop = k_out.data_ptr()
     pages, _, page, _ = k_cache.shape
-    _here("q", q, stream)
     _check("tb_rotary_cache_write", load().tb_rotary_cache_write(
-        q.data_ptr(), ldq, Hq, k.data_ptr(), ldk, v.data_ptr(), ldv, H, T, D, _flat("pos", pos, i32, T),
-        _flat("slots", slots, i64, T), plan.data_ptr(), R, layout, int(bool(inverse)), q_out.data_ptr(), ldqo, kop, ldko,
-        _flat("k_cache", k_cache, f16, pages, H, page, D), _flat("v_cache", v_cache, f16, pages, H, page, D), pages, page,
-        _ptr(dev_status), _stream(stream)))
+        q.data_ptr(), ldq, Hq, k.data_ptr(), ldk, v.data_ptr(), ldv, H, T, D, _flat_at(at, "pos", pos, i32, T),
+        _flat_at(at, "slots", slots, i64, T), _bytes(at, "plan", plan, 16 + 4 * R)[0], R, layout, 1 if inverse else 0,
+        q_out.data_ptr(), ldqo, kop, ldko, _flat_at(at, "k_cache", k_cache, f16, pages, H, page, D),
+        _flat_at(at, "v_cache", v_cache, f16, pages, H, page, D), pages, page, _status(dev_status, at), _launch("q", at, stream)))
 
 
 def tb_adapter_plan_size(T, n):
@@ -608,11 +667,11 @@ def tb_adapter_plan(row_start, adapter, T, n, plan, dev_status=None, stream=None
     adapters -> plan (tb_adapter_plan_size(T, n) bytes)."""
     _, _, i32, _ = _types()
     B = adapter.numel()
-    buf, nbytes = _scratch(plan)
-    _here("plan", plan, stream)
+    at = plan.get_device()
+    buf, nbytes = _bytes(at, "plan", plan)
     _check("tb_adapter_plan", load().tb_adapter_plan(
-        _flat("row_start", row_start, i32, B + 1), _flat("adapter", adapter, i32, B), B, T, n, buf, nbytes, _ptr(dev_status),
-        _stream(stream)))
+        _flat_at(at, "row_start", row_start, i32, B + 1), _flat_at(at, "adapter", adapter, i32, B), B, T, n, buf, nbytes,
+        _status(dev_status, at), _launch("plan", at, stream)))
 
 
 def tb_adapter_linear_workspace_size(T, n, K, N, R):
@@ -623,17 +682,19 @@ def tb_adapter_linear(x, a, b, scale, plan, y, workspace=None, out=None, rank=No
     """out[t] = y[t] + scale[g] b[g] (a[g] x[t]): x fp16 [T, K], a fp16 [n, R, K], b fp16 [n, N, R], scale fp32
     [n], y fp16 [T, N], plan from tb_adapter_plan; rank: int32 [n] or None (all R); out: y unless given."""
     f16, f32, i32, _ = _types()
-    T, K = x.shape
+    at = x.get_device()
+    ldx, (T, K) = _matrix_at(at, "x", x, (f16,))
+    ldy, (rows, N) = _matrix_at(at, "y", y, (f16,))
+    if rows != T:
+        raise ValueError(f"y must have x's {T} rows, got {rows}")
     n, R, _ = a.shape
-    N = y.shape[1]
-    ldx, ldy = _matrix("x", x, (f16,)), _matrix("y", y, (f16,), (T, N))
-    ldo, op = (ldy, y.data_ptr()) if out is None else (_matrix("out", out, (f16,), (T, N)), out.data_ptr())
-    ws, ws_bytes = _scratch(workspace)
-    _here("x", x, stream)
+    ldo, op = (ldy, y.data_ptr()) if out is None else (_matrix_at(at, "out", out, (f16,), (T, N))[0], out.data_ptr())
+    ws, ws_bytes = _bytes(at, "workspace", workspace)
+    # (a plan's first 32 bytes say of which step it is: one of another, which may be shorter, is refused by its status)
     _check("tb_adapter_linear", load().tb_adapter_linear(
-        x.data_ptr(), ldx, T, K, _flat("a", a, f16, n, R, K), _flat("b", b, f16, n, N, R), n, R, N, _flat("rank", rank, i32, n),
-        _flat("scale", scale, f32, n), plan.data_ptr(), y.data_ptr(), ldy, op, ldo, ws, ws_bytes, _ptr(dev_status),
-        _stream(stream)))
+        x.data_ptr(), ldx, T, K, _flat_at(at, "a", a, f16, n, R, K), _flat_at(at, "b", b, f16, n, N, R), n, R, N,
+        _flat_at(at, "rank", rank, i32, n), _flat_at(at, "scale", scale, f32, n), _bytes(at, "plan", plan, 32)[0],
+        y.data_ptr(), ldy, op, ldo, ws, ws_bytes, _status(dev_status, at), _launch("x", at, stream)))
 
 
 def tb_logits_adjust(logits, out, history, hist_len, prompt_len=None, row_start=None, slot=None, fresh=None, tree=None,
@@ -645,18 +706,20 @@ def tb_logits_adjust(logits, out, history, hist_len, prompt_len=None, row_start=
     repetition, presence, frequency fp32 [B]; bias_start int32 [B + 1], bias_ids int32 and bias_values fp32 [n];
     mask int32 (bits) [rows, ceil(V / 32)], mask_row int32 [T]."""
     f16, f32, i32, i64 = _types()
-    T, V = logits.shape
-    ld, ldo = _matrix("logits", logits, (f16,)), _matrix("out", out, (f16, f32), (T, V))
+    at = logits.get_device()
+    ld, (T, V) = _matrix_at(at, "logits", logits, (f16,))
+    ldo, _ = _matrix_at(at, "out", out, (f16, f32), (T, V))
     B, (n_hist, L) = hist_len.numel(), history.shape
     n_bias = 0 if bias_ids is None else bias_ids.numel()
     mask_rows = 0 if mask is None else mask.shape[0]
-    _here("logits", logits, stream)
     _check("tb_logits_adjust", load().tb_logits_adjust(
-        logits.data_ptr(), ld, T, V, _flat("row_start", row_start, i32, B + 1), B, _flat("history", history, i32, n_hist, L),
-        n_hist, L, _flat("slot", slot, i32, B), _flat("hist_len", hist_len, i32, B), _flat("prompt_len", prompt_len, i32, B),
-        _flat("fresh", fresh, i32, T), _flat("tree", tree, i64, T), _flat("repetition", repetition, f32, B),
-        _flat("presence", presence, f32, B), _flat("frequency", frequency, f32, B),
-        _flat("bias_start", bias_start, i32, B + 1), _flat("bias_ids", bias_ids, i32, n_bias),
-        _flat("bias_values", bias_values, f32, n_bias), n_bias, _flat("mask", mask, i32, mask_rows, (V + 31) // 32), mask_rows,
-        _flat("mask_row", mask_row, i32, T), out.data_ptr(), ldo, TB_OUT_F16 if out.dtype is f16 else TB_OUT_F32,
-        _ptr(dev_status), _stream(stream)))
+        logits.data_ptr(), ld, T, V, _flat_at(at, "row_start", row_start, i32, B + 1), B,
+        _flat_at(at, "history", history, i32, n_hist, L), n_hist, L, _flat_at(at, "slot", slot, i32, B),
+        _flat_at(at, "hist_len", hist_len, i32, B), _flat_at(at, "prompt_len", prompt_len, i32, B),
+        _flat_at(at, "fresh", fresh, i32, T), _flat_at(at, "tree", tree, i64, T), _flat_at(at, "repetition", repetition, f32, B),
+        _flat_at(at, "presence", presence, f32, B), _flat_at(at, "frequency", frequency, f32, B),
+        _flat_at(at, "bias_start", bias_start, i32, B + 1), _flat_at(at, "bias_ids", bias_ids, i32, n_bias),
+        _flat_at(at, "bias_values", bias_values, f32, n_bias), n_bias,
+        _flat_at(at, "mask", mask, i32, mask_rows, (V + 31) // 32), mask_rows, _flat_at(at, "mask_row", mask_row, i32, T),
+        out.data_ptr(), ldo, TB_OUT_F16 if out.dtype is f16 else TB_OUT_F32, _status(dev_status, at),
+        _launch("logits", at, stream)))
