@@ -101,3 +101,71 @@ def test_one_tensor_left_on_the_host(no_library, fn, name):
     for stream in (None, torch.cuda.current_stream(), torch.cuda.current_stream().cuda_stream):
         with pytest.raises(ValueError, match="lies on c|must be a CUDA tensor"):
             getattr(tb, fn)(**own, stream=stream)
+
+
+# Types, shapes and strides, argument by argument.  The name of the refused argument begins the message.
+
+def first_lines(t):
+    return t[: t.shape[0] - 1]
+
+
+def strided(t):
+    return torch.stack([t, t], -1)[..., 0]
+
+
+ANY_SIZE = {"plan", "workspace", "dev_status", "bias_ids", "history"}  # (their number of elements is their own)
+FROM_THE_FIRST = {"q", "x", "logits", "adapter", "hist_len"}  # (they say how many there have to be: another argument is refused)
+
+
+@pytest.mark.parametrize("fn,name", [p for p in PAIRS if p[1] not in ("plan", "workspace", "dev_status")])
+def test_a_tensor_of_another_type(no_library, fn, name):
+    tb, args = no_library
+    other = F64 if args[fn][name].dtype is not F64 else F32
+    with pytest.raises(ValueError, match=rf"^{name} must be .* got {other}"):
+        getattr(tb, fn)(**dict(args[fn], **{name: args[fn][name].to(other)}))
+    if fn == "tb_logits_adjust" and name == "out":
+        return  # (fp32 is a type of its own there)
+    near = {F16: F32, F32: F16, I32: I64, I64: I32, F64: F32}[args[fn][name].dtype]
+    with pytest.raises(ValueError, match=rf"^{name} must be "):
+        getattr(tb, fn)(**dict(args[fn], **{name: args[fn][name].to(near)}))
+
+
+@pytest.mark.parametrize("fn,name", [p for p in PAIRS if p[1] not in ANY_SIZE | FROM_THE_FIRST])
+def test_a_tensor_of_another_length(no_library, fn, name):
+    tb, args = no_library
+    refused = {"a": "b", "k_cache": "v_cache"}.get(name, name)  # (the first of two that have to agree says how many)
+    changed = args[fn][name][:, 1:].contiguous() if name == "mask" else first_lines(args[fn][name])
+    with pytest.raises(ValueError, match=rf"^{refused} (must|and)"):
+        getattr(tb, fn)(**dict(args[fn], **{name: changed}))
+
+
+@pytest.mark.parametrize("fn,name", [("tb_rotary", "q"), ("tb_rotary_cache_write", "q"), ("tb_adapter_plan", "adapter"), ("tb_logits_adjust", "hist_len"),
+                                     ("tb_adapter_linear", "x"), ("tb_logits_adjust", "logits")])
+def test_the_tensor_that_says_how_many(no_library, fn, name):
+    tb, args = no_library
+    refused = {"q": "(k|q_out)", "adapter": "row_start", "hist_len": "row_start", "x": "y", "logits": "out"}[name]
+    with pytest.raises(ValueError, match=rf"^{refused} (must|and)"):
+        getattr(tb, fn)(**dict(args[fn], **{name: first_lines(args[fn][name])}))
+    if name == "hist_len":
+        with pytest.raises(ValueError, match="^bias_values must"):
+            tb.tb_logits_adjust(**dict(args[fn], bias_ids=first_lines(args[fn]["bias_ids"])))
+
+
+@pytest.mark.parametrize("fn,name", [p for p in PAIRS if p[1] not in ("plan", "workspace", "dev_status")])
+def test_a_tensor_with_gaps(no_library, fn, name):
+    tb, args = no_library
+    with pytest.raises(ValueError, match=rf"^{name}(:| must be contiguous)"):
+        getattr(tb, fn)(**dict(args[fn], **{name: strided(args[fn][name])}))
+
+
+def test_more_shapes(no_library):
+    tb, args = no_library
+    z = lambda *s: torch.zeros(*s, dtype=F16)  # noqa: E731
+    for fn, name, value, refused in [
+            ("tb_rotary", "k", z(4, 1, 72), "k and q"), ("tb_rotary", "k_out", z(4, 2, 64), "k_out and k"), ("tb_rotary", "q_out", z(4, 2, 72), "q_out and q"),
+            ("tb_rotary", "q", z(4, 128), "q must"), ("tb_rotary_cache_write", "v", z(4, 2, 64), "v and k"), ("tb_rotary_cache_write", "v_cache", z(3, 1, 32, 64), "v_cache must"),
+            ("tb_rotary_cache_write", "k_cache", z(3, 2, 16, 64), "k_cache must"), ("tb_rotary_cache_write", "k_cache", z(3, 1, 16, 72), "k_cache must"),
+            ("tb_adapter_linear", "a", z(2, 8, 24), "a must"), ("tb_adapter_linear", "a", z(2, 16, 16), "b must"), ("tb_adapter_linear", "b", z(2, 16, 8), "b must"),
+            ("tb_adapter_linear", "out", z(4, 32), "out must"), ("tb_logits_adjust", "out", z(4, 99), "out must")]:
+        with pytest.raises(ValueError, match=f"^{refused}"):
+            getattr(tb, fn)(**dict(args[fn], **{name: value}))
