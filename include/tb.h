@@ -641,7 +641,8 @@ int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int64_t K, cons
  * is.  Negative tokens are padding; rows of no request are neither read nor written.  T and B up to 65535
  * (TB_ERR_TOO_LARGE), V up to 2^24.  dev_status optional: TB_DEV_BAD_ID (a token, a history's or a mask's row past
  * its table: left out), TB_DEV_BAD_LEN (a length, a list or row starts that do not fit: cut, taken as empty, or
- * the row left out; more than 64 fresh tokens: the first 64).
+ * the row left out; more than 64 fresh tokens: the first 64).  The history's row, lengths and list are looked at of a
+ * request without rows too, its tokens are not.
  */
 int tb_logits_adjust(const uint16_t* logits, int64_t ld, int64_t T, int64_t V, const int32_t* row_start,
                      int64_t B, const int32_t* history, int64_t n_hist, int64_t ldh, const int32_t* slot,

@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(kFixThreads, 3) logits_fix_kernel(const Logits
     }
   }
   if (first >= end) {
+    if (bad && tid == 0) set_status(a.status, bad);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // this launch is not over before the first
     return;
   }
