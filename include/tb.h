@@ -599,9 +599,9 @@ int tb_adapter_plan(const int32_t* row_start, const int32_t* adapter, int64_t B,
  *            distance; rows without an adapter are then not touched) and must not overlap it or x otherwise.
  * A x and the sum are fp32; scale A x enters the second product off by at most 2^-22 of itself or 2^-51 of the largest
  * of the token's 64 ranks around it, the greater of the two; sums are rounded to the place of their largest term, in
- * which an element below 2^-14 counts as 2^-14; one rounding to fp16 at the end.  What is not finite
- * stays in the rows and columns that it reaches (an infinite element of B may give NaN there).  A token's row depends on no
- * other token's.  K, N and R multiples of 8, R up to 256 (TB_ERR_UNSUPPORTED above).  workspace: at least
+ * which an element below 2^-14 counts as 2^-14; one rounding to fp16 at the end.  What is not finite stays in the rows
+ * and columns that it reaches (an infinite element of B may give NaN there).  A token's row depends on no other token's x
+ * and y; the order of its sums, and with it the last bits, also goes by T and n.  K, N and R multiples of 8, R up to 256 (TB_ERR_UNSUPPORTED above).  workspace: at least
  * tb_adapter_linear_workspace_size(T, n, K, N, R) bytes of scratch; its contents do not matter; calls that share
  * one are ordered on one stream.  dev_status optional: TB_DEV_BAD_PLAN.
  */
@@ -638,7 +638,7 @@ int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int64_t K, cons
  *   out        [T, V] of out_type, rows ldo apart (out); may be logits where that is fp16 (with its distance), and
  *              must not overlap it otherwise.
  * Every step in fp32, rounded as written; one rounding to fp16.  A masked token gives -infinity whatever its logit
- * is.  Negative tokens are padding; rows of no request are neither read nor written.  T and B up to 65535
+ * is.  Negative tokens are padding; rows of no request are not written (they are read).  T and B up to 65535
  * (TB_ERR_TOO_LARGE), V up to 2^24.  dev_status optional: TB_DEV_BAD_ID (a token, a history's or a mask's row past
  * its table: left out), TB_DEV_BAD_LEN (a length, a list or row starts that do not fit: cut, taken as empty, or
  * the row left out; more than 64 fresh tokens: the first 64).  The history's row, lengths and list are looked at of a

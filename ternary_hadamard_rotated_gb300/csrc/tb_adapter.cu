@@ -33,15 +33,14 @@ struct AdapterArgs {
   const float* scale;
   const AdapterPlan* plan;
   const int32_t* order;
-  const AdapterTile* down_tiles;
-  const AdapterTile* up_tiles;
+  const AdapterTile* tiles;
   __half* terms;  // [T][blocks][hi, lo][block]
   float* back;    // [T][blocks], 2^-e
   int32_t* status;
   int64_t ldx, ldy, ldo;
   int T, n, K, N, R;
   int block, blocks;  // ranks of a block (16, 32 or 64), blocks of R
-  int cluster, down_kind, up_kind;
+  int cluster, kind;  // CTAs that share out K, kind of tiles
 };
 
 TB_DEVI bool plan_fits(const AdapterArgs& a) {
@@ -70,9 +69,6 @@ TB_DEVI void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a
 
 TB_DEVI void cp_async16(uint32_t dst, const void* src, int bytes) {  // the rest of the 16 bytes is zeroed
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-TB_DEVI void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
 
 // ---------------------------------------------------------------- h as fp16
@@ -167,8 +163,8 @@ __global__ void __launch_bounds__(kDownThreads, 2) adapter_down_few_kernel(const
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(a.status, TB_DEV_BAD_PLAN);
     return;
   }
-  if (tile >= a.plan->tiles[a.down_kind]) return;  // (all CTAs of the cluster)
-  const AdapterTile t = a.down_tiles[tile];  // (not before the plan is known to be one of T tokens)
+  if (tile >= a.plan->tiles[a.kind]) return;  // (all CTAs of the cluster)
+  const AdapterTile t = a.tiles[tile];  // (not before the plan is known to be one of T tokens)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int r0 = blockIdx.y * N, live = live_rank(a, t.adapter);
 
@@ -262,8 +258,8 @@ __global__ void __launch_bounds__(kManyThreads, 2) adapter_down_many_kernel(cons
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(a.status, TB_DEV_BAD_PLAN);
     return;
   }
-  if (tile >= a.plan->tiles[a.down_kind]) return;  // (all CTAs of the cluster)
-  const AdapterTile t = a.down_tiles[tile];  // (not before the plan is known to be one of T tokens)
+  if (tile >= a.plan->tiles[a.kind]) return;  // (all CTAs of the cluster)
+  const AdapterTile t = a.tiles[tile];  // (not before the plan is known to be one of T tokens)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = blockIdx.y * N, live = live_rank(a, t.adapter);
   unsigned char* const stages = tile_smem + ((1024 - (smem_u32(tile_smem) & 1023)) & 1023);
@@ -425,7 +421,7 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
   }
   copy_bare(a);
   const int units = (a.N + 31) / 32;
-  const int64_t all = (int64_t)a.plan->tiles[a.up_kind] * units;
+  const int64_t all = (int64_t)a.plan->tiles[a.kind] * units;
   const int64_t warps = (int64_t)gridDim.x * kUpFewWarps, warp = (int64_t)blockIdx.x * kUpFewWarps + (threadIdx.x >> 5);
   int64_t at = all * warp / warps;
   const int64_t stop = all * (warp + 1) / warps;
@@ -437,7 +433,7 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
     const int tile = (int)(at / units), begin = (int)(at - (int64_t)tile * units);
     const int end = (int)(stop - at < units - begin ? begin + (stop - at) : units);
     at += end - begin;
-    const AdapterTile t = a.up_tiles[tile];
+    const AdapterTile t = a.tiles[tile];
     const int live = live_rank(a, t.adapter);
     const int half = t.count > 8 ? 4 : 2;  // tokens a thread has: 2 c, 2 c + 1 of each eight
     int64_t yo[4], oo[4];  // where they begin in y and out, -1: no token
@@ -612,7 +608,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const Ad
   const int pitch = up_pitch(KS * 16, MULTI ? a.blocks : 1);
   const uint32_t base = smem_u32(up_smem), y_ring = base + tid * 16, b_ring = base + S * kUpY, stage_bytes = kUpCols * pitch;
   const int cols = (a.N + kUpCols - 1) / kUpCols;
-  const int64_t all = (int64_t)a.plan->tiles[a.up_kind] * cols;
+  const int64_t all = (int64_t)a.plan->tiles[a.kind] * cols;
   bool waited = false;
   int64_t at = 0, stop = 0;
   for (int side = 0;;) {
@@ -627,7 +623,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_up_many_kernel(const Ad
     const int tile = (int)(at / cols), begin = (int)(at - (int64_t)tile * cols);
     const int end = (int)(stop - at < cols - begin ? begin + (stop - at) : cols);
     at += end - begin;
-    const AdapterTile t = a.up_tiles[tile];
+    const AdapterTile t = a.tiles[tile];
     const int live = live_rank(a, t.adapter), blocks = MULTI ? max(1, (live + KS * 16 - 1) / (KS * 16)) : 1;
     const int p0 = warp * 16 + g;  // the thread's tokens: p0 and p0 + 8 of the tile
     const __half* yp[2];
@@ -862,12 +858,11 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   g.rank = rank;
   g.scale = scale;
   const bool few = T <= kFewTokens;
-  g.down_kind = g.up_kind = few ? 0 : 1;
+  g.kind = few ? 0 : 1;
   const char* base = static_cast<const char*>(plan);
   g.plan = static_cast<const AdapterPlan*>(plan);
   g.order = reinterpret_cast<const int32_t*>(base + adapter_order_at());
-  g.down_tiles = reinterpret_cast<const AdapterTile*>(base + adapter_tiles_at(T, n, g.down_kind));
-  g.up_tiles = reinterpret_cast<const AdapterTile*>(base + adapter_tiles_at(T, n, g.up_kind));
+  g.tiles = reinterpret_cast<const AdapterTile*>(base + adapter_tiles_at(T, n, g.kind));
   g.block = rank_block(R);
   g.blocks = (int)((R + g.block - 1) / g.block);
   g.terms = static_cast<__half*>(workspace);
@@ -882,16 +877,16 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   g.N = (int)N;
   g.R = (int)R;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int64_t down = adapter_max_tiles(T, n, g.down_kind), up = adapter_max_tiles(T, n, g.up_kind);
+  const int64_t tiles = adapter_max_tiles(T, n, g.kind);
   // K is split over a cluster, as long as two CTAs an SM are enough for all (64 tiles by eight, as more than fit at once:
   // 22 us for 64 tokens; by four: 19): few tokens, of at least four steps a warp; many, of at least 16 stages
   g.cluster = 1;
   if (few)
-    while (g.cluster < 8 && down * g.cluster * 2 <= 2 * f.sms && K / 32 >= g.cluster * 2 * kDownWarps) g.cluster *= 2;
+    while (g.cluster < 8 && tiles * g.cluster * 2 <= 2 * f.sms && K / 32 >= g.cluster * 2 * kDownWarps) g.cluster *= 2;
   else
-    while (g.cluster < 8 && down * g.cluster * 2 <= 2 * f.sms && K / 64 >= g.cluster * 16) g.cluster *= 2;
+    while (g.cluster < 8 && tiles * g.cluster * 2 <= 2 * f.sms && K / 64 >= g.cluster * 16) g.cluster *= 2;
   const int nt = g.block / 8;
-  const dim3 grid((unsigned)(down * g.cluster), (unsigned)g.blocks);
+  const dim3 grid((unsigned)(tiles * g.cluster), (unsigned)g.blocks);
   cudaError_t e;
 #define TB_DOWN_FEW(NT)                                                                                                         \
   ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_down_few_kernel<NT>), f.device, down_few_smem<NT>())) != TB_OK \
@@ -911,7 +906,7 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
   if (e == cudaSuccess) {
     if (few) {
       // two CTAs an SM share all tiles' columns; at least 32 columns a warp
-      int64_t ctas = (up * ((N + 31) / 32) + kUpFewWarps - 1) / kUpFewWarps;
+      int64_t ctas = (tiles * ((N + 31) / 32) + kUpFewWarps - 1) / kUpFewWarps;
       const dim3 some((unsigned)(ctas < 2 * f.sms ? ctas : 2 * f.sms));
 #define TB_UP(W, MULTI)                                                                                                            \
   ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_up_few_kernel<W, MULTI>), f.device, up_few_smem<W>())) != TB_OK \
@@ -922,7 +917,7 @@ extern "C" int tb_adapter_linear(const uint16_t* x, int64_t ldx, int64_t T, int6
       if (rc != TB_OK) return rc;
     } else {
       const size_t smem = (size_t)up_stages(R > 64) * (kUpY + kUpCols * up_pitch(g.block, g.blocks));
-      const int64_t ctas = up * ((N + kUpCols - 1) / kUpCols);
+      const int64_t ctas = tiles * ((N + kUpCols - 1) / kUpCols);
       const dim3 some((unsigned)(ctas < 2 * f.sms ? ctas : 2 * f.sms));
 #define TB_UP(KS, MULTI)                                                                                                           \
   ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(adapter_up_many_kernel<KS, MULTI>), f.device, (int)smem)) != TB_OK \
