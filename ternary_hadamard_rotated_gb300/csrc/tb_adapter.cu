@@ -408,6 +408,8 @@ TB_DEVI void cp_async8(uint32_t dst, const void* src, int bytes) {  // the rest 
 
 // W: elements of a row of B a thread loads at a time (16 as twice 8, so that four threads' are 64 bytes in a row), of
 // blocks of 16, 32 or 64 ranks; MULTI: several blocks.  An item of the ring is a block of a unit, with the unit's y at its first block.
+// 64 tokens of 40 adapters, N 17408: rank 16 15.0 us for both launches in a graph, 64 26.8 (floor 18), 128 51 (35); of 128 registers
+// blocks of 64 ranks spill 8 bytes, several 120.
 template <int W, bool MULTI>
 __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const AdapterArgs a) {
   constexpr int kBlock = W * 4, kMma = W / 4, S = up_few_stages(W);  // ranks of a block, its MMAs of 16
@@ -581,11 +583,14 @@ __global__ void __launch_bounds__(kUpFewThreads, 2) adapter_up_few_kernel(const 
 
 // ---------------------------------------------------------------- up, many tokens
 // Every CTA takes equal runs of all row tiles' (at most 128 tokens) column tiles of 64, back and forth over them, as tiles
-// of few tokens take less time (packed prompts 115 us then, 122 now that the two terms of h have sums of their own; 120 with one run
-// a CTA and with four); a warp takes 16 of the tokens.  A
+// of few tokens take less time (packed prompts 115 us; 120 with one run a CTA and with four); a warp takes 16 of the tokens.  A
 // thread keeps its tokens' terms as the mma's left operand (of up to 64 ranks; above, they are read again); B's rows come
 // by cp.async three column tiles ahead, and y into a ring of the thread's own with them.  Which column of out is which of the MMAs' columns is free: thread
 // (g, c) has twice 8 neighbouring ones of tokens g and g + 8, so that four threads' y and out are 64 bytes in a row.
+// The two terms' sums in registers of their own: packed prompts 121 us in a graph, 115 with one sum for both (see above);
+// other orders 122 to 132 (B read twice and one sum scaled between the terms, columns two MMAs at a time).  This launch by
+// itself 102 us of them, 387 MB at 3.8 TB/s, the tensor pipe busy 28 % and a thread issuing in 42 % of the cycles.  8192 tokens of one
+// adapter, K 5120, N 17408: rank 32 127 us, 64 169, 128 388 (floors 97); ranks of 256, N 5120, four adapters: 322 (40).
 constexpr int kUpThreads = 256, kUpCols = 64, kUpRuns = 2;
 constexpr int up_stages(bool multi) { return multi ? 3 : 4; }
 
@@ -817,7 +822,15 @@ static cudaError_t launch(void (*fn)(Args...), dim3 grid, int threads, size_t sm
 // ranks that share a power of two, and a launch of `down`'s part of A
 static int rank_block(int64_t R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 
-// Up to this many tokens of a step the tiles are of 16.
+// Up to this many tokens of a step the tiles are of 16.  In a graph, K 5120, N 17408, rank 16, tiles of 16 against those of 128:
+//   tokens   one adapter       10 adapters in turn   100 in turn
+//      64     7.7 / 10.6 us       8.5 / 15.5 us        17.9 / 45.7 us
+//     256    12.9 / 15.5         14.8 / 19.2           25.8 / 69.1
+//     512    17.7 / 18.9         20.8 / 20.7           28.8 / 69.2
+//    1024    27.1 / 24.4         30.0 / 25.6           38.1 / 77.0
+// rank 64: 17.2 / 20.5, 20.3 / 27.3 and 56.5 / 116 at 256 tokens, 35.7 / 35.1, 39.6 / 39.1 and 67.8 / 124 at 1024.  The two
+// cross between 512 and 1024 tokens where adapters are few, and later than 1024 where they are many: up to there a higher
+// number than 256, and one that goes by the adapters, would be the faster one.
 constexpr int kFewTokens = 256;
 
 }  // namespace tb

@@ -107,8 +107,10 @@ template <typename Out>
 constexpr int move_stage() { return kMoveChunk * 2 + kMoveChunk / move_each<Out>() * 4; }
 
 // Every CTA takes an equal run of all rows' chunks; logits and mask words come by cp.async into a ring of the thread's own,
-// kMoveStages - 1 chunks ahead (rows whose distance is no multiple of 8: one element at a time).  Bound by the bytes: 64
-// rows of 248320 to fp32, 96 MB in 16.0 us by itself, 6.0 TB/s (0.89 of measured HBM).  Three CTAs an SM of four stages
+// kMoveStages - 1 chunks ahead (rows whose distance is no multiple of 8: one element at a time, 64 rows of 248319 behind
+// 8000 tokens 53.6 us in a graph against 32.3 where the rows are 248320 apart; of 50257 behind 700 14.8 against 8.9; one row
+// of 50257 6.1, as of 50256).  64 rows of 248320 to fp32, 96 MB in 16.0 us by itself; 38 MB of them pass DRAM, 2.4 TB/s, as what
+// is written stays in L2, so that loads' latency bounds it, not HBM.  Three CTAs an SM of four stages
 // leave shared memory for the second launch beside them (with six stages it began when these were through).
 template <typename Out, bool ALIGNED>
 __global__ void __launch_bounds__(kMoveThreads, 4) logits_move_kernel(const LogitsArgs a) {
@@ -203,7 +205,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) logits_move_kernel(const Logi
 // have a chain of a scattered load and a scattered store a row.  64 requests with histories up to 8000, by itself 19.6 us,
 // both launches 25.4 in a graph; nine trees of 5 to 16 drafts behind 2000 to 30000, 31.4 and 42.2: about 13 to count, 10
 // to gather the rows' logits, 6 to store them, 3 for the masks.  (With counts of the whole vocabulary in one launch
-// that moves the rows too: 31 to 46, and 46 to 89.)
+// that moves the rows too: 31 to 46, and 46 to 89.)  Alone, in place without a mask: 64 requests of 8000 31.9 us (to another
+// place 32.4, in place under masks 38.6).  Three CTAs an SM, 40 registers a thread, 16 bytes spilled.
 constexpr int kFixThreads = 512, kTable = 4096, kMostTokens = kTable / 4 * 3;
 constexpr int kRows = 64;    // of a request at a time
 constexpr int kResults = 4096;
@@ -475,7 +478,11 @@ extern "C" int tb_logits_adjust(const uint16_t* logits, int64_t ld, int64_t T, i
   a.B = (int)B;
   a.chunks = (int)((V + kMoveChunk - 1) / kMoveChunk);
   // 1024 tokens of the history a CTA (half as many, or twice, cost 64 decoding requests and verification 5 to 15 us more),
-  // fewer where requests are few
+  // 256 where requests are few: one of 700, 4000 and 30000 tokens takes 6.2, 6.3 and 17.3 us in a graph, with 1024 a CTA 7.9, 9.7
+  // and 17.3; three 6.8, 7.0 and 18.7, with 1024 8.1, 10.1 and 18.6.  (Four, and eight, would gain the same by 256: 6.8, 6.8 and
+  // 18.6 against 8.2, 10.4 and 18.4; 7.2, 7.8 and 24.7 against 8.3, 11.0 and 24.7.)  There are CTAs for what the buffer can hold,
+  // whose surplus leaves at once: 64 requests of 8000 tokens in a buffer of 262144 take 36.1 us, in one of 8000 32.4; of 700 21.0
+  // and 16.2
   a.part_tokens = B >= 4 ? 1024 : 256;
   a.parts_log2 = 0;
   while (a.parts_log2 < 5 && (int64_t)a.part_tokens << a.parts_log2 < ldh + n_bias / B) ++a.parts_log2;

@@ -113,7 +113,10 @@ TB_DEVI uint4 pack8(const Eight& e) {
 constexpr int kRotaryThreads = 256;
 constexpr int kRotaryAngles = 2048;  // (token, pair) angles a CTA holds: 16 KB
 
-// WIDE: R a multiple of 16, rotations of 8 pairs by two 16-byte loads; otherwise pair by pair.
+// WIDE: R a multiple of 16, rotations of 8 pairs by two 16-byte loads; otherwise pair by pair, 2 bytes an access.
+// 20000 tokens of 32/8 heads of 80 and 96, all turned: 53 and 60 us in a graph (floors 38 and 45); 12000 of 24/4 heads of 192:
+// 48 (38).  Of 34 turned elements, pair by pair: 251 us for 12000 tokens of 24/4 heads of 256 (floor 51), 267 for 20000 of 32/8
+// heads of 128 (60).  64 tokens: 2.6 us for heads of 80, 4.6 with 34 turned of 128 (rows of 128, all turned: 3.5).
 template <bool WIDE>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs a) {
   __shared__ __align__(16) float cosines[kRotaryAngles], sines[kRotaryAngles];
@@ -233,7 +236,8 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
 // where tokens are few: kAhead rows of loads on their way before the angles are made, by all lanes together, a pair at a
 // time, and kept in registers for all of the token's heads.  Bound by the bytes: 12289 tokens of 24/4 heads of 256, 64 of
 // them turned, with the cache's write, 428 MB in 71.8 us, 0.88 of measured HBM; 40001 tokens of 32/8 heads of 128, 819 MB
-// in 125 us, 0.97 (the form for any head: 137 and 147).  Four CTAs an SM: with five the registers spill (88, 137).
+// in 125 us, 0.97 (the form for any head: 137 and 147).  Four CTAs an SM, 64 registers a thread: halves spill 40 bytes,
+// pairs of neighbours none; with five CTAs 88 and 137 us.
 constexpr int kRowsThreads = 256, kRowsWarps = kRowsThreads / 32;
 
 template <int L, bool PAIRS>
