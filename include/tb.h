@@ -601,7 +601,8 @@ int tb_adapter_plan(const int32_t* row_start, const int32_t* adapter, int64_t B,
  * of the token's 64 ranks around it, the greater of the two; sums are rounded to the place of their largest term, in
  * which an element below 2^-14 counts as 2^-14; one rounding to fp16 at the end.  What is not finite stays in the rows
  * and columns that it reaches (an infinite element of B may give NaN there).  A token's row depends on no other token's x
- * and y; the order of its sums, and with it the last bits, also goes by T and n.  K, N and R multiples of 8, R up to 256 (TB_ERR_UNSUPPORTED above).  workspace: at least
+ * and y; the order of its sums, and with it the last bits, also goes by T and n.  K, N and R multiples of 8, R up to
+ * 256 (TB_ERR_UNSUPPORTED above).  workspace: at least
  * tb_adapter_linear_workspace_size(T, n, K, N, R) bytes of scratch; its contents do not matter; calls that share
  * one are ordered on one stream.  dev_status optional: TB_DEV_BAD_PLAN.
  */

@@ -12,7 +12,7 @@
 // holds 11 bits more of it wherever hi is a normal number: h is off by at most 2^-22 of itself or 2^-51 of that largest, the
 // greater of the two (hi + lo at one scale is off by 2^-40 of the largest: half a thousandth of an h that is 2^-29 of it,
 // all that a column has whose B is 0 for the largest).  Products and sums are fp32; the
-// sum with lo takes 2^-12 before that with hi is added to it, and 2^-e is applied to each sum.
+// sum with lo takes 2^-12 before it meets that with hi, and 2^-e is applied to both.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <limits.h>
